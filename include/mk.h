@@ -451,6 +451,111 @@ int mk_attention_decode_noalloc(void* stream, const float* qkv, void* kcache, vo
                                 int B, int Hq, int Hkv, int D, int capacity, const int32_t* pos,
                                 const int32_t* len0, int chunk, double rope_theta);
 
+/* ---- paged KV cache and draft verification ------------------------------
+ * Operators on device pointers, enqueued on `stream`, that allocate nothing
+ * and keep nothing between calls.  No counterpart on the pages: they serve a
+ * loop that holds its KV cache in pages and whose requests change from step
+ * to step.  One step is mk_paged_plan, per layer mk_qk_norm_rope and
+ * mk_paged_attention, and mk_verify_drafts where the new tokens were drafts.
+ *
+ *  - A pool holds a layer's keys or values: bf16 [num_pages, Hkv, page_size,
+ *    D], page_size 16, 32, 64, 128 or 256.  Row s of the block table int32
+ *    [B, max_pages] lists the pages of request s in order of positions; a
+ *    slot is page * page_size + offset.
+ *  - Lengths, tables and maps are read on the GPU.  What they hold is checked
+ *    there: `status` (int32 on the device, NULL for none, zeroed by the
+ *    caller) receives the first MK_DEV_* code; the library does not clear it.
+ *  - Pointers to float, bf16 and workspace memory must be 16-byte aligned.
+ *    All tensors belong to the caller and live on the current device.
+ *  - Every call can be captured into a CUDA graph.
+ *  - Host errors: MK_ERR_ARG, MK_ERR_LIMIT, MK_ERR_CUDA (also when an error
+ *    of the caller's earlier work is pending: it is reported, not cleared,
+ *    and nothing is launched), MK_ERR_NOMEM. */
+
+/* Block tables and slot maps of a step.  Request b has ctx_len[b] cached and
+ * new_len[b] new tokens and holds held[b] pages; after the call it holds
+ * ceil((ctx_len + new_len) / page_size).  Pages it no longer needs (drafts
+ * rolled back, a finished request: both lengths 0) go back on the stack
+ * free_pages[0 .. *free_count), in order of requests and pages, and then the
+ * growing requests, in order, take theirs from its top into their table rows.
+ * held_out and free_count_out receive the new values (they may be held and
+ * free_count themselves); table entries from held_out[b] on and stack entries
+ * from *free_count_out on are left as they were.
+ *  cu int32 [B + 1]: exclusive sums of new_len.
+ *  positions, slots int32 [max_tokens]: token cu[b] + t has position
+ *  ctx_len[b] + t and the slot that its page gives it; -1 behind the last.
+ * Status: MK_DEV_BAD_INDEX (a negative length, a held count or stack count
+ * out of range), MK_DEV_CAPACITY (a request over max_pages, more than
+ * max_tokens new tokens, not enough free pages): then nothing moves, cu is
+ * all 0 and positions and slots are all -1.  A page id outside the pool, from
+ * the stack or a table, gives slot -1 and MK_DEV_BAD_INDEX.
+ * 1 <= B <= 4096; num_pages is also the length of free_pages. */
+int mk_paged_plan(void* stream, int B, int page_size, int max_pages, int num_pages, int max_tokens,
+                  const int32_t* ctx_len, const int32_t* new_len, int32_t* table, const int32_t* held,
+                  int32_t* held_out, int32_t* free_pages, const int32_t* free_count, int32_t* free_count_out,
+                  int32_t* cu, int32_t* positions, int32_t* slots, int32_t* status);
+
+/* RMS norms of queries and keys for each head, the rotate-half rotary
+ * embedding, and the stores of keys and values into their pages, in one pass.
+ *  qkv f32 or bf16 (qkv_dtype MK_F32 / MK_BF16), N rows ld_qkv elements
+ *  apart: Hq query heads, Hkv key heads, Hkv value heads of D = 64 or 128.
+ *  q, k <- x / sqrt(mean(x^2) + eps) * gamma, gamma bf16 [D] (q_gamma,
+ *  k_gamma; NULL: no norm); pairs (i, i + D/2) turned by
+ *  position * rope_theta^(-2i/D); then
+ *  q_out bf16, N rows ld_q elements apart, [Hq, D] each; k and v to
+ *  kpool / vpool at slots[row].
+ * A row with a negative position is left out (its q_out row stays); one with
+ * a negative slot is not stored.  A slot outside the pool is not stored
+ * either and gives MK_DEV_BAD_INDEX.  The slots of a call are distinct.  Row
+ * strides are multiples of 16 bytes.  qkv may not overlap q_out. */
+int mk_qk_norm_rope(void* stream, int N, int Hq, int Hkv, int D, const void* qkv, int qkv_dtype, int64_t ld_qkv,
+                    const void* q_gamma, const void* k_gamma, float eps, double rope_theta,
+                    const int32_t* positions, const int32_t* slots, void* q_out, int64_t ld_q, void* kpool,
+                    void* vpool, int num_pages, int page_size, int32_t* status);
+
+/* Attention of the new tokens of B requests over their pages, causal among
+ * the new ones: token t of request b (row cu[b] + t of q) sees the keys at
+ * positions 0 .. ctx_len[b] + t, whose pages row b of the table lists.
+ *  q, out bf16, N rows ld_q / ld_out elements apart, [Hq, D] each; query head
+ *  h reads key/value head h / (Hq / Hkv).  cu int32 [B + 1] (cu[B] <= N).
+ *  Softmax scale `scale` (1/sqrt(D) as a rule).
+ *  max_new: no request has more new tokens than this; with max_new * Hq / Hkv
+ *  at most 32 the kernel for tokens and drafts runs, else the one for chunks.
+ *  workspace: mk_paged_attention_workspace bytes for the same max_new, heads
+ *  and D, for partial results; calls that share it must not overlap.
+ * Rows of no request (before cu[0], behind cu[B]) stay as they are.  Keys of
+ * a page id outside the pool are left out (MK_DEV_BAD_INDEX), and a row
+ * without any key is zero.  Cache memory behind a request's last key may
+ * hold anything.  Lengths that do not fit (cu decreasing or past N, a request
+ * over max_new or max_pages, a negative length) give MK_DEV_BAD_INDEX and
+ * nothing is written.  D 64 or 128, Hq / Hkv <= 128.  q may not overlap out. */
+int mk_paged_attention(void* stream, int B, int N, int max_new, int Hq, int Hkv, int D, const void* q, int64_t ld_q,
+                       const void* kpool, const void* vpool, int num_pages, int page_size, const int32_t* table,
+                       int max_pages, const int32_t* cu, const int32_t* ctx_len, float scale, void* out,
+                       int64_t ld_out, void* workspace, size_t workspace_size, int32_t* status);
+
+/* Bytes of workspace mk_paged_attention needs on the current device. */
+int mk_paged_attention_workspace(int max_new, int Hq, int Hkv, int D, size_t* bytes);
+
+/* Verification of drafted tokens from given random numbers (speculative
+ * sampling).  Per request, K drafts (draft_len[b] of them; NULL: all K):
+ *  p f32, B (K + 1) rows ld_p elements apart: the target's probabilities
+ *  before drafts 0 .. K-1 and behind the last; q f32, B K rows ld_q apart: the
+ *  draft model's, or NULL for drafts without probabilities (each taken as
+ *  certain); u f32 [B, K + 1] in [0, 1).
+ *  Draft t is accepted while u[t] q_t[x_t] < p_t[x_t].  The token behind the
+ *  accepted ones is drawn with u[K] from max(p_t - q_t, 0) after a rejection
+ *  (from p_t if that is zero everywhere), from p after the last draft: the
+ *  smallest index whose running sum exceeds u[K] times the sum.  Negative and
+ *  NaN weights count as zero; if all are, the token is -1.
+ *  tokens int32 [B, K + 1]: the accepted drafts, the drawn token, then -1.
+ *  accepted int32 [B]: the number of accepted drafts.
+ * A draft outside [0, V) ends the drafts there and gives MK_DEV_BAD_INDEX.
+ * 0 <= K <= 1024. */
+int mk_verify_drafts(void* stream, int B, int K, int V, const float* p, int64_t ld_p, const float* q, int64_t ld_q,
+                     const int32_t* drafts, const int32_t* draft_len, const float* u, int32_t* tokens,
+                     int32_t* accepted, int32_t* status);
+
 /* Release everything the library allocated.  Safe on NULL. */
 void mk_destroy(mk_graph* g);
 

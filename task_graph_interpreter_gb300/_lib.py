@@ -34,6 +34,7 @@ EXPORTS = [
     "mk_decode_step", "mk_decode_step_ex", "mk_decode_step_host", "mk_status",
     "mk_get_trace", "mk_kernel_info", "mk_destroy", "mk_last_error", "mk_debug_patch_task",
     "mk_attention_decode_noalloc", "mk_gemv_tensor_core_tiles", "mk_debug_set_epoch", "mk_set_chunk",
+    "mk_paged_plan", "mk_qk_norm_rope", "mk_paged_attention", "mk_paged_attention_workspace", "mk_verify_drafts",
 ]
 
 
@@ -97,6 +98,16 @@ def lib():
         "mk_attention_decode_noalloc": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int,
                                                 c_int, c_int, c_int, POINTER(c_int32), POINTER(c_int32), c_int,
                                                 c_double]),
+        "mk_paged_plan": (c_int, [c_void_p] + [c_int] * 5 + [c_void_p] * 12),
+        "mk_qk_norm_rope": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_int, c_int64, c_void_p, c_void_p,
+                                    c_float, c_double, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p,
+                                    c_int, c_int, c_void_p]),
+        "mk_paged_attention": (c_int, [c_void_p] + [c_int] * 6 + [c_void_p, c_int64, c_void_p, c_void_p, c_int, c_int,
+                                                                  c_void_p, c_int, c_void_p, c_void_p, c_float,
+                                                                  c_void_p, c_int64, c_void_p, c_size_t, c_void_p]),
+        "mk_paged_attention_workspace": (c_int, [c_int, c_int, c_int, c_int, POINTER(c_size_t)]),
+        "mk_verify_drafts": (c_int, [c_void_p, c_int, c_int, c_int, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                                     c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
         "mk_last_error": (c_char_p, []),
     }
     for name, (res, args) in sig.items():
@@ -298,6 +309,44 @@ def mk_attention_decode_noalloc(stream: int, qkv: int, kcache: int, vcache: int,
     check(lib().mk_attention_decode_noalloc(c_void_p(stream), c_void_p(qkv), c_void_p(kcache), c_void_p(vcache),
                                             c_void_p(out), B, Hq, Hkv, D, capacity, pa, la, chunk, float(theta)),
           "mk_attention_decode_noalloc")
+
+
+def mk_paged_plan(stream: int, B: int, page_size: int, max_pages: int, num_pages: int, max_tokens: int, ctx_len: int,
+                  new_len: int, table: int, held: int, held_out: int, free_pages: int, free_count: int,
+                  free_count_out: int, cu: int, positions: int, slots: int, status: int = 0):
+    """Device pointers as ints (0: none), as in every operator below."""
+    check(lib().mk_paged_plan(stream, B, page_size, max_pages, num_pages, max_tokens, ctx_len, new_len, table, held,
+                              held_out, free_pages, free_count, free_count_out, cu, positions, slots, status),
+          "mk_paged_plan")
+
+
+def mk_qk_norm_rope(stream: int, N: int, Hq: int, Hkv: int, D: int, qkv: int, qkv_dtype: int, ld_qkv: int,
+                    q_gamma: int, k_gamma: int, eps: float, rope_theta: float, positions: int, slots: int, q_out: int,
+                    ld_q: int, kpool: int, vpool: int, num_pages: int, page_size: int, status: int = 0):
+    check(lib().mk_qk_norm_rope(stream, N, Hq, Hkv, D, qkv, qkv_dtype, ld_qkv, q_gamma, k_gamma, eps, rope_theta,
+                                positions, slots, q_out, ld_q, kpool, vpool, num_pages, page_size, status),
+          "mk_qk_norm_rope")
+
+
+def mk_paged_attention(stream: int, B: int, N: int, max_new: int, Hq: int, Hkv: int, D: int, q: int, ld_q: int,
+                       kpool: int, vpool: int, num_pages: int, page_size: int, table: int, max_pages: int, cu: int,
+                       ctx_len: int, scale: float, out: int, ld_out: int, workspace: int, workspace_size: int,
+                       status: int = 0):
+    check(lib().mk_paged_attention(stream, B, N, max_new, Hq, Hkv, D, q, ld_q, kpool, vpool, num_pages, page_size,
+                                   table, max_pages, cu, ctx_len, scale, out, ld_out, workspace, workspace_size,
+                                   status), "mk_paged_attention")
+
+
+def mk_paged_attention_workspace(max_new: int, Hq: int, Hkv: int, D: int) -> int:
+    n = c_size_t()
+    check(lib().mk_paged_attention_workspace(max_new, Hq, Hkv, D, ctypes.byref(n)), "mk_paged_attention_workspace")
+    return n.value
+
+
+def mk_verify_drafts(stream: int, B: int, K: int, V: int, p: int, ld_p: int, q: int, ld_q: int, drafts: int,
+                     draft_len: int, u: int, tokens: int, accepted: int, status: int = 0):
+    check(lib().mk_verify_drafts(stream, B, K, V, p, ld_p, q, ld_q, drafts, draft_len, u, tokens, accepted, status),
+          "mk_verify_drafts")
 
 
 def mk_last_error() -> str:

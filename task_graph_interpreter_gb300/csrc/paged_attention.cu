@@ -1,0 +1,150 @@
+// Entry points of paged attention: checks, tensor maps, the choice of kernel.
+#include <atomic>
+#include <cmath>
+
+#include "paged_attention.cuh"
+
+namespace mk {
+
+cudaError_t launch_join(const AttnParams& p, int D, bool chunk, cudaStream_t stream);
+
+namespace {
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encoder() {
+  static std::atomic<EncodeTiledFn> known{nullptr};
+  EncodeTiledFn fn = known.load();
+  if (fn) return fn;
+  void* f = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess || !f)
+    return nullptr;
+  fn = reinterpret_cast<EncodeTiledFn>(f);
+  known.store(fn);
+  return fn;
+}
+
+bool encode(EncodeTiledFn enc, CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dim,
+            const cuuint64_t* stride, const cuuint32_t* box) {
+  const cuuint32_t one[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), dim, stride, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Few query rows (tokens and drafts) or chunks: a request and head of at most
+// 32 rows fills two 16-row warp products; beyond that the 128-row tensor-core
+// tiles take fewer passes over the keys.
+bool few_rows(int max_new, int G) { return (int64_t)max_new * G <= kMaxFewRows; }
+
+size_t workspace_bytes(int max_new, int G, int D, int sms) {
+  const size_t record = (size_t)(D + 2) * 4;
+  if (few_rows(max_new, G)) return (size_t)2 * kRowWarps * sms * (max_new * G <= 16 ? 16 : 32) * record;
+  return (size_t)2 * sms * 256 * record;
+}
+
+int check_shape(const char* who, int max_new, int Hq, int Hkv, int D) {
+  if (D != 64 && D != 128) return fail(MK_ERR_ARG, std::string(who) + ": D must be 64 or 128");
+  if (Hkv < 1 || Hkv > 1024 || Hq < Hkv || Hq % Hkv || Hq / Hkv > 128)
+    return fail(MK_ERR_ARG, std::string(who) + ": need Hq a multiple of Hkv (at most 1024) with Hq/Hkv <= 128");
+  if (max_new < 1) return fail(MK_ERR_ARG, std::string(who) + ": max_new must be positive");
+  return MK_OK;
+}
+
+int device_sms(const char* who, int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return fail(MK_ERR_CUDA, std::string(who) + ": no current device");
+  return MK_OK;
+}
+
+}  // namespace
+}  // namespace mk
+
+using namespace mk;
+
+extern "C" int mk_paged_attention_workspace(int max_new, int Hq, int Hkv, int D, size_t* bytes) try {
+  if (!bytes) return fail(MK_ERR_ARG, "mk_paged_attention_workspace: null argument");
+  if (int rc = check_shape("mk_paged_attention_workspace", max_new, Hq, Hkv, D)) return rc;
+  int sms = 0;
+  if (int rc = device_sms("mk_paged_attention_workspace", &sms)) return rc;
+  *bytes = workspace_bytes(max_new, Hq / Hkv, D, sms);
+  return MK_OK;
+} catch (...) {
+  return MK_ERR_NOMEM;
+}
+
+extern "C" int mk_paged_attention(void* stream_, int B, int N, int max_new, int Hq, int Hkv, int D, const void* q,
+                                  int64_t ld_q, const void* kpool, const void* vpool, int num_pages, int page_size,
+                                  const int32_t* table, int max_pages, const int32_t* cu, const int32_t* ctx_len,
+                                  float scale, void* out, int64_t ld_out, void* workspace, size_t workspace_size,
+                                  int32_t* status) try {
+  const char* who = "mk_paged_attention";
+  if (!q || !kpool || !vpool || !table || !cu || !ctx_len || !out || !workspace)
+    return fail(MK_ERR_ARG, "mk_paged_attention: null argument");
+  if (int rc = check_shape(who, max_new, Hq, Hkv, D)) return rc;
+  if (B < 0 || N < 0 || max_pages < 1) return fail(MK_ERR_ARG, "mk_paged_attention: need B, N >= 0 and max_pages >= 1");
+  if (!page_size_ok(page_size))
+    return fail(MK_ERR_ARG, "mk_paged_attention: page_size must be 16, 32, 64, 128 or 256");
+  if (num_pages < 1 || (int64_t)num_pages * Hkv * page_size > INT32_MAX ||
+      (int64_t)max_pages * page_size > INT32_MAX)
+    return fail(MK_ERR_ARG, "mk_paged_attention: rows of the pools and positions must fit int32");
+  if (ld_q < (int64_t)Hq * D || ld_q % 8 || ld_out < (int64_t)Hq * D || ld_out % 8)
+    return fail(MK_ERR_ARG, "mk_paged_attention: row strides must cover a row and be multiples of 16 bytes");
+  if (!aligned16(q) || !aligned16(kpool) || !aligned16(vpool) || !aligned16(out) || !aligned16(workspace))
+    return fail(MK_ERR_ARG, "mk_paged_attention: pointers must be 16-byte aligned");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(MK_ERR_ARG, "mk_paged_attention: scale must be positive");
+  if (int rc = pending_error(who)) return rc;
+  int sms = 0;
+  if (int rc = device_sms(who, &sms)) return rc;
+  const int G = Hq / Hkv;
+  if (workspace_size < workspace_bytes(max_new, G, D, sms))
+    return fail(MK_ERR_LIMIT, "mk_paged_attention: the workspace needs " +
+                                  std::to_string(workspace_bytes(max_new, G, D, sms)) + " bytes");
+  if (B == 0 || N == 0) return MK_OK;
+  EncodeTiledFn enc = encoder();
+  if (!enc) return fail(MK_ERR_CUDA, "mk_paged_attention: cuTensorMapEncodeTiled is not available");
+
+  const bool few = few_rows(max_new, G);
+  AttnParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.v = static_cast<const __nv_bfloat16*>(vpool);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.ld_q = ld_q; p.ld_out = ld_out;
+  p.table = table; p.cu = cu; p.ctx = ctx_len;
+  p.part = static_cast<float*>(workspace);
+  p.status = status;
+  p.scale = scale * 1.4426950408889634f;
+  p.B = B; p.N = N; p.Hq = Hq; p.Hkv = Hkv; p.G = G; p.max_new = max_new;
+  p.max_pages = max_pages; p.num_pages = num_pages;
+  while ((1 << p.page_shift) < page_size) ++p.page_shift;
+  p.workers = few ? sms * kRowWarps : sms;
+  p.rows = few ? (max_new * G <= 16 ? 16 : 32) : 256;
+  p.tq = few ? 0 : 128 / G;
+
+  // pools as [rows, D], pages one after the other; a box is what one page gives a block of keys
+  CUtensorMap kmap, vmap, qmap;
+  const int keys = few ? 32 * 128 / D : 128;
+  const cuuint64_t dim[2] = {(cuuint64_t)D, (cuuint64_t)num_pages * Hkv * page_size}, stride[1] = {(cuuint64_t)D * 2};
+  const cuuint32_t box[2] = {64u, (cuuint32_t)(page_size < keys ? page_size : keys)};
+  bool ok = encode(enc, &kmap, kpool, 2, dim, stride, box) && encode(enc, &vmap, vpool, 2, dim, stride, box);
+  if (ok && !few) {
+    const cuuint64_t qdim[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)N};
+    const cuuint64_t qstride[2] = {(cuuint64_t)D * 2, (cuuint64_t)ld_q * 2};
+    const cuuint32_t qbox[3] = {64u, (cuuint32_t)G, (cuuint32_t)p.tq};
+    ok = encode(enc, &qmap, q, 3, qdim, qstride, qbox);
+  }
+  if (!ok) return fail(MK_ERR_CUDA, "mk_paged_attention: a tensor map could not be encoded");
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (int rc = launch_result(few ? launch_rows(p, kmap, vmap, D, stream) : launch_chunk(p, qmap, kmap, vmap, D, stream),
+                             who))
+    return rc;
+  return launch_result(launch_join(p, D, !few, stream), who);
+} catch (...) {
+  return MK_ERR_NOMEM;
+}

@@ -1,0 +1,216 @@
+// Attention over a paged cache: what its two kernels and their join share --
+// parameters, and the even division of the work over workers.
+//
+// An item is what one worker could do alone: a key/value head of a request,
+// with all of its query rows (few rows) or with one tile of them (chunks).
+// Items lie one after the other on a line, each as long as the keys it reads
+// plus a constant for its fixed cost, in order of request, head and tile.
+// Worker w of W takes the part [U w / W, U (w + 1) / W) of the line's length
+// U, rounded to whole blocks of keys.  Lengths are read on the GPU, so
+// every worker finds its part for itself: one pass over the requests for U,
+// one to its first item.  An item cut by a worker's border leaves partial
+// (m, l, o) records, at most two per worker (its first and its last item),
+// which the join kernel merges in order of keys.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "paged.h"
+#include "ptx.cuh"
+
+namespace mk {
+
+struct AttnParams {
+  const __nv_bfloat16 *q, *v;  // v: the value pool
+  __nv_bfloat16* out;
+  int64_t ld_q, ld_out;
+  const int32_t *table, *cu, *ctx;
+  float* part;      // partial records: [slots][rows][D], then (m, l) [slots][rows][2]
+  int32_t* status;
+  float scale;      // softmax scale times log2(e)
+  int B, N, Hq, Hkv, G, max_new, max_pages, num_pages, page_shift;
+  int workers;
+  int rows;         // rows of a partial record
+  int tq;           // tokens per query tile (chunks): 128 / G
+};
+
+// Geometry of an item: few query rows (all of a request's), or a pair of
+// 128-row query tiles.
+template <int D, bool CHUNK>
+struct Geometry {
+  static constexpr int kKeys = CHUNK ? 128 : 32 * 128 / D;  // keys per block
+  static constexpr int kFixed = CHUNK ? 192 : 64;           // an item's fixed cost, in keys
+};
+
+struct Seq {
+  int n, ctx, nq;      // new tokens, cached tokens, items per head
+  int64_t base, step;  // cost of item i: base + i step
+  int64_t per_head;
+  bool bad;
+};
+
+template <int D, bool CHUNK>
+__device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
+  Seq s;
+  const int c0 = p.cu[b], c1 = p.cu[b + 1];
+  s.ctx = p.ctx[b];
+  s.n = c1 - c0;
+  s.bad = c0 < 0 || c1 < c0 || c1 > p.N || s.n > p.max_new || s.ctx < 0 ||
+          (int64_t)s.ctx + s.n > ((int64_t)p.max_pages << p.page_shift);
+  if (s.bad || s.n == 0) {
+    s.n = 0;
+    s.nq = 0;
+    s.base = s.step = s.per_head = 0;
+    return s;
+  }
+  constexpr int F = Geometry<D, CHUNK>::kFixed;
+  if (CHUNK) {
+    const int tp = 2 * p.tq;
+    s.nq = (s.n + tp - 1) / tp;
+    s.base = (int64_t)s.ctx + tp + F;
+    s.step = tp;
+  } else {
+    s.nq = 1;
+    s.base = (int64_t)s.ctx + s.n + F;
+    s.step = 0;
+  }
+  s.per_head = s.nq * s.base + s.step * ((int64_t)s.nq * (s.nq - 1) / 2);
+  return s;
+}
+
+__device__ __forceinline__ int64_t warp_incl_scan(int64_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// The line's length (a whole warp; lanes agree).  Sets *bad on lengths that do not fit.
+template <int D, bool CHUNK>
+__device__ __forceinline__ int64_t line_length(const AttnParams& p, int lane, bool* bad) {
+  int64_t u = 0;
+  bool wrong = false;
+  for (int b = lane; b < p.B; b += 32) {
+    const Seq s = load_seq<D, CHUNK>(p, b);
+    u += s.per_head * p.Hkv;
+    wrong |= s.bad;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+  *bad = __any_sync(0xffffffffu, wrong);
+  return u;
+}
+
+__device__ __forceinline__ int64_t border(int64_t u, int w, int workers) {
+  return u / workers * w + u % workers * w / workers;
+}
+
+// A place on the line: the item holding it.  Uniform over the warp.
+template <int D, bool CHUNK>
+struct Cursor {
+  int b, g, i;      // request, key/value head, tile
+  Seq s;
+  int64_t start;    // where the item begins
+  __device__ __forceinline__ int64_t cost() const { return s.base + i * s.step; }
+  // blocks of keys the item has
+  __device__ __forceinline__ int blocks(const AttnParams& p) const {
+    int keys = s.ctx + s.n;
+    if (CHUNK) keys = (int)min((int64_t)keys, s.ctx + (i + 1) * s.step);
+    constexpr int K = Geometry<D, CHUNK>::kKeys;
+    return (keys + K - 1) / K;
+  }
+  // the block that a place on the line falls to
+  __device__ __forceinline__ int block_at(int64_t x, int nk) const {
+    constexpr int K = Geometry<D, CHUNK>::kKeys;
+    if (x >= start + cost()) return nk;
+    const int64_t k = x - start - Geometry<D, CHUNK>::kFixed + K / 2;
+    return k <= 0 ? 0 : (int)min((int64_t)nk, k / K);
+  }
+  // the item holding place x of the line (0 <= x < U)
+  __device__ __forceinline__ void find(const AttnParams& p, int64_t x, int lane) {
+    int64_t before = 0;
+    for (int b0 = 0;; b0 += 32) {
+      Seq t;
+      t.per_head = 0;
+      if (b0 + lane < p.B) t = load_seq<D, CHUNK>(p, b0 + lane);
+      const int64_t own = t.per_head * p.Hkv, end = warp_incl_scan(own, lane) + before;
+      const unsigned hit = __ballot_sync(0xffffffffu, own > 0 && end > x);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        b = b0 + src;
+        start = __shfl_sync(0xffffffffu, end - own, src);
+        break;
+      }
+      before = __shfl_sync(0xffffffffu, end, 31);
+      if (b0 + 32 >= p.B) {  // not reached for x < U
+        b = p.B;
+        start = before;
+        return;
+      }
+    }
+    s = load_seq<D, CHUNK>(p, b);
+    const int64_t r = x - start;
+    g = (int)(r / s.per_head);
+    start += g * s.per_head;
+    i = 0;
+    if (CHUNK) {
+      const int64_t rr = x - start;
+      int lo = 0, hi = s.nq - 1;  // the last tile that begins at or before rr
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (mid * s.base + s.step * ((int64_t)mid * (mid - 1) / 2) <= rr) lo = mid;
+        else hi = mid - 1;
+      }
+      i = lo;
+      start += i * s.base + s.step * ((int64_t)i * (i - 1) / 2);
+    }
+  }
+  // the next item; b == p.B behind the last
+  __device__ __forceinline__ void next(const AttnParams& p) {
+    start += cost();
+    if (++i < s.nq) return;
+    i = 0;
+    if (++g < p.Hkv) return;
+    g = 0;
+    while (++b < p.B) {
+      s = load_seq<D, CHUNK>(p, b);
+      if (s.n > 0) return;
+    }
+  }
+};
+
+__device__ __forceinline__ float* part_ml(const AttnParams& p, int D, int slot, int row) {
+  // (m, l) records follow the outputs of all 2 * workers slots
+  return p.part + (size_t)2 * p.workers * p.rows * D + ((size_t)slot * p.rows + row) * 2;
+}
+__device__ __forceinline__ float* part_o(const AttnParams& p, int D, int slot, int row) {
+  return p.part + ((size_t)slot * p.rows + row) * D;
+}
+
+// Wait for a phase of an mbarrier, at most about two seconds, or until
+// another thread has given up.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (ptx::globaltimer() - t0 > 2000000000ull) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
+
+cudaError_t launch_rows(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int D,
+                        cudaStream_t stream);
+cudaError_t launch_chunk(const AttnParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                         const CUtensorMap& vmap, int D, cudaStream_t stream);
+constexpr int kRowWarps = 4;     // warps (workers) per CTA of the few-rows kernel
+constexpr int kMaxFewRows = 32;  // query rows of a request and head that it takes
+
+}  // namespace mk
