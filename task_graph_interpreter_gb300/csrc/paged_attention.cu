@@ -41,10 +41,11 @@ bool encode(EncodeTiledFn enc, CUtensorMap* m, const void* ptr, int rank, const 
 // tiles take fewer passes over the keys.
 bool few_rows(int max_new, int G) { return (int64_t)max_new * G <= kMaxFewRows; }
 
+// Two partial records and a note per worker (paged_attention.cuh).
 size_t workspace_bytes(int max_new, int G, int D, int sms) {
-  const size_t record = (size_t)(D + 2) * 4;
-  if (few_rows(max_new, G)) return (size_t)2 * kRowWarps * sms * (max_new * G <= 16 ? 16 : 32) * record;
-  return (size_t)2 * sms * 256 * record;
+  const bool few = few_rows(max_new, G);
+  const size_t workers = (size_t)sms * (few ? kRowWarps : 1), rows = !few ? 256 : max_new * G <= 16 ? 16 : 32;
+  return 2 * workers * rows * (D + 2) * 4 + workers * 16;
 }
 
 int check_shape(const char* who, int max_new, int Hq, int Hkv, int D) {
@@ -124,6 +125,7 @@ extern "C" int mk_paged_attention(void* stream_, int B, int N, int max_new, int 
   p.max_pages = max_pages; p.num_pages = num_pages;
   while ((1 << p.page_shift) < page_size) ++p.page_shift;
   p.workers = few ? sms * kRowWarps : sms;
+  if (p.workers > kMaxWorkers) return fail(MK_ERR_LIMIT, "mk_paged_attention: more SMs than the join can list");
   p.rows = few ? (max_new * G <= 16 ? 16 : 32) : 256;
   p.tq = few ? 0 : 128 / G;
 

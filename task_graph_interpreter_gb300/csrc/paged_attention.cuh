@@ -9,8 +9,9 @@
 // U, rounded to whole blocks of keys.  Lengths are read on the GPU, so
 // every worker finds its part for itself: one pass over the requests for U,
 // one to its first item.  An item cut by a worker's border leaves partial
-// (m, l, o) records, at most two per worker (its first and its last item),
-// which the join kernel merges in order of keys.
+// (m, l, o) records, at most two per worker (its first and its last item).
+// Each worker leaves a note of them, and the join kernel merges an item's
+// records, in order of keys, where the item ends.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -39,7 +40,7 @@ struct AttnParams {
 template <int D, bool CHUNK>
 struct Geometry {
   static constexpr int kKeys = CHUNK ? 128 : 32 * 128 / D;  // keys per block
-  static constexpr int kFixed = CHUNK ? 192 : 64;           // an item's fixed cost, in keys
+  static constexpr int kFixed = CHUNK ? 384 : 64;           // an item's fixed cost, in keys
 };
 
 struct Seq {
@@ -87,24 +88,43 @@ __device__ __forceinline__ int64_t warp_incl_scan(int64_t v, int lane) {
   return v;
 }
 
-// The line's length (a whole warp; lanes agree).  Sets *bad on lengths that do not fit.
+// r / d for 0 <= r, 0 < d and a quotient under 2^20: a float quotient put right (64-bit division is a long
+// routine, and the workers' start is on the critical path of a small call)
+__device__ __forceinline__ int small_quotient(int64_t r, int64_t d) {
+  int q = (int)((float)r / (float)d);
+  while ((int64_t)q * d > r) --q;
+  while ((int64_t)(q + 1) * d <= r) ++q;
+  return q;
+}
+
+// The line: its length, the length of a worker's part, and this lane's first request.
+struct Line {
+  int64_t u, part;
+  int64_t own;  // requests' lengths on the line, lane = request, of the first 32
+  bool bad;     // lengths that do not fit
+  __device__ __forceinline__ int64_t border(int w) const { return min(part * w, u); }
+};
+
+// A whole warp; lanes agree but for `own`.
 template <int D, bool CHUNK>
-__device__ __forceinline__ int64_t line_length(const AttnParams& p, int lane, bool* bad) {
+__device__ __forceinline__ Line measure_line(const AttnParams& p, int lane) {
+  Line l;
+  l.own = 0;
   int64_t u = 0;
   bool wrong = false;
   for (int b = lane; b < p.B; b += 32) {
     const Seq s = load_seq<D, CHUNK>(p, b);
-    u += s.per_head * p.Hkv;
+    const int64_t v = s.per_head * p.Hkv;
+    if (b == lane) l.own = v;
+    u += v;
     wrong |= s.bad;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-  *bad = __any_sync(0xffffffffu, wrong);
-  return u;
-}
-
-__device__ __forceinline__ int64_t border(int64_t u, int w, int workers) {
-  return u / workers * w + u % workers * w / workers;
+  l.bad = __any_sync(0xffffffffu, wrong);
+  l.u = u;
+  l.part = (u + p.workers - 1) / p.workers;
+  return l;
 }
 
 // A place on the line: the item holding it.  Uniform over the warp.
@@ -129,13 +149,12 @@ struct Cursor {
     return k <= 0 ? 0 : (int)min((int64_t)nk, k / K);
   }
   // the item holding place x of the line (0 <= x < U)
-  __device__ __forceinline__ void find(const AttnParams& p, int64_t x, int lane) {
+  __device__ __forceinline__ void find(const AttnParams& p, const Line& line, int64_t x, int lane) {
     int64_t before = 0;
     for (int b0 = 0;; b0 += 32) {
-      Seq t;
-      t.per_head = 0;
-      if (b0 + lane < p.B) t = load_seq<D, CHUNK>(p, b0 + lane);
-      const int64_t own = t.per_head * p.Hkv, end = warp_incl_scan(own, lane) + before;
+      int64_t own = line.own;
+      if (b0 > 0) own = b0 + lane < p.B ? load_seq<D, CHUNK>(p, b0 + lane).per_head * p.Hkv : 0;
+      const int64_t end = warp_incl_scan(own, lane) + before;
       const unsigned hit = __ballot_sync(0xffffffffu, own > 0 && end > x);
       if (hit) {
         const int src = __ffs(hit) - 1;
@@ -152,7 +171,7 @@ struct Cursor {
     }
     s = load_seq<D, CHUNK>(p, b);
     const int64_t r = x - start;
-    g = (int)(r / s.per_head);
+    g = small_quotient(r, s.per_head);
     start += g * s.per_head;
     i = 0;
     if (CHUNK) {
@@ -181,25 +200,39 @@ struct Cursor {
   }
 };
 
-__device__ __forceinline__ float* part_ml(const AttnParams& p, int D, int slot, int row) {
-  // (m, l) records follow the outputs of all 2 * workers slots
-  return p.part + (size_t)2 * p.workers * p.rows * D + ((size_t)slot * p.rows + row) * 2;
-}
+// The workspace: outputs [2 * workers slots][rows][D], (m, l) [2 * workers][rows][2], notes [workers].
+// Slot 2 w is worker w's part of an item that began before it, slot 2 w + 1
+// its part of an item that goes on behind it.
 __device__ __forceinline__ float* part_o(const AttnParams& p, int D, int slot, int row) {
   return p.part + ((size_t)slot * p.rows + row) * D;
+}
+__device__ __forceinline__ float* part_ml(const AttnParams& p, int D, int slot, int row) {
+  return p.part + (size_t)2 * p.workers * p.rows * D + ((size_t)slot * p.rows + row) * 2;
+}
+struct Note {
+  int flags;   // kCameIn ...
+  int row0;    // of the item that ends here: its first row of q,
+  int g;       // key/value head,
+  int tokens;  // and tokens
+};
+constexpr int kCameIn = 1;   // slot 2 w is in use
+constexpr int kEnded = 2;    // and that part ends its item
+constexpr int kGoesOn = 4;   // slot 2 w + 1 is in use
+__device__ __forceinline__ int4* note_of(const AttnParams& p, int D, int w) {
+  return reinterpret_cast<int4*>(p.part + (size_t)2 * p.workers * p.rows * (D + 2)) + w;
 }
 
 // Wait for a phase of an mbarrier, at most about two seconds, or until
 // another thread has given up.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = ptx::globaltimer();
+  const long long t0 = clock64();
   for (;;) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (ptx::mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
-    if (ptx::globaltimer() - t0 > 2000000000ull) {
+    if (clock64() - t0 > 4000000000ll) {
       *abort = 1;
       return false;
     }
@@ -210,6 +243,7 @@ cudaError_t launch_rows(const AttnParams& p, const CUtensorMap& kmap, const CUte
                         cudaStream_t stream);
 cudaError_t launch_chunk(const AttnParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
                          const CUtensorMap& vmap, int D, cudaStream_t stream);
+constexpr int kMaxWorkers = 1024;  // records of one item that the join lists
 constexpr int kRowWarps = 4;     // warps (workers) per CTA of the few-rows kernel
 constexpr int kMaxFewRows = 32;  // query rows of a request and head that it takes
 

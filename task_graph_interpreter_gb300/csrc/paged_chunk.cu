@@ -6,15 +6,16 @@
 // so one pass over the keys serves the whole group.  One persistent CTA per
 // SM walks its part of the work line:
 //
-//   warp 8   copies: query tiles, then key and value blocks of 128 keys, pages
+//   warps 0-7, 8-15   softmax of tile 0 and tile 1: two threads per row, each
+//            with 64 of a block's 128 keys
+//   warp 16  copies: query tiles, then key and value blocks of 128 keys, pages
 //            gathered by TMA into 128-byte-swizzled tiles, a ring of blocks
-//   warp 9   products: S_w = Q_w K^T, O_w += P_w V for the tiles w = 0, 1
-//   warp 10  division of the work: one descriptor per part of an item
-//   warp 11  values of blocks that some row does not wholly see: what was not
+//   warps 17, 19  products of tile 0 and of tile 1: S_w = Q_w K^T, O_w += P_w V
+//   warp 18  division of the work, one descriptor per part of an item; and the
+//            values of blocks that some row does not wholly see: what was not
 //            loaded becomes zero and what is not finite is set aside, since
 //            0 * NaN would reach rows behind the mask; the rows that do see
 //            such a value get it when they store their result
-//   warps 0-3, 4-7   softmax of tile 0 and tile 1, one row per thread
 //
 // Tensor memory holds S_0, S_1 (128 columns each) and O_0, O_1 (D columns):
 // all of it at D = 128, so P (bf16) overwrites S and enters the second
@@ -23,6 +24,15 @@
 // P_w V (block j), S_w (block j + 1) keeps S_w from being overwritten before
 // P_w is read, since products execute in order, and makes the barrier of
 // S_w (j + 1) cover P_w V (j) too.
+//
+// The two products of a block take the tensor cores 1025 cycles per tile (16
+// instructions of 64).  A tile's softmax has to fit beside the other tile's
+// products: with one thread per row it took 1300 cycles, and a block of both
+// tiles 3080.  Each tile's products have a warp of their own, since one
+// block's waits, instructions and commits take it some 1300 cycles; the two
+// pass a token, because instructions of both tiles mixed in the queue finish
+// together, and the tiles' softmaxes then run at the same time with the tensor
+// cores idle (3600 cycles).
 //
 // The running maximum moves only when a block exceeds it by 2^8 (the sums
 // have that much room in f32 and the probabilities' relative precision in
@@ -39,12 +49,12 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kStages = 5;
 constexpr int kSegRing = 4;
-// registers: the launch's 3 x 128 threads x 168, moved to the softmax warpgroups
-constexpr int kLaunchRegs = 168, kConsumerRegs = 224, kOtherRegs = 56;
-static_assert(2 * kConsumerRegs + kOtherRegs <= 3 * kLaunchRegs, "register shares within the launch's");
+// registers: the launch's 5 x 128 threads x 96, moved to the four softmax warpgroups
+constexpr int kLaunchRegs = 96, kConsumerRegs = 104, kOtherRegs = 64;
+static_assert(4 * kConsumerRegs + kOtherRegs <= 5 * kLaunchRegs, "register shares within the launch's");
 
 struct Segment {
   int row0;       // first query row of the item (token index in q)
@@ -61,8 +71,22 @@ template <int D>
 struct Smem {
   static constexpr int kHalf = 128 * 128;        // 128 rows of 128 bytes
   static constexpr int kTile = kHalf * (D / 64);
-  static constexpr int kBytes = 1024 + 2 * kTile + kStages * kTile;
+  static constexpr int kControl = 3072;          // barriers, descriptors, row maxima (struct Control)
+  static constexpr int kBytes = kControl + 2 * kTile + kStages * kTile;
 };
+static_assert(Smem<128>::kBytes <= 232448, "227 KB of shared memory per CTA");
+
+struct Control {
+  uint64_t kv_full[kStages], kv_empty[kStages], v_raw[kStages], q_full[2], q_empty[2], s_full[2], p_full[2][2], o_done[2],
+      turn[2], row_bar[2][4], seg_full[kSegRing], seg_empty[kSegRing], drained[2], m_bar;
+  Segment segs[kSegRing];
+  int odd[kSegRing];      // a value set aside in this part
+  uint32_t missing[8];    // per key block (ring): pages of it that are not in the pool, one bit each
+  uint32_t tmem;
+  int gave_up;
+  float row[2][2][128];   // per tile and half: rows' maxima, at the end their sums
+};
+static_assert(sizeof(Control) <= Smem<128>::kControl, "control block");
 
 __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs)); }
 __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs)); }
@@ -90,7 +114,7 @@ __device__ __forceinline__ void zero_values(uint32_t v0, int valid, uint32_t mis
 // Bits of a bf16 pair that belong to a value that is not finite.
 __device__ __forceinline__ uint32_t odd_bits(uint32_t w) { return __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u); }
 
-// For 32 columns of a row's result, the sum of the values that are not finite, of the
+// For 16 columns of a row's result, the sum of the values that are not finite, of the
 // keys it sees in this part's masked blocks (they were set aside).
 __device__ __noinline__ void add_odd_values(const AttnParams& p, const Segment& s, int lim, int D, int c, float* add) {
   const int pmask = (1 << p.page_shift) - 1;
@@ -99,7 +123,7 @@ __device__ __noinline__ void add_odd_values(const AttnParams& p, const Segment& 
     if ((unsigned)id >= (unsigned)p.num_pages) continue;
     const __nv_bfloat16* v =
         p.v + ((((int64_t)id * p.Hkv + s.g) << p.page_shift) + (key & pmask)) * D + c;
-    for (int e = 0; e < 32; ++e) {
+    for (int e = 0; e < 16; ++e) {
       const float x = __bfloat162float(v[e]);
       if (!isfinite(x)) add[e] += x;
     }
@@ -113,62 +137,79 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Smem<D>;
   constexpr int NH = D / 64;
   constexpr uint32_t kSCol = 0, kOCol = 256;  // tensor memory columns of S_0, S_1 and O_0, O_1
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t kv_full[kStages], kv_empty[kStages], q_full, q_empty, s_full[2], p_full[2],
-      o_done[2], v_raw[kStages], seg_full[kSegRing], seg_empty[kSegRing], drained;
-  __shared__ Segment segs[kSegRing];
-  __shared__ int odd[kSegRing];  // a value set aside in this part
-  __shared__ uint32_t tmem_s;
-  __shared__ int gave_up;
-  __shared__ uint32_t missing[8];  // per key block (ring): pages of it that are not in the pool, one bit each
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t* qt = base;                  // [2][NH][128 rows][128 B]
-  uint8_t* ring = base + 2 * S::kTile;  // [kStages][NH][128 keys][128 B]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // no static shared memory: the dynamic part starts 1024-byte aligned, as the swizzled tiles need
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Control& ctl = *reinterpret_cast<Control*>(smem_raw);
+  auto &kv_full = ctl.kv_full, &kv_empty = ctl.kv_empty, &v_raw = ctl.v_raw;
+  auto &q_full = ctl.q_full, &q_empty = ctl.q_empty, &s_full = ctl.s_full, &o_done = ctl.o_done,
+       &turn = ctl.turn, &drained = ctl.drained;
+  auto &seg_full = ctl.seg_full, &seg_empty = ctl.seg_empty;
+  auto& p_full = ctl.p_full;  // [tile][half of the scores handed over]
+  auto& m_bar = ctl.m_bar;
+  auto& segs = ctl.segs;
+  auto& odd = ctl.odd;
+  auto& missing = ctl.missing;
+  int& gave_up = ctl.gave_up;
+  uint8_t* qt = smem_raw + S::kControl;  // [2][NH][128 rows][128 B]
+  uint8_t* ring = qt + 2 * S::kTile;     // [kStages][NH][128 keys][128 B]
+  // (broadcast, so that the compiler knows a warp's role and what follows from it uniform)
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  if (smem_addr(smem_raw) & 1023u) {
+    if (threadIdx.x == 0) set_status(p.status, MK_DEV_RING_TIMEOUT);
+    return;
+  }
   if (threadIdx.x == 0) {
     gave_up = 0;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&kv_empty[i], 2);
       mbar_init(&v_raw[i], 1);
     }
-    mbar_init(&q_full, 1);
-    mbar_init(&q_empty, 1);
-    mbar_init(&drained, 1);
+    mbar_init(&m_bar, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&drained[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i][0], 8);
+      mbar_init(&p_full[i][1], 8);
+      mbar_init(&turn[i], 1);
+      for (int k = 0; k < 4; ++k) mbar_init(&ctl.row_bar[i][k], 2);
       mbar_init(&o_done[i], 1);
     }
     for (int i = 0; i < kSegRing; ++i) {
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_empty[i], 11);  // 8 softmax warps, the copy, product and value warps
+      mbar_init(&seg_empty[i], kThreads / 32);
     }
     fence_mbar_init();
   }
-  if (warp == 9) {
-    tmem_alloc(&tmem_s, 512);
+  if (warp == 17) {
+    tmem_alloc(&ctl.tmem, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   launch_dependents();
-  const uint32_t tmem = tmem_s;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0);
   const int pmask = (1 << p.page_shift) - 1;
 
-  if (warp >= 8) {
+  if (warp >= 16) {
     reg_dec();
-    if (warp == 10) {
-      // ------------------------------------------------ division of the work
-      bool bad;
-      const int64_t u = line_length<D, true>(p, lane, &bad);
-      if (bad && blockIdx.x == 0 && lane == 0) set_status(p.status, MK_DEV_BAD_INDEX);
-      const int64_t x0 = border(u, blockIdx.x, p.workers), x1 = border(u, blockIdx.x + 1, p.workers);
+    if (warp == 18) {
+      // ------------------------------------------------ division of the work; values behind masks
+      const Line line = measure_line<D, true>(p, lane);
+      if (line.bad && blockIdx.x == 0 && lane == 0) set_status(p.status, MK_DEV_BAD_INDEX);
+      const int64_t x0 = line.border(blockIdx.x), x1 = line.border(blockIdx.x + 1);
+      int4 note = make_int4(0, 0, 0, 0);
+      if (lane == 0) *note_of(p, D, blockIdx.x) = note;
       Cursor<D, true> c;
-      bool more = !bad && x0 < x1;
-      if (more) c.find(p, x0, lane);
-      for (uint32_t i = 0;; ++i) {
+      bool more = !line.bad && x0 < x1, told = false;
+      if (more) c.find(p, line, x0, lane);
+      uint32_t made = 0;
+      // the next part of this CTA, or the note that there is none
+      auto publish = [&]() {
+        if (told) return true;
         int k0 = 0, k1 = 0, nk = 0;
         while (more) {
           nk = c.blocks(p);
@@ -178,40 +219,108 @@ __global__ void __launch_bounds__(kThreads, 1)
           c.next(p);
           more = c.b < p.B && c.start < x1;
         }
-        const int st = i % kSegRing;
-        if (!wait_phase(&seg_empty[st], ((i / kSegRing) & 1) ^ 1, &gave_up)) break;
+        const int st = made % kSegRing;
+        if (!wait_phase(&seg_empty[st], ((made / kSegRing) & 1) ^ 1, &gave_up)) return false;
         if (lane == 0) {
-          Segment s;
+          Segment& s = segs[st];
           s.valid = more ? 1 : 0;
           if (more) {
+            const int t0 = c.i * 2 * p.tq;
             s.b = c.b;
             s.g = c.g;
             s.ctx = c.s.ctx;
             s.n = c.s.n;
-            s.t0 = c.i * 2 * p.tq;
-            s.row0 = p.cu[c.b] + s.t0;
+            s.t0 = t0;
+            s.row0 = p.cu[c.b] + t0;
             s.k0 = k0;
             s.k1 = k1;
             s.slot = k0 == 0 && k1 == nk ? -1 : 2 * (int)blockIdx.x + (k0 == 0 ? 1 : 0);
+            if (s.slot >= 0) {
+              note.x |= k0 == 0 ? kGoesOn : k1 == nk ? kCameIn | kEnded : kCameIn;
+              if (k0 != 0) {
+                note.y = s.row0;
+                note.z = c.g;
+                note.w = min(2 * p.tq, c.s.n - t0);
+              }
+              *note_of(p, D, blockIdx.x) = note;
+            }
+#pragma unroll
             for (int w = 0; w < 2; ++w) {
-              const int first = s.t0 + w * p.tq, last = min(first + p.tq, s.n) - 1;
-              s.end[w] = first < s.n ? max(k0, min(k1, (s.ctx + last) / 128 + 1)) : k0;
+              const int first = t0 + w * p.tq, last = min(first + p.tq, c.s.n) - 1;
+              s.end[w] = first < c.s.n ? max(k0, min(k1, (c.s.ctx + last) / 128 + 1)) : k0;
             }
           }
-          segs[st] = s;
           odd[st] = 0;
           mbar_arrive(&seg_full[st]);
         }
         __syncwarp();
-        if (!more) break;
-        c.next(p);
-        more = c.b < p.B && c.start < x1;
+        ++made;
+        told = !more;
+        if (more) {
+          c.next(p);
+          more = c.b < p.B && c.start < x1;
+        }
+        return true;
+      };
+      const uint32_t r0 = smem_addr(ring);
+      uint32_t it = 0, blk = 0, raw_phase = 0;
+      bool ok = publish() && publish();
+      for (uint32_t i = 0; ok; ++i) {
+        const int sst = i % kSegRing;
+        if (!segs[sst].valid) break;
+        const int ctx = segs[sst].ctx, n = segs[sst].n, k0 = segs[sst].k0, k1 = segs[sst].k1, jd = first_masked(segs[sst]);
+        for (int k = max(k0, jd); k < k1; ++k) {
+          const uint32_t vit = it + 2 * (k - k0) + 1;
+          const int st = vit % kStages;
+          if (!(ok = wait_phase(&v_raw[st], (raw_phase >> st) & 1, &gave_up))) break;
+          raw_phase ^= 1u << st;
+          const uint32_t v0 = r0 + st * S::kTile;
+          const int valid = min(128, ctx + n - k * 128);
+          const uint32_t miss = missing[(blk + k - k0) & 7];
+          if (valid < 128 || miss) zero_values<D>(v0, valid, miss, p.page_shift, lane);
+          // 0 * v summed over the block is zero unless some v is not finite: one packed instruction per pair
+          __nv_bfloat162 acc[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[q] = __float2bfloat162_rn(0.f);
+          const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+#pragma unroll 4
+          for (int e = lane; e < valid * 8; e += 32) {
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+              const uint4 v = lds128(v0 + h * S::kHalf + e * 16);
+              const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) acc[q] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u[q]), zero, acc[q]);
+            }
+          }
+          const __nv_bfloat162 sum = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
+          const bool any = __hisnan(__low2bfloat16(sum)) || __hisnan(__high2bfloat16(sum));
+          if (__any_sync(0xffffffffu, any)) {
+            for (int e = lane; e < valid * 32; e += 32) {
+              for (int h = 0; h < NH; ++h) {
+                const uint32_t a = v0 + h * S::kHalf + e * 4, v = lds32(a), o = odd_bits(v);
+                if (o) sts32(a, v & ~o);
+              }
+            }
+            if (lane == 0) odd[sst] = 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(&kv_full[st]);
+          __syncwarp();
+        }
+        if (!ok) break;
+        it += 2 * (k1 - k0);
+        blk += k1 - k0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_empty[sst]);
+        ok = publish();
       }
-    } else if (warp == 8) {
+    } else if (warp == 16) {
       // ------------------------------------------------ copies
       const int box = min(128, pmask + 1), npg = 128 / box;
-      uint32_t it = 0, nq = 0;  // key and value blocks; query tiles
-      uint32_t raw_at = 0, raw_phase = 0;  // stages last filled through v_raw, and its phases
+      uint32_t it = 0, nq = 0;  // key and value blocks; query tile pairs
+      uint32_t raw_at = 0, raw_phase = 0, misses = 0, hole = 0;  // stages last filled through v_raw, and its phases; uses of m_bar
       for (uint32_t i = 0;; ++i) {
         const int sst = i % kSegRing;
         if (!wait_phase(&seg_full[sst], (i / kSegRing) & 1, &gave_up)) break;
@@ -219,15 +328,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&seg_empty[sst]);
         if (!s.valid) break;
-        if (!wait_phase(&q_empty, (nq & 1) ^ 1, &gave_up)) break;
-        ++nq;
-        if (lane == 0) {
-          const int tiles = s.t0 + p.tq < s.n ? 2 : 1;
-          mbar_arrive_expect_tx(&q_full, tiles * NH * p.tq * p.G * 128);
-          for (int w = 0; w < tiles; ++w)
-            for (int h = 0; h < NH; ++h)
-              tma_load_3d(qt + w * S::kTile + h * S::kHalf, &qmap, h * 64, s.g * p.G, s.row0 + w * p.tq, &q_full);
-        }
         const int L = s.ctx + s.n, jd = first_masked(s);
         bool ok = true;
         for (int k = s.k0; k < s.k1 && ok; ++k) {
@@ -240,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (in && !good) set_status(p.status, MK_DEV_BAD_INDEX);
           const unsigned lanes = __ballot_sync(0xffffffffu, good);
           unsigned miss = __ballot_sync(0xffffffffu, in && !good && half == 0);
-          if (NH == 2) {  // one bit per page
+          if (NH == 2 && miss) {  // one bit per page
             unsigned m2 = 0;
             for (int j = 0; j < npg; ++j) m2 |= ((miss >> (2 * j)) & 1) << j;
             miss = m2;
@@ -248,13 +348,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = ((id * p.Hkv + s.g) << p.page_shift) + (key & pmask);
           for (int v = 0; v < 2; ++v, ++it) {
             const int st = it % kStages;
-            if (!wait_phase(&kv_empty[st], ((it / kStages) & 1) ^ 1, &gave_up)) {
-              ok = false;
-              break;
-            }
-            // values of a masked block go by the value warp, which passes them on as full
-            const bool raw = v == 1 && k >= jd;
-            uint64_t* bar = raw ? &v_raw[st] : &kv_full[st];
+            if (!(ok = wait_phase(&kv_empty[st], ((it / kStages) & 1) ^ 1, &gave_up))) break;
+            // values of a masked block go by warp 18, which passes them on as full; those of other
+            // blocks with a missing page by this warp
+            const bool raw = v == 1 && k >= jd, holes = v == 1 && k < jd && miss;
+            uint64_t* bar = raw ? &v_raw[st] : holes ? &m_bar : &kv_full[st];
             raw_at = raw ? raw_at | 1u << st : raw_at & ~(1u << st);
             raw_phase ^= raw ? 1u << st : 0u;
             if (lane == 0) {
@@ -265,6 +363,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (good)
               tma_load_2d(ring + st * S::kTile + half * S::kHalf + pg * box * 128, v ? &vmap : &kmap, half * 64, row,
                           bar);
+            if (holes) {
+              hole = 1;
+              if (!(ok = wait_phase(&m_bar, misses & 1, &gave_up))) break;
+              ++misses;
+              hole = 0;
+              zero_values<D>(smem_addr(ring) + st * S::kTile, 128, miss, p.page_shift, lane);
+              if (lane == 0) mbar_arrive(&kv_full[st]);
+            }
+            __syncwarp();
+          }
+          if (ok && k == s.k0) {
+            // the query tiles, behind the first keys and values, which need not wait for the last item's products
+#pragma unroll
+              for (int w = 0; w < 2 && ok; ++w) {
+              ok = wait_phase(&q_empty[w], (nq & 1) ^ 1, &gave_up);
+              if (ok && lane == 0) {
+                // (a second tile without tokens is not read)
+                const bool some = w == 0 || s.t0 + p.tq < s.n;
+                mbar_arrive_expect_tx(&q_full[w], some ? NH * p.tq * p.G * 128 : 0);
+                for (int h = 0; h < NH && some; ++h)
+                  tma_load_3d(qt + w * S::kTile + h * S::kHalf, &qmap, h * 64, s.g * p.G, s.row0 + w * p.tq, &q_full[w]);
+              }
+              __syncwarp();
+            }
+            nq += ok;
           }
         }
         if (!ok) break;
@@ -280,195 +403,198 @@ __global__ void __launch_bounds__(kThreads, 1)
                ++j) {
           }
         }
-        if (nq)
-          for (int j = 0; j < 100000 && !mbar_try_wait(&q_full, (nq - 1) & 1); ++j) {
+        for (int j = 0; hole && j < 100000 && !mbar_try_wait(&m_bar, misses & 1); ++j) {
+        }
+        for (int w = 0; w < 2 && nq; ++w)
+          for (int j = 0; j < 100000 && !mbar_try_wait(&q_full[w], (nq - 1) & 1); ++j) {
           }
       }
-    } else if (warp == 9) {
-      // ------------------------------------------------ products
+    } else {
+      // ------------------------------------------------ products of tile w
+      // Whatever steers this loop or makes up a descriptor is a vote's or a broadcast's result: the compiler
+      // then knows it uniform and keeps the descriptors in uniform registers (otherwise each instruction
+      // took 70 to 100 cycles to issue, the tensor cores 64 to execute).
+      const int w = warp == 17 ? 0 : 1;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_phase(bar, parity, &gave_up)) != 0;
+      };
       const uint32_t idesc_s = idesc_bf16_f32(128, 128);
       const uint32_t idesc_o = idesc_bf16_f32(128, D) | kIdescBMnMajor;
-      const uint32_t q0 = smem_addr(qt), r0 = smem_addr(ring);
-      uint32_t it = 0, blk = 0, np[2] = {0, 0};
+      const uint32_t r0 = smem_addr(ring);
+      // low words of the operands' descriptors; a 16-element step along a 128-byte row adds 32
+      // bytes, 16 value rows 2048, a stage its size
+      const uint64_t qd = smem_desc_sw128(smem_addr(qt) + w * S::kTile, 1024u), kd = smem_desc_sw128(r0, 1024u),
+                     vd = smem_desc_sw128_mn(r0, S::kHalf, 1024u);
+      const uint32_t khi = (uint32_t)(kd >> 32), vhi = (uint32_t)(vd >> 32);
+      const uint32_t ts = tmem + kSCol + w * 128, to = tmem + kOCol + w * D;
+      const uint32_t a_lo = (uint32_t)qd;
+      uint32_t st = 0, ph = 0, np = 0, nturn = 0;  // ring place; P handed over; turns taken
       bool ok = true;
+      auto advance = [&]() {
+        if (++st == kStages) {
+          st = 0;
+          ph ^= 1;
+        }
+      };
       for (uint32_t i = 0; ok; ++i) {
         const int sst = i % kSegRing;
-        if (!(ok = wait_phase(&seg_full[sst], (i / kSegRing) & 1, &gave_up))) break;
-        const Segment s = segs[sst];
+        if (!(ok = wait(&seg_full[sst], (i / kSegRing) & 1))) break;
+        const int valid = __shfl_sync(0xffffffffu, segs[sst].valid, 0), k0 = segs[sst].k0;
+        const int nt = __shfl_sync(0xffffffffu, segs[sst].k1 - k0, 0);
+        const int ntw = __shfl_sync(0xffffffffu, segs[sst].end[w] - k0, 0);
         __syncwarp();
         if (lane == 0) mbar_arrive(&seg_empty[sst]);
-        if (!s.valid) break;
-        if (!(ok = wait_phase(&q_full, i & 1, &gave_up))) break;
-        const int nt = s.k1 - s.k0, jd = first_masked(s);
-        const int ntw[2] = {s.end[0] - s.k0, s.end[1] - s.k0};
-        auto product_s = [&](int w, uint32_t kit) {
-          const uint32_t a0 = q0 + w * S::kTile, b0 = r0 + (kit % kStages) * S::kTile;
-          if (lane == 0) {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              tc_mma_bf16(tmem + kSCol + w * 128, smem_desc_sw128(a0 + (kk >> 2) * S::kHalf, 1024u) + (kk & 3) * 2u,
-                          smem_desc_sw128(b0 + (kk >> 2) * S::kHalf, 1024u) + (kk & 3) * 2u, idesc_s, kk != 0 ? 1u : 0u);
-            tc_commit(&s_full[w]);
+        if (!valid) break;
+        if (!(ok = wait(&q_full[w], i & 1))) break;
+        if (ntw == 0 && lane == 0) mbar_arrive(&q_empty[w]);
+        // blocks in the order of the ring: K 0, V 0, K 1, V 1, ...; P V (block j) before S (block j + 1).  A
+        // block that this tile does not need is handed back as it comes
+        for (int j = -1; j < nt; ++j) {
+          const uint32_t vst = st;
+          if (j >= 0) {
+            if (!(ok = wait(&kv_full[st], ph))) break;
+            advance();
           }
-          __syncwarp();
-        };
-        if (!(ok = wait_phase(&kv_full[it % kStages], (it / kStages) & 1, &gave_up))) break;
-        tc_fence_after();
-        for (int w = 0; w < 2; ++w)
-          if (ntw[w] > 0) product_s(w, it);
-        if (lane == 0) {
-          tc_commit(&kv_empty[it % kStages]);
-          if (nt == 1) tc_commit(&q_empty);
-        }
-        for (int j = 0; j < nt && ok; ++j) {
-          const uint32_t vit = it + 2 * j + 1, kit = it + 2 * j + 2;
-          bool have_v = false, have_k = false;
-          for (int w = 0; w < 2 && ok; ++w) {
-            if (j >= ntw[w]) continue;
-            if (!have_v) {
-              if (!(ok = wait_phase(&kv_full[vit % kStages], (vit / kStages) & 1, &gave_up))) break;
-              have_v = true;
-              // (in masked blocks the value warp has seen to missing pages)
-              const uint32_t miss = s.k0 + j < jd ? missing[(blk + j) & 7] : 0u;
-              if (miss) zero_values<D>(r0 + (vit % kStages) * S::kTile, 128, miss, p.page_shift, lane);
-            }
-            if (!(ok = wait_phase(&p_full[w], np[w] & 1, &gave_up))) break;
-            ++np[w];
-            tc_fence_after();
-            if (lane == 0) {
-              const uint32_t v0 = r0 + (vit % kStages) * S::kTile;
+          const uint32_t kst = st;
+          if (j + 1 < nt) {
+            if (!(ok = wait(&kv_full[st], ph))) break;
+            advance();
+          }
+          const bool pv = j >= 0 && j < ntw, qk = j + 1 < ntw;
+          if (pv && !(ok = wait(&p_full[w][0], np & 1))) break;
+          // tile 0 starts; then each block's products of one tile, then of the other
+          if (!(ok = wait(&turn[w], (nturn & 1) ^ (w ^ 1)))) break;
+          ++nturn;
+          tc_fence_after();
+          if (pv) {
+            const uint32_t b_lo = (uint32_t)vd + vst * (S::kTile >> 4);
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                tc_mma_bf16_ts(tmem + kOCol + w * D, tmem + kSCol + w * 128 + kk * 8,
-                               smem_desc_sw128_mn(v0 + kk * 2048u, S::kHalf, 1024u), idesc_o, (j | kk) != 0 ? 1u : 0u);
-            }
-            __syncwarp();
-            if (j + 1 < ntw[w]) {
-              if (!have_k) {
-                if (!(ok = wait_phase(&kv_full[kit % kStages], (kit / kStages) & 1, &gave_up))) break;
-                have_k = true;
+            for (int c = 0; c < 2; ++c) {
+              if (c == 1) {
+                if (!(ok = wait(&p_full[w][1], np & 1))) break;
                 tc_fence_after();
               }
-              product_s(w, kit);
-            } else if (lane == 0) {
-              tc_commit(&o_done[w]);
+              if (elect_one()) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int kk = (e >> 1) * 4 + c * 2 + (e & 1);  // 16 keys; the second half's P lies 64 columns on
+                  tc_mma_bf16_ts_lo(to, ts + (kk >> 2) * 64 + (kk & 3) * 8, b_lo + kk * 128, vhi, idesc_o,
+                                    c + e != 0 ? 1u : j != 0 ? 1u : 0u);
+                }
+                if (c == 1) {
+                  tc_commit(&kv_empty[vst]);
+                  if (!qk) tc_commit(&o_done[w]);
+                }
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+            ++np;
+          } else if (j >= 0 && lane == 0) {
+            mbar_arrive(&kv_empty[vst]);
+          }
+          if (qk) {
+            const uint32_t b_lo = (uint32_t)kd + kst * (S::kTile >> 4);
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                tc_mma_bf16_lo(ts, a_lo + (kk >> 2) * (S::kHalf >> 4) + (kk & 3) * 2, khi,
+                               b_lo + (kk >> 2) * (S::kHalf >> 4) + (kk & 3) * 2, khi, idesc_s, kk != 0 ? 1u : 0u);
+                // the other tile's warp takes a while to see its turn
+                if (kk == D / 32 - 1) mbar_arrive(&turn[w ^ 1]);
+              }
+              tc_commit(&s_full[w]);
+              tc_commit(&kv_empty[kst]);
+              if (j + 2 == ntw) tc_commit(&q_empty[w]);
+            }
+            __syncwarp();
+          } else {
+            if (lane == 0) {
+              mbar_arrive(&turn[w ^ 1]);
+              if (j + 1 < nt) mbar_arrive(&kv_empty[kst]);
             }
             __syncwarp();
           }
-          if (!ok) break;
-          if (lane == 0) {
-            tc_commit(&kv_empty[vit % kStages]);
-            if (j + 1 < nt) tc_commit(&kv_empty[kit % kStages]);
-            if (j + 2 == nt) tc_commit(&q_empty);
-          }
-          __syncwarp();
         }
-        it += 2 * nt;
-        blk += nt;
       }
       if (*(volatile int*)&gave_up) {
         // products in flight end before the tensor memory is freed
-        if (lane == 0) tc_commit(&drained);
-        for (int j = 0; j < 100000 && !mbar_try_wait(&drained, 0); ++j) {
-        }
-      }
-    } else {
-      // ------------------------------------------------ values behind masks
-      const uint32_t r0 = smem_addr(ring);
-      uint32_t it = 0, blk = 0, raw_phase = 0;
-      bool ok = true;
-      for (uint32_t i = 0; ok; ++i) {
-        const int sst = i % kSegRing;
-        if (!wait_phase(&seg_full[sst], (i / kSegRing) & 1, &gave_up)) break;
-        const Segment s = segs[sst];
-        if (!s.valid) break;
-        for (int k = max(s.k0, first_masked(s)); k < s.k1; ++k) {
-          const uint32_t vit = it + 2 * (k - s.k0) + 1;
-          const int st = vit % kStages;
-          if (!(ok = wait_phase(&v_raw[st], (raw_phase >> st) & 1, &gave_up))) break;
-          raw_phase ^= 1u << st;
-          const uint32_t v0 = r0 + st * S::kTile;
-          const int valid = min(128, s.ctx + s.n - k * 128);
-          const uint32_t miss = missing[(blk + k - s.k0) & 7];
-          if (valid < 128 || miss) zero_values<D>(v0, valid, miss, p.page_shift, lane);
-          uint32_t any = 0;
-#pragma unroll 4
-          for (int e = lane; e < valid * 8; e += 32) {
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-              const uint4 v = lds128(v0 + h * S::kHalf + e * 16);
-              any |= odd_bits(v.x) | odd_bits(v.y) | odd_bits(v.z) | odd_bits(v.w);
-            }
-          }
-          if (__any_sync(0xffffffffu, any != 0)) {
-            for (int e = lane; e < valid * 32; e += 32) {
-              for (int h = 0; h < NH; ++h) {
-                const uint32_t a = v0 + h * S::kHalf + e * 4, v = lds32(a), o = odd_bits(v);
-                if (o) sts32(a, v & ~o);
-              }
-            }
-            if (lane == 0) odd[sst] = 1;
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          if (lane == 0) mbar_arrive(&kv_full[st]);
-          __syncwarp();
-        }
-        it += 2 * (s.k1 - s.k0);
-        blk += s.k1 - s.k0;
+        if (elect_one()) tc_commit(&drained[w]);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&seg_empty[sst]);
+        for (int j = 0; j < 100000 && !mbar_try_wait(&drained[w], 0); ++j) {
+        }
       }
     }
   } else {
-    // -------------------------------------------------- softmax: one row per thread
+    // -------------------------------------------------- softmax: two threads per row
     reg_inc();
-    const int w = warp >> 2, row = threadIdx.x & 127;
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's tensor-memory lanes (lane field, bits 16 up)
-    const uint32_t ts = tmem + lanes + kSCol + w * 128, to = tmem + lanes + kOCol + w * D;
-    const int tok_in = row / p.G, head = row % p.G;
-    uint32_t ns = 0, no = 0, blk = 0;
+    // (104 registers, 64 of them a block's scores: what only the start and the end of a part need is
+    // worked out there again)
+    const int w = warp >> 3, hh = (warp >> 2) & 1;
+    // this warp's lanes (lane field, bits 16 up) and its half of the tile's columns of S; P takes the
+    // first half of those
+    const uint32_t ts = tmem + ((uint32_t)(warp & 3) << 21) + kSCol + w * 128 + hh * 64;
+    const uint32_t mine_s = smem_addr(&ctl.row[w][hh][(warp & 3) * 32 + lane]);
+    uint64_t* pair = &ctl.row_bar[w][warp & 3];
+    uint32_t ns = 0, no = 0, nx = 0, blk = 0;
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair);
+      return wait_phase(pair, nx++ & 1, &gave_up);
+    };
+    // the value that the row's other thread has for this one's
+    auto exchange = [&](float mine, float& other) {
+      sts32(mine_s, __float_as_uint(mine));
+      if (!meet()) return false;
+      other = __uint_as_float(lds32(hh ? mine_s - 512 : mine_s + 512));
+      return true;
+    };
     for (uint32_t i = 0;; ++i) {
-      const int sst = i % kSegRing;
-      if (!wait_phase(&seg_full[sst], (i / kSegRing) & 1, &gave_up)) break;
-      const Segment s = segs[sst];
-      if (!s.valid) break;
-      const int tok = s.t0 + w * p.tq + tok_in;  // in the request
-      const bool mine = tok_in < p.tq && tok < s.n;
-      const int lim = min(s.ctx + tok, s.ctx + s.n - 1);  // the last key this row sees
-      const int lim0 = s.ctx + s.t0 + w * p.tq;           // ... and the tile's first row
-      const int nt = s.end[w] - s.k0;
+      if (!wait_phase(&seg_full[i % kSegRing], (i / kSegRing) & 1, &gave_up)) break;
+      if (!segs[i % kSegRing].valid) break;
+      int nt, jm;
+      {
+        const Segment& s = segs[i % kSegRing];
+        nt = s.end[w] - s.k0;
+        // the first block that this tile does not wholly see
+        jm = ((s.ctx + s.t0 + w * p.tq + 1) >> 7) - s.k0;
+      }
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       for (int j = 0; j < nt; ++j) {
         if (!(ok = wait_phase(&s_full[w], ns & 1, &gave_up))) break;
         ++ns;
         tc_fence_after();
-        float x[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, x + c * 32);
+        float x[64];
+        tmem_ld32(ts, x);
+        tmem_ld32(ts + 32, x + 32);
         tmem_wait_ld();
-        const int key0 = (s.k0 + j) * 128;
         const uint32_t miss = missing[(blk + j) & 7];
-        if (key0 + 127 > lim0 || miss) {
-          const int last = lim - key0;
+        if (j >= jm || miss) {
+          const Segment& s = segs[i % kSegRing];
+          // the last key this row sees, counted from this thread's first
+          const int last = min(s.ctx + s.t0 + w * p.tq + ((warp & 3) * 32 + lane) / p.G, s.ctx + s.n - 1) -
+                           ((s.k0 + j) * 128 + hh * 64);
           if (miss) {
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if ((miss >> (c >> p.page_shift)) & 1) x[c] = -INFINITY;
+            for (int c = 0; c < 64; ++c)
+              if ((miss >> ((c + hh * 64) >> p.page_shift)) & 1) x[c] = -INFINITY;
           }
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
+          for (int c = 0; c < 64; ++c)
             if (c > last) x[c] = -INFINITY;
         }
         float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int c = 4; c < 128; c += 8) {
+        for (int c = 4; c < 64; c += 8) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            mx[e] = c + 4 + e < 128 ? fmaxf(fmaxf(mx[e], x[c + e]), x[c + 4 + e]) : fmaxf(mx[e], x[c + e]);
+            mx[e] = c + 4 + e < 64 ? fmaxf(fmaxf(mx[e], x[c + e]), x[c + 4 + e]) : fmaxf(mx[e], x[c + e]);
         }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale;
+        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale, other;
+        // (the other thread has read this before it hands over its P, which the next block's S waits for)
+        if (!(ok = exchange(top, other))) break;
+        top = fmaxf(top, other);
         if (j == 0) {
           m = top;
         } else {
@@ -478,106 +604,101 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f = far ? ex2(m - top) : 1.f;
             if (far) m = top;
             l *= f;
+            const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + kOCol + w * D + hh * (D / 2);
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float o[32];
-              tmem_ld32(to + c, o);
-              tmem_wait_ld();
+            for (int c = 0; c < D / 2; c += 16) {
+              float o[16];
+              tmem_ld16(to + c, o);
+              uint32_t r[16];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= f;
-              tmem_st32(to + c, o);
+              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(o[e] * f);
+              tmem_st16(to + c, r);
             }
           }
         }
         const float mu = m == -INFINITY ? 0.f : -m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t scale2 = pair_f32(p.scale, p.scale), mu2 = pair_f32(mu, mu);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t r[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float a = ex2(fmaf(x[c * 32 + 2 * e], p.scale, mu)), b = ex2(fmaf(x[c * 32 + 2 * e + 1], p.scale, mu));
-            sum[(2 * e) & 3] += a;
-            sum[(2 * e + 1) & 3] += b;
+            const float2 y = unpair_f32(fma2(pair_f32(x[c * 32 + 2 * e], x[c * 32 + 2 * e + 1]), scale2, mu2));
+            const float a = ex2(y.x), b = ex2(y.y);
+            sum[e & 1] = add2(sum[e & 1], pair_f32(a, b));
             r[e] = pack_bf16(a, b);
           }
           tmem_st16(ts + c * 16, r);
+          // a quarter of the keys per thread and side: the product starts on the first half of P
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[w][c]);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[w]);
+        const float2 t = unpair_f32(add2(sum[0], sum[1]));
+        l += t.x + t.y;
       }
       if (!ok) break;
-      blk += s.k1 - s.k0;
       if (nt > 0) {
         if (!wait_phase(&o_done[w], no & 1, &gave_up)) break;
         ++no;
         tc_fence_after();
       }
-      const bool set_aside = nt > 0 && odd[sst];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&seg_empty[sst]);
-      const float f = l == 0.f ? 0.f : 1.0f / l;  // a row without keys is zero
-      const int64_t token = (int64_t)s.row0 + w * p.tq + tok_in;
-      if (s.slot < 0) {
-        __nv_bfloat16* dst = p.out + token * p.ld_out + (int64_t)(s.g * p.G + head) * D;
+      // the row's sum; both threads have read it before the next part's maxima go there
+      float other;
+      if (!exchange(l, other)) break;
+      l += other;
+      if (!meet()) break;
+      const Segment& s = segs[i % kSegRing];
+      blk += s.k1 - s.k0;
+      const int row = (warp & 3) * 32 + lane, tok_in = row / p.G, head = row % p.G;
+      const int tok = s.t0 + w * p.tq + tok_in;
+      const bool mine = tok_in < p.tq && tok < s.n;
+      const bool set_aside = nt > 0 && odd[i % kSegRing];
+      const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + kOCol + w * D + hh * (D / 2);
+      const float f = s.slot >= 0 ? 1.f : nt == 0 || l == 0.f ? 0.f : 1.0f / l;  // a row without keys is zero
+      __nv_bfloat16* dst = p.out + ((int64_t)s.row0 + w * p.tq + tok_in) * p.ld_out + (int64_t)(s.g * p.G + head) * D +
+                           hh * (D / 2);
+      float* rec = nullptr;
+      if (s.slot >= 0) {
+        rec = part_o(p, D, s.slot, w * 128 + row) + hh * (D / 2);
+        if (mine && hh == 0)
+          *reinterpret_cast<float2*>(part_ml(p, D, s.slot, w * 128 + row)) = make_float2(m, nt > 0 ? l : 0.f);
+      }
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          if (nt > 0) {
-            tmem_ld32(to + c, o);
-            tmem_wait_ld();
-          }
-          if (set_aside && mine) {
-            float add[32] = {};
-            add_odd_values(p, s, lim, D, c, add);
+      for (int c = 0; c < D / 2; c += 16) {
+        float o[16];
+        if (nt > 0) tmem_ld16(to + c, o);
+        if (set_aside && mine) {
+          float add[16] = {};
+          add_odd_values(p, s, min(s.ctx + tok, s.ctx + s.n - 1), D, hh * (D / 2) + c, add);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] += add[e];
-          }
-          if (mine) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (nt > 0 && l != 0.f)
-                v = make_uint4(pack_bf16(o[e] * f, o[e + 1] * f), pack_bf16(o[e + 2] * f, o[e + 3] * f),
-                               pack_bf16(o[e + 4] * f, o[e + 5] * f), pack_bf16(o[e + 6] * f, o[e + 7] * f));
-              *reinterpret_cast<uint4*>(dst + c + e) = v;
-            }
-          }
+          for (int e = 0; e < 16; ++e) o[e] += add[e];
         }
-      } else if (p.part) {
-        const int rec = w * 128 + row;
-        if (mine) *reinterpret_cast<float2*>(part_ml(p, D, s.slot, rec)) = make_float2(m, l);
-        if (nt > 0) {
-          float* dst = part_o(p, D, s.slot, rec);
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            float o[32];
-            tmem_ld32(to + c, o);
-            tmem_wait_ld();
-            if (set_aside && mine) {
-              float add[32] = {};
-              add_odd_values(p, s, lim, D, c, add);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] += add[e];
-            }
-            if (mine) {
+        for (int e = 0; e < 16; ++e) o[e] = f == 0.f ? 0.f : o[e] * f;
+        if (mine && !rec) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<float4*>(dst + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            }
-          }
+          for (int e = 0; e < 16; e += 8)
+            *reinterpret_cast<uint4*>(dst + c + e) =
+                make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]), pack_bf16(o[e + 4], o[e + 5]),
+                           pack_bf16(o[e + 6], o[e + 7]));
+        } else if (mine && nt > 0) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(rec + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
       tc_fence_before();  // O is read before the next part's first P is handed over
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_empty[i % kSegRing]);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 template <int D>

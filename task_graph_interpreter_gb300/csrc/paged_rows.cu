@@ -68,20 +68,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   launch_dependents();
 
   const int w = blockIdx.x * kRowWarps + warp;
-  bool bad;
-  const int64_t u = line_length<D, false>(p, lane, &bad);
-  if (bad) {
-    if (w == 0 && lane == 0) set_status(p.status, MK_DEV_BAD_INDEX);
-    return;
-  }
-  const int64_t x0 = border(u, w, p.workers), x1 = border(u, w + 1, p.workers);
-  if (x0 >= x1) return;
+  const Line line = measure_line<D, false>(p, lane);
+  if (line.bad && w == 0 && lane == 0) set_status(p.status, MK_DEV_BAD_INDEX);
+  const int64_t x0 = line.border(w), x1 = line.border(w + 1);
+  int4 note = make_int4(0, 0, 0, 0);
+  if (lane == 0) *note_of(p, D, w) = note;
+  if (line.bad || x0 >= x1) return;
   const int pmask = (1 << p.page_shift) - 1;
   const int box = min(KU, pmask + 1);     // keys per TMA box
   const int npg = KU / box;               // pages a block touches
 
   Cursor<D, false> cons;
-  cons.find(p, x0, lane);
+  cons.find(p, line, x0, lane);
   Cursor<D, false> prod = cons;
   int pk = 0, pke = 0;        // the producer's next block and the end of its item's part
   bool pdone = false;
@@ -365,6 +363,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const bool whole = kb == 0 && cke == nk;
     const int slot = 2 * w + (kb == 0 ? 1 : 0);
+    if (!whole) {
+      note.x |= kb == 0 ? kGoesOn : cke == nk ? kCameIn | kEnded : kCameIn;
+      if (kb != 0) {
+        note.y = p.cu[cons.b];
+        note.z = cons.g;
+        note.w = n;
+      }
+    }
     __nv_bfloat16* ob = p.out + (int64_t)p.cu[cons.b] * p.ld_out + (int64_t)cons.g * p.G * D;
 #pragma unroll
     for (int i = 0; i < 2 * NM; ++i) {
@@ -388,55 +394,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     more = next_part(cons, ck, cke);
   }
+  if (lane == 0 && note.x) *note_of(p, D, w) = note;
 }
 
-// Join of the items that workers' borders cut: block x is border x + 1; the
-// first border inside an item does the item.  Its partial records are the
-// second slot of the worker before the border, then the first slots of the
-// workers from the border on, in order of keys.  A warp merges a share of a
-// row's records; shares meet in shared memory.
+// Join of the items that workers' borders cut: block w looks whether an item
+// ends in worker w's part that began before it.  Its partial records are the
+// second slot of the nearest worker before whose last item goes on, then the
+// first slots of the workers from there to w, in order of keys.  A warp
+// merges a share of a row's records; shares meet in shared memory.
 constexpr int kJoinWarps = 16;
 
 template <int D, bool CHUNK>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int E = D / 32;
   __shared__ float so[kJoinWarps][D], sml[kJoinWarps][2];
+  __shared__ int slots[kMaxWorkers + 1];
+  __shared__ int count_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = blockIdx.x + 1;
-  bool bad;
-  const int64_t u = line_length<D, CHUNK>(p, lane, &bad);
-  if (bad || u == 0) return;
-  const int64_t xc = border(u, c, p.workers);
-  if (xc >= u) return;
-  Cursor<D, CHUNK> it;
-  it.find(p, xc, lane);
-  const int nk = it.blocks(p), k = it.block_at(xc, nk);
-  if (k <= 0 || k >= nk) return;
-  const int64_t xb = border(u, c - 1, p.workers);
-  if (xb > it.start && it.block_at(xb, nk) > 0) return;  // an earlier border is inside too
-  // records: i = 0 is worker c - 1's, i >= 1 worker c + i - 1's
-  int count = 1;
-  for (int i0 = 0;; i0 += 32) {
-    const int wk = c + i0 + lane;
-    const bool in = wk < p.workers && it.block_at(border(u, wk, p.workers), nk) < nk;
-    const unsigned b = __ballot_sync(0xffffffffu, in);
-    count += __popc(b);
-    if (b != 0xffffffffu) break;
-  }
-  int rows, row_base = 0;
-  if (CHUNK) {
-    rows = min(2 * p.tq, it.s.n - it.i * 2 * p.tq) * p.G;
-  } else {
-    rows = it.s.n * p.G;
-  }
-  const int per = (rows + gridDim.y - 1) / gridDim.y;
-  row_base = blockIdx.y * per;
-  rows = min(per, rows - row_base);
-  if (rows <= 0) return;
-  int shares = 1;
-  while (shares * 2 * rows <= kJoinWarps && shares * 8 < count) shares *= 2;
-  const int rows_at_once = kJoinWarps / shares, share = warp % shares;
+  const int w = blockIdx.x;
   wait_dependency();
+  const int4 note = *note_of(p, D, w);
+  if (!(note.x & kEnded)) return;
+  const int rows_all = note.w * p.G, per = (rows_all + gridDim.y - 1) / gridDim.y;
+  const int row_base = blockIdx.y * per, rows = min(per, rows_all - row_base);
+  if (rows <= 0) return;
+  if (warp == 0) {
+    // records from the last to the first (a worker whose part rounds to nothing left none)
+    int n = 1;
+    if (lane == 0) slots[0] = 2 * w;
+    for (int c0 = w - 1; c0 >= 0; c0 -= 32) {
+      const int c = c0 - lane, flags = c >= 0 ? note_of(p, D, c)->x : 0;
+      const unsigned begin = __ballot_sync(0xffffffffu, flags & kGoesOn);
+      const unsigned upto = begin ? (begin & -begin) - 1 : 0xffffffffu;  // workers after the one where it began
+      const unsigned in = __ballot_sync(0xffffffffu, flags & kCameIn) & upto;
+      const int at = n + __popc(in & ((1u << lane) - 1));
+      if (((in >> lane) & 1)) slots[at] = 2 * c;
+      n += __popc(in);
+      if (begin) {
+        if (lane == __ffs(begin) - 1) slots[n] = 2 * c + 1;
+        ++n;
+        break;
+      }
+    }
+    if (lane == 0) count_s = n;
+  }
+  __syncthreads();
+  const int count = count_s;
+  int shares = 1;
+  while (shares * 2 * rows <= kJoinWarps && shares * 4 < count) shares *= 2;
+  const int rows_at_once = kJoinWarps / shares, share = warp % shares;
   for (int rr0 = 0; rr0 < rows; rr0 += rows_at_once) {
     const int rr = rr0 + warp / shares;
     const bool on = rr < rows;
@@ -455,18 +461,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
         const int i = i0 + j * shares;
         ml[j] = make_float2(-INFINITY, 0.f);
         if (i < count) {
-          const int wk = c + i - 1, slot = 2 * wk + (i == 0 ? 1 : 0);
-          // a worker whose part of the item rounds to nothing left no record
-          if (i == 0 || it.block_at(border(u, wk, p.workers), nk) < it.block_at(border(u, wk + 1, p.workers), nk)) {
-            ml[j] = __ldcg(reinterpret_cast<const float2*>(part_ml(p, D, slot, rec)));
-            const float* src = part_o(p, D, slot, rec) + lane * E;
-            if constexpr (E == 4) {
-              const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
-              v[j][0] = t.x; v[j][1] = t.y; v[j][2] = t.z; v[j][3] = t.w;
-            } else {
-              const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
-              v[j][0] = t.x; v[j][1] = t.y;
-            }
+          const int slot = slots[count - 1 - i];
+          ml[j] = __ldcg(reinterpret_cast<const float2*>(part_ml(p, D, slot, rec)));
+          const float* src = part_o(p, D, slot, rec) + lane * E;
+          if constexpr (E == 4) {
+            const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
+            v[j][0] = t.x; v[j][1] = t.y; v[j][2] = t.z; v[j][3] = t.w;
+          } else {
+            const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
+            v[j][0] = t.x; v[j][1] = t.y;
           }
         }
       }
@@ -505,8 +508,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     }
     if (on && share == 0) {
       const float f = l == 0.f ? 0.f : 1.0f / l;
-      const int64_t token = (int64_t)p.cu[it.b] + (CHUNK ? it.i * 2 * p.tq : 0) + tok;
-      __nv_bfloat16* dst = p.out + token * p.ld_out + (int64_t)(it.g * p.G + head) * D + lane * E;
+      __nv_bfloat16* dst = p.out + ((int64_t)note.y + tok) * p.ld_out + (int64_t)(note.z * p.G + head) * D + lane * E;
       if constexpr (E == 4)
         *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f));
       else
@@ -520,7 +522,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
 cudaError_t launch_join(const AttnParams& p, int D, bool chunk, cudaStream_t stream) {
   if (p.workers < 2) return cudaSuccess;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(p.workers - 1), chunk ? 8u : 1u);
+  cfg.gridDim = dim3((unsigned)p.workers, chunk ? 8u : 1u);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
