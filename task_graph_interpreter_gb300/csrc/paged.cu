@@ -445,15 +445,24 @@ extern "C" int mk_qk_norm_rope(void* stream, int N, int Hq, int Hkv, int D, cons
   p.vpool = static_cast<__nv_bfloat16*>(vpool);
   p.status = status; p.N = N; p.Hq = Hq; p.Hkv = Hkv; p.num_pages = num_pages; p.eps = eps;
   while ((1 << p.page_shift) < page_size) ++p.page_shift;
-  for (int i = 0; i < D / 2; ++i) {
-    // revolutions per position, reduced below one, in units of 2^-64
-    const double f = std::fmod(std::pow(rope_theta, -2.0 * i / D) / 6.283185307179586476925, 1.0);
-    p.freq[i] = (uint64_t)std::ldexp(f, 64);
+  // the last base's frequencies: a decoder asks for the same ones in every layer
+  thread_local struct {
+    double theta = 0.0;
+    int D = 0;
+    uint64_t f[64];
+  } known;
+  if (known.theta != rope_theta || known.D != D) {
+    for (int i = 0; i < D / 2; ++i) {
+      // revolutions per position, reduced below one, in units of 2^-64
+      const double f = std::fmod(std::pow(rope_theta, -2.0 * i / D) / 6.283185307179586476925, 1.0);
+      known.f[i] = (uint64_t)std::ldexp(f, 64);
+    }
+    known.theta = rope_theta;
+    known.D = D;
   }
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return fail(MK_ERR_CUDA, "mk_qk_norm_rope: no current device");
+  for (int i = 0; i < D / 2; ++i) p.freq[i] = known.f[i];
+  int sms = 0;
+  if (int rc = device_sms("mk_qk_norm_rope", &sms)) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (qkv_dtype == MK_F32) e = D == 128 ? launch_norm<float, 128>(p, sms, s) : launch_norm<float, 64>(p, sms, s);

@@ -5,6 +5,7 @@
 #include <cuda.h>  // CUtensorMap types
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <string>
 
@@ -23,6 +24,28 @@ inline int pending_error(const char* who) {
   const cudaError_t e = cudaPeekAtLastError();
   if (e == cudaSuccess) return MK_OK;
   return fail(MK_ERR_CUDA, std::string(who) + ": an earlier CUDA error is pending: " + cudaGetErrorString(e));
+}
+
+// SMs of the current device.
+inline int device_sms(const char* who, int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return fail(MK_ERR_CUDA, std::string(who) + ": no current device");
+  return MK_OK;
+}
+
+// Let kernel `fn` use `bytes` of dynamic shared memory, once per device (`done`: that kernel's own record).
+template <typename Fn>
+cudaError_t allow_smem(Fn fn, int bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done->load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done->fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 inline int launch_result(cudaError_t e, const char* who) {

@@ -44,7 +44,7 @@ bool few_rows(int max_new, int G) { return (int64_t)max_new * G <= kMaxFewRows; 
 // Two partial records and a note per worker (paged_attention.cuh).
 size_t workspace_bytes(int max_new, int G, int D, int sms) {
   const bool few = few_rows(max_new, G);
-  const size_t workers = (size_t)sms * (few ? kRowWarps : 1), rows = !few ? 256 : max_new * G <= 16 ? 16 : 32;
+  const size_t workers = (size_t)sms * (few ? kRowWarps : 1), rows = few ? max_new * G : 256;
   return 2 * workers * rows * (D + 2) * 4 + workers * 16;
 }
 
@@ -53,14 +53,6 @@ int check_shape(const char* who, int max_new, int Hq, int Hkv, int D) {
   if (Hkv < 1 || Hkv > 1024 || Hq < Hkv || Hq % Hkv || Hq / Hkv > 128)
     return fail(MK_ERR_ARG, std::string(who) + ": need Hq a multiple of Hkv (at most 1024) with Hq/Hkv <= 128");
   if (max_new < 1) return fail(MK_ERR_ARG, std::string(who) + ": max_new must be positive");
-  return MK_OK;
-}
-
-int device_sms(const char* who, int* sms) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return fail(MK_ERR_CUDA, std::string(who) + ": no current device");
   return MK_OK;
 }
 
@@ -126,7 +118,7 @@ extern "C" int mk_paged_attention(void* stream_, int B, int N, int max_new, int 
   while ((1 << p.page_shift) < page_size) ++p.page_shift;
   p.workers = few ? sms * kRowWarps : sms;
   if (p.workers > kMaxWorkers) return fail(MK_ERR_LIMIT, "mk_paged_attention: more SMs than the join can list");
-  p.rows = few ? (max_new * G <= 16 ? 16 : 32) : 256;
+  p.rows = few ? max_new * G : 256;
   p.tq = few ? 0 : 128 / G;
 
   // pools as [rows, D], pages one after the other; a box is what one page gives a block of keys

@@ -704,12 +704,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 cudaError_t launch_chunk_t(const AttnParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
                            const CUtensorMap& vmap, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+  static std::atomic<uint64_t> allowed{0};
+  static std::atomic<int> regs{0};
+  cudaError_t e = allow_smem(chunk_kernel<D>, Smem<D>::kBytes, &allowed);
   if (e != cudaSuccess) return e;
-  cudaFuncAttributes a;
-  if ((e = cudaFuncGetAttributes(&a, chunk_kernel<D>)) != cudaSuccess) return e;
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes a;
+    if ((e = cudaFuncGetAttributes(&a, chunk_kernel<D>)) != cudaSuccess) return e;
+    regs.store(a.numRegs, std::memory_order_relaxed);
+  }
   // the register shares add up to this allocation: with fewer a warpgroup would wait for registers for ever
-  if (a.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+  if (regs.load(std::memory_order_relaxed) != kLaunchRegs) return cudaErrorInvalidKernelImage;
   chunk_kernel<D><<<(unsigned)p.workers, kThreads, Smem<D>::kBytes, stream>>>(p, qmap, kmap, vmap);
   return cudaGetLastError();
 }

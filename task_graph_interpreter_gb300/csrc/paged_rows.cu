@@ -538,7 +538,8 @@ template <int D, int NM>
 static cudaError_t launch_rows_t(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                                  cudaStream_t stream) {
   constexpr int smem = smem_bytes_rows<D>();
-  const cudaError_t e = cudaFuncSetAttribute(rows_kernel<D, NM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(rows_kernel<D, NM>, smem, &allowed);
   if (e != cudaSuccess) return e;
   rows_kernel<D, NM><<<(unsigned)(p.workers / kRowWarps), kThreads, smem, stream>>>(p, kmap, vmap);
   return cudaGetLastError();

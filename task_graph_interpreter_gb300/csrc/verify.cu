@@ -279,10 +279,8 @@ extern "C" int mk_verify_drafts(void* stream, int B, int K, int V, const float* 
   if (V > (1 << 28) || B > (1 << 24)) return fail(MK_ERR_LIMIT, "mk_verify_drafts: V at most 2^28, B at most 2^24");
   if (int rc = pending_error("mk_verify_drafts")) return rc;
   if (B == 0) return MK_OK;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return fail(MK_ERR_CUDA, "mk_verify_drafts: no current device");
+  int sms = 0;
+  if (int rc = device_sms("mk_verify_drafts", &sms)) return rc;
   VerifyParams v{};
   v.p = p; v.q = q; v.u = u; v.drafts = drafts; v.draft_len = draft_len;
   v.tokens = tokens; v.accepted = accepted; v.status = status;
