@@ -26,7 +26,8 @@ namespace {
 // up to 4096 requests) rather than exchange them, and the only barrier
 // before the held pages, the count and the returned pages are stored, since
 // those may be the arrays that other CTAs still read.
-constexpr int kPlanThreads = 512;
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanMaxB = 4096;
 constexpr int kPlanCtas = 8;
 
@@ -37,14 +38,20 @@ struct PlanParams {
   int vec;  // positions and slots 16-byte aligned
 };
 
-__device__ __forceinline__ int plan_want(const PlanParams& p, int b) {
-  return (int)(((int64_t)p.ctx[b] + p.len[b] + (1 << p.page_shift) - 1) >> p.page_shift);
-}
-
+// What a CTA knows of every request, in shared memory: exclusive sums of new
+// tokens, of pages taken and of pages returned [B + 1 each], cached tokens,
+// and the pages kept from before, min(held, want).
 struct PlanPages {
   const PlanParams& p;
-  const int32_t *goff, *boff;
+  int32_t *cu, *goff, *boff, *ctx, *kept;
   int count, top;
+  __device__ PlanPages(const PlanParams& p_, int32_t* sm) : p(p_) {
+    cu = sm;
+    goff = cu + p.B + 1;
+    boff = goff + p.B + 1;
+    ctx = boff + p.B + 1;
+    kept = ctx + p.B;
+  }
   // the a-th page taken from the stack
   __device__ int taken(int a) const {
     const int v = top - 1 - a;
@@ -53,24 +60,23 @@ struct PlanPages {
   }
   __device__ int returned(int f) const {
     const int b = upper_row(boff, p.B, f);
-    return p.table[(size_t)b * p.max_pages + plan_want(p, b) + (f - boff[b])];
+    return p.table[(size_t)b * p.max_pages + kept[b] + (f - boff[b])];
   }
   // the page holding page index j of request b after the step
-  __device__ int of(int b, int j, int held) const {
-    if (j < held) return p.table[(size_t)b * p.max_pages + j];
-    return taken(goff[b] + j - held);
+  __device__ int of(int b, int j) const {
+    if (j < kept[b]) return p.table[(size_t)b * p.max_pages + j];
+    return taken(goff[b] + j - kept[b]);
   }
 };
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
   extern __shared__ int32_t sm[];
-  int32_t* cu = sm;                 // [B + 1]
-  int32_t* goff = cu + p.B + 1;     // [B + 1] pages taken
-  int32_t* boff = goff + p.B + 1;   // [B + 1] pages returned
-  __shared__ long long warp_sum[3][kPlanThreads / 32];
+  __shared__ long long warp_sum[3][kPlanWarps];
   __shared__ int err_s;
+  PlanPages pages(p, sm);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x, ctas = gridDim.x;
+  const int count = *p.count;
   if (tid == 0) err_s = MK_DEV_OK;
   __syncthreads();
   const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
@@ -79,22 +85,29 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   int err = MK_DEV_OK;
   for (int b = b0; b < b1; ++b) {
     const int c = p.ctx[b], n = p.len[b], h = p.held[b];
+    const int64_t w = ((int64_t)c + n + (1 << p.page_shift) - 1) >> p.page_shift;
     if (c < 0 || n < 0 || h < 0 || h > p.max_pages) {
       err = MK_DEV_BAD_INDEX;
       continue;
     }
-    const int64_t w = ((int64_t)c + n + (1 << p.page_shift) - 1) >> p.page_shift;
     if (w > p.max_pages) {
       if (err == MK_DEV_OK) err = MK_DEV_CAPACITY;
       continue;
     }
+    const int grow = max((int)w - h, 0), back = max(h - (int)w, 0);
+    // (each request's own counts, until the sums before them are known)
+    pages.cu[b] = n;
+    pages.goff[b] = grow;
+    pages.boff[b] = back;
+    pages.ctx[b] = c;
+    pages.kept[b] = min(h, (int)w);
     sum[0] += n;
-    sum[1] += max((int)w - h, 0);
-    sum[2] += max(h - (int)w, 0);
+    sum[1] += grow;
+    sum[2] += back;
   }
   if (err != MK_DEV_OK) atomicCAS(&err_s, MK_DEV_OK, err);
   // exclusive scan of the three sums over the block
-  long long ex[3];
+  long long ex[3], total[3];
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     long long v = sum[k];
@@ -107,18 +120,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     ex[k] = v - sum[k];
   }
   __syncthreads();
-  long long total[3];
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
-    long long before = 0, all = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-      if (w < warp) before += warp_sum[k][w];
-      all += warp_sum[k][w];
+    long long v = warp_sum[k][lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
     }
-    ex[k] += before;
-    total[k] = all;
+    total[k] = __shfl_sync(0xffffffffu, v, 31);
+    const long long before = __shfl_sync(0xffffffffu, v, max(warp - 1, 0));
+    if (warp > 0) ex[k] += before;
   }
-  const int count = *p.count;
   int code = err_s;
   if (code == MK_DEV_OK) {
     if (count < 0 || count > p.num_pages || count + total[2] > p.num_pages) code = MK_DEV_BAD_INDEX;
@@ -126,57 +139,40 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   }
   const bool ok = code == MK_DEV_OK;
   const int ntok = ok ? (int)total[0] : 0, ngrow = ok ? (int)total[1] : 0, nback = ok ? (int)total[2] : 0;
-  if (ok) {
-    for (int b = b0; b < b1; ++b) {
-      const int n = p.len[b], h = p.held[b], w = plan_want(p, b);
-      cu[b] = (int)ex[0];
-      goff[b] = (int)ex[1];
-      boff[b] = (int)ex[2];
-      ex[0] += n;
-      ex[1] += max(w - h, 0);
-      ex[2] += max(h - w, 0);
-    }
-  } else {
-    for (int b = b0; b < b1; ++b) cu[b] = goff[b] = boff[b] = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int n = ok ? pages.cu[b] : 0, grow = ok ? pages.goff[b] : 0, back = ok ? pages.boff[b] : 0;
+    pages.cu[b] = ok ? (int)ex[0] : 0;
+    pages.goff[b] = ok ? (int)ex[1] : 0;
+    pages.boff[b] = ok ? (int)ex[2] : 0;
+    ex[0] += n;
+    ex[1] += grow;
+    ex[2] += back;
   }
   if (tid == 0) {
-    cu[p.B] = ntok;
-    goff[p.B] = ngrow;
-    boff[p.B] = nback;
+    pages.cu[p.B] = ntok;
+    pages.goff[p.B] = ngrow;
+    pages.boff[p.B] = nback;
   }
+  pages.count = count;
+  pages.top = count + nback;
   __syncthreads();
-  const PlanPages pages{p, goff, boff, count, count + nback};
   const int gtid = rank * kPlanThreads + tid, nthr = ctas * kPlanThreads;
-  // block tables: the pages taken
-  for (int a = gtid; a < ngrow; a += nthr) {
-    const int b = upper_row(goff, p.B, a);
-    const int held = plan_want(p, b) - (goff[b + 1] - goff[b]);
-    const int id = pages.taken(a);
-    p.table[(size_t)b * p.max_pages + held + (a - goff[b])] = id;
-    if ((unsigned)id >= (unsigned)p.num_pages) set_status(p.status, MK_DEV_BAD_INDEX);
-  }
   // positions and slots, four tokens a thread
   const int pmask = (1 << p.page_shift) - 1;
   for (int i0 = gtid * 4; i0 < p.max_tokens; i0 += nthr * 4) {
     int pos[4], slot[4];
-    int b = i0 < ntok ? upper_row(cu, p.B, i0) : 0, at_b = -1, at_j = -1, id = -1, ctx = 0, held = 0;
+    int b = i0 < ntok ? upper_row(pages.cu, p.B, i0) : 0, at_b = -1, at_j = -1, id = -1;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int i = i0 + k;
       pos[k] = slot[k] = -1;
       if (i < ntok) {
-        while (cu[b + 1] <= i) ++b;
-        if (b != at_b) {
-          ctx = p.ctx[b];
-          // pages kept from before: all of the held ones, or the wanted ones
-          held = plan_want(p, b) - (goff[b + 1] - goff[b]);
-          at_b = b;
-          at_j = -1;
-        }
-        pos[k] = ctx + (i - cu[b]);
+        while (pages.cu[b + 1] <= i) ++b;
+        pos[k] = pages.ctx[b] + (i - pages.cu[b]);
         const int j = pos[k] >> p.page_shift;
-        if (j != at_j) {
-          id = pages.of(b, j, held);
+        if (j != at_j || b != at_b) {
+          id = pages.of(b, j);
+          at_b = b;
           at_j = j;
         }
         if ((unsigned)id < (unsigned)p.num_pages) slot[k] = (id << p.page_shift) + (pos[k] & pmask);
@@ -193,6 +189,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
       }
     }
   }
+  // block tables: the pages taken
+  for (int a = gtid; a < ngrow; a += nthr) {
+    const int b = upper_row(pages.goff, p.B, a);
+    const int id = pages.taken(a);
+    p.table[(size_t)b * p.max_pages + pages.kept[b] + (a - pages.goff[b])] = id;
+    if ((unsigned)id >= (unsigned)p.num_pages) set_status(p.status, MK_DEV_BAD_INDEX);
+  }
   // the returned pages that stay on the stack
   const int left = count + nback - ngrow;
   for (int f = gtid; f < nback && count + f < left; f += nthr) p.free_pages[count + f] = pages.returned(f);
@@ -205,9 +208,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   if (rank != 0) return;
   for (int b = tid; b < p.B; b += kPlanThreads) {
     const int h = p.held[b];
-    p.held_out[b] = ok ? plan_want(p, b) : h;
+    p.held_out[b] = ok ? pages.kept[b] + (pages.goff[b + 1] - pages.goff[b]) : h;
   }
-  for (int b = tid; b <= p.B; b += kPlanThreads) p.cu[b] = cu[b];
+  for (int b = tid; b <= p.B; b += kPlanThreads) p.cu[b] = pages.cu[b];
   if (tid == 0) {
     *p.count_out = ok ? left : count;
     if (!ok) set_status(p.status, code);
@@ -223,9 +226,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
 // to the pages.  Bound by bytes: every element is read once and written
 // once.  A head belongs to D / (2 E) neighbouring lanes, E = 4 (f32) or 8
 // (16 bits) elements of each half per lane, so loads are 16 bytes and the
-// two halves of a pair meet in one lane.  A lane group keeps its token's
-// angles in registers over the heads it does in turn; the launch gives it
-// as many as leave a thousand threads per SM.
+// two halves of a pair meet in one lane.  A block takes the heads of one to
+// four tokens: each lane group loads its heads of one token, the block works
+// out the tokens' angles with the gains folded in,
+//   y_a = r (a ca - b sb),  y_b = r (b cb + a sa),
+// once in shared memory, and the heads are then done in packed pairs of
+// floats: at 16 bits the instructions per element are the second bound.
 //
 // The angle in revolutions is pos * f mod 1, f = theta^(-2i/D) / (2 pi): with
 // f as a 64-bit fraction (units of 2^-64) the product modulo 2^64 is that
@@ -240,34 +246,49 @@ struct NormParams {
   const int32_t *positions, *slots;
   __nv_bfloat16 *q, *kpool, *vpool;
   int32_t* status;
-  int N, Hq, Hkv, page_shift, num_pages, splits;
+  int N, Hq, Hkv, page_shift, num_pages;
+  int tokens, splits;  // tokens of a block; blocks that share a token's heads
   float eps;
   uint64_t freq[64];  // [D / 2]
 };
 
+// E elements as they come, and as floats
+template <typename T, int E>
+struct Raw;
 template <int E>
-__device__ __forceinline__ void load_half(const float* p, float (&v)[E]) {
+struct Raw<float, E> {
+  float4 v[E / 4];
+  __device__ __forceinline__ void load(const float* p) {
 #pragma unroll
-  for (int i = 0; i < E; i += 4) {
-    const float4 t = __ldg(reinterpret_cast<const float4*>(p + i));
-    v[i] = t.x; v[i + 1] = t.y; v[i + 2] = t.z; v[i + 3] = t.w;
+    for (int i = 0; i < E / 4; ++i) v[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
   }
-}
-template <int E>
-__device__ __forceinline__ void load_half(const __nv_bfloat16* p, float (&v)[E]) {
-  if constexpr (E == 8) {
-    const uint4 t = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+  __device__ __forceinline__ void get(float (&f)[E]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = ptx::bf_lo(w[i]);
-      v[2 * i + 1] = ptx::bf_hi(w[i]);
+    for (int i = 0; i < E / 4; ++i) {
+      f[4 * i] = v[i].x; f[4 * i + 1] = v[i].y; f[4 * i + 2] = v[i].z; f[4 * i + 3] = v[i].w;
     }
-  } else {
-    const uint2 t = __ldg(reinterpret_cast<const uint2*>(p));
-    v[0] = ptx::bf_lo(t.x); v[1] = ptx::bf_hi(t.x); v[2] = ptx::bf_lo(t.y); v[3] = ptx::bf_hi(t.y);
   }
-}
+};
+template <int E>
+struct Raw<__nv_bfloat16, E> {
+  uint2 v[E / 4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    if constexpr (E == 8) {
+      const uint4 t = __ldg(reinterpret_cast<const uint4*>(p));
+      v[0] = make_uint2(t.x, t.y);
+      v[1] = make_uint2(t.z, t.w);
+    } else {
+      v[0] = __ldg(reinterpret_cast<const uint2*>(p));
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[E]) const {
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) {
+      f[4 * i] = ptx::bf_lo(v[i].x); f[4 * i + 1] = ptx::bf_hi(v[i].x);
+      f[4 * i + 2] = ptx::bf_lo(v[i].y); f[4 * i + 3] = ptx::bf_hi(v[i].y);
+    }
+  }
+};
 using ptx::pack_bf16;
 template <int E>
 __device__ __forceinline__ void store_half(__nv_bfloat16* p, const float (&v)[E]) {
@@ -278,84 +299,131 @@ __device__ __forceinline__ void store_half(__nv_bfloat16* p, const float (&v)[E]
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
 
+constexpr int kNormBatch = 3;      // heads a lane group has in flight
+constexpr int kNormMaxTokens = 4;  // tokens of a block
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kNormThreads, 3) norm_rope_kernel(const __grid_constant__ NormParams p) {
   constexpr int E = sizeof(T) == 4 ? 4 : 8;
-  constexpr int LPH = D / 2 / E;  // lanes per head
-  const int gl = threadIdx.x % LPH;
-  const int64_t unit = (int64_t)blockIdx.x * (kNormThreads / LPH) + threadIdx.x / LPH;
-  const int row = (int)(unit / p.splits), split = (int)(unit % p.splits);
-  if (row >= p.N) return;  // whole lane groups leave; the shuffles below name their group's lanes only
-  const int pos = p.positions[row], slot = p.slots[row];
-  if (pos < 0) return;
+  constexpr int LPH = D / 2 / E;              // lanes per head
+  constexpr int GP = kNormThreads / LPH;      // lane groups of a block
+  // per token, for query and key heads: ca, -sb, cb, sa
+  __shared__ __align__(16) float coef[kNormMaxTokens][2][4][D / 2];
+  const int gl = threadIdx.x % LPH, group = threadIdx.x / LPH;
+  const int gt = GP / p.tokens;                          // lane groups of a token
+  const int tk = group / gt;
+  const int row0 = blockIdx.x / p.splits * p.tokens, row = row0 + tk;
+  const int step = gt * p.splits, h0 = group % gt + blockIdx.x % p.splits * gt;
+  const int hk0 = p.Hq, hv0 = p.Hq + p.Hkv, heads = p.Hq + 2 * p.Hkv;
   const unsigned mask = (LPH == 32 ? 0xffffffffu : ((1u << LPH) - 1u)) << ((threadIdx.x & 31) / LPH * LPH);
-  float cs[E], sn[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const uint64_t turn = (uint64_t)(uint32_t)pos * p.freq[gl * E + i];
-    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn[i], &cs[i]);
-  }
-  const int heads = p.Hq + 2 * p.Hkv;
-  const T* x = static_cast<const T*>(p.x) + (int64_t)row * p.ld_x + gl * E;
+  const bool there = row < p.N;
+  const T* x = static_cast<const T*>(p.x) + (int64_t)(there ? row : 0) * p.ld_x + gl * E;
+  const int pos = there ? p.positions[row] : -1, slot = there ? p.slots[row] : -1;
+  __nv_bfloat16* q = p.q + (int64_t)row * p.ld_q + gl * E;
   const int pg = slot >> p.page_shift, off = slot & ((1 << p.page_shift) - 1);
   const bool store = slot >= 0 && pg < p.num_pages;
-  if (slot >= 0 && !store && gl == 0 && split == 0) set_status(p.status, MK_DEV_BAD_INDEX);
-#pragma unroll 2
-  for (int h = split; h < heads; h += p.splits) {
-    float a[E], b[E];
-    load_half<E>(x + (int64_t)h * D, a);
-    load_half<E>(x + (int64_t)h * D + D / 2, b);
-    const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-    if (!is_v) {
-      const __nv_bfloat16* gamma = is_q ? p.q_gamma : p.k_gamma;
-      if (gamma) {
-        float ss = 0.f;
+  const int64_t at = (((int64_t)pg * p.Hkv << p.page_shift) + off) * D + gl * E;  // head 0's row in its page
+  if (pos >= 0 && slot >= 0 && !store && gl == 0 && group % gt == 0) set_status(p.status, MK_DEV_BAD_INDEX);
+  for (int h = h0; h < heads || h == h0; h += kNormBatch * step) {
+    Raw<T, E> ra[kNormBatch], rb[kNormBatch];
 #pragma unroll
-        for (int i = 0; i < E; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
+    for (int k = 0; k < kNormBatch; ++k) {
+      const int hk = h + k * step;
+      if (pos >= 0 && hk < heads) {
+        ra[k].load(x + hk * D);
+        rb[k].load(x + hk * D + D / 2);
+      }
+    }
+    if (h == h0) {
+      for (int i = threadIdx.x; i < p.tokens * (D / 2); i += kNormThreads) {
+        const int t = i / (D / 2), j = i % (D / 2), r = row0 + t;
+        const uint64_t turn = (uint64_t)(uint32_t)(r < p.N ? p.positions[r] : 0) * p.freq[j];
+        float s, c;
+        sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
 #pragma unroll
-        for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-        const float r = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
-        float ga[E], gb[E];
-        load_half<E>(gamma + gl * E, ga);
-        load_half<E>(gamma + gl * E + D / 2, gb);
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          a[i] *= r * ga[i];
-          b[i] *= r * gb[i];
+        for (int cl = 0; cl < 2; ++cl) {
+          const __nv_bfloat16* g = cl ? p.k_gamma : p.q_gamma;
+          const float ga = g ? __bfloat162float(g[j]) : 1.f, gb = g ? __bfloat162float(g[j + D / 2]) : 1.f;
+          coef[t][cl][0][j] = c * ga;
+          coef[t][cl][1][j] = -s * gb;
+          coef[t][cl][2][j] = c * gb;
+          coef[t][cl][3][j] = s * ga;
         }
       }
+      __syncthreads();
+    }
+    if (pos < 0) break;  // left out (whole lane groups; the shuffles name their lanes only)
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const float u = a[i], w = b[i];
-        a[i] = u * cs[i] - w * sn[i];
-        b[i] = w * cs[i] + u * sn[i];
+    for (int k = 0; k < kNormBatch; ++k) {
+      const int hk = h + k * step;
+      if (hk >= heads) break;
+      float a[E], b[E];
+      ra[k].get(a);
+      rb[k].get(b);
+      if (hk < hv0) {
+        const bool is_q = hk < hk0;
+        float r = 1.f;
+        if ((is_q ? p.q_gamma : p.k_gamma) != nullptr) {
+          uint64_t ss = 0;
+#pragma unroll
+          for (int i = 0; i < E; i += 2) {
+            const uint64_t u = ptx::pair_f32(a[i], a[i + 1]), v = ptx::pair_f32(b[i], b[i + 1]);
+            ss = ptx::fma2(u, u, ptx::fma2(v, v, ss));
+          }
+          const float2 two = ptx::unpair_f32(ss);
+          float sum = two.x + two.y;
+#pragma unroll
+          for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
+          r = rsqrtf(sum * (1.0f / D) + p.eps);
+        }
+        const uint64_t r2 = ptx::pair_f32(r, r);
+        const float* cf = &coef[tk][is_q ? 0 : 1][0][gl * E];
+#pragma unroll
+        for (int i = 0; i < E; i += 4) {
+          const float4 ca = *reinterpret_cast<const float4*>(cf + i), sb = *reinterpret_cast<const float4*>(cf + D / 2 + i);
+          const float4 cb = *reinterpret_cast<const float4*>(cf + D + i),
+                       sa = *reinterpret_cast<const float4*>(cf + 3 * D / 2 + i);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint64_t u = ptx::mul2(r2, ptx::pair_f32(a[i + 2 * e], a[i + 2 * e + 1]));
+            const uint64_t v = ptx::mul2(r2, ptx::pair_f32(b[i + 2 * e], b[i + 2 * e + 1]));
+            const uint64_t c1 = e ? ptx::pair_f32(ca.z, ca.w) : ptx::pair_f32(ca.x, ca.y);
+            const uint64_t s1 = e ? ptx::pair_f32(sb.z, sb.w) : ptx::pair_f32(sb.x, sb.y);
+            const uint64_t c2 = e ? ptx::pair_f32(cb.z, cb.w) : ptx::pair_f32(cb.x, cb.y);
+            const uint64_t s2 = e ? ptx::pair_f32(sa.z, sa.w) : ptx::pair_f32(sa.x, sa.y);
+            const float2 ya = ptx::unpair_f32(ptx::fma2(v, s1, ptx::mul2(u, c1)));
+            const float2 yb = ptx::unpair_f32(ptx::fma2(u, s2, ptx::mul2(v, c2)));
+            a[i + 2 * e] = ya.x;
+            a[i + 2 * e + 1] = ya.y;
+            b[i + 2 * e] = yb.x;
+            b[i + 2 * e + 1] = yb.y;
+          }
+        }
       }
+      __nv_bfloat16* dst = q + hk * D;
+      if (hk >= hk0) {
+        if (!store) continue;
+        dst = hk < hv0 ? p.kpool + at + ((int64_t)(hk - hk0) << p.page_shift) * D
+                       : p.vpool + at + ((int64_t)(hk - hv0) << p.page_shift) * D;
+      }
+      store_half<E>(dst, a);
+      store_half<E>(dst + D / 2, b);
     }
-    __nv_bfloat16* dst;
-    if (is_q) {
-      dst = p.q + (int64_t)row * p.ld_q + (int64_t)h * D;
-    } else {
-      if (!store) continue;
-      const int g = h - p.Hq - (is_v ? p.Hkv : 0);
-      dst = (is_v ? p.vpool : p.kpool) + ((((int64_t)pg * p.Hkv + g) << p.page_shift) + off) * D;
-    }
-    store_half<E>(dst + gl * E, a);
-    store_half<E>(dst + gl * E + D / 2, b);
   }
 }
 
 template <typename T, int D>
 cudaError_t launch_norm(NormParams& p, int sms, cudaStream_t stream) {
   constexpr int E = sizeof(T) == 4 ? 4 : 8;
-  constexpr int LPH = D / 2 / E;
+  constexpr int GP = kNormThreads / (D / 2 / E);
   const int heads = p.Hq + 2 * p.Hkv;
-  // heads in turn per lane group: fewer while the launch would hold under a
-  // thousand threads per SM
-  int turns = 8;
-  while (turns > 1 && (int64_t)p.N * ((heads + turns - 1) / turns) * LPH < (int64_t)sms * 1024) turns >>= 1;
-  p.splits = (heads + turns - 1) / turns;
-  const int64_t units = (int64_t)p.N * p.splits, per = kNormThreads / LPH;
-  norm_rope_kernel<T, D><<<(unsigned)((units + per - 1) / per), kNormThreads, 0, stream>>>(p);
+  // tokens whose heads fill a block's batch; few tokens: a head per lane group, over several blocks
+  p.tokens = 1;
+  while (p.tokens < kNormMaxTokens && 2 * p.tokens * heads <= kNormBatch * GP) p.tokens *= 2;
+  while (p.tokens > 1 && (p.N + p.tokens - 1) / p.tokens < 2 * sms) p.tokens /= 2;
+  p.splits = p.N < sms ? (heads + GP - 1) / GP : 1;
+  const int64_t blocks = (int64_t)((p.N + p.tokens - 1) / p.tokens) * p.splits;
+  norm_rope_kernel<T, D><<<(unsigned)blocks, kNormThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -387,12 +455,13 @@ extern "C" int mk_paged_plan(void* stream, int B, int page_size, int max_pages, 
   p.B = B; p.max_pages = max_pages; p.num_pages = num_pages; p.max_tokens = max_tokens;
   while ((1 << p.page_shift) < page_size) ++p.page_shift;
   p.vec = aligned16(positions) && aligned16(slots);
-  const size_t smem = (size_t)3 * (B + 1) * 4;
-  if (smem > 48 * 1024 - 512) {
-    const cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const size_t smem = (size_t)5 * (B + 1) * 4;
+  if (smem > 48 * 1024 - 1024) {
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(plan_kernel, 5 * (kPlanMaxB + 1) * 4, &allowed);
     if (e != cudaSuccess) return launch_result(e, "mk_paged_plan");
   }
-  // one CTA does 2048 tokens in one pass of its threads; the sums are the rest of its time
+  // one CTA does 4096 tokens in one pass of its threads; the sums are the rest of its time
   int ctas = 1;
   while (ctas < kPlanCtas && max_tokens > ctas * kPlanThreads * 4) ctas *= 2;
   cudaLaunchConfig_t cfg{};

@@ -11,15 +11,15 @@
 // their probabilities, the row, the chosen segment).  A cluster serves a
 // request; each warp sums a contiguous segment of the vocabulary, the
 // segments' sums are exchanged through distributed shared memory, and the
-// warp that owns the segment holding the draw reads that segment once more
-// (out of L2) to find the token.
+// CTA that owns the segment holding the draw reads that segment once more
+// (out of L2), all its warps together, to find the token.
 //
 // The product of two floats is exact in double.  The sums decide between
 // neighbouring tokens of a vocabulary of 10^5, so they are carried far below
 // float precision: every weight as an unevaluated pair (difference and its
 // rounding error), pairs added without loss to about 2^-48, in float
-// arithmetic, since the card's double adders are 64 times slower; segments
-// and the final search use double.
+// arithmetic, since a warp's double addition takes 16 cycles of an SM; only
+// one warp at a time adds the sums of segments in double.
 #include <cfloat>
 
 #include "paged.h"
@@ -76,7 +76,34 @@ struct PairSum {
     c += ((s - (t - z)) + (w.x - z)) + w.y;
     s = t;
   }
+  // the warp's sum, in a fixed order
+  __device__ __forceinline__ double reduce() {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float2 w = make_float2(__shfl_xor_sync(0xffffffffu, s, o), __shfl_xor_sync(0xffffffffu, c, o));
+      add(w);
+    }
+    return (double)s + (double)c;
+  }
 };
+
+// Inclusive sums over the lanes.
+__device__ __forceinline__ double lane_scan(double v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double up = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += up;
+  }
+  return v;
+}
+
+// The lane whose range of the running sum holds the target: the first with a weight whose end exceeds it, or
+// the last with a weight where none does (u at 1 or beyond, or the rounding of sums taken in another order).
+__device__ __forceinline__ int pick_lane(double own, double end, double target) {
+  const unsigned hits = __ballot_sync(0xffffffffu, own > 0.0 && end > target);
+  const unsigned some = __ballot_sync(0xffffffffu, own > 0.0);
+  return hits ? __ffs(hits) - 1 : 31 - __clz(some);
+}
 
 // Sum of entries [i0, i1) over the warp (every lane gets it), in a fixed order.
 template <bool Q>
@@ -84,50 +111,59 @@ __device__ __forceinline__ double segment_sum(const Weights& w, int i0, int i1, 
   PairSum acc;
   if (vec) {
     int i = i0 + lane * 4;
-#pragma unroll 4
-    for (; i + 4 <= i1; i += 128) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(w.p + i));
-      float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (Q) b = __ldg(reinterpret_cast<const float4*>(w.q + i));
-      float2 d[4] = {w.pair(a.x, b.x), w.pair(a.y, b.y), w.pair(a.z, b.z), w.pair(a.w, b.w)};
-      const int h = w.hole - i;
+    const auto add4 = [&](int j, float4 a, float4 b) {
+      const float2 d[4] = {w.pair(a.x, b.x), w.pair(a.y, b.y), w.pair(a.z, b.z), w.pair(a.w, b.w)};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (!Q && k == h) d[k] = make_float2(0.f, 0.f);
-        acc.add(d[k]);
+      for (int k = 0; k < 4; ++k)
+        if (Q || j + k != w.hole) acc.add(d[k]);
+    };
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int U = 4;  // groups of each row in flight
+    for (; i + (U - 1) * 128 + 4 <= i1; i += U * 128) {
+      float4 a[U], b[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        a[k] = __ldg(reinterpret_cast<const float4*>(w.p + i + k * 128));
+        b[k] = Q ? __ldg(reinterpret_cast<const float4*>(w.q + i + k * 128)) : none;
       }
+#pragma unroll
+      for (int k = 0; k < U; ++k) add4(i + k * 128, a[k], b[k]);
     }
+    for (; i + 4 <= i1; i += 128)
+      add4(i, __ldg(reinterpret_cast<const float4*>(w.p + i)),
+           Q ? __ldg(reinterpret_cast<const float4*>(w.q + i)) : none);
     for (int k = i; k < i1 && k < i + 4; ++k)  // the row's last, partial group
       if (Q || k != w.hole) acc.add(w.pair(w.p[k], Q ? w.q[k] : 0.f));
   } else {
-#pragma unroll 4
+#pragma unroll 8
     for (int i = i0 + lane; i < i1; i += 32) {
       const float a = __ldg(w.p + i), b = Q ? __ldg(w.q + i) : 0.f;
       if (Q || i != w.hole) acc.add(w.pair(a, b));
     }
   }
-  double s = (double)acc.s + (double)acc.c;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
+  return acc.reduce();
 }
 
 __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams v) {
   __shared__ double seg_sum[2][kVerifyMaxCtas * kVerifyWarps];
-  __shared__ int at_s, mode_s;
+  __shared__ double sub_sum[kVerifyWarps];
+  __shared__ double base_s, target_s, sub_base_s;
+  __shared__ int at_s, mode_s, seg_s, sub_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / v.ctas, rank = blockIdx.x % v.ctas;
   const int32_t* tok = v.drafts + (int64_t)b * v.K;
   const float* u = v.u + (int64_t)b * (v.K + 1);
+  // (waited for before another CTA's shared memory is written: it has to be running)
+  if (v.ctas > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   if (warp == 0) {
     const int len = v.draft_len ? min(max(v.draft_len[b], 0), v.K) : v.K;
     int at = len, mode = 0;  // mode 1: rejected, the draft's row is taken off
-    for (int t0 = 0; t0 < len; t0 += 32) {
+    for (int t0 = 0; t0 < v.K; t0 += 32) {
       const int t = t0 + lane;
       bool valid = false, yes = false;
-      if (t < len) {
-        const int x = tok[t];
-        valid = (unsigned)x < (unsigned)v.V;
+      if (t < v.K) {
+        const int x = tok[t];  // (not behind the draft's length, so that both loads are in flight)
+        valid = t < len && (unsigned)x < (unsigned)v.V;
         if (valid) {
           const double pt = v.p[((int64_t)b * (v.K + 1) + t) * v.ld_p + x];
           const double qt = v.q ? (double)v.q[((int64_t)b * v.K + t) * v.ld_q + x] : 1.0;
@@ -156,10 +192,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
   w.p = v.p + ((int64_t)b * (v.K + 1) + at) * v.ld_p;
   const int segs = v.ctas * kVerifyWarps, mine = rank * kVerifyWarps + warp;
   const int i0 = min(mine * v.seg, v.V), i1 = min(i0 + v.seg, v.V);
-  bool found = false;
-  int seg_at = 0;
-  double base = 0.0, target = 0.0;
-  if (v.ctas > 1) cluster_barrier();  // every CTA of the cluster runs before its shared memory is written
+  if (v.ctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     w.q = mode && v.q ? v.q + ((int64_t)b * v.K + at) * v.ld_q : nullptr;
@@ -170,95 +203,91 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
                    : "memory");
     if (v.ctas > 1) cluster_barrier();
     else __syncthreads();
-    // every warp finds the segment of the draw for itself: lanes hold
-    // consecutive segments, summed in order
-    const int per = segs / 32 > 0 ? segs / 32 : 1;
-    double own = 0.0;
-    for (int k = 0; k < per; ++k) {
-      const int g = lane * per + k;
-      if (g < segs) own += seg_sum[pass][g];
-    }
-    double end = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double up = __shfl_up_sync(0xffffffffu, end, o);
-      if (lane >= o) end += up;
-    }
-    const double total = __shfl_sync(0xffffffffu, end, 31);
-    if (!(total > 0.0)) {
-      if (!mode) break;
-      mode = 0;  // nothing is left of the target over the draft: draw from the target
-      continue;
-    }
-    double r = u[v.K];
-    r = r >= 0.0 ? r : 0.0;  // a NaN counts as zero
-    target = r * total;
-    // the first segment whose end exceeds the target; at u >= 1 (or by the
-    // rounding of the sums) none does, and the last one of any weight is it
-    double run = end - own;
-    int hit = -1, last = -1;
-    double hit_base = 0.0, last_base = 0.0;
-    for (int k = 0; k < per; ++k) {
-      const int g = lane * per + k;
-      if (g >= segs) break;
-      const double sg = seg_sum[pass][g];
-      if (sg > 0.0) {
-        last = g;
-        last_base = run;
-        if (hit < 0 && run + sg > target) {
-          hit = g;
-          hit_base = run;
+    if (warp == 0) {
+      // the segment of the draw: lanes hold consecutive segments, summed in order
+      const int per = (segs + 31) / 32;
+      double own = 0.0;
+      for (int k = 0; k < per; ++k)
+        if (lane * per + k < segs) own += seg_sum[pass][lane * per + k];
+      const double end = lane_scan(own, lane), total = __shfl_sync(0xffffffffu, end, 31);
+      int seg = -1;
+      double r = u[v.K], base = 0.0;
+      r = r >= 0.0 ? r : 0.0;  // a NaN counts as zero
+      const double target = r * total;
+      if (total > 0.0) {
+        const int src = pick_lane(own, end, target);
+        double run = end - own;
+        for (int k = 0; k < per; ++k) {
+          const int g = lane * per + k;
+          const double x = g < segs ? seg_sum[pass][g] : 0.0;
+          if (x > 0.0) {
+            seg = g;
+            base = run;
+            if (run + x > target) break;
+          }
+          run += x;
         }
+        seg = __shfl_sync(0xffffffffu, seg, src);
+        base = __shfl_sync(0xffffffffu, base, src);
       }
-      run += sg;
+      if (lane == 0) {
+        seg_s = seg;
+        base_s = base;
+        target_s = target;
+      }
     }
-    const unsigned hits = __ballot_sync(0xffffffffu, hit >= 0), lasts = __ballot_sync(0xffffffffu, last >= 0);
-    const int src = hits ? __ffs(hits) - 1 : 31 - __clz(lasts);
-    seg_at = __shfl_sync(0xffffffffu, hits ? hit : last, src);
-    base = __shfl_sync(0xffffffffu, hits ? hit_base : last_base, src);
-    found = true;
-    break;
+    __syncthreads();
+    if (seg_s >= 0 || !mode) break;
+    mode = 0;  // nothing is left of the target over the draft: draw from the target
+    __syncthreads();
   }
-  if (!found) {
+  const int seg = seg_s;
+  if (seg < 0) {
     if (rank == 0 && warp == 0) {
       for (int t = lane; t <= v.K; t += 32) v.tokens[(int64_t)b * (v.K + 1) + t] = t < at ? tok[t] : -1;
       if (lane == 0) v.accepted[b] = at;
     }
     return;
   }
-  if (rank != seg_at / kVerifyWarps || warp != 0) return;
-  // the token: the first entry of the segment whose running sum exceeds the target
-  const int s0 = min(seg_at * v.seg, v.V), s1 = min(s0 + v.seg, v.V);
-  int pick = -1, last = -1;
-  for (int i = s0; i < s1 && pick < 0; i += 128) {
-    double x[4], own = 0.0;
-    int mine_last = -1;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int g = i + lane * 4 + k;
-      x[k] = g < s1 ? w.at(g) : 0.0;
-      own += x[k];
-      if (x[k] > 0.0) mine_last = g;
+  if (rank != seg / kVerifyWarps) return;
+  // the token: each warp sums a sixteenth of the segment, a lane consecutive entries
+  const int s0 = min(seg * v.seg, v.V), s1 = min(s0 + v.seg, v.V), sub = v.seg / kVerifyWarps;
+  const int per = (sub + 31) / 32, e0 = s0 + warp * sub, e1 = min(e0 + sub, s1);
+  const int l0 = min(e0 + lane * per, e1), l1 = min(l0 + per, e1);
+  PairSum acc;
+#pragma unroll 4
+  for (int i = l0; i < l1; ++i)
+    if (i != w.hole) acc.add(w.pair(__ldg(w.p + i), w.q ? __ldg(w.q + i) : 0.f));
+  const double own = (double)acc.s + (double)acc.c;
+  const double all = acc.reduce();
+  if (lane == 0) sub_sum[warp] = all;
+  __syncthreads();
+  const double target = target_s;
+  if (warp == 0) {
+    const double x = lane < kVerifyWarps ? sub_sum[lane] : 0.0, end = base_s + lane_scan(x, lane);
+    const int src = pick_lane(x, end, target);
+    if (lane == src) {
+      sub_s = src;
+      sub_base_s = end - x;
     }
-    double end = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double up = __shfl_up_sync(0xffffffffu, end, o);
-      if (lane >= o) end += up;
-    }
-    double run = base + (end - own);
-    int hit = -1;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      run += x[k];
-      if (hit < 0 && x[k] > 0.0 && run > target) hit = i + lane * 4 + k;
-    }
-    const unsigned hits = __ballot_sync(0xffffffffu, hit >= 0), some = __ballot_sync(0xffffffffu, mine_last >= 0);
-    if (some) last = __shfl_sync(0xffffffffu, mine_last, 31 - __clz(some));
-    if (hits) pick = __shfl_sync(0xffffffffu, hit, __ffs(hits) - 1);
-    base += __shfl_sync(0xffffffffu, end, 31);
   }
-  if (pick < 0) pick = last;
+  __syncthreads();
+  if (warp != sub_s) return;
+  const double end = sub_base_s + lane_scan(own, lane);
+  const int src = pick_lane(own, end, target);
+  int pick = -1;
+  if (lane == src) {
+    double run = end - own;
+    for (int i = l0; i < l1; ++i) {
+      const double x = w.at(i);
+      run += x;
+      if (x > 0.0) {
+        pick = i;
+        if (run > target) break;
+      }
+    }
+  }
+  pick = __shfl_sync(0xffffffffu, pick, src);
   for (int t = lane; t <= v.K; t += 32)
     v.tokens[(int64_t)b * (v.K + 1) + t] = t < at ? tok[t] : t == at ? pick : -1;
   if (lane == 0) v.accepted[b] = at;
@@ -287,9 +316,10 @@ extern "C" int mk_verify_drafts(void* stream, int B, int K, int V, const float* 
   v.ld_p = ld_p; v.ld_q = ld_q; v.B = B; v.K = K; v.V = V;
   v.vec = aligned16(p) && ld_p % 4 == 0 && (!q || (aligned16(q) && ld_q % 4 == 0));
   // as many CTAs per request as still give every warp a few 128-entry steps,
-  // fewer once the requests alone fill the SMs twice
+  // fewer once two CTAs per SM are there (64 requests of 128256 entries: 3, 4,
+  // 6, 8 CTAs each took 16.6, 14.3, 14.9 and 17.6 us; one request 8.8 us with 8)
   int ctas = kVerifyMaxCtas;
-  while (ctas > 1 && ((int64_t)V < (int64_t)ctas * kVerifyWarps * 256 || (int64_t)B * ctas > 4 * (int64_t)sms)) ctas /= 2;
+  while (ctas > 1 && ((int64_t)V < (int64_t)ctas * kVerifyWarps * 256 || (int64_t)B * ctas > 2 * (int64_t)sms)) ctas /= 2;
   v.ctas = ctas;
   const int64_t warps = (int64_t)ctas * kVerifyWarps;
   v.seg = (int)((((int64_t)V + warps - 1) / warps + 127) / 128 * 128);
