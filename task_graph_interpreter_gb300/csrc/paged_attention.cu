@@ -44,7 +44,7 @@ bool few_rows(int max_new, int G) { return (int64_t)max_new * G <= kMaxFewRows; 
 // Two partial records and a note per worker (paged_attention.cuh).
 size_t workspace_bytes(int max_new, int G, int D, int sms) {
   const bool few = few_rows(max_new, G);
-  const size_t workers = (size_t)sms * (few ? kRowWarps : 1), rows = few ? max_new * G : 256;
+  const size_t workers = (size_t)sms * (few ? row_warps(max_new * G) : 1), rows = few ? max_new * G : 256;
   return 2 * workers * rows * (D + 2) * 4 + workers * 16;
 }
 
@@ -116,14 +116,13 @@ extern "C" int mk_paged_attention(void* stream_, int B, int N, int max_new, int 
   p.B = B; p.N = N; p.Hq = Hq; p.Hkv = Hkv; p.G = G; p.max_new = max_new;
   p.max_pages = max_pages; p.num_pages = num_pages;
   while ((1 << p.page_shift) < page_size) ++p.page_shift;
-  p.workers = few ? sms * kRowWarps : sms;
-  if (p.workers > kMaxWorkers) return fail(MK_ERR_LIMIT, "mk_paged_attention: more SMs than the join can list");
+  p.workers = few ? sms * row_warps(max_new * G) : sms;
   p.rows = few ? max_new * G : 256;
   p.tq = few ? 0 : 128 / G;
 
   // pools as [rows, D], pages one after the other; a box is what one page gives a block of keys
   CUtensorMap kmap, vmap, qmap;
-  const int keys = few ? 32 * 128 / D : 128;
+  const int keys = few ? kRowBlockBytes / D / 4 : 128;
   const cuuint64_t dim[2] = {(cuuint64_t)D, (cuuint64_t)num_pages * Hkv * page_size}, stride[1] = {(cuuint64_t)D * 2};
   const cuuint32_t box[2] = {64u, (cuuint32_t)(page_size < keys ? page_size : keys)};
   bool ok = encode(enc, &kmap, kpool, 2, dim, stride, box) && encode(enc, &vmap, vpool, 2, dim, stride, box);

@@ -35,11 +35,13 @@ struct AttnParams {
   int tq;           // tokens per query tile (chunks): 128 / G
 };
 
+constexpr int kRowBlockBytes = 8192;  // keys and values of a few-rows block
+
 // Geometry of an item: few query rows (all of a request's), or a pair of
 // 128-row query tiles.
 template <int D, bool CHUNK>
 struct Geometry {
-  static constexpr int kKeys = CHUNK ? 128 : 32 * 128 / D;  // keys per block
+  static constexpr int kKeys = CHUNK ? 128 : kRowBlockBytes / D / 4;  // keys per block
   static constexpr int kFixed = CHUNK ? 384 : 64;           // an item's fixed cost, in keys
 };
 
@@ -123,7 +125,11 @@ __device__ __forceinline__ Line measure_line(const AttnParams& p, int lane) {
   for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
   l.bad = __any_sync(0xffffffffu, wrong);
   l.u = u;
-  l.part = (u + p.workers - 1) / p.workers;
+  // whole blocks, a few at least: fewer records to join where there is little to do, and a worker behind an
+  // item's first block always has a part of it
+  constexpr int K = Geometry<D, CHUNK>::kKeys, kLeast = (CHUNK ? 1 : 4) * K;
+  const int64_t even = (u + p.workers - 1) / p.workers;
+  l.part = even <= kLeast ? kLeast : (even + K - 1) / K * K;
   return l;
 }
 
@@ -147,6 +153,12 @@ struct Cursor {
     if (x >= start + cost()) return nk;
     const int64_t k = x - start - Geometry<D, CHUNK>::kFixed + K / 2;
     return k <= 0 ? 0 : (int)min((int64_t)nk, k / K);
+  }
+  // the worker that has the item's first block: the last whose part begins before the place from which
+  // block_at() is 1
+  __device__ __forceinline__ int first_worker(const Line& line) const {
+    constexpr int K = Geometry<D, CHUNK>::kKeys;
+    return small_quotient(start + Geometry<D, CHUNK>::kFixed + K / 2 - 1, line.part);
   }
   // the item holding place x of the line (0 <= x < U)
   __device__ __forceinline__ void find(const AttnParams& p, const Line& line, int64_t x, int lane) {
@@ -209,17 +221,14 @@ __device__ __forceinline__ float* part_o(const AttnParams& p, int D, int slot, i
 __device__ __forceinline__ float* part_ml(const AttnParams& p, int D, int slot, int row) {
   return p.part + (size_t)2 * p.workers * p.rows * D + ((size_t)slot * p.rows + row) * 2;
 }
+// A worker's note of the item that began before it and ends with it (tokens 0: there is none): the
+// worker it began with, whose second slot has its first part, the first query row, the key/value head,
+// the tokens.
 struct Note {
-  int flags;   // kCameIn ...
-  int row0;    // of the item that ends here: its first row of q,
-  int g;       // key/value head,
-  int tokens;  // and tokens
+  int first, row0, g, tokens;
 };
-constexpr int kCameIn = 1;   // slot 2 w is in use
-constexpr int kEnded = 2;    // and that part ends its item
-constexpr int kGoesOn = 4;   // slot 2 w + 1 is in use
-__device__ __forceinline__ int4* note_of(const AttnParams& p, int D, int w) {
-  return reinterpret_cast<int4*>(p.part + (size_t)2 * p.workers * p.rows * (D + 2)) + w;
+__device__ __forceinline__ Note* note_of(const AttnParams& p, int D, int w) {
+  return reinterpret_cast<Note*>(p.part + (size_t)2 * p.workers * p.rows * (D + 2)) + w;
 }
 
 // Wait for a phase of an mbarrier, at most about two seconds, or until
@@ -243,8 +252,8 @@ cudaError_t launch_rows(const AttnParams& p, const CUtensorMap& kmap, const CUte
                         cudaStream_t stream);
 cudaError_t launch_chunk(const AttnParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
                          const CUtensorMap& vmap, int D, cudaStream_t stream);
-constexpr int kMaxWorkers = 1024;  // records of one item that the join lists
-constexpr int kRowWarps = 4;     // warps (workers) per CTA of the few-rows kernel
+// warps (workers) per CTA of the few-rows kernel
+__host__ __device__ constexpr int row_warps(int rows) { return rows <= 16 ? 8 : 7; }
 constexpr int kMaxFewRows = 32;  // query rows of a request and head that it takes
 
 }  // namespace mk

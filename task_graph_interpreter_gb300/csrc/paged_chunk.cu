@@ -201,8 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Line line = measure_line<D, true>(p, lane);
       if (line.bad && blockIdx.x == 0 && lane == 0) set_status(p.status, MK_DEV_BAD_INDEX);
       const int64_t x0 = line.border(blockIdx.x), x1 = line.border(blockIdx.x + 1);
-      int4 note = make_int4(0, 0, 0, 0);
-      if (lane == 0) *note_of(p, D, blockIdx.x) = note;
+      if (lane == 0) *note_of(p, D, blockIdx.x) = Note{0, 0, 0, 0};
       Cursor<D, true> c;
       bool more = !line.bad && x0 < x1, told = false;
       if (more) c.find(p, line, x0, lane);
@@ -235,15 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             s.k0 = k0;
             s.k1 = k1;
             s.slot = k0 == 0 && k1 == nk ? -1 : 2 * (int)blockIdx.x + (k0 == 0 ? 1 : 0);
-            if (s.slot >= 0) {
-              note.x |= k0 == 0 ? kGoesOn : k1 == nk ? kCameIn | kEnded : kCameIn;
-              if (k0 != 0) {
-                note.y = s.row0;
-                note.z = c.g;
-                note.w = min(2 * p.tq, c.s.n - t0);
-              }
-              *note_of(p, D, blockIdx.x) = note;
-            }
+            if (k0 != 0 && k1 == nk)
+              *note_of(p, D, blockIdx.x) = Note{c.first_worker(line), s.row0, c.g, min(2 * p.tq, c.s.n - t0)};
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               const int first = t0 + w * p.tq, last = min(first + p.tq, c.s.n) - 1;

@@ -7,9 +7,10 @@
 // 1.5 us.  Each warp is a worker of its own, with its own part of the work
 // line, its own ring of three blocks filled by TMA (pages gathered into a
 // 128-byte-swizzled tile), its own softmax state in registers: no warp waits
-// for another.  The products run on m16n8k16 warp matrix instructions, which
-// take 16 rows at a time; a tcgen05 product has 128 rows, of which a decode
-// step would fill four, and would put two more round trips (through tensor
+// for another.  The products run on m16n8k16 warp matrix instructions with
+// the keys (and the columns of the values) along their 16 and the query rows
+// along their 8, so a decode step's four rows fill half of one; a tcgen05
+// product has 128 rows, and would put two more round trips (through tensor
 // memory) into each block's chain.
 //
 //   s = q k^T scale;  m' = max(m, max s);  p = 2^(s - m');
@@ -26,13 +27,12 @@ namespace {
 using namespace ptx;
 
 constexpr int kStages = 3;
-constexpr int kHalfBytes = 8192;             // keys, or values, of a block
-constexpr int kStageBytes = 2 * kHalfBytes;
-constexpr int kThreads = kRowWarps * 32;
+constexpr int kHalfBytes = kRowBlockBytes / 2;  // keys, or values, of a block
+constexpr int kStageBytes = kRowBlockBytes;
 
-template <int D>
+template <int D, int NB>
 constexpr int smem_bytes_rows() {
-  return 1024 + kRowWarps * (kStages * kStageBytes + kMaxFewRows * D * 2);
+  return 1024 + row_warps(8 * NB) * (kStages * kStageBytes + 8 * NB * D * 2);
 }
 
 // 16-byte chunk c of row r in a tile of 128-byte rows, 128-byte swizzle
@@ -43,13 +43,15 @@ __device__ __forceinline__ uint32_t swz(uint32_t base, int r, int c) {
 __device__ __forceinline__ bool nonfinite_lo(uint32_t w) { return (w & 0x7F80u) == 0x7F80u; }
 __device__ __forceinline__ bool nonfinite_hi(uint32_t w) { return (w & 0x7F800000u) == 0x7F800000u; }
 
-template <int D, int NM>
-__global__ void __launch_bounds__(kThreads, 1)
+// NB: eights of query rows
+template <int D, int NB>
+__global__ void __launch_bounds__(row_warps(8 * NB) * 32, 1)
     rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap) {
   constexpr int KU = Geometry<D, false>::kKeys;  // keys per block
   constexpr int NH = D / 64;                     // 128-byte column halves
-  constexpr int NT = KU / 8;
+  constexpr int NK = KU / 16;                    // key tiles of a block
+  constexpr int kRowWarps = row_warps(8 * NB);
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kRowWarps][kStages];
   __shared__ uint64_t live[kRowWarps][kStages];  // keys of a block that were loaded
@@ -57,7 +59,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* ring = base + warp * kStages * kStageBytes;
-  const uint32_t qs = smem_addr(base + kRowWarps * kStages * kStageBytes + warp * kMaxFewRows * D * 2);
+  const uint32_t qs = smem_addr(base + kRowWarps * kStages * kStageBytes + warp * 8 * NB * D * 2);
   if (threadIdx.x == 0) {
     gave_up = 0;
     for (int i = 0; i < kRowWarps; ++i)
@@ -67,11 +69,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   launch_dependents();
 
-  const int w = blockIdx.x * kRowWarps + warp;
+  const int w = warp * gridDim.x + blockIdx.x;  // (few workers are spread over the SMs)
   const Line line = measure_line<D, false>(p, lane);
   if (line.bad && w == 0 && lane == 0) set_status(p.status, MK_DEV_BAD_INDEX);
   const int64_t x0 = line.border(w), x1 = line.border(w + 1);
-  int4 note = make_int4(0, 0, 0, 0);
+  Note note = {0, 0, 0, 0};
   if (lane == 0) *note_of(p, D, w) = note;
   if (line.bad || x0 >= x1) return;
   const int pmask = (1 << p.page_shift) - 1;
@@ -114,10 +116,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     uint64_t keys = 0;
 #pragma unroll
-    for (int h = 0; h < KU / 32; ++h) {
+    for (int h = 0; h < (KU + 31) / 32; ++h) {
       const int key = key0 + h * 32 + lane;
       const int id = __shfl_sync(0xffffffffu, win, ((key >> p.page_shift) - win0) & 31);
-      const bool in = key < L, ok = in && (unsigned)id < (unsigned)p.num_pages;
+      const bool in = key < L && h * 32 + lane < KU, ok = in && (unsigned)id < (unsigned)p.num_pages;
       keys |= (uint64_t)__ballot_sync(0xffffffffu, ok) << (32 * h);
       if (in && !ok) set_status(p.status, MK_DEV_BAD_INDEX);
     }
@@ -149,49 +151,54 @@ __global__ void __launch_bounds__(kThreads, 1)
   pke = cke;
   for (int i = 0; i < kStages; ++i) issue();
 
-  const int r0 = lane >> 2, c0 = (lane & 3) * 2;
+  // this lane's place in the 16 x 8 results: keys (columns of the values) g and g + 8, query rows c0, c0 + 1
+  const int g = lane >> 2, c0 = (lane & 3) * 2;
   while (more) {
     const int n = cons.s.n, ctx = cons.s.ctx, L = ctx + n, nrows = n * p.G;
     const int nk = cons.blocks(p), kb = ck;
     // query rows, row r = token * G + head, into shared memory; rows past the last are zero
     const __nv_bfloat16* qb = p.q + (int64_t)p.cu[cons.b] * p.ld_q + (int64_t)cons.g * p.G * D;
-    for (int i = lane; i < NM * 16 * (D / 8); i += 32) {
+    __syncwarp();
+    for (int i = lane; i < NB * 8 * (D / 8); i += 32) {
       const int r = i / (D / 8), c = i % (D / 8);
       uint4 v = make_uint4(0, 0, 0, 0);
       if (r < nrows) v = __ldg(reinterpret_cast<const uint4*>(qb + (int64_t)(r / p.G) * p.ld_q + (r % p.G) * D + c * 8));
-      const uint32_t a = swz(qs + (c >> 3) * (NM * 16 * 128), r, c & 7);
+      const uint32_t a = swz(qs + (c >> 3) * (NB * 8 * 128), r, c & 7);
       asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                    : "memory");
     }
     __syncwarp();
     // the last key each of this lane's rows sees
-    int lim[2 * NM];
+    int lim[NB][2];
 #pragma unroll
-    for (int i = 0; i < 2 * NM; ++i) {
-      const int r = i * 8 + r0;
-      lim[i] = r < nrows ? ctx + r / p.G : L - 1;
-    }
-    auto load_q = [&](int m, int kk, uint32_t (&a)[4]) {
-      // matrices: rows 0-7 / 8-15 of the tile, then the same at the next 8 columns
-      const int r = m * 16 + (lane & 15), c = kk * 2 + (lane >> 4);
-      ldsm4(swz(qs + (c >> 3) * (NM * 16 * 128), r, c & 7), a);
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = i * 8 + c0 + e;
+        lim[i][e] = r < nrows ? ctx + r / p.G : L - 1;
+      }
+    // query operands of two 16-column steps: columns kk * 16 .. + 31 of rows i * 8 .. + 7
+    auto load_q = [&](int i, int kk, uint32_t (&b)[4]) {
+      const int c = kk * 2 + (lane >> 3);
+      ldsm4(swz(qs + (c >> 3) * (NB * 8 * 128), i * 8 + (lane & 7), c & 7), b);
     };
-    uint32_t qf[NM == 1 ? D / 16 : 1][4];
-    if constexpr (NM == 1) {
+    constexpr bool kQRegs = NB <= 2;
+    uint32_t qf[kQRegs ? NB : 1][kQRegs ? D / 32 : 1][4];
+    if constexpr (kQRegs) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) load_q(0, kk, qf[kk]);
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk) load_q(i, kk * 2, qf[i][kk]);
     }
-    float o[NM][D / 8][4], m[2 * NM], l[2 * NM];
+    float o[D / 16][NB][4], m[NB][2], l[NB][2];
 #pragma unroll
-    for (int i = 0; i < NM; ++i)
+    for (int i = 0; i < NB; ++i) {
 #pragma unroll
-      for (int t = 0; t < D / 8; ++t)
+      for (int t = 0; t < D / 16; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][t][e] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 2 * NM; ++i) {
-      m[i] = -INFINITY;
-      l[i] = 0.f;
+        for (int e = 0; e < 4; ++e) o[t][i][e] = 0.f;
+      m[i][0] = m[i][1] = -INFINITY;
+      l[i][0] = l[i][1] = 0.f;
     }
 
     for (; ck < cke; ++ck) {
@@ -210,145 +217,159 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint64_t kAll = KU == 64 ? ~0ull : (1ull << (KU & 63)) - 1;
       const bool masked = keys != kAll || key0 + KU > ctx + 1;
 
-      float s[NM][NT][4];
+      float s[NK][NB][4];
 #pragma unroll
-      for (int i = 0; i < NM; ++i)
+      for (int t = 0; t < NK; ++t)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int i = 0; i < NB; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[i][t][e] = 0.f;
+          for (int e = 0; e < 4; ++e) s[t][i][e] = 0.f;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t a[NM][4];
+      for (int kk = 0; kk < D / 32; ++kk) {
+        uint32_t b[NB][4];
 #pragma unroll
-        for (int i = 0; i < NM; ++i) {
-          if constexpr (NM == 1) {
+        for (int i = 0; i < NB; ++i) {
+          if constexpr (kQRegs) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) a[i][e] = qf[kk][e];
+            for (int e = 0; e < 4; ++e) b[i][e] = qf[i][kk][e];
           } else {
-            load_q(i, kk, a[i]);
+            load_q(i, kk * 2, b[i]);
           }
         }
 #pragma unroll
-        for (int t = 0; t < NT; t += 2) {
-          uint32_t b[4];  // keys t*8.. and t*8+8.., columns kk*16.. and +8
-          const int r = t * 8 + (lane >> 4) * 8 + (lane & 7), c = kk * 2 + ((lane >> 3) & 1);
-          ldsm4(swz(ks + (c >> 3) * (KU * 128), r, c & 7), b);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t a[NK][4];  // keys t * 16 .. + 15, columns (kk * 2 + h) * 16 .. + 15
+          const int c = (kk * 2 + h) * 2 + (lane >> 4);
 #pragma unroll
-          for (int i = 0; i < NM; ++i) {
-            mma_bf16(s[i][t], a[i], b[0], b[1]);
-            mma_bf16(s[i][t + 1], a[i], b[2], b[3]);
-          }
+          for (int t = 0; t < NK; ++t) ldsm4(swz(ks + (c >> 3) * (KU * 128), t * 16 + (lane & 15), c & 7), a[t]);
+#pragma unroll
+          for (int t = 0; t < NK; ++t)
+#pragma unroll
+            for (int i = 0; i < NB; ++i) mma_bf16(s[t][i], a[t], b[i][2 * h], b[i][2 * h + 1]);
         }
       }
       if (masked) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NK; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int k = t * 8 + c0 + (e & 1);
+            const int k = t * 16 + g + (e >> 1) * 8;
             const bool there = (keys >> k) & 1;
 #pragma unroll
-            for (int i = 0; i < NM; ++i)
-              if (!there || key0 + k > lim[2 * i + (e >> 1)]) s[i][t][e] = -INFINITY;
+            for (int i = 0; i < NB; ++i)
+              if (!there || key0 + k > lim[i][e & 1]) s[t][i][e] = -INFINITY;
           }
       }
       bool moved = false;
-      float mnew[2 * NM], muse[2 * NM];
+      float mnew[NB][2], muse[NB][2];
 #pragma unroll
-      for (int i = 0; i < 2 * NM; ++i) {
-        float x = -INFINITY;
+      for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) x = fmaxf(x, fmaxf(s[i >> 1][t][(i & 1) * 2], s[i >> 1][t][(i & 1) * 2 + 1]));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-        mnew[i] = fmaxf(m[i], x * p.scale);
-        muse[i] = mnew[i] == -INFINITY ? 0.f : mnew[i];  // a row without any key so far
-        moved |= mnew[i] != m[i];
-      }
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(s[0][i][e], s[0][i][e + 2]);
+#pragma unroll
+          for (int t = 1; t < NK; ++t) x = fmaxf(x, fmaxf(s[t][i][e], s[t][i][e + 2]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          mnew[i][e] = fmaxf(m[i][e], x * p.scale);
+          muse[i][e] = mnew[i][e] == -INFINITY ? 0.f : mnew[i][e];  // a row without any key so far
+          moved |= mnew[i][e] != m[i][e];
+        }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int i = 0; i < 2 * NM; ++i) {
-          const float f = ex2(m[i] - muse[i]);
-          m[i] = mnew[i];
-          l[i] *= f;
+        for (int i = 0; i < NB; ++i)
 #pragma unroll
-          for (int t = 0; t < D / 8; ++t) {
-            o[i >> 1][t][(i & 1) * 2] *= f;
-            o[i >> 1][t][(i & 1) * 2 + 1] *= f;
+          for (int e = 0; e < 2; ++e) {
+            const float f = ex2(m[i][e] - muse[i][e]);
+            m[i][e] = mnew[i][e];
+            l[i][e] *= f;
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) {
+              o[t][i][e] *= f;
+              o[t][i][e + 2] *= f;
+            }
           }
-        }
       }
 #pragma unroll
-      for (int i = 0; i < NM; ++i)
+      for (int t = 0; t < NK; ++t)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int i = 0; i < NB; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float x = ex2(fmaf(s[i][t][e], p.scale, -muse[2 * i + (e >> 1)]));
-            s[i][t][e] = x;
-            l[2 * i + (e >> 1)] += x;
+            const float x = ex2(fmaf(s[t][i][e], p.scale, -muse[i][e & 1]));
+            s[t][i][e] = x;
+            l[i][e & 1] += x;
           }
-      bool odd = false;  // a value that is not finite behind a mask
+      bool bad_v = false;  // a value that is not finite behind a mask
 #pragma unroll
-      for (int kk = 0; kk < KU / 16; ++kk) {
-        uint32_t hi[NM][4], lo[NM][4];
+      for (int t = 0; t < NK; ++t) {
+        // probabilities as operands: 16 keys by 8 rows, transposed, in two parts
+        uint32_t hi[NB][2], lo[NB][2];
 #pragma unroll
-        for (int i = 0; i < NM; ++i)
+        for (int i = 0; i < NB; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = s[i][2 * kk + (e >> 1)][(e & 1) * 2], y = s[i][2 * kk + (e >> 1)][(e & 1) * 2 + 1];
+          for (int e = 0; e < 2; ++e) {
+            const float x = s[t][i][2 * e], y = s[t][i][2 * e + 1];
             const uint32_t h = pack_bf16(x, y);
-            hi[i][e] = h;
-            lo[i][e] = pack_bf16(x - bf_lo(h), y - bf_hi(h));
+            hi[i][e] = movm_trans(h);
+            lo[i][e] = movm_trans(pack_bf16(x - bf_lo(h), y - bf_hi(h)));
           }
         // this lane's four keys of the 16: c0, c0 + 1, c0 + 8, c0 + 9
         uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
         if (masked) {
-          const uint32_t kb16 = (uint32_t)(keys >> (kk * 16)) >> c0;
-          keep0 = ((kb16 & 1) ? 0xFFFFu : 0u) | ((kb16 & 2) ? 0xFFFF0000u : 0u);
-          keep1 = ((kb16 & 0x100) ? 0xFFFFu : 0u) | ((kb16 & 0x200) ? 0xFFFF0000u : 0u);
+          const uint32_t k16 = (uint32_t)(keys >> (t * 16)) >> c0;
+          keep0 = ((k16 & 1) ? 0xFFFFu : 0u) | ((k16 & 2) ? 0xFFFF0000u : 0u);
+          keep1 = ((k16 & 0x100) ? 0xFFFFu : 0u) | ((k16 & 0x200) ? 0xFFFF0000u : 0u);
         }
 #pragma unroll
-        for (int t = 0; t < D / 8; t += 2) {
-          uint32_t b[4];  // columns t*8.. (keys 0-7, 8-15), then the next 8 columns
-          const int r = kk * 16 + (lane & 15), c = t + (lane >> 4);
-          ldsm4t(swz(vs + (c >> 3) * (KU * 128), r, c & 7), b);
-          if (masked) {
-            // values that were not loaded are zero, whatever the memory held
-            b[0] &= keep0; b[1] &= keep1; b[2] &= keep0; b[3] &= keep1;
-            if (n > 1) {
+        for (int d = 0; d < D / 16; d += 2) {
+          uint32_t a[2][4];  // columns d * 16 .. + 15 (+ 16) of the values by the 16 keys
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if (nonfinite_lo(b[e])) { b[e] &= 0xFFFF0000u; odd = true; }
-                if (nonfinite_hi(b[e])) { b[e] &= 0xFFFFu; odd = true; }
+          for (int q = 0; q < 2; ++q) {
+            const int r = t * 16 + (lane >> 4) * 8 + (lane & 7), c = (d + q) * 2 + ((lane >> 3) & 1);
+            ldsm4t(swz(vs + (c >> 3) * (KU * 128), r, c & 7), a[q]);
+            if (masked) {
+              // values that were not loaded are zero, whatever the memory held
+              a[q][0] &= keep0; a[q][1] &= keep0; a[q][2] &= keep1; a[q][3] &= keep1;
+              if (n > 1) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if (nonfinite_lo(a[q][e])) { a[q][e] &= 0xFFFF0000u; bad_v = true; }
+                  if (nonfinite_hi(a[q][e])) { a[q][e] &= 0xFFFFu; bad_v = true; }
+                }
               }
             }
           }
 #pragma unroll
-          for (int i = 0; i < NM; ++i) {
-            mma_bf16(o[i][t], hi[i], b[0], b[1]);
-            mma_bf16(o[i][t + 1], hi[i], b[2], b[3]);
-            mma_bf16(o[i][t], lo[i], b[0], b[1]);
-            mma_bf16(o[i][t + 1], lo[i], b[2], b[3]);
-          }
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < NB; ++i) mma_bf16(o[d + q][i], a[q], hi[i][0], hi[i][1]);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < NB; ++i) mma_bf16(o[d + q][i], a[q], lo[i][0], lo[i][1]);
         }
       }
-      if (masked && n > 1 && __any_sync(0xffffffffu, odd)) {
+      if (masked && n > 1 && __any_sync(0xffffffffu, bad_v)) {
         // 0 * inf would reach the rows that do not see the key: such values were left
         // out above and go to the rows that see it only
         for (int k = 0; k < KU; ++k) {
           if (!((keys >> k) & 1)) continue;
 #pragma unroll
-          for (int t = 0; t < D / 8; ++t) {
-            const uint32_t v = lds32(swz(vs + (t >> 3) * (KU * 128), k, t & 7) + c0 * 2);
+          for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-            for (int i = 0; i < 2 * NM; ++i) {
-              if (key0 + k > lim[i]) continue;
-              if (nonfinite_lo(v)) o[i >> 1][t][(i & 1) * 2] += bf_lo(v);
-              if (nonfinite_hi(v)) o[i >> 1][t][(i & 1) * 2 + 1] += bf_hi(v);
+            for (int q = 0; q < 2; ++q) {
+              const int col = d * 16 + q * 8 + g, c = col >> 3;
+              const uint32_t w2 = lds32(swz(vs + (c >> 3) * (KU * 128), k, c & 7) + ((col & 7) >> 1) * 4);
+              const uint32_t v = col & 1 ? w2 >> 16 : w2 & 0xFFFFu;
+              if ((v & 0x7F80u) != 0x7F80u) continue;
+#pragma unroll
+              for (int i = 0; i < NB; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (key0 + k <= lim[i][e]) o[d][i][2 * q + e] += bf_lo(v);
             }
-          }
         }
       }
       __syncwarp();  // every lane has read the block
@@ -357,89 +378,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
 #pragma unroll
-    for (int i = 0; i < 2 * NM; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-    }
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], 4);
+        l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], 8);
+        l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], 16);
+      }
     const bool whole = kb == 0 && cke == nk;
     const int slot = 2 * w + (kb == 0 ? 1 : 0);
-    if (!whole) {
-      note.x |= kb == 0 ? kGoesOn : cke == nk ? kCameIn | kEnded : kCameIn;
-      if (kb != 0) {
-        note.y = p.cu[cons.b];
-        note.z = cons.g;
-        note.w = n;
-      }
-    }
+    if (kb != 0 && cke == nk) note = {cons.first_worker(line), p.cu[cons.b], cons.g, n};
     __nv_bfloat16* ob = p.out + (int64_t)p.cu[cons.b] * p.ld_out + (int64_t)cons.g * p.G * D;
 #pragma unroll
-    for (int i = 0; i < 2 * NM; ++i) {
-      const int r = i * 8 + r0;
-      if (r >= nrows) continue;
+    for (int i = 0; i < NB; ++i) {
       if (whole) {
-        const float f = l[i] == 0.f ? 0.f : 1.0f / l[i];  // a row without keys is zero
-        __nv_bfloat16* dst = ob + (int64_t)(r / p.G) * p.ld_out + (r % p.G) * D + c0;
+        const float f0 = l[i][0] == 0.f ? 0.f : 1.0f / l[i][0], f1 = l[i][1] == 0.f ? 0.f : 1.0f / l[i][1];
+        // neighbouring columns sit in lanes g and g ^ 1: even g stores row c0, odd g row c0 + 1
+        const int r = i * 8 + c0 + (g & 1);
+        __nv_bfloat16* dst = ob + (int64_t)(r / p.G) * p.ld_out + (r % p.G) * D + (g & ~1);
 #pragma unroll
-        for (int t = 0; t < D / 8; ++t)
-          *reinterpret_cast<uint32_t*>(dst + t * 8) =
-              pack_bf16(o[i >> 1][t][(i & 1) * 2] * f, o[i >> 1][t][(i & 1) * 2 + 1] * f);
+        for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float x = o[d][i][2 * q] * f0, y = o[d][i][2 * q + 1] * f1;  // (a row without keys is zero)
+            const float other = __shfl_xor_sync(0xffffffffu, g & 1 ? x : y, 4);
+            const uint32_t two = g & 1 ? pack_bf16(other, y) : pack_bf16(x, other);
+            if (r < nrows) *reinterpret_cast<uint32_t*>(dst + d * 16 + q * 8) = two;
+          }
       } else {
-        float* dst = part_o(p, D, slot, r) + c0;
 #pragma unroll
-        for (int t = 0; t < D / 8; ++t)
-          *reinterpret_cast<float2*>(dst + t * 8) =
-              make_float2(o[i >> 1][t][(i & 1) * 2], o[i >> 1][t][(i & 1) * 2 + 1]);
-        if ((lane & 3) == 0) *reinterpret_cast<float2*>(part_ml(p, D, slot, r)) = make_float2(m[i], l[i]);
+        for (int e = 0; e < 2; ++e) {
+          const int r = i * 8 + c0 + e;
+          if (r >= nrows) continue;
+          float* dst = part_o(p, D, slot, r) + g;
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) {
+            dst[d * 16] = o[d][i][e];
+            dst[d * 16 + 8] = o[d][i][e + 2];
+          }
+          if (g == 0) *reinterpret_cast<float2*>(part_ml(p, D, slot, r)) = make_float2(m[i][e], l[i][e]);
+        }
       }
     }
     more = next_part(cons, ck, cke);
   }
-  if (lane == 0 && note.x) *note_of(p, D, w) = note;
+  if (lane == 0 && note.tokens) *note_of(p, D, w) = note;
 }
 
-// Join of the items that workers' borders cut: block w looks whether an item
-// ends in worker w's part that began before it.  Its partial records are the
-// second slot of the nearest worker before whose last item goes on, then the
-// first slots of the workers from there to w, in order of keys.  A warp
-// merges a share of a row's records; shares meet in shared memory.
-constexpr int kJoinWarps = 16;
+// Join of the items that workers' borders cut: block w does the item that ends
+// in worker w's part and began before it.  Its partial records are the second
+// slot of the worker it began with, then the first slots of the workers up to
+// w, in order of keys.  A warp merges a share of a row's records; shares meet
+// in shared memory.
+constexpr int kJoinWarps = 8;
 
 template <int D, bool CHUNK>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int E = D / 32;
   __shared__ float so[kJoinWarps][D], sml[kJoinWarps][2];
-  __shared__ int slots[kMaxWorkers + 1];
-  __shared__ int count_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w = blockIdx.x;
   wait_dependency();
-  const int4 note = *note_of(p, D, w);
-  if (!(note.x & kEnded)) return;
-  const int rows_all = note.w * p.G, per = (rows_all + gridDim.y - 1) / gridDim.y;
+  const int4 n4 = __ldcg(reinterpret_cast<const int4*>(note_of(p, D, w)));
+  const Note note = {n4.x, n4.y, n4.z, n4.w};
+  if (note.tokens == 0) return;
+  const int rows_all = note.tokens * p.G, per = (rows_all + gridDim.y - 1) / gridDim.y;
   const int row_base = blockIdx.y * per, rows = min(per, rows_all - row_base);
   if (rows <= 0) return;
-  if (warp == 0) {
-    // records from the last to the first (a worker whose part rounds to nothing left none)
-    int n = 1;
-    if (lane == 0) slots[0] = 2 * w;
-    for (int c0 = w - 1; c0 >= 0; c0 -= 32) {
-      const int c = c0 - lane, flags = c >= 0 ? note_of(p, D, c)->x : 0;
-      const unsigned begin = __ballot_sync(0xffffffffu, flags & kGoesOn);
-      const unsigned upto = begin ? (begin & -begin) - 1 : 0xffffffffu;  // workers after the one where it began
-      const unsigned in = __ballot_sync(0xffffffffu, flags & kCameIn) & upto;
-      const int at = n + __popc(in & ((1u << lane) - 1));
-      if (((in >> lane) & 1)) slots[at] = 2 * c;
-      n += __popc(in);
-      if (begin) {
-        if (lane == __ffs(begin) - 1) slots[n] = 2 * c + 1;
-        ++n;
-        break;
-      }
-    }
-    if (lane == 0) count_s = n;
-  }
-  __syncthreads();
-  const int count = count_s;
+  const int count = w - note.first + 1;
   int shares = 1;
   while (shares * 2 * rows <= kJoinWarps && shares * 4 < count) shares *= 2;
   const int rows_at_once = kJoinWarps / shares, share = warp % shares;
@@ -452,7 +458,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
-    constexpr int U = 8;  // records in flight
+    constexpr int U = CHUNK ? 4 : 16;  // records in flight
     for (int i0 = share; on && i0 < count; i0 += U * shares) {
       float2 ml[U];
       float v[U][E];
@@ -461,7 +467,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
         const int i = i0 + j * shares;
         ml[j] = make_float2(-INFINITY, 0.f);
         if (i < count) {
-          const int slot = slots[count - 1 - i];
+          const int slot = i == 0 ? 2 * note.first + 1 : 2 * (note.first + i);
           ml[j] = __ldcg(reinterpret_cast<const float2*>(part_ml(p, D, slot, rec)));
           const float* src = part_o(p, D, slot, rec) + lane * E;
           if constexpr (E == 4) {
@@ -508,7 +514,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     }
     if (on && share == 0) {
       const float f = l == 0.f ? 0.f : 1.0f / l;
-      __nv_bfloat16* dst = p.out + ((int64_t)note.y + tok) * p.ld_out + (int64_t)(note.z * p.G + head) * D + lane * E;
+      __nv_bfloat16* dst = p.out + ((int64_t)note.row0 + tok) * p.ld_out + (int64_t)(note.g * p.G + head) * D + lane * E;
       if constexpr (E == 4)
         *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f));
       else
@@ -534,21 +540,31 @@ cudaError_t launch_join(const AttnParams& p, int D, bool chunk, cudaStream_t str
   return D == 128 ? cudaLaunchKernelEx(&cfg, join_kernel<128, false>, p) : cudaLaunchKernelEx(&cfg, join_kernel<64, false>, p);
 }
 
-template <int D, int NM>
+template <int D, int NB>
 static cudaError_t launch_rows_t(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                                  cudaStream_t stream) {
-  constexpr int smem = smem_bytes_rows<D>();
+  constexpr int smem = smem_bytes_rows<D, NB>(), warps = row_warps(8 * NB);
   static std::atomic<uint64_t> allowed{0};
-  const cudaError_t e = allow_smem(rows_kernel<D, NM>, smem, &allowed);
+  const cudaError_t e = allow_smem(rows_kernel<D, NB>, smem, &allowed);
   if (e != cudaSuccess) return e;
-  rows_kernel<D, NM><<<(unsigned)(p.workers / kRowWarps), kThreads, smem, stream>>>(p, kmap, vmap);
+  rows_kernel<D, NB><<<(unsigned)(p.workers / warps), warps * 32, smem, stream>>>(p, kmap, vmap);
   return cudaGetLastError();
+}
+
+template <int D>
+static cudaError_t launch_rows_d(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                 cudaStream_t stream) {
+  switch ((p.rows + 7) / 8) {
+    case 1: return launch_rows_t<D, 1>(p, kmap, vmap, stream);
+    case 2: return launch_rows_t<D, 2>(p, kmap, vmap, stream);
+    case 3: return launch_rows_t<D, 3>(p, kmap, vmap, stream);
+    default: return launch_rows_t<D, 4>(p, kmap, vmap, stream);
+  }
 }
 
 cudaError_t launch_rows(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int D,
                         cudaStream_t stream) {
-  if (p.rows <= 16) return D == 128 ? launch_rows_t<128, 1>(p, kmap, vmap, stream) : launch_rows_t<64, 1>(p, kmap, vmap, stream);
-  return D == 128 ? launch_rows_t<128, 2>(p, kmap, vmap, stream) : launch_rows_t<64, 2>(p, kmap, vmap, stream);
+  return D == 128 ? launch_rows_d<128>(p, kmap, vmap, stream) : launch_rows_d<64>(p, kmap, vmap, stream);
 }
 
 }  // namespace mk
