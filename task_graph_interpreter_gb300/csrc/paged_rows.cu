@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
 cudaError_t launch_join(const AttnParams& p, int D, bool chunk, cudaStream_t stream) {
   if (p.workers < 2) return cudaSuccess;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)p.workers, chunk ? 8u : 1u);
+  cfg.gridDim = dim3((unsigned)p.workers, (unsigned)((p.rows + kJoinWarps - 1) / kJoinWarps));  // a row per warp
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
