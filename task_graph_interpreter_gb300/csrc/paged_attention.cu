@@ -44,7 +44,7 @@ bool few_rows(int max_new, int G) { return (int64_t)max_new * G <= kMaxFewRows; 
 // Two partial records and a note per worker (paged_attention.cuh).
 size_t workspace_bytes(int max_new, int G, int D, int sms) {
   const bool few = few_rows(max_new, G);
-  const size_t workers = (size_t)sms * (few ? row_warps(max_new * G) : 1), rows = few ? max_new * G : 256;
+  const size_t workers = (size_t)sms * (few ? row_warps(max_new * G) : 1), rows = few ? max_new * G : kTileRows;
   return 2 * workers * rows * (D + 2) * 4 + workers * 16;
 }
 
@@ -117,7 +117,7 @@ extern "C" int mk_paged_attention(void* stream_, int B, int N, int max_new, int 
   p.max_pages = max_pages; p.num_pages = num_pages;
   while ((1 << p.page_shift) < page_size) ++p.page_shift;
   p.workers = few ? sms * row_warps(max_new * G) : sms;
-  p.rows = few ? max_new * G : 256;
+  p.rows = few ? max_new * G : kTileRows;
   p.tq = few ? 0 : 128 / G;
 
   // pools as [rows, D], pages one after the other; a box is what one page gives a block of keys

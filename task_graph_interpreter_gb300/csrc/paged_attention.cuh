@@ -42,7 +42,7 @@ constexpr int kRowBlockBytes = 8192;  // keys and values of a few-rows block
 template <int D, bool CHUNK>
 struct Geometry {
   static constexpr int kKeys = CHUNK ? 128 : kRowBlockBytes / D / 4;  // keys per block
-  static constexpr int kFixed = CHUNK ? 384 : 64;           // an item's fixed cost, in keys
+  static constexpr int kFixed = CHUNK ? 320 : 64;           // an item's fixed cost, in keys
 };
 
 struct Seq {
@@ -212,11 +212,17 @@ struct Cursor {
   }
 };
 
-// The workspace: outputs [2 * workers slots][rows][D], (m, l) [2 * workers][rows][2], notes [workers].
+// The workspace: outputs [2 * workers slots][rows][D] (chunks: [D][rows], a row per lane), (m, l)
+// [2 * workers][rows][2], notes [workers].
 // Slot 2 w is worker w's part of an item that began before it, slot 2 w + 1
 // its part of an item that goes on behind it.
 __device__ __forceinline__ float* part_o(const AttnParams& p, int D, int slot, int row) {
   return p.part + ((size_t)slot * p.rows + row) * D;
+}
+// the same of a chunk: column 0 of the row, columns kTileRows apart
+constexpr int kTileRows = 256;
+__device__ __forceinline__ float* part_col(const AttnParams& p, int D, int slot, int row) {
+  return p.part + (size_t)slot * kTileRows * D + row;
 }
 __device__ __forceinline__ float* part_ml(const AttnParams& p, int D, int slot, int row) {
   return p.part + (size_t)2 * p.workers * p.rows * D + ((size_t)slot * p.rows + row) * 2;

@@ -6,12 +6,11 @@
 // so one pass over the keys serves the whole group.  One persistent CTA per
 // SM walks its part of the work line:
 //
-//   warps 0-7, 8-15   softmax of tile 0 and tile 1: two threads per row, each
-//            with 64 of a block's 128 keys
-//   warp 16  copies: query tiles, then key and value blocks of 128 keys, pages
+//   warps 0-3, 4-7   softmax of tile 0 and tile 1, one row per thread
+//   warp 8   copies: query tiles, then key and value blocks of 128 keys, pages
 //            gathered by TMA into 128-byte-swizzled tiles, a ring of blocks
-//   warps 17, 19  products of tile 0 and of tile 1: S_w = Q_w K^T, O_w += P_w V
-//   warp 18  division of the work, one descriptor per part of an item; and the
+//   warps 9, 11   products of tile 0 and of tile 1: S_w = Q_w K^T, O_w += P_w V
+//   warp 10  division of the work, one descriptor per part of an item; and the
 //            values of blocks that some row does not wholly see: what was not
 //            loaded becomes zero and what is not finite is set aside, since
 //            0 * NaN would reach rows behind the mask; the rows that do see
@@ -25,14 +24,22 @@
 // P_w is read, since products execute in order, and makes the barrier of
 // S_w (j + 1) cover P_w V (j) too.
 //
-// The two products of a block take the tensor cores 1025 cycles per tile (16
-// instructions of 64).  A tile's softmax has to fit beside the other tile's
-// products: with one thread per row it took 1300 cycles, and a block of both
-// tiles 3080.  Each tile's products have a warp of their own, since one
-// block's waits, instructions and commits take it some 1300 cycles; the two
-// pass a token, because instructions of both tiles mixed in the queue finish
-// together, and the tiles' softmaxes then run at the same time with the tensor
-// cores idle (3600 cycles).
+// What bounds it at D = 128: the products, 1025 cycles per tile and block (16
+// instructions of 64 cycles), 2050 for both tiles; an 8192-token prompt of 32
+// heads takes 2300 per block and 325 us in all (1.69 PFLOP/s of causal
+// arithmetic).  A tile's chain is S, its softmax (128 powers per row at 4.4
+// cycles of the SM's quarter, the maximum, two transfers: 1250 cycles), P V and
+// the next S; it fits beside the other tile's products only because the
+// second product starts on half of P and hand-overs are few:
+//  - each tile's products have a warp of their own (waits, instructions and
+//    commits of a block take one some 1300 cycles), and the two pass a token:
+//    instructions of both tiles mixed in the queue finish together, after which
+//    both softmaxes run at once with the tensor cores idle (3600 cycles);
+//  - two threads per row, which halves a thread's powers, exchange maxima and
+//    hold fewer registers: 2900 cycles.
+// At D = 64 P V is half the arithmetic in the same time (64-column products
+// run at half rate): 786 cycles of products per tile, 2200 per block of both
+// tiles, which the softmax sets.
 //
 // The running maximum moves only when a block exceeds it by 2^8 (the sums
 // have that much room in f32 and the probabilities' relative precision in
@@ -49,12 +56,12 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 384;
 constexpr int kStages = 5;
 constexpr int kSegRing = 4;
-// registers: the launch's 5 x 128 threads x 96, moved to the four softmax warpgroups
-constexpr int kLaunchRegs = 96, kConsumerRegs = 104, kOtherRegs = 64;
-static_assert(4 * kConsumerRegs + kOtherRegs <= 5 * kLaunchRegs, "register shares within the launch's");
+// registers: the launch's 3 x 128 threads x 168, moved to the softmax warpgroups
+constexpr int kLaunchRegs = 168, kConsumerRegs = 224, kOtherRegs = 56;
+static_assert(2 * kConsumerRegs + kOtherRegs <= 3 * kLaunchRegs, "register shares within the launch's");
 
 struct Segment {
   int row0;       // first query row of the item (token index in q)
@@ -78,13 +85,12 @@ static_assert(Smem<128>::kBytes <= 232448, "227 KB of shared memory per CTA");
 
 struct Control {
   uint64_t kv_full[kStages], kv_empty[kStages], v_raw[kStages], q_full[2], q_empty[2], s_full[2], p_full[2][2], o_done[2],
-      turn[2], row_bar[2][4], seg_full[kSegRing], seg_empty[kSegRing], drained[2], m_bar;
+      turn[2], seg_full[kSegRing], seg_empty[kSegRing], drained[2], m_bar;
   Segment segs[kSegRing];
   int odd[kSegRing];      // a value set aside in this part
   uint32_t missing[8];    // per key block (ring): pages of it that are not in the pool, one bit each
   uint32_t tmem;
   int gave_up;
-  float row[2][2][128];   // per tile and half: rows' maxima, at the end their sums
 };
 static_assert(sizeof(Control) <= Smem<128>::kControl, "control block");
 
@@ -114,7 +120,7 @@ __device__ __forceinline__ void zero_values(uint32_t v0, int valid, uint32_t mis
 // Bits of a bf16 pair that belong to a value that is not finite.
 __device__ __forceinline__ uint32_t odd_bits(uint32_t w) { return __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u); }
 
-// For 16 columns of a row's result, the sum of the values that are not finite, of the
+// For 32 columns of a row's result, the sum of the values that are not finite, of the
 // keys it sees in this part's masked blocks (they were set aside).
 __device__ __noinline__ void add_odd_values(const AttnParams& p, const Segment& s, int lim, int D, int c, float* add) {
   const int pmask = (1 << p.page_shift) - 1;
@@ -123,7 +129,7 @@ __device__ __noinline__ void add_odd_values(const AttnParams& p, const Segment& 
     if ((unsigned)id >= (unsigned)p.num_pages) continue;
     const __nv_bfloat16* v =
         p.v + ((((int64_t)id * p.Hkv + s.g) << p.page_shift) + (key & pmask)) * D + c;
-    for (int e = 0; e < 16; ++e) {
+    for (int e = 0; e < 32; ++e) {
       const float x = __bfloat162float(v[e]);
       if (!isfinite(x)) add[e] += x;
     }
@@ -171,10 +177,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&q_empty[i], 1);
       mbar_init(&drained[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i][0], 8);
-      mbar_init(&p_full[i][1], 8);
+      mbar_init(&p_full[i][0], 4);
+      mbar_init(&p_full[i][1], 4);
       mbar_init(&turn[i], 1);
-      for (int k = 0; k < 4; ++k) mbar_init(&ctl.row_bar[i][k], 2);
       mbar_init(&o_done[i], 1);
     }
     for (int i = 0; i < kSegRing; ++i) {
@@ -183,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_mbar_init();
   }
-  if (warp == 17) {
+  if (warp == 9) {
     tmem_alloc(&ctl.tmem, 512);
     tmem_relinquish();
   }
@@ -194,9 +199,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0);
   const int pmask = (1 << p.page_shift) - 1;
 
-  if (warp >= 16) {
+  if (warp >= 8) {
     reg_dec();
-    if (warp == 18) {
+    if (warp == 10) {
       // ------------------------------------------------ division of the work; values behind masks
       const Line line = measure_line<D, true>(p, lane);
       if (line.bad && blockIdx.x == 0 && lane == 0) set_status(p.status, MK_DEV_BAD_INDEX);
@@ -308,11 +313,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&seg_empty[sst]);
         ok = publish();
       }
-    } else if (warp == 16) {
+    } else if (warp == 8) {
       // ------------------------------------------------ copies
       const int box = min(128, pmask + 1), npg = 128 / box;
       uint32_t it = 0, nq = 0;  // key and value blocks; query tile pairs
       uint32_t raw_at = 0, raw_phase = 0, misses = 0, hole = 0;  // stages last filled through v_raw, and its phases; uses of m_bar
+      const auto load_q = [&](const Segment& s) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (!wait_phase(&q_empty[w], (nq & 1) ^ 1, &gave_up)) return false;
+          if (lane == 0) {
+            // (a second tile without tokens is not read)
+            const bool some = w == 0 || s.t0 + p.tq < s.n;
+            mbar_arrive_expect_tx(&q_full[w], some ? NH * p.tq * p.G * 128 : 0);
+            for (int h = 0; h < NH && some; ++h)
+              tma_load_3d(qt + w * S::kTile + h * S::kHalf, &qmap, h * 64, s.g * p.G, s.row0 + w * p.tq, &q_full[w]);
+          }
+          __syncwarp();
+        }
+        ++nq;
+        return true;
+      };
       for (uint32_t i = 0;; ++i) {
         const int sst = i % kSegRing;
         if (!wait_phase(&seg_full[sst], (i / kSegRing) & 1, &gave_up)) break;
@@ -321,7 +342,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&seg_empty[sst]);
         if (!s.valid) break;
         const int L = s.ctx + s.n, jd = first_masked(s);
-        bool ok = true;
+        // the query tiles, behind the first keys and values where the last item's products still read theirs
+        const bool early = __all_sync(0xffffffffu, mbar_test_wait(&q_empty[0], (nq & 1) ^ 1) &&
+                                                       mbar_test_wait(&q_empty[1], (nq & 1) ^ 1));
+        bool ok = !early || load_q(s);
         for (int k = s.k0; k < s.k1 && ok; ++k) {
           // lane = page * NH + column half
           const int pg = lane / NH, half = lane % NH, key = k * 128 + pg * box;
@@ -341,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int v = 0; v < 2; ++v, ++it) {
             const int st = it % kStages;
             if (!(ok = wait_phase(&kv_empty[st], ((it / kStages) & 1) ^ 1, &gave_up))) break;
-            // values of a masked block go by warp 18, which passes them on as full; those of other
+            // values of a masked block go by warp 10, which passes them on as full; those of other
             // blocks with a missing page by this warp
             const bool raw = v == 1 && k >= jd, holes = v == 1 && k < jd && miss;
             uint64_t* bar = raw ? &v_raw[st] : holes ? &m_bar : &kv_full[st];
@@ -365,22 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
           }
-          if (ok && k == s.k0) {
-            // the query tiles, behind the first keys and values, which need not wait for the last item's products
-#pragma unroll
-              for (int w = 0; w < 2 && ok; ++w) {
-              ok = wait_phase(&q_empty[w], (nq & 1) ^ 1, &gave_up);
-              if (ok && lane == 0) {
-                // (a second tile without tokens is not read)
-                const bool some = w == 0 || s.t0 + p.tq < s.n;
-                mbar_arrive_expect_tx(&q_full[w], some ? NH * p.tq * p.G * 128 : 0);
-                for (int h = 0; h < NH && some; ++h)
-                  tma_load_3d(qt + w * S::kTile + h * S::kHalf, &qmap, h * 64, s.g * p.G, s.row0 + w * p.tq, &q_full[w]);
-              }
-              __syncwarp();
-            }
-            nq += ok;
-          }
+          if (ok && k == s.k0 && !early) ok = load_q(s);
         }
         if (!ok) break;
       }
@@ -406,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Whatever steers this loop or makes up a descriptor is a vote's or a broadcast's result: the compiler
       // then knows it uniform and keeps the descriptors in uniform registers (otherwise each instruction
       // took 70 to 100 cycles to issue, the tensor cores 64 to execute).
-      const int w = warp == 17 ? 0 : 1;
+      const int w = warp == 9 ? 0 : 1;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, wait_phase(bar, parity, &gave_up)) != 0;
       };
@@ -469,9 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (elect_one()) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  const int kk = (e >> 1) * 4 + c * 2 + (e & 1);  // 16 keys; the second half's P lies 64 columns on
-                  tc_mma_bf16_ts_lo(to, ts + (kk >> 2) * 64 + (kk & 3) * 8, b_lo + kk * 128, vhi, idesc_o,
-                                    c + e != 0 ? 1u : j != 0 ? 1u : 0u);
+                  const int kk = c * 4 + e;  // 16 keys
+                  tc_mma_bf16_ts_lo(to, ts + kk * 8, b_lo + kk * 128, vhi, idesc_o, kk != 0 ? 1u : j != 0 ? 1u : 0u);
                 }
                 if (c == 1) {
                   tc_commit(&kv_empty[vst]);
@@ -518,75 +526,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // -------------------------------------------------- softmax: two threads per row
+    // -------------------------------------------------- softmax: one row per thread
     reg_inc();
-    // (104 registers, 64 of them a block's scores: what only the start and the end of a part need is
-    // worked out there again)
-    const int w = warp >> 3, hh = (warp >> 2) & 1;
-    // this warp's lanes (lane field, bits 16 up) and its half of the tile's columns of S; P takes the
-    // first half of those
-    const uint32_t ts = tmem + ((uint32_t)(warp & 3) << 21) + kSCol + w * 128 + hh * 64;
-    const uint32_t mine_s = smem_addr(&ctl.row[w][hh][(warp & 3) * 32 + lane]);
-    uint64_t* pair = &ctl.row_bar[w][warp & 3];
-    uint32_t ns = 0, no = 0, nx = 0, blk = 0;
-    auto meet = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(pair);
-      return wait_phase(pair, nx++ & 1, &gave_up);
-    };
-    // the value that the row's other thread has for this one's
-    auto exchange = [&](float mine, float& other) {
-      sts32(mine_s, __float_as_uint(mine));
-      if (!meet()) return false;
-      other = __uint_as_float(lds32(hh ? mine_s - 512 : mine_s + 512));
-      return true;
-    };
+    const int w = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's tensor-memory lanes (lane field, bits 16 up)
+    const uint32_t ts = tmem + lanes + kSCol + w * 128, to = tmem + lanes + kOCol + w * D;
+    const int tok_in = row / p.G, head = row % p.G;
+    uint32_t ns = 0, no = 0, blk = 0;
     for (uint32_t i = 0;; ++i) {
-      if (!wait_phase(&seg_full[i % kSegRing], (i / kSegRing) & 1, &gave_up)) break;
-      if (!segs[i % kSegRing].valid) break;
-      int nt, jm;
-      {
-        const Segment& s = segs[i % kSegRing];
-        nt = s.end[w] - s.k0;
-        // the first block that this tile does not wholly see
-        jm = ((s.ctx + s.t0 + w * p.tq + 1) >> 7) - s.k0;
-      }
+      const int sst = i % kSegRing;
+      if (!wait_phase(&seg_full[sst], (i / kSegRing) & 1, &gave_up)) break;
+      const Segment& s = segs[sst];
+      if (!s.valid) break;
+      const int k0 = s.k0, nt = s.end[w] - k0;
+      const int tok = s.t0 + w * p.tq + tok_in;  // in the request
+      const bool mine = tok_in < p.tq && tok < s.n;
+      const int lim = min(s.ctx + tok, s.ctx + s.n - 1);       // the last key this row sees
+      const int jm = ((s.ctx + s.t0 + w * p.tq + 1) >> 7) - k0;  // the first block that the tile does not wholly see
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       for (int j = 0; j < nt; ++j) {
         if (!(ok = wait_phase(&s_full[w], ns & 1, &gave_up))) break;
         ++ns;
         tc_fence_after();
-        float x[64];
-        tmem_ld32(ts, x);
-        tmem_ld32(ts + 32, x + 32);
+        float x[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, x + c * 32);
         tmem_wait_ld();
         const uint32_t miss = missing[(blk + j) & 7];
         if (j >= jm || miss) {
-          const Segment& s = segs[i % kSegRing];
-          // the last key this row sees, counted from this thread's first
-          const int last = min(s.ctx + s.t0 + w * p.tq + ((warp & 3) * 32 + lane) / p.G, s.ctx + s.n - 1) -
-                           ((s.k0 + j) * 128 + hh * 64);
+          const int last = lim - (k0 + j) * 128;
           if (miss) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if ((miss >> ((c + hh * 64) >> p.page_shift)) & 1) x[c] = -INFINITY;
+            for (int c = 0; c < 128; ++c)
+              if ((miss >> (c >> p.page_shift)) & 1) x[c] = -INFINITY;
           }
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
+          for (int c = 0; c < 128; ++c)
             if (c > last) x[c] = -INFINITY;
         }
-        float mx[4] = {x[0], x[1], x[2], x[3]};
+        float mx[8];
 #pragma unroll
-        for (int c = 4; c < 64; c += 8) {
+        for (int e = 0; e < 8; ++e) mx[e] = fmaxf(x[e], x[e + 8]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mx[e] = c + 4 + e < 64 ? fmaxf(fmaxf(mx[e], x[c + e]), x[c + 4 + e]) : fmaxf(mx[e], x[c + e]);
-        }
-        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale, other;
-        // (the other thread has read this before it hands over its P, which the next block's S waits for)
-        if (!(ok = exchange(top, other))) break;
-        top = fmaxf(top, other);
+        for (int c = 16; c < 128; c += 16)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mx[e] = fmaxf(fmaxf(mx[e], x[c + e]), x[c + 8 + e]);
+        const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * p.scale;
         if (j == 0) {
           m = top;
         } else {
@@ -596,101 +583,101 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f = far ? ex2(m - top) : 1.f;
             if (far) m = top;
             l *= f;
-            const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + kOCol + w * D + hh * (D / 2);
 #pragma unroll 1
-            for (int c = 0; c < D / 2; c += 16) {
-              float o[16];
-              tmem_ld16(to + c, o);
-              uint32_t r[16];
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              tmem_ld32(to + c, o);
+              tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(o[e] * f);
-              tmem_st16(to + c, r);
+              for (int e = 0; e < 32; ++e) o[e] *= f;
+              tmem_st32(to + c, o);
             }
           }
         }
         const float mu = m == -INFINITY ? 0.f : -m;
         const uint64_t scale2 = pair_f32(p.scale, p.scale), mu2 = pair_f32(mu, mu);
-        uint64_t sum[2] = {0, 0};
+        uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < 4; ++c) {
           uint32_t r[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 y = unpair_f32(fma2(pair_f32(x[c * 32 + 2 * e], x[c * 32 + 2 * e + 1]), scale2, mu2));
             const float a = ex2(y.x), b = ex2(y.y);
-            sum[e & 1] = add2(sum[e & 1], pair_f32(a, b));
+            sum[e & 3] = add2(sum[e & 3], pair_f32(a, b));
             r[e] = pack_bf16(a, b);
           }
           tmem_st16(ts + c * 16, r);
-          // a quarter of the keys per thread and side: the product starts on the first half of P
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[w][c]);
+          if (c & 1) {  // half of the keys: the product starts on them
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[w][c >> 1]);
+          }
         }
-        const float2 t = unpair_f32(add2(sum[0], sum[1]));
+        const float2 t = unpair_f32(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
         l += t.x + t.y;
       }
       if (!ok) break;
+      blk += s.k1 - k0;
       if (nt > 0) {
         if (!wait_phase(&o_done[w], no & 1, &gave_up)) break;
         ++no;
         tc_fence_after();
       }
-      // the row's sum; both threads have read it before the next part's maxima go there
-      float other;
-      if (!exchange(l, other)) break;
-      l += other;
-      if (!meet()) break;
-      const Segment& s = segs[i % kSegRing];
-      blk += s.k1 - s.k0;
-      const int row = (warp & 3) * 32 + lane, tok_in = row / p.G, head = row % p.G;
-      const int tok = s.t0 + w * p.tq + tok_in;
-      const bool mine = tok_in < p.tq && tok < s.n;
-      const bool set_aside = nt > 0 && odd[i % kSegRing];
-      const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + kOCol + w * D + hh * (D / 2);
+      const bool set_aside = nt > 0 && odd[sst];
       const float f = s.slot >= 0 ? 1.f : nt == 0 || l == 0.f ? 0.f : 1.0f / l;  // a row without keys is zero
-      __nv_bfloat16* dst = p.out + ((int64_t)s.row0 + w * p.tq + tok_in) * p.ld_out + (int64_t)(s.g * p.G + head) * D +
-                           hh * (D / 2);
+      __nv_bfloat16* dst = p.out + ((int64_t)s.row0 + w * p.tq + tok_in) * p.ld_out + (int64_t)(s.g * p.G + head) * D;
       float* rec = nullptr;
       if (s.slot >= 0) {
-        rec = part_o(p, D, s.slot, w * 128 + row) + hh * (D / 2);
-        if (mine && hh == 0)
-          *reinterpret_cast<float2*>(part_ml(p, D, s.slot, w * 128 + row)) = make_float2(m, nt > 0 ? l : 0.f);
+        rec = part_col(p, D, s.slot, w * 128 + row);
+        if (mine) *reinterpret_cast<float2*>(part_ml(p, D, s.slot, w * 128 + row)) = make_float2(m, nt > 0 ? l : 0.f);
       }
+      // (32-byte stores where a row allows it: lanes hold different rows, and each store takes a cycle per
+      // lane: 16-byte ones took 4000 cycles of a part's end, these 2500)
+      const bool wide = (p.ld_out & 15) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
 #pragma unroll 1
-      for (int c = 0; c < D / 2; c += 16) {
-        float o[16];
-        if (nt > 0) tmem_ld16(to + c, o);
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        if (nt > 0) {
+          tmem_ld32(to + c, o);
+          tmem_wait_ld();
+        }
         if (set_aside && mine) {
-          float add[16] = {};
-          add_odd_values(p, s, min(s.ctx + tok, s.ctx + s.n - 1), D, hh * (D / 2) + c, add);
+          float add[32] = {};
+          add_odd_values(p, s, lim, D, c, add);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] += add[e];
+          for (int e = 0; e < 32; ++e) o[e] += add[e];
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = f == 0.f ? 0.f : o[e] * f;
+        for (int e = 0; e < 32; ++e) o[e] = f == 0.f ? 0.f : o[e] * f;
         if (mine && !rec) {
 #pragma unroll
-          for (int e = 0; e < 16; e += 8)
-            *reinterpret_cast<uint4*>(dst + c + e) =
-                make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]), pack_bf16(o[e + 4], o[e + 5]),
-                           pack_bf16(o[e + 6], o[e + 7]));
+          for (int e = 0; e < 32; e += 16) {
+            uint32_t v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = pack_bf16(o[e + 2 * k], o[e + 2 * k + 1]);
+            if (wide) {
+              st_v8(dst + c + e, v);
+            } else {
+              *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(v[0], v[1], v[2], v[3]);
+              *reinterpret_cast<uint4*>(dst + c + e + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+            }
+          }
         } else if (mine && nt > 0) {
 #pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4*>(rec + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int e = 0; e < 32; ++e) rec[(c + e) * kTileRows] = o[e];
         }
       }
       tc_fence_before();  // O is read before the next part's first P is handed over
       __syncwarp();
-      if (lane == 0) mbar_arrive(&seg_empty[i % kSegRing]);
+      if (lane == 0) mbar_arrive(&seg_empty[sst]);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 17) tmem_dealloc(tmem, 512);
+  if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
 template <int D>

@@ -432,15 +432,21 @@ __global__ void __launch_bounds__(row_warps(8 * NB) * 32, 1)
 // in shared memory.
 constexpr int kJoinWarps = 8;
 
-template <int D, bool CHUNK>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttnParams p) {
+__device__ __forceinline__ Note read_note(const AttnParams& p, int D, int w) {
+  const int4 n = __ldcg(reinterpret_cast<const int4*>(note_of(p, D, w)));
+  return Note{n.x, n.y, n.z, n.w};
+}
+// the i-th partial record of a noted item
+__device__ __forceinline__ int record(const Note& n, int i) { return i == 0 ? 2 * n.first + 1 : 2 * (n.first + i); }
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_rows_kernel(const __grid_constant__ AttnParams p) {
   constexpr int E = D / 32;
   __shared__ float so[kJoinWarps][D], sml[kJoinWarps][2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w = blockIdx.x;
   wait_dependency();
-  const int4 n4 = __ldcg(reinterpret_cast<const int4*>(note_of(p, D, w)));
-  const Note note = {n4.x, n4.y, n4.z, n4.w};
+  const Note note = read_note(p, D, w);
   if (note.tokens == 0) return;
   const int rows_all = note.tokens * p.G, per = (rows_all + gridDim.y - 1) / gridDim.y;
   const int row_base = blockIdx.y * per, rows = min(per, rows_all - row_base);
@@ -452,13 +458,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   for (int rr0 = 0; rr0 < rows; rr0 += rows_at_once) {
     const int rr = rr0 + warp / shares;
     const bool on = rr < rows;
-    // row of the item -> token and head; row of a partial record
+    // row of the item -> token and head
     const int row = row_base + (on ? rr : 0), tok = row / p.G, head = row % p.G;
-    const int rec = CHUNK ? (tok / p.tq) * 128 + (tok % p.tq) * p.G + head : row;
     float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
-    constexpr int U = CHUNK ? 4 : 16;  // records in flight
+    constexpr int U = 16;  // records in flight
     for (int i0 = share; on && i0 < count; i0 += U * shares) {
       float2 ml[U];
       float v[U][E];
@@ -467,9 +472,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
         const int i = i0 + j * shares;
         ml[j] = make_float2(-INFINITY, 0.f);
         if (i < count) {
-          const int slot = i == 0 ? 2 * note.first + 1 : 2 * (note.first + i);
-          ml[j] = __ldcg(reinterpret_cast<const float2*>(part_ml(p, D, slot, rec)));
-          const float* src = part_o(p, D, slot, rec) + lane * E;
+          const int slot = record(note, i);
+          ml[j] = __ldcg(reinterpret_cast<const float2*>(part_ml(p, D, slot, row)));
+          const float* src = part_o(p, D, slot, row) + lane * E;
           if constexpr (E == 4) {
             const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
             v[j][0] = t.x; v[j][1] = t.y; v[j][2] = t.z; v[j][3] = t.w;
@@ -523,21 +528,58 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   }
 }
 
+// The same of chunks: a thread per row of the item's two tiles, a block per 16 columns.
+template <int D>
+__global__ void __launch_bounds__(kTileRows) join_chunk_kernel(const __grid_constant__ AttnParams p) {
+  wait_dependency();
+  const Note note = read_note(p, D, blockIdx.x);
+  if (note.tokens == 0) return;
+  const int row = threadIdx.x, col0 = blockIdx.y * 16;
+  const int t = (row & 127) / p.G, head = (row & 127) % p.G, tok = (row >> 7) * p.tq + t;
+  if (t >= p.tq || tok >= note.tokens) return;
+  const int count = blockIdx.x - note.first + 1;
+  float m = -INFINITY, l = 0.f, o[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) o[e] = 0.f;
+  for (int i = 0; i < count; ++i) {
+    const int slot = record(note, i);
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_ml(p, D, slot, row)));
+    const float* src = part_col(p, D, slot, row) + col0 * kTileRows;
+    float v[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = __ldcg(src + e * kTileRows);
+    if (ml.y == 0.f) continue;  // no key
+    const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
+    const float f0 = ex2(m - mu), f1 = ex2(ml.x - mu);
+    l = l * f0 + ml.y * f1;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = o[e] * f0 + v[e] * f1;
+    m = mn;
+  }
+  const float f = l == 0.f ? 0.f : 1.0f / l;
+  __nv_bfloat16* dst = p.out + ((int64_t)note.row0 + tok) * p.ld_out + (int64_t)(note.g * p.G + head) * D + col0;
+#pragma unroll
+  for (int e = 0; e < 16; e += 8)
+    *reinterpret_cast<uint4*>(dst + e) = make_uint4(pack_bf16(o[e] * f, o[e + 1] * f), pack_bf16(o[e + 2] * f, o[e + 3] * f),
+                                                    pack_bf16(o[e + 4] * f, o[e + 5] * f), pack_bf16(o[e + 6] * f, o[e + 7] * f));
+}
+
 }  // namespace
 
 cudaError_t launch_join(const AttnParams& p, int D, bool chunk, cudaStream_t stream) {
   if (p.workers < 2) return cudaSuccess;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)p.workers, (unsigned)((p.rows + kJoinWarps - 1) / kJoinWarps));  // a row per warp
-  cfg.blockDim = dim3(kJoinWarps * 32);
+  // a row per warp, or 16 columns of a pair of tiles per block
+  cfg.gridDim = dim3((unsigned)p.workers, (unsigned)(chunk ? D / 16 : (p.rows + kJoinWarps - 1) / kJoinWarps));
+  cfg.blockDim = dim3(chunk ? kTileRows : kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (chunk) return D == 128 ? cudaLaunchKernelEx(&cfg, join_kernel<128, true>, p) : cudaLaunchKernelEx(&cfg, join_kernel<64, true>, p);
-  return D == 128 ? cudaLaunchKernelEx(&cfg, join_kernel<128, false>, p) : cudaLaunchKernelEx(&cfg, join_kernel<64, false>, p);
+  if (chunk) return cudaLaunchKernelEx(&cfg, D == 128 ? join_chunk_kernel<128> : join_chunk_kernel<64>, p);
+  return cudaLaunchKernelEx(&cfg, D == 128 ? join_rows_kernel<128> : join_rows_kernel<64>, p);
 }
 
 template <int D, int NB>

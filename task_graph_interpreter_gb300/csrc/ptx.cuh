@@ -116,6 +116,13 @@ __device__ __forceinline__ void ldcg_v8f(const float* p, float (&v)[8]) {
                : "l"(p));
 }
 
+// 32 bytes (one L2 sector) in one request; p 32-byte aligned.
+__device__ __forceinline__ void st_v8(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // 32 bytes (four pairs, one L2 sector) in one request; p 32-byte aligned.
 __device__ __forceinline__ void ld_relaxed_v4u64(const uint64_t* p, uint64_t (&v)[4]) {
   asm volatile("ld.relaxed.gpu.global.v4.u64 {%0, %1, %2, %3}, [%4];"
