@@ -36,15 +36,15 @@ bool encode(EncodeTiledFn enc, CUtensorMap* m, const void* ptr, int rank, const 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Few query rows (tokens and drafts) or chunks: a request and head of at most
-// 32 rows fills two 16-row warp products; beyond that the 128-row tensor-core
-// tiles take fewer passes over the keys.
+// Few query rows or chunks: a request and head of at most eight rows fills one
+// warp product; beyond that the 128-row tensor-core tiles are faster although
+// mostly empty (paged_rows.cu has both sides).
 bool few_rows(int max_new, int G) { return (int64_t)max_new * G <= kMaxFewRows; }
 
 // Two partial records and a note per worker (paged_attention.cuh).
 size_t workspace_bytes(int max_new, int G, int D, int sms) {
   const bool few = few_rows(max_new, G);
-  const size_t workers = (size_t)sms * (few ? row_warps(max_new * G) : 1), rows = few ? max_new * G : kTileRows;
+  const size_t workers = (size_t)sms * (few ? kRowWarps : 1), rows = few ? max_new * G : kTileRows;
   return 2 * workers * rows * (D + 2) * 4 + workers * 16;
 }
 
@@ -116,7 +116,7 @@ extern "C" int mk_paged_attention(void* stream_, int B, int N, int max_new, int 
   p.B = B; p.N = N; p.Hq = Hq; p.Hkv = Hkv; p.G = G; p.max_new = max_new;
   p.max_pages = max_pages; p.num_pages = num_pages;
   while ((1 << p.page_shift) < page_size) ++p.page_shift;
-  p.workers = few ? sms * row_warps(max_new * G) : sms;
+  p.workers = few ? sms * kRowWarps : sms;
   p.rows = few ? max_new * G : kTileRows;
   p.tq = few ? 0 : 128 / G;
 

@@ -35,7 +35,7 @@ struct AttnParams {
   int tq;           // tokens per query tile (chunks): 128 / G
 };
 
-constexpr int kRowBlockBytes = 8192;  // keys and values of a few-rows block
+constexpr int kRowBlockBytes = 16384;  // keys and values of a few-rows block
 
 // Geometry of an item: few query rows (all of a request's), or a pair of
 // 128-row query tiles.
@@ -127,7 +127,7 @@ __device__ __forceinline__ Line measure_line(const AttnParams& p, int lane) {
   l.u = u;
   // whole blocks, a few at least: fewer records to join where there is little to do, and a worker behind an
   // item's first block always has a part of it
-  constexpr int K = Geometry<D, CHUNK>::kKeys, kLeast = (CHUNK ? 1 : 4) * K;
+  constexpr int K = Geometry<D, CHUNK>::kKeys, kLeast = (CHUNK ? 1 : 2) * K;
   const int64_t even = (u + p.workers - 1) / p.workers;
   l.part = even <= kLeast ? kLeast : (even + K - 1) / K * K;
   return l;
@@ -258,8 +258,7 @@ cudaError_t launch_rows(const AttnParams& p, const CUtensorMap& kmap, const CUte
                         cudaStream_t stream);
 cudaError_t launch_chunk(const AttnParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
                          const CUtensorMap& vmap, int D, cudaStream_t stream);
-// warps (workers) per CTA of the few-rows kernel
-__host__ __device__ constexpr int row_warps(int rows) { return rows <= 16 ? 8 : 7; }
-constexpr int kMaxFewRows = 32;  // query rows of a request and head that it takes
+constexpr int kRowWarps = 4;    // warps (workers) per CTA of the few-rows kernel
+constexpr int kMaxFewRows = 8;  // query rows of a request and head that it takes
 
 }  // namespace mk

@@ -1,17 +1,23 @@
-// Paged attention of few query rows per request and key/value head (single
-// tokens, drafts: at most 32 rows), and the join of partial results.
+// Paged attention of few query rows per request and key/value head (a decode
+// step's one token of a group of up to eight heads), and the join of partial
+// results.
 //
 // Every key and value is read once for a handful of rows, so HBM bounds it
 // and the arithmetic only has to keep out of the way: at the SM's share of
-// HBM (about 45 GB/s) a 16 KB block of keys and values lands per warp every
-// 1.5 us.  Each warp is a worker of its own, with its own part of the work
-// line, its own ring of three blocks filled by TMA (pages gathered into a
-// 128-byte-swizzled tile), its own softmax state in registers: no warp waits
-// for another.  The products run on m16n8k16 warp matrix instructions with
-// the keys (and the columns of the values) along their 16 and the query rows
-// along their 8, so a decode step's four rows fill half of one; a tcgen05
-// product has 128 rows, and would put two more round trips (through tensor
-// memory) into each block's chain.
+// HBM (about 45 GB/s) 64 KB of keys and values land per SM every 1.5 us.  Each
+// warp is a worker of its own, with its own part of the work line, its own
+// ring of blocks filled by TMA (pages gathered into a 128-byte-swizzled tile),
+// its own softmax state in registers: no warp waits for another.  The products
+// run on m16n8k16 warp matrix instructions with the keys (and the columns of
+// the values) along their 16 and the query rows along their 8, so a decode
+// step's four rows fill half of one; a tcgen05 product has 128 rows, and would
+// put two more round trips (through tensor memory) into each block's chain.
+// With nine to 32 rows the chunk kernel is faster all the same (four requests
+// of 32768 keys: 20 rows 93 us there, 113 us with three eights of rows here;
+// 64 requests of 512 to 8192 keys and four rows 199 us there, 178 us here),
+// so this one has a single eight.  Four warps with three blocks of 16 KB each:
+// 183 us for those 64 requests; six with two 187, twelve with two of 8 KB 189,
+// eight with three of 8 KB 193.
 //
 //   s = q k^T scale;  m' = max(m, max s);  p = 2^(s - m');
 //   l = l 2^(m - m') + sum p;  o = o 2^(m - m') + p v
@@ -27,12 +33,13 @@ namespace {
 using namespace ptx;
 
 constexpr int kStages = 3;
+static_assert(kMaxFewRows == 8, "the query tile is one eight of rows, a whole swizzle atom");
 constexpr int kHalfBytes = kRowBlockBytes / 2;  // keys, or values, of a block
 constexpr int kStageBytes = kRowBlockBytes;
 
-template <int D, int NB>
+template <int D>
 constexpr int smem_bytes_rows() {
-  return 1024 + row_warps(8 * NB) * (kStages * kStageBytes + 8 * NB * D * 2);
+  return 1024 + kRowWarps * (kStages * kStageBytes + kMaxFewRows * D * 2);
 }
 
 // 16-byte chunk c of row r in a tile of 128-byte rows, 128-byte swizzle
@@ -43,15 +50,13 @@ __device__ __forceinline__ uint32_t swz(uint32_t base, int r, int c) {
 __device__ __forceinline__ bool nonfinite_lo(uint32_t w) { return (w & 0x7F80u) == 0x7F80u; }
 __device__ __forceinline__ bool nonfinite_hi(uint32_t w) { return (w & 0x7F800000u) == 0x7F800000u; }
 
-// NB: eights of query rows
-template <int D, int NB>
-__global__ void __launch_bounds__(row_warps(8 * NB) * 32, 1)
+template <int D>
+__global__ void __launch_bounds__(kRowWarps * 32, 1)
     rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap) {
   constexpr int KU = Geometry<D, false>::kKeys;  // keys per block
   constexpr int NH = D / 64;                     // 128-byte column halves
   constexpr int NK = KU / 16;                    // key tiles of a block
-  constexpr int kRowWarps = row_warps(8 * NB);
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kRowWarps][kStages];
   __shared__ uint64_t live[kRowWarps][kStages];  // keys of a block that were loaded
@@ -59,7 +64,7 @@ __global__ void __launch_bounds__(row_warps(8 * NB) * 32, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* ring = base + warp * kStages * kStageBytes;
-  const uint32_t qs = smem_addr(base + kRowWarps * kStages * kStageBytes + warp * 8 * NB * D * 2);
+  const uint32_t qs = smem_addr(base + kRowWarps * kStages * kStageBytes + warp * kMaxFewRows * D * 2);
   if (threadIdx.x == 0) {
     gave_up = 0;
     for (int i = 0; i < kRowWarps; ++i)
@@ -159,47 +164,30 @@ __global__ void __launch_bounds__(row_warps(8 * NB) * 32, 1)
     // query rows, row r = token * G + head, into shared memory; rows past the last are zero
     const __nv_bfloat16* qb = p.q + (int64_t)p.cu[cons.b] * p.ld_q + (int64_t)cons.g * p.G * D;
     __syncwarp();
-    for (int i = lane; i < NB * 8 * (D / 8); i += 32) {
+    for (int i = lane; i < kMaxFewRows * (D / 8); i += 32) {
       const int r = i / (D / 8), c = i % (D / 8);
       uint4 v = make_uint4(0, 0, 0, 0);
       if (r < nrows) v = __ldg(reinterpret_cast<const uint4*>(qb + (int64_t)(r / p.G) * p.ld_q + (r % p.G) * D + c * 8));
-      const uint32_t a = swz(qs + (c >> 3) * (NB * 8 * 128), r, c & 7);
+      const uint32_t a = swz(qs + (c >> 3) * (kMaxFewRows * 128), r, c & 7);
       asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                    : "memory");
     }
     __syncwarp();
-    // the last key each of this lane's rows sees
-    int lim[NB][2];
+    // the last key each of this lane's two rows sees
+    int lim[2];
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
+    for (int e = 0; e < 2; ++e) lim[e] = c0 + e < nrows ? ctx + (c0 + e) / p.G : L - 1;
+    uint32_t qf[D / 32][4];  // query operands of two 16-column steps each
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = i * 8 + c0 + e;
-        lim[i][e] = r < nrows ? ctx + r / p.G : L - 1;
-      }
-    // query operands of two 16-column steps: columns kk * 16 .. + 31 of rows i * 8 .. + 7
-    auto load_q = [&](int i, int kk, uint32_t (&b)[4]) {
-      const int c = kk * 2 + (lane >> 3);
-      ldsm4(swz(qs + (c >> 3) * (NB * 8 * 128), i * 8 + (lane & 7), c & 7), b);
-    };
-    constexpr bool kQRegs = NB <= 2;
-    uint32_t qf[kQRegs ? NB : 1][kQRegs ? D / 32 : 1][4];
-    if constexpr (kQRegs) {
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int kk = 0; kk < D / 32; ++kk) load_q(i, kk * 2, qf[i][kk]);
+    for (int kk = 0; kk < D / 32; ++kk) {
+      const int c = kk * 4 + (lane >> 3);
+      ldsm4(swz(qs + (c >> 3) * (kMaxFewRows * 128), lane & 7, c & 7), qf[kk]);
     }
-    float o[D / 16][NB][4], m[NB][2], l[NB][2];
+    float o[D / 16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
+    for (int t = 0; t < D / 16; ++t)
 #pragma unroll
-      for (int t = 0; t < D / 16; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[t][i][e] = 0.f;
-      m[i][0] = m[i][1] = -INFINITY;
-      l[i][0] = l[i][1] = 0.f;
-    }
+      for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
 
     for (; ck < cke; ++ck) {
       const int st = done % kStages;
@@ -217,36 +205,19 @@ __global__ void __launch_bounds__(row_warps(8 * NB) * 32, 1)
       constexpr uint64_t kAll = KU == 64 ? ~0ull : (1ull << (KU & 63)) - 1;
       const bool masked = keys != kAll || key0 + KU > ctx + 1;
 
-      float s[NK][NB][4];
+      float s[NK][4];
 #pragma unroll
       for (int t = 0; t < NK; ++t)
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
+        for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[t][i][e] = 0.f;
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t a[NK][4];  // keys t * 16 .. + 15, columns kk * 16 .. + 15
+        const int c = kk * 2 + (lane >> 4);
 #pragma unroll
-      for (int kk = 0; kk < D / 32; ++kk) {
-        uint32_t b[NB][4];
+        for (int t = 0; t < NK; ++t) ldsm4(swz(ks + (c >> 3) * (KU * 128), t * 16 + (lane & 15), c & 7), a[t]);
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-          if constexpr (kQRegs) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) b[i][e] = qf[i][kk][e];
-          } else {
-            load_q(i, kk * 2, b[i]);
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t a[NK][4];  // keys t * 16 .. + 15, columns (kk * 2 + h) * 16 .. + 15
-          const int c = (kk * 2 + h) * 2 + (lane >> 4);
-#pragma unroll
-          for (int t = 0; t < NK; ++t) ldsm4(swz(ks + (c >> 3) * (KU * 128), t * 16 + (lane & 15), c & 7), a[t]);
-#pragma unroll
-          for (int t = 0; t < NK; ++t)
-#pragma unroll
-            for (int i = 0; i < NB; ++i) mma_bf16(s[t][i], a[t], b[i][2 * h], b[i][2 * h + 1]);
-        }
+        for (int t = 0; t < NK; ++t) mma_bf16(s[t], a[t], qf[kk >> 1][(kk & 1) * 2], qf[kk >> 1][(kk & 1) * 2 + 1]);
       }
       if (masked) {
 #pragma unroll
@@ -254,67 +225,56 @@ __global__ void __launch_bounds__(row_warps(8 * NB) * 32, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int k = t * 16 + g + (e >> 1) * 8;
-            const bool there = (keys >> k) & 1;
-#pragma unroll
-            for (int i = 0; i < NB; ++i)
-              if (!there || key0 + k > lim[i][e & 1]) s[t][i][e] = -INFINITY;
+            if (!((keys >> k) & 1) || key0 + k > lim[e & 1]) s[t][e] = -INFINITY;
           }
       }
       bool moved = false;
-      float mnew[NB][2], muse[NB][2];
+      float mnew[2], muse[2];
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
+      for (int e = 0; e < 2; ++e) {
+        float x = fmaxf(s[0][e], s[0][e + 2]);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = fmaxf(s[0][i][e], s[0][i][e + 2]);
-#pragma unroll
-          for (int t = 1; t < NK; ++t) x = fmaxf(x, fmaxf(s[t][i][e], s[t][i][e + 2]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          mnew[i][e] = fmaxf(m[i][e], x * p.scale);
-          muse[i][e] = mnew[i][e] == -INFINITY ? 0.f : mnew[i][e];  // a row without any key so far
-          moved |= mnew[i][e] != m[i][e];
-        }
+        for (int t = 1; t < NK; ++t) x = fmaxf(x, fmaxf(s[t][e], s[t][e + 2]));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        mnew[e] = fmaxf(m[e], x * p.scale);
+        muse[e] = mnew[e] == -INFINITY ? 0.f : mnew[e];  // a row without any key so far
+        moved |= mnew[e] != m[e];
+      }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
+        for (int e = 0; e < 2; ++e) {
+          const float f = ex2(m[e] - muse[e]);
+          m[e] = mnew[e];
+          l[e] *= f;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float f = ex2(m[i][e] - muse[i][e]);
-            m[i][e] = mnew[i][e];
-            l[i][e] *= f;
-#pragma unroll
-            for (int t = 0; t < D / 16; ++t) {
-              o[t][i][e] *= f;
-              o[t][i][e + 2] *= f;
-            }
+          for (int t = 0; t < D / 16; ++t) {
+            o[t][e] *= f;
+            o[t][e + 2] *= f;
           }
+        }
       }
 #pragma unroll
       for (int t = 0; t < NK; ++t)
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = ex2(fmaf(s[t][i][e], p.scale, -muse[i][e & 1]));
-            s[t][i][e] = x;
-            l[i][e & 1] += x;
-          }
+        for (int e = 0; e < 4; ++e) {
+          const float x = ex2(fmaf(s[t][e], p.scale, -muse[e & 1]));
+          s[t][e] = x;
+          l[e & 1] += x;
+        }
       bool bad_v = false;  // a value that is not finite behind a mask
 #pragma unroll
       for (int t = 0; t < NK; ++t) {
         // probabilities as operands: 16 keys by 8 rows, transposed, in two parts
-        uint32_t hi[NB][2], lo[NB][2];
+        uint32_t hi[2], lo[2];
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float x = s[t][i][2 * e], y = s[t][i][2 * e + 1];
-            const uint32_t h = pack_bf16(x, y);
-            hi[i][e] = movm_trans(h);
-            lo[i][e] = movm_trans(pack_bf16(x - bf_lo(h), y - bf_hi(h)));
-          }
+        for (int e = 0; e < 2; ++e) {
+          const float x = s[t][2 * e], y = s[t][2 * e + 1];
+          const uint32_t h = pack_bf16(x, y);
+          hi[e] = movm_trans(h);
+          lo[e] = movm_trans(pack_bf16(x - bf_lo(h), y - bf_hi(h)));
+        }
         // this lane's four keys of the 16: c0, c0 + 1, c0 + 8, c0 + 9
         uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
         if (masked) {
@@ -323,10 +283,10 @@ __global__ void __launch_bounds__(row_warps(8 * NB) * 32, 1)
           keep1 = ((k16 & 0x100) ? 0xFFFFu : 0u) | ((k16 & 0x200) ? 0xFFFF0000u : 0u);
         }
 #pragma unroll
-        for (int d = 0; d < D / 16; d += 2) {
-          uint32_t a[2][4];  // columns d * 16 .. + 15 (+ 16) of the values by the 16 keys
+        for (int d = 0; d < D / 16; d += 4) {
+          uint32_t a[4][4];  // columns (d + q) * 16 .. + 15 of the values by the 16 keys
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+          for (int q = 0; q < 4; ++q) {
             const int r = t * 16 + (lane >> 4) * 8 + (lane & 7), c = (d + q) * 2 + ((lane >> 3) & 1);
             ldsm4t(swz(vs + (c >> 3) * (KU * 128), r, c & 7), a[q]);
             if (masked) {
@@ -342,13 +302,9 @@ __global__ void __launch_bounds__(row_warps(8 * NB) * 32, 1)
             }
           }
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
+          for (int q = 0; q < 4; ++q) mma_bf16(o[d + q], a[q], hi[0], hi[1]);
 #pragma unroll
-            for (int i = 0; i < NB; ++i) mma_bf16(o[d + q][i], a[q], hi[i][0], hi[i][1]);
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int i = 0; i < NB; ++i) mma_bf16(o[d + q][i], a[q], lo[i][0], lo[i][1]);
+          for (int q = 0; q < 4; ++q) mma_bf16(o[d + q], a[q], lo[0], lo[1]);
         }
       }
       if (masked && n > 1 && __any_sync(0xffffffffu, bad_v)) {
@@ -365,10 +321,8 @@ __global__ void __launch_bounds__(row_warps(8 * NB) * 32, 1)
               const uint32_t v = col & 1 ? w2 >> 16 : w2 & 0xFFFFu;
               if ((v & 0x7F80u) != 0x7F80u) continue;
 #pragma unroll
-              for (int i = 0; i < NB; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  if (key0 + k <= lim[i][e]) o[d][i][2 * q + e] += bf_lo(v);
+              for (int e = 0; e < 2; ++e)
+                if (key0 + k <= lim[e]) o[d][2 * q + e] += bf_lo(v);
             }
         }
       }
@@ -378,46 +332,41 @@ __global__ void __launch_bounds__(row_warps(8 * NB) * 32, 1)
     }
 
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], 4);
-        l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], 8);
-        l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], 16);
-      }
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
+    }
     const bool whole = kb == 0 && cke == nk;
     const int slot = 2 * w + (kb == 0 ? 1 : 0);
     if (kb != 0 && cke == nk) note = {cons.first_worker(line), p.cu[cons.b], cons.g, n};
     __nv_bfloat16* ob = p.out + (int64_t)p.cu[cons.b] * p.ld_out + (int64_t)cons.g * p.G * D;
+    if (whole) {
+      const float f0 = l[0] == 0.f ? 0.f : 1.0f / l[0], f1 = l[1] == 0.f ? 0.f : 1.0f / l[1];
+      // neighbouring columns sit in lanes g and g ^ 1: even g stores row c0, odd g row c0 + 1
+      const int r = c0 + (g & 1);
+      __nv_bfloat16* dst = ob + (int64_t)(r / p.G) * p.ld_out + (r % p.G) * D + (g & ~1);
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      if (whole) {
-        const float f0 = l[i][0] == 0.f ? 0.f : 1.0f / l[i][0], f1 = l[i][1] == 0.f ? 0.f : 1.0f / l[i][1];
-        // neighbouring columns sit in lanes g and g ^ 1: even g stores row c0, odd g row c0 + 1
-        const int r = i * 8 + c0 + (g & 1);
-        __nv_bfloat16* dst = ob + (int64_t)(r / p.G) * p.ld_out + (r % p.G) * D + (g & ~1);
+      for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d)
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const float x = o[d][i][2 * q] * f0, y = o[d][i][2 * q + 1] * f1;  // (a row without keys is zero)
-            const float other = __shfl_xor_sync(0xffffffffu, g & 1 ? x : y, 4);
-            const uint32_t two = g & 1 ? pack_bf16(other, y) : pack_bf16(x, other);
-            if (r < nrows) *reinterpret_cast<uint32_t*>(dst + d * 16 + q * 8) = two;
-          }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = i * 8 + c0 + e;
-          if (r >= nrows) continue;
-          float* dst = part_o(p, D, slot, r) + g;
-#pragma unroll
-          for (int d = 0; d < D / 16; ++d) {
-            dst[d * 16] = o[d][i][e];
-            dst[d * 16 + 8] = o[d][i][e + 2];
-          }
-          if (g == 0) *reinterpret_cast<float2*>(part_ml(p, D, slot, r)) = make_float2(m[i][e], l[i][e]);
+        for (int q = 0; q < 2; ++q) {
+          const float x = o[d][2 * q] * f0, y = o[d][2 * q + 1] * f1;  // (a row without keys is zero)
+          const float other = __shfl_xor_sync(0xffffffffu, g & 1 ? x : y, 4);
+          const uint32_t two = g & 1 ? pack_bf16(other, y) : pack_bf16(x, other);
+          if (r < nrows) *reinterpret_cast<uint32_t*>(dst + d * 16 + q * 8) = two;
         }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = c0 + e;
+        if (r >= nrows) continue;
+        float* dst = part_o(p, D, slot, r) + g;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          dst[d * 16] = o[d][e];
+          dst[d * 16 + 8] = o[d][e + 2];
+        }
+        if (g == 0) *reinterpret_cast<float2*>(part_ml(p, D, slot, r)) = make_float2(m[e], l[e]);
       }
     }
     more = next_part(cons, ck, cke);
@@ -528,40 +477,50 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_rows_kernel(const __grid
   }
 }
 
-// The same of chunks: a thread per row of the item's two tiles, a block per 16 columns.
+// The same of chunks: a thread per row of the item's two tiles, a block per eight columns.
+constexpr int kJoinCols = 8;
+
 template <int D>
 __global__ void __launch_bounds__(kTileRows) join_chunk_kernel(const __grid_constant__ AttnParams p) {
   wait_dependency();
   const Note note = read_note(p, D, blockIdx.x);
   if (note.tokens == 0) return;
-  const int row = threadIdx.x, col0 = blockIdx.y * 16;
+  const int row = threadIdx.x, col0 = blockIdx.y * kJoinCols;
   const int t = (row & 127) / p.G, head = (row & 127) % p.G, tok = (row >> 7) * p.tq + t;
   if (t >= p.tq || tok >= note.tokens) return;
   const int count = blockIdx.x - note.first + 1;
-  float m = -INFINITY, l = 0.f, o[16];
+  float m = -INFINITY, l = 0.f, o[kJoinCols];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) o[e] = 0.f;
-  for (int i = 0; i < count; ++i) {
-    const int slot = record(note, i);
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_ml(p, D, slot, row)));
-    const float* src = part_col(p, D, slot, row) + col0 * kTileRows;
-    float v[16];
+  for (int e = 0; e < kJoinCols; ++e) o[e] = 0.f;
+  constexpr int U = 4;  // records in flight
+  for (int i0 = 0; i0 < count; i0 += U) {
+    float2 ml[U];
+    float v[U][kJoinCols];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = __ldcg(src + e * kTileRows);
-    if (ml.y == 0.f) continue;  // no key
-    const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
-    const float f0 = ex2(m - mu), f1 = ex2(ml.x - mu);
-    l = l * f0 + ml.y * f1;
+    for (int j = 0; j < U; ++j) {
+      ml[j] = make_float2(-INFINITY, 0.f);
+      if (i0 + j >= count) continue;
+      const int slot = record(note, i0 + j);
+      ml[j] = __ldcg(reinterpret_cast<const float2*>(part_ml(p, D, slot, row)));
+      const float* src = part_col(p, D, slot, row) + col0 * kTileRows;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) o[e] = o[e] * f0 + v[e] * f1;
-    m = mn;
+      for (int e = 0; e < kJoinCols; ++e) v[j][e] = __ldcg(src + e * kTileRows);
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (ml[j].y == 0.f) continue;  // no key, or no record
+      const float mn = fmaxf(m, ml[j].x), mu = mn == -INFINITY ? 0.f : mn;
+      const float f0 = ex2(m - mu), f1 = ex2(ml[j].x - mu);
+      l = l * f0 + ml[j].y * f1;
+#pragma unroll
+      for (int e = 0; e < kJoinCols; ++e) o[e] = o[e] * f0 + v[j][e] * f1;
+      m = mn;
+    }
   }
   const float f = l == 0.f ? 0.f : 1.0f / l;
   __nv_bfloat16* dst = p.out + ((int64_t)note.row0 + tok) * p.ld_out + (int64_t)(note.g * p.G + head) * D + col0;
-#pragma unroll
-  for (int e = 0; e < 16; e += 8)
-    *reinterpret_cast<uint4*>(dst + e) = make_uint4(pack_bf16(o[e] * f, o[e + 1] * f), pack_bf16(o[e + 2] * f, o[e + 3] * f),
-                                                    pack_bf16(o[e + 4] * f, o[e + 5] * f), pack_bf16(o[e + 6] * f, o[e + 7] * f));
+  *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f),
+                                              pack_bf16(o[4] * f, o[5] * f), pack_bf16(o[6] * f, o[7] * f));
 }
 
 }  // namespace
@@ -569,8 +528,8 @@ __global__ void __launch_bounds__(kTileRows) join_chunk_kernel(const __grid_cons
 cudaError_t launch_join(const AttnParams& p, int D, bool chunk, cudaStream_t stream) {
   if (p.workers < 2) return cudaSuccess;
   cudaLaunchConfig_t cfg{};
-  // a row per warp, or 16 columns of a pair of tiles per block
-  cfg.gridDim = dim3((unsigned)p.workers, (unsigned)(chunk ? D / 16 : (p.rows + kJoinWarps - 1) / kJoinWarps));
+  // a row per warp, or eight columns of a pair of tiles per block
+  cfg.gridDim = dim3((unsigned)p.workers, (unsigned)(chunk ? D / kJoinCols : (p.rows + kJoinWarps - 1) / kJoinWarps));
   cfg.blockDim = dim3(chunk ? kTileRows : kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -582,26 +541,15 @@ cudaError_t launch_join(const AttnParams& p, int D, bool chunk, cudaStream_t str
   return cudaLaunchKernelEx(&cfg, D == 128 ? join_rows_kernel<128> : join_rows_kernel<64>, p);
 }
 
-template <int D, int NB>
-static cudaError_t launch_rows_t(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                                 cudaStream_t stream) {
-  constexpr int smem = smem_bytes_rows<D, NB>(), warps = row_warps(8 * NB);
-  static std::atomic<uint64_t> allowed{0};
-  const cudaError_t e = allow_smem(rows_kernel<D, NB>, smem, &allowed);
-  if (e != cudaSuccess) return e;
-  rows_kernel<D, NB><<<(unsigned)(p.workers / warps), warps * 32, smem, stream>>>(p, kmap, vmap);
-  return cudaGetLastError();
-}
-
 template <int D>
 static cudaError_t launch_rows_d(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                                  cudaStream_t stream) {
-  switch ((p.rows + 7) / 8) {
-    case 1: return launch_rows_t<D, 1>(p, kmap, vmap, stream);
-    case 2: return launch_rows_t<D, 2>(p, kmap, vmap, stream);
-    case 3: return launch_rows_t<D, 3>(p, kmap, vmap, stream);
-    default: return launch_rows_t<D, 4>(p, kmap, vmap, stream);
-  }
+  constexpr int smem = smem_bytes_rows<D>();
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(rows_kernel<D>, smem, &allowed);
+  if (e != cudaSuccess) return e;
+  rows_kernel<D><<<(unsigned)(p.workers / kRowWarps), kRowWarps * 32, smem, stream>>>(p, kmap, vmap);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_rows(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int D,
