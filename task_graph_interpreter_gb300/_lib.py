@@ -118,6 +118,33 @@ def lib():
     return L
 
 
+_calls = None
+
+
+def calls():
+    """The CPython module of the tensor-level calls (csrc/calls.cpp), bound to
+    the loaded libmk.  Raises if it is missing (build it first)."""
+    global _calls
+    if _calls is not None:
+        return _calls
+    L = lib()
+    path = os.path.join(HERE, "_calls.so")
+    if not os.path.exists(path):
+        raise ImportError(f"_calls.so not built ({path}); run task_graph_interpreter_gb300.build.build()")
+    import importlib.machinery
+    import importlib.util
+
+    import torch  # noqa: F401  (its libraries come first)
+    loader = importlib.machinery.ExtensionFileLoader("_calls", path)
+    m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+    loader.exec_module(m)
+    m.bind(MkError, *[ctypes.cast(getattr(L, f), c_void_p).value for f in
+                      ("mk_paged_plan", "mk_qk_norm_rope", "mk_paged_attention", "mk_paged_attention_workspace",
+                       "mk_verify_drafts", "mk_last_error")])
+    _calls = m
+    return m
+
+
 def check(rc: int, fn: str):
     if rc != MK_OK:
         raise MkError(fn, rc, lib().mk_last_error().decode(errors="replace"))

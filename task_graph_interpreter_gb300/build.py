@@ -1,7 +1,8 @@
-"""Build libmk.so in-tree with nvcc for sm_103a.
+"""Build libmk.so in-tree with nvcc for sm_103a, and _calls.so, the CPython
+module of its tensor-level calls, with the host compiler.
 
 Each translation unit compiles in parallel into ``_build/``; the shared
-library lands next to this file.  No CMake, one -gencode.
+libraries land next to this file.  No CMake, one -gencode.
 """
 from __future__ import annotations
 
@@ -17,6 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmk.so")
+CALLS = os.path.join(HERE, "_calls.so")   # CPython module of the tensor-level calls (csrc/calls.cpp)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["graph.cpp", "runtime.cu", "megakernel.cu", "noalloc.cu", "paged.cu", "paged_rows.cu", "paged_chunk.cu",
            "paged_attention.cu", "verify.cu"]
@@ -45,10 +47,32 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _compile_calls() -> None:
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    lib = os.path.join(base, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("no C++ compiler found")
+    tmp = CALLS + ".tmp"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", INCLUDE, "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"), "-isystem", cuda,
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "calls.cpp"), "-o", tmp, "-L", lib,
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the C++ compiler failed on calls.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "mk.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
@@ -57,8 +81,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(_compile_calls)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        calls.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)
