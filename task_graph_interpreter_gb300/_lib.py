@@ -122,7 +122,7 @@ _calls = None
 
 
 def calls():
-    """The CPython module of the tensor-level calls (csrc/calls.cpp), bound to
+    """The CPython module of the tensor-level calls (csrc_ops/calls.cpp), bound to
     the loaded libmk.  Raises if it is missing (build it first)."""
     global _calls
     if _calls is not None:

@@ -14,14 +14,16 @@ from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-CSRC = os.path.join(HERE, "csrc")
+CSRC = os.path.join(HERE, "csrc")          # graph, lowering, interpreter
+OPS = os.path.join(HERE, "csrc_ops")       # operators that are called one by one
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmk.so")
-CALLS = os.path.join(HERE, "_calls.so")   # CPython module of the tensor-level calls (csrc/calls.cpp)
+CALLS = os.path.join(HERE, "_calls.so")   # CPython module of the tensor-level calls (csrc_ops/calls.cpp)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["graph.cpp", "runtime.cu", "megakernel.cu", "noalloc.cu", "paged.cu", "paged_rows.cu", "paged_chunk.cu",
-           "paged_attention.cu", "verify.cu"]
+SOURCES = [os.path.join(CSRC, f) for f in ("graph.cpp", "runtime.cu", "megakernel.cu", "noalloc.cu")] + \
+          [os.path.join(OPS, f) for f in ("paged.cu", "paged_rows.cu", "paged_chunk.cu", "paged_attention.cu",
+                                          "verify.cu")]
 
 
 def nvcc() -> str:
@@ -32,16 +34,17 @@ def nvcc() -> str:
 
 
 def _compile(src: str, verbose: bool) -> str:
-    obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
+    name = os.path.basename(src)
+    obj = os.path.join(BUILD, os.path.splitext(name)[0] + ".o")
     cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O3",
-           "-I", INCLUDE, "-I", CSRC, "-c", os.path.join(CSRC, src), "-o", obj]
+           "-I", INCLUDE, "-I", CSRC, "-I", OPS, "-c", src, "-o", obj]
     if src.endswith(".cpp"):
         cmd[1:1] = ["-x", "cu"]
-    if verbose and src == "megakernel.cu":
+    if verbose and name in ("megakernel.cu", "paged_chunk.cu"):
         cmd.append("-Xptxas=-v")
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"nvcc failed on {name}:\n{r.stdout}\n{r.stderr}")
     if verbose and r.stderr:
         sys.stderr.write(r.stderr)
     return obj
@@ -61,7 +64,7 @@ def _compile_calls() -> None:
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            "-I", INCLUDE, "-isystem", os.path.join(base, "include"),
            "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"), "-isystem", cuda,
-           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "calls.cpp"), "-o", tmp, "-L", lib,
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(OPS, "calls.cpp"), "-o", tmp, "-L", lib,
            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -73,7 +76,7 @@ def _stale() -> bool:
     if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return True
     t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "mk.h")]
+    deps = [os.path.join(d, f) for d in (CSRC, OPS) for f in os.listdir(d)] + [os.path.join(INCLUDE, "mk.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -5,7 +5,7 @@
 #include <cuda_bf16.h>
 
 #include "paged.h"
-#include "ptx.cuh"
+#include "ptx_ops.cuh"
 
 namespace mk {
 namespace {

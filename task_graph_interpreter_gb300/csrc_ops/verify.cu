@@ -23,7 +23,7 @@
 #include <cfloat>
 
 #include "paged.h"
-#include "ptx.cuh"
+#include "ptx_ops.cuh"
 
 namespace mk {
 namespace {

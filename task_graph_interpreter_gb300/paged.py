@@ -5,7 +5,7 @@ mk_paged_plan, mk_qk_norm_rope and mk_paged_attention of include/mk.h).
 The functions take PyTorch tensors on one CUDA device (not necessarily the
 current one) and enqueue on that device's current stream, or on ``stream``;
 nothing synchronises.  Tensors that do not fit raise ValueError, what the
-library refuses MkError (the checks are in csrc/calls.cpp).  Lengths,
+library refuses MkError (the checks are in csrc_ops/calls.cpp).  Lengths,
 tables and maps are int32 tensors that the GPU reads; what is wrong with
 their values is reported in ``status`` (an int32 device tensor, zeroed by the
 caller, that receives the first MK_DEV_* code).  ``PagedCache`` holds a
