@@ -8,6 +8,7 @@
 #include <atomic>
 #include <cstdint>
 #include <string>
+#include <utility>
 
 #include "graph.h"
 #include "mk.h"
@@ -46,6 +47,23 @@ cudaError_t allow_smem(Fn fn, int bytes, std::atomic<uint64_t>* done) {
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess && dev < 64) done->fetch_or(bit, std::memory_order_relaxed);
   return e;
+}
+
+// Launch with programmatic dependent launch: the kernel's CTAs may start before the kernel ahead of it in the
+// stream has ended, and wait for it themselves (wait_dependency) before they touch global memory.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
 inline int launch_result(cudaError_t e, const char* who) {

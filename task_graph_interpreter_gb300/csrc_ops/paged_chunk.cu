@@ -187,6 +187,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&seg_empty[i], kThreads / 32);
     }
     fence_mbar_init();
+    prefetch_tmap(&qmap);
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
   }
   if (warp == 9) {
     tmem_alloc(&ctl.tmem, 512);
@@ -196,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   launch_dependents();
+  wait_dependency();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0);
   const int pmask = (1 << p.page_shift) - 1;
 
@@ -694,8 +698,8 @@ cudaError_t launch_chunk_t(const AttnParams& p, const CUtensorMap& qmap, const C
   }
   // the register shares add up to this allocation: with fewer a warpgroup would wait for registers for ever
   if (regs.load(std::memory_order_relaxed) != kLaunchRegs) return cudaErrorInvalidKernelImage;
-  chunk_kernel<D><<<(unsigned)p.workers, kThreads, Smem<D>::kBytes, stream>>>(p, qmap, kmap, vmap);
-  return cudaGetLastError();
+  return launch_early(chunk_kernel<D>, dim3((unsigned)p.workers), dim3(kThreads), Smem<D>::kBytes, stream, p, qmap, kmap,
+                      vmap);
 }
 
 }  // namespace

@@ -70,9 +70,12 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     for (int i = 0; i < kRowWarps; ++i)
       for (int j = 0; j < kStages; ++j) mbar_init(&full[i][j], 1);
     fence_mbar_init();
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
   }
   __syncthreads();
   launch_dependents();
+  wait_dependency();
 
   const int w = warp * gridDim.x + blockIdx.x;  // (few workers are spread over the SMs)
   const Line line = measure_line<D, false>(p, lane);
@@ -394,6 +397,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_rows_kernel(const __grid
   __shared__ float so[kJoinWarps][D], sml[kJoinWarps][2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w = blockIdx.x;
+  launch_dependents();
   wait_dependency();
   const Note note = read_note(p, D, w);
   if (note.tokens == 0) return;
@@ -482,6 +486,7 @@ constexpr int kJoinCols = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kTileRows) join_chunk_kernel(const __grid_constant__ AttnParams p) {
+  launch_dependents();
   wait_dependency();
   const Note note = read_note(p, D, blockIdx.x);
   if (note.tokens == 0) return;
@@ -527,18 +532,12 @@ __global__ void __launch_bounds__(kTileRows) join_chunk_kernel(const __grid_cons
 
 cudaError_t launch_join(const AttnParams& p, int D, bool chunk, cudaStream_t stream) {
   if (p.workers < 2) return cudaSuccess;
-  cudaLaunchConfig_t cfg{};
   // a row per warp, or eight columns of a pair of tiles per block
-  cfg.gridDim = dim3((unsigned)p.workers, (unsigned)(chunk ? D / kJoinCols : (p.rows + kJoinWarps - 1) / kJoinWarps));
-  cfg.blockDim = dim3(chunk ? kTileRows : kJoinWarps * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (chunk) return cudaLaunchKernelEx(&cfg, D == 128 ? join_chunk_kernel<128> : join_chunk_kernel<64>, p);
-  return cudaLaunchKernelEx(&cfg, D == 128 ? join_rows_kernel<128> : join_rows_kernel<64>, p);
+  const dim3 grid((unsigned)p.workers, (unsigned)(chunk ? D / kJoinCols : (p.rows + kJoinWarps - 1) / kJoinWarps));
+  if (chunk)
+    return launch_early(D == 128 ? join_chunk_kernel<128> : join_chunk_kernel<64>, grid, dim3(kTileRows), 0, stream, p);
+  return launch_early(D == 128 ? join_rows_kernel<128> : join_rows_kernel<64>, grid, dim3(kJoinWarps * 32), 0, stream,
+                      p);
 }
 
 template <int D>
@@ -548,8 +547,8 @@ static cudaError_t launch_rows_d(const AttnParams& p, const CUtensorMap& kmap, c
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_smem(rows_kernel<D>, smem, &allowed);
   if (e != cudaSuccess) return e;
-  rows_kernel<D><<<(unsigned)(p.workers / kRowWarps), kRowWarps * 32, smem, stream>>>(p, kmap, vmap);
-  return cudaGetLastError();
+  return launch_early(rows_kernel<D>, dim3((unsigned)(p.workers / kRowWarps)), dim3(kRowWarps * 32), smem, stream, p,
+                      kmap, vmap);
 }
 
 cudaError_t launch_rows(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int D,
