@@ -75,11 +75,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   __shared__ int err_s;
   PlanPages pages(p, sm);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = blockIdx.x, ctas = gridDim.x;
+  const int rank = blockIdx.x, ctas = gridDim.x, threads = blockDim.x;
   const int count = *p.count;
   if (tid == 0) err_s = MK_DEV_OK;
   __syncthreads();
-  const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
+  const int per = (p.B + threads - 1) / threads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
   long long sum[3] = {0, 0, 0};
   int err = MK_DEV_OK;
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
-    long long v = warp_sum[k][lane];
+    long long v = lane < threads / 32 ? warp_sum[k][lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long u = __shfl_up_sync(0xffffffffu, v, o);
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   pages.count = count;
   pages.top = count + nback;
   __syncthreads();
-  const int gtid = rank * kPlanThreads + tid, nthr = ctas * kPlanThreads;
+  const int gtid = rank * threads + tid, nthr = ctas * threads;
   // positions and slots, four tokens a thread
   const int pmask = (1 << p.page_shift) - 1;
   for (int i0 = gtid * 4; i0 < p.max_tokens; i0 += nthr * 4) {
@@ -206,11 +206,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     __syncthreads();
   }
   if (rank != 0) return;
-  for (int b = tid; b < p.B; b += kPlanThreads) {
+  for (int b = tid; b < p.B; b += threads) {
     const int h = p.held[b];
     p.held_out[b] = ok ? pages.kept[b] + (pages.goff[b + 1] - pages.goff[b]) : h;
   }
-  for (int b = tid; b <= p.B; b += kPlanThreads) p.cu[b] = pages.cu[b];
+  for (int b = tid; b <= p.B; b += threads) p.cu[b] = pages.cu[b];
   if (tid == 0) {
     *p.count_out = ok ? left : count;
     if (!ok) set_status(p.status, code);
@@ -478,12 +478,14 @@ extern "C" int mk_paged_plan(void* stream, int B, int page_size, int max_pages, 
     const cudaError_t e = allow_smem(plan_kernel, 5 * (kPlanMaxB + 1) * 4, &allowed);
     if (e != cudaSuccess) return launch_result(e, "mk_paged_plan");
   }
-  // one CTA does 4096 tokens in one pass of its threads; the sums are the rest of its time
-  int ctas = 1;
+  // one CTA does 4096 tokens in one pass of its threads; the sums are the rest of its time, and fewer warps
+  // scan and meet sooner where they cover requests and tokens
+  int ctas = 1, threads = 128;
+  while (threads < kPlanThreads && (B > threads || max_tokens > threads * 4)) threads *= 2;
   while (ctas < kPlanCtas && max_tokens > ctas * kPlanThreads * 4) ctas *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kPlanThreads);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute at[1];
