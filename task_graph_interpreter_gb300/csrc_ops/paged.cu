@@ -23,9 +23,12 @@ namespace {
 //
 // Bound by latency, not bytes (a full server's step moves under 1 MB): one
 // cluster, whose CTAs each compute the sums for themselves (a block scan of
-// up to 4096 requests) rather than exchange them, and the only barrier
-// before the held pages, the count and the returned pages are stored, since
-// those may be the arrays that other CTAs still read.
+// up to 4096 requests) rather than exchange them.  One barrier: before it the
+// tables get their new pages, after it tokens look their pages up there and
+// the held pages, the count and the returned pages are stored, which may be
+// the arrays that were read before.  (509 requests, 65,000 tokens: 39 us of
+// work for one CTA, so eight; tokens that resolved new pages themselves took
+// twice as long.)
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanMaxB = 4096;
@@ -52,20 +55,14 @@ struct PlanPages {
     ctx = boff + p.B + 1;
     kept = ctx + p.B;
   }
-  // the a-th page taken from the stack
-  __device__ int taken(int a) const {
-    const int v = top - 1 - a;
-    if (v < count) return p.free_pages[v];
-    return returned(v - count);
-  }
+  // a returned page, and the a-th page taken from the stack
   __device__ int returned(int f) const {
     const int b = upper_row(boff, p.B, f);
     return p.table[(size_t)b * p.max_pages + kept[b] + (f - boff[b])];
   }
-  // the page holding page index j of request b after the step
-  __device__ int of(int b, int j) const {
-    if (j < kept[b]) return p.table[(size_t)b * p.max_pages + j];
-    return taken(goff[b] + j - kept[b]);
+  __device__ int taken(int a) const {
+    const int v = top - 1 - a;
+    return v < count ? p.free_pages[v] : returned(v - count);
   }
 };
 
@@ -157,26 +154,56 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   pages.top = count + nback;
   __syncthreads();
   const int gtid = rank * threads + tid, nthr = ctas * threads;
+  // block tables: the pages taken
+  for (int a = gtid; a < ngrow; a += nthr) {
+    const int b = upper_row(pages.goff, p.B, a);
+    const int id = pages.taken(a);
+    p.table[(size_t)b * p.max_pages + pages.kept[b] + (a - pages.goff[b])] = id;
+    if ((unsigned)id >= (unsigned)p.num_pages) set_status(p.status, MK_DEV_BAD_INDEX);
+  }
+  // the tables are whole, and every CTA has read the held pages and the count, which may be stored in place
+  if (ctas > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  } else {
+    __syncthreads();
+  }
   // positions and slots, four tokens a thread
   const int pmask = (1 << p.page_shift) - 1;
   for (int i0 = gtid * 4; i0 < p.max_tokens; i0 += nthr * 4) {
     int pos[4], slot[4];
-    int b = i0 < ntok ? upper_row(pages.cu, p.B, i0) : 0, at_b = -1, at_j = -1, id = -1;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = i0 + k;
-      pos[k] = slot[k] = -1;
-      if (i < ntok) {
-        while (pages.cu[b + 1] <= i) ++b;
-        pos[k] = pages.ctx[b] + (i - pages.cu[b]);
-        const int j = pos[k] >> p.page_shift;
-        if (j != at_j || b != at_b) {
-          id = pages.of(b, j);
-          at_b = b;
-          at_j = j;
+    for (int k = 0; k < 4; ++k) pos[k] = slot[k] = -1;
+    if (i0 < ntok) {
+      int b = upper_row(pages.cu, p.B, i0);
+      const int n = min(4, ntok - i0);
+      if (pages.cu[b + 1] >= i0 + n) {  // one request: at most two pages
+        const int p0 = pages.ctx[b] + (i0 - pages.cu[b]), j0 = p0 >> p.page_shift, j1 = (p0 + n - 1) >> p.page_shift;
+        const int32_t* at = p.table + (size_t)b * p.max_pages;
+        const int id0 = __ldcg(at + j0), id1 = __ldcg(at + j1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k >= n) break;
+          pos[k] = p0 + k;
+          slot[k] = (pos[k] >> p.page_shift) == j0 ? id0 : id1;
         }
-        if ((unsigned)id < (unsigned)p.num_pages) slot[k] = (id << p.page_shift) + (pos[k] & pmask);
-        else set_status(p.status, MK_DEV_BAD_INDEX);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k >= n) break;
+          while (pages.cu[b + 1] <= i0 + k) ++b;
+          pos[k] = pages.ctx[b] + (i0 + k - pages.cu[b]);
+          slot[k] = __ldcg(p.table + (size_t)b * p.max_pages + (pos[k] >> p.page_shift));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k >= n) break;
+        if ((unsigned)slot[k] < (unsigned)p.num_pages) {
+          slot[k] = (slot[k] << p.page_shift) + (pos[k] & pmask);
+        } else {
+          slot[k] = -1;
+          set_status(p.status, MK_DEV_BAD_INDEX);
+        }
       }
     }
     if (p.vec && i0 + 4 <= p.max_tokens) {
@@ -189,22 +216,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
       }
     }
   }
-  // block tables: the pages taken
-  for (int a = gtid; a < ngrow; a += nthr) {
-    const int b = upper_row(pages.goff, p.B, a);
-    const int id = pages.taken(a);
-    p.table[(size_t)b * p.max_pages + pages.kept[b] + (a - pages.goff[b])] = id;
-    if ((unsigned)id >= (unsigned)p.num_pages) set_status(p.status, MK_DEV_BAD_INDEX);
-  }
   // the returned pages that stay on the stack
   const int left = count + nback - ngrow;
   for (int f = gtid; f < nback && count + f < left; f += nthr) p.free_pages[count + f] = pages.returned(f);
-  // held pages and the count may be the arrays that every CTA reads above
-  if (ctas > 1) {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  } else {
-    __syncthreads();
-  }
   if (rank != 0) return;
   for (int b = tid; b < p.B; b += threads) {
     const int h = p.held[b];
