@@ -535,6 +535,70 @@ def test_two_calls_on_two_streams_with_their_own_workspaces():
             assert torch.equal(o, want)  # the division of the work and the order of joins are fixed
 
 
+@pytest.mark.parametrize("ctx,new", [([900, 33, 4000], [1, 2, 1]), ([900, 0, 33], [70, 130, 1])])
+def test_captured_attention_replays_on_new_inputs_and_repeats_itself(ctx, new):
+    """Two graphs of one memory pool, replayed in turn with eager calls between: the same bits as an eager call."""
+    Hq, Hkv, D, page = 8, 2, 128, 16
+    q, k, v, table, cu = attention_case(ctx, new, Hq, Hkv, D, page, 22)
+    args = (i32(cu), i32(ctx), max(new))
+    other = (1.5 * torch.randn(q.shape, device=DEV, generator=torch.Generator(device=DEV).manual_seed(3))).bfloat16()
+    want = [paged.attention(x, k, v, table, *args).clone() for x in (q, other)]
+    attention_close(want[1], *attention_ref(other, k, v, table, cu, ctx, page, D ** -0.5), D, is_few(new, Hq, Hkv))
+    buf = [torch.zeros_like(q) for _ in range(2)]
+    graphs, outs = [], []
+    pool = torch.cuda.graph_pool_handle()
+    for b in buf:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, pool=pool):
+            outs.append(paged.attention(b, k, v, table, *args))
+        graphs.append(g)
+    for first in (0, 1):
+        for i in (0, 1):
+            buf[i].copy_((q, other)[i ^ first])
+        for i in (0, 1):
+            graphs[i].replay()
+            got = outs[i].clone()
+            assert torch.equal(paged.attention(buf[i], k, v, table, *args), got)
+            assert torch.equal(got, want[i ^ first])
+
+
+@pytest.mark.parametrize("new", [[1, 2], [50, 3]])
+def test_offsets_past_32_bits_and_a_shared_prefix(new):
+    """Pools of 2.6 G elements whose last pages hold the requests; the second request shares the first one's pages
+    for its prefix."""
+    Hq, Hkv, D, page, pages = 16, 8, 128, 64, 40000
+    pool = [torch.zeros(pages, Hkv, page, D, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    assert pool[0].numel() > 1 << 31
+    ctx = [300, 130]
+    need = [-(-(c + n) // page) for c, n in zip(ctx, new)]
+    table = torch.full((2, max(need)), -1, dtype=torch.int32, device=DEV)
+    table[0, :need[0]] = torch.arange(pages - 1, pages - 1 - need[0], -1, device=DEV)
+    table[1, :2] = table[0, :2]                                  # 128 shared tokens
+    table[1, 2:need[1]] = torch.arange(pages - 20, pages - 20 - (need[1] - 2), -1, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(9)
+    width = (Hq + 2 * Hkv) * D
+    # both requests' cached tokens, then the new ones, through the norms and stores
+    for lens, at in ((ctx, [0, 128]), (new, ctx)):
+        slots, pos = [], []
+        for b in range(2):
+            first = at[b]
+            last = ctx[b] if at[b] != ctx[b] else ctx[b] + new[b]
+            for p in range(first, last):
+                pos.append(p)
+                slots.append(int(table[b, p // page]) * page + p % page)
+        x = torch.randn(len(pos), width, device=DEV, generator=g)
+        q = paged.qk_norm_rope(x, Hq, Hkv, D, i32(pos), i32(slots), pool[0], pool[1])
+    for t in (0, 1):
+        p = ctx[0] - 1
+        row = pool[t].view(-1)[((int(table[0, p // page]) * Hkv) * page + p % page) * D:][:D]
+        assert bool((row != 0).any())
+    cu = [0, new[0], sum(new)]
+    q = q.clone()
+    got = paged.attention(q, pool[0], pool[1], table, i32(cu), i32(ctx), max(new))
+    want, size, reach = attention_ref(q, pool[0], pool[1], table, cu, ctx, page, D ** -0.5)
+    attention_close(got, want, size, reach, D, is_few(new, Hq, Hkv))
+
+
 # ------------------------------------------------------------------ refusals of the tensor functions
 def test_tensor_functions_refuse_what_does_not_fit():
     q, k, v, table, cu = attention_case([30], [2], 8, 2, 64, 16, 31)
