@@ -78,7 +78,7 @@ template <int D>
 struct Smem {
   static constexpr int kHalf = 128 * 128;        // 128 rows of 128 bytes
   static constexpr int kTile = kHalf * (D / 64);
-  static constexpr int kControl = 3072;          // barriers, descriptors, row maxima (struct Control)
+  static constexpr int kControl = 1024;          // barriers, descriptors (struct Control)
   static constexpr int kBytes = kControl + 2 * kTile + kStages * kTile;
 };
 static_assert(Smem<128>::kBytes <= 232448, "227 KB of shared memory per CTA");

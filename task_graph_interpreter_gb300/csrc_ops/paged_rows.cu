@@ -377,12 +377,15 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   if (lane == 0 && note.tokens) *note_of(p, D, w) = note;
 }
 
-// Join of the items that workers' borders cut: block w does the item that ends
-// in worker w's part and began before it.  Its partial records are the second
-// slot of the worker it began with, then the first slots of the workers up to
-// w, in order of keys.  A warp merges a share of a row's records; shares meet
-// in shared memory.
-constexpr int kJoinWarps = 8;
+// Join of the items that workers' borders cut.  The item that ends in worker
+// w's part and began before it is worker w's to note; its partial records are
+// the second slot of the worker it began with, then the first slots of the
+// workers up to w, in order of keys.  A block looks at the notes of kRowWarps
+// workers and deals their items' rows out to its warps; with few rows several
+// warps share the records of one and meet in shared memory.  (A block per
+// worker spent more on its 608 blocks than on the records: one request of 4096
+// keys 14.2 us, 64 of 512 to 8192 keys 175.4; this way 13.2 and 173.8.)
+constexpr int kJoinWarps = 16;
 
 __device__ __forceinline__ Note read_note(const AttnParams& p, int D, int w) {
   const int4 n = __ldcg(reinterpret_cast<const int4*>(note_of(p, D, w)));
@@ -396,28 +399,46 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_rows_kernel(const __grid
   constexpr int E = D / 32;
   __shared__ float so[kJoinWarps][D], sml[kJoinWarps][2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int w = blockIdx.x;
   launch_dependents();
   wait_dependency();
-  const Note note = read_note(p, D, w);
-  if (note.tokens == 0) return;
-  const int rows_all = note.tokens * p.G, per = (rows_all + gridDim.y - 1) / gridDim.y;
-  const int row_base = blockIdx.y * per, rows = min(per, rows_all - row_base);
-  if (rows <= 0) return;
-  const int count = w - note.first + 1;
+  Note notes[kRowWarps];
+#pragma unroll
+  for (int k = 0; k < kRowWarps; ++k) notes[k] = read_note(p, D, blockIdx.x + k * gridDim.x);
+  int total = 0, most = 0;  // rows of the noted items; records of the longest
+#pragma unroll
+  for (int k = 0; k < kRowWarps; ++k) {
+    if (notes[k].tokens == 0) continue;
+    total += notes[k].tokens * p.G;
+    most = max(most, (int)(blockIdx.x + k * gridDim.x) - notes[k].first + 1);
+  }
   int shares = 1;
-  while (shares * 2 * rows <= kJoinWarps && shares * 4 < count) shares *= 2;
-  const int rows_at_once = kJoinWarps / shares, share = warp % shares;
-  for (int rr0 = 0; rr0 < rows; rr0 += rows_at_once) {
-    const int rr = rr0 + warp / shares;
-    const bool on = rr < rows;
-    // row of the item -> token and head
-    const int row = row_base + (on ? rr : 0), tok = row / p.G, head = row % p.G;
+  while (shares * 2 * total <= kJoinWarps && shares * 4 < most) shares *= 2;
+  const int at_once = kJoinWarps / shares, share = warp % shares;
+  for (int r0 = 0; r0 < total; r0 += at_once) {
+    // this warp's row: of which item, which token and head
+    int row = r0 + warp / shares, w = 0;
+    const bool on = row < total;
+    Note note = {0, 0, 0, 0};
+    bool found = false;
+#pragma unroll
+    for (int k = 0; k < kRowWarps; ++k) {
+      const int rows = notes[k].tokens * p.G;
+      if (on && !found) {
+        if (row < rows) {
+          found = true;
+          note = notes[k];
+          w = blockIdx.x + k * gridDim.x;
+        } else {
+          row -= rows;
+        }
+      }
+    }
+    const int count = on ? w - note.first + 1 : 0, tok = row / p.G, head = row % p.G;
     float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
-    constexpr int U = 16;  // records in flight
-    for (int i0 = share; on && i0 < count; i0 += U * shares) {
+    constexpr int U = 8;  // records in flight
+    for (int i0 = share; i0 < count; i0 += U * shares) {
       float2 ml[U];
       float v[U][E];
 #pragma unroll
@@ -524,20 +545,22 @@ __global__ void __launch_bounds__(kTileRows) join_chunk_kernel(const __grid_cons
   }
   const float f = l == 0.f ? 0.f : 1.0f / l;
   __nv_bfloat16* dst = p.out + ((int64_t)note.row0 + tok) * p.ld_out + (int64_t)(note.g * p.G + head) * D + col0;
-  *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f),
-                                              pack_bf16(o[4] * f, o[5] * f), pack_bf16(o[6] * f, o[7] * f));
+#pragma unroll
+  for (int e = 0; e < kJoinCols; e += 8)
+    *reinterpret_cast<uint4*>(dst + e) =
+        make_uint4(pack_bf16(o[e] * f, o[e + 1] * f), pack_bf16(o[e + 2] * f, o[e + 3] * f),
+                   pack_bf16(o[e + 4] * f, o[e + 5] * f), pack_bf16(o[e + 6] * f, o[e + 7] * f));
 }
 
 }  // namespace
 
 cudaError_t launch_join(const AttnParams& p, int D, bool chunk, cudaStream_t stream) {
   if (p.workers < 2) return cudaSuccess;
-  // a row per warp, or eight columns of a pair of tiles per block
-  const dim3 grid((unsigned)p.workers, (unsigned)(chunk ? D / kJoinCols : (p.rows + kJoinWarps - 1) / kJoinWarps));
-  if (chunk)
-    return launch_early(D == 128 ? join_chunk_kernel<128> : join_chunk_kernel<64>, grid, dim3(kTileRows), 0, stream, p);
-  return launch_early(D == 128 ? join_rows_kernel<128> : join_rows_kernel<64>, grid, dim3(kJoinWarps * 32), 0, stream,
-                      p);
+  if (chunk)  // a block per worker and eight columns
+    return launch_early(D == 128 ? join_chunk_kernel<128> : join_chunk_kernel<64>,
+                        dim3((unsigned)p.workers, (unsigned)(D / kJoinCols)), dim3(kTileRows), 0, stream, p);
+  return launch_early(D == 128 ? join_rows_kernel<128> : join_rows_kernel<64>, dim3((unsigned)(p.workers / kRowWarps)),
+                      dim3(kJoinWarps * 32), 0, stream, p);
 }
 
 template <int D>
