@@ -94,7 +94,9 @@ __device__ __forceinline__ int64_t warp_incl_scan(int64_t v, int lane) {
 // routine, and the workers' start is on the critical path of a small call)
 __device__ __forceinline__ int small_quotient(int64_t r, int64_t d) {
   int q = (int)((float)r / (float)d);
+#pragma unroll 1
   while ((int64_t)q * d > r) --q;
+#pragma unroll 1
   while ((int64_t)(q + 1) * d <= r) ++q;
   return q;
 }
@@ -114,6 +116,7 @@ __device__ __forceinline__ Line measure_line(const AttnParams& p, int lane) {
   l.own = 0;
   int64_t u = 0;
   bool wrong = false;
+#pragma unroll 1
   for (int b = lane; b < p.B; b += 32) {
     const Seq s = load_seq<D, CHUNK>(p, b);
     const int64_t v = s.per_head * p.Hkv;
@@ -163,6 +166,7 @@ struct Cursor {
   // the item holding place x of the line (0 <= x < U)
   __device__ __forceinline__ void find(const AttnParams& p, const Line& line, int64_t x, int lane) {
     int64_t before = 0;
+#pragma unroll 1
     for (int b0 = 0;; b0 += 32) {
       int64_t own = line.own;
       if (b0 > 0) own = b0 + lane < p.B ? load_seq<D, CHUNK>(p, b0 + lane).per_head * p.Hkv : 0;
@@ -189,6 +193,7 @@ struct Cursor {
     if (CHUNK) {
       const int64_t rr = x - start;
       int lo = 0, hi = s.nq - 1;  // the last tile that begins at or before rr
+#pragma unroll 1
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (mid * s.base + s.step * ((int64_t)mid * (mid - 1) / 2) <= rr) lo = mid;
@@ -205,6 +210,7 @@ struct Cursor {
     i = 0;
     if (++g < p.Hkv) return;
     g = 0;
+#pragma unroll 1
     while (++b < p.B) {
       s = load_seq<D, CHUNK>(p, b);
       if (s.n > 0) return;
@@ -237,21 +243,17 @@ __device__ __forceinline__ Note* note_of(const AttnParams& p, int D, int w) {
   return reinterpret_cast<Note*>(p.part + (size_t)2 * p.workers * p.rows * (D + 2)) + w;
 }
 
-// Wait for a phase of an mbarrier, at most about two seconds, or until
-// another thread has given up.
+// Wait for a phase of an mbarrier, at most about a second, or until another
+// thread has given up.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  for (;;) {
+  const uint32_t t0 = (uint32_t)clock();
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (ptx::mbar_try_wait(bar, parity)) return true;
+  while (!ptx::mbar_try_wait(bar, parity)) {
     if (*abort) return false;
-    if (clock64() - t0 > 4000000000ll) {
-      *abort = 1;
-      return false;
-    }
+    if ((uint32_t)clock() - t0 > 2000000000u) *abort = 1;
   }
+  return true;
 }
 
 cudaError_t launch_rows(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int D,

@@ -26,7 +26,7 @@
 //
 // What bounds it at D = 128: the products, 1025 cycles per tile and block (16
 // instructions of 64 cycles), 2050 for both tiles; an 8192-token prompt of 32
-// heads takes 2300 per block and 325 us in all (1.69 PFLOP/s of causal
+// heads takes 2300 per block and 313 us in all (1.76 PFLOP/s of causal
 // arithmetic).  A tile's chain is S, its softmax (128 powers per row at 4.4
 // cycles of the SM's quarter, the maximum, two transfers: 1250 cycles), P V and
 // the next S; it fits beside the other tile's products only because the
@@ -40,6 +40,17 @@
 // At D = 64 P V is half the arithmetic in the same time (64-column products
 // run at half rate): 786 cycles of products per tile, 2200 per block of both
 // tiles, which the softmax sets.
+//
+// Short parts are bound by what surrounds their blocks: the first scores'
+// wait, the last product and the store of the results, the values behind
+// masks, and instructions.  Warps of four kinds go through all of their code
+// for each part, which is more than the instruction cache keeps: bringing it
+// from 109 KB to 66 (loops left rolled, each step written out once) and moving
+// registers from the softmaxes to the others, which spilled, took eleven
+// requests of 400 new tokens, 64 query heads on 8, from 87 to 75 us, eight
+// requests of five tokens from 19 to 15.  Results by way of shared memory and TMA
+// (two ring places lent at the end of a part) took 309 us for the long prompt but
+// 82 for the eleven requests, for its code.
 //
 // The running maximum moves only when a block exceeds it by 2^8 (the sums
 // have that much room in f32 and the probabilities' relative precision in
@@ -60,7 +71,7 @@ constexpr int kThreads = 384;
 constexpr int kStages = 5;
 constexpr int kSegRing = 4;
 // registers: the launch's 3 x 128 threads x 168, moved to the softmax warpgroups
-constexpr int kLaunchRegs = 168, kConsumerRegs = 224, kOtherRegs = 56;
+constexpr int kLaunchRegs = 168, kConsumerRegs = 208, kOtherRegs = 88;
 static_assert(2 * kConsumerRegs + kOtherRegs <= 3 * kLaunchRegs, "register shares within the launch's");
 
 struct Segment {
@@ -84,8 +95,8 @@ struct Smem {
 static_assert(Smem<128>::kBytes <= 232448, "227 KB of shared memory per CTA");
 
 struct Control {
-  uint64_t kv_full[kStages], kv_empty[kStages], v_raw[kStages], q_full[2], q_empty[2], s_full[2], p_full[2][2], o_done[2],
-      turn[2], seg_full[kSegRing], seg_empty[kSegRing], drained[2], m_bar;
+  uint64_t kv_full[kStages], kv_empty[kStages], v_raw[kStages], q_full[2], q_empty[2], s_full[2], p_full[2][2],
+      o_done[2], turn[2], seg_full[kSegRing], seg_empty[kSegRing], drained[2], m_bar;
   Segment segs[kSegRing];
   int odd[kSegRing];      // a value set aside in this part
   uint32_t missing[8];    // per key block (ring): pages of it that are not in the pool, one bit each
@@ -97,19 +108,21 @@ static_assert(sizeof(Control) <= Smem<128>::kControl, "control block");
 __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs)); }
 __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs)); }
 
-// The first key block with a key that the item's first row does not see.
-__device__ __forceinline__ int first_masked(const Segment& s) { return (s.ctx + s.t0 + 1) >> 7; }
+// The first key that the item's first row does not see, and the first that no row of it does.
+__device__ __forceinline__ int masked_from(const Segment& s) { return s.ctx + s.t0 + 1; }
+__device__ __forceinline__ int masked_to(const Segment& s, const AttnParams& p) {
+  return s.ctx + min(s.n, s.t0 + 2 * p.tq);
+}
 
 // Zero the rows of a value block from `valid` on and those of missing pages,
 // and let the tensor cores see it.  A whole warp.
 template <int D>
 __device__ __forceinline__ void zero_values(uint32_t v0, int valid, uint32_t miss, int page_shift, int lane) {
-  constexpr int NH = D / 64;
-  for (int e = lane; e < 128 * NH * 8; e += 32) {
-    const int key = e / (NH * 8), c = e % (NH * 8);
-    if (key >= valid || ((miss >> (key >> page_shift)) & 1))
-      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v0 + (c >> 3) * Smem<D>::kHalf + key * 128 +
-                                                                   (c & 7) * 16),
+  for (int key = (miss ? 0 : valid & ~3) + (lane >> 3); key < 128; key += 4) {
+    if (key < valid && !((miss >> (key >> page_shift)) & 1)) continue;
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v0 + h * Smem<D>::kHalf + key * 128 + (lane & 7) * 16),
                    "r"(0)
                    : "memory");
   }
@@ -117,14 +130,22 @@ __device__ __forceinline__ void zero_values(uint32_t v0, int valid, uint32_t mis
   __syncwarp();
 }
 
+// Of 32 keys of a block, from `key` on, those of missing pages.
+__device__ __forceinline__ uint32_t missing_keys(uint32_t miss, int key, int page_shift) {
+  uint32_t bits = 0;
+#pragma unroll 1
+  for (int c = 0; c < 32; ++c) bits |= ((miss >> ((key + c) >> page_shift)) & 1) << c;
+  return bits;
+}
+
 // Bits of a bf16 pair that belong to a value that is not finite.
 __device__ __forceinline__ uint32_t odd_bits(uint32_t w) { return __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u); }
 
 // For 32 columns of a row's result, the sum of the values that are not finite, of the
-// keys it sees in this part's masked blocks (they were set aside).
+// keys it sees that other rows of the item do not (they were set aside).
 __device__ __noinline__ void add_odd_values(const AttnParams& p, const Segment& s, int lim, int D, int c, float* add) {
   const int pmask = (1 << p.page_shift) - 1;
-  for (int key = max(s.k0, first_masked(s)) * 128; key <= min(lim, s.k1 * 128 - 1); ++key) {
+  for (int key = max(s.k0 * 128, masked_from(s)); key <= min(lim, s.k1 * 128 - 1); ++key) {
     const int id = p.table[(size_t)s.b * p.max_pages + (key >> p.page_shift)];
     if ((unsigned)id >= (unsigned)p.num_pages) continue;
     const __nv_bfloat16* v =
@@ -212,71 +233,69 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t x0 = line.border(blockIdx.x), x1 = line.border(blockIdx.x + 1);
       if (lane == 0) *note_of(p, D, blockIdx.x) = Note{0, 0, 0, 0};
       Cursor<D, true> c;
-      bool more = !line.bad && x0 < x1, told = false;
+      bool more = !line.bad && x0 < x1, told = false, begun = false;
       if (more) c.find(p, line, x0, lane);
       uint32_t made = 0;
-      // the next part of this CTA, or the note that there is none
-      auto publish = [&]() {
-        if (told) return true;
-        int k0 = 0, k1 = 0, nk = 0;
-        while (more) {
-          nk = c.blocks(p);
-          k0 = c.block_at(x0, nk);
-          k1 = c.block_at(x1, nk);
-          if (k0 < k1) break;
-          c.next(p);
-          more = c.b < p.B && c.start < x1;
-        }
-        const int st = made % kSegRing;
-        if (!wait_phase(&seg_empty[st], ((made / kSegRing) & 1) ^ 1, &gave_up)) return false;
-        if (lane == 0) {
-          Segment& s = segs[st];
-          s.valid = more ? 1 : 0;
-          if (more) {
-            const int t0 = c.i * 2 * p.tq;
-            s.b = c.b;
-            s.g = c.g;
-            s.ctx = c.s.ctx;
-            s.n = c.s.n;
-            s.t0 = t0;
-            s.row0 = p.cu[c.b] + t0;
-            s.k0 = k0;
-            s.k1 = k1;
-            s.slot = k0 == 0 && k1 == nk ? -1 : 2 * (int)blockIdx.x + (k0 == 0 ? 1 : 0);
-            if (k0 != 0 && k1 == nk)
-              *note_of(p, D, blockIdx.x) = Note{c.first_worker(line), s.row0, c.g, min(2 * p.tq, c.s.n - t0)};
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              const int first = t0 + w * p.tq, last = min(first + p.tq, c.s.n) - 1;
-              s.end[w] = first < c.s.n ? max(k0, min(k1, (c.s.ctx + last) / 128 + 1)) : k0;
-            }
-          }
-          odd[st] = 0;
-          mbar_arrive(&seg_full[st]);
-        }
-        __syncwarp();
-        ++made;
-        told = !more;
-        if (more) {
-          c.next(p);
-          more = c.b < p.B && c.start < x1;
-        }
-        return true;
-      };
       const uint32_t r0 = smem_addr(ring);
       uint32_t it = 0, blk = 0, raw_phase = 0;
-      bool ok = publish() && publish();
-      for (uint32_t i = 0; ok; ++i) {
-        const int sst = i % kSegRing;
+      bool ok = true;
+      // one part is made known ahead of the one whose values are looked after
+      for (uint32_t i = 0;; ++i) {
+        if (!told) {
+          // the next part of this CTA, or the note that there is none
+          int k0 = 0, k1 = 0, nk = 0;
+          while (more) {
+            if (begun) c.next(p);
+            begun = true;
+            more = c.b < p.B && c.start < x1;
+            if (!more) break;
+            nk = c.blocks(p);
+            k0 = c.block_at(x0, nk);
+            k1 = c.block_at(x1, nk);
+            if (k0 < k1) break;
+          }
+          const int st = made % kSegRing;
+          if (!wait_phase(&seg_empty[st], ((made / kSegRing) & 1) ^ 1, &gave_up)) break;
+          if (lane == 0) {
+            Segment& s = segs[st];
+            s.valid = more ? 1 : 0;
+            if (more) {
+              const int t0 = c.i * 2 * p.tq;
+              s.b = c.b;
+              s.g = c.g;
+              s.ctx = c.s.ctx;
+              s.n = c.s.n;
+              s.t0 = t0;
+              s.row0 = p.cu[c.b] + t0;
+              s.k0 = k0;
+              s.k1 = k1;
+              s.slot = k0 == 0 && k1 == nk ? -1 : 2 * (int)blockIdx.x + (k0 == 0 ? 1 : 0);
+              if (k0 != 0 && k1 == nk)
+                *note_of(p, D, blockIdx.x) = Note{c.first_worker(line), s.row0, c.g, min(2 * p.tq, c.s.n - t0)};
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                const int first = t0 + w * p.tq, last = min(first + p.tq, c.s.n) - 1;
+                s.end[w] = first < c.s.n ? max(k0, min(k1, (c.s.ctx + last) / 128 + 1)) : k0;
+              }
+            }
+            odd[st] = 0;
+            mbar_arrive(&seg_full[st]);
+          }
+          __syncwarp();
+          ++made;
+          told = !more;
+        }
+        if (i < 1) continue;
+        const int sst = (i - 1) % kSegRing;
         if (!segs[sst].valid) break;
-        const int ctx = segs[sst].ctx, n = segs[sst].n, k0 = segs[sst].k0, k1 = segs[sst].k1, jd = first_masked(segs[sst]);
-        for (int k = max(k0, jd); k < k1; ++k) {
+        const int k0 = segs[sst].k0, k1 = segs[sst].k1, from = masked_from(segs[sst]), to = masked_to(segs[sst], p);
+        for (int k = max(k0, from >> 7); k < k1; ++k) {
           const uint32_t vit = it + 2 * (k - k0) + 1;
           const int st = vit % kStages;
           if (!(ok = wait_phase(&v_raw[st], (raw_phase >> st) & 1, &gave_up))) break;
           raw_phase ^= 1u << st;
           const uint32_t v0 = r0 + st * S::kTile;
-          const int valid = min(128, ctx + n - k * 128);
+          const int first = max(0, from - k * 128), valid = min(128, to - k * 128);
           const uint32_t miss = missing[(blk + k - k0) & 7];
           if (valid < 128 || miss) zero_values<D>(v0, valid, miss, p.page_shift, lane);
           // 0 * v summed over the block is zero unless some v is not finite: one packed instruction per pair
@@ -285,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 4; ++q) acc[q] = __float2bfloat162_rn(0.f);
           const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
 #pragma unroll 4
-          for (int e = lane; e < valid * 8; e += 32) {
+          for (int e = first * 8 + lane; e < valid * 8; e += 32) {
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
               const uint4 v = lds128(v0 + h * S::kHalf + e * 16);
@@ -297,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const __nv_bfloat162 sum = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
           const bool any = __hisnan(__low2bfloat16(sum)) || __hisnan(__high2bfloat16(sum));
           if (__any_sync(0xffffffffu, any)) {
-            for (int e = lane; e < valid * 32; e += 32) {
+            for (int e = first * 32 + lane; e < valid * 32; e += 32) {
               for (int h = 0; h < NH; ++h) {
                 const uint32_t a = v0 + h * S::kHalf + e * 4, v = lds32(a), o = odd_bits(v);
                 if (o) sts32(a, v & ~o);
@@ -315,15 +334,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         blk += k1 - k0;
         __syncwarp();
         if (lane == 0) mbar_arrive(&seg_empty[sst]);
-        ok = publish();
       }
     } else if (warp == 8) {
       // ------------------------------------------------ copies
       const int box = min(128, pmask + 1), npg = 128 / box;
-      uint32_t it = 0, nq = 0;  // key and value blocks; query tile pairs
+      uint32_t it = 0, nb = 0, nq = 0;  // places of the ring; blocks; query tile pairs
       uint32_t raw_at = 0, raw_phase = 0, misses = 0, hole = 0;  // stages last filled through v_raw, and its phases; uses of m_bar
       const auto load_q = [&](const Segment& s) {
-#pragma unroll
+#pragma unroll 1
         for (int w = 0; w < 2; ++w) {
           if (!wait_phase(&q_empty[w], (nq & 1) ^ 1, &gave_up)) return false;
           if (lane == 0) {
@@ -345,17 +363,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&seg_empty[sst]);
         if (!s.valid) break;
-        const int L = s.ctx + s.n, jd = first_masked(s);
+        const int L = masked_to(s, p), jd = masked_from(s) >> 7;
         // the query tiles, behind the first keys and values where the last item's products still read theirs
         const bool early = __all_sync(0xffffffffu, mbar_test_wait(&q_empty[0], (nq & 1) ^ 1) &&
                                                        mbar_test_wait(&q_empty[1], (nq & 1) ^ 1));
         bool ok = !early || load_q(s);
+        // lane = page * NH + column half; table entries are read a block ahead
+        const int pg = lane / NH, half = lane % NH;
+        const int32_t* table = p.table + (size_t)s.b * p.max_pages;
+        const auto entry = [&](int key) { return pg < npg && key < L ? table[key >> p.page_shift] : -1; };
+        int next_id = entry(s.k0 * 128 + pg * box);
         for (int k = s.k0; k < s.k1 && ok; ++k) {
-          // lane = page * NH + column half
-          const int pg = lane / NH, half = lane % NH, key = k * 128 + pg * box;
-          int id = -1;
+          const int key = k * 128 + pg * box, id = next_id;
+          next_id = entry(key + 128);
           const bool in = pg < npg && key < L;
-          if (in) id = p.table[(size_t)s.b * p.max_pages + (key >> p.page_shift)];
           const bool good = in && (unsigned)id < (unsigned)p.num_pages;
           if (in && !good) set_status(p.status, MK_DEV_BAD_INDEX);
           const unsigned lanes = __ballot_sync(0xffffffffu, good);
@@ -366,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             miss = m2;
           }
           const int row = ((id * p.Hkv + s.g) << p.page_shift) + (key & pmask);
+#pragma unroll 1
           for (int v = 0; v < 2; ++v, ++it) {
             const int st = it % kStages;
             if (!(ok = wait_phase(&kv_empty[st], ((it / kStages) & 1) ^ 1, &gave_up))) break;
@@ -376,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             raw_at = raw ? raw_at | 1u << st : raw_at & ~(1u << st);
             raw_phase ^= raw ? 1u << st : 0u;
             if (lane == 0) {
-              if (v == 0) missing[(it >> 1) & 7] = miss;
+              if (v == 0) missing[nb & 7] = miss;
               mbar_arrive_expect_tx(bar, __popc(lanes) * box * 128);
             }
             __syncwarp();
@@ -393,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
           }
+          ++nb;
           if (ok && k == s.k0 && !early) ok = load_q(s);
         }
         if (!ok) break;
@@ -553,22 +576,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait_phase(&s_full[w], ns & 1, &gave_up))) break;
         ++ns;
         tc_fence_after();
+        const uint32_t miss = missing[(blk + j) & 7];
+        if (j >= jm || miss) {
+          // scores of keys that the row does not see become -inf where they lie, 32 columns at a time (a loop,
+          // for the sake of the code's size)
+          const int last = lim - (k0 + j) * 128;
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            const int n = last + 1 - c;
+            uint32_t see = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
+            if (miss) see &= ~missing_keys(miss, c, p.page_shift);
+            if (__all_sync(0xffffffffu, see == ~0u)) continue;
+            float y[32];
+            tmem_ld32(ts + c, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((see >> e) & 1)) y[e] = -INFINITY;
+            tmem_st32(ts + c, y);
+          }
+          tmem_wait_st();
+        }
         float x[128];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, x + c * 32);
         tmem_wait_ld();
-        const uint32_t miss = missing[(blk + j) & 7];
-        if (j >= jm || miss) {
-          const int last = lim - (k0 + j) * 128;
-          if (miss) {
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if ((miss >> (c >> p.page_shift)) & 1) x[c] = -INFINITY;
-          }
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c > last) x[c] = -INFINITY;
-        }
         float mx[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) mx[e] = fmaxf(x[e], x[e + 8]);
