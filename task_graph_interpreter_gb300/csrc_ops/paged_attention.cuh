@@ -218,17 +218,17 @@ struct Cursor {
   }
 };
 
-// The workspace: outputs [2 * workers slots][rows][D] (chunks: [D][rows], a row per lane), (m, l)
+// The workspace: outputs [2 * workers slots][rows][D] (chunks: [D / 4][rows][4], a row per lane), (m, l)
 // [2 * workers][rows][2], notes [workers].
 // Slot 2 w is worker w's part of an item that began before it, slot 2 w + 1
 // its part of an item that goes on behind it.
 __device__ __forceinline__ float* part_o(const AttnParams& p, int D, int slot, int row) {
   return p.part + ((size_t)slot * p.rows + row) * D;
 }
-// the same of a chunk: column 0 of the row, columns kTileRows apart
+// the same of a chunk: four columns of the row, the next four kTileRows pieces on
 constexpr int kTileRows = 256;
-__device__ __forceinline__ float* part_col(const AttnParams& p, int D, int slot, int row) {
-  return p.part + (size_t)slot * kTileRows * D + row;
+__device__ __forceinline__ float4* part_cols(const AttnParams& p, int D, int slot, int row, int col) {
+  return reinterpret_cast<float4*>(p.part + (size_t)slot * kTileRows * D) + (col / 4) * kTileRows + row;
 }
 __device__ __forceinline__ float* part_ml(const AttnParams& p, int D, int slot, int row) {
   return p.part + (size_t)2 * p.workers * p.rows * D + ((size_t)slot * p.rows + row) * 2;

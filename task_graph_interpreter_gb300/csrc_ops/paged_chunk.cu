@@ -664,9 +664,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool set_aside = nt > 0 && odd[sst];
       const float f = s.slot >= 0 ? 1.f : nt == 0 || l == 0.f ? 0.f : 1.0f / l;  // a row without keys is zero
       __nv_bfloat16* dst = p.out + ((int64_t)s.row0 + w * p.tq + tok_in) * p.ld_out + (int64_t)(s.g * p.G + head) * D;
-      float* rec = nullptr;
+      float4* rec = nullptr;
       if (s.slot >= 0) {
-        rec = part_col(p, D, s.slot, w * 128 + row);
+        rec = part_cols(p, D, s.slot, w * 128 + row, 0);
         if (mine) *reinterpret_cast<float2*>(part_ml(p, D, s.slot, w * 128 + row)) = make_float2(m, nt > 0 ? l : 0.f);
       }
       // (32-byte stores where a row allows it: lanes hold different rows, and each store takes a cycle per
@@ -702,7 +702,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else if (mine && nt > 0) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) rec[(c + e) * kTileRows] = o[e];
+          for (int e = 0; e < 32; e += 4)
+            rec[(c + e) / 4 * kTileRows] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
       tc_fence_before();  // O is read before the next part's first P is handed over

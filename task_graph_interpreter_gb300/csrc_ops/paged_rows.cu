@@ -528,9 +528,12 @@ __global__ void __launch_bounds__(kTileRows) join_chunk_kernel(const __grid_cons
       if (i0 + j >= count) continue;
       const int slot = record(note, i0 + j);
       ml[j] = __ldcg(reinterpret_cast<const float2*>(part_ml(p, D, slot, row)));
-      const float* src = part_col(p, D, slot, row) + col0 * kTileRows;
+      const float4* src = part_cols(p, D, slot, row, col0);
 #pragma unroll
-      for (int e = 0; e < kJoinCols; ++e) v[j][e] = __ldcg(src + e * kTileRows);
+      for (int e = 0; e < kJoinCols; e += 4) {
+        const float4 x = __ldcg(src + e / 4 * kTileRows);
+        v[j][e] = x.x; v[j][e + 1] = x.y; v[j][e + 2] = x.z; v[j][e + 3] = x.w;
+      }
     }
 #pragma unroll
     for (int j = 0; j < U; ++j) {
