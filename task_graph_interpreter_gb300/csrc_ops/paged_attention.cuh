@@ -42,11 +42,12 @@ constexpr int kRowBlockBytes = 16384;  // keys and values of a few-rows block
 template <int D, bool CHUNK>
 struct Geometry {
   static constexpr int kKeys = CHUNK ? 128 : kRowBlockBytes / D / 4;  // keys per block
-  static constexpr int kFixed = CHUNK ? 320 : 64;           // an item's fixed cost, in keys
+  static constexpr int kFixed = CHUNK ? 320 : 128;          // an item's fixed cost, in keys
 };
 
 struct Seq {
   int n, ctx, nq;      // new tokens, cached tokens, items per head
+  int row0;            // first query row
   int64_t base, step;  // cost of item i: base + i step
   int64_t per_head;
   bool bad;
@@ -57,6 +58,7 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
   Seq s;
   const int c0 = p.cu[b], c1 = p.cu[b + 1];
   s.ctx = p.ctx[b];
+  s.row0 = c0;
   s.n = c1 - c0;
   s.bad = c0 < 0 || c1 < c0 || c1 > p.N || s.n > p.max_new || s.ctx < 0 ||
           (int64_t)s.ctx + s.n > ((int64_t)p.max_pages << p.page_shift);

@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               s.ctx = c.s.ctx;
               s.n = c.s.n;
               s.t0 = t0;
-              s.row0 = p.cu[c.b] + t0;
+              s.row0 = c.s.row0 + t0;
               s.k0 = k0;
               s.k1 = k1;
               s.slot = k0 == 0 && k1 == nk ? -1 : 2 * (int)blockIdx.x + (k0 == 0 ? 1 : 0);

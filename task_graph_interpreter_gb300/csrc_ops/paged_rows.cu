@@ -17,7 +17,10 @@
 // 64 requests of 512 to 8192 keys and four rows 199 us there, 178 us here),
 // so this one has a single eight.  Four warps with three blocks of 16 KB each:
 // 183 us for those 64 requests; six with two 187, twelve with two of 8 KB 189,
-// eight with three of 8 KB 193.
+// eight with three of 8 KB 193.  Since then 173 (5.9 TB/s at a copy's 6.8),
+// with the next item's query rows read ahead and an item's fixed cost in the
+// division at 128 keys (256 requests of 500 keys: 71 us with 64, 67 with 128, 73
+// with 256; with the rows read ahead 65).
 //
 //   s = q k^T scale;  m' = max(m, max s);  p = 2^(s - m');
 //   l = l 2^(m - m') + sum p;  o = o 2^(m - m') + p v
@@ -152,8 +155,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
 
   int ck = 0, cke = 0;
   part_of(cons, ck, cke);
-  bool more = ck < cke || next_part(cons, ck, cke);
-  if (!more) return;
+  if (ck >= cke && !next_part(cons, ck, cke)) return;
   prod = cons;
   pk = ck;
   pke = cke;
@@ -161,21 +163,38 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
 
   // this lane's place in the 16 x 8 results: keys (columns of the values) g and g + 8, query rows c0, c0 + 1
   const int g = lane >> 2, c0 = (lane & 3) * 2;
-  while (more) {
+  // this lane's pieces of an item's query rows (row r = token * G + head; rows past the last are zero), read while
+  // the item before is worked on
+  constexpr int QP = kMaxFewRows * (D / 8) / 32;
+  uint4 qv[QP];
+  auto load_q = [&](const Cursor<D, false>& c) {
+    const __nv_bfloat16* qb = p.q + (int64_t)c.s.row0 * p.ld_q + (int64_t)c.g * p.G * D;
+    const int nrows = c.s.n * p.G;
+#pragma unroll
+    for (int j = 0; j < QP; ++j) {
+      const int r = (lane + j * 32) / (D / 8), col = (lane + j * 32) % (D / 8) * 8;
+      qv[j] = make_uint4(0, 0, 0, 0);
+      if (r < nrows) qv[j] = __ldg(reinterpret_cast<const uint4*>(qb + (int64_t)(r / p.G) * p.ld_q + (r % p.G) * D + col));
+    }
+  };
+  load_q(cons);
+  for (bool more = true; more;) {
     const int n = cons.s.n, ctx = cons.s.ctx, L = ctx + n, nrows = n * p.G;
     const int nk = cons.blocks(p), kb = ck;
-    // query rows, row r = token * G + head, into shared memory; rows past the last are zero
-    const __nv_bfloat16* qb = p.q + (int64_t)p.cu[cons.b] * p.ld_q + (int64_t)cons.g * p.G * D;
     __syncwarp();
-    for (int i = lane; i < kMaxFewRows * (D / 8); i += 32) {
-      const int r = i / (D / 8), c = i % (D / 8);
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < nrows) v = __ldg(reinterpret_cast<const uint4*>(qb + (int64_t)(r / p.G) * p.ld_q + (r % p.G) * D + c * 8));
+#pragma unroll
+    for (int j = 0; j < QP; ++j) {
+      const int r = (lane + j * 32) / (D / 8), c = (lane + j * 32) % (D / 8);
       const uint32_t a = swz(qs + (c >> 3) * (kMaxFewRows * 128), r, c & 7);
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(qv[j].x), "r"(qv[j].y), "r"(qv[j].z),
+                   "r"(qv[j].w)
                    : "memory");
     }
     __syncwarp();
+    Cursor<D, false> coming = cons;
+    int nk0 = 0, nk1 = 0;
+    more = next_part(coming, nk0, nk1);
+    if (more) load_q(coming);
     // the last key each of this lane's two rows sees
     int lim[2];
 #pragma unroll
@@ -342,8 +361,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     }
     const bool whole = kb == 0 && cke == nk;
     const int slot = 2 * w + (kb == 0 ? 1 : 0);
-    if (kb != 0 && cke == nk) note = {cons.first_worker(line), p.cu[cons.b], cons.g, n};
-    __nv_bfloat16* ob = p.out + (int64_t)p.cu[cons.b] * p.ld_out + (int64_t)cons.g * p.G * D;
+    if (kb != 0 && cke == nk) note = {cons.first_worker(line), cons.s.row0, cons.g, n};
+    __nv_bfloat16* ob = p.out + (int64_t)cons.s.row0 * p.ld_out + (int64_t)cons.g * p.G * D;
     if (whole) {
       const float f0 = l[0] == 0.f ? 0.f : 1.0f / l[0], f1 = l[1] == 0.f ? 0.f : 1.0f / l[1];
       // neighbouring columns sit in lanes g and g ^ 1: even g stores row c0, odd g row c0 + 1
@@ -372,7 +391,9 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
         if (g == 0) *reinterpret_cast<float2*>(part_ml(p, D, slot, r)) = make_float2(m[e], l[e]);
       }
     }
-    more = next_part(cons, ck, cke);
+    cons = coming;
+    ck = nk0;
+    cke = nk1;
   }
   if (lane == 0 && note.tokens) *note_of(p, D, w) = note;
 }
