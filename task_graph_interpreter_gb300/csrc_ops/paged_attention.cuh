@@ -42,7 +42,7 @@ constexpr int kRowBlockBytes = 16384;  // keys and values of a few-rows block
 template <int D, bool CHUNK>
 struct Geometry {
   static constexpr int kKeys = CHUNK ? 128 : kRowBlockBytes / D / 4;  // keys per block
-  static constexpr int kFixed = CHUNK ? 320 : 128;          // an item's fixed cost, in keys
+  static constexpr int kFixed = CHUNK ? 320 : 96;           // an item's fixed cost, in keys
 };
 
 struct Seq {
