@@ -520,7 +520,7 @@ int mk_qk_norm_rope(void* stream, int N, int Hq, int Hkv, int D, const void* qkv
  *  h reads key/value head h / (Hq / Hkv).  cu int32 [B + 1] (cu[B] <= N).
  *  Softmax scale `scale` (1/sqrt(D) as a rule).
  *  max_new: no request has more new tokens than this; with max_new * Hq / Hkv
- *  at most 32 the kernel for tokens and drafts runs, else the one for chunks.
+ *  at most 8 the kernel for single tokens runs, else the one for chunks.
  *  workspace: mk_paged_attention_workspace bytes for the same max_new, heads
  *  and D, for partial results; calls that share it must not overlap.
  * Rows of no request (before cu[0], behind cu[B]) stay as they are.  Keys of

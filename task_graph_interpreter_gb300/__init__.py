@@ -7,8 +7,5 @@ Python binding (``_lib``, same names as the C ABI), a graph builder
 """
 from . import _lib  # noqa: F401
 from ._lib import MkError  # noqa: F401
-
-
-def build(force: bool = False, verbose: bool = False) -> str:
-    from .build import build as _build
-    return _build(force=force, verbose=verbose)
+# (the function, not the module of its name: a function here that imported the module would be replaced by it)
+from .build import build  # noqa: F401

@@ -9,6 +9,7 @@
 // and the ctypes binding use the one library that the binding loaded.
 #include <Python.h>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -70,6 +71,11 @@ int device_of(const at::Tensor& t, const char* name) {
   if (!t.is_cuda()) refuse(std::string(name) + " must be a CUDA tensor");
   return (int)t.get_device();
 }
+// The operators have no backward pass: a gradient that would silently be missing is refused.
+void no_gradient(const at::Tensor& t, const char* name) {
+  if (t.requires_grad() && at::GradMode::is_enabled())
+    refuse(std::string(name) + " requires a gradient, and this operator has none (call it under torch.no_grad())");
+}
 bool on(const at::Tensor& t, int dev) { return t.is_cuda() && t.get_device() == dev; }
 
 int32_t* int32s(const at::Tensor& t, const char* name, int64_t n, int dev) {
@@ -98,6 +104,8 @@ Pools pools(const at::Tensor& k, const at::Tensor& v, int dev) {
   if (k.dim() != 4 || k.sizes() != v.sizes() || k.scalar_type() != at::kBFloat16 || v.scalar_type() != at::kBFloat16 ||
       !k.is_contiguous() || !v.is_contiguous() || !on(k, dev) || !on(v, dev))
     refuse("kpool and vpool must be contiguous bf16 [num_pages, Hkv, page_size, D] on cuda:" + std::to_string(dev));
+  no_gradient(k, "kpool");
+  no_gradient(v, "vpool");
   return {k.data_ptr(), v.data_ptr(), small_size(k.size(0), "num_pages"), small_size(k.size(1), "Hkv"),
           small_size(k.size(2), "page_size"), small_size(k.size(3), "D")};
 }
@@ -107,6 +115,7 @@ int64_t row_stride(const at::Tensor& t, const char* name, int64_t N, int64_t Hq,
       t.size(2) != D)
     refuse(std::string(name) + " must be bf16 [" + std::to_string(N) + ", " + std::to_string(Hq) + ", " +
            std::to_string(D) + "] on cuda:" + std::to_string(dev));
+  no_gradient(t, name);
   if (t.is_contiguous() || N == 0) return Hq * D;
   if ((D > 1 && t.stride(2) != 1) || (Hq > 1 && t.stride(1) != D))
     refuse(std::string("each row of ") + name + " must be contiguous");
@@ -117,6 +126,7 @@ void* gain(PyObject* o, const char* name, int64_t D, int dev) {
   if (!t) return nullptr;
   if (t->scalar_type() != at::kBFloat16 || t->numel() != D || !t->is_contiguous() || !on(*t, dev))
     refuse(std::string(name) + " must be bf16 [" + std::to_string(D) + "] on cuda:" + std::to_string(dev));
+  no_gradient(*t, name);
   return t->data_ptr();
 }
 // elements between the rows of f32 [B, rows, V]
@@ -125,6 +135,7 @@ int64_t probability_stride(const at::Tensor& t, const char* name, int64_t B, int
       t.size(2) != V)
     refuse(std::string(name) + " must be f32 [" + std::to_string(B) + ", " + std::to_string(rows) + ", " +
            std::to_string(V) + "] on cuda:" + std::to_string(dev));
+  no_gradient(t, name);
   if (t.is_contiguous()) return V;
   if ((V > 1 && t.stride(2) != 1) || (B > 1 && rows > 1 && t.stride(0) != rows * t.stride(1)))
     refuse(std::string(name) + " must have evenly spaced contiguous rows");
@@ -226,6 +237,7 @@ PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if ((!f32 && x.scalar_type() != at::kBFloat16) || x.dim() != 2 || x.size(1) != width ||
         (width > 1 && x.stride(1) != 1))
       refuse("qkv must be f32 or bf16 [N, " + std::to_string(width) + "] with contiguous rows");
+    no_gradient(x, "qkv");
     const int N = small_size(x.size(0), "N");
     const Pools pl = pools(tensor(a[6], "kpool"), tensor(a[7], "vpool"), dev);
     if (pl.Hkv != Hkv || pl.D != D)

@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int next_id = entry(s.k0 * 128 + pg * box);
         for (int k = s.k0; k < s.k1 && ok; ++k) {
           const int key = k * 128 + pg * box, id = next_id;
-          next_id = entry(key + 128);
+          next_id = k + 1 < s.k1 ? entry(key + 128) : -1;  // (no key past the last block: it could pass 2^31)
           const bool in = pg < npg && key < L;
           const bool good = in && (unsigned)id < (unsigned)p.num_pages;
           if (in && !good) set_status(p.status, MK_DEV_BAD_INDEX);

@@ -8,8 +8,9 @@ nothing synchronises.  Tensors that do not fit raise ValueError, what the
 library refuses MkError (the checks are in csrc_ops/calls.cpp).  Lengths,
 tables and maps are int32 tensors that the GPU reads; what is wrong with
 their values is reported in ``status`` (an int32 device tensor, zeroed by the
-caller, that receives the first MK_DEV_* code).  ``PagedCache`` holds a
-cache's pools, tables and free pages and runs the operators on them.
+caller, that receives the first MK_DEV_* code).  They serve inference: a tensor
+that requires a gradient is refused outside ``torch.no_grad()``.  ``PagedCache``
+holds a cache's pools, tables and free pages and runs the operators on them.
 """
 from __future__ import annotations
 
@@ -18,6 +19,7 @@ from typing import NamedTuple
 import torch
 
 from . import _lib as L
+
 
 def on_stream(fn, stream, args):
     """Call ``fn`` with ``stream`` current; the tensors have to be on its device."""
