@@ -547,7 +547,8 @@ int mk_paged_attention_workspace(int max_new, int Hq, int Hkv, int D, size_t* by
  *  accepted ones is drawn with u[K] from max(p_t - q_t, 0) after a rejection
  *  (from p_t if that is zero everywhere), from p after the last draft: the
  *  smallest index whose running sum exceeds u[K] times the sum.  Negative and
- *  NaN weights count as zero; if all are, the token is -1.
+ *  NaN weights count as zero; if all are, or their sum is not finite, the token
+ *  is -1.
  *  tokens int32 [B, K + 1]: the accepted drafts, the drawn token, then -1.
  *  accepted int32 [B]: the number of accepted drafts.
  * A draft outside [0, V) ends the drafts there and gives MK_DEV_BAD_INDEX.

@@ -638,3 +638,45 @@ def test_empty_calls():
     for most in (1, 50):  # no request has a new token
         paged.attention(out.clone(), k, k, i32([[0], [1]]), i32([0, 0, 0]), i32([5, 0]), most, out=out)
     assert torch.all(out == 2.0)
+
+
+@pytest.mark.parametrize("bad", [math.nan, -math.inf])
+@pytest.mark.parametrize("key", [70, 71, 127, 128, 133, 134, 197, 198, 255, 256, 369])
+def test_a_bad_value_reaches_the_rows_that_see_it_and_no_other(key, bad):
+    """300 tokens behind 70 keys, four rows to a token: items of 64 tokens, whose first and last keys fall on and
+    beside block borders."""
+    ctx, new, Hq, Hkv, D, page = [70], [300], 8, 2, 128, 16
+    q, k, v, table, cu = attention_case(ctx, new, Hq, Hkv, D, page, 41)
+    want, size, reach = attention_ref(q, k, v, table, cu, ctx, page, D ** -0.5)
+    v[int(table[0, key // page]), 1, key % page, 5] = bad
+    got = paged.attention(q, k, v, table, i32(cu), i32(ctx), 300)
+    first = key - ctx[0]  # the first token that sees the key
+    seen = got[first:, 4:, 5].float()
+    assert bool((torch.isnan(seen) if math.isnan(bad) else seen == bad).all())
+    got[first:, 4:, 5] = want[first:, 4:, 5].bfloat16()
+    attention_close(got, want, size, reach, D, False)
+
+
+@pytest.mark.parametrize("G", [1, 3, 4, 7, 8, 16, 48, 128])
+def test_attention_with_items_cut_at_every_place(G):
+    """Requests of lengths on both sides of the tiles' and blocks' sizes, as many that workers' borders fall anywhere."""
+    ctx, new = [0, 1, 127, 128, 255, 900, 0, 383], [9, 130, 128, 1, 33, 2, 257, 64]
+    q, k, v, table, cu = attention_case(ctx, new, 2 * G, 2, 64, 32, G)
+    got = paged.attention(q, k, v, table, i32(cu), i32(ctx), max(new))
+    attention_close(got, *attention_ref(q, k, v, table, cu, ctx, 32, 64 ** -0.5), 64, False)
+
+
+def test_a_tensor_that_requires_a_gradient_is_refused():
+    q, k, v, table, cu = attention_case([30], [2], 8, 2, 64, 16, 31)
+    args = (k, v, table, i32(cu), i32([30]), 2)
+    q.requires_grad_()
+    with pytest.raises(ValueError, match="gradient"):
+        paged.attention(q, *args)
+    with torch.no_grad():
+        paged.attention(q, *args)
+    x, pos = torch.zeros(2, 12 * 64, device=DEV), i32([0, 1])
+    gain = torch.ones(64, dtype=torch.bfloat16, device=DEV, requires_grad=True)
+    with pytest.raises(ValueError, match="gradient"):
+        paged.qk_norm_rope(x, 8, 2, 64, pos, pos, k, v, q_gamma=gain)
+    with pytest.raises(ValueError, match="gradient"):
+        paged.qk_norm_rope(x.requires_grad_(), 8, 2, 64, pos, pos, k, v)

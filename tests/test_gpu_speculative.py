@@ -159,3 +159,13 @@ def test_verify_captured_and_on_another_stream():
     graph.replay()
     want = speculative.verify_drafts(p, drafts, u, q=q)
     assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+def test_verify_without_a_finite_sum_draws_nothing_and_refuses_gradients():
+    p = torch.full((2, 1, 5000), 1.0 / 5000, device=DEV)
+    p[1, 0, 4000] = float("inf")
+    none = torch.zeros(2, 0, dtype=torch.int32, device=DEV)
+    tokens, accepted = speculative.verify_drafts(p, none, torch.full((2, 1), 0.5, device=DEV))
+    assert accepted.tolist() == [0, 0] and 0 <= int(tokens[0, 0]) < 5000 and int(tokens[1, 0]) == -1
+    with pytest.raises(ValueError, match="gradient"):
+        speculative.verify_drafts(p.requires_grad_(), none, torch.full((2, 1), 0.5, device=DEV))
