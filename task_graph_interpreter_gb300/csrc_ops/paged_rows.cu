@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   prod = cons;
   pk = ck;
   pke = cke;
+#pragma unroll 1
   for (int i = 0; i < kStages; ++i) issue();
 
   // this lane's place in the 16 x 8 results: keys (columns of the values) g and g + 8, query rows c0, c0 + 1
@@ -332,6 +333,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       if (masked && n > 1 && __any_sync(0xffffffffu, bad_v)) {
         // 0 * inf would reach the rows that do not see the key: such values were left
         // out above and go to the rows that see it only
+#pragma unroll 1
         for (int k = 0; k < KU; ++k) {
           if (!((keys >> k) & 1)) continue;
 #pragma unroll

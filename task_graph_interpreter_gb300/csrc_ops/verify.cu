@@ -129,13 +129,14 @@ __device__ __forceinline__ double segment_sum(const Weights& w, int i0, int i1, 
 #pragma unroll
       for (int k = 0; k < U; ++k) add4(i + k * 128, a[k], b[k]);
     }
+#pragma unroll 1
     for (; i + 4 <= i1; i += 128)
       add4(i, __ldg(reinterpret_cast<const float4*>(w.p + i)),
            Q ? __ldg(reinterpret_cast<const float4*>(w.q + i)) : none);
     for (int k = i; k < i1 && k < i + 4; ++k)  // the row's last, partial group
       if (Q || k != w.hole) acc.add(w.pair(w.p[k], Q ? w.q[k] : 0.f));
   } else {
-#pragma unroll 8
+#pragma unroll 4
     for (int i = i0 + lane; i < i1; i += 32) {
       const float a = __ldg(w.p + i), b = Q ? __ldg(w.q + i) : 0.f;
       if (Q || i != w.hole) acc.add(w.pair(a, b));
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
   if (warp == 0) {
     const int len = v.draft_len ? min(max(v.draft_len[b], 0), v.K) : v.K;
     int at = len, mode = 0;  // mode 1: rejected, the draft's row is taken off
+#pragma unroll 1
     for (int t0 = 0; t0 < v.K; t0 += 32) {
       const int t = t0 + lane;
       bool valid = false, yes = false;
@@ -207,6 +209,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
       // the segment of the draw: lanes hold consecutive segments, summed in order
       const int per = (segs + 31) / 32;
       double own = 0.0;
+#pragma unroll 1
       for (int k = 0; k < per; ++k)
         if (lane * per + k < segs) own += seg_sum[pass][lane * per + k];
       const double end = lane_scan(own, lane), total = __shfl_sync(0xffffffffu, end, 31);
@@ -217,7 +220,8 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
       if (total > 0.0) {
         const int src = pick_lane(own, end, target);
         double run = end - own;
-        for (int k = 0; k < per; ++k) {
+  #pragma unroll 1
+      for (int k = 0; k < per; ++k) {
           const int g = lane * per + k;
           const double x = g < segs ? seg_sum[pass][g] : 0.0;
           if (x > 0.0) {
@@ -244,6 +248,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
   const int seg = seg_s;
   if (seg < 0) {
     if (rank == 0 && warp == 0) {
+#pragma unroll 1
       for (int t = lane; t <= v.K; t += 32) v.tokens[(int64_t)b * (v.K + 1) + t] = t < at ? tok[t] : -1;
       if (lane == 0) v.accepted[b] = at;
     }
@@ -278,6 +283,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
   int pick = -1;
   if (lane == src) {
     double run = end - own;
+#pragma unroll 1
     for (int i = l0; i < l1; ++i) {
       const double x = w.at(i);
       run += x;
@@ -288,6 +294,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     }
   }
   pick = __shfl_sync(0xffffffffu, pick, src);
+#pragma unroll 1
   for (int t = lane; t <= v.K; t += 32)
     v.tokens[(int64_t)b * (v.K + 1) + t] = t < at ? tok[t] : t == at ? pick : -1;
   if (lane == 0) v.accepted[b] = at;
