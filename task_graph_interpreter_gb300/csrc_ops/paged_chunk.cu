@@ -57,7 +57,7 @@
 // bf16 does not depend on their scale), so O is rarely rescaled; the softmax
 // warps do it themselves, before they hand over P.
 //
-// Probabilities are rounded to bf16 (2^-9 each, in the mean far less in the
+// Probabilities are rounded to bf16 (2^-8 each, in the mean far less in the
 // sum), the form the tensor cores multiply with bf16 values; maxima, sums
 // and O are f32.
 #include "paged_attention.cuh"
@@ -96,7 +96,7 @@ static_assert(Smem<128>::kBytes <= 232448, "227 KB of shared memory per CTA");
 
 struct Control {
   uint64_t kv_full[kStages], kv_empty[kStages], v_raw[kStages], q_full[2], q_empty[2], s_full[2], p_full[2][2],
-      o_done[2], turn[2], seg_full[kSegRing], seg_empty[kSegRing], drained[2], m_bar;
+      o_done[2], s_free[2], turn[2], seg_full[kSegRing], seg_empty[kSegRing], drained[2], m_bar;
   Segment segs[kSegRing];
   int odd[kSegRing];      // a value set aside in this part
   uint32_t missing[8];    // per key block (ring): pages of it that are not in the pool, one bit each
@@ -163,13 +163,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using S = Smem<D>;
   constexpr int NH = D / 64;
-  constexpr uint32_t kSCol = 0, kOCol = 256;  // tensor memory columns of S_0, S_1 and O_0, O_1
+  // tensor memory columns of S_0, S_1, of O_0, O_1, and of P_0, P_1: over the scores at D = 128, apart at D = 64
+  constexpr bool kApart = D == 64;
+  constexpr uint32_t kSCol = 0, kOCol = 256, kPCol = kApart ? 384 : 0, kPStep = kApart ? 64 : 128;
   // no static shared memory: the dynamic part starts 1024-byte aligned, as the swizzled tiles need
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Control& ctl = *reinterpret_cast<Control*>(smem_raw);
   auto &kv_full = ctl.kv_full, &kv_empty = ctl.kv_empty, &v_raw = ctl.v_raw;
   auto &q_full = ctl.q_full, &q_empty = ctl.q_empty, &s_full = ctl.s_full, &o_done = ctl.o_done,
-       &turn = ctl.turn, &drained = ctl.drained;
+       &turn = ctl.turn, &drained = ctl.drained, &s_free = ctl.s_free;
   auto &seg_full = ctl.seg_full, &seg_empty = ctl.seg_empty;
   auto& p_full = ctl.p_full;  // [tile][half of the scores handed over]
   auto& m_bar = ctl.m_bar;
@@ -201,6 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&p_full[i][0], 4);
       mbar_init(&p_full[i][1], 4);
       mbar_init(&turn[i], 1);
+      mbar_init(&s_free[i], 4);
       mbar_init(&o_done[i], 1);
     }
     for (int i = 0; i < kSegRing; ++i) {
@@ -454,16 +457,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t qd = smem_desc_sw128(smem_addr(qt) + w * S::kTile, 1024u), kd = smem_desc_sw128(r0, 1024u),
                      vd = smem_desc_sw128_mn(r0, S::kHalf, 1024u);
       const uint32_t khi = (uint32_t)(kd >> 32), vhi = (uint32_t)(vd >> 32);
-      const uint32_t ts = tmem + kSCol + w * 128, to = tmem + kOCol + w * D;
+      const uint32_t ts = tmem + kSCol + w * 128, to = tmem + kOCol + w * D, tp = tmem + kPCol + w * kPStep;
       const uint32_t a_lo = (uint32_t)qd;
-      uint32_t st = 0, ph = 0, np = 0, nturn = 0;  // ring place; P handed over; turns taken
+      uint32_t it = 0, np = 0, nturn = 0;  // places of the ring; P handed over; turns taken (scores made, at D = 64)
       bool ok = true;
-      auto advance = [&]() {
-        if (++st == kStages) {
-          st = 0;
-          ph ^= 1;
-        }
-      };
       for (uint32_t i = 0; ok; ++i) {
         const int sst = i % kSegRing;
         if (!(ok = wait(&seg_full[sst], (i / kSegRing) & 1))) break;
@@ -475,72 +472,111 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!valid) break;
         if (!(ok = wait(&q_full[w], i & 1))) break;
         if (ntw == 0 && lane == 0) mbar_arrive(&q_empty[w]);
-        // blocks in the order of the ring: K 0, V 0, K 1, V 1, ...; P V (block j) before S (block j + 1).  A
-        // block that this tile does not need is handed back as it comes
-        for (int j = -1; j < nt; ++j) {
-          const uint32_t vst = st;
-          if (j >= 0) {
-            if (!(ok = wait(&kv_full[st], ph))) break;
-            advance();
-          }
-          const uint32_t kst = st;
-          if (j + 1 < nt) {
-            if (!(ok = wait(&kv_full[st], ph))) break;
-            advance();
-          }
-          const bool pv = j >= 0 && j < ntw, qk = j + 1 < ntw;
-          if (pv && !(ok = wait(&p_full[w][0], np & 1))) break;
-          // tile 0 starts; then each block's products of one tile, then of the other
-          if (!(ok = wait(&turn[w], (nturn & 1) ^ (w ^ 1)))) break;
-          ++nturn;
-          tc_fence_after();
-          if (pv) {
-            const uint32_t b_lo = (uint32_t)vd + vst * (S::kTile >> 4);
+        // P V of block j out of ring place vst; as soon as half of P is there
+        const auto values = [&](int j, uint32_t vst) {
+          const uint32_t b_lo = (uint32_t)vd + vst * (S::kTile >> 4);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              if (c == 1) {
-                if (!(ok = wait(&p_full[w][1], np & 1))) break;
-                tc_fence_after();
+          for (int c = 0; c < 2; ++c) {
+            if (c == 1) {
+              if (!wait(&p_full[w][1], np & 1)) return false;
+              tc_fence_after();
+            }
+            if (elect_one()) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int kk = c * 4 + e;  // 16 keys
+                tc_mma_bf16_ts_lo(to, tp + kk * 8, b_lo + kk * 128, vhi, idesc_o, kk != 0 ? 1u : j != 0 ? 1u : 0u);
               }
-              if (elect_one()) {
+              if (c == 1) {
+                tc_commit(&kv_empty[vst]);
+                if (kApart || j + 1 == ntw) tc_commit(&o_done[w]);
+              }
+            }
+            __syncwarp();
+          }
+          ++np;
+          return true;
+        };
+        // S of block j out of ring place kst
+        const auto scores = [&](int j, uint32_t kst) {
+          const uint32_t b_lo = (uint32_t)kd + kst * (S::kTile >> 4);
+          if (elect_one()) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int kk = c * 4 + e;  // 16 keys
-                  tc_mma_bf16_ts_lo(to, ts + kk * 8, b_lo + kk * 128, vhi, idesc_o, kk != 0 ? 1u : j != 0 ? 1u : 0u);
-                }
-                if (c == 1) {
-                  tc_commit(&kv_empty[vst]);
-                  if (!qk) tc_commit(&o_done[w]);
-                }
+            for (int kk = 0; kk < D / 16; ++kk) {
+              tc_mma_bf16_lo(ts, a_lo + (kk >> 2) * (S::kHalf >> 4) + (kk & 3) * 2, khi,
+                             b_lo + (kk >> 2) * (S::kHalf >> 4) + (kk & 3) * 2, khi, idesc_s, kk != 0 ? 1u : 0u);
+              // the other tile's warp takes a while to see its turn
+              if (!kApart && kk == D / 32 - 1) mbar_arrive(&turn[w ^ 1]);
+            }
+            tc_commit(&s_full[w]);
+            tc_commit(&kv_empty[kst]);
+            if (j + 1 == ntw) tc_commit(&q_empty[w]);
+          }
+          __syncwarp();
+        };
+        if constexpr (kApart) {
+          // S (block j + 1) as soon as the softmax has S (block j) in registers, P V (block j) as P comes
+          for (int j = -1; j < nt; ++j) {
+            if (j + 1 < nt) {
+              const uint32_t at = it + 2 * (j + 1), kst = at % kStages;
+              if (!(ok = wait(&kv_full[kst], (at / kStages) & 1))) break;
+              if (j + 1 < ntw) {
+                if (!(ok = wait(&s_free[w], (nturn & 1) ^ 1))) break;
+                ++nturn;
+                tc_fence_after();
+                scores(j + 1, kst);
+              } else if (lane == 0) {
+                mbar_arrive(&kv_empty[kst]);
+              }
+            }
+            if (j >= 0) {
+              const uint32_t at = it + 2 * j + 1, vst = at % kStages;
+              if (!(ok = wait(&kv_full[vst], (at / kStages) & 1))) break;
+              if (j < ntw) {
+                if (!(ok = wait(&p_full[w][0], np & 1))) break;
+                tc_fence_after();
+                if (!(ok = values(j, vst))) break;
+              } else if (lane == 0) {
+                mbar_arrive(&kv_empty[vst]);
+              }
+            }
+            __syncwarp();
+          }
+          it += 2 * nt;
+        } else {
+          // blocks in the order of the ring: K 0, V 0, K 1, V 1, ...; P V (block j) before S (block j + 1).  A
+          // block that this tile does not need is handed back as it comes
+          for (int j = -1; j < nt; ++j) {
+            const uint32_t vst = it % kStages;
+            if (j >= 0) {
+              if (!(ok = wait(&kv_full[vst], (it / kStages) & 1))) break;
+              ++it;
+            }
+            const uint32_t kst = it % kStages;
+            if (j + 1 < nt) {
+              if (!(ok = wait(&kv_full[kst], (it / kStages) & 1))) break;
+              ++it;
+            }
+            const bool pv = j >= 0 && j < ntw, qk = j + 1 < ntw;
+            if (pv && !(ok = wait(&p_full[w][0], np & 1))) break;
+            // tile 0 starts; then each block's products of one tile, then of the other
+            if (!(ok = wait(&turn[w], (nturn & 1) ^ (w ^ 1)))) break;
+            ++nturn;
+            tc_fence_after();
+            if (pv) {
+              if (!(ok = values(j, vst))) break;
+            } else if (j >= 0 && lane == 0) {
+              mbar_arrive(&kv_empty[vst]);
+            }
+            if (qk) {
+              scores(j + 1, kst);
+            } else {
+              if (lane == 0) {
+                mbar_arrive(&turn[w ^ 1]);
+                if (j + 1 < nt) mbar_arrive(&kv_empty[kst]);
               }
               __syncwarp();
             }
-            if (!ok) break;
-            ++np;
-          } else if (j >= 0 && lane == 0) {
-            mbar_arrive(&kv_empty[vst]);
-          }
-          if (qk) {
-            const uint32_t b_lo = (uint32_t)kd + kst * (S::kTile >> 4);
-            if (elect_one()) {
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                tc_mma_bf16_lo(ts, a_lo + (kk >> 2) * (S::kHalf >> 4) + (kk & 3) * 2, khi,
-                               b_lo + (kk >> 2) * (S::kHalf >> 4) + (kk & 3) * 2, khi, idesc_s, kk != 0 ? 1u : 0u);
-                // the other tile's warp takes a while to see its turn
-                if (kk == D / 32 - 1) mbar_arrive(&turn[w ^ 1]);
-              }
-              tc_commit(&s_full[w]);
-              tc_commit(&kv_empty[kst]);
-              if (j + 2 == ntw) tc_commit(&q_empty[w]);
-            }
-            __syncwarp();
-          } else {
-            if (lane == 0) {
-              mbar_arrive(&turn[w ^ 1]);
-              if (j + 1 < nt) mbar_arrive(&kv_empty[kst]);
-            }
-            __syncwarp();
           }
         }
       }
@@ -557,7 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     reg_inc();
     const int w = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's tensor-memory lanes (lane field, bits 16 up)
-    const uint32_t ts = tmem + lanes + kSCol + w * 128, to = tmem + lanes + kOCol + w * D;
+    const uint32_t ts = tmem + lanes + kSCol + w * 128, to = tmem + lanes + kOCol + w * D,
+                   tp = tmem + lanes + kPCol + w * kPStep;
     const int tok_in = row / p.G, head = row % p.G;
     uint32_t ns = 0, no = 0, blk = 0;
     for (uint32_t i = 0;; ++i) {
@@ -601,6 +638,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, x + c * 32);
         tmem_wait_ld();
+        if constexpr (kApart) {  // the next scores may come
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[w]);
+        }
         float mx[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) mx[e] = fmaxf(x[e], x[e + 8]);
@@ -613,9 +655,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j == 0) {
           m = top;
         } else {
+          if constexpr (kApart) {  // the last block's product has read P, and O is whole
+            if (!(ok = wait_phase(&o_done[w], no & 1, &gave_up))) break;
+            ++no;
+            tc_fence_after();
+          }
           const bool far = top > m + 8.f;
           if (__any_sync(0xffffffffu, far)) {
-            // every product into O is complete: the barrier of this block's S covers them
+            // (at D = 128 the barrier of this block's S covers every product into O)
             const float f = far ? ex2(m - top) : 1.f;
             if (far) m = top;
             l *= f;
@@ -643,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum[e & 3] = add2(sum[e & 3], pair_f32(a, b));
             r[e] = pack_bf16(a, b);
           }
-          tmem_st16(ts + c * 16, r);
+          tmem_st16(tp + c * 16, r);
           if (c & 1) {  // half of the keys: the product starts on them
             tmem_wait_st();
             tc_fence_before();

@@ -26,7 +26,7 @@
 //   l = l 2^(m - m') + sum p;  o = o 2^(m - m') + p v
 //
 // The probabilities enter the second product as two bf16 parts (p and what
-// its rounding leaves), which keeps them to 2^-17; the extra products cost
+// its rounding leaves), which keeps them to 2^-16; the extra products cost
 // nothing here.
 #include "paged_attention.cuh"
 
