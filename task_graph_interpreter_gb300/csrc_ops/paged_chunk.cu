@@ -38,8 +38,11 @@
 //  - two threads per row, which halves a thread's powers, exchange maxima and
 //    hold fewer registers: 2900 cycles.
 // At D = 64 P V is half the arithmetic in the same time (64-column products
-// run at half rate): 786 cycles of products per tile, 2200 per block of both
-// tiles, which the softmax sets.
+// run at half rate): 786 cycles of products per tile.  Tensor memory has room
+// for P beside S there, so the next scores are made while a softmax runs and
+// no turns are needed; a block of both tiles takes 2150 cycles (2200 with P
+// over S), which the two softmaxes set: 1370 of powers, 650 of loads and
+// maxima, waits.  Making their powers take turns changed nothing.
 //
 // Short parts are bound by what surrounds their blocks: the first scores'
 // wait, the last product and the store of the results, the values behind
