@@ -4,7 +4,12 @@ mk_paged_plan, mk_qk_norm_rope and mk_paged_attention of include/mk.h).
 
 The functions take PyTorch tensors on one CUDA device (not necessarily the
 current one) and enqueue on that device's current stream, or on ``stream``;
-nothing synchronises.  Tensors that do not fit raise ValueError, what the
+nothing synchronises.  With ``stream`` they behave as under
+``torch.cuda.stream(stream)``: the caller orders that stream behind whatever
+made the inputs, and other streams behind it before they use the results; fresh
+results are its memory.  Tensors that the caller passes may be dropped as soon
+as the call returns: their memory is not given out again before ``stream`` is
+through with them.  Tensors that do not fit raise ValueError, what the
 library refuses MkError (the checks are in csrc_ops/calls.cpp).  Lengths,
 tables and maps are int32 tensors that the GPU reads; what is wrong with
 their values is reported in ``status`` (an int32 device tensor, zeroed by the
@@ -22,9 +27,14 @@ from . import _lib as L
 
 
 def on_stream(fn, stream, args):
-    """Call ``fn`` with ``stream`` current; the tensors have to be on its device."""
-    if any(isinstance(t, torch.Tensor) and t.is_cuda and t.device != stream.device for t in args):
+    """Call ``fn`` with ``stream`` current; the tensors have to be on its device.  The allocator learns that
+    ``stream`` uses them: their memory may belong to another stream, which would hand it out again while the call
+    still waits."""
+    tensors = [t for t in args if isinstance(t, torch.Tensor) and t.is_cuda]
+    if any(t.device != stream.device for t in tensors):
         raise ValueError(f"the stream is on {stream.device}, a tensor is not")
+    for t in tensors:
+        t.record_stream(stream)
     with torch.cuda.stream(stream):
         return fn(*args)
 

@@ -680,3 +680,60 @@ def test_a_tensor_that_requires_a_gradient_is_refused():
         paged.qk_norm_rope(x, 8, 2, 64, pos, pos, k, v, q_gamma=gain)
     with pytest.raises(ValueError, match="gradient"):
         paged.qk_norm_rope(x.requires_grad_(), 8, 2, 64, pos, pos, k, v)
+
+
+# ------------------------------------------------------------------ streams, lifetimes, threads
+@pytest.mark.parametrize("op", ["plan", "norms", "attention", "verify"])
+def test_an_input_dropped_behind_a_call_on_another_stream_is_not_made_over(op):
+    """The call's stream is still busy when the input's memory goes back to the allocator and the caller's own stream
+    asks for as much again."""
+    g = torch.Generator(device=DEV).manual_seed(51)
+    if op == "plan":
+        source = i32([40, 3, 100])
+        new, table, held, free, count = i32([3, 1, 20]), i32([[-1] * 9] * 3), i32([0] * 3), i32(range(20)), i32([20])
+        keep = dict(held_out=i32([0] * 3), count_out=i32([0]), max_tokens=30)
+        run = lambda x, **kw: paged.plan(x, new, table, held, free, count, 16, **keep, **kw)  # noqa: E731
+    elif op == "norms":
+        source = torch.randn(40, 12 * 64, device=DEV, generator=g)
+        pool = [torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        at = torch.arange(40, dtype=torch.int32, device=DEV)
+        run = lambda x, **kw: (paged.qk_norm_rope(x, 8, 2, 64, at, at, *pool, **kw),)  # noqa: E731
+    elif op == "attention":
+        source, k, v, table, cu = attention_case([300], [3], 8, 2, 64, 16, 51)
+        lens = i32(cu), i32([300])
+        run = lambda x, **kw: (paged.attention(x, k, v, table, *lens, 3, **kw),)  # noqa: E731
+    else:
+        from task_graph_interpreter_gb300 import speculative
+        source = torch.softmax(torch.randn(3, 4, 1000, device=DEV, generator=g), -1)
+        drafts, u = i32([[1, 2, 3]] * 3), torch.full((3, 4), 0.5, device=DEV)
+        run = lambda x, **kw: speculative.verify_drafts(x, drafts, u, **kw)  # noqa: E731
+    want = [t.clone() for t in run(source.clone())]
+    s = torch.cuda.Stream()
+    dropped = source.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(400_000_000)  # about 0.2 s
+    got = run(dropped, stream=s)
+    at_address = dropped.data_ptr()
+    del dropped
+    over = [torch.zeros_like(source) for _ in range(4)]
+    assert at_address not in [t.data_ptr() for t in over]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_a_call_on_a_side_stream_of_a_capture_with_an_input_made_there():
+    q, k, v, table, cu = attention_case([300], [3], 8, 2, 64, 16, 53)
+    lens = i32(cu), i32([300])
+    buf, s, graph = torch.zeros_like(q), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.wait_stream(torch.cuda.current_stream())
+        got = paged.attention(buf * 2, k, v, table, *lens, 3, stream=s)
+        over = [torch.zeros_like(q) for _ in range(4)]  # the doubled queries are dropped by now
+        torch.cuda.current_stream().wait_stream(s)
+    for scale in (0.5, 1.0):
+        buf.copy_(q * scale)
+        graph.replay()
+        assert torch.equal(got, paged.attention(buf * 2, k, v, table, *lens, 3))
+    assert not any(bool(t.any()) for t in over)
