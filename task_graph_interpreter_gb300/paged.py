@@ -117,16 +117,24 @@ class PagedCache:
         self.positions = torch.full((max_tokens,), -1, **i32)
         self.slots = torch.full((max_tokens,), -1, **i32)
         self.status = torch.zeros(1, **i32)
+        self._ctx_len = torch.zeros(max_requests, **i32)
         self.ctx_len = None
 
     def plan(self, ctx_len, new_len, stream=None) -> Plan:
         """Pages, positions and slots for every request's new_len tokens behind
-        its ctx_len cached ones (int32 [max_requests]; both 0 for a free row)."""
+        its ctx_len cached ones (int32 [max_requests]; both 0 for a free row).  The cache keeps a copy of the
+        lengths for the step's attention; the caller may count its own on."""
         if ctx_len.numel() != self.held.numel():
             raise ValueError(f"lengths of all {self.held.numel()} requests are needed")
-        self.ctx_len = ctx_len
-        return plan(ctx_len, new_len, self.table, self.held, self.free_pages, self.free_count, self.page_size,
+        made = plan(ctx_len, new_len, self.table, self.held, self.free_pages, self.free_count, self.page_size,
                     cu=self.cu, positions=self.positions, slots=self.slots, status=self.status, stream=stream)
+        if stream is None:
+            self._ctx_len.copy_(ctx_len.view(-1))
+        else:
+            with torch.cuda.stream(stream):
+                self._ctx_len.copy_(ctx_len.view(-1))
+        self.ctx_len = self._ctx_len
+        return made
 
     def append(self, layer: int, qkv, Hq: int, *, q_gamma=None, k_gamma=None, eps: float = 1e-5,
                rope_theta: float = 5e5, out=None, stream=None):

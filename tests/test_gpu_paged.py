@@ -737,3 +737,30 @@ def test_a_call_on_a_side_stream_of_a_capture_with_an_input_made_there():
         graph.replay()
         assert torch.equal(got, paged.attention(buf * 2, k, v, table, *lens, 3))
     assert not any(bool(t.any()) for t in over)
+
+
+def test_a_cache_attends_over_the_lengths_it_planned_with():
+    """The caller counts its lengths on in place, between the plan and the step's attention."""
+    c = paged.PagedCache(1, 8, 16, 2, 64, 2, 4, 64)
+    ctx, new = i32([0, 0]), i32([20, 5])
+    x = torch.randn(25, 12 * 64, device=DEV, generator=torch.Generator(device=DEV).manual_seed(52))
+    with pytest.raises(ValueError):  # nothing is planned yet
+        c.attention(0, torch.zeros(25, 8, 64, dtype=torch.bfloat16, device=DEV), 20)
+    c.plan(ctx, new)
+    want = c.attention(0, c.append(0, x, 8), 20).clone()
+    for stream in (None, torch.cuda.Stream()):
+        torch.cuda.synchronize()
+        c.plan(ctx, new, stream=stream)
+        torch.cuda.synchronize()
+        ctx += new
+        torch.cuda.synchronize()
+        got = c.attention(0, c.append(0, x, 8, stream=stream), 20, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        c.check()
+        ctx -= new
+    planned = c.ctx_len.clone()
+    for wrong in (i32([1, 2, 3]), ctx.long()):  # a refused plan leaves the step before it
+        with pytest.raises(ValueError):
+            c.plan(wrong, new)
+    assert torch.equal(c.ctx_len, planned) and torch.equal(c.attention(0, c.append(0, x, 8), 20), want)
