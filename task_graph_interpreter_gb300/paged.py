@@ -149,8 +149,11 @@ class PagedCache:
                          scale=scale, out=out, status=self.status, stream=stream)
 
     def check(self):
-        """Synchronise; raise if a step's lengths, pages or slots were wrong (and clear the status)."""
+        """Wait for the device; raise if a step's lengths, pages or slots were wrong, whatever stream it ran on
+        (and clear the status, before any later step)."""
+        torch.cuda.synchronize(self.status.device)
         code = int(self.status.item())
         if code:
             self.status.zero_()
+            torch.cuda.synchronize(self.status.device)
             raise L.MkError("PagedCache", code, "the device found a length, page or capacity that does not fit")

@@ -764,3 +764,20 @@ def test_a_cache_attends_over_the_lengths_it_planned_with():
         with pytest.raises(ValueError):
             c.plan(wrong, new)
     assert torch.equal(c.ctx_len, planned) and torch.equal(c.attention(0, c.append(0, x, 8), 20), want)
+
+
+def test_a_cache_is_checked_for_steps_on_every_stream():
+    c = paged.PagedCache(1, 4, 16, 2, 64, 1, 4, 2000)
+    ctx, new = i32([0]), i32([1000])  # more than its pages hold
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(400_000_000)
+    c.plan(ctx, new, stream=s)
+    with pytest.raises(L.MkError) as e:
+        c.check()
+    assert e.value.code == L.MK_DEV_CAPACITY
+    c.check()  # told once
+    c.plan(ctx, new, stream=s)  # behind the clearing, whatever the stream
+    with pytest.raises(L.MkError):
+        c.check()
