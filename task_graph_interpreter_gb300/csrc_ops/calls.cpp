@@ -265,16 +265,21 @@ PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// Workspace bytes, asked of the library once per device and shape.
+// Workspace bytes, asked of the library once per device and shape.  The lock is never held where Python code can
+// run (the exception of a refused shape is Python code): another thread may be waiting for it with the interpreter's
+// lock.
 size_t workspace_size(int dev, int max_new, int Hq, int Hkv, int D) {
   static std::mutex mu;
   static std::map<std::tuple<int, int, int, int, int>, size_t> known;
-  const std::lock_guard<std::mutex> lock(mu);
   const auto key = std::make_tuple(dev, max_new, Hq, Hkv, D);
-  const auto it = known.find(key);
-  if (it != known.end()) return it->second;
+  {
+    const std::lock_guard<std::mutex> lock(mu);
+    const auto it = known.find(key);
+    if (it != known.end()) return it->second;
+  }
   size_t bytes = 0;
   check(paged_attention_workspace(max_new, Hq, Hkv, D, &bytes), "mk_paged_attention_workspace");
+  const std::lock_guard<std::mutex> lock(mu);
   known.emplace(key, bytes);
   return bytes;
 }

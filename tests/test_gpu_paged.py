@@ -781,3 +781,43 @@ def test_a_cache_is_checked_for_steps_on_every_stream():
     c.plan(ctx, new, stream=s)  # behind the clearing, whatever the stream
     with pytest.raises(L.MkError):
         c.check()
+
+
+def test_a_refused_call_in_one_thread_does_not_hold_up_another():
+    """The exception's own Python code gives other threads a turn while it is made.  In a process of its own, so that
+    a lock held there ends this test and not the run."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import threading, time
+import torch
+from task_graph_interpreter_gb300 import _lib as L, paged
+q = torch.zeros(2, 8, 64, dtype=torch.bfloat16, device="cuda")
+pool = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+args = [torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([[0, 1]], [0, 2], [10])]
+raising, refused = threading.Event(), []
+plain = L.MkError.__init__
+def slow(self, *a):
+    raising.set()
+    time.sleep(1.0)
+    plain(self, *a)
+L.MkError.__init__ = slow
+def wrong():
+    try:
+        paged.attention(q, pool, pool, *args, 0)
+    except L.MkError as e:
+        refused.append(e.code)
+t = threading.Thread(target=wrong)
+t.start()
+assert raising.wait(60)
+for most in (2, 3, 4):
+    paged.attention(q, pool, pool, *args, most)
+torch.cuda.synchronize()
+t.join()
+assert refused == [L.MK_ERR_ARG], refused
+print("both done")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=180)
+    assert r.returncode == 0 and "both done" in r.stdout, r.stderr
