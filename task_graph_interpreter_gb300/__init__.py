@@ -7,5 +7,12 @@ Python binding (``_lib``, same names as the C ABI), a graph builder
 """
 from . import _lib  # noqa: F401
 from ._lib import MkError  # noqa: F401
-# (the function, not the module of its name: a function here that imported the module would be replaced by it)
-from .build import build  # noqa: F401
+
+
+def __getattr__(name):
+    # `build` is the module of that name, which can be called like its function: both spellings work, whichever was
+    # imported first.  (Not imported here: `python -m` would find it imported already.)
+    if name == "build":
+        import importlib
+        return importlib.import_module(".build", __name__)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

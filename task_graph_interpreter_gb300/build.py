@@ -10,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import types
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -96,6 +97,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.replace(tmp, LIB)
     return LIB
 
+
+class _Callable(types.ModuleType):
+    """The package's attribute ``build`` is this module; calling it builds."""
+
+    def __call__(self, force: bool = False, verbose: bool = False) -> str:
+        return build(force=force, verbose=verbose)
+
+
+sys.modules[__name__].__class__ = _Callable
 
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
