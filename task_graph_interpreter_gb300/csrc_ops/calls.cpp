@@ -11,6 +11,7 @@
 
 #include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/AutogradState.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -71,10 +72,13 @@ int device_of(const at::Tensor& t, const char* name) {
   if (!t.is_cuda()) refuse(std::string(name) + " must be a CUDA tensor");
   return (int)t.get_device();
 }
-// The operators have no backward pass: a gradient that would silently be missing is refused.
+// The operators have no derivatives: a gradient or a forward-mode tangent that would silently be missing is refused.
+// (torch.no_grad() does not end forward mode; its levels are one at most.)
 void no_gradient(const at::Tensor& t, const char* name) {
   if (t.requires_grad() && at::GradMode::is_enabled())
     refuse(std::string(name) + " requires a gradient, and this operator has none (call it under torch.no_grad())");
+  if (t._fw_grad(0).defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode())
+    refuse(std::string(name) + " carries a forward-mode tangent, and this operator has none (unpack the dual tensor)");
 }
 bool on(const at::Tensor& t, int dev) { return t.is_cuda() && t.get_device() == dev; }
 
@@ -353,6 +357,7 @@ PyObject* py_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (u.scalar_type() != at::kFloat || !on(u, dev) || u.numel() != (int64_t)B * (K + 1) || !u.is_contiguous())
       refuse("u must be contiguous f32 [" + std::to_string(B) + ", " + std::to_string(K + 1) + "] on cuda:" +
              std::to_string(dev));
+    no_gradient(u, "u");
     if (drafts.numel() != (int64_t)B * K)
       refuse("drafts must be int32 [" + std::to_string(B) + ", " + std::to_string(K) + "]");
     const int32_t* d = int32s(drafts, "drafts", (int64_t)B * K, dev);

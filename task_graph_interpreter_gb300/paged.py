@@ -14,7 +14,8 @@ library refuses MkError (the checks are in csrc_ops/calls.cpp).  Lengths,
 tables and maps are int32 tensors that the GPU reads; what is wrong with
 their values is reported in ``status`` (an int32 device tensor, zeroed by the
 caller, that receives the first MK_DEV_* code).  They serve inference: a tensor
-that requires a gradient is refused outside ``torch.no_grad()``.  ``PagedCache``
+that requires a gradient is refused outside ``torch.no_grad()``, one that
+carries a forward-mode tangent altogether.  ``PagedCache``
 holds a cache's pools, tables and free pages and runs the operators on them.
 """
 from __future__ import annotations

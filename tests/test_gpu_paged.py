@@ -821,3 +821,27 @@ print("both done")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=180)
     assert r.returncode == 0 and "both done" in r.stdout, r.stderr
+
+
+def test_a_tensor_that_carries_a_tangent_is_refused():
+    """Forward-mode tangents would be lost as silently as gradients, under torch.no_grad() too."""
+    import torch.autograd.forward_ad as forward_ad
+    from task_graph_interpreter_gb300 import speculative
+    q, k, v, table, cu = attention_case([30], [2], 8, 2, 64, 16, 31)
+    lens = i32(cu), i32([30])
+    x, pos = torch.zeros(2, 12 * 64, device=DEV), i32([0, 1])
+    gain = torch.ones(64, dtype=torch.bfloat16, device=DEV)
+    p, u, drafts = torch.full((1, 2, 10), 0.1, device=DEV), torch.full((1, 2), 0.5, device=DEV), i32([[3]])
+    with forward_ad.dual_level(), torch.no_grad():
+        dual = lambda t: forward_ad.make_dual(t, torch.ones_like(t))  # noqa: E731
+        for call in (lambda: paged.attention(dual(q), k, v, table, *lens, 2),
+                     lambda: paged.attention(q, k, dual(v), table, *lens, 2),
+                     lambda: paged.qk_norm_rope(dual(x), 8, 2, 64, pos, pos, k, v),
+                     lambda: paged.qk_norm_rope(x, 8, 2, 64, pos, pos, k, v, k_gamma=dual(gain)),
+                     lambda: speculative.verify_drafts(dual(p), drafts, u),
+                     lambda: speculative.verify_drafts(p, drafts, dual(u))):
+            with pytest.raises(ValueError, match="tangent"):
+                call()
+        paged.attention(forward_ad.unpack_dual(dual(q)).primal, k, v, table, *lens, 2)
+    with pytest.raises(ValueError, match="gradient"):
+        speculative.verify_drafts(p, drafts, u.requires_grad_())
