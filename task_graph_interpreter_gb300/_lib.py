@@ -128,13 +128,16 @@ def calls():
     if _calls is not None:
         return _calls
     L = lib()
-    path = os.path.join(HERE, "_calls.so")
-    if not os.path.exists(path):
-        raise ImportError(f"_calls.so not built ({path}); run task_graph_interpreter_gb300.build.build()")
     import importlib.machinery
     import importlib.util
 
     import torch  # noqa: F401  (its libraries come first)
+
+    from .build import calls_path
+    path = calls_path()
+    if not os.path.exists(path):
+        raise ImportError(f"the tensor-level calls are not built for this Python and PyTorch ({path}); run "
+                          "task_graph_interpreter_gb300.build.build()")
     loader = importlib.machinery.ExtensionFileLoader("_calls", path)
     m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
     loader.exec_module(m)

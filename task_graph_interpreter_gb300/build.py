@@ -1,5 +1,5 @@
-"""Build libmk.so in-tree with nvcc for sm_103a, and _calls.so, the CPython
-module of its tensor-level calls, with the host compiler.
+"""Build libmk.so in-tree with nvcc for sm_103a, and the CPython module of its
+tensor-level calls (_calls.*.so) with the host compiler.
 
 Each translation unit compiles in parallel into ``_build/``; the shared
 libraries land next to this file.  No CMake, one -gencode.
@@ -7,9 +7,11 @@ libraries land next to this file.  No CMake, one -gencode.
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 import types
 from concurrent.futures import ThreadPoolExecutor
 
@@ -20,7 +22,6 @@ OPS = os.path.join(HERE, "csrc_ops")       # operators that are called one by on
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmk.so")
-CALLS = os.path.join(HERE, "_calls.so")   # CPython module of the tensor-level calls (csrc_ops/calls.cpp)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = [os.path.join(CSRC, f) for f in ("graph.cpp", "runtime.cu", "megakernel.cu", "noalloc.cu")] + \
           [os.path.join(OPS, f) for f in ("paged.cu", "paged_rows.cu", "paged_chunk.cu", "paged_attention.cu",
@@ -51,9 +52,15 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def _compile_calls() -> None:
-    import sysconfig
+def calls_path() -> str:
+    """The CPython module of the tensor-level calls (csrc_ops/calls.cpp).  It is bound to the layouts of the Python and
+    the PyTorch it was compiled against, so its name holds both: another environment on the same tree builds its own."""
+    import torch
+    tag = re.sub(r"[^0-9A-Za-z.]+", "_", f"torch{torch.__version__}")
+    return os.path.join(HERE, f"_calls.{tag}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
+
+def _compile_calls() -> None:
     import torch
     base = os.path.dirname(torch.__file__)
     lib = os.path.join(base, "lib")
@@ -61,7 +68,8 @@ def _compile_calls() -> None:
     cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
     if not cxx:
         raise RuntimeError("no C++ compiler found")
-    tmp = CALLS + ".tmp"
+    path = calls_path()
+    tmp = path + ".tmp"
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            "-I", INCLUDE, "-isystem", os.path.join(base, "include"),
            "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"), "-isystem", cuda,
@@ -70,13 +78,14 @@ def _compile_calls() -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"the C++ compiler failed on calls.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS)
+    os.replace(tmp, path)
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
+    calls = calls_path()
+    if not os.path.exists(LIB) or not os.path.exists(calls):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
+    t = min(os.path.getmtime(LIB), os.path.getmtime(calls))
     deps = [os.path.join(d, f) for d in (CSRC, OPS) for f in os.listdir(d)] + [os.path.join(INCLUDE, "mk.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 

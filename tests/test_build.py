@@ -30,3 +30,19 @@ def test_the_package_has_no_other_attributes():
     import task_graph_interpreter_gb300 as p
     with pytest.raises(AttributeError):
         p.no_such_name
+
+
+def test_the_calls_module_belongs_to_one_python_and_one_torch(monkeypatch):
+    """A module that was compiled against another PyTorch is neither taken for up to date nor loaded."""
+    import torch
+
+    from task_graph_interpreter_gb300 import _lib
+    from task_graph_interpreter_gb300 import build as b
+    b.build()
+    assert not b._stale() and os.path.exists(b.calls_path())
+    assert b.calls_path().endswith(b.sysconfig.get_config_var("EXT_SUFFIX")) and torch.__version__[:4] in b.calls_path()
+    monkeypatch.setattr(torch, "__version__", "1.0.0+other")
+    assert b._stale() and not os.path.exists(b.calls_path())
+    monkeypatch.setattr(_lib, "_calls", None)
+    with pytest.raises(ImportError, match="PyTorch"):
+        _lib.calls()
