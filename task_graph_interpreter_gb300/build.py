@@ -81,29 +81,40 @@ def _compile_calls() -> None:
     os.replace(tmp, path)
 
 
-def _stale() -> bool:
-    calls = calls_path()
-    if not os.path.exists(LIB) or not os.path.exists(calls):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(calls))
-    deps = [os.path.join(d, f) for d in (CSRC, OPS) for f in os.listdir(d)] + [os.path.join(INCLUDE, "mk.h")]
-    return any(os.path.getmtime(d) > t for d in deps)
-
-
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        calls = ex.submit(_compile_calls)
-        objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-        calls.result()
+def _link(objs: list[str]) -> None:
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+
+
+def _stale(built: str, sources: list[str]) -> bool:
+    return not os.path.exists(built) or any(os.path.getmtime(s) > os.path.getmtime(built) for s in sources)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Bring libmk.so and the module of the tensor-level calls up to date.  The library is linked whatever becomes of
+    the module, which only PyTorch's users need: without PyTorch it is left out, and a failure to compile it is
+    raised behind the link."""
+    header, calls = os.path.join(INCLUDE, "mk.h"), os.path.join(OPS, "calls.cpp")
+    sources = [os.path.join(d, f) for d in (CSRC, OPS) for f in os.listdir(d)]
+    sources.remove(calls)
+    lib_stale = force or _stale(LIB, [*sources, header])
+    try:
+        calls_stale = _stale(calls_path(), [calls, header]) or force
+    except ImportError:
+        calls_stale = False
+    if not lib_stale and not calls_stale:
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        compiled = ex.submit(_compile_calls) if calls_stale else None
+        if lib_stale:
+            _link(list(ex.map(lambda s: _compile(s, verbose), SOURCES)))
+        if compiled:
+            compiled.result()
     return LIB
 
 

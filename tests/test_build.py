@@ -39,10 +39,79 @@ def test_the_calls_module_belongs_to_one_python_and_one_torch(monkeypatch):
     from task_graph_interpreter_gb300 import _lib
     from task_graph_interpreter_gb300 import build as b
     b.build()
-    assert not b._stale() and os.path.exists(b.calls_path())
+    assert os.path.exists(b.calls_path())
     assert b.calls_path().endswith(b.sysconfig.get_config_var("EXT_SUFFIX")) and torch.__version__[:4] in b.calls_path()
     monkeypatch.setattr(torch, "__version__", "1.0.0+other")
-    assert b._stale() and not os.path.exists(b.calls_path())
+    assert not os.path.exists(b.calls_path())
+    compiled = []
+    monkeypatch.setattr(b, "_compile_calls", lambda: compiled.append(b.calls_path()))
+    b.build()
+    assert compiled == [b.calls_path()]
     monkeypatch.setattr(_lib, "_calls", None)
     with pytest.raises(ImportError, match="PyTorch"):
         _lib.calls()
+
+
+@pytest.fixture
+def fake(monkeypatch, tmp_path):
+    """The build module with nothing built and nothing that really compiles; the steps it takes, in a list."""
+    import importlib
+    b = importlib.import_module("task_graph_interpreter_gb300.build")
+    steps = []
+    monkeypatch.setattr(b, "LIB", str(tmp_path / "libmk.so"))
+    monkeypatch.setattr(b, "BUILD", str(tmp_path / "build"))
+    monkeypatch.setattr(b, "calls_path", lambda: str(tmp_path / "calls.so"))
+    monkeypatch.setattr(b, "_compile", lambda src, verbose: os.path.basename(src))
+
+    def link(objs):
+        assert objs == [os.path.basename(s) for s in b.SOURCES]
+        steps.append("link")
+        open(b.LIB, "w").close()
+
+    def calls():
+        steps.append("calls")
+        open(b.calls_path(), "w").close()
+    monkeypatch.setattr(b, "_link", link)
+    monkeypatch.setattr(b, "_compile_calls", calls)
+    return b, steps
+
+
+def test_each_library_is_built_when_it_is_out_of_date(fake):
+    b, steps = fake
+    b.build()
+    assert sorted(steps) == ["calls", "link"]
+    b.build()
+    assert len(steps) == 2
+    os.unlink(b.calls_path())
+    b.build()
+    os.unlink(b.LIB)
+    b.build()
+    assert steps[2:] == ["calls", "link"]
+    os.utime(b.calls_path(), (0, 0))
+    b.build()
+    assert steps[4:] == ["calls"]
+    b.build(force=True)
+    assert len(steps) == 7
+
+
+def test_the_library_is_linked_although_the_calls_do_not_compile(fake, monkeypatch):
+    b, steps = fake
+
+    def fails():
+        raise RuntimeError("no C++ compiler found")
+    monkeypatch.setattr(b, "_compile_calls", fails)
+    with pytest.raises(RuntimeError, match="compiler"):
+        b.build()
+    assert steps == ["link"] and os.path.exists(b.LIB)
+
+
+def test_the_library_is_built_without_torch(fake, monkeypatch):
+    b, steps = fake
+
+    def missing():
+        raise ImportError("No module named 'torch'")
+    monkeypatch.setattr(b, "calls_path", missing)
+    assert b.build() == b.LIB and b.build() == b.LIB
+    assert steps == ["link"]
+    b.build(force=True)
+    assert steps == ["link", "link"]
