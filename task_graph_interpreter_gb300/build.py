@@ -35,6 +35,18 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def check_launch_registers(source: str, log: str) -> None:
+    """The chunk kernel's warpgroups trade registers at run time, and their shares add up to exactly what it is
+    launched with (kLaunchRegs of its source).  Another count by the compiler is an error of the build; the launch
+    refuses it too."""
+    want = int(re.search(r"kLaunchRegs = (\d+)", source).group(1))
+    used = re.findall(r"Compiling entry function '\w*chunk_kernel\w*'(?:(?!Compiling entry).)*?Used (\d+) registers", log,
+                      re.S)
+    if not used or any(int(n) != want for n in used):
+        raise RuntimeError(f"paged_chunk.cu: the chunk kernel has to be compiled to {want} registers, not to "
+                           f"{', '.join(used) or 'an unknown number'}: set kLaunchRegs and the shares to this compiler's")
+
+
 def _compile(src: str, verbose: bool) -> str:
     name = os.path.basename(src)
     obj = os.path.join(BUILD, os.path.splitext(name)[0] + ".o")
@@ -42,11 +54,14 @@ def _compile(src: str, verbose: bool) -> str:
            "-I", INCLUDE, "-I", CSRC, "-I", OPS, "-c", src, "-o", obj]
     if src.endswith(".cpp"):
         cmd[1:1] = ["-x", "cu"]
-    if verbose and name in ("megakernel.cu", "paged_chunk.cu"):
+    if name == "paged_chunk.cu" or verbose and name == "megakernel.cu":
         cmd.append("-Xptxas=-v")
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed on {name}:\n{r.stdout}\n{r.stderr}")
+    if name == "paged_chunk.cu":
+        with open(src) as f:
+            check_launch_registers(f.read(), r.stdout + r.stderr)
     if verbose and r.stderr:
         sys.stderr.write(r.stderr)
     return obj

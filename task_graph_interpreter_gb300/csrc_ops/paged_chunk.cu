@@ -779,7 +779,8 @@ cudaError_t launch_chunk_t(const AttnParams& p, const CUtensorMap& qmap, const C
     if ((e = cudaFuncGetAttributes(&a, chunk_kernel<D>)) != cudaSuccess) return e;
     regs.store(a.numRegs, std::memory_order_relaxed);
   }
-  // the register shares add up to this allocation: with fewer a warpgroup would wait for registers for ever
+  // the register shares add up to this allocation: with fewer a warpgroup would wait for registers for ever (build.py
+  // checks the compiler's count, so that this is met by builds of another kind only)
   if (regs.load(std::memory_order_relaxed) != kLaunchRegs) return cudaErrorInvalidKernelImage;
   return launch_early(chunk_kernel<D>, dim3((unsigned)p.workers), dim3(kThreads), Smem<D>::kBytes, stream, p, qmap, kmap,
                       vmap);

@@ -115,3 +115,25 @@ def test_the_library_is_built_without_torch(fake, monkeypatch):
     assert steps == ["link"]
     b.build(force=True)
     assert steps == ["link", "link"]
+
+
+LOG = """ptxas info    : Compiling entry function '_ZN2mk_12chunk_kernelILi64EEEvNS' for 'sm_103a'
+ptxas info    : Function properties for _ZN2mk_12chunk_kernelILi64EEEvNS
+    128 bytes stack frame, 0 bytes spill stores, 0 bytes spill loads
+ptxas info    : Used %d registers, used 1 barriers, 128 bytes cumulative stack size
+ptxas info    : Compiling entry function '_ZN2mk_12chunk_kernelILi128EEEvNS' for 'sm_103a'
+ptxas info    : Used %d registers, used 1 barriers
+ptxas info    : Compiling entry function '_ZN2mk_other' for 'sm_103a'
+ptxas info    : Used 40 registers, used 1 barriers
+"""
+
+
+def test_the_chunk_kernel_has_to_be_compiled_to_the_registers_of_its_launch():
+    import importlib
+    b = importlib.import_module("task_graph_interpreter_gb300.build")
+    with open(os.path.join(b.OPS, "paged_chunk.cu")) as f:
+        source = f.read()
+    b.check_launch_registers(source, LOG % (168, 168))
+    for log in (LOG % (166, 168), LOG % (168, 128), LOG.split("ptxas info    : Compiling entry function '_ZN2mk_other")[1], ""):
+        with pytest.raises(RuntimeError, match="168 registers"):
+            b.check_launch_registers(source, log)
