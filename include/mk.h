@@ -528,7 +528,9 @@ int mk_qk_norm_rope(void* stream, int N, int Hq, int Hkv, int D, const void* qkv
  * without any key is zero.  Cache memory behind a request's last key may
  * hold anything.  Lengths that do not fit (cu decreasing or past N, a request
  * over max_new or max_pages, a negative length) give MK_DEV_BAD_INDEX and
- * nothing is written.  D 64 or 128, Hq / Hkv <= 128.  q may not overlap out. */
+ * nothing is written.  D 64 or 128, Hq / Hkv <= 128, num_pages * Hkv *
+ * page_size < 2^31, max_pages * page_size <= 2^31 - 256.  q may not overlap
+ * out. */
 int mk_paged_attention(void* stream, int B, int N, int max_new, int Hq, int Hkv, int D, const void* q, int64_t ld_q,
                        const void* kpool, const void* vpool, int num_pages, int page_size, const int32_t* table,
                        int max_pages, const int32_t* cu, const int32_t* ctx_len, float scale, void* out,

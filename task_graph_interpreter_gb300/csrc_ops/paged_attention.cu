@@ -84,9 +84,11 @@ extern "C" int mk_paged_attention(void* stream_, int B, int N, int max_new, int 
   if (B < 0 || N < 0 || max_pages < 1) return fail(MK_ERR_ARG, "mk_paged_attention: need B, N >= 0 and max_pages >= 1");
   if (!page_size_ok(page_size))
     return fail(MK_ERR_ARG, "mk_paged_attention: page_size must be 16, 32, 64, 128 or 256");
+  // (positions are counted on to the end of a block of 128 keys, and past a request's last token to the end of two
+  // tiles' rows: at most 254)
   if (num_pages < 1 || (int64_t)num_pages * Hkv * page_size > INT32_MAX ||
-      (int64_t)max_pages * page_size > INT32_MAX)
-    return fail(MK_ERR_ARG, "mk_paged_attention: rows of the pools and positions must fit int32");
+      (int64_t)max_pages * page_size > INT32_MAX - 255)
+    return fail(MK_ERR_ARG, "mk_paged_attention: rows of the pools must fit int32, max_pages * page_size 2^31 - 256");
   if (ld_q < (int64_t)Hq * D || ld_q % 8 || ld_out < (int64_t)Hq * D || ld_out % 8)
     return fail(MK_ERR_ARG, "mk_paged_attention: row strides must cover a row and be multiples of 16 bytes");
   if (!aligned16(q) || !aligned16(kpool) || !aligned16(vpool) || !aligned16(out) || !aligned16(workspace))

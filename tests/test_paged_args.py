@@ -100,3 +100,11 @@ def test_tensor_functions_refuse_host_tensors():
         paged.attention(torch.zeros(4, 2, 64, dtype=torch.bfloat16), pool, pool, i.view(2, 2), i, i[:2], 1)
     with pytest.raises(ValueError):
         speculative.verify_drafts(torch.zeros(2, 3, 10), i.view(2, 2), torch.zeros(2, 3))
+
+
+@pytest.mark.parametrize("page_size,max_pages", [(16, (1 << 27) - 1), (16, (1 << 27) - 15), (128, (1 << 24) - 1)])
+def test_attention_refuses_tables_up_to_the_end_of_int32(L, page_size, max_pages):
+    """The kernels count keys in whole blocks of up to 128, and rows of a tile up to 254 past a request's last: the
+    last 255 positions that int32 holds are theirs."""
+    assert max_pages * page_size < 2 ** 31
+    refused(L, "mk_paged_attention", ATTN, L.MK_ERR_ARG, page_size=page_size, max_pages=max_pages)
