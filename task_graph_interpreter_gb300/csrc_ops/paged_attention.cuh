@@ -37,6 +37,12 @@ struct AttnParams {
 
 constexpr int kRowBlockBytes = 16384;  // keys and values of a few-rows block
 
+// Keys that a part's results are summed over by the products alone.  The tensor cores cut each sum off towards zero
+// (measured: 2^-22 of it per 16 keys), which over a long part is a shrinkage: values of 1.0 came out as 0.996 behind
+// 2^20 keys and as 0.976 behind 2^22.  So every 2^16 keys a worker adds its results to the place of its partial
+// record, in f32 and rounded to nearest, and goes on from zero; what is lost stays under 2^-11.
+constexpr int kFoldKeys = 65536;
+
 // Geometry of an item: few query rows (all of a request's), or a pair of
 // 128-row query tiles.
 template <int D, bool CHUNK>
@@ -244,6 +250,9 @@ struct Note {
 __device__ __forceinline__ Note* note_of(const AttnParams& p, int D, int w) {
   return reinterpret_cast<Note*>(p.part + (size_t)2 * p.workers * p.rows * (D + 2)) + w;
 }
+
+// What results folded at the maximum `at` are worth at the maximum `m` (both -inf: nothing was seen, and they are 0).
+__device__ __forceinline__ float fold_weight(float at, float m) { return at == m ? 1.f : ptx::ex2(at - m); }
 
 // Wait for a phase of an mbarrier, at most about a second, or until another
 // thread has given up.

@@ -160,6 +160,41 @@ __device__ __noinline__ void add_odd_values(const AttnParams& p, const Segment& 
   }
 }
 
+// Every kFold blocks of a part a row's results go from tensor memory to the place of the part's record (where the
+// part is a whole item, to the worker's second, which is still free), and at the part's end what lies there is added
+// to the rest (`last`).  `m` is the row's maximum now, `some` whether results lie there already.  A whole warp, out of
+// line: few parts are so long, and inside the loop over the blocks this cost 3 % of the long prompt's time, folding or
+// not (314 us to 323; this way 313, seven chunks of 64-wide heads 40.0 to 40.3).
+constexpr int kFold = kFoldKeys / 128;
+__device__ __noinline__ void fold_results(const AttnParams& p, int D, int slot, int row, uint32_t to, float m,
+                                          bool mine, bool some, bool last) {
+  float* at = part_ml(p, D, slot, row);  // the maximum that the results there are worth
+  const float f = mine && some ? fold_weight(*at, m) : 0.f;
+  if (mine) *at = m;
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    float o[32];
+    tmem_ld32(to + c, o);
+    tmem_wait_ld();
+    float4* rec = part_cols(p, D, slot, row, c);
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (mine) {
+        if (some) x = rec[e / 4 * kTileRows];
+        x = make_float4(o[e] + x.x * f, o[e + 1] + x.y * f, o[e + 2] + x.z * f, o[e + 3] + x.w * f);
+        if (!last) rec[e / 4 * kTileRows] = x;
+      }
+      o[e] = last ? x.x : 0.f;
+      o[e + 1] = last ? x.y : 0.f;
+      o[e + 2] = last ? x.z : 0.f;
+      o[e + 3] = last ? x.w : 0.f;
+    }
+    tmem_st32(to + c, o);
+  }
+  tmem_wait_st();
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap qmap,
@@ -612,97 +647,106 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int jm = ((s.ctx + s.t0 + w * p.tq + 1) >> 7) - k0;  // the first block that the tile does not wholly see
       float m = -INFINITY, l = 0.f;
       bool ok = true;
-      for (int j = 0; j < nt; ++j) {
-        if (!(ok = wait_phase(&s_full[w], ns & 1, &gave_up))) break;
-        ++ns;
-        tc_fence_after();
-        const uint32_t miss = missing[(blk + j) & 7];
-        if (j >= jm || miss) {
-          // scores of keys that the row does not see become -inf where they lie, 32 columns at a time (a loop,
-          // for the sake of the code's size)
-          const int last = lim - (k0 + j) * 128;
+      const int fold_slot = s.slot >= 0 ? s.slot : 2 * (int)blockIdx.x + 1;
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
-            const int n = last + 1 - c;
-            uint32_t see = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
-            if (miss) see &= ~missing_keys(miss, c, p.page_shift);
-            if (__all_sync(0xffffffffu, see == ~0u)) continue;
-            float y[32];
-            tmem_ld32(ts + c, y);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((see >> e) & 1)) y[e] = -INFINITY;
-            tmem_st32(ts + c, y);
-          }
-          tmem_wait_st();
-        }
-        float x[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, x + c * 32);
-        tmem_wait_ld();
-        if constexpr (kApart) {  // the next scores may come
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_free[w]);
-        }
-        float mx[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) mx[e] = fmaxf(x[e], x[e + 8]);
-#pragma unroll
-        for (int c = 16; c < 128; c += 16)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) mx[e] = fmaxf(fmaxf(mx[e], x[c + e]), x[c + 8 + e]);
-        const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * p.scale;
-        if (j == 0) {
-          m = top;
-        } else {
-          if constexpr (kApart) {  // the last block's product has read P, and O is whole
-            if (!(ok = wait_phase(&o_done[w], no & 1, &gave_up))) break;
-            ++no;
-            tc_fence_after();
-          }
-          const bool far = top > m + 8.f;
-          if (__any_sync(0xffffffffu, far)) {
-            // (at D = 128 the barrier of this block's S covers every product into O)
-            const float f = far ? ex2(m - top) : 1.f;
-            if (far) m = top;
-            l *= f;
+      for (int j = 0, stop = kFold; ok; stop += kFold) {
+        for (; j < min(nt, stop); ++j) {
+          if (!(ok = wait_phase(&s_full[w], ns & 1, &gave_up))) break;
+          ++ns;
+          tc_fence_after();
+          const uint32_t miss = missing[(blk + j) & 7];
+          if (j >= jm || miss) {
+            // scores of keys that the row does not see become -inf where they lie, 32 columns at a time (a loop,
+            // for the sake of the code's size)
+            const int last = lim - (k0 + j) * 128;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float o[32];
-              tmem_ld32(to + c, o);
+            for (int c = 0; c < 128; c += 32) {
+              const int n = last + 1 - c;
+              uint32_t see = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
+              if (miss) see &= ~missing_keys(miss, c, p.page_shift);
+              if (__all_sync(0xffffffffu, see == ~0u)) continue;
+              float y[32];
+              tmem_ld32(ts + c, y);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= f;
-              tmem_st32(to + c, o);
+              for (int e = 0; e < 32; ++e)
+                if (!((see >> e) & 1)) y[e] = -INFINITY;
+              tmem_st32(ts + c, y);
             }
-          }
-        }
-        const float mu = m == -INFINITY ? 0.f : -m;
-        const uint64_t scale2 = pair_f32(p.scale, p.scale), mu2 = pair_f32(mu, mu);
-        uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 y = unpair_f32(fma2(pair_f32(x[c * 32 + 2 * e], x[c * 32 + 2 * e + 1]), scale2, mu2));
-            const float a = ex2(y.x), b = ex2(y.y);
-            sum[e & 3] = add2(sum[e & 3], pair_f32(a, b));
-            r[e] = pack_bf16(a, b);
-          }
-          tmem_st16(tp + c * 16, r);
-          if (c & 1) {  // half of the keys: the product starts on them
             tmem_wait_st();
+          }
+          float x[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, x + c * 32);
+          tmem_wait_ld();
+          if constexpr (kApart) {  // the next scores may come
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[w][c >> 1]);
+            if (lane == 0) mbar_arrive(&s_free[w]);
           }
+          float mx[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mx[e] = fmaxf(x[e], x[e + 8]);
+#pragma unroll
+          for (int c = 16; c < 128; c += 16)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mx[e] = fmaxf(fmaxf(mx[e], x[c + e]), x[c + 8 + e]);
+          const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                  fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * p.scale;
+          if (j == 0) {
+            m = top;
+          } else {
+            if constexpr (kApart) {  // the last block's product has read P, and O is whole
+              if (!(ok = wait_phase(&o_done[w], no & 1, &gave_up))) break;
+              ++no;
+              tc_fence_after();
+            }
+            const bool far = top > m + 8.f;
+            if (__any_sync(0xffffffffu, far)) {
+              // (at D = 128 the barrier of this block's S covers every product into O)
+              const float f = far ? ex2(m - top) : 1.f;
+              if (far) m = top;
+              l *= f;
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_ld32(to + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= f;
+                tmem_st32(to + c, o);
+              }
+            }
+          }
+          const float mu = m == -INFINITY ? 0.f : -m;
+          const uint64_t scale2 = pair_f32(p.scale, p.scale), mu2 = pair_f32(mu, mu);
+          uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 y = unpair_f32(fma2(pair_f32(x[c * 32 + 2 * e], x[c * 32 + 2 * e + 1]), scale2, mu2));
+              const float a = ex2(y.x), b = ex2(y.y);
+              sum[e & 3] = add2(sum[e & 3], pair_f32(a, b));
+              r[e] = pack_bf16(a, b);
+            }
+            tmem_st16(tp + c * 16, r);
+            if (c & 1) {  // half of the keys: the product starts on them
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&p_full[w][c >> 1]);
+            }
+          }
+          const float2 t = unpair_f32(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+          l += t.x + t.y;
         }
-        const float2 t = unpair_f32(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
-        l += t.x + t.y;
+        if (!ok || j >= nt) break;
+        // O is whole once the next scores are there (at D = 64, once its last product is done)
+        if (!(ok = wait_phase(kApart ? &o_done[w] : &s_full[w], (kApart ? no : ns) & 1, &gave_up))) break;
+        tc_fence_after();
+        fold_results(p, D, fold_slot, w * 128 + row, to, m, mine, stop > kFold, false);
       }
       if (!ok) break;
       blk += s.k1 - k0;
@@ -711,6 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++no;
         tc_fence_after();
       }
+      if (nt > kFold) fold_results(p, D, fold_slot, w * 128 + row, to, m, mine, true, true);
       const bool set_aside = nt > 0 && odd[sst];
       const float f = s.slot >= 0 ? 1.f : nt == 0 || l == 0.f ? 0.f : 1.0f / l;  // a row without keys is zero
       __nv_bfloat16* dst = p.out + ((int64_t)s.row0 + w * p.tq + tok_in) * p.ld_out + (int64_t)(s.g * p.G + head) * D;

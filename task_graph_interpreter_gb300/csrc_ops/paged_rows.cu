@@ -206,153 +206,180 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       const int c = kk * 4 + (lane >> 3);
       ldsm4(swz(qs + (c >> 3) * (kMaxFewRows * 128), lane & 7, c & 7), qf[kk]);
     }
+    const int slot = 2 * w + (kb == 0 ? 1 : 0);  // of the part's record (free while a whole item is worked on)
     float o[D / 16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int t = 0; t < D / 16; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
 
-    for (; ck < cke; ++ck) {
-      const int st = done % kStages;
-      if (!wait_phase(&full[warp][st], (done / kStages) & 1, &gave_up)) {
-        if (lane == 0) set_status(p.status, MK_DEV_RING_TIMEOUT);
-        // the copies in flight land in this CTA's memory: give them time before it goes
-        for (uint32_t d = done; d < issued; ++d)
-          for (int i = 0; i < 100000 && !mbar_try_wait(&full[warp][d % kStages], (d / kStages) & 1); ++i) {
-          }
-        return;
-      }
-      const uint32_t ks = smem_addr(ring + st * kStageBytes), vs = ks + kHalfBytes;
-      const uint64_t keys = live[warp][st];
-      const int key0 = ck * KU;
-      constexpr uint64_t kAll = KU == 64 ? ~0ull : (1ull << (KU & 63)) - 1;
-      const bool masked = keys != kAll || key0 + KU > ctx + 1;
+    constexpr int kFold = kFoldKeys / KU;
+    float mfold[2] = {-INFINITY, -INFINITY};  // the maxima that folded results are worth
+#pragma unroll 1
+    for (int stop = kb + kFold;; stop += kFold) {
+      for (; ck < min(cke, stop); ++ck) {
+        const int st = done % kStages;
+        if (!wait_phase(&full[warp][st], (done / kStages) & 1, &gave_up)) {
+          if (lane == 0) set_status(p.status, MK_DEV_RING_TIMEOUT);
+          // the copies in flight land in this CTA's memory: give them time before it goes
+          for (uint32_t d = done; d < issued; ++d)
+            for (int i = 0; i < 100000 && !mbar_try_wait(&full[warp][d % kStages], (d / kStages) & 1); ++i) {
+            }
+          return;
+        }
+        const uint32_t ks = smem_addr(ring + st * kStageBytes), vs = ks + kHalfBytes;
+        const uint64_t keys = live[warp][st];
+        const int key0 = ck * KU;
+        constexpr uint64_t kAll = KU == 64 ? ~0ull : (1ull << (KU & 63)) - 1;
+        const bool masked = keys != kAll || key0 + KU > ctx + 1;
 
-      float s[NK][4];
+        float s[NK][4];
 #pragma unroll
-      for (int t = 0; t < NK; ++t)
+        for (int t = 0; t < NK; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+          for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t a[NK][4];  // keys t * 16 .. + 15, columns kk * 16 .. + 15
-        const int c = kk * 2 + (lane >> 4);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          uint32_t a[NK][4];  // keys t * 16 .. + 15, columns kk * 16 .. + 15
+          const int c = kk * 2 + (lane >> 4);
 #pragma unroll
-        for (int t = 0; t < NK; ++t) ldsm4(swz(ks + (c >> 3) * (KU * 128), t * 16 + (lane & 15), c & 7), a[t]);
+          for (int t = 0; t < NK; ++t) ldsm4(swz(ks + (c >> 3) * (KU * 128), t * 16 + (lane & 15), c & 7), a[t]);
 #pragma unroll
-        for (int t = 0; t < NK; ++t) mma_bf16(s[t], a[t], qf[kk >> 1][(kk & 1) * 2], qf[kk >> 1][(kk & 1) * 2 + 1]);
-      }
-      if (masked) {
+          for (int t = 0; t < NK; ++t) mma_bf16(s[t], a[t], qf[kk >> 1][(kk & 1) * 2], qf[kk >> 1][(kk & 1) * 2 + 1]);
+        }
+        if (masked) {
+#pragma unroll
+          for (int t = 0; t < NK; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int k = t * 16 + g + (e >> 1) * 8;
+              if (!((keys >> k) & 1) || key0 + k > lim[e & 1]) s[t][e] = -INFINITY;
+            }
+        }
+        bool moved = false;
+        float mnew[2], muse[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(s[0][e], s[0][e + 2]);
+#pragma unroll
+          for (int t = 1; t < NK; ++t) x = fmaxf(x, fmaxf(s[t][e], s[t][e + 2]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          mnew[e] = fmaxf(m[e], x * p.scale);
+          muse[e] = mnew[e] == -INFINITY ? 0.f : mnew[e];  // a row without any key so far
+          moved |= mnew[e] != m[e];
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float f = ex2(m[e] - muse[e]);
+            m[e] = mnew[e];
+            l[e] *= f;
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) {
+              o[t][e] *= f;
+              o[t][e + 2] *= f;
+            }
+          }
+        }
 #pragma unroll
         for (int t = 0; t < NK; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int k = t * 16 + g + (e >> 1) * 8;
-            if (!((keys >> k) & 1) || key0 + k > lim[e & 1]) s[t][e] = -INFINITY;
+            const float x = ex2(fmaf(s[t][e], p.scale, -muse[e & 1]));
+            s[t][e] = x;
+            l[e & 1] += x;
           }
-      }
-      bool moved = false;
-      float mnew[2], muse[2];
+        bool bad_v = false;  // a value that is not finite behind a mask
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = fmaxf(s[0][e], s[0][e + 2]);
+        for (int t = 0; t < NK; ++t) {
+          // probabilities as operands: 16 keys by 8 rows, transposed, in two parts
+          uint32_t hi[2], lo[2];
 #pragma unroll
-        for (int t = 1; t < NK; ++t) x = fmaxf(x, fmaxf(s[t][e], s[t][e + 2]));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-        mnew[e] = fmaxf(m[e], x * p.scale);
-        muse[e] = mnew[e] == -INFINITY ? 0.f : mnew[e];  // a row without any key so far
-        moved |= mnew[e] != m[e];
-      }
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float f = ex2(m[e] - muse[e]);
-          m[e] = mnew[e];
-          l[e] *= f;
-#pragma unroll
-          for (int t = 0; t < D / 16; ++t) {
-            o[t][e] *= f;
-            o[t][e + 2] *= f;
+          for (int e = 0; e < 2; ++e) {
+            const float x = s[t][2 * e], y = s[t][2 * e + 1];
+            const uint32_t h = pack_bf16(x, y);
+            hi[e] = movm_trans(h);
+            lo[e] = movm_trans(pack_bf16(x - bf_lo(h), y - bf_hi(h)));
           }
-        }
-      }
+          // this lane's four keys of the 16: c0, c0 + 1, c0 + 8, c0 + 9
+          uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+          if (masked) {
+            const uint32_t k16 = (uint32_t)(keys >> (t * 16)) >> c0;
+            keep0 = ((k16 & 1) ? 0xFFFFu : 0u) | ((k16 & 2) ? 0xFFFF0000u : 0u);
+            keep1 = ((k16 & 0x100) ? 0xFFFFu : 0u) | ((k16 & 0x200) ? 0xFFFF0000u : 0u);
+          }
 #pragma unroll
-      for (int t = 0; t < NK; ++t)
+          for (int d = 0; d < D / 16; d += 4) {
+            uint32_t a[4][4];  // columns (d + q) * 16 .. + 15 of the values by the 16 keys
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = ex2(fmaf(s[t][e], p.scale, -muse[e & 1]));
-          s[t][e] = x;
-          l[e & 1] += x;
-        }
-      bool bad_v = false;  // a value that is not finite behind a mask
+            for (int q = 0; q < 4; ++q) {
+              const int r = t * 16 + (lane >> 4) * 8 + (lane & 7), c = (d + q) * 2 + ((lane >> 3) & 1);
+              ldsm4t(swz(vs + (c >> 3) * (KU * 128), r, c & 7), a[q]);
+              if (masked) {
+                // values that were not loaded are zero, whatever the memory held
+                a[q][0] &= keep0; a[q][1] &= keep0; a[q][2] &= keep1; a[q][3] &= keep1;
+                if (n > 1) {
 #pragma unroll
-      for (int t = 0; t < NK; ++t) {
-        // probabilities as operands: 16 keys by 8 rows, transposed, in two parts
-        uint32_t hi[2], lo[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float x = s[t][2 * e], y = s[t][2 * e + 1];
-          const uint32_t h = pack_bf16(x, y);
-          hi[e] = movm_trans(h);
-          lo[e] = movm_trans(pack_bf16(x - bf_lo(h), y - bf_hi(h)));
-        }
-        // this lane's four keys of the 16: c0, c0 + 1, c0 + 8, c0 + 9
-        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-        if (masked) {
-          const uint32_t k16 = (uint32_t)(keys >> (t * 16)) >> c0;
-          keep0 = ((k16 & 1) ? 0xFFFFu : 0u) | ((k16 & 2) ? 0xFFFF0000u : 0u);
-          keep1 = ((k16 & 0x100) ? 0xFFFFu : 0u) | ((k16 & 0x200) ? 0xFFFF0000u : 0u);
-        }
-#pragma unroll
-        for (int d = 0; d < D / 16; d += 4) {
-          uint32_t a[4][4];  // columns (d + q) * 16 .. + 15 of the values by the 16 keys
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int r = t * 16 + (lane >> 4) * 8 + (lane & 7), c = (d + q) * 2 + ((lane >> 3) & 1);
-            ldsm4t(swz(vs + (c >> 3) * (KU * 128), r, c & 7), a[q]);
-            if (masked) {
-              // values that were not loaded are zero, whatever the memory held
-              a[q][0] &= keep0; a[q][1] &= keep0; a[q][2] &= keep1; a[q][3] &= keep1;
-              if (n > 1) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  if (nonfinite_lo(a[q][e])) { a[q][e] &= 0xFFFF0000u; bad_v = true; }
-                  if (nonfinite_hi(a[q][e])) { a[q][e] &= 0xFFFFu; bad_v = true; }
+                  for (int e = 0; e < 4; ++e) {
+                    if (nonfinite_lo(a[q][e])) { a[q][e] &= 0xFFFF0000u; bad_v = true; }
+                    if (nonfinite_hi(a[q][e])) { a[q][e] &= 0xFFFFu; bad_v = true; }
+                  }
                 }
               }
             }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mma_bf16(o[d + q], a[q], hi[0], hi[1]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mma_bf16(o[d + q], a[q], lo[0], lo[1]);
           }
-#pragma unroll
-          for (int q = 0; q < 4; ++q) mma_bf16(o[d + q], a[q], hi[0], hi[1]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) mma_bf16(o[d + q], a[q], lo[0], lo[1]);
         }
-      }
-      if (masked && n > 1 && __any_sync(0xffffffffu, bad_v)) {
-        // 0 * inf would reach the rows that do not see the key: such values were left
-        // out above and go to the rows that see it only
+        if (masked && n > 1 && __any_sync(0xffffffffu, bad_v)) {
+          // 0 * inf would reach the rows that do not see the key: such values were left
+          // out above and go to the rows that see it only
 #pragma unroll 1
-        for (int k = 0; k < KU; ++k) {
-          if (!((keys >> k) & 1)) continue;
+          for (int k = 0; k < KU; ++k) {
+            if (!((keys >> k) & 1)) continue;
 #pragma unroll
-          for (int d = 0; d < D / 16; ++d)
+            for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const int col = d * 16 + q * 8 + g, c = col >> 3;
-              const uint32_t w2 = lds32(swz(vs + (c >> 3) * (KU * 128), k, c & 7) + ((col & 7) >> 1) * 4);
-              const uint32_t v = col & 1 ? w2 >> 16 : w2 & 0xFFFFu;
-              if ((v & 0x7F80u) != 0x7F80u) continue;
+              for (int q = 0; q < 2; ++q) {
+                const int col = d * 16 + q * 8 + g, c = col >> 3;
+                const uint32_t w2 = lds32(swz(vs + (c >> 3) * (KU * 128), k, c & 7) + ((col & 7) >> 1) * 4);
+                const uint32_t v = col & 1 ? w2 >> 16 : w2 & 0xFFFFu;
+                if ((v & 0x7F80u) != 0x7F80u) continue;
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (key0 + k <= lim[e]) o[d][2 * q + e] += bf_lo(v);
-            }
+                for (int e = 0; e < 2; ++e)
+                  if (key0 + k <= lim[e]) o[d][2 * q + e] += bf_lo(v);
+              }
+          }
         }
+        __syncwarp();  // every lane has read the block
+        ++done;
+        issue();
       }
-      __syncwarp();  // every lane has read the block
-      ++done;
-      issue();
+      if (cke - kb <= kFold) break;
+      // a long part: the results so far go to the place of its record, at its end what lies there is added to the rest
+      const bool some = stop > kb + kFold, last = ck >= cke;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = c0 + e;
+        if (r >= nrows) continue;
+        float* dst = part_o(p, D, slot, r) + g;
+        const float f = fold_weight(mfold[e], m[e]);
+        mfold[e] = m[e];
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float* at = dst + d * 16 + q * 8;
+            const float x = o[d][2 * q + e] + (some ? *at * f : 0.f);
+            if (!last) *at = x;
+            o[d][2 * q + e] = last ? x : 0.f;
+          }
+      }
+      if (last) break;
     }
 
 #pragma unroll
@@ -362,7 +389,6 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
     }
     const bool whole = kb == 0 && cke == nk;
-    const int slot = 2 * w + (kb == 0 ? 1 : 0);
     if (kb != 0 && cke == nk) note = {cons.first_worker(line), cons.s.row0, cons.g, n};
     __nv_bfloat16* ob = p.out + (int64_t)cons.s.row0 * p.ld_out + (int64_t)cons.g * p.G * D;
     if (whole) {

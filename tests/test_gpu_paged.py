@@ -845,3 +845,35 @@ def test_a_tensor_that_carries_a_tangent_is_refused():
         paged.attention(forward_ad.unpack_dual(dual(q)).primal, k, v, table, *lens, 2)
     with pytest.raises(ValueError, match="gradient"):
         speculative.verify_drafts(p, drafts, u.requires_grad_())
+
+
+# ------------------------------------------------------------------ long contexts
+@pytest.mark.parametrize("heads,n,D,ctx", [(1.0, 9, 128, (1 << 22) - 9), (0.67, 9, 128, (1 << 22) + 77), (1.0, 40, 64, 3 << 20),
+                                           (0.67, 9, 64, 1 << 22), (4.0, 1, 128, (1 << 21) - 1), (2.7, 2, 64, 1 << 22)])
+def test_attention_over_millions_of_keys_keeps_its_sums(heads, n, D, ctx):
+    """As many heads to an SM that a worker sums millions of keys of one item, whole items and cut ones.  The keys are
+    1024 distinct ones in turn, from four pages, so the softmax over them is one over 1024 with counts; the values
+    have one sign, so that nothing hides what their sums lose.
+
+    Beside the tolerance of shorter contexts: the products cut 2^-22 of the running sum off per 16 keys, twice where
+    probabilities are in two parts, over 65536 keys (2^-10 of a sum that grows evenly), and a row's sum of
+    probabilities is added up in at most 2^16 steps of 2^-24 (2^-9)."""
+    page, Hkv = 256, int(heads * torch.cuda.get_device_properties(0).multi_processor_count)
+    g = torch.Generator(device=DEV).manual_seed(n + D)
+    k = torch.randn(4, Hkv, page, D, device=DEV, generator=g).bfloat16()
+    v = (1 + 0.25 * torch.randn(4, Hkv, page, D, device=DEV, generator=g)).bfloat16()
+    q = torch.randn(n, Hkv, D, device=DEV, generator=g).bfloat16()
+    table = (torch.arange(-(-(ctx + n) // page), dtype=torch.int32, device=DEV) % 4)[None].contiguous()
+    status = i32([0])
+    got = paged.attention(q, k, v, table, i32([0, n]), i32([ctx]), n, status=status)
+    assert int(status) == 0
+    kk, vv = (t.permute(1, 0, 2, 3).reshape(Hkv, 4 * page, D).double() for t in (k, v))
+    qq = q.double().transpose(0, 1)                          # [Hkv, n, D]
+    seen = ctx + 1 + torch.arange(n, device=DEV)
+    count = seen[:, None] // 1024 + (torch.arange(1024, device=DEV)[None] < seen[:, None] % 1024)
+    w = torch.softmax(qq @ kk.transpose(1, 2) * D ** -0.5 + count.double().log()[None], -1)
+    want, size = (w @ vv).transpose(0, 1), (w @ vv.abs()).transpose(0, 1)
+    reach = float((qq.abs() @ kk.abs().transpose(1, 2)).max()) * D ** -0.5
+    e = (2.0 ** -16 if n <= 8 else 2.0 ** -8) + reach * (D + 4) * 2.0 ** -23 + 2.0 ** -10 + 2.0 ** -9
+    err = (got.double() - want).abs()
+    assert bool((err <= 2.0 ** -8 * want.abs() + 2 * e * size).all()), f"largest error {float(err.max())}"
