@@ -40,7 +40,8 @@ constexpr int kRowBlockBytes = 16384;  // keys and values of a few-rows block
 // Keys that a part's results are summed over by the products alone.  The tensor cores cut each sum off towards zero
 // (measured: 2^-22 of it per 16 keys), which over a long part is a shrinkage: values of 1.0 came out as 0.996 behind
 // 2^20 keys and as 0.976 behind 2^22.  So every 2^16 keys a worker adds its results to the place of its partial
-// record, in f32 and rounded to nearest, and goes on from zero; what is lost stays under 2^-11.
+// record, in f32 and rounded to nearest, and goes on from zero; what is lost stays under 2^-11.  The sums of
+// probabilities likewise: added block by block to a sum of 2^25, equal blocks may all be rounded the same way, by 1 %.
 constexpr int kFoldKeys = 65536;
 
 // Geometry of an item: few query rows (all of a request's), or a pair of

@@ -162,15 +162,16 @@ __device__ __noinline__ void add_odd_values(const AttnParams& p, const Segment& 
 
 // Every kFold blocks of a part a row's results go from tensor memory to the place of the part's record (where the
 // part is a whole item, to the worker's second, which is still free), and at the part's end what lies there is added
-// to the rest (`last`).  `m` is the row's maximum now, `some` whether results lie there already.  A whole warp, out of
-// line: few parts are so long, and inside the loop over the blocks this cost 3 % of the long prompt's time, folding or
+// to the rest (`last`); so does its sum of probabilities, l, whose new value is returned.  `m` is the row's maximum
+// now, `some` whether results lie there already.  A whole warp, out of line: few parts are so long, and inside the loop over the blocks this cost 3 % of the long prompt's time, folding or
 // not (314 us to 323; this way 313, seven chunks of 64-wide heads 40.0 to 40.3).
 constexpr int kFold = kFoldKeys / 128;
-__device__ __noinline__ void fold_results(const AttnParams& p, int D, int slot, int row, uint32_t to, float m,
-                                          bool mine, bool some, bool last) {
-  float* at = part_ml(p, D, slot, row);  // the maximum that the results there are worth
-  const float f = mine && some ? fold_weight(*at, m) : 0.f;
-  if (mine) *at = m;
+__device__ __noinline__ float fold_results(const AttnParams& p, int D, int slot, int row, uint32_t to, float m, float l,
+                                           bool mine, bool some, bool last) {
+  float2* at = reinterpret_cast<float2*>(part_ml(p, D, slot, row));  // the maximum of what lies there, and its sum
+  const float2 there = mine && some ? *at : make_float2(m, 0.f);
+  const float f = fold_weight(there.x, m), sum = l + there.y * f;
+  if (mine) *at = make_float2(m, sum);
 #pragma unroll 1
   for (int c = 0; c < D; c += 32) {
     float o[32];
@@ -193,6 +194,7 @@ __device__ __noinline__ void fold_results(const AttnParams& p, int D, int slot, 
     tmem_st32(to + c, o);
   }
   tmem_wait_st();
+  return last ? sum : 0.f;
 }
 
 template <int D>
@@ -746,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // O is whole once the next scores are there (at D = 64, once its last product is done)
         if (!(ok = wait_phase(kApart ? &o_done[w] : &s_full[w], (kApart ? no : ns) & 1, &gave_up))) break;
         tc_fence_after();
-        fold_results(p, D, fold_slot, w * 128 + row, to, m, mine, stop > kFold, false);
+        l = fold_results(p, D, fold_slot, w * 128 + row, to, m, l, mine, stop > kFold, false);
       }
       if (!ok) break;
       blk += s.k1 - k0;
@@ -755,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++no;
         tc_fence_after();
       }
-      if (nt > kFold) fold_results(p, D, fold_slot, w * 128 + row, to, m, mine, true, true);
+      if (nt > kFold) l = fold_results(p, D, fold_slot, w * 128 + row, to, m, l, mine, true, true);
       const bool set_aside = nt > 0 && odd[sst];
       const float f = s.slot >= 0 ? 1.f : nt == 0 || l == 0.f ? 0.f : 1.0f / l;  // a row without keys is zero
       __nv_bfloat16* dst = p.out + ((int64_t)s.row0 + w * p.tq + tok_in) * p.ld_out + (int64_t)(s.g * p.G + head) * D;

@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
 
     constexpr int kFold = kFoldKeys / KU;
-    float mfold[2] = {-INFINITY, -INFINITY};  // the maxima that folded results are worth
+    float mfold[2] = {-INFINITY, -INFINITY}, lfold[2] = {0.f, 0.f};  // the maxima of folded results, and their sums
 #pragma unroll 1
     for (int stop = kb + kFold;; stop += kFold) {
       for (; ck < min(cke, stop); ++ck) {
@@ -369,6 +369,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
         float* dst = part_o(p, D, slot, r) + g;
         const float f = fold_weight(mfold[e], m[e]);
         mfold[e] = m[e];
+        lfold[e] = lfold[e] * f + l[e];
+        l[e] = last ? lfold[e] : 0.f;
 #pragma unroll
         for (int d = 0; d < D / 16; ++d)
 #pragma unroll

@@ -877,3 +877,27 @@ def test_attention_over_millions_of_keys_keeps_its_sums(heads, n, D, ctx):
     e = (2.0 ** -16 if n <= 8 else 2.0 ** -8) + reach * (D + 4) * 2.0 ** -23 + 2.0 ** -10 + 2.0 ** -9
     err = (got.double() - want).abs()
     assert bool((err <= 2.0 ** -8 * want.abs() + 2 * e * size).all()), f"largest error {float(err.max())}"
+
+
+@pytest.mark.parametrize("heads,n", [(4.0, 1), (2.7, 8)])
+def test_attention_over_millions_of_keys_keeps_its_sums_of_probabilities(heads, n):
+    """Two scores in turn, so that every block adds the same amount to a row's sum and is rounded the same way: a lane
+    of the few-rows kernel adds eight keys a block, 4 (1 + w), to a sum that reaches 2^19 (1 + w), in steps of 2^-4
+    and 2^-3; the heads' weights w put that amount anywhere between two steps.  Within the tolerance of the test
+    before, without its allowance for the sum of probabilities."""
+    D, page, ctx = 64, 256, (1 << 23) - n
+    Hkv = int(heads * torch.cuda.get_device_properties(0).multi_processor_count)
+    k = torch.zeros(1, Hkv, page, D, dtype=torch.bfloat16, device=DEV)
+    # scores 0 and -s (D^-0.5 = 2^-3): weights between 0.2 and 0.9
+    s = 8 * torch.linspace(0.1, 1.6, Hkv, device=DEV)
+    k[0, :, 1::2, 0] = -s.bfloat16()[:, None]
+    v = torch.ones_like(k)
+    v[..., 1::2] = -0.7
+    q = torch.zeros(n, Hkv, D, dtype=torch.bfloat16, device=DEV)
+    q[:, :, 0] = 1.0
+    table = torch.zeros(1, (1 << 23) // page, dtype=torch.int32, device=DEV)
+    got = paged.attention(q, k, v, table, i32([0, n]), i32([ctx]), n).double()
+    want = v[0, 0, 0].double()  # every value is the same
+    tol = (2.0 ** -8 + 2 * (2.0 ** -16 + 2 * 66 * 2.0 ** -23 + 2.0 ** -10)) * want.abs()
+    worst = (got - want).abs().amax((0, 1))
+    assert bool((worst <= tol).all()), worst.tolist()
