@@ -901,3 +901,68 @@ def test_attention_over_millions_of_keys_keeps_its_sums_of_probabilities(heads, 
     tol = (2.0 ** -8 + 2 * (2.0 ** -16 + 2 * 66 * 2.0 ** -23 + 2.0 ** -10)) * want.abs()
     worst = (got - want).abs().amax((0, 1))
     assert bool((worst <= tol).all()), worst.tolist()
+
+
+MIXED = [  # ctx, new, Hq, Hkv, D: both kernels, cut and whole items, many records and few
+    ([4096], [1], 32, 8, 128), ([0, 1000, 0, 64], [700, 33, 0, 256], 32, 4, 64), ([31, 900], [1, 1], 12, 12, 64),
+    ([2000], [64], 8, 1, 128), ([513, 100], [4, 2], 4, 2, 128), ([0], [1500], 5, 5, 128), ([5], [2], 32, 1, 64)]
+
+
+def test_attention_on_a_workspace_of_the_caller():
+    """One buffer of the largest size for calls of both kernels in turn, and one of each call's own size, both full of
+    NaN and of the call before: the same bits as without."""
+    sizes = [paged.attention_workspace(max(new), Hq, Hkv, D).numel() for _, new, Hq, Hkv, D in MIXED]
+    shared = torch.full((max(sizes),), 255, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        for i, (ctx, new, Hq, Hkv, D) in enumerate(MIXED):
+            q, k, v, table, cu = attention_case(ctx, new, Hq, Hkv, D, 32, 61 + i)
+            args = (q, k, v, table, i32(cu), i32(ctx), max(new))
+            status = i32([0])
+            want = paged.attention(*args, status=status)
+            attention_close(want, *attention_ref(q, k, v, table, cu, ctx, 32, D ** -0.5), D, is_few(new, Hq, Hkv))
+            own = torch.full((sizes[i] + 64,), 255, dtype=torch.uint8, device=DEV)
+            for ws in (shared, own[:sizes[i]]):
+                assert torch.equal(paged.attention(*args, workspace=ws, status=status), want)
+            assert torch.all(own[sizes[i]:] == 255) and int(status) == 0
+            with pytest.raises(L.MkError) as e:
+                paged.attention(*args, workspace=own[:sizes[i] - 1])
+            assert e.value.code == L.MK_ERR_LIMIT
+
+
+def test_calls_that_overlap_on_two_streams_each_with_a_workspace_of_its_own():
+    ctx, Hq, Hkv, D, page = [3000, 500], 32, 8, 128, 16
+    for new in ([1, 1], [5, 90]):
+        q, k, v, table, cu = attention_case(ctx, new, Hq, Hkv, D, page, 71)
+        qs = (q, q.flip(0).contiguous())
+        lens = i32(cu), i32(ctx)
+        wants = [paged.attention(x, k, v, table, *lens, max(new)) for x in qs]
+        spaces = [paged.attention_workspace(max(new), Hq, Hkv, D) for _ in range(2)]
+        outs = [[torch.zeros_like(q) for _ in range(20)] for _ in range(2)]
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        torch.cuda.synchronize()
+        for n in range(20):
+            for i in (0, 1):
+                paged.attention(qs[i], k, v, table, *lens, max(new), out=outs[i][n], workspace=spaces[i],
+                                stream=streams[i])
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            assert all(torch.equal(o, wants[i]) for o in outs[i])
+
+
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D", [([0, 1000, 0, 64], [700, 33, 0, 256], 32, 4, 64), ([2000], [64], 8, 1, 128),
+                                              ([40] * 300, [9] * 300, 4, 1, 128), ([0, 7], [130, 3], 4, 2, 64),
+                                              ([4096, 3], [1, 1], 8, 2, 128)])
+def test_attention_into_rows_that_are_aligned_to_16_bytes_only(ctx, new, Hq, Hkv, D):
+    """Outputs whose rows lie Hq D + 8 elements apart, or that begin 8 elements into the buffer, cut items and whole
+    ones: the same bits, and what lies between the rows stays."""
+    q, k, v, table, cu = attention_case(ctx, new, Hq, Hkv, D, 16, 81)
+    args = (q, k, v, table, i32(cu), i32(ctx), max(new))
+    want = paged.attention(*args)
+    n, row = cu[-1], Hq * D
+    for ld, first in ((row + 8, 0), (row + 16, 8), (row, 8), (row + 24, 8)):
+        buf = torch.full((n * ld + 64,), 5.0, dtype=torch.bfloat16, device=DEV)
+        out = buf.as_strided((n, Hq, D), (ld, D, 1), first)
+        paged.attention(*args, out=out)
+        assert torch.equal(out, want)
+        out.fill_(5.0)
+        assert torch.all(buf == 5.0)
