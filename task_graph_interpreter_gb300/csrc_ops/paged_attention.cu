@@ -121,6 +121,9 @@ extern "C" int mk_paged_attention(void* stream_, int B, int N, int max_new, int 
   p.workers = few ? sms * kRowWarps : sms;
   p.rows = few ? max_new * G : kTileRows;
   p.tq = few ? 0 : 128 / G;
+  // The chunk kernel's softmax of a tile without tokens, and its warp for masked values, wait while a part's other
+  // blocks go by: 65536 blocks of 128 keys take 48 ms and more.
+  p.wait_limit = 1 + (int)((int64_t)max_pages * page_size >> 23);
 
   // pools as [rows, D], pages one after the other; a box is what one page gives a block of keys
   CUtensorMap kmap, vmap, qmap;

@@ -33,6 +33,7 @@ struct AttnParams {
   int workers;
   int rows;         // rows of a partial record
   int tq;           // tokens per query tile (chunks): 128 / G
+  int wait_limit;   // seconds that a wait may take: a part of the longest request
 };
 
 constexpr int kRowBlockBytes = 16384;  // keys and values of a few-rows block
@@ -255,15 +256,22 @@ __device__ __forceinline__ Note* note_of(const AttnParams& p, int D, int w) {
 // What results folded at the maximum `at` are worth at the maximum `m` (both -inf: nothing was seen, and they are 0).
 __device__ __forceinline__ float fold_weight(float at, float m) { return at == m ? 1.f : ptx::ex2(at - m); }
 
-// Wait for a phase of an mbarrier, at most about a second, or until another
-// thread has given up.
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort) {
+// Wait for a phase of an mbarrier, at most `limit` seconds or so, or until another thread has given up.
+struct Patience {
+  int gave_up;  // a wait has run out
+  int limit;
+};
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile Patience* state) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
-  const uint32_t t0 = (uint32_t)clock();
+  uint32_t t0 = (uint32_t)clock();
+  int left = state->limit;
 #pragma unroll 1
   while (!ptx::mbar_try_wait(bar, parity)) {
-    if (*abort) return false;
-    if ((uint32_t)clock() - t0 > 2000000000u) *abort = 1;
+    if (state->gave_up) return false;
+    if ((uint32_t)clock() - t0 > 2000000000u) {
+      if (--left <= 0) state->gave_up = 1;
+      t0 = (uint32_t)clock();
+    }
   }
   return true;
 }

@@ -104,7 +104,7 @@ struct Control {
   int odd[kSegRing];      // a value set aside in this part
   uint32_t missing[8];    // per key block (ring): pages of it that are not in the pool, one bit each
   uint32_t tmem;
-  int gave_up;
+  Patience patience;
 };
 static_assert(sizeof(Control) <= Smem<128>::kControl, "control block");
 
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto& segs = ctl.segs;
   auto& odd = ctl.odd;
   auto& missing = ctl.missing;
-  int& gave_up = ctl.gave_up;
+  auto& patience = ctl.patience;
   uint8_t* qt = smem_raw + S::kControl;  // [2][NH][128 rows][128 B]
   uint8_t* ring = qt + 2 * S::kTile;     // [kStages][NH][128 keys][128 B]
   // (broadcast, so that the compiler knows a warp's role and what follows from it uniform)
@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   if (threadIdx.x == 0) {
-    gave_up = 0;
+    patience.gave_up = 0;
+    patience.limit = p.wait_limit;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], 2);
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (k0 < k1) break;
           }
           const int st = made % kSegRing;
-          if (!wait_phase(&seg_empty[st], ((made / kSegRing) & 1) ^ 1, &gave_up)) break;
+          if (!wait_phase(&seg_empty[st], ((made / kSegRing) & 1) ^ 1, &patience)) break;
           if (lane == 0) {
             Segment& s = segs[st];
             s.valid = more ? 1 : 0;
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = max(k0, from >> 7); k < k1; ++k) {
           const uint32_t vit = it + 2 * (k - k0) + 1;
           const int st = vit % kStages;
-          if (!(ok = wait_phase(&v_raw[st], (raw_phase >> st) & 1, &gave_up))) break;
+          if (!(ok = wait_phase(&v_raw[st], (raw_phase >> st) & 1, &patience))) break;
           raw_phase ^= 1u << st;
           const uint32_t v0 = r0 + st * S::kTile;
           const int first = max(0, from - k * 128), valid = min(128, to - k * 128);
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const auto load_q = [&](const Segment& s) {
 #pragma unroll 1
         for (int w = 0; w < 2; ++w) {
-          if (!wait_phase(&q_empty[w], (nq & 1) ^ 1, &gave_up)) return false;
+          if (!wait_phase(&q_empty[w], (nq & 1) ^ 1, &patience)) return false;
           if (lane == 0) {
             // (a second tile without tokens is not read)
             const bool some = w == 0 || s.t0 + p.tq < s.n;
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (uint32_t i = 0;; ++i) {
         const int sst = i % kSegRing;
-        if (!wait_phase(&seg_full[sst], (i / kSegRing) & 1, &gave_up)) break;
+        if (!wait_phase(&seg_full[sst], (i / kSegRing) & 1, &patience)) break;
         const Segment s = segs[sst];
         __syncwarp();
         if (lane == 0) mbar_arrive(&seg_empty[sst]);
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int v = 0; v < 2; ++v, ++it) {
             const int st = it % kStages;
-            if (!(ok = wait_phase(&kv_empty[st], ((it / kStages) & 1) ^ 1, &gave_up))) break;
+            if (!(ok = wait_phase(&kv_empty[st], ((it / kStages) & 1) ^ 1, &patience))) break;
             // values of a masked block go by warp 10, which passes them on as full; those of other
             // blocks with a missing page by this warp
             const bool raw = v == 1 && k >= jd, holes = v == 1 && k < jd && miss;
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           bar);
             if (holes) {
               hole = 1;
-              if (!(ok = wait_phase(&m_bar, misses & 1, &gave_up))) break;
+              if (!(ok = wait_phase(&m_bar, misses & 1, &patience))) break;
               ++misses;
               hole = 0;
               zero_values<D>(smem_addr(ring) + st * S::kTile, 128, miss, p.page_shift, lane);
@@ -463,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
       }
-      if (*(volatile int*)&gave_up) {
+      if (*(volatile int*)&patience.gave_up) {
         if (lane == 0) set_status(p.status, MK_DEV_RING_TIMEOUT);
         // copies in flight land before the shared memory goes
         for (uint32_t d = it > kStages ? it - kStages : 0; d < it; ++d) {
@@ -487,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // took 70 to 100 cycles to issue, the tensor cores 64 to execute).
       const int w = warp == 9 ? 0 : 1;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, wait_phase(bar, parity, &gave_up)) != 0;
+        return __all_sync(0xffffffffu, wait_phase(bar, parity, &patience)) != 0;
       };
       const uint32_t idesc_s = idesc_bf16_f32(128, 128);
       const uint32_t idesc_o = idesc_bf16_f32(128, D) | kIdescBMnMajor;
@@ -620,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (*(volatile int*)&gave_up) {
+      if (*(volatile int*)&patience.gave_up) {
         // products in flight end before the tensor memory is freed
         if (elect_one()) tc_commit(&drained[w]);
         __syncwarp();
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ns = 0, no = 0, blk = 0;
     for (uint32_t i = 0;; ++i) {
       const int sst = i % kSegRing;
-      if (!wait_phase(&seg_full[sst], (i / kSegRing) & 1, &gave_up)) break;
+      if (!wait_phase(&seg_full[sst], (i / kSegRing) & 1, &patience)) break;
       const Segment& s = segs[sst];
       if (!s.valid) break;
       const int k0 = s.k0, nt = s.end[w] - k0;
@@ -653,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int j = 0, stop = kFold; ok; stop += kFold) {
         for (; j < min(nt, stop); ++j) {
-          if (!(ok = wait_phase(&s_full[w], ns & 1, &gave_up))) break;
+          if (!(ok = wait_phase(&s_full[w], ns & 1, &patience))) break;
           ++ns;
           tc_fence_after();
           const uint32_t miss = missing[(blk + j) & 7];
@@ -699,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = top;
           } else {
             if constexpr (kApart) {  // the last block's product has read P, and O is whole
-              if (!(ok = wait_phase(&o_done[w], no & 1, &gave_up))) break;
+              if (!(ok = wait_phase(&o_done[w], no & 1, &patience))) break;
               ++no;
               tc_fence_after();
             }
@@ -746,14 +747,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok || j >= nt) break;
         // O is whole once the next scores are there (at D = 64, once its last product is done)
-        if (!(ok = wait_phase(kApart ? &o_done[w] : &s_full[w], (kApart ? no : ns) & 1, &gave_up))) break;
+        if (!(ok = wait_phase(kApart ? &o_done[w] : &s_full[w], (kApart ? no : ns) & 1, &patience))) break;
         tc_fence_after();
         l = fold_results(p, D, fold_slot, w * 128 + row, to, m, l, mine, stop > kFold, false);
       }
       if (!ok) break;
       blk += s.k1 - k0;
       if (nt > 0) {
-        if (!wait_phase(&o_done[w], no & 1, &gave_up)) break;
+        if (!wait_phase(&o_done[w], no & 1, &patience)) break;
         ++no;
         tc_fence_after();
       }

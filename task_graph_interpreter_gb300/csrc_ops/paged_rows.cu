@@ -63,13 +63,14 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kRowWarps][kStages];
   __shared__ uint64_t live[kRowWarps][kStages];  // keys of a block that were loaded
-  __shared__ int gave_up;
+  __shared__ Patience patience;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* ring = base + warp * kStages * kStageBytes;
   const uint32_t qs = smem_addr(base + kRowWarps * kStages * kStageBytes + warp * kMaxFewRows * D * 2);
   if (threadIdx.x == 0) {
-    gave_up = 0;
+    patience.gave_up = 0;
+    patience.limit = 1;  // (a block's copies)
     for (int i = 0; i < kRowWarps; ++i)
       for (int j = 0; j < kStages; ++j) mbar_init(&full[i][j], 1);
     fence_mbar_init();
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     for (int stop = kb + kFold;; stop += kFold) {
       for (; ck < min(cke, stop); ++ck) {
         const int st = done % kStages;
-        if (!wait_phase(&full[warp][st], (done / kStages) & 1, &gave_up)) {
+        if (!wait_phase(&full[warp][st], (done / kStages) & 1, &patience)) {
           if (lane == 0) set_status(p.status, MK_DEV_RING_TIMEOUT);
           // the copies in flight land in this CTA's memory: give them time before it goes
           for (uint32_t d = done; d < issued; ++d)

@@ -966,3 +966,24 @@ def test_attention_into_rows_that_are_aligned_to_16_bytes_only(ctx, new, Hq, Hkv
         assert torch.equal(out, want)
         out.fill_(5.0)
         assert torch.all(buf == 5.0)
+
+
+def test_a_part_that_takes_longer_than_a_second_is_waited_for():
+    """2^28 keys of one head for nine tokens: the kernel's warps for masked values and for the empty second tile wait
+    from the part's first block to its last, some 1.5 s.  All keys are the same, so the result is their value."""
+    D, page, n = 64, 256, 9
+    Hkv, ctx = torch.cuda.get_device_properties(0).multi_processor_count, (1 << 28) - 9
+    g = torch.Generator(device=DEV).manual_seed(91)
+    k = torch.randn(1, Hkv, 1, D, device=DEV, generator=g).bfloat16().expand(1, Hkv, page, D).contiguous()
+    v = torch.randn(1, Hkv, 1, D, device=DEV, generator=g).bfloat16().expand(1, Hkv, page, D).contiguous()
+    q = torch.randn(n, Hkv, D, device=DEV, generator=g).bfloat16()
+    table = torch.zeros(1, (1 << 28) // page, dtype=torch.int32, device=DEV)
+    status = i32([0])
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    got = paged.attention(q, k, v, table, i32([0, n]), i32([ctx]), n, status=status)
+    end.record()
+    assert int(status) == 0 and start.elapsed_time(end) > 1200.0
+    want = v[0, :, 0].double()
+    # equal probabilities round alike and cancel; the products' sums lose 2^-11 (see above), the result 2^-8
+    assert bool(((got.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -10) * want.abs()).all())
