@@ -465,6 +465,8 @@ int mk_attention_decode_noalloc(void* stream, const float* qkv, void* kcache, vo
  *  - Lengths, tables and maps are read on the GPU.  What they hold is checked
  *    there: `status` (int32 on the device, NULL for none, zeroed by the
  *    caller) receives the first MK_DEV_* code; the library does not clear it.
+ *    It is the only word of such a fault: without it, rows that were not
+ *    written look like any others.
  *  - Pointers to float, bf16 and workspace memory must be 16-byte aligned.
  *    All tensors belong to the caller and live on the current device.
  *  - Every call can be captured into a CUDA graph.
@@ -489,6 +491,10 @@ int mk_attention_decode_noalloc(void* stream, const float* qkv, void* kcache, vo
  * max_tokens new tokens, not enough free pages): then nothing moves, cu is
  * all 0 and positions and slots are all -1.  A page id outside the pool, from
  * the stack or a table, gives slot -1 and MK_DEV_BAD_INDEX.
+ * Each page has one holder: one that two requests list within their held
+ * counts (a shared prefix) goes on the stack once for each that gives it back,
+ * and is then handed out twice.  Attention reads shared pages, but whoever
+ * shares them takes care of the tables without this operator.
  * 1 <= B <= 4096; num_pages is also the length of free_pages. */
 int mk_paged_plan(void* stream, int B, int page_size, int max_pages, int num_pages, int max_tokens,
                   const int32_t* ctx_len, const int32_t* new_len, int32_t* table, const int32_t* held,
@@ -523,12 +529,20 @@ int mk_qk_norm_rope(void* stream, int N, int Hq, int Hkv, int D, const void* qkv
  *  at most 8 the kernel for single tokens runs, else the one for chunks.
  *  workspace: mk_paged_attention_workspace bytes for the same max_new, heads
  *  and D, for partial results; calls that share it must not overlap.
+ * Scores, maxima, sums and results are f32.  Probabilities enter the second
+ * product in two bf16 parts (to 2^-16) in the kernel for single tokens, and
+ * rounded to bf16 (to 2^-8) in the one for chunks: relative errors of 1.7e-3
+ * and 2.1e-3 to 2.4e-3 with the result's own rounding.  max_new chooses for the
+ * whole call, so a single token beside a prompt is computed as the prompt is;
+ * tokens that are to keep the closer form get a call of their own.
  * Rows of no request (before cu[0], behind cu[B]) stay as they are.  Keys of
  * a page id outside the pool are left out (MK_DEV_BAD_INDEX), and a row
  * without any key is zero.  Cache memory behind a request's last key may
  * hold anything.  Lengths that do not fit (cu decreasing or past N, a request
  * over max_new or max_pages, a negative length) give MK_DEV_BAD_INDEX and
- * nothing is written.  D 64 or 128, Hq / Hkv <= 128, num_pages * Hkv *
+ * nothing is written.  A wait on the device that runs out (a second, and one
+ * more for every 2^23 of max_pages * page_size) gives MK_DEV_RING_TIMEOUT and
+ * leaves rows unwritten.  D 64 or 128, Hq / Hkv <= 128, num_pages * Hkv *
  * page_size < 2^31, max_pages * page_size <= 2^31 - 256.  q may not overlap
  * out. */
 int mk_paged_attention(void* stream, int B, int N, int max_new, int Hq, int Hkv, int D, const void* q, int64_t ld_q,
@@ -553,6 +567,7 @@ int mk_paged_attention_workspace(int max_new, int Hq, int Hkv, int D, size_t* by
  *  is -1.
  *  tokens int32 [B, K + 1]: the accepted drafts, the drawn token, then -1.
  *  accepted int32 [B]: the number of accepted drafts.
+ *  tokens and accepted may not overlap the inputs.
  * A draft outside [0, V) ends the drafts there and gives MK_DEV_BAD_INDEX.
  * 0 <= K <= 1024. */
 int mk_verify_drafts(void* stream, int B, int K, int V, const float* p, int64_t ld_p, const float* q, int64_t ld_q,

@@ -13,7 +13,8 @@ through with them.  Tensors that do not fit raise ValueError, what the
 library refuses MkError (the checks are in csrc_ops/calls.cpp).  Lengths,
 tables and maps are int32 tensors that the GPU reads; what is wrong with
 their values is reported in ``status`` (an int32 device tensor, zeroed by the
-caller, that receives the first MK_DEV_* code).  They serve inference: a tensor
+caller, that receives the first MK_DEV_* code) and nowhere else: without one,
+rows that a wrong length left unwritten look like any others.  They serve inference: a tensor
 that requires a gradient is refused outside ``torch.no_grad()``, one that
 carries a forward-mode tangent altogether.  ``PagedCache``
 holds a cache's pools, tables and free pages and runs the operators on them.
@@ -56,7 +57,8 @@ def plan(ctx_len, new_len, table, held, free_pages, free_count, page_size: int, 
     listed in table[b]; pages it no longer needs go back on the stack
     free_pages[:free_count], then missing ones come from its top.  ``held``
     and ``free_count`` are updated in place unless ``held_out`` and
-    ``count_out`` are given.  ``positions`` and ``slots`` (or ``max_tokens``)
+    ``count_out`` are given.  A page has one holder: one that two requests
+    hold would go back on the stack twice.  ``positions`` and ``slots`` (or ``max_tokens``)
     set how many new tokens the step can have."""
     args = (ctx_len, new_len, table, held, held_out, free_pages, free_count, count_out, page_size, cu, positions,
             slots, max_tokens, status)
@@ -69,7 +71,7 @@ def qk_norm_rope(qkv, Hq: int, Hkv: int, D: int, positions, slots, kpool, vpool,
     None), the rotate-half rotary embedding at ``positions``, and the stores
     of keys and values at ``slots`` (mk_qk_norm_rope).  qkv f32 or bf16
     [N, (Hq + 2 Hkv) D], rows may lie apart; returns the queries, bf16
-    [N, Hq, D] (``out`` if given).  Rows with a negative position are left
+    [N, Hq, D] (``out`` if given, which may not overlap qkv).  Rows with a negative position are left
     out; ``out`` keeps what it had there (a fresh one holds anything)."""
     args = (qkv, Hq, Hkv, D, positions, slots, kpool, vpool, q_gamma, k_gamma, eps, rope_theta, out, status)
     return L.calls().qk_norm_rope(*args) if stream is None else on_stream(L.calls().qk_norm_rope, stream, args)
@@ -90,7 +92,13 @@ def attention(q, kpool, vpool, table, cu, ctx_len, max_new: int, *, scale: float
     positions 0 .. ctx_len[b] + t of the pages table[b]; no request has more
     than ``max_new`` new tokens.  Returns ``out`` bf16 [N, Hq, D]; rows of no
     request keep what it had (a fresh one holds anything).  Without a
-    ``workspace`` one is taken from PyTorch's allocator for the call."""
+    ``workspace`` one is taken from PyTorch's allocator for the call.
+    ``out`` may not overlap q.
+
+    With max_new Hq / Hkv <= 8 probabilities keep 2^-16, beyond it they are
+    rounded to bf16 (results off by 1.7e-3 and 2.1e-3 to 2.4e-3, their own
+    rounding included).  That goes for the whole call: a single token beside
+    a prompt is computed as the prompt is, unless it has a call of its own."""
     args = (q, kpool, vpool, table, cu, ctx_len, max_new, scale, out, workspace, status)
     return L.calls().attention(*args) if stream is None else on_stream(L.calls().attention, stream, args)
 
@@ -100,7 +108,10 @@ class PagedCache:
     requests and ``max_tokens`` new tokens a step.  Per step: ``plan`` with
     the requests' lengths, then per layer ``append`` (norms, rotation, page
     stores) and ``attention``.  A request that ends, or whose drafts were
-    rejected, gives its pages back through the next plan's lengths."""
+    rejected, gives its pages back through the next plan's lengths.  No two
+    requests may hold the same page.  ``check`` tells of lengths that did not
+    fit.  The cache is made on the current stream, and its steps follow one
+    another: the caller orders a step on another stream behind both."""
 
     def __init__(self, layers: int, num_pages: int, page_size: int, Hkv: int, D: int, max_requests: int,
                  max_pages: int, max_tokens: int, device="cuda"):
