@@ -987,3 +987,28 @@ def test_a_part_that_takes_longer_than_a_second_is_waited_for():
     want = v[0, :, 0].double()
     # equal probabilities round alike and cancel; the products' sums lose 2^-11 (see above), the result 2^-8
     assert bool(((got.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -10) * want.abs()).all())
+
+
+@pytest.mark.parametrize("heads,n,D,lost", [(1.0, 9, 128, 300), (0.67, 40, 64, 600), (4.0, 1, 64, 300), (2.7, 3, 128, 520)])
+def test_long_parts_whose_first_pages_are_missing(heads, n, D, lost):
+    """Folded results of rows that had seen no key yet count for nothing, whole items and cut ones."""
+    page, Hkv, ctx = 256, int(heads * torch.cuda.get_device_properties(0).multi_processor_count), 200000
+    g = torch.Generator(device=DEV).manual_seed(lost)
+    k, v = (torch.randn(4, Hkv, page, D, device=DEV, generator=g).bfloat16() for _ in range(2))
+    q = torch.randn(n, Hkv, D, device=DEV, generator=g).bfloat16()
+    pages = torch.arange(-(-(ctx + n) // page), dtype=torch.int32, device=DEV)
+    table = torch.where(pages < lost, -1, pages % 4)[None].contiguous()
+    status = i32([0])
+    got = paged.attention(q, k, v, table, i32([0, n]), i32([ctx]), n, status=status)
+    assert int(status) == L.MK_DEV_BAD_INDEX
+    kk, vv = (t.permute(1, 0, 2, 3).reshape(Hkv, 4 * page, D).double() for t in (k, v))
+    at = torch.arange(1024, device=DEV)[None]
+    upto = lambda m: m // 1024 + (at < m % 1024)  # noqa: E731  (keys among the first m, each page as it comes)
+    count = upto((ctx + 1 + torch.arange(n, device=DEV))[:, None]) - upto(torch.tensor([[lost * page]], device=DEV))
+    s = q.double().transpose(0, 1) @ kk.transpose(1, 2) * D ** -0.5
+    w = torch.softmax(s + count.double().log()[None], -1)
+    reach = float((q.double().abs().transpose(0, 1) @ kk.abs().transpose(1, 2)).max()) * D ** -0.5
+    want, size = (w @ vv).transpose(0, 1), (w @ vv.abs()).transpose(0, 1)
+    # as for shorter contexts, and 2^-10 for what the products' sums lose over 65536 keys
+    e = (2.0 ** -16 if n <= 8 else 2.0 ** -8) + reach * (D + 4) * 2.0 ** -23 + 2.0 ** -10
+    assert bool(((got.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2 * e * size).all())
