@@ -50,7 +50,10 @@ constexpr int kFoldKeys = 65536;
 template <int D, bool CHUNK>
 struct Geometry {
   static constexpr int kKeys = CHUNK ? 128 : kRowBlockBytes / D / 4;  // keys per block
-  static constexpr int kFixed = CHUNK ? 320 : 96;           // an item's fixed cost, in keys
+  // an item's fixed cost, in keys: measured for few rows (paged_rows.cu); for chunks what surrounds a part's
+  // blocks, some 2 us at 1.1 us for 128 keys of both tiles (256, 288 and 384 took the same time within noise, on
+  // seven ragged chunks)
+  static constexpr int kFixed = CHUNK ? 320 : 96;
 };
 
 struct Seq {

@@ -26,11 +26,12 @@
 //
 // What bounds it at D = 128: the products, 1025 cycles per tile and block (16
 // instructions of 64 cycles), 2050 for both tiles; an 8192-token prompt of 32
-// heads takes 2300 per block and 310 us in all (1.77 PFLOP/s of causal
-// arithmetic; 350 us once the card is at its power limit, at 1650 MHz).  A tile's chain is S, its softmax (128 powers per row at 4.4
-// cycles of the SM's quarter, the maximum, two transfers: 1250 cycles), P V and
-// the next S; it fits beside the other tile's products only because the
-// second product starts on half of P and hand-overs are few:
+// heads takes 2300 per block and 314 us in all (1.75 PFLOP/s of causal
+// arithmetic; 350 us once the card is at its power limit, at 1650 MHz).  A
+// tile's chain is S, its softmax (128 powers per row at 4.4 cycles of the SM's
+// quarter, the maximum, two transfers: 1250 cycles), P V and the next S; it
+// fits beside the other tile's products only because the second product starts
+// on half of P and hand-overs are few:
 //  - each tile's products have a warp of their own (waits, instructions and
 //    commits of a block take one some 1300 cycles), and the two pass a token:
 //    instructions of both tiles mixed in the queue finish together, after which

@@ -17,10 +17,10 @@
 // 64 requests of 512 to 8192 keys and four rows 199 us there, 178 us here),
 // so this one has a single eight.  Four warps with three blocks of 16 KB each:
 // 183 us for those 64 requests; six with two 187, twelve with two of 8 KB 189,
-// eight with three of 8 KB 193.  Since then 171 (6.5 TB/s at a copy's 6.8),
+// eight with three of 8 KB 193.  Since then 179 (6.5 TB/s at a copy's 6.8),
 // with the next item's query rows read ahead and an item's fixed cost in the
 // division at 96 keys (256 requests of 500 keys: 71 us with 64 and the rows not
-// read ahead, 63 now; with 128 keys 65, with 160 67).
+// read ahead, 63 after; with 128 keys 65, with 160 67).
 //
 //   s = q k^T scale;  m' = max(m, max s);  p = 2^(s - m');
 //   l = l 2^(m - m') + sum p;  o = o 2^(m - m') + p v

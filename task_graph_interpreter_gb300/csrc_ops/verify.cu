@@ -324,7 +324,8 @@ extern "C" int mk_verify_drafts(void* stream, int B, int K, int V, const float* 
   v.vec = aligned16(p) && ld_p % 4 == 0 && (!q || (aligned16(q) && ld_q % 4 == 0));
   // as many CTAs per request as still give every warp a few 128-entry steps,
   // fewer once two CTAs per SM are there (64 requests of 128256 entries: 3, 4,
-  // 6, 8 CTAs each took 16.6, 14.3, 14.9 and 17.6 us; one request 8.8 us with 8)
+  // 6, 8 CTAs each took 16.6, 14.3, 14.9 and 17.6 us, one request 8.8 us with 8;
+  // in a graph, with the rows in the L2: on changing rows the 64 take 20 us)
   int ctas = kVerifyMaxCtas;
   while (ctas > 1 && ((int64_t)V < (int64_t)ctas * kVerifyWarps * 256 || (int64_t)B * ctas > 2 * (int64_t)sms)) ctas /= 2;
   v.ctas = ctas;
