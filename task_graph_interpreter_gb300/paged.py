@@ -9,15 +9,17 @@ nothing synchronises.  With ``stream`` they behave as under
 made the inputs, and other streams behind it before they use the results; fresh
 results are its memory.  Tensors that the caller passes may be dropped as soon
 as the call returns: their memory is not given out again before ``stream`` is
-through with them.  Tensors that do not fit raise ValueError, what the
-library refuses MkError (the checks are in csrc_ops/calls.cpp).  Lengths,
-tables and maps are int32 tensors that the GPU reads; what is wrong with
-their values is reported in ``status`` (an int32 device tensor, zeroed by the
-caller, that receives the first MK_DEV_* code) and nowhere else: without one,
-rows that a wrong length left unwritten look like any others.  They serve inference: a tensor
-that requires a gradient is refused outside ``torch.no_grad()``, one that
-carries a forward-mode tangent altogether.  ``PagedCache``
-holds a cache's pools, tables and free pages and runs the operators on them.
+through with them.  Tensors that do not fit raise ValueError, what the library
+refuses MkError (the checks are in csrc_ops/calls.cpp).
+
+Lengths, tables and maps are int32 tensors that the GPU reads; what is wrong
+with their values is reported in ``status`` (an int32 device tensor, zeroed by
+the caller, that receives the first MK_DEV_* code) and nowhere else: without
+one, rows that a wrong length left unwritten look like any others.  The
+operators serve inference: a tensor that requires a gradient is refused outside
+``torch.no_grad()``, one that carries a forward-mode tangent altogether.
+``PagedCache`` holds a cache's pools, tables and free pages and runs the
+operators on them.
 """
 from __future__ import annotations
 
@@ -58,8 +60,8 @@ def plan(ctx_len, new_len, table, held, free_pages, free_count, page_size: int, 
     free_pages[:free_count], then missing ones come from its top.  ``held``
     and ``free_count`` are updated in place unless ``held_out`` and
     ``count_out`` are given.  A page has one holder: one that two requests
-    hold would go back on the stack twice.  ``positions`` and ``slots`` (or ``max_tokens``)
-    set how many new tokens the step can have."""
+    hold would go back on the stack twice.  ``positions`` and ``slots`` (or
+    ``max_tokens``) set how many new tokens the step can have."""
     args = (ctx_len, new_len, table, held, held_out, free_pages, free_count, count_out, page_size, cu, positions,
             slots, max_tokens, status)
     return Plan._make(L.calls().plan(*args) if stream is None else on_stream(L.calls().plan, stream, args))
@@ -71,8 +73,9 @@ def qk_norm_rope(qkv, Hq: int, Hkv: int, D: int, positions, slots, kpool, vpool,
     None), the rotate-half rotary embedding at ``positions``, and the stores
     of keys and values at ``slots`` (mk_qk_norm_rope).  qkv f32 or bf16
     [N, (Hq + 2 Hkv) D], rows may lie apart; returns the queries, bf16
-    [N, Hq, D] (``out`` if given, which may not overlap qkv).  Rows with a negative position are left
-    out; ``out`` keeps what it had there (a fresh one holds anything)."""
+    [N, Hq, D] (``out`` if given, which may not overlap qkv).  Rows with a
+    negative position are left out; ``out`` keeps what it had there (a fresh
+    one holds anything)."""
     args = (qkv, Hq, Hkv, D, positions, slots, kpool, vpool, q_gamma, k_gamma, eps, rope_theta, out, status)
     return L.calls().qk_norm_rope(*args) if stream is None else on_stream(L.calls().qk_norm_rope, stream, args)
 
