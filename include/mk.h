@@ -456,7 +456,9 @@ int mk_attention_decode_noalloc(void* stream, const float* qkv, void* kcache, vo
  * and keep nothing between calls.  No counterpart on the pages: they serve a
  * loop that holds its KV cache in pages and whose requests change from step
  * to step.  One step is mk_paged_plan, per layer mk_qk_norm_rope and
- * mk_paged_attention, and mk_verify_drafts where the new tokens were drafts.
+ * mk_paged_attention (or their forms for a cache in 8 bits), mk_verify_drafts
+ * where the new tokens were drafts, and mk_token_logprobs for what is answered
+ * beside the tokens.
  *
  *  - A pool holds a layer's keys or values: bf16 [num_pages, Hkv, page_size,
  *    D], page_size 16, 32, 64, 128 or 256.  Row s of the block table int32
@@ -553,6 +555,38 @@ int mk_paged_attention(void* stream, int B, int N, int max_new, int Hq, int Hkv,
 /* Bytes of workspace mk_paged_attention needs on the current device. */
 int mk_paged_attention_workspace(int max_new, int Hq, int Hkv, int D, size_t* bytes);
 
+/* The same two operators on a cache in 8 bits: pools are e4m3 [num_pages, Hkv,
+ * page_size, D], and kscale, vscale f32 [num_pages, Hkv] hold the scale of each
+ * page and head; a cached value is its code times that scale.
+ *
+ * Stores: with x the page's new values, each finite one counted, s is the smallest
+ * power of two (2^-126 at least) with max |x| <= 448 s.  A page whose first token
+ * (offset 0) is among the new ones gets the scale s; a page that is begun keeps its
+ * scale if that is at least s, else what it holds at offsets below its last new one
+ * is rounded to s.  x / scale is rounded to e4m3, to nearest; a value that is not
+ * finite is stored as NaN.  The new tokens of a page are to be in ascending order in
+ * rows that follow one another (as mk_paged_plan makes them), with at most 15 rows
+ * between them that are not stored; a row that comes back to its predecessor's page
+ * at no higher offset is not stored, nor what follows it there (MK_DEV_BAD_INDEX).
+ * The rows of a call that go to a page are to be of one such run.  Queries, norms
+ * and rotation as in mk_qk_norm_rope. */
+int mk_qk_norm_rope_e4m3(void* stream, int N, int Hq, int Hkv, int D, const void* qkv, int qkv_dtype, int64_t ld_qkv,
+                         const void* q_gamma, const void* k_gamma, float eps, double rope_theta,
+                         const int32_t* positions, const int32_t* slots, void* q_out, int64_t ld_q, void* kpool,
+                         void* vpool, float* kscale, float* vscale, int num_pages, int page_size, int32_t* status);
+
+/* Attention: arguments, workspace, checks and status of mk_paged_attention.  Scales
+ * are positive and finite.  Queries keep 2^-18 of a row's largest element and more.
+ * Probabilities are rounded to f16 (2^-11) in both kernels, maxima, sums and results
+ * are f32.  Keys' scales are f32 factors of the scores.  Values' scales are exact
+ * where they are powers of two (what the stores write) within 2^15 of each other;
+ * others are rounded to f16 in the kernel for chunks. */
+int mk_paged_attention_e4m3(void* stream, int B, int N, int max_new, int Hq, int Hkv, int D, const void* q,
+                            int64_t ld_q, const void* kpool, const void* vpool, const float* kscale,
+                            const float* vscale, int num_pages, int page_size, const int32_t* table, int max_pages,
+                            const int32_t* cu, const int32_t* ctx_len, float scale, void* out, int64_t ld_out,
+                            void* workspace, size_t workspace_size, int32_t* status);
+
 /* Verification of drafted tokens from given random numbers (speculative
  * sampling).  Per request, K drafts (draft_len[b] of them; NULL: all K):
  *  p f32, B (K + 1) rows ld_p elements apart: the target's probabilities
@@ -573,6 +607,23 @@ int mk_paged_attention_workspace(int max_new, int Hq, int Hkv, int D, size_t* by
 int mk_verify_drafts(void* stream, int B, int K, int V, const float* p, int64_t ld_p, const float* q, int64_t ld_q,
                      const int32_t* drafts, const int32_t* draft_len, const float* u, int32_t* tokens,
                      int32_t* accepted, int32_t* status);
+
+/* Log probabilities of given tokens, with the entropy and the likeliest
+ * alternatives, from N rows of V logits, f32 or bf16 (logits_dtype MK_F32 / MK_BF16),
+ * ld elements apart, at any alignment of their type.  With lse = ln sum exp x:
+ *  logprobs f32 [N]: x[tokens[i]] - lse (tokens int32 [N]; NULL: no tokens, and
+ *  logprobs is not used).  entropy f32 [N]: lse - sum p x, in nats.
+ *  top_ids int32, top_logprobs f32 [N, top]: the largest logits in descending order,
+ *  of equal ones the lower index first, and their log probabilities.
+ * Logits of -inf have no probability (-inf among the alternatives).  A row with a NaN
+ * or +inf, or without a finite logit, has NaN probabilities and entropy; NaN is no
+ * alternative (id -1 where a row has too few others).
+ * A row with a negative token is left out: its results stay as they were.  A token of
+ * V or more gets NaN and gives MK_DEV_BAD_INDEX.
+ * 1 <= V < 2^30, 0 <= top <= min(32, V).  The results may not overlap the inputs. */
+int mk_token_logprobs(void* stream, int N, int V, const void* logits, int logits_dtype, int64_t ld,
+                      const int32_t* tokens, int top, float* logprobs, float* entropy, int32_t* top_ids,
+                      float* top_logprobs, int32_t* status);
 
 /* Release everything the library allocated.  Safe on NULL. */
 void mk_destroy(mk_graph* g);

@@ -106,6 +106,14 @@ def lib():
                                                                   c_void_p, c_int, c_void_p, c_void_p, c_float,
                                                                   c_void_p, c_int64, c_void_p, c_size_t, c_void_p]),
         "mk_paged_attention_workspace": (c_int, [c_int, c_int, c_int, c_int, POINTER(c_size_t)]),
+        "mk_qk_norm_rope_e4m3": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_int, c_int64, c_void_p,
+                                         c_void_p, c_float, c_double, c_void_p, c_void_p, c_void_p, c_int64, c_void_p,
+                                         c_void_p, c_void_p, c_void_p, c_int, c_int, c_void_p]),
+        "mk_paged_attention_e4m3": (c_int, [c_void_p] + [c_int] * 6 + [c_void_p, c_int64] + [c_void_p] * 4 +
+                                    [c_int, c_int, c_void_p, c_int, c_void_p, c_void_p, c_float, c_void_p, c_int64,
+                                     c_void_p, c_size_t, c_void_p]),
+        "mk_token_logprobs": (c_int, [c_void_p, c_int, c_int, c_void_p, c_int, c_int64, c_void_p, c_int] +
+                              [c_void_p] * 5),
         "mk_verify_drafts": (c_int, [c_void_p, c_int, c_int, c_int, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
                                      c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
         "mk_last_error": (c_char_p, []),
@@ -143,7 +151,8 @@ def calls():
     loader.exec_module(m)
     m.bind(MkError, *[ctypes.cast(getattr(L, f), c_void_p).value for f in
                       ("mk_paged_plan", "mk_qk_norm_rope", "mk_paged_attention", "mk_paged_attention_workspace",
-                       "mk_verify_drafts", "mk_last_error")])
+                       "mk_verify_drafts", "mk_last_error", "mk_qk_norm_rope_e4m3", "mk_paged_attention_e4m3",
+                       "mk_token_logprobs")])
     _calls = m
     return m
 
@@ -365,6 +374,30 @@ def mk_paged_attention(stream: int, B: int, N: int, max_new: int, Hq: int, Hkv: 
     check(lib().mk_paged_attention(stream, B, N, max_new, Hq, Hkv, D, q, ld_q, kpool, vpool, num_pages, page_size,
                                    table, max_pages, cu, ctx_len, scale, out, ld_out, workspace, workspace_size,
                                    status), "mk_paged_attention")
+
+
+def mk_qk_norm_rope_e4m3(stream: int, N: int, Hq: int, Hkv: int, D: int, qkv: int, qkv_dtype: int, ld_qkv: int,
+                         q_gamma: int, k_gamma: int, eps: float, rope_theta: float, positions: int, slots: int,
+                         q_out: int, ld_q: int, kpool: int, vpool: int, kscale: int, vscale: int, num_pages: int,
+                         page_size: int, status: int = 0):
+    check(lib().mk_qk_norm_rope_e4m3(stream, N, Hq, Hkv, D, qkv, qkv_dtype, ld_qkv, q_gamma, k_gamma, eps, rope_theta,
+                                     positions, slots, q_out, ld_q, kpool, vpool, kscale, vscale, num_pages, page_size,
+                                     status), "mk_qk_norm_rope_e4m3")
+
+
+def mk_paged_attention_e4m3(stream: int, B: int, N: int, max_new: int, Hq: int, Hkv: int, D: int, q: int, ld_q: int,
+                            kpool: int, vpool: int, kscale: int, vscale: int, num_pages: int, page_size: int,
+                            table: int, max_pages: int, cu: int, ctx_len: int, scale: float, out: int, ld_out: int,
+                            workspace: int, workspace_size: int, status: int = 0):
+    check(lib().mk_paged_attention_e4m3(stream, B, N, max_new, Hq, Hkv, D, q, ld_q, kpool, vpool, kscale, vscale,
+                                        num_pages, page_size, table, max_pages, cu, ctx_len, scale, out, ld_out,
+                                        workspace, workspace_size, status), "mk_paged_attention_e4m3")
+
+
+def mk_token_logprobs(stream: int, N: int, V: int, logits: int, logits_dtype: int, ld: int, tokens: int, top: int,
+                      logprobs: int, entropy: int, top_ids: int, top_logprobs: int, status: int = 0):
+    check(lib().mk_token_logprobs(stream, N, V, logits, logits_dtype, ld, tokens, top, logprobs, entropy, top_ids,
+                                  top_logprobs, status), "mk_token_logprobs")
 
 
 def mk_paged_attention_workspace(max_new: int, Hq: int, Hkv: int, D: int) -> int:

@@ -25,7 +25,9 @@ LIB = os.path.join(HERE, "libmk.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = [os.path.join(CSRC, f) for f in ("graph.cpp", "runtime.cu", "megakernel.cu", "noalloc.cu")] + \
           [os.path.join(OPS, f) for f in ("paged.cu", "paged_rows.cu", "paged_chunk.cu", "paged_attention.cu",
+                                          "paged_store8.cu", "paged_rows8.cu", "paged_chunk8.cu", "token_logprobs.cu",
                                           "verify.cu")]
+REGISTERS_CHECKED = ("paged_chunk.cu", "paged_chunk8.cu")
 
 
 def nvcc() -> str:
@@ -35,15 +37,15 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def check_launch_registers(source: str, log: str) -> None:
-    """The chunk kernel's warpgroups trade registers at run time, and their shares add up to exactly what it is
+def check_launch_registers(source: str, log: str, name: str = "paged_chunk.cu") -> None:
+    """A chunk kernel's warpgroups trade registers at run time, and their shares add up to exactly what it is
     launched with (kLaunchRegs of its source).  Another count by the compiler is an error of the build; the launch
     refuses it too."""
     want = int(re.search(r"kLaunchRegs = (\d+)", source).group(1))
-    used = re.findall(r"Compiling entry function '\w*chunk_kernel\w*'(?:(?!Compiling entry).)*?Used (\d+) registers", log,
+    used = re.findall(r"Compiling entry function '\w*chunk8?_kernel\w*'(?:(?!Compiling entry).)*?Used (\d+) registers", log,
                       re.S)
     if not used or any(int(n) != want for n in used):
-        raise RuntimeError(f"paged_chunk.cu: the chunk kernel has to be compiled to {want} registers, not to "
+        raise RuntimeError(f"{name}: the chunk kernel has to be compiled to {want} registers, not to "
                            f"{', '.join(used) or 'an unknown number'}: set kLaunchRegs and the shares to this compiler's")
 
 
@@ -54,14 +56,14 @@ def _compile(src: str, verbose: bool) -> str:
            "-I", INCLUDE, "-I", CSRC, "-I", OPS, "-c", src, "-o", obj]
     if src.endswith(".cpp"):
         cmd[1:1] = ["-x", "cu"]
-    if name == "paged_chunk.cu" or verbose and name == "megakernel.cu":
+    if name in REGISTERS_CHECKED or verbose and name == "megakernel.cu":
         cmd.append("-Xptxas=-v")
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed on {name}:\n{r.stdout}\n{r.stderr}")
-    if name == "paged_chunk.cu":
+    if name in REGISTERS_CHECKED:
         with open(src) as f:
-            check_launch_registers(f.read(), r.stdout + r.stderr)
+            check_launch_registers(f.read(), r.stdout + r.stderr, name)
     if verbose and r.stderr:
         sys.stderr.write(r.stderr)
     return obj

@@ -1,5 +1,5 @@
-// The tensor-level calls of the paged-cache operators and of draft
-// verification, as a CPython module: checks of the tensors, fresh outputs and
+// The tensor-level calls of the paged-cache operators, of draft verification
+// and of token log probabilities, as a CPython module: checks of the tensors, fresh outputs and
 // scratch, the current stream, and the C ABI call, without a Python-level
 // access per property.  A decode step makes two such calls per layer, and in
 // Python the checks took longer than the small kernels: norms of one token
@@ -33,6 +33,9 @@ decltype(&mk_qk_norm_rope) qk_norm_rope = nullptr;
 decltype(&mk_paged_attention) paged_attention = nullptr;
 decltype(&mk_paged_attention_workspace) paged_attention_workspace = nullptr;
 decltype(&mk_verify_drafts) verify_drafts = nullptr;
+decltype(&mk_qk_norm_rope_e4m3) qk_norm_rope_e4m3 = nullptr;
+decltype(&mk_paged_attention_e4m3) paged_attention_e4m3 = nullptr;
+decltype(&mk_token_logprobs) token_logprobs = nullptr;
 decltype(&mk_last_error) last_error = nullptr;
 PyObject* mk_error = nullptr;  // the binding's exception class
 
@@ -102,16 +105,31 @@ int32_t* block_table(const at::Tensor& t, int64_t B, int dev, int* max_pages) {
 }
 struct Pools {
   void *k, *v;
+  float *kscale, *vscale;  // of e4m3 pools
   int num_pages, Hkv, page, D;
 };
-Pools pools(const at::Tensor& k, const at::Tensor& v, int dev) {
-  if (k.dim() != 4 || k.sizes() != v.sizes() || k.scalar_type() != at::kBFloat16 || v.scalar_type() != at::kBFloat16 ||
-      !k.is_contiguous() || !v.is_contiguous() || !on(k, dev) || !on(v, dev))
-    refuse("kpool and vpool must be contiguous bf16 [num_pages, Hkv, page_size, D] on cuda:" + std::to_string(dev));
+float* page_scales(const at::Tensor& t, const char* name, const at::Tensor& pool, int dev) {
+  if (t.scalar_type() != at::kFloat || t.dim() != 2 || t.size(0) != pool.size(0) || t.size(1) != pool.size(1) ||
+      !t.is_contiguous() || !on(t, dev))
+    refuse(std::string(name) + " must be contiguous f32 [" + std::to_string(pool.size(0)) + ", " +
+           std::to_string(pool.size(1)) + "] on cuda:" + std::to_string(dev));
+  no_gradient(t, name);
+  return static_cast<float*>(t.data_ptr());
+}
+Pools pools(const at::Tensor& k, const at::Tensor& v, PyObject* kscale, PyObject* vscale, int dev) {
+  const bool e4m3 = k.scalar_type() == at::kFloat8_e4m3fn;
+  if (k.dim() != 4 || k.sizes() != v.sizes() || (!e4m3 && k.scalar_type() != at::kBFloat16) ||
+      v.scalar_type() != k.scalar_type() || !k.is_contiguous() || !v.is_contiguous() || !on(k, dev) || !on(v, dev))
+    refuse("kpool and vpool must be contiguous bf16 or e4m3 [num_pages, Hkv, page_size, D] on cuda:" +
+           std::to_string(dev));
   no_gradient(k, "kpool");
   no_gradient(v, "vpool");
-  return {k.data_ptr(), v.data_ptr(), small_size(k.size(0), "num_pages"), small_size(k.size(1), "Hkv"),
-          small_size(k.size(2), "page_size"), small_size(k.size(3), "D")};
+  const at::Tensor *ks = tensor_or_none(kscale, "kscale"), *vs = tensor_or_none(vscale, "vscale");
+  if (e4m3 ? !ks || !vs : ks || vs)
+    refuse(e4m3 ? "e4m3 pools need kscale and vscale" : "kscale and vscale belong to e4m3 pools");
+  return {k.data_ptr(), v.data_ptr(), ks ? page_scales(*ks, "kscale", k, dev) : nullptr,
+          vs ? page_scales(*vs, "vscale", v, dev) : nullptr, small_size(k.size(0), "num_pages"),
+          small_size(k.size(1), "Hkv"), small_size(k.size(2), "page_size"), small_size(k.size(3), "D")};
 }
 // elements between the rows of bf16 [N, Hq, D], which may lie apart
 int64_t row_stride(const at::Tensor& t, const char* name, int64_t N, int64_t Hq, int64_t D, int dev) {
@@ -229,9 +247,10 @@ PyObject* py_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// qk_norm_rope(qkv, Hq, Hkv, D, positions, slots, kpool, vpool, q_gamma, k_gamma, eps, rope_theta, out, status) -> out
+// qk_norm_rope(qkv, Hq, Hkv, D, positions, slots, kpool, vpool, q_gamma, k_gamma, eps, rope_theta, out, status, kscale,
+//              vscale) -> out
 PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded("qk_norm_rope", 14, n, [&]() -> PyObject* {
+  return guarded("qk_norm_rope", 16, n, [&]() -> PyObject* {
     const at::Tensor& x = tensor(a[0], "qkv");
     const int dev = device_of(x, "qkv");
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
@@ -243,7 +262,7 @@ PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       refuse("qkv must be f32 or bf16 [N, " + std::to_string(width) + "] with contiguous rows");
     no_gradient(x, "qkv");
     const int N = small_size(x.size(0), "N");
-    const Pools pl = pools(tensor(a[6], "kpool"), tensor(a[7], "vpool"), dev);
+    const Pools pl = pools(tensor(a[6], "kpool"), tensor(a[7], "vpool"), a[14], a[15], dev);
     if (pl.Hkv != Hkv || pl.D != D)
       refuse("the pools have " + std::to_string(pl.Hkv) + " heads of " + std::to_string(pl.D) + ", the call " +
              std::to_string(Hkv) + " of " + std::to_string(D));
@@ -259,11 +278,20 @@ PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (N > 0) {
       void* stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
       const int64_t ld_x = N > 1 ? x.stride(0) : width;
-      check(unlocked([&] {
-              return qk_norm_rope(stream, N, Hq, Hkv, D, x.data_ptr(), f32 ? MK_F32 : MK_BF16, ld_x, gq, gk, eps, theta,
-                                  pos, slots, out.data_ptr(), ld, pl.k, pl.v, pl.num_pages, pl.page, status);
-            }),
-            "mk_qk_norm_rope");
+      const int type = f32 ? MK_F32 : MK_BF16;
+      if (pl.kscale)
+        check(unlocked([&] {
+                return qk_norm_rope_e4m3(stream, N, Hq, Hkv, D, x.data_ptr(), type, ld_x, gq, gk, eps, theta, pos, slots,
+                                         out.data_ptr(), ld, pl.k, pl.v, pl.kscale, pl.vscale, pl.num_pages, pl.page,
+                                         status);
+              }),
+              "mk_qk_norm_rope_e4m3");
+      else
+        check(unlocked([&] {
+                return qk_norm_rope(stream, N, Hq, Hkv, D, x.data_ptr(), type, ld_x, gq, gk, eps, theta, pos, slots,
+                                    out.data_ptr(), ld, pl.k, pl.v, pl.num_pages, pl.page, status);
+              }),
+              "mk_qk_norm_rope");
     }
     return THPVariable_Wrap(out);
   });
@@ -296,13 +324,13 @@ struct Scratch {
   }
 };
 
-// attention(q, kpool, vpool, table, cu, ctx_len, max_new, scale, out, workspace, status) -> out
+// attention(q, kpool, vpool, table, cu, ctx_len, max_new, scale, out, workspace, status, kscale, vscale) -> out
 PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded("attention", 11, n, [&]() -> PyObject* {
+  return guarded("attention", 13, n, [&]() -> PyObject* {
     const at::Tensor& q = tensor(a[0], "q");
     const int dev = device_of(q, "q");
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
-    const Pools pl = pools(tensor(a[1], "kpool"), tensor(a[2], "vpool"), dev);
+    const Pools pl = pools(tensor(a[1], "kpool"), tensor(a[2], "vpool"), a[11], a[12], dev);
     if (q.dim() != 3) refuse("q must be bf16 [N, Hq, D]");
     const int N = small_size(q.size(0), "N"), Hq = small_size(q.size(1), "Hq");
     const int64_t ld_q = row_stride(q, "q", N, Hq, pl.D, dev);
@@ -331,7 +359,15 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         work = scratch.p = c10::cuda::CUDACachingAllocator::raw_alloc(size);
       }
       void* stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
-      check(unlocked([&] {
+      if (pl.kscale)
+        check(unlocked([&] {
+                return paged_attention_e4m3(stream, B, N, max_new, Hq, pl.Hkv, pl.D, q.data_ptr(), ld_q, pl.k, pl.v,
+                                            pl.kscale, pl.vscale, pl.num_pages, pl.page, table, max_pages, cu, c, scale,
+                                            out.data_ptr(), ld_out, work, size, status);
+              }),
+              "mk_paged_attention_e4m3");
+      else
+        check(unlocked([&] {
               return paged_attention(stream, B, N, max_new, Hq, pl.Hkv, pl.D, q.data_ptr(), ld_q, pl.k, pl.v,
                                      pl.num_pages, pl.page, table, max_pages, cu, c, scale, out.data_ptr(), ld_out, work,
                                      size, status);
@@ -378,15 +414,69 @@ PyObject* py_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A given result, or a fresh one.
+at::Tensor result(PyObject* o, const char* name, at::IntArrayRef size, at::ScalarType type, int dev) {
+  const at::Tensor* given = tensor_or_none(o, name);
+  if (!given) return fresh(size, type, dev);
+  if (given->scalar_type() != type || given->sizes() != size || !given->is_contiguous() || !on(*given, dev))
+    refuse(std::string(name) + " must be contiguous " + (type == at::kFloat ? "f32" : "int32") + " of " +
+           std::to_string(size.size()) + " dimensions that fit the call, on cuda:" + std::to_string(dev));
+  no_gradient(*given, name);
+  return *given;
+}
+
+// logprobs(logits, tokens, top, logprobs, entropy, top_ids, top_logprobs, status)
+//   -> (logprobs or None, entropy, top_ids, top_logprobs)
+PyObject* py_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("logprobs", 8, n, [&]() -> PyObject* {
+    const at::Tensor& x = tensor(a[0], "logits");
+    const int dev = device_of(x, "logits");
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    const bool f32 = x.scalar_type() == at::kFloat;
+    if ((!f32 && x.scalar_type() != at::kBFloat16) || x.dim() != 2 || (x.size(1) > 1 && x.stride(1) != 1))
+      refuse("logits must be f32 or bf16 [N, V] with contiguous rows");
+    no_gradient(x, "logits");
+    const int N = small_size(x.size(0), "N"), V = small_size(x.size(1), "V"), top = small_integer(a[2], "top");
+    if (V < 1 || top < 0 || top > 32 || top > V) refuse("need V of at least 1 and top in [0, min(32, V)]");
+    const at::Tensor* tk = tensor_or_none(a[1], "tokens");
+    if (tk && tk->numel() != N) refuse("tokens must be int32 [" + std::to_string(N) + "]");
+    const int32_t* tokens = tk ? int32s(*tk, "tokens", N, dev) : nullptr;
+    if (!tk && a[3] != Py_None) refuse("logprobs are those of tokens, and none are given");
+    at::Tensor lp;
+    if (tk) lp = result(a[3], "logprobs", {N}, at::kFloat, dev);
+    const at::Tensor ent = result(a[4], "entropy", {N}, at::kFloat, dev);
+    const at::Tensor ids = result(a[5], "top_ids", {N, top}, at::kInt, dev);
+    const at::Tensor tlp = result(a[6], "top_logprobs", {N, top}, at::kFloat, dev);
+    int32_t* status = int32s_or_null(a[7], "status", 1, dev);
+    if (N > 0) {
+      void* stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
+      const int64_t ld = N > 1 ? x.stride(0) : V;
+      float *l = tk ? static_cast<float*>(lp.data_ptr()) : nullptr, *e = static_cast<float*>(ent.data_ptr()),
+            *tl = static_cast<float*>(tlp.data_ptr());
+      int32_t* ti = static_cast<int32_t*>(ids.data_ptr());
+      check(unlocked([&] {
+              return token_logprobs(stream, N, V, x.data_ptr(), f32 ? MK_F32 : MK_BF16, ld, tokens, top, l, e, ti, tl,
+                                    status);
+            }),
+            "mk_token_logprobs");
+    }
+    PyObject* first = Py_None;
+    if (tk) first = THPVariable_Wrap(lp);
+    else Py_INCREF(Py_None);
+    return Py_BuildValue("(NNNN)", first, THPVariable_Wrap(ent), THPVariable_Wrap(ids), THPVariable_Wrap(tlp));
+  });
+}
+
 // bind(MkError, addresses of mk_paged_plan, mk_qk_norm_rope, mk_paged_attention, mk_paged_attention_workspace,
-//      mk_verify_drafts, mk_last_error)
+//      mk_verify_drafts, mk_last_error, mk_qk_norm_rope_e4m3, mk_paged_attention_e4m3, mk_token_logprobs)
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 7) {
-    PyErr_SetString(PyExc_TypeError, "bind takes 7 arguments");
+  constexpr int kFunctions = 9;
+  if (n != kFunctions + 1) {
+    PyErr_SetString(PyExc_TypeError, "bind takes 10 arguments");
     return nullptr;
   }
-  void* f[6];
-  for (int i = 0; i < 6; ++i) {
+  void* f[kFunctions];
+  for (int i = 0; i < kFunctions; ++i) {
     f[i] = PyLong_AsVoidPtr(a[i + 1]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -398,6 +488,9 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   paged_attention_workspace = reinterpret_cast<decltype(paged_attention_workspace)>(f[3]);
   verify_drafts = reinterpret_cast<decltype(verify_drafts)>(f[4]);
   last_error = reinterpret_cast<decltype(last_error)>(f[5]);
+  qk_norm_rope_e4m3 = reinterpret_cast<decltype(qk_norm_rope_e4m3)>(f[6]);
+  paged_attention_e4m3 = reinterpret_cast<decltype(paged_attention_e4m3)>(f[7]);
+  token_logprobs = reinterpret_cast<decltype(token_logprobs)>(f[8]);
   paged_plan = reinterpret_cast<decltype(paged_plan)>(f[0]);
   Py_RETURN_NONE;
 }
@@ -412,6 +505,7 @@ PyMethodDef methods[] = {{"bind", fast(py_bind), METH_FASTCALL, nullptr},
                          {"qk_norm_rope", fast(py_norm), METH_FASTCALL, nullptr},
                          {"attention", fast(py_attention), METH_FASTCALL, nullptr},
                          {"verify", fast(py_verify), METH_FASTCALL, nullptr},
+                         {"logprobs", fast(py_logprobs), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

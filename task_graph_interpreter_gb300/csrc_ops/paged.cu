@@ -1,11 +1,6 @@
 // Paged KV cache: the step plan (block tables, slot maps) and the per-head
 // norms with the rotary position embedding and the stores into pages.
-#include <cmath>
-
-#include <cuda_bf16.h>
-
-#include "paged.h"
-#include "ptx_ops.cuh"
+#include "paged_norm.cuh"
 
 namespace mk {
 namespace {
@@ -252,66 +247,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
 // remainder without rounding, for any position, and its upper 32 bits give
 // the angle to 2^-32 of a turn; sincospif then works on [-1, 1).
 
-struct NormParams {
-  const void* x;
-  int64_t ld_x, ld_q;
-  const __nv_bfloat16 *q_gamma, *k_gamma;
-  const int32_t *positions, *slots;
-  __nv_bfloat16 *q, *kpool, *vpool;
-  int32_t* status;
-  int N, Hq, Hkv, page_shift, num_pages;
-  int tokens, splits;  // tokens of a block; blocks that share a token's heads
-  float eps;
-  uint64_t freq[64];  // [D / 2]
-};
-
-// E elements as they come, and as floats
-template <typename T, int E>
-struct Raw;
-template <int E>
-struct Raw<float, E> {
-  float4 v[E / 4];
-  __device__ __forceinline__ void load(const float* p) {
-#pragma unroll
-    for (int i = 0; i < E / 4; ++i) v[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
-  }
-  __device__ __forceinline__ void get(float (&f)[E]) const {
-#pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-      f[4 * i] = v[i].x; f[4 * i + 1] = v[i].y; f[4 * i + 2] = v[i].z; f[4 * i + 3] = v[i].w;
-    }
-  }
-};
-template <int E>
-struct Raw<__nv_bfloat16, E> {
-  uint2 v[E / 4];
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    if constexpr (E == 8) {
-      const uint4 t = __ldg(reinterpret_cast<const uint4*>(p));
-      v[0] = make_uint2(t.x, t.y);
-      v[1] = make_uint2(t.z, t.w);
-    } else {
-      v[0] = __ldg(reinterpret_cast<const uint2*>(p));
-    }
-  }
-  __device__ __forceinline__ void get(float (&f)[E]) const {
-#pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-      f[4 * i] = ptx::bf_lo(v[i].x); f[4 * i + 1] = ptx::bf_hi(v[i].x);
-      f[4 * i + 2] = ptx::bf_lo(v[i].y); f[4 * i + 3] = ptx::bf_hi(v[i].y);
-    }
-  }
-};
-using ptx::pack_bf16;
-template <int E>
-__device__ __forceinline__ void store_half(__nv_bfloat16* p, const float (&v)[E]) {
-  if constexpr (E == 8)
-    *reinterpret_cast<uint4*>(p) =
-        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-  else
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-}
-
 constexpr int kNormBatch = 3;      // heads a lane group has in flight
 constexpr int kNormMaxTokens = 4;  // tokens of a block
 // Small blocks: a block's loads, angles and stores follow one another, and
@@ -518,23 +453,9 @@ extern "C" int mk_qk_norm_rope(void* stream, int N, int Hq, int Hkv, int D, cons
                                int64_t ld_qkv, const void* q_gamma, const void* k_gamma, float eps, double rope_theta,
                                const int32_t* positions, const int32_t* slots, void* q_out, int64_t ld_q, void* kpool,
                                void* vpool, int num_pages, int page_size, int32_t* status) try {
-  if (!qkv || !positions || !slots || !q_out || !kpool || !vpool)
-    return fail(MK_ERR_ARG, "mk_qk_norm_rope: null argument");
-  if (N < 0 || Hq < 1 || Hkv < 1 || Hq > 1024 || Hkv > 1024)
-    return fail(MK_ERR_ARG, "mk_qk_norm_rope: need N >= 0 and 1 to 1024 heads");
-  if (D != 64 && D != 128) return fail(MK_ERR_ARG, "mk_qk_norm_rope: D must be 64 or 128");
-  if (qkv_dtype != MK_F32 && qkv_dtype != MK_BF16) return fail(MK_ERR_ARG, "mk_qk_norm_rope: qkv must be f32 or bf16");
-  if (!page_size_ok(page_size)) return fail(MK_ERR_ARG, "mk_qk_norm_rope: page_size must be 16, 32, 64, 128 or 256");
-  if (num_pages < 1 || (int64_t)num_pages * page_size > INT32_MAX)
-    return fail(MK_ERR_ARG, "mk_qk_norm_rope: num_pages * page_size must be in [1, 2^31)");
-  if (!(rope_theta > 0.0) || !std::isfinite(rope_theta) || !(eps >= 0.f) || !std::isfinite(eps))
-    return fail(MK_ERR_ARG, "mk_qk_norm_rope: bad rope_theta or eps");
-  const int64_t width = (int64_t)(Hq + 2 * Hkv) * D, unit = qkv_dtype == MK_F32 ? 4 : 8;
-  if (ld_qkv < width || ld_qkv % unit || ld_q < (int64_t)Hq * D || ld_q % 8)
-    return fail(MK_ERR_ARG, "mk_qk_norm_rope: row strides must cover a row and be multiples of 16 bytes");
-  if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(kpool) || !aligned16(vpool) || !aligned16(q_gamma) ||
-      !aligned16(k_gamma))
-    return fail(MK_ERR_ARG, "mk_qk_norm_rope: pointers must be 16-byte aligned");
+  if (int rc = check_norm("mk_qk_norm_rope", N, Hq, Hkv, D, qkv, qkv_dtype, ld_qkv, q_gamma, k_gamma, eps, rope_theta,
+                          positions, slots, q_out, ld_q, kpool, vpool, num_pages, page_size))
+    return rc;
   if (int rc = pending_error("mk_qk_norm_rope")) return rc;
   if (N == 0) return MK_OK;
   NormParams p{};
@@ -547,22 +468,7 @@ extern "C" int mk_qk_norm_rope(void* stream, int N, int Hq, int Hkv, int D, cons
   p.vpool = static_cast<__nv_bfloat16*>(vpool);
   p.status = status; p.N = N; p.Hq = Hq; p.Hkv = Hkv; p.num_pages = num_pages; p.eps = eps;
   while ((1 << p.page_shift) < page_size) ++p.page_shift;
-  // the last base's frequencies: a decoder asks for the same ones in every layer
-  thread_local struct {
-    double theta = 0.0;
-    int D = 0;
-    uint64_t f[64];
-  } known;
-  if (known.theta != rope_theta || known.D != D) {
-    for (int i = 0; i < D / 2; ++i) {
-      // revolutions per position, reduced below one, in units of 2^-64
-      const double f = std::fmod(std::pow(rope_theta, -2.0 * i / D) / 6.283185307179586476925, 1.0);
-      known.f[i] = (uint64_t)std::ldexp(f, 64);
-    }
-    known.theta = rope_theta;
-    known.D = D;
-  }
-  for (int i = 0; i < D / 2; ++i) p.freq[i] = known.f[i];
+  rope_frequencies(rope_theta, D, p.freq);
   int sms = 0;
   if (int rc = device_sms("mk_qk_norm_rope", &sms)) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -29,10 +29,11 @@ EncodeTiledFn encoder() {
 }
 
 bool encode(EncodeTiledFn enc, CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dim,
-            const cuuint64_t* stride, const cuuint32_t* box) {
+            const cuuint64_t* stride, const cuuint32_t* box, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+            CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   const cuuint32_t one[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), dim, stride, box, one,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return enc(m, type, (cuuint32_t)rank, const_cast<void*>(ptr), dim, stride, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -72,43 +73,47 @@ extern "C" int mk_paged_attention_workspace(int max_new, int Hq, int Hkv, int D,
   return MK_ERR_NOMEM;
 }
 
-extern "C" int mk_paged_attention(void* stream_, int B, int N, int max_new, int Hq, int Hkv, int D, const void* q,
-                                  int64_t ld_q, const void* kpool, const void* vpool, int num_pages, int page_size,
-                                  const int32_t* table, int max_pages, const int32_t* cu, const int32_t* ctx_len,
-                                  float scale, void* out, int64_t ld_out, void* workspace, size_t workspace_size,
-                                  int32_t* status) try {
-  const char* who = "mk_paged_attention";
-  if (!q || !kpool || !vpool || !table || !cu || !ctx_len || !out || !workspace)
-    return fail(MK_ERR_ARG, "mk_paged_attention: null argument");
+// Both forms of the operator: e4m3 pages have scales, bf16 pages none.
+static int attention(const char* who, bool e4m3, void* stream_, int B, int N, int max_new, int Hq, int Hkv, int D,
+                     const void* q, int64_t ld_q, const void* kpool, const void* vpool, const float* kscale,
+                     const float* vscale, int num_pages, int page_size, const int32_t* table, int max_pages,
+                     const int32_t* cu, const int32_t* ctx_len, float scale, void* out, int64_t ld_out, void* workspace,
+                     size_t workspace_size, int32_t* status) {
+  const std::string name(who);
+  if (!q || !kpool || !vpool || !table || !cu || !ctx_len || !out || !workspace ||
+      (e4m3 && (!kscale || !vscale)))
+    return fail(MK_ERR_ARG, name + ": null argument");
   if (int rc = check_shape(who, max_new, Hq, Hkv, D)) return rc;
-  if (B < 0 || N < 0 || max_pages < 1) return fail(MK_ERR_ARG, "mk_paged_attention: need B, N >= 0 and max_pages >= 1");
+  if (B < 0 || N < 0 || max_pages < 1) return fail(MK_ERR_ARG, name + ": need B, N >= 0 and max_pages >= 1");
   if (!page_size_ok(page_size))
-    return fail(MK_ERR_ARG, "mk_paged_attention: page_size must be 16, 32, 64, 128 or 256");
+    return fail(MK_ERR_ARG, name + ": page_size must be 16, 32, 64, 128 or 256");
   // (positions are counted on to the end of a block of 128 keys, and past a request's last token to the end of two
   // tiles' rows: at most 254)
   if (num_pages < 1 || (int64_t)num_pages * Hkv * page_size > INT32_MAX ||
       (int64_t)max_pages * page_size > INT32_MAX - 255)
-    return fail(MK_ERR_ARG, "mk_paged_attention: rows of the pools must fit int32, max_pages * page_size 2^31 - 256");
+    return fail(MK_ERR_ARG, name + ": rows of the pools must fit int32, max_pages * page_size 2^31 - 256");
   if (ld_q < (int64_t)Hq * D || ld_q % 8 || ld_out < (int64_t)Hq * D || ld_out % 8)
-    return fail(MK_ERR_ARG, "mk_paged_attention: row strides must cover a row and be multiples of 16 bytes");
+    return fail(MK_ERR_ARG, name + ": row strides must cover a row and be multiples of 16 bytes");
   if (!aligned16(q) || !aligned16(kpool) || !aligned16(vpool) || !aligned16(out) || !aligned16(workspace))
-    return fail(MK_ERR_ARG, "mk_paged_attention: pointers must be 16-byte aligned");
-  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(MK_ERR_ARG, "mk_paged_attention: scale must be positive");
+    return fail(MK_ERR_ARG, name + ": pointers must be 16-byte aligned");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(MK_ERR_ARG, name + ": scale must be positive");
   if (int rc = pending_error(who)) return rc;
   int sms = 0;
   if (int rc = device_sms(who, &sms)) return rc;
   const int G = Hq / Hkv;
   if (workspace_size < workspace_bytes(max_new, G, D, sms))
-    return fail(MK_ERR_LIMIT, "mk_paged_attention: the workspace needs " +
+    return fail(MK_ERR_LIMIT, name + ": the workspace needs " +
                                   std::to_string(workspace_bytes(max_new, G, D, sms)) + " bytes");
   if (B == 0 || N == 0) return MK_OK;
   EncodeTiledFn enc = encoder();
-  if (!enc) return fail(MK_ERR_CUDA, "mk_paged_attention: cuTensorMapEncodeTiled is not available");
+  if (!enc) return fail(MK_ERR_CUDA, name + ": cuTensorMapEncodeTiled is not available");
 
   const bool few = few_rows(max_new, G);
-  AttnParams p{};
+  Attn8Params p{};
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.v = static_cast<const __nv_bfloat16*>(vpool);
+  p.v8 = static_cast<const uint8_t*>(vpool);
+  p.kscale = kscale; p.vscale = vscale;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.ld_q = ld_q; p.ld_out = ld_out;
   p.table = table; p.cu = cu; p.ctx = ctx_len;
@@ -127,22 +132,48 @@ extern "C" int mk_paged_attention(void* stream_, int B, int N, int max_new, int 
 
   // pools as [rows, D], pages one after the other; a box is what one page gives a block of keys
   CUtensorMap kmap, vmap, qmap;
-  const int keys = few ? kRowBlockBytes / D / 4 : 128;
-  const cuuint64_t dim[2] = {(cuuint64_t)D, (cuuint64_t)num_pages * Hkv * page_size}, stride[1] = {(cuuint64_t)D * 2};
-  const cuuint32_t box[2] = {64u, (cuuint32_t)(page_size < keys ? page_size : keys)};
-  bool ok = encode(enc, &kmap, kpool, 2, dim, stride, box) && encode(enc, &vmap, vpool, 2, dim, stride, box);
+  const int keys = !few ? 128 : e4m3 ? kRowKeys8 : kRowBlockBytes / D / 4, size = e4m3 ? 1 : 2;
+  const cuuint64_t dim[2] = {(cuuint64_t)D, (cuuint64_t)num_pages * Hkv * page_size}, stride[1] = {(cuuint64_t)D * size};
+  const cuuint32_t box[2] = {e4m3 ? (cuuint32_t)D : 64u, (cuuint32_t)(page_size < keys ? page_size : keys)};
+  const CUtensorMapDataType type = e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle swizzle = e4m3 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  bool ok = encode(enc, &kmap, kpool, 2, dim, stride, box, type, swizzle) &&
+            encode(enc, &vmap, vpool, 2, dim, stride, box, type, swizzle);
   if (ok && !few) {
     const cuuint64_t qdim[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)N};
     const cuuint64_t qstride[2] = {(cuuint64_t)D * 2, (cuuint64_t)ld_q * 2};
     const cuuint32_t qbox[3] = {64u, (cuuint32_t)G, (cuuint32_t)p.tq};
     ok = encode(enc, &qmap, q, 3, qdim, qstride, qbox);
   }
-  if (!ok) return fail(MK_ERR_CUDA, "mk_paged_attention: a tensor map could not be encoded");
+  if (!ok) return fail(MK_ERR_CUDA, name + ": a tensor map could not be encoded");
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  if (int rc = launch_result(few ? launch_rows(p, kmap, vmap, D, stream) : launch_chunk(p, qmap, kmap, vmap, D, stream),
-                             who))
-    return rc;
+  const cudaError_t e = e4m3 ? few ? launch_rows8(p, kmap, vmap, D, stream) : launch_chunk8(p, qmap, kmap, vmap, D, stream)
+                        : few ? launch_rows(p, kmap, vmap, D, stream)
+                              : launch_chunk(p, qmap, kmap, vmap, D, stream);
+  if (int rc = launch_result(e, who)) return rc;
   return launch_result(launch_join(p, D, !few, stream), who);
+}
+
+extern "C" int mk_paged_attention(void* stream, int B, int N, int max_new, int Hq, int Hkv, int D, const void* q,
+                                  int64_t ld_q, const void* kpool, const void* vpool, int num_pages, int page_size,
+                                  const int32_t* table, int max_pages, const int32_t* cu, const int32_t* ctx_len,
+                                  float scale, void* out, int64_t ld_out, void* workspace, size_t workspace_size,
+                                  int32_t* status) try {
+  return attention("mk_paged_attention", false, stream, B, N, max_new, Hq, Hkv, D, q, ld_q, kpool, vpool, nullptr, nullptr,
+                   num_pages, page_size, table, max_pages, cu, ctx_len, scale, out, ld_out, workspace, workspace_size,
+                   status);
+} catch (...) {
+  return MK_ERR_NOMEM;
+}
+
+extern "C" int mk_paged_attention_e4m3(void* stream, int B, int N, int max_new, int Hq, int Hkv, int D, const void* q,
+                                       int64_t ld_q, const void* kpool, const void* vpool, const float* kscale,
+                                       const float* vscale, int num_pages, int page_size, const int32_t* table,
+                                       int max_pages, const int32_t* cu, const int32_t* ctx_len, float scale, void* out,
+                                       int64_t ld_out, void* workspace, size_t workspace_size, int32_t* status) try {
+  return attention("mk_paged_attention_e4m3", true, stream, B, N, max_new, Hq, Hkv, D, q, ld_q, kpool, vpool, kscale,
+                   vscale, num_pages, page_size, table, max_pages, cu, ctx_len, scale, out, ld_out, workspace,
+                   workspace_size, status);
 } catch (...) {
   return MK_ERR_NOMEM;
 }

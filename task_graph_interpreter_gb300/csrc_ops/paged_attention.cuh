@@ -45,15 +45,22 @@ constexpr int kRowBlockBytes = 16384;  // keys and values of a few-rows block
 // probabilities likewise: added block by block to a sum of 2^25, equal blocks may all be rounded the same way, by 1 %.
 constexpr int kFoldKeys = 65536;
 
+// The same over e4m3 pages (paged_rows8.cu, paged_chunk8.cu): codes, and a scale per page and head.
+struct Attn8Params : AttnParams {
+  const uint8_t* v8;
+  const float *kscale, *vscale;
+};
+constexpr int kRowKeys8 = 64;  // keys of a few-rows block of e4m3
+
 // Geometry of an item: few query rows (all of a request's), or a pair of
-// 128-row query tiles.
-template <int D, bool CHUNK>
+// 128-row query tiles; E8: of e4m3 pages.
+template <int D, bool CHUNK, bool E8 = false>
 struct Geometry {
-  static constexpr int kKeys = CHUNK ? 128 : kRowBlockBytes / D / 4;  // keys per block
+  static constexpr int kKeys = CHUNK ? 128 : E8 ? kRowKeys8 : kRowBlockBytes / D / 4;  // keys per block
   // an item's fixed cost, in keys: measured for few rows (paged_rows.cu); for chunks what surrounds a part's
   // blocks, some 2 us at 1.1 us for 128 keys of both tiles (256, 288 and 384 took the same time within noise, on
   // seven ragged chunks)
-  static constexpr int kFixed = CHUNK ? 320 : 96;
+  static constexpr int kFixed = CHUNK ? 320 : E8 ? 192 : 96;
 };
 
 struct Seq {
@@ -64,7 +71,7 @@ struct Seq {
   bool bad;
 };
 
-template <int D, bool CHUNK>
+template <int D, bool CHUNK, bool E8 = false>
 __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
   Seq s;
   const int c0 = p.cu[b], c1 = p.cu[b + 1];
@@ -79,7 +86,7 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
     s.base = s.step = s.per_head = 0;
     return s;
   }
-  constexpr int F = Geometry<D, CHUNK>::kFixed;
+  constexpr int F = Geometry<D, CHUNK, E8>::kFixed;
   if (CHUNK) {
     const int tp = 2 * p.tq;
     s.nq = (s.n + tp - 1) / tp;
@@ -123,7 +130,7 @@ struct Line {
 };
 
 // A whole warp; lanes agree but for `own`.
-template <int D, bool CHUNK>
+template <int D, bool CHUNK, bool E8 = false>
 __device__ __forceinline__ Line measure_line(const AttnParams& p, int lane) {
   Line l;
   l.own = 0;
@@ -131,7 +138,7 @@ __device__ __forceinline__ Line measure_line(const AttnParams& p, int lane) {
   bool wrong = false;
 #pragma unroll 1
   for (int b = lane; b < p.B; b += 32) {
-    const Seq s = load_seq<D, CHUNK>(p, b);
+    const Seq s = load_seq<D, CHUNK, E8>(p, b);
     const int64_t v = s.per_head * p.Hkv;
     if (b == lane) l.own = v;
     u += v;
@@ -143,14 +150,14 @@ __device__ __forceinline__ Line measure_line(const AttnParams& p, int lane) {
   l.u = u;
   // whole blocks, a few at least: fewer records to join where there is little to do, and a worker behind an
   // item's first block always has a part of it
-  constexpr int K = Geometry<D, CHUNK>::kKeys, kLeast = (CHUNK ? 1 : 2) * K;
+  constexpr int K = Geometry<D, CHUNK, E8>::kKeys, kLeast = (CHUNK ? 1 : 2) * K;
   const int64_t even = (u + p.workers - 1) / p.workers;
   l.part = even <= kLeast ? kLeast : (even + K - 1) / K * K;
   return l;
 }
 
 // A place on the line: the item holding it.  Uniform over the warp.
-template <int D, bool CHUNK>
+template <int D, bool CHUNK, bool E8 = false>
 struct Cursor {
   int b, g, i;      // request, key/value head, tile
   Seq s;
@@ -160,21 +167,21 @@ struct Cursor {
   __device__ __forceinline__ int blocks(const AttnParams& p) const {
     int keys = s.ctx + s.n;
     if (CHUNK) keys = (int)min((int64_t)keys, s.ctx + (i + 1) * s.step);
-    constexpr int K = Geometry<D, CHUNK>::kKeys;
+    constexpr int K = Geometry<D, CHUNK, E8>::kKeys;
     return (keys + K - 1) / K;
   }
   // the block that a place on the line falls to
   __device__ __forceinline__ int block_at(int64_t x, int nk) const {
-    constexpr int K = Geometry<D, CHUNK>::kKeys;
+    constexpr int K = Geometry<D, CHUNK, E8>::kKeys;
     if (x >= start + cost()) return nk;
-    const int64_t k = x - start - Geometry<D, CHUNK>::kFixed + K / 2;
+    const int64_t k = x - start - Geometry<D, CHUNK, E8>::kFixed + K / 2;
     return k <= 0 ? 0 : (int)min((int64_t)nk, k / K);
   }
   // the worker that has the item's first block: the last whose part begins before the place from which
   // block_at() is 1
   __device__ __forceinline__ int first_worker(const Line& line) const {
-    constexpr int K = Geometry<D, CHUNK>::kKeys;
-    return small_quotient(start + Geometry<D, CHUNK>::kFixed + K / 2 - 1, line.part);
+    constexpr int K = Geometry<D, CHUNK, E8>::kKeys;
+    return small_quotient(start + Geometry<D, CHUNK, E8>::kFixed + K / 2 - 1, line.part);
   }
   // the item holding place x of the line (0 <= x < U)
   __device__ __forceinline__ void find(const AttnParams& p, const Line& line, int64_t x, int lane) {
@@ -182,7 +189,7 @@ struct Cursor {
 #pragma unroll 1
     for (int b0 = 0;; b0 += 32) {
       int64_t own = line.own;
-      if (b0 > 0) own = b0 + lane < p.B ? load_seq<D, CHUNK>(p, b0 + lane).per_head * p.Hkv : 0;
+      if (b0 > 0) own = b0 + lane < p.B ? load_seq<D, CHUNK, E8>(p, b0 + lane).per_head * p.Hkv : 0;
       const int64_t end = warp_incl_scan(own, lane) + before;
       const unsigned hit = __ballot_sync(0xffffffffu, own > 0 && end > x);
       if (hit) {
@@ -198,7 +205,7 @@ struct Cursor {
         return;
       }
     }
-    s = load_seq<D, CHUNK>(p, b);
+    s = load_seq<D, CHUNK, E8>(p, b);
     const int64_t r = x - start;
     g = small_quotient(r, s.per_head);
     start += g * s.per_head;
@@ -225,7 +232,7 @@ struct Cursor {
     g = 0;
 #pragma unroll 1
     while (++b < p.B) {
-      s = load_seq<D, CHUNK>(p, b);
+      s = load_seq<D, CHUNK, E8>(p, b);
       if (s.n > 0) return;
     }
   }
@@ -283,6 +290,10 @@ cudaError_t launch_rows(const AttnParams& p, const CUtensorMap& kmap, const CUte
                         cudaStream_t stream);
 cudaError_t launch_chunk(const AttnParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
                          const CUtensorMap& vmap, int D, cudaStream_t stream);
+cudaError_t launch_rows8(const Attn8Params& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int D,
+                         cudaStream_t stream);
+cudaError_t launch_chunk8(const Attn8Params& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                          const CUtensorMap& vmap, int D, cudaStream_t stream);
 constexpr int kRowWarps = 4;    // warps (workers) per CTA of the few-rows kernel
 constexpr int kMaxFewRows = 8;  // query rows of a request and head that it takes
 

@@ -64,7 +64,7 @@
 // Probabilities are rounded to bf16 (2^-8 each, in the mean far less in the
 // sum), the form the tensor cores multiply with bf16 values; maxima, sums
 // and O are f32.
-#include "paged_attention.cuh"
+#include "paged_chunk.cuh"
 
 namespace mk {
 namespace {
@@ -73,21 +73,9 @@ using namespace ptx;
 
 constexpr int kThreads = 384;
 constexpr int kStages = 5;
-constexpr int kSegRing = 4;
 // registers: the launch's 3 x 128 threads x 168, moved to the softmax warpgroups
 constexpr int kLaunchRegs = 168, kConsumerRegs = 208, kOtherRegs = 88;
 static_assert(2 * kConsumerRegs + kOtherRegs <= 3 * kLaunchRegs, "register shares within the launch's");
-
-struct Segment {
-  int row0;       // first query row of the item (token index in q)
-  int b, g;       // request, key/value head
-  int ctx, t0;    // cached tokens; the item's first token in its request
-  int n;          // new tokens of the request
-  int k0, k1;     // key blocks of this part
-  int end[2];     // end of each tile's key blocks, >= k0
-  int slot;       // partial record, or -1: the part is the whole item
-  int valid;      // 0: no more parts
-};
 
 template <int D>
 struct Smem {
@@ -112,12 +100,6 @@ static_assert(sizeof(Control) <= Smem<128>::kControl, "control block");
 __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs)); }
 __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs)); }
 
-// The first key that the item's first row does not see, and the first that no row of it does.
-__device__ __forceinline__ int masked_from(const Segment& s) { return s.ctx + s.t0 + 1; }
-__device__ __forceinline__ int masked_to(const Segment& s, const AttnParams& p) {
-  return s.ctx + min(s.n, s.t0 + 2 * p.tq);
-}
-
 // Zero the rows of a value block from `valid` on and those of missing pages,
 // and let the tensor cores see it.  A whole warp.
 template <int D>
@@ -132,14 +114,6 @@ __device__ __forceinline__ void zero_values(uint32_t v0, int valid, uint32_t mis
   }
   fence_proxy_async_smem();
   __syncwarp();
-}
-
-// Of 32 keys of a block, from `key` on, those of missing pages.
-__device__ __forceinline__ uint32_t missing_keys(uint32_t miss, int key, int page_shift) {
-  uint32_t bits = 0;
-#pragma unroll 1
-  for (int c = 0; c < 32; ++c) bits |= ((miss >> ((key + c) >> page_shift)) & 1) << c;
-  return bits;
 }
 
 // Bits of a bf16 pair that belong to a value that is not finite.

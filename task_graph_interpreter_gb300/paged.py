@@ -1,6 +1,8 @@
 """A paged KV cache: block tables and slot maps, per-head norms with rotation
 and page stores, and attention of new tokens over the pages (the operators
-mk_paged_plan, mk_qk_norm_rope and mk_paged_attention of include/mk.h).
+mk_paged_plan, mk_qk_norm_rope and mk_paged_attention of include/mk.h).  Pages are
+bf16, or e4m3 with a scale for each page and head (mk_qk_norm_rope_e4m3,
+mk_paged_attention_e4m3): half the memory, and half the bytes that decoding reads.
 
 The functions take PyTorch tensors on one CUDA device (not necessarily the
 current one) and enqueue on that device's current stream, or on ``stream``;
@@ -67,16 +69,26 @@ def plan(ctx_len, new_len, table, held, free_pages, free_count, page_size: int, 
     return Plan._make(L.calls().plan(*args) if stream is None else on_stream(L.calls().plan, stream, args))
 
 
-def qk_norm_rope(qkv, Hq: int, Hkv: int, D: int, positions, slots, kpool, vpool, *, q_gamma=None, k_gamma=None,
-                 eps: float = 1e-5, rope_theta: float = 5e5, out=None, status=None, stream=None):
+def qk_norm_rope(qkv, Hq: int, Hkv: int, D: int, positions, slots, kpool, vpool, *, kscale=None, vscale=None,
+                 q_gamma=None, k_gamma=None, eps: float = 1e-5, rope_theta: float = 5e5, out=None, status=None,
+                 stream=None):
     """RMS norms of queries and keys for each head (none where its gain is
     None), the rotate-half rotary embedding at ``positions``, and the stores
     of keys and values at ``slots`` (mk_qk_norm_rope).  qkv f32 or bf16
     [N, (Hq + 2 Hkv) D], rows may lie apart; returns the queries, bf16
     [N, Hq, D] (``out`` if given, which may not overlap qkv).  Rows with a
     negative position are left out; ``out`` keeps what it had there (a fresh
-    one holds anything)."""
-    args = (qkv, Hq, Hkv, D, positions, slots, kpool, vpool, q_gamma, k_gamma, eps, rope_theta, out, status)
+    one holds anything).
+
+    With e4m3 pools (torch.float8_e4m3fn), ``kscale`` and ``vscale`` f32
+    [num_pages, Hkv] are read and updated too: a page's scale is the smallest
+    power of two s with max |x| <= 448 s, set by the call that stores its first
+    token and raised by later ones, when what the page holds is rounded to the
+    larger scale.  A page's new tokens are neighbouring rows in ascending order,
+    as ``plan`` makes them; rows that go back in a page are not stored
+    (MK_DEV_BAD_INDEX).  Values that are not finite are stored as NaN."""
+    args = (qkv, Hq, Hkv, D, positions, slots, kpool, vpool, q_gamma, k_gamma, eps, rope_theta, out, status, kscale,
+            vscale)
     return L.calls().qk_norm_rope(*args) if stream is None else on_stream(L.calls().qk_norm_rope, stream, args)
 
 
@@ -87,8 +99,8 @@ def attention_workspace(max_new: int, Hq: int, Hkv: int, D: int, device="cuda") 
         return torch.empty(L.mk_paged_attention_workspace(max_new, Hq, Hkv, D), dtype=torch.uint8, device=device)
 
 
-def attention(q, kpool, vpool, table, cu, ctx_len, max_new: int, *, scale: float = None, out=None, workspace=None,
-              status=None, stream=None):
+def attention(q, kpool, vpool, table, cu, ctx_len, max_new: int, *, kscale=None, vscale=None, scale: float = None,
+              out=None, workspace=None, status=None, stream=None):
     """Attention of the requests' new tokens over their pages, causal among
     the new ones (mk_paged_attention).  q bf16 [N, Hq, D] (rows may lie
     apart), row cu[b] + t is token t of request b, which sees the keys at
@@ -101,8 +113,12 @@ def attention(q, kpool, vpool, table, cu, ctx_len, max_new: int, *, scale: float
     With max_new Hq / Hkv <= 8 probabilities keep 2^-16, beyond it they are
     rounded to bf16 (results off by 1.7e-3 and 2.1e-3 to 2.4e-3, their own
     rounding included).  That goes for the whole call: a single token beside
-    a prompt is computed as the prompt is, unless it has a call of its own."""
-    args = (q, kpool, vpool, table, cu, ctx_len, max_new, scale, out, workspace, status)
+    a prompt is computed as the prompt is, unless it has a call of its own.
+
+    With e4m3 pools, ``kscale`` and ``vscale`` f32 [num_pages, Hkv] are the
+    positive scales of their pages and heads; probabilities are rounded to f16
+    (2^-11) whatever max_new is."""
+    args = (q, kpool, vpool, table, cu, ctx_len, max_new, scale, out, workspace, status, kscale, vscale)
     return L.calls().attention(*args) if stream is None else on_stream(L.calls().attention, stream, args)
 
 
@@ -114,16 +130,24 @@ class PagedCache:
     rejected, gives its pages back through the next plan's lengths.  No two
     requests may hold the same page.  ``check`` tells of lengths that did not
     fit.  The cache is made on the current stream, and its steps follow one
-    another: the caller orders a step on another stream behind both."""
+    another: the caller orders a step on another stream behind both.
+
+    ``dtype`` torch.float8_e4m3fn holds it in 8 bits, with ``kscale`` and
+    ``vscale`` [num_pages, Hkv] per layer (None in 16 bits)."""
 
     def __init__(self, layers: int, num_pages: int, page_size: int, Hkv: int, D: int, max_requests: int,
-                 max_pages: int, max_tokens: int, device="cuda"):
+                 max_pages: int, max_tokens: int, device="cuda", dtype=torch.bfloat16):
         dev = torch.device(device)
         i32 = dict(dtype=torch.int32, device=dev)
         self.page_size, self.Hkv, self.D = page_size, Hkv, D
+        if dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError(f"a paged cache holds torch.bfloat16 or torch.float8_e4m3fn, not {dtype}")
         shape = (num_pages, Hkv, page_size, D)
-        self.kpool = [torch.empty(shape, dtype=torch.bfloat16, device=dev) for _ in range(layers)]
-        self.vpool = [torch.empty(shape, dtype=torch.bfloat16, device=dev) for _ in range(layers)]
+        self.kpool = [torch.empty(shape, dtype=dtype, device=dev) for _ in range(layers)]
+        self.vpool = [torch.empty(shape, dtype=dtype, device=dev) for _ in range(layers)]
+        scale = (lambda: None) if dtype == torch.bfloat16 else (lambda: torch.ones(shape[:2], device=dev))
+        self.kscale = [scale() for _ in range(layers)]
+        self.vscale = [scale() for _ in range(layers)]
         self.table = torch.full((max_requests, max_pages), -1, **i32)
         self.held = torch.zeros(max_requests, **i32)
         self.free_pages = torch.arange(num_pages - 1, -1, -1, **i32)
@@ -155,13 +179,15 @@ class PagedCache:
                rope_theta: float = 5e5, out=None, stream=None):
         """The layer's queries, normed and rotated; its keys and values go to their pages."""
         return qk_norm_rope(qkv, Hq, self.Hkv, self.D, self.positions, self.slots, self.kpool[layer],
-                            self.vpool[layer], q_gamma=q_gamma, k_gamma=k_gamma, eps=eps, rope_theta=rope_theta,
-                            out=out, status=self.status, stream=stream)
+                            self.vpool[layer], kscale=self.kscale[layer], vscale=self.vscale[layer], q_gamma=q_gamma,
+                            k_gamma=k_gamma, eps=eps, rope_theta=rope_theta, out=out, status=self.status,
+                            stream=stream)
 
     def attention(self, layer: int, q, max_new: int, *, scale: float = None, out=None, stream=None):
         """Attention of the planned step's tokens over the layer's pages."""
         return attention(q, self.kpool[layer], self.vpool[layer], self.table, self.cu, self.ctx_len, max_new,
-                         scale=scale, out=out, status=self.status, stream=stream)
+                         kscale=self.kscale[layer], vscale=self.vscale[layer], scale=scale, out=out,
+                         status=self.status, stream=stream)
 
     def check(self):
         """Wait for the device; raise if a step's lengths, pages or slots were wrong, whatever stream it ran on

@@ -1,0 +1,717 @@
+"""The paged cache in 8 bits against plain float64 implementations: the stores
+with a scale for each page and head, attention over e4m3 pages, and a run of
+them together.
+
+Tolerances count roundings.  A stored value is off by half a step of e4m3: 2^-4
+of it, or 2^-10 of the scale where its code is subnormal; f32 arithmetic before
+it as for bf16 pages (2^-17 of the pair's size).  A bf16 result is off by 2^-8 of
+its value.  In attention, with A = sum_j w_j |v_j| (w the softmax weights), a
+relative error e of every weight moves the result by at most 2 e A (numerator and
+sum).  e is 2^-11 for the probabilities' rounding to f16, plus the scores' own
+error: queries lose 2^-17 of a row's largest element where the chunk kernel
+splits them in two e4m3 parts (times sum |k|), D terms are summed in f32 (2^-23
+each, tensor cores truncate) and the exponent is off by 2^-23, both times |score|
+sums.  Probabilities under 2^-28 of the largest lose 2^-39 of it in f16.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from task_graph_interpreter_gb300 import _lib as L
+from task_graph_interpreter_gb300 import paged
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+E4M3 = torch.float8_e4m3fn
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def pow2(e):
+    """2^e in float64, by its bits (a power function may be a rounding off)."""
+    return (e.long() + 1023 << 52).view(torch.float64)
+
+
+def e4m3(x):
+    """float64 rounded to e4m3 values (four significant bits, steps of 2^-9 at least, ties to even)."""
+    _, e = torch.frexp(x)
+    step = pow2((e - 4).clamp(min=-9))
+    return torch.where(torch.isfinite(x), (torch.round(x / step) * step).clamp(-448, 448), x * math.nan)
+
+
+def pow2_scale(amax):
+    m, e = torch.frexp(amax)  # 448 is 0.875 * 2^9
+    return pow2(torch.where(amax > 0, (e - 9 + (m > 0.875)).clamp(min=-126), -126))
+
+
+# ------------------------------------------------------------------ stores
+def turned(x, gamma, pos, eps, theta):
+    """float64 [N, D]: normed (gamma given) and turned, and the size that f32 errors scale with."""
+    D = x.shape[-1]
+    if gamma is not None:
+        x = x / torch.sqrt((x * x).mean(-1, keepdim=True) + eps) * gamma.double()
+    ang = pos.double()[:, None] * theta ** (-2.0 * torch.arange(D // 2, dtype=torch.float64, device=DEV) / D)
+    c, s = torch.cos(ang), torch.sin(ang)
+    a, b = x[:, :D // 2], x[:, D // 2:]
+    size = a.abs() + b.abs()
+    return torch.cat([a * c - b * s, b * c + a * s], -1), torch.cat([size, size], -1)
+
+
+def filled(pages, Hkv, page, D, g, spread=1.0, junk=False):
+    """A pool with pages of different magnitude, and its scales; `junk`: NaN codes and scales instead."""
+    if junk:
+        return (torch.full((pages, Hkv, page, D), 0x7F, dtype=torch.uint8, device=DEV).view(E4M3),
+                torch.full((pages, Hkv), math.nan, device=DEV))
+    x = torch.randn(pages, Hkv, page, D, generator=g, device=DEV) * torch.exp2(
+        spread * torch.randn(pages, Hkv, 1, 1, generator=g, device=DEV))
+    scale = pow2_scale(x.abs().amax((2, 3)).double()).float()
+    return (x / scale[:, :, None, None]).to(E4M3), scale
+
+
+def check_stores(pool, scale, pool0, scale0, rows, slots, x, size, page):
+    """Rows `rows` (in order) of x [N, Hkv, D] float64 were stored at `slots`; everything else stayed."""
+    pages, Hkv, _, D = pool.shape
+    got, was = pool.double(), pool0.double()
+    by_page = {}
+    for r in rows:
+        by_page.setdefault(slots[r] // page, []).append(r)
+    untouched = torch.ones(pages, dtype=torch.bool, device=DEV)
+    for pg, mine in by_page.items():
+        untouched[pg] = False
+        offs = [slots[r] % page for r in mine]
+        v, err = x[mine], 2.0 ** -17 * size[mine]  # [n, Hkv, D]
+        top, slack = v.abs().amax((0, 2)), err.amax((0, 2))
+        lo, hi = pow2_scale((top - slack).clamp(min=0)), pow2_scale(top + slack)
+        old = scale0[pg].double()
+        if 0 not in offs:
+            lo, hi = torch.maximum(lo, old), torch.maximum(hi, old)
+        s = scale[pg].double()
+        assert bool(((s == lo) | (s == hi)).all()), (pg, s, lo, hi)
+        want, tol = v, (2.0 ** -4 * v.abs()).maximum(2.0 ** -10 * s[:, None].expand_as(v)) + err * 1.1
+        assert bool(((got[pg][:, offs].transpose(0, 1) * s[:, None] - want).abs() <= tol).all()), pg
+        below = [o for o in range(max(offs)) if o not in offs]
+        above = [o for o in range(max(offs) + 1, page)]
+        held = was[pg][:, below]
+        if 0 not in offs:
+            again = e4m3(held * (old / s)[:, None, None])
+            held = torch.where((s != old)[:, None, None], again, held)
+            differ = int((torch.nan_to_num(got[pg][:, below], nan=1e9) != torch.nan_to_num(held, nan=1e9)).sum())
+            assert differ == 0, pg
+        a, b = pool.view(torch.uint8)[pg][:, above], pool0.view(torch.uint8)[pg][:, above]
+        assert torch.equal(a, b)
+    assert torch.equal(pool.view(torch.uint8)[untouched], pool0.view(torch.uint8)[untouched])
+    assert torch.equal(scale[untouched].view(torch.int32), scale0[untouched].view(torch.int32))
+
+
+def store_case(ctx, new, Hq, Hkv, D, page, dtype, norm, seed, pad=0, strided=False, gaps=0, junk=False, spread=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    rng = np.random.default_rng(seed)
+    slots, pos = [], []
+    need = [-(-(c + n) // page) - c // page if n else 0 for c, n in zip(ctx, new)]
+    pages = sum(need) + 3
+    ids, at = rng.permutation(pages).tolist(), 0
+    for c, n, k in zip(ctx, new, need):
+        for t in range(n):
+            p = c + t
+            slots.append(ids[at + p // page - c // page] * page + p % page)
+            pos.append(p)
+            if gaps and rng.random() < 0.2:  # rows between a request's that are left out, or not stored
+                for _ in range(int(rng.integers(1, gaps + 1))):
+                    left = rng.random() < 0.5
+                    slots.append(7 if left else -1)
+                    pos.append(-1 if left else 5)
+        at += k
+    slots += [-1] * pad
+    pos += [-1] * pad
+    N, width = len(slots), (Hq + 2 * Hkv) * D
+    qkv = torch.randn(N, width + (24 if strided else 0), device=DEV, generator=g).to(dtype)[:, :width]
+    gq, gk = ((1 + 0.1 * torch.randn(D, device=DEV, generator=g)).bfloat16() if w in norm else None for w in "qk")
+    kpool, kscale = filled(pages, Hkv, page, D, g, spread, junk)
+    vpool, vscale = filled(pages, Hkv, page, D, g, spread, junk)
+    return dict(qkv=qkv, pos=pos, slots=slots, gq=gq, gk=gk, kpool=kpool, vpool=vpool, kscale=kscale, vscale=vscale)
+
+
+def run_store(c, Hq, Hkv, D, page, check=True, eps=1e-5, theta=5e5, status=None):
+    qkv, N = c["qkv"], len(c["slots"])
+    kp, vp, ks, vs = (c[k].clone() for k in ("kpool", "vpool", "kscale", "vscale"))
+    out = torch.full((N, Hq + 1, D), 7.0, dtype=torch.bfloat16, device=DEV)[:, :Hq]
+    st = i32([0]) if status is None else status
+    paged.qk_norm_rope(qkv, Hq, Hkv, D, i32(c["pos"]), i32(c["slots"]), kp, vp, kscale=ks, vscale=vs, q_gamma=c["gq"],
+                       k_gamma=c["gk"], eps=eps, rope_theta=theta, out=out, status=st)
+    if check:
+        assert int(st) == 0
+        x = qkv.double().view(N, Hq + 2 * Hkv, D)
+        live = [r for r in range(N) if c["pos"][r] >= 0]
+        rows = [r for r in live if c["slots"][r] >= 0]
+        pos = torch.tensor(c["pos"], device=DEV).clamp(min=0)
+        for h in range(Hq):
+            want, size = turned(x[:, h], c["gq"], pos, eps, theta)
+            tol = 2.0 ** -8 * want.abs() + 2.0 ** -17 * size + 1e-30
+            assert bool(((out[:, h].double() - want).abs() <= tol)[live].all()), h
+        dead = [r for r in range(N) if c["pos"][r] < 0]
+        assert bool((out[dead] == 7.0).all())
+        k = [turned(x[:, Hq + h], c["gk"], pos, eps, theta) for h in range(Hkv)]
+        kx, ksize = (torch.stack([a[i] for a in k], 1) for i in (0, 1))
+        v = x[:, Hq + Hkv:]
+        check_stores(kp, ks, c["kpool"], c["kscale"], rows, c["slots"], kx, ksize, page)
+        check_stores(vp, vs, c["vpool"], c["vscale"], rows, c["slots"], v, torch.zeros_like(v), page)
+    return out, kp, vp, ks, vs
+
+
+F32, BF = torch.float32, torch.bfloat16
+STORES = [  # ctx, new, Hq, Hkv, D, page, dtype, norm, pad, strided, gaps
+    ([0], [1], 32, 8, 128, 64, F32, "qk", 0, False, 0), ([5], [1], 4, 2, 64, 16, F32, "", 3, True, 0),
+    ([15, 16, 17, 31, 0], [1] * 5, 12, 12, 64, 16, BF, "k", 0, False, 0),
+    ([15, 16, 17, 31, 0, 200], [2, 1, 3, 40, 33, 1], 28, 4, 128, 32, F32, "qk", 23, True, 0),
+    ([2 ** 31 - 300], [250], 8, 1, 128, 64, F32, "q", 0, False, 0), ([63, 64, 1], [64, 65, 130], 6, 2, 128, 64, BF, "qk", 5, True, 0),
+    ([100, 0], [300, 256], 4, 1, 128, 256, BF, "k", 0, False, 0), ([255, 3], [257, 300], 3, 1, 64, 128, F32, "qk", 1, False, 0),
+    ([0], [700], 3, 3, 64, 16, BF, "", 0, False, 0), (list(range(100, 220)), [1] * 120, 8, 2, 128, 16, BF, "qk", 8, False, 0),
+    ([17, 30, 0], [40, 100, 64], 4, 2, 128, 64, BF, "qk", 0, False, 3), ([3, 250, 9], [90, 1, 50], 4, 2, 64, 256, F32, "k", 4, True, 15),
+    ([0] * 30, list(range(1, 31)), 2, 1, 64, 32, BF, "qk", 0, False, 0)]
+
+
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D,page,dtype,norm,pad,strided,gaps", STORES)
+def test_stores_match_float64(ctx, new, Hq, Hkv, D, page, dtype, norm, pad, strided, gaps):
+    c = store_case(ctx, new, Hq, Hkv, D, page, dtype, norm, len(ctx) * 31 + page, pad, strided, gaps)
+    run_store(c, Hq, Hkv, D, page)
+
+
+@pytest.mark.parametrize("spread", [0.0, 12.0])
+def test_scales_far_below_and_above_the_new_values(spread):
+    """Pages begun with scales of 2^-40 to 2^40 times the new values', held codes become subnormal or zero."""
+    c = store_case([7, 33, 50, 100, 3], [3, 1, 20, 40, 2], 4, 2, 128, 32, F32, "qk", 5, spread=spread)
+    run_store(c, 4, 2, 128, 32)
+
+
+def test_pages_whose_first_token_is_new_forget_what_they_held():
+    c = store_case([0, 32, 64], [5, 32, 70], 4, 2, 128, 32, BF, "qk", 9, junk=True)
+    out, kp, vp, ks, vs = run_store(c, 4, 2, 128, 32)
+    touched = sorted({s // 32 for s in c["slots"]})
+    assert torch.isfinite(ks[touched]).all() and torch.isfinite(vs[touched]).all()
+
+
+@pytest.mark.parametrize("page,cuts", [(16, [1] * 40), (32, [3, 30, 1, 40, 2]), (64, [64, 1, 1, 62, 20]), (256, [100, 100, 90])])
+def test_a_cache_filled_in_steps_holds_what_one_call_stores(page, cuts):
+    """Codes and scales do not depend on the steps but where a code became subnormal on the way (off by 2^-9 then)."""
+    n, Hq, Hkv, D = sum(cuts), 4, 2, 128
+    c = store_case([0], [n], Hq, Hkv, D, page, F32, "qk", 3, junk=True)
+    whole = run_store(c, Hq, Hkv, D, page)
+    step = dict(c)
+    at = 0
+    for k in cuts:
+        part = dict(step, qkv=c["qkv"][at:at + k], pos=c["pos"][at:at + k], slots=c["slots"][at:at + k])
+        out, *now = run_store(part, Hq, Hkv, D, page, check=False)
+        assert torch.equal(out, whole[0][at:at + k])
+        step.update(zip(("kpool", "vpool", "kscale", "vscale"), now))
+        at += k
+    last = c["slots"][-1]
+    for pool, scale, p1, s1 in ((step["kpool"], step["kscale"], whole[1], whole[3]), (step["vpool"], step["vscale"], whole[2], whole[4])):
+        for pg in {s // page for s in c["slots"]}:
+            m = last % page + 1 if pg == last // page else page
+            assert torch.equal(scale[pg], s1[pg])
+            # a code rounded twice: half a subnormal step more
+            assert float((pool[pg, :, :m].float() - p1[pg, :, :m].float()).abs().max()) <= 2.0 ** -9
+
+
+def test_values_that_are_not_finite_are_stored_as_nan():
+    c = store_case([0, 20], [20, 30], 4, 2, 64, 32, F32, "", 4)
+    c["qkv"][3, (4 + 2) * 64 + 7] = math.inf   # value head 0
+    c["qkv"][4, (4 + 3) * 64 + 9] = -math.inf  # value head 1
+    c["qkv"][30, (4 + 2) * 64 + 1] = math.nan
+    c["qkv"][5, 4 * 64 + 5] = math.inf         # key head 0: its pair turns into inf or NaN
+    out, kp, vp, ks, vs = run_store(c, 4, 2, 64, 32, check=False)
+    at = lambda pool, r, h: pool.float()[c["slots"][r] // 32, h, c["slots"][r] % 32]  # noqa: E731
+    assert torch.isfinite(ks[[s // 32 for s in c["slots"]]]).all() and torch.isfinite(vs[[s // 32 for s in c["slots"]]]).all()
+    for r, h, d in ((3, 0, 7), (4, 1, 9), (30, 0, 1)):
+        row = at(vp, r, h)
+        assert math.isnan(row[d]) and torch.isfinite(torch.cat([row[:d], row[d + 1:]])).all()
+    row = at(kp, 5, 0)
+    assert torch.isnan(row[[5, 37]]).all() and int(torch.isnan(row).sum()) == 2
+
+
+def test_zero_and_tiny_and_huge_values():
+    c = store_case([0, 0, 0], [4, 4, 4], 1, 1, 64, 16, F32, "", 4)
+    c["qkv"][:4] = 0
+    c["qkv"][4:8] *= 1e-38
+    c["qkv"][8:] *= 1e36
+    out, kp, vp, ks, vs = run_store(c, 1, 1, 64, 16)
+    assert float(vs[c["slots"][0] // 16, 0]) == 2.0 ** -126 and bool((vp.float()[c["slots"][0] // 16, 0, :4] == 0).all())
+
+
+def test_rows_that_go_back_in_a_page_and_slots_outside_the_pool_are_reported():
+    c = store_case([0], [8], 2, 1, 64, 16, F32, "", 4)
+    base = c["slots"][0]
+    for slots, stored in (([0, 1, 2, 2, 3, 4, 5, 6], 3), ([4, 5, 3, 4, 6, 7, 8, 9], 2), ([0, 1, 10 ** 6, 2 ** 31 - 1], 2)):
+        c2 = dict(c, qkv=c["qkv"][:len(slots)], pos=c["pos"][:len(slots)],
+                  slots=[base + s if s < 16 else s for s in slots])
+        status = i32([0])
+        out, kp, vp, ks, vs = run_store(c2, 2, 1, 64, 16, check=False, status=status)
+        assert int(status) == L.MK_DEV_BAD_INDEX
+        keep = dict(c2, pos=c2["pos"][:stored], slots=c2["slots"][:stored], qkv=c2["qkv"][:stored])
+        out2, kp2, vp2, ks2, vs2 = run_store(keep, 2, 1, 64, 16)
+        assert torch.equal(kp.view(torch.uint8), kp2.view(torch.uint8)) and torch.equal(vs, vs2)
+        assert torch.equal(vp.view(torch.uint8), vp2.view(torch.uint8)) and torch.equal(ks, ks2)
+
+
+# ------------------------------------------------------------------ attention
+def attention_case(ctx, new, Hq, Hkv, D, page, seed, spread=1.0, spare=3):
+    """Codes of requests on scattered pages of different scales; what no request holds is NaN, scales too."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    need = [-(-(c + n) // page) for c, n in zip(ctx, new)]
+    pages = sum(need) + spare
+    ids = torch.randperm(pages, device=DEV, generator=g)
+    width = max(need + [1]) + 1
+    table = torch.full((len(ctx), width), -1, dtype=torch.int32, device=DEV)
+    pools, scales = [], []
+    for _ in range(2):
+        pool, scale = filled(pages, Hkv, page, D, g, spread)
+        held = torch.zeros(pages, page, dtype=torch.bool, device=DEV)
+        at = 0
+        for b, (c, n) in enumerate(zip(ctx, new)):
+            mine = ids[at:at + need[b]]
+            at += need[b]
+            table[b, :need[b]] = mine.int()
+            held[mine] = torch.arange(need[b] * page, device=DEV).view(-1, page) < c + n
+        pool = pool.view(torch.uint8).masked_fill_(~held[:, None, :, None], 0x7F).view(E4M3)
+        scale[~held.any(1)] = math.nan
+        pools.append(pool)
+        scales.append(scale)
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    q = (1.5 * torch.randn(cu[-1], Hq, D, device=DEV, generator=g)).bfloat16()
+    return q, pools[0], pools[1], scales[0], scales[1], table, cu
+
+
+def attention_ref(q, kpool, vpool, ks, vs, table, cu, ctx, page, scale, lost=()):
+    """float64 (result, sum of weights times |v|, relative error of weights); `lost`: (request, page index) left out."""
+    Hq, D = q.shape[1:]
+    Hkv = kpool.shape[1]
+    G = Hq // Hkv
+    out, size = (torch.zeros(q.shape, dtype=torch.float64, device=DEV) for _ in range(2))
+    reach = lose = top = 0.0
+    for b in range(len(ctx)):
+        n = cu[b + 1] - cu[b]
+        if n == 0:
+            continue
+        Lb = ctx[b] + n
+        ids = table[b, : -(-Lb // page)].long().clamp(0, kpool.shape[0] - 1)
+        k, v = ((p.view(torch.uint8)[ids].view(E4M3).double() * s[ids].double()[:, :, None, None]).permute(1, 0, 2, 3)
+                .reshape(Hkv, -1, D)[:, :Lb] for p, s in ((kpool, ks), (vpool, vs)))
+        j = torch.arange(Lb, device=DEV)
+        see = j[None] <= ctx[b] + torch.arange(n, device=DEV)[:, None]
+        for (rb, rj) in lost:
+            if rb == b:
+                see &= (j // page != rj)[None]
+        qb = q[cu[b]:cu[b + 1]].double()
+        for h in range(Hq):
+            s = (qb[:, h] @ k[h // G].T * scale).masked_fill(~see, -math.inf)
+            w = torch.nan_to_num(torch.softmax(s, -1))  # a row that sees no key is zero
+            w = torch.where(see, w, 0.0)
+            vv = torch.where(see.any(0)[:, None], v[h // G], 0.0)
+            out[cu[b]:cu[b + 1], h] = w @ vv
+            size[cu[b]:cu[b + 1], h] = w @ vv.abs()
+            a = (qb[:, h].abs() @ k[h // G].abs().T * scale).masked_fill(~see, 0.0)
+            reach = max(reach, float(torch.nan_to_num(a).max()))
+            cut = qb[:, h].abs().amax(-1)[:, None] * k[h // G].abs().sum(-1)[None] * scale
+            lose = max(lose, float(torch.nan_to_num(cut.masked_fill(~see, 0.0)).max()))
+            top = max(top, float(torch.nan_to_num(vv).abs().max()))
+    return out, size, 2.0 ** -11 + reach * (D + 4) * 2.0 ** -23 + lose * 2.0 ** -17, top
+
+
+def close(got, want, size, e, top):
+    tol = 2.0 ** -8 * want.abs() + 2 * e * size + 2.0 ** -38 * top + 1e-30
+    err = (got.double() - want).abs()
+    assert torch.isfinite(got).all()
+    assert bool((err <= tol).all()), f"max excess {float((err - tol).max())}, max error {float(err.max())}"
+
+
+FEW = [  # ctx, new, Hq, Hkv, D, page
+    ([0], [1], 4, 2, 64, 16), ([0], [1], 32, 8, 128, 64), ([1], [1], 8, 1, 128, 16), ([4096], [1], 32, 8, 128, 64),
+    ([31, 32, 33, 63, 64, 65], [1] * 6, 32, 8, 128, 32), ([15, 16, 17, 127, 128, 129], [1] * 6, 12, 12, 64, 16),
+    ([700, 0, 5, 3000, 12], [1, 0, 1, 1, 0], 28, 4, 128, 16), ([1000, 0, 77], [5, 8, 1], 16, 4, 128, 128),
+    ([0, 3, 250], [8, 8, 3], 32, 8, 64, 256), ([333], [1], 32, 1, 64, 32), ([513, 100], [4, 2], 8, 1, 128, 16),
+    ([513, 100], [4, 2], 4, 2, 128, 16), ([30, 31, 32, 33], [8, 7, 6, 5], 3, 3, 64, 16), ([100] * 300, [1] * 300, 4, 2, 64, 16),
+    ([20000, 9], [1, 1], 40, 8, 128, 16)]
+CHUNK = [
+    ([0], [9], 4, 1, 64, 16), ([0], [128], 4, 4, 128, 64), ([0], [129], 12, 12, 64, 16), ([5, 0, 300], [40, 1, 77], 32, 8, 128, 32),
+    ([0, 1000, 0, 64], [700, 33, 0, 256], 32, 4, 64, 16), ([100, 37], [257, 511], 28, 4, 128, 128),
+    ([2000], [64], 8, 1, 128, 256), ([0], [1500], 5, 5, 128, 16), ([127, 128, 129], [127, 128, 129], 6, 2, 64, 64),
+    ([50], [30], 96, 1, 64, 32), ([0] * 40, [33 + i for i in range(40)], 8, 2, 128, 16), ([30000], [5], 32, 8, 128, 16)]
+
+
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D,page", FEW + CHUNK)
+def test_attention_matches_float64(ctx, new, Hq, Hkv, D, page):
+    q, k, v, ks, vs, table, cu = attention_case(ctx, new, Hq, Hkv, D, page, len(ctx) + D)
+    status = i32([0])
+    got = paged.attention(q, k, v, table, i32(cu), i32(ctx), max(new), kscale=ks, vscale=vs, status=status)
+    assert int(status) == 0
+    close(got, *attention_ref(q, k, v, ks, vs, table, cu, ctx, page, D ** -0.5))
+
+
+@pytest.mark.parametrize("new", [[2, 1, 2], [2, 1, 3], [60, 1, 33]])
+def test_attention_strides_and_rows_of_no_request(new):
+    """Queries inside a wider row, outputs apart, rows before, between and behind the requests' own; a scale."""
+    ctx, Hq, Hkv, D, page = [40, 0, 500], 8, 2, 128, 16
+    q0, k, v, ks, vs, table, cu = attention_case(ctx, new, Hq, Hkv, D, page, 11)
+    n = cu[-1]
+    wide = torch.full((n + 9, Hq + 4, D), float("nan"), dtype=torch.bfloat16, device=DEV)
+    wide[3:3 + n, :Hq] = q0
+    out = torch.full((n + 9, Hq + 2, D), 5.0, dtype=torch.bfloat16, device=DEV)
+    got = paged.attention(wide[:, :Hq], k, v, table, i32([c + 3 for c in cu]), i32(ctx), max(new), kscale=ks, vscale=vs,
+                          out=out[:, :Hq], scale=0.2)
+    close(got[3:3 + n], *attention_ref(q0, k, v, ks, vs, table, cu, ctx, page, 0.2))
+    assert torch.all(out[:3] == 5.0) and torch.all(out[3 + n:] == 5.0) and torch.all(out[:, Hq:] == 5.0)
+
+
+@pytest.mark.parametrize("D,page", [(128, 16), (64, 32)])
+@pytest.mark.parametrize("new", [[1, 2, 1], [1, 1, 4], [50, 40, 3]])
+def test_attention_leaves_out_pages_outside_the_pool(new, D, page):
+    ctx, Hq, Hkv = [300, 10, 90], 16, 4
+    q, k, v, ks, vs, table, cu = attention_case(ctx, new, Hq, Hkv, D, page, 12)
+    keep = table.clone()
+    table[0, 3] = -1
+    table[0, 7] = k.shape[0]
+    table[1] = 2 ** 31 - 1   # nothing of the second request is there
+    status = i32([0])
+    got = paged.attention(q, k, v, table, i32(cu), i32(ctx), max(new), kscale=ks, vscale=vs, status=status)
+    assert int(status) == L.MK_DEV_BAD_INDEX
+    lost = [(0, 3), (0, 7)] + [(1, j) for j in range(table.shape[1])]
+    close(got, *attention_ref(q, k, v, ks, vs, keep, cu, ctx, page, D ** -0.5, lost))
+    assert torch.all(got[cu[1]:cu[2]] == 0)
+
+
+@pytest.mark.parametrize("new,few", [([1, 1], True), ([40, 20], False)])
+@pytest.mark.parametrize("what", ["cu", "past", "max_new", "pages", "negative"])
+def test_attention_refuses_lengths_that_do_not_fit(new, few, what):
+    ctx, Hq, Hkv, D, page = [30, 40], 8, 2, 64, 16
+    q, k, v, ks, vs, table, cu = attention_case(ctx, new, Hq, Hkv, D, page, 13)
+    cu2, ctx2, most = list(cu), list(ctx), max(new)
+    if what == "cu":
+        cu2[1] = cu2[2] + 1
+    elif what == "past":
+        cu2[2] += 1
+        most += 1
+    elif what == "max_new":
+        most = 40 if not few else 1
+        cu2 = [0, cu[-1], cu[-1]]
+        if not few:
+            q = torch.cat([q, q])
+            cu2 = [0, 41, 60]
+    elif what == "pages":
+        ctx2[0] = table.shape[1] * page
+    else:
+        ctx2[1] = -1
+    out = torch.full_like(q, 5.0)
+    status = i32([0])
+    paged.attention(q, k, v, table, i32(cu2), i32(ctx2), most, kscale=ks, vscale=vs, out=out, status=status)
+    assert int(status) == L.MK_DEV_BAD_INDEX
+    assert torch.all(out == 5.0)
+
+
+@pytest.mark.parametrize("shift", [3e4, -3e4])
+@pytest.mark.parametrize("new", [[2], [3], [70]])
+def test_attention_with_far_apart_scores(new, shift):
+    """Scores that jump by thousands from key to key (running maxima move, old sums vanish) and rows of equal scores."""
+    ctx, Hq, Hkv, D, page = [400], 4, 1, 128, 16
+    q, k, v, ks, vs, table, cu = attention_case(ctx, new, Hq, Hkv, D, page, 14)
+    q.zero_()
+    q[:, 0, 0] = 1.0
+    q[:, 1, 0] = 64.0
+    ids = table[0, : -(-(ctx[0] + new[0]) // page)].long()
+    flat = torch.arange(ids.numel() * page, device=DEV, dtype=torch.float32)
+    ks[ids, 0] = 2.0 ** 7
+    codes = k.view(torch.uint8)
+    codes[ids, 0, :, 0] = (flat / flat.numel() * shift / 2 ** 7).view(-1, page).to(E4M3).view(torch.uint8)
+    got = paged.attention(q, k, v, table, i32(cu), i32(ctx), max(new), kscale=ks, vscale=vs, scale=1.0)
+    want, size, _, top = attention_ref(q, k, v, ks, vs, table, cu, ctx, page, 1.0)
+    # one product per score, exact in f32; the exponent's error is 2^-23 of the difference to the
+    # maximum, which matters only where that is under 150 or so
+    close(got, want, size, 2.0 ** -11 + 150 * 2.0 ** -22, top)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("key", [70, 71, 127, 128, 133, 134, 197, 198, 255, 256, 369])
+def test_a_nan_reaches_the_rows_that_see_it_and_no_other(key, D):
+    for n in (2, 8, 100, 300):
+        ctx, Hq, Hkv, page = [370 - n], 4, 1, 16
+        q, k, v, ks, vs, table, cu = attention_case(ctx, [n], Hq, Hkv, D, page, 15)
+        run = lambda: paged.attention(q, k, v, table, i32(cu), i32(ctx), n, kscale=ks, vscale=vs)  # noqa: E731
+        clean = run()
+        first = max(0, key - ctx[0])  # the first row that sees the key
+        pg = int(table[0, key // page])
+        v.view(torch.uint8)[pg, 0, key % page, 5] = 0xFF
+        got = run()
+        assert torch.equal(got[:first], clean[:first])
+        assert torch.isnan(got[first:, :, 5]).all()
+        other = [d for d in range(D) if d != 5]
+        assert torch.equal(got[first:][..., other], clean[first:][..., other])
+        k.view(torch.uint8)[pg, 0, key % page, 3] = 0x7F
+        got = run()
+        assert torch.equal(got[:first], clean[:first]) and torch.isnan(got[first:]).all()
+
+
+@pytest.mark.parametrize("n", [2, 60])
+def test_queries_of_every_magnitude_and_queries_that_are_not_finite(n):
+    ctx, Hq, Hkv, D, page = [200], 4, 1, 128, 32
+    q, k, v, ks, vs, table, cu = attention_case(ctx, [n], Hq, Hkv, D, page, 16)
+    q[0] *= 2.0 ** 100
+    q[1] *= 2.0 ** -120
+    ks *= 2.0 ** -104  # scores of the first row are as before, of the others nothing
+    got = paged.attention(q, k, v, table, i32(cu), i32(ctx), n, kscale=ks, vscale=vs)
+    close(got, *attention_ref(q, k, v, ks, vs, table, cu, ctx, page, D ** -0.5))
+    q[0, 1, 7] = math.nan
+    q[1, 2, 9] = math.inf
+    got = paged.attention(q, k, v, table, i32(cu), i32(ctx), n, kscale=ks, vscale=vs)
+    want, size, e, top = attention_ref(torch.nan_to_num(q, posinf=0.0), k, v, ks, vs, table, cu, ctx, page, D ** -0.5)
+    fine = torch.ones(n, Hq, dtype=torch.bool, device=DEV)
+    fine[0, 1] = fine[1, 2] = False
+    assert torch.isnan(got[0, 1]).all() and torch.isnan(got[1, 2]).all()
+    close(got[fine], want[fine], size[fine], e, top)
+
+
+@pytest.mark.parametrize("n", [1, 2, 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_scales_of_every_magnitude(n, D):
+    """Pages whose values' scales are 2^30 apart, zero scales, and scales that are no powers of two."""
+    ctx, Hq, Hkv, page = [500], 4, 1, 16
+    q, k, v, ks, vs, table, cu = attention_case(ctx, [n], Hq, Hkv, D, page, 17, spread=0.0)
+    pages = -(-(500 + n) // page)
+    ids = table[0, :pages].long()
+    factor = torch.exp2(torch.randint(-15, 16, (pages,), device=DEV, generator=torch.Generator(device=DEV).manual_seed(1)).float())
+    vs[ids, 0] *= factor
+    ks[ids[3], 0] = 0.0
+    vs[ids[4], 0] = 0.0
+    args = (q, k, v, table, i32(cu), i32(ctx), n)
+    got = paged.attention(*args, kscale=ks, vscale=vs)
+    want, size, e, top = attention_ref(q, k, v, ks, vs, table, cu, ctx, page, D ** -0.5)
+    # a widened value under 2^-14 loses 2^-25 of the largest scale, of which `top` has at least 1 (its code is 2 or more)
+    close(got, want, size + 2.0 ** -13 * top, e, top)
+    ks[ids, 0] *= 1.3
+    vs[ids, 0] *= 0.77
+    got = paged.attention(*args, kscale=ks, vscale=vs)
+    want, size, e, top = attention_ref(q, k, v, ks, vs, table, cu, ctx, page, D ** -0.5)
+    # the scale's rounding to f16 and the widened value's: 2^-11 each
+    close(got, want, size + 2.0 ** -13 * top, e + 2.0 ** -10, top)
+
+
+@pytest.mark.parametrize("G", [1, 3, 4, 7, 8, 16, 48, 128])
+def test_attention_with_items_cut_at_every_place(G):
+    ctx, new = [1000 + 37 * i for i in range(23)], [1 + i % 3 for i in range(23)]
+    q, k, v, ks, vs, table, cu = attention_case(ctx, new, G, 1, 64, 16, 18)
+    got = paged.attention(q, k, v, table, i32(cu), i32(ctx), 3, kscale=ks, vscale=vs)
+    close(got, *attention_ref(q, k, v, ks, vs, table, cu, ctx, 16, 64 ** -0.5))
+
+
+@pytest.mark.parametrize("Hq,n,D,ctx", [(4, 1, 128, (1 << 22) + 5), (4, 2, 64, 3 << 20), (1, 9, 128, (1 << 22) - 9), (1, 40, 64, 3 << 20)])
+def test_attention_over_millions_of_keys_keeps_its_sums(Hq, n, D, ctx):
+    """Equal scores and values of one: every result is one, whatever the sums have to hold; pages of two scales."""
+    page = 256
+    pages = -(-(ctx + n) // page)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+    k = torch.zeros(pages, 1, page, D, device=DEV).to(E4M3)
+    v = torch.full((pages, 1, page, D), 64.0, device=DEV).to(E4M3)
+    ks = torch.ones(pages, 1, device=DEV)
+    vs = torch.full((pages, 1), 2.0 ** -6, device=DEV)
+    v.view(torch.uint8)[1::2] = torch.full((1,), 256.0, device=DEV).to(E4M3).view(torch.uint8)
+    vs[1::2] = 2.0 ** -8
+    q = torch.ones(n, Hq, D, dtype=torch.bfloat16, device=DEV)
+    got = paged.attention(q, k, v, table, i32([0, n]), i32([ctx]), n, kscale=ks, vscale=vs)
+    # sums by the products lose 2^-22 per 16 keys at most over the 2^16 that they take alone: 2^-10, and half a bf16 step
+    assert float((got.float() - 1).abs().max()) <= 2.0 ** -8
+
+
+@pytest.mark.parametrize("Hq,n,lost", [(4, 1, 300), (1, 9, 300), (1, 40, 600)])
+def test_long_parts_whose_first_pages_are_missing(Hq, n, lost):
+    ctx, D, page = 200 * 256 * 6, 128, 256
+    pages = -(-(ctx + n) // page)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None].clone()
+    table[0, :lost] = -1
+    g = torch.Generator(device=DEV).manual_seed(3)
+    k, ks = filled(pages, 1, page, D, g, 0.2)
+    v, vs = filled(pages, 1, page, D, g, 1.0)
+    q = torch.randn(n, Hq, D, device=DEV, generator=g).bfloat16()
+    got = paged.attention(q, k, v, table, i32([0, n]), i32([ctx]), n, kscale=ks, vscale=vs)
+    keep = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+    close(got, *attention_ref(q, k, v, ks, vs, keep, [0, n], [ctx], page, D ** -0.5, [(0, j) for j in range(lost)]))
+
+
+@pytest.mark.parametrize("new", [[1, 2], [50, 3]])
+def test_offsets_past_32_bits_and_a_shared_prefix(new):
+    """Pools of more than 2^31 (and 2^32) codes, pages at their far end, and pages that two requests list."""
+    Hkv, page, D, ctx = 2, 256, 128, [600, 700]
+    pages = (1 << 32) // (Hkv * page * D) + 64
+    k = torch.zeros(pages, Hkv, page, D, dtype=torch.uint8, device=DEV)
+    v = torch.zeros_like(k)
+    ks, vs = (torch.ones(pages, Hkv, device=DEV) for _ in range(2))
+    g = torch.Generator(device=DEV).manual_seed(1)
+    table = torch.full((2, 5), -1, dtype=torch.int32, device=DEV)
+    ids = torch.arange(pages - 6, pages, dtype=torch.int32, device=DEV)
+    table[0, :3] = ids[:3]
+    table[1, :3] = torch.stack([ids[0], ids[3], ids[4]])
+    for t, s in ((k, ks), (v, vs)):
+        part, sc = filled(6, Hkv, page, D, g)
+        t[-6:] = part.view(torch.uint8)
+        s[-6:] = sc
+    cu = [0, new[0], sum(new)]
+    q = torch.randn(cu[-1], 4, D, device=DEV, generator=g).bfloat16()
+    got = paged.attention(q, k.view(E4M3), v.view(E4M3), table, i32(cu), i32(ctx), max(new), kscale=ks, vscale=vs)
+    near = table.clone()
+    near[table >= 0] -= pages - 6
+    tail = [t[-6:] for t in (k.view(E4M3), v.view(E4M3), ks, vs)]
+    close(got, *attention_ref(q, *tail, near, cu, ctx, page, D ** -0.5))
+    # stores at the far end
+    qkv = torch.randn(3, 8 * D, device=DEV, generator=g)
+    slots = [(pages - 1) * page + 253 + i for i in range(3)]
+    k0 = k[-1].clone()
+    s0 = ks[-1].clone()
+    paged.qk_norm_rope(qkv, 4, Hkv, D, i32([0, 0, 0]), i32(slots), k.view(E4M3), v.view(E4M3), kscale=ks, vscale=vs)
+    x = qkv.double().view(3, 8, D)[:, 4:6]
+    check_stores(k[-1:].view(E4M3), ks[-1:], k0[None].view(E4M3), s0[None], [0, 1, 2], [253, 254, 255], x,
+                 torch.zeros_like(x), page)
+
+
+def test_captured_calls_replay_on_new_inputs_and_repeat_themselves():
+    ctx, new, Hq, Hkv, D, page = [900, 33, 4000], [1, 2, 70], 8, 2, 128, 16
+    for most, lens in ((2, [1, 2, 1]), (70, new)):
+        q, k, v, ks, vs, table, cu = attention_case(ctx, lens, Hq, Hkv, D, page, 21)
+        ws = paged.attention_workspace(most, Hq, Hkv, D)
+        cu_t, ctx_t, out = i32(cu), i32(ctx), torch.zeros_like(q)
+        call = lambda: paged.attention(q, k, v, table, cu_t, ctx_t, most, kscale=ks, vscale=vs, out=out, workspace=ws)  # noqa: E731,B023
+        call()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        q.normal_()
+        graph.replay()
+        first = out.clone()
+        want = attention_ref(q, k, v, ks, vs, table, cu, ctx, page, D ** -0.5)
+        close(first, *want)
+        for _ in range(3):
+            out.zero_()
+            graph.replay()
+            assert torch.equal(out, first)
+        ctx_t.copy_(i32([c - 20 for c in ctx]))
+        graph.replay()
+        got, eager = out.clone(), call().clone()
+        assert torch.equal(got, eager)
+
+
+# ------------------------------------------------------------------ together
+def test_a_serving_loop_over_an_8_bit_cache():
+    """Prompts, decodes, drafts rolled back and finished requests through PagedCache, against a cache of the values that
+    were stored; then what the step answers: log probabilities from its logits."""
+    from task_graph_interpreter_gb300 import logprobs
+    Hq, Hkv, D, page, B = 8, 2, 128, 16, 5
+    cache = paged.PagedCache(2, 60, page, Hkv, D, B, 24, 400, dtype=E4M3)
+    g = torch.Generator(device=DEV).manual_seed(0)
+    head = torch.randn(Hq * D, 1000, device=DEV, generator=g) * 0.1
+    gk = (1 + 0.1 * torch.randn(D, device=DEV, generator=g)).bfloat16()
+    ctx = [0] * B
+    hist = [[torch.zeros(0, 2, Hkv, D, device=DEV, dtype=torch.float64) for _ in range(B)] for _ in range(2)]
+    steps = [[70, 0, 5, 33, 1], [1, 40, 1, 1, 1], [1, 1, 1, 1, 1], [4, 4, 4, 4, 0], [1, 1, 1, 0, 1], [1, 1, 30, 90, 2]]
+    back = {3: [3, 0, 2, 4, 0], 4: [0, 0, 0, 31 + 1 + 1 + 1, 0]}  # tokens rolled back after the step (request 3 ends)
+    for t, new in enumerate(steps):
+        plan = cache.plan(i32(ctx), i32(new))
+        n, cu = sum(new), plan.cu.tolist()
+        x = torch.randn(400, (Hq + 2 * Hkv) * D, device=DEV, generator=g) * (1 + t)
+        for layer in range(2):
+            q = cache.append(layer, x, Hq, k_gamma=gk)
+            out = cache.attention(layer, q, max(new))
+            for b in range(B):
+                pos = torch.arange(ctx[b], ctx[b] + new[b], device=DEV)
+                rows = x[cu[b]:cu[b + 1]].double().view(-1, Hq + 2 * Hkv, D)
+                k = torch.stack([turned(rows[:, Hq + h], gk, pos, 1e-5, 5e5)[0] for h in range(Hkv)], 1)
+                both = torch.stack([k, rows[:, Hq + Hkv:]], 1)
+                hist[layer][b] = torch.cat([hist[layer][b][:ctx[b]], both])
+                Lb = ctx[b] + new[b]
+                if not Lb:
+                    continue
+                ids = cache.table[b, : -(-Lb // page)].long()
+                held = []
+                for i, (pool, scale) in enumerate(((cache.kpool, cache.kscale), (cache.vpool, cache.vscale))):
+                    s = scale[layer][ids].double()[:, :, None, None]
+                    y = (pool[layer].view(torch.uint8)[ids].view(E4M3).double() * s)
+                    y = y.permute(0, 2, 1, 3).reshape(-1, Hkv, D)[:Lb]
+                    step = (s * torch.ones(1, 1, page, 1, device=DEV)).permute(0, 2, 1, 3).reshape(-1, Hkv, 1)[:Lb]
+                    want = hist[layer][b][:Lb, i]
+                    # half a step, twice where the scale grew behind a value (its code became subnormal)
+                    tol = 2.0 ** -4 * want.abs() + 2.0 ** -9 * step + 2.0 ** -16 * want.abs().amax()
+                    assert bool(((y - want).abs() <= tol).all()), (t, layer, b, i)
+                    held.append(y.permute(1, 0, 2))
+                qb, k, v = q[cu[b]:cu[b + 1]].double(), *held
+                see = torch.arange(Lb, device=DEV)[None] <= pos[:, None]
+                for h in range(Hq):
+                    s = (qb[:, h] @ k[h // 4].T * D ** -0.5).masked_fill(~see, -math.inf)
+                    w = torch.softmax(s, -1)
+                    want, size = w @ v[h // 4], w @ v[h // 4].abs()
+                    got = out[cu[b]:cu[b + 1], h].double()
+                    e = 2.0 ** -11 + 2.0 ** -8  # (scores here are under 2^10 in their sums)
+                    assert bool(((got - want).abs() <= 2.0 ** -8 * want.abs() + 2 * e * size + 1e-6).all()), (t, layer, b, h)
+        cache.check()
+        logits = out[:n].float().view(n, -1) @ head
+        tokens = logits.argmax(-1).int()
+        r = logprobs.token_logprobs(logits, tokens, top=3)
+        want = torch.log_softmax(logits.double(), -1)
+        assert torch.equal(r.top_ids[:, 0], tokens)
+        assert float((r.logprobs.double() - want.amax(-1)).abs().max()) < 1e-5
+        ctx = [c + k - b for c, k, b in zip(ctx, new, back.get(t, [0] * B))]
+        if t == 4:
+            ctx[3] = 0
+    cache.plan(i32([0] * B), i32([0] * B))
+    cache.check()
+    assert int(cache.free_count) == 60
+
+
+def test_tensor_functions_refuse_what_does_not_fit():
+    q, k, v, ks, vs, table, cu = attention_case([5], [1], 4, 2, 64, 16, 1)
+    ok = dict(q=q, kpool=k, vpool=v, table=table, cu=i32(cu), ctx_len=i32([5]), max_new=1, kscale=ks, vscale=vs)
+    bf = k.float().bfloat16()
+    for change in (dict(kscale=None), dict(vscale=None), dict(kscale=ks[:, :1]), dict(kscale=ks.double()), dict(vscale=vs.cpu()),
+                   dict(vscale=vs.t().contiguous().t()), dict(kpool=bf), dict(kpool=bf, vpool=bf), dict(kpool=k[:, :, ::2]),
+                   dict(kpool=k.view(torch.uint8), vpool=v.view(torch.uint8)), dict(kscale=3.0),
+                   dict(kscale=ks.clone().requires_grad_())):
+        with pytest.raises(ValueError):
+            paged.attention(**{**ok, **change})
+    qkv = torch.zeros(1, 8 * 64, device=DEV)
+    ok = dict(qkv=qkv, Hq=4, Hkv=2, D=64, positions=i32([0]), slots=i32([0]), kpool=k, vpool=v, kscale=ks, vscale=vs)
+    for change in (dict(kscale=None), dict(vscale=vs[:1]), dict(kpool=bf, vpool=bf), dict(vpool=bf), dict(kscale=ks.half())):
+        with pytest.raises(ValueError):
+            paged.qk_norm_rope(**{**ok, **change})
+    with pytest.raises(ValueError):
+        paged.PagedCache(1, 4, 16, 2, 64, 2, 2, 8, dtype=torch.float16)
+    with pytest.raises(L.MkError):
+        paged.attention(**{**dict(q=q, kpool=k, vpool=v, table=table, cu=i32(cu), ctx_len=i32([5]), max_new=0, kscale=ks,
+                                  vscale=vs)})
+
+
+def test_empty_calls():
+    q, k, v, ks, vs, table, cu = attention_case([5], [1], 4, 2, 64, 16, 1)
+    none = paged.attention(q[:0], k, v, table, i32([0, 0]), i32([5]), 1, kscale=ks, vscale=vs)
+    assert none.shape == (0, 4, 64)
+    out = torch.full_like(q, 3.0)
+    paged.attention(q, k, v, table, i32([0, 0]), i32([5]), 1, kscale=ks, vscale=vs, out=out)
+    assert torch.all(out == 3.0)
+    r = paged.qk_norm_rope(torch.zeros(0, 8 * 64, device=DEV), 4, 2, 64, i32([]), i32([]), k, v, kscale=ks, vscale=vs)
+    assert r.shape == (0, 4, 64)
+
+
+def test_calls_on_another_stream_and_two_workspaces():
+    a = attention_case([5000, 40], [1, 1], 32, 8, 128, 16, 31)
+    b = attention_case([700, 90], [60, 33], 32, 8, 128, 16, 32)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    cases = [(a, [5000, 40], 1), (b, [700, 90], 60)]
+    dev = [(i32(c[6]), i32(ctx)) for c, ctx, _ in cases]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        got = [paged.attention(c[0], c[1], c[2], c[5], cu, cx, m, kscale=c[3], vscale=c[4], stream=s)
+               for (c, _, m), (cu, cx), s in zip(cases, dev, streams)]
+    torch.cuda.synchronize()
+    for (c, ctx, m), g in zip(cases, got):
+        close(g, *attention_ref(c[0], c[1], c[2], c[3], c[4], c[5], c[6], ctx, 16, 128 ** -0.5))
