@@ -39,7 +39,7 @@ using namespace ptx;
 
 constexpr int kThreads = 512;
 // registers: the launch's 4 x 128 threads x 128, moved to the softmax warpgroups
-constexpr int kLaunchRegs = 128, kConsumerRegs = 184, kOtherRegs = 72, kWidenRegs = 72;
+constexpr int kLaunchRegs = 128, kConsumerRegs = 160, kOtherRegs = 96, kWidenRegs = 96;
 static_assert(2 * kConsumerRegs + kOtherRegs + kWidenRegs <= 4 * kLaunchRegs, "register shares within the launch's");
 constexpr float kBias = 6.f;  // probabilities are kept times 2^kBias; a row's maximum may lag by 2^8
 
@@ -63,7 +63,8 @@ struct Block {  // what is known of a block of keys
 };
 struct Control {
   uint64_t k_full[4], k_empty[4], raw_full[4], raw_empty[4], v_full[4], v_empty[4], q_full[2], q_ready[2], q_empty[2],
-      s_full[2], p_full[2][2], o_done[2], s_free[2], turn[2], seg_full[kSegRing], seg_empty[kSegRing], drained[2];
+      s_full[2], p_full[2][2], o_done[2], s_free[2], turn[2], seg_full[kSegRing], seg_empty[kSegRing], drained[2],
+      known[8], half_done[2];
   Segment segs[kSegRing];
   int odd[kSegRing];      // a value set aside in this part
   Block blocks[8];        // ring
@@ -207,6 +208,37 @@ __device__ __noinline__ float fold_results(const Attn8Params& p, int D, int slot
   return last ? sum : 0.f;
 }
 
+// The largest of 64 scores, in the exponent of two: 16 columns have one factor.
+__device__ __forceinline__ float most_of(const float (&x)[64], const float* kf) {
+  float top = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float a = fmaxf(fmaxf(x[c * 16], x[c * 16 + 1]), x[c * 16 + 2]);
+    float d = fmaxf(fmaxf(x[c * 16 + 3], x[c * 16 + 4]), x[c * 16 + 5]);
+#pragma unroll
+    for (int e = 6; e < 16; e += 4) {
+      a = fmaxf(fmaxf(a, x[c * 16 + e]), x[c * 16 + e + 1]);
+      if (e + 3 < 16) d = fmaxf(fmaxf(d, x[c * 16 + e + 2]), x[c * 16 + e + 3]);
+    }
+    top = fmaxf(top, fmaxf(a, d) * kf[c]);
+  }
+  return top;
+}
+
+// A row's results in tensor memory times f.
+template <int D>
+__device__ __forceinline__ void rescale(uint32_t to, float f) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    float o[32];
+    tmem_ld32(to + c, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] *= f;
+    tmem_st32(to + c, o);
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk8_kernel(const __grid_constant__ Attn8Params p, const __grid_constant__ CUtensorMap qmap,
@@ -253,7 +285,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl.turn[i], 1);
       mbar_init(&ctl.s_free[i], 4);
       mbar_init(&ctl.o_done[i], 1);
+      mbar_init(&ctl.half_done[i], 1);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&ctl.known[i], 1);
     for (int i = 0; i < kSegRing; ++i) {
       mbar_init(&ctl.seg_full[i], 1);
       mbar_init(&ctl.seg_empty[i], kThreads / 32 - 1);  // every warp but the one that makes them
@@ -305,35 +339,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait_phase(&ctl.v_empty[vst], ((blk / VS) & 1) ^ 1, &patience))) break;
         const Block& b = ctl.blocks[blk & 7];
         const int key = k * 128 + row;
-        const bool there = key < to && !((b.missing >> (row >> p.page_shift)) & 1);
-        const bool watch = key >= from;  // a key that some row of the item does not see
         const float rel = b.vs[min(row >> p.page_shift, 7)] * unit_of(254 - b.ve);
         const __half2 rel2 = __float2half2_rn(rel);
+        // 16 codes of the row, from and to where the swizzles put them
         const uint32_t src = raw0 + rst * S::kCodes + row * D, dst = v0 + vst * S::kValues + row * 128;
-        uint32_t odd = 0;
-#pragma unroll 2
-        for (int c = 0; c < D / 16; ++c) {
-          uint4 v = lds128(src + ((c ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4));
-          uint32_t in[4] = {v.x, v.y, v.z, v.w}, out[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (watch) {
-              const uint32_t nan = nan_codes(in[e]);
-              odd |= nan;
-              in[e] &= ~nan;
-            }
-            widen_e4m3(in[e], out[2 * e], out[2 * e + 1]);
-          }
+        const auto codes = [&](int c) { return lds128(src + ((c ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4)); };
+        const auto put = [&](int c, const uint4& v) {
+          uint32_t out[8];
+          widen_e4m3(v.x, out[0], out[1]);
+          widen_e4m3(v.y, out[2], out[3]);
+          widen_e4m3(v.z, out[4], out[5]);
+          widen_e4m3(v.w, out[6], out[7]);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const __half2 x = __hmul2(*reinterpret_cast<__half2*>(&out[e]), rel2);
-            out[e] = there ? *reinterpret_cast<const uint32_t*>(&x) : 0u;
+            const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&out[e]), rel2);
+            out[e] = *reinterpret_cast<const uint32_t*>(&x);
           }
           const uint32_t d = dst + (c >> 2) * S::kHalf;
           sts128(d + ((((c & 3) * 2) ^ (row & 7)) << 4), make_uint4(out[0], out[1], out[2], out[3]));
           sts128(d + ((((c & 3) * 2 + 1) ^ (row & 7)) << 4), make_uint4(out[4], out[5], out[6], out[7]));
+        };
+        bool odd = false;
+        if (k * 128 + 128 <= from && b.missing == 0) {
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) put(c, codes(c));
+        } else {
+          // keys that were not loaded are zero; a NaN of a key that some row of the item does not see is set aside
+          const bool there = key < to && !((b.missing >> (row >> p.page_shift)) & 1);
+          const auto clean = [&](uint32_t w) {
+            const uint32_t nan = nan_codes(w);
+            odd |= there && nan != 0 && key >= from;
+            return !there ? 0u : key >= from ? w & ~nan : w;
+          };
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            const uint4 v = codes(c);
+            // (a page that is not there has no scale: 0 times 0)
+            put(c, make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w)));
+          }
         }
-        if (odd && there) ctl.odd[sst] = 1;
+        if (odd) ctl.odd[sst] = 1;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -469,7 +514,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             b.ve = ve;
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(&ctl.k_full[kst], bytes);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&ctl.k_full[kst], bytes);
+            mbar_arrive(&ctl.known[blk & 7]);
+          }
           ++nk;
           if (!(ok = wait_phase(&ctl.raw_empty[rst], ((blk / RS) & 1) ^ 1, &patience))) break;
           if (lane == 0) mbar_arrive_expect_tx(&ctl.raw_full[rst], bytes);
@@ -543,6 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int kk = c * 4 + e;  // 16 keys
                 tc_mma_bf16_ts_lo(to, tp + kk * 8, b_lo + kk * 128, vhi, idesc_o, kk != 0 ? 1u : j != 0 ? 1u : 0u);
               }
+              if (c == 0) tc_commit(&ctl.half_done[w]);
               if (c == 1) {
                 tc_commit(&ctl.v_empty[vst]);
                 if (kApart || j + 1 == ntw) tc_commit(&ctl.o_done[w]);
@@ -602,10 +651,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // P V (block j) before S (block j + 1).  A block that this tile does not need is handed back as it comes
             if (j >= 0 && !(ok = wait(&ctl.v_full[vst], (vb / VS) & 1))) break;
             if (j + 1 < nt && !(ok = wait(&ctl.k_full[kst], (kb / KS) & 1))) break;
-            if (pv && !(ok = wait(&ctl.p_full[w][0], np & 1))) break;
             // tile 0 starts; then each block's products of one tile, then of the other
             if (!(ok = wait(&ctl.turn[w], (nturn & 1) ^ (w ^ 1)))) break;
             ++nturn;
+            if (pv && !(ok = wait(&ctl.p_full[w][0], np & 1))) break;
             tc_fence_after();
             if (pv) {
               if (!(ok = values(j, vst))) break;
@@ -642,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    tp = tmem + lanes + kPCol + w * kPStep;
     const int tok_in = row / p.G, head = row % p.G;
     const int per16 = p.page_shift - 4;  // a page has 2^per16 sixteens of keys
-    uint32_t ns = 0, no = 0, blk = 0;
+    uint32_t ns = 0, no = 0, np = 0, blk = 0;  // scores, results seen; P handed over; blocks
     for (uint32_t i = 0;; ++i) {
       const int sst = i % kSegRing;
       if (!wait_phase(&ctl.seg_full[sst], (i / kSegRing) & 1, &patience)) break;
@@ -656,6 +705,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f, rowf = 0.f;
       int ve = 127;
       bool ok = true;
+      // what is known of the next block, read while its scores are on their way
+      float kf[8];
+      uint32_t miss = 0;
+      int now = 127;
+      const auto look = [&](uint32_t n) {
+        if (!wait_phase(&ctl.known[n & 7], (n >> 3) & 1, &patience)) return false;
+        const Block& b = ctl.blocks[n & 7];
+        miss = b.missing;
+        now = b.ve;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) kf[e] = b.ks[e >> per16];
+        return true;
+      };
+      if (nt > 0) ok = look(blk);
       const int fold_slot = s.slot >= 0 ? s.slot : 2 * (int)blockIdx.x + 1;
 #pragma unroll 1
       for (int j = 0, stop = kFold; ok; stop += kFold) {
@@ -663,8 +726,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = wait_phase(&ctl.s_full[w], ns & 1, &patience))) break;
           ++ns;
           tc_fence_after();
-          const Block& b = ctl.blocks[(blk + j) & 7];
-          const uint32_t miss = b.missing;
           if (j >= jm || miss) {
             // scores of keys that the row does not see become -inf where they lie, 32 columns at a time (a loop,
             // for the sake of the code's size)
@@ -687,31 +748,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // softmax scale 2^(e - 134): what a row's scores are worth before the keys' scales
           if (j == 0) rowf = p.scale * unit_of(max((int)ctl.q_exp[i & 1][w][row] - 7, 1));
-          float x[128];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, x + c * 32);
-          float kf[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) kf[e] = fmaxf(b.ks[e >> per16] * rowf, 0x1p-126f);  // (a masked score times 0 is NaN)
+          for (int e = 0; e < 8; ++e) kf[e] = fmaxf(kf[e] * rowf, 0x1p-126f);  // (a masked score times 0 is NaN)
+          float x[64];
+          tmem_ld32(ts, x);
+          tmem_ld32(ts + 32, x + 32);
           tmem_wait_ld();
-          if constexpr (kApart) {  // the next scores may come
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.s_free[w]);
-          }
-          float top = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            float a = fmaxf(fmaxf(x[c * 16], x[c * 16 + 1]), x[c * 16 + 2]);
-            float d = fmaxf(fmaxf(x[c * 16 + 3], x[c * 16 + 4]), x[c * 16 + 5]);
-#pragma unroll
-            for (int e = 6; e < 16; e += 4) {
-              a = fmaxf(fmaxf(a, x[c * 16 + e]), x[c * 16 + e + 1]);
-              if (e + 3 < 16) d = fmaxf(fmaxf(d, x[c * 16 + e + 2]), x[c * 16 + e + 3]);
-            }
-            top = fmaxf(top, fmaxf(a, d) * kf[c]);
-          }
-          const int now = b.ve;
+          float top = most_of(x, kf);
           if (j == 0) {
             m = top;
             ve = now;
@@ -725,35 +768,51 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (__any_sync(0xffffffffu, far || now != ve)) {
               // (at D = 128 the barrier of this block's S covers every product into O)
               const float f = far ? ex2(m - top) : 1.f;
-              const float fo = now - ve > 126 ? 0.f : f * unit_of(127 + ve - now);
-              ve = now;
               if (far) m = top;
               l *= f;
-#pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                float o[32];
-                tmem_ld32(to + c, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= fo;
-                tmem_st32(to + c, o);
-              }
+              rescale<D>(to, now - ve > 126 ? 0.f : f * unit_of(127 + ve - now));
+              ve = now;
             }
           }
-          const float mu = m == -INFINITY ? 0.f : kBias - m;
-          const uint64_t mu2 = pair_f32(mu, mu);
+          float mu = m == -INFINITY ? 0.f : kBias - m;
           uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
+            float* xc = x + (c & 1) * 32;
+            if (c == 2) {
+              // the second half of the scores: its maximum moves the row's only where it is far above the first half's,
+              // whose product is waited for then
+              tmem_wait_ld();
+              if constexpr (kApart) {  // the next scores may come
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.s_free[w]);
+              }
+              top = most_of(x, kf + 4);
+              const bool far = top > m + 8.f;
+              if (__any_sync(0xffffffffu, far)) {
+                if (!(ok = wait_phase(&ctl.half_done[w], np & 1, &patience))) break;
+                tc_fence_after();
+                const float f = far ? ex2(m - top) : 1.f;
+                if (far) m = top;
+                l *= f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] = mul2(sum[e], pair_f32(f, f));
+                rescale<D>(to, f);
+                mu = m == -INFINITY ? 0.f : kBias - m;
+              }
+            }
+            const uint64_t mu2 = pair_f32(mu, mu);
             uint32_t r[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float f = kf[c * 2 + e / 8];
-              const float2 y = unpair_f32(fma2(pair_f32(x[c * 32 + 2 * e], x[c * 32 + 2 * e + 1]), pair_f32(f, f), mu2));
+              const float2 y = unpair_f32(fma2(pair_f32(xc[2 * e], xc[2 * e + 1]), pair_f32(f, f), mu2));
               const float a = ex2(y.x), d = ex2(y.y);
               sum[e & 3] = add2(sum[e & 3], pair_f32(a, d));
               r[e] = pack_f16(a, d);
             }
+            if (c < 2) tmem_ld32(ts + 64 + c * 32, xc);
             tmem_st16(tp + c * 16, r);
             if (c & 1) {  // half of the keys: the product starts on them
               tmem_wait_st();
@@ -762,8 +821,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (lane == 0) mbar_arrive(&ctl.p_full[w][c >> 1]);
             }
           }
+          if (!ok) break;
+          ++np;
           const float2 t = unpair_f32(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
           l += t.x + t.y;
+          if (j + 1 < nt && !(ok = look(blk + j + 1))) break;
         }
         if (!ok || j >= nt) break;
         // O is whole once the next scores are there (at D = 64, once its last product is done)
