@@ -11,12 +11,13 @@
 //
 // The alternatives are the largest of unique 64-bit keys (the logit's order,
 // then the lower index), so their order never depends on the order of work.
-// Each CTA keeps a buffer of candidates: after its first 8192 logits the
-// top-th largest of 64 thread groups' maxima is a lower bound of the top-th
-// largest logit, what exceeds the bound goes to the buffer (about `top` per
-// 8192 logits), and a buffer that fills up is cut down to its `top` largest,
-// which raises the bound.  A key's rank is the number of larger keys, counted
-// by a thread per key.
+// The pass over the row does nothing for them: it leaves each thread's maximum,
+// the top-th largest of 64 thread groups' maxima is a lower bound of the top-th
+// largest logit, and only the logits of threads whose maximum reaches it are
+// looked at again (about `top` of 256 threads; out of the L2), by the whole CTA.
+// Should more reach the bound than there is room for (equal logits), each warp
+// goes through its part with a buffer that is cut down to its `top` largest when
+// it is full.  A key's rank is the number of larger keys, counted by four threads.
 #include <cuda_bf16.h>
 
 #include "paged.h"
@@ -27,11 +28,15 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 256;
-constexpr int kPer = 32;                      // logits of a thread and step
-constexpr int kCap = 2048, kHigh = 512;       // candidates: room, and the count from which they are cut down
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kBytes = 64;                    // logits of a thread and step
+constexpr int kCap = 128;                     // candidates of a warp, where there are too many
 constexpr int kMaxTop = 32, kMaxCluster = 8;
-constexpr int kGroups = 64;                   // groups whose maxima give the first bound
+constexpr int kGroups = 64;                   // groups whose maxima give a bound
+constexpr int kGroupThreads = kThreads / kGroups;
+constexpr int kFew = kWarps * kCap;           // candidates
+constexpr int kFirst = 64;                    // logits that a part is filled up from with -inf
+static_assert(kFew >= (kMaxTop - 1) * kGroupThreads * 8 + 16 && kFew >= kMaxTop + kFirst, "parts of fewer groups than `top` fit");
 
 struct LogprobParams {
   const void* x;
@@ -67,63 +72,79 @@ __device__ __forceinline__ float logit_of(uint64_t key) {
 }
 
 struct Shared {
-  uint64_t buf[kCap], few[kCap / kGroups * kMaxTop], best[kMaxTop], group[kGroups];
+  uint64_t few[kFew], best[kMaxTop], group[kGroups];
   uint64_t all[kMaxCluster][kMaxTop];  // of the first CTA: every part's alternatives, and sums
-  Sums sums[kMaxCluster], warp[kThreads / 32];
+  Sums sums[kMaxCluster], warp[kWarps];
   uint64_t bound;
-  int count, few_count;
+  int few_count, hit_count, odd;
+  uint8_t hits[kThreads];              // threads whose maximum reaches the bound
 };
 
-// The number of keys[0 .. n) larger than `key`.
-__device__ __forceinline__ int rank_of(const uint64_t* keys, int n, uint64_t key) {
+// The number of keys[0 .. n), from `part` on in steps of four, larger than `key`, summed over four lanes.
+__device__ __forceinline__ int rank_of(const uint64_t* keys, int n, uint64_t key, int part) {
   int r = 0;
 #pragma unroll 4
-  for (int i = 0; i < n; ++i) r += keys[i] > key;
-  return r;
+  for (int i = part; i < n; i += 4) r += keys[i] > key;
+  r += __shfl_xor_sync(0xffffffffu, r, 1);
+  return r + __shfl_xor_sync(0xffffffffu, r, 2);
 }
 
 // The top-th largest of 64 thread groups' largest keys: at least `top` keys are as large.  0: fewer groups have one.
+// The whole CTA.
 __device__ __forceinline__ uint64_t group_bound(Shared& sm, uint64_t own, int top) {
-  for (int o = 1; o < kThreads / kGroups; o <<= 1) {
+  static_assert(kGroupThreads == 4, "a group is four lanes, and four threads count a rank");
+#pragma unroll
+  for (int o = 1; o < kGroupThreads; o <<= 1) {
     const uint64_t other = __shfl_xor_sync(0xffffffffu, own, o);
     own = other > own ? other : own;
   }
-  if (threadIdx.x % (kThreads / kGroups) == 0) sm.group[threadIdx.x / (kThreads / kGroups)] = own;
+  if (threadIdx.x % kGroupThreads == 0) sm.group[threadIdx.x / kGroupThreads] = own;
   if (threadIdx.x == 0) sm.bound = 0;
   __syncthreads();
-  if (threadIdx.x < kGroups) {
-    const uint64_t key = sm.group[threadIdx.x];
-    if (key != 0 && rank_of(sm.group, kGroups, key) == top - 1) sm.bound = key;
-  }
+  const int r = rank_of(sm.group, kGroups, own, threadIdx.x % 4);
+  if (own != 0 && r == top - 1 && threadIdx.x % 4 == 0) sm.bound = own;
   __syncthreads();
   return sm.bound;
 }
 
-// best[0 .. top) = the largest of buf[0 .. n), in order, 0 where there are fewer.  The whole CTA.
-__device__ __noinline__ void select(Shared& sm, int n, int top) {
-  const uint64_t* from = sm.buf;
+// best[0 .. top) = the largest of keys[0 .. n), in order, 0 where there are fewer.  The whole CTA; keys are there.
+__device__ __forceinline__ void rank_all(Shared& sm, const uint64_t* keys, int n, int top) {
   if (threadIdx.x < kMaxTop) sm.best[threadIdx.x] = 0;
-  if (n > kThreads) {
-    uint64_t own = 0;
-    for (int i = threadIdx.x; i < n; i += kThreads) own = max(own, sm.buf[i]);
-    const uint64_t bound = group_bound(sm, own, top);
-    if (threadIdx.x == 0) sm.few_count = 0;
-    __syncthreads();
-    // at most top groups reach the bound, with kCap / kGroups keys each
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      const uint64_t key = sm.buf[i];
-      if (key >= bound) sm.few[atomicAdd(&sm.few_count, 1)] = key;
+  __syncthreads();
+  for (int i0 = 0; i0 < n; i0 += kThreads / 4) {
+    const int i = i0 + threadIdx.x / 4;
+    const uint64_t key = i < n ? keys[i] : 0;
+    const int r = rank_of(keys, n, key, threadIdx.x % 4);
+    if (key != 0 && r < top && threadIdx.x % 4 == 0) sm.best[r] = key;
+  }
+  __syncthreads();
+}
+
+// A warp's buffer of n keys cut down to its `top` largest, in order; the last of them.
+__device__ __noinline__ uint64_t cut_down(uint64_t* buf, int n, int top) {
+  const int lane = threadIdx.x % 32;
+  __syncwarp();
+  uint64_t k[kCap / 32], last = 0;
+#pragma unroll
+  for (int i = 0; i < kCap / 32; ++i) k[i] = i * 32 + lane < n ? buf[i * 32 + lane] : 0;
+  __syncwarp();
+  for (int t = 0; t < top; ++t) {
+    uint64_t most = 0;
+#pragma unroll
+    for (int i = 0; i < kCap / 32; ++i) most = k[i] > most ? k[i] : most;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t other = __shfl_xor_sync(0xffffffffu, most, o);
+      most = other > most ? other : most;
     }
-    __syncthreads();
-    from = sm.few;
-    n = sm.few_count;
+#pragma unroll
+    for (int i = 0; i < kCap / 32; ++i)
+      if (k[i] == most) k[i] = 0;
+    if (lane == 0) buf[t] = most;
+    last = most;
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int r = rank_of(from, n, from[i]);
-    if (r < top) sm.best[r] = from[i];
-  }
-  __syncthreads();
+  __syncwarp();
+  return last;
 }
 
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
@@ -142,15 +163,160 @@ __device__ __forceinline__ void widen(const uint4& v, float* f, __nv_bfloat16) {
   f[0] = bf_lo(v.x); f[1] = bf_hi(v.x); f[2] = bf_lo(v.y); f[3] = bf_hi(v.y);
   f[4] = bf_lo(v.z); f[5] = bf_hi(v.z); f[6] = bf_lo(v.w); f[7] = bf_hi(v.w);
 }
+// the largest of a step's logits, NaN left out
+template <int U>
+__device__ __forceinline__ float most_of(const uint4 (&v)[U], float) {
+  float m[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    m[u] = fmaxf(fmaxf(__uint_as_float(v[u].x), __uint_as_float(v[u].y)),
+                 fmaxf(__uint_as_float(v[u].z), __uint_as_float(v[u].w)));
+#pragma unroll
+  for (int u = 1; u < U; ++u) m[0] = fmaxf(m[0], m[u]);
+  return m[0];
+}
+template <int U>
+__device__ __forceinline__ float most_of(const uint4 (&v)[U], __nv_bfloat16) {
+  const auto two = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+  __nv_bfloat162 m[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) m[u] = __hmax2(__hmax2(two(v[u].x), two(v[u].y)), __hmax2(two(v[u].z), two(v[u].w)));
+#pragma unroll
+  for (int u = 1; u < U; ++u) m[0] = __hmax2(m[0], m[u]);
+  return fmaxf(__low2float(m[0]), __high2float(m[0]));
+}
 __device__ __forceinline__ float widen1(float x) { return x; }
 __device__ __forceinline__ float widen1(__nv_bfloat16 x) { return __bfloat162float(x); }
 
+// A CTA's part of a row: logits before the first 16-byte boundary (of the row's first part), vectors, logits behind
+// the last (of its last part).
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) logprob_kernel(const __grid_constant__ LogprobParams p) {
-  constexpr int VEC = 16 / sizeof(T), U = kPer / VEC;
+struct Part {
+  static constexpr int VEC = 16 / sizeof(T);
+  const T* x;          // the row
+  int head, v0, v1;    // index of vector 0's first logit; the part's vectors
+  int lead, trail;     // logits before, and behind the vectors
+  int behind;          // index of the first of those behind
+  __device__ __forceinline__ const uint4* vectors() const { return reinterpret_cast<const uint4*>(x + head); }
+  // the i-th logit that is in no vector, by index; -1: there are fewer
+  __device__ __forceinline__ int end(int i) const { return i < lead ? i : i - lead < trail ? behind + i - lead : -1; }
+};
+
+// Candidates of a part where too many logits reach a bound: every warp's `top` largest, in few[].  The whole CTA.
+template <typename T>
+__device__ __noinline__ int sift(Shared& sm, const Part<T>& p, int top, float bound) {
+  constexpr int VEC = Part<T>::VEC;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  uint64_t* buf = sm.few + warp * kCap;
+  int count = 0, before = INT32_MAX;  // a logit equal to the bound has to lie before this index
+  __syncthreads();
+  const auto offer = [&](float v, int index, bool there) {
+    bool yes = there && (v > bound || (v == bound && index < before));
+    unsigned who = __ballot_sync(0xffffffffu, yes);
+    if (who == 0) return;
+    if (count > kCap - 32) {
+      const uint64_t last = cut_down(buf, count, top);
+      count = top;
+      bound = logit_of(last);
+      before = (int32_t)~(uint32_t)last;
+      yes = there && (v > bound || (v == bound && index < before));
+      who = __ballot_sync(0xffffffffu, yes);
+    }
+    if (yes) buf[count + __popc(who & ((1u << lane) - 1))] = key_of(v, index);
+    count += __popc(who);
+  };
+  for (int v = p.v0 + warp * 32; v < p.v1; v += kThreads) {
+    const bool there = v + lane < p.v1;
+    float f[VEC];
+    widen(there ? __ldg(p.vectors() + v + lane) : make_uint4(0, 0, 0, 0), f, T());
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) offer(f[e], p.head + (v + lane) * VEC + e, there);
+  }
+  if (warp == 0) {
+    const int i = p.end(lane);
+    offer(i >= 0 ? widen1(p.x[i]) : 0.f, i, i >= 0);
+  }
+  if (count > top) {
+    cut_down(buf, count, top);
+    count = top;
+  }
+  if (lane >= count && lane < top) buf[lane] = 0;
+  __syncthreads();
+  // the warps' lists side by side
+  const uint64_t key = threadIdx.x < kWarps * top ? sm.few[threadIdx.x / top * kCap + threadIdx.x % top] : 0;
+  __syncthreads();
+  if (threadIdx.x < kWarps * top) sm.few[threadIdx.x] = key;
+  __syncthreads();
+  return kWarps * top;
+}
+
+// best[0 .. top): a part's largest logits.  `most`: the largest of this thread's (vectors v0 + tid + i * kThreads, and
+// the end tid), `odd` whether there is a NaN among them.  The whole CTA.
+template <typename T>
+__device__ __forceinline__ void alternatives(Shared& sm, const Part<T>& p, int top, float most, bool odd) {
+  constexpr int VEC = Part<T>::VEC;
+  const int tid = threadIdx.x, per = (p.v1 - p.v0 + kThreads - 1) / kThreads;  // vectors of a thread
+  const bool some = p.v0 + tid < p.v1 || p.end(tid) >= 0;
+  const uint64_t least = group_bound(sm, some ? key_of(most, tid) : 0, top);
+  // without a bound, every logit but NaN is a candidate
+  const float bound = least ? logit_of(least) : -INFINITY;
+  if (tid == 0) sm.few_count = sm.hit_count = sm.odd = 0;
+  __syncthreads();
+  const bool finite = least != 0 && bound == -INFINITY;  // (only those over -inf)
+  if (some && (finite ? most > bound : most >= bound)) sm.hits[atomicAdd(&sm.hit_count, 1)] = (uint8_t)tid;
+  if (odd) sm.odd = 1;
+  __syncthreads();
+  const auto offer = [&](float v, int index) {
+    if (!(finite ? v > bound : v >= bound)) return;
+    const int at = atomicAdd(&sm.few_count, 1);
+    if (at < kFew) sm.few[at] = key_of(v, index);
+  };
+  const int items = sm.hit_count * per;
+  constexpr int B = 4;  // loads in flight
+  for (int i0 = tid; i0 < items; i0 += B * kThreads) {
+    uint4 raw[B];
+    int v[B];
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      const int i = i0 + k * kThreads;
+      v[k] = i < items ? p.v0 + sm.hits[i / per] + i % per * kThreads : p.v1;
+      if (v[k] < p.v1) raw[k] = __ldg(p.vectors() + v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      if (v[k] >= p.v1) continue;
+      float f[VEC];
+      widen(raw[k], f, T());
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) offer(f[e], p.head + v[k] * VEC + e);
+    }
+  }
+  const int e = p.end(tid);
+  if (e >= 0) offer(widen1(p.x[e]), e);
+  __syncthreads();
+  int n = sm.few_count;
+  if (n < top && finite && !sm.odd) {
+    // fewer logits than alternatives have a probability: the first ones without follow (of kFirst neighbours fewer
+    // than `top` have one)
+    const int first = p.lead > 0 ? 0 : p.head + p.v0 * VEC;
+    const int end = p.trail > 0 ? p.behind + p.trail : p.head + p.v1 * VEC;
+    __syncthreads();
+    if (tid < kFirst && first + tid < end && widen1(p.x[first + tid]) == -INFINITY)
+      sm.few[atomicAdd(&sm.few_count, 1)] = key_of(-INFINITY, first + tid);
+    __syncthreads();
+    n = sm.few_count;
+  } else if (n > kFew || (n < top && sm.odd)) {
+    n = sift(sm, p, top, bound);
+  }
+  rank_all(sm, sm.few, n, top);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const __grid_constant__ LogprobParams p) {
+  constexpr int VEC = 16 / sizeof(T), U = kBytes / 16;
   constexpr float kLog2e = 1.4426950408889634f;
   __shared__ Shared sm;
-  const int tid = threadIdx.x, C = p.cluster, rank = blockIdx.x % C;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, C = p.cluster, rank = blockIdx.x % C;
   const int64_t row = blockIdx.x / C;
   int token = -1;
   if (p.tokens) {
@@ -158,138 +324,80 @@ __global__ void __launch_bounds__(kThreads, 3) logprob_kernel(const __grid_const
     if (token < 0) return;  // left out (the whole cluster)
   }
   if (C > 1) cluster_arrive();
-  const T* x = static_cast<const T*>(p.x) + row * p.ld;
-  // logits before the first 16-byte boundary, vectors, logits behind the last
-  const int head = min(p.V, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(T));
-  const int nv = (p.V - head) / VEC, tail = p.V - head - nv * VEC;
-  const int per = (nv + C - 1) / C, v0 = min(nv, rank * per), v1 = min(nv, v0 + per);
-  const uint4* xv = reinterpret_cast<const uint4*>(x + head);
-  const int steps = max(1, (v1 - v0 + kThreads * U - 1) / (kThreads * U));
-
-  uint4 raw[U];
+  Part<T> part;
+  {
+    const T* x = static_cast<const T*>(p.x) + row * p.ld;
+    const int head = min(p.V, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(T));
+    const int nv = (p.V - head) / VEC, per = (nv + C - 1) / C;
+    part.x = x;
+    part.head = head;
+    part.v0 = min(nv, rank * per);
+    part.v1 = min(nv, part.v0 + per);
+    part.lead = rank == 0 ? head : 0;
+    part.behind = head + nv * VEC;
+    part.trail = rank == C - 1 ? p.V - part.behind : 0;
+  }
+  const int steps = (part.v1 - part.v0 + kThreads * U - 1) / (kThreads * U);
+  uint4 next[U];
   const uint32_t fill = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;  // -inf
   auto load = [&](int c) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int v = v0 + (c * U + u) * kThreads + tid;
-      raw[u] = v < v1 ? __ldg(xv + v) : make_uint4(fill, fill, fill, fill);
+      const int v = part.v0 + (c * U + u) * kThreads + tid;
+      next[u] = v < part.v1 ? __ldg(part.vectors() + v) : make_uint4(fill, fill, fill, fill);
     }
   };
-  load(0);
-  if (tid == 0) sm.count = 0;
+  if (steps > 0) load(0);
   Sums own = {-INFINITY, 0.f, 0.f};
-  float bound = -INFINITY;   // what a logit has to exceed to be a candidate
-  bool open = true;          // no bound yet
+  if (part.end(tid) >= 0) {  // (at most 14 threads)
+    own.m = widen1(part.x[part.end(tid)]);
+    own.s = ex2((own.m == -INFINITY ? own.m : own.m - own.m) * kLog2e);  // 1, 0 or NaN
+    if (own.m != own.m) own.m = -INFINITY;
+  }
   for (int c = 0; c < steps; ++c) {
-    float f[kPer];
+    uint4 now[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) widen(raw[u], f + u * VEC, T());
+    for (int u = 0; u < U; ++u) now[u] = next[u];
     if (c + 1 < steps) load(c + 1);
-    // at most one of the row's ends: the first part has those before the vectors, the last those behind
-    int ends = -1;
-    if (c == 0 && rank == 0 && tid < head) ends = tid;
-    if (c == steps - 1 && rank == C - 1 && tid >= kThreads / 2 && tid - kThreads / 2 < tail)
-      ends = head + nv * VEC + tid - kThreads / 2;
-    const float fe = ends >= 0 ? widen1(x[ends]) : -INFINITY;
-    float top[4] = {fmaxf(f[0], fe), f[1], f[2], f[3]};
-#pragma unroll
-    for (int e = 4; e < kPer; ++e) top[e & 3] = fmaxf(top[e & 3], f[e]);
-    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    const float most = most_of(now, T());
     if (most > own.m) own = merge(own, {most, 0.f, 0.f});
     const float at = own.m == -INFINITY ? 0.f : own.m;
     const uint64_t at2 = pair_f32(-at, -at), log2 = pair_f32(kLog2e, kLog2e);
     uint64_t s2[2] = {0, 0}, u2[2] = {0, 0};
 #pragma unroll
-    for (int e = 0; e < kPer; e += 2) {
-      const uint64_t d = add2(pair_f32(f[e], f[e + 1]), at2);
-      const float2 t = unpair_f32(mul2(d, log2)), dd = unpair_f32(d);
-      const uint64_t w = pair_f32(ex2(t.x), ex2(t.y));
-      s2[(e >> 1) & 1] = add2(s2[(e >> 1) & 1], w);
-      // (a weight of zero times -inf would be NaN)
-      u2[(e >> 1) & 1] = fma2(w, pair_f32(fmaxf(dd.x, -1e30f), fmaxf(dd.y, -1e30f)), u2[(e >> 1) & 1]);
+    for (int u = 0; u < U; ++u) {
+      float f[VEC];
+      widen(now[u], f, T());
+#pragma unroll
+      for (int e = 0; e < VEC; e += 2) {
+        const uint64_t d = add2(pair_f32(f[e], f[e + 1]), at2);
+        const float2 t = unpair_f32(mul2(d, log2)), dd = unpair_f32(d);
+        const uint64_t w = pair_f32(ex2(t.x), ex2(t.y));
+        s2[(e >> 1) & 1] = add2(s2[(e >> 1) & 1], w);
+        // (a weight of zero times -inf would be NaN)
+        u2[(e >> 1) & 1] = fma2(w, pair_f32(fmaxf(dd.x, -1e30f), fmaxf(dd.y, -1e30f)), u2[(e >> 1) & 1]);
+      }
     }
     const float2 s = unpair_f32(add2(s2[0], s2[1])), u = unpair_f32(add2(u2[0], u2[1]));
     own.s += s.x + s.y;
     own.u += u.x + u.y;
-    if (ends >= 0) {
-      const float w = ex2((fe - at) * kLog2e);
-      own.s += w;
-      own.u += w * fmaxf(fe - at, -1e30f);
-    }
-    if (p.top == 0) continue;
-
-    // candidates: keys from `least` on
-    const int first = head + (v0 + c * U * kThreads + tid) * VEC;
-    auto each = [&](auto&& use) {
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        const int v = v0 + (c * U + e / VEC) * kThreads + tid;
-        if (v < v1) use(f[e], first + (e / VEC) * kThreads * VEC + e % VEC);
-      }
-      if (ends >= 0) use(fe, ends);
-    };
-    uint64_t least;
-    if (open) {
-      uint64_t largest = 0;
-      each([&](float v, int i) {
-        const uint64_t key = key_of(v, i);
-        largest = key > largest ? key : largest;
-      });
-      least = group_bound(sm, largest, p.top);
-      if (least == 0) least = 1;
-    } else {
-      least = ((key_of(bound, 0) >> 32) + 1) << 32;
-    }
-    bool scan = open || most > bound;
-    __syncthreads();  // (everyone has read the last step's count)
-    const int before = sm.count;
-    __syncthreads();
-    for (;;) {
-      if (scan) {
-        each([&](float v, int i) {
-          const uint64_t key = key_of(v, i);
-          if (key >= least) {
-            const int at_buf = atomicAdd(&sm.count, 1);
-            if (at_buf < kCap) sm.buf[at_buf] = key;
-          }
-        });
-      }
-      __syncthreads();
-      const int n = sm.count;
-      if (n <= kCap) break;
-      // too many: the bound rises to what the buffer holds, and this step's logits are looked at again
-      select(sm, kCap, p.top);
-      least = sm.best[p.top - 1];
-      if (tid == 0) sm.count = before;
-      __syncthreads();
-    }
-    const int n = sm.count;
-    if (n > kHigh || open) {
-      select(sm, n, p.top);
-      const uint64_t last = sm.best[p.top - 1];
-      open = last == 0;
-      if (!open) bound = logit_of(last);
-      if (n > kHigh) {
-        if (tid < p.top) sm.buf[tid] = sm.best[tid];
-        if (tid == 0) sm.count = open ? n : p.top;
-      }
-      __syncthreads();
-    }
   }
+  const float most = own.m;
+  const bool odd = own.s != own.s;
 
   // the part's sums
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1)
     own = merge(own, {__shfl_xor_sync(0xffffffffu, own.m, o), __shfl_xor_sync(0xffffffffu, own.s, o),
                       __shfl_xor_sync(0xffffffffu, own.u, o)});
-  if (tid % 32 == 0) sm.warp[tid / 32] = own;
-  __syncthreads();
-  if (p.top > 0) select(sm, sm.count, p.top);
-  if (tid == 0) {
-    for (int w = 1; w < kThreads / 32; ++w) own = merge(own, sm.warp[w]);
-  }
-  __syncwarp();
+  if (lane == 0) sm.warp[warp] = own;
+  if (p.top > 0) alternatives(sm, part, p.top, most, odd);
+  else __syncthreads();
+  own = sm.warp[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) own = merge(own, sm.warp[w]);
   if (C > 1) {
+    __syncwarp();
     cluster_wait();  // the first CTA is there
     if (tid == 0) {
       const uint32_t a = cluster_addr(&sm.sums[rank], 0);
@@ -307,25 +415,26 @@ __global__ void __launch_bounds__(kThreads, 3) logprob_kernel(const __grid_const
     if (rank != 0) return;
     own = sm.sums[0];
     for (int r = 1; r < C; ++r) own = merge(own, sm.sums[r]);
-    if (tid < kMaxTop) sm.best[tid] = 0;
-    __syncthreads();
-    for (int i = tid; i < C * p.top; i += kThreads) {
-      const uint64_t key = sm.all[0][i];
-      const int r = key ? rank_of(sm.all[0], C * p.top, key) : p.top;
-      if (r < p.top) sm.best[r] = key;
+    if (p.top > 0) {
+      const int n = C * p.top;
+      if (n <= kThreads / 4) {
+        rank_all(sm, sm.all[0], n, p.top);
+      } else {
+        const uint64_t key = tid < n ? sm.all[0][tid] : 0, bound = group_bound(sm, key, p.top);
+        if (tid == 0) sm.few_count = 0;
+        __syncthreads();
+        if (key != 0 && key >= bound) sm.few[atomicAdd(&sm.few_count, 1)] = key;
+        __syncthreads();
+        rank_all(sm, sm.few, sm.few_count, p.top);
+      }
     }
-  } else {
-    if (tid == 0) sm.sums[0] = own;
-    __syncthreads();
-    own = sm.sums[0];
   }
-  __syncthreads();
   const float ln_s = logf(own.s);
   if (tid == 0) {
     p.entropy[row] = ln_s - own.u / own.s;
     if (p.tokens) {
       float lp = __uint_as_float(0x7FC00000u);
-      if (token < p.V) lp = (widen1(x[token]) - own.m) - ln_s;
+      if (token < p.V) lp = (widen1(part.x[token]) - own.m) - ln_s;
       else set_status(p.status, MK_DEV_BAD_INDEX);
       p.logprobs[row] = lp;
     }
@@ -377,7 +486,7 @@ extern "C" int mk_token_logprobs(void* stream, int N, int V, const void* logits,
   if (int rc = device_sms("mk_token_logprobs", &sms)) return rc;
   LogprobParams p{logits, ld, tokens, logprobs, entropy, top_logprobs, top_ids, status, V, top, 1};
   // parts of a row while there are SMs without one, none under a step of a CTA
-  while (p.cluster < kMaxCluster && (int64_t)N * p.cluster * 2 <= 4 * sms && V / (2 * p.cluster) >= kThreads * kPer)
+  while (p.cluster < kMaxCluster && (int64_t)N * p.cluster * 2 <= 4 * sms && V / (2 * p.cluster) >= kThreads * kBytes / 4)
     p.cluster *= 2;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return launch_result(logits_dtype == MK_F32 ? launch_logprobs<float>(p, N, s) : launch_logprobs<__nv_bfloat16>(p, N, s),
