@@ -28,15 +28,20 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kBytes = 64;                    // logits of a thread and step
 constexpr int kCap = 128;                     // candidates of a warp, where there are too many
 constexpr int kMaxTop = 32, kMaxCluster = 8;
-constexpr int kGroups = 64;                   // groups whose maxima give a bound
-constexpr int kGroupThreads = kThreads / kGroups;
-constexpr int kFew = kWarps * kCap;           // candidates
+constexpr int kGroups = 64;                   // groups of threads whose maxima give a bound
 constexpr int kFirst = 64;                    // logits that a part is filled up from with -inf
-static_assert(kFew >= (kMaxTop - 1) * kGroupThreads * 8 + 16 && kFew >= kMaxTop + kFirst, "parts of fewer groups than `top` fit");
+// A CTA of THREADS, whose threads take STEP bytes of logits at a time (with the next step's on their way).
+template <typename T_, int THREADS_, int STEP_, int CTAS_>
+struct Shape {
+  using T = T_;
+  static constexpr int THREADS = THREADS_, WARPS = THREADS / 32, STEP = STEP_, CTAS = CTAS_;
+  static constexpr int VEC = 16 / sizeof(T), U = STEP / 16;
+  static constexpr int MATES = THREADS / kGroups;  // threads of a group; threads that count a key's rank
+  static constexpr int FEW = WARPS * kCap;         // candidates
+  static_assert(FEW >= (kMaxTop - 1) * MATES * 8 + 16 && FEW >= kMaxTop + kFirst, "parts of fewer groups than `top` fit");
+};
 
 struct LogprobParams {
   const void* x;
@@ -71,51 +76,57 @@ __device__ __forceinline__ float logit_of(uint64_t key) {
   return __uint_as_float(order & 0x80000000u ? order ^ 0x80000000u : ~order);
 }
 
+template <typename S>
 struct Shared {
-  uint64_t few[kFew], best[kMaxTop], group[kGroups];
+  uint64_t few[S::FEW], best[kMaxTop], group[kGroups];
   uint64_t all[kMaxCluster][kMaxTop];  // of the first CTA: every part's alternatives, and sums
-  Sums sums[kMaxCluster], warp[kWarps];
+  Sums sums[kMaxCluster], warp[S::WARPS];
   uint64_t bound;
   int few_count, hit_count, odd;
-  uint8_t hits[kThreads];              // threads whose maximum reaches the bound
+  uint8_t hits[S::THREADS];            // threads whose maximum reaches the bound
 };
 
-// The number of keys[0 .. n), from `part` on in steps of four, larger than `key`, summed over four lanes.
-__device__ __forceinline__ int rank_of(const uint64_t* keys, int n, uint64_t key, int part) {
+// The number of keys[0 .. n) larger than `key`, counted by MATES neighbouring lanes.
+template <int MATES>
+__device__ __forceinline__ int rank_of(const uint64_t* keys, int n, uint64_t key) {
   int r = 0;
 #pragma unroll 4
-  for (int i = part; i < n; i += 4) r += keys[i] > key;
-  r += __shfl_xor_sync(0xffffffffu, r, 1);
-  return r + __shfl_xor_sync(0xffffffffu, r, 2);
+  for (int i = threadIdx.x % MATES; i < n; i += MATES) r += keys[i] > key;
+#pragma unroll
+  for (int o = 1; o < MATES; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+  return r;
 }
 
 // The top-th largest of 64 thread groups' largest keys: at least `top` keys are as large.  0: fewer groups have one.
 // The whole CTA.
-__device__ __forceinline__ uint64_t group_bound(Shared& sm, uint64_t own, int top) {
-  static_assert(kGroupThreads == 4, "a group is four lanes, and four threads count a rank");
+template <typename S>
+__device__ __forceinline__ uint64_t group_bound(Shared<S>& sm, uint64_t own, int top) {
+  constexpr int MATES = S::MATES;
 #pragma unroll
-  for (int o = 1; o < kGroupThreads; o <<= 1) {
+  for (int o = 1; o < MATES; o <<= 1) {
     const uint64_t other = __shfl_xor_sync(0xffffffffu, own, o);
     own = other > own ? other : own;
   }
-  if (threadIdx.x % kGroupThreads == 0) sm.group[threadIdx.x / kGroupThreads] = own;
+  if (threadIdx.x % MATES == 0) sm.group[threadIdx.x / MATES] = own;
   if (threadIdx.x == 0) sm.bound = 0;
   __syncthreads();
-  const int r = rank_of(sm.group, kGroups, own, threadIdx.x % 4);
-  if (own != 0 && r == top - 1 && threadIdx.x % 4 == 0) sm.bound = own;
+  const int r = rank_of<MATES>(sm.group, kGroups, own);
+  if (own != 0 && r == top - 1 && threadIdx.x % MATES == 0) sm.bound = own;
   __syncthreads();
   return sm.bound;
 }
 
 // best[0 .. top) = the largest of keys[0 .. n), in order, 0 where there are fewer.  The whole CTA; keys are there.
-__device__ __forceinline__ void rank_all(Shared& sm, const uint64_t* keys, int n, int top) {
+template <typename S>
+__device__ __forceinline__ void rank_all(Shared<S>& sm, const uint64_t* keys, int n, int top) {
+  constexpr int MATES = S::MATES;
   if (threadIdx.x < kMaxTop) sm.best[threadIdx.x] = 0;
   __syncthreads();
-  for (int i0 = 0; i0 < n; i0 += kThreads / 4) {
-    const int i = i0 + threadIdx.x / 4;
+  for (int i0 = 0; i0 < n; i0 += kGroups) {
+    const int i = i0 + threadIdx.x / MATES;
     const uint64_t key = i < n ? keys[i] : 0;
-    const int r = rank_of(keys, n, key, threadIdx.x % 4);
-    if (key != 0 && r < top && threadIdx.x % 4 == 0) sm.best[r] = key;
+    const int r = rank_of<MATES>(keys, n, key);
+    if (key != 0 && r < top && threadIdx.x % MATES == 0) sm.best[r] = key;
   }
   __syncthreads();
 }
@@ -192,7 +203,6 @@ __device__ __forceinline__ float widen1(__nv_bfloat16 x) { return __bfloat162flo
 // the last (of its last part).
 template <typename T>
 struct Part {
-  static constexpr int VEC = 16 / sizeof(T);
   const T* x;          // the row
   int head, v0, v1;    // index of vector 0's first logit; the part's vectors
   int lead, trail;     // logits before, and behind the vectors
@@ -203,9 +213,10 @@ struct Part {
 };
 
 // Candidates of a part where too many logits reach a bound: every warp's `top` largest, in few[].  The whole CTA.
-template <typename T>
-__device__ __noinline__ int sift(Shared& sm, const Part<T>& p, int top, float bound) {
-  constexpr int VEC = Part<T>::VEC;
+template <typename S>
+__device__ __noinline__ int sift(Shared<S>& sm, const Part<typename S::T>& p, int top, float bound) {
+  using T = typename S::T;
+  constexpr int VEC = S::VEC, kWarps = S::WARPS, kThreads = S::THREADS;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   uint64_t* buf = sm.few + warp * kCap;
   int count = 0, before = INT32_MAX;  // a logit equal to the bound has to lie before this index
@@ -252,9 +263,10 @@ __device__ __noinline__ int sift(Shared& sm, const Part<T>& p, int top, float bo
 
 // best[0 .. top): a part's largest logits.  `most`: the largest of this thread's (vectors v0 + tid + i * kThreads, and
 // the end tid), `odd` whether there is a NaN among them.  The whole CTA.
-template <typename T>
-__device__ __forceinline__ void alternatives(Shared& sm, const Part<T>& p, int top, float most, bool odd) {
-  constexpr int VEC = Part<T>::VEC;
+template <typename S>
+__device__ __forceinline__ void alternatives(Shared<S>& sm, const Part<typename S::T>& p, int top, float most, bool odd) {
+  using T = typename S::T;
+  constexpr int VEC = S::VEC, kThreads = S::THREADS;
   const int tid = threadIdx.x, per = (p.v1 - p.v0 + kThreads - 1) / kThreads;  // vectors of a thread
   const bool some = p.v0 + tid < p.v1 || p.end(tid) >= 0;
   const uint64_t least = group_bound(sm, some ? key_of(most, tid) : 0, top);
@@ -269,7 +281,7 @@ __device__ __forceinline__ void alternatives(Shared& sm, const Part<T>& p, int t
   const auto offer = [&](float v, int index) {
     if (!(finite ? v > bound : v >= bound)) return;
     const int at = atomicAdd(&sm.few_count, 1);
-    if (at < kFew) sm.few[at] = key_of(v, index);
+    if (at < S::FEW) sm.few[at] = key_of(v, index);
   };
   const int items = sm.hit_count * per;
   constexpr int B = 4;  // loads in flight
@@ -305,17 +317,18 @@ __device__ __forceinline__ void alternatives(Shared& sm, const Part<T>& p, int t
       sm.few[atomicAdd(&sm.few_count, 1)] = key_of(-INFINITY, first + tid);
     __syncthreads();
     n = sm.few_count;
-  } else if (n > kFew || (n < top && sm.odd)) {
+  } else if (n > S::FEW || (n < top && sm.odd)) {
     n = sift(sm, p, top, bound);
   }
   rank_all(sm, sm.few, n, top);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const __grid_constant__ LogprobParams p) {
-  constexpr int VEC = 16 / sizeof(T), U = kBytes / 16;
+template <typename S>
+__global__ void __launch_bounds__(S::THREADS, S::CTAS) logprob_kernel(const __grid_constant__ LogprobParams p) {
+  using T = typename S::T;
+  constexpr int VEC = S::VEC, U = S::U, kThreads = S::THREADS, kWarps = S::WARPS;
   constexpr float kLog2e = 1.4426950408889634f;
-  __shared__ Shared sm;
+  __shared__ Shared<S> sm;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, C = p.cluster, rank = blockIdx.x % C;
   const int64_t row = blockIdx.x / C;
   int token = -1;
@@ -417,13 +430,16 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const __grid_const
     for (int r = 1; r < C; ++r) own = merge(own, sm.sums[r]);
     if (p.top > 0) {
       const int n = C * p.top;
-      if (n <= kThreads / 4) {
+      if (n <= kGroups) {
         rank_all(sm, sm.all[0], n, p.top);
       } else {
-        const uint64_t key = tid < n ? sm.all[0][tid] : 0, bound = group_bound(sm, key, p.top);
+        uint64_t key = 0;
+        for (int i = tid; i < n; i += kThreads) key = sm.all[0][i] > key ? sm.all[0][i] : key;
+        const uint64_t bound = group_bound(sm, key, p.top);
         if (tid == 0) sm.few_count = 0;
         __syncthreads();
-        if (key != 0 && key >= bound) sm.few[atomicAdd(&sm.few_count, 1)] = key;
+        for (int i = tid; i < n; i += kThreads)
+          if (sm.all[0][i] != 0 && sm.all[0][i] >= bound) sm.few[atomicAdd(&sm.few_count, 1)] = sm.all[0][i];
         __syncthreads();
         rank_all(sm, sm.few, sm.few_count, p.top);
       }
@@ -446,11 +462,16 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const __grid_const
   }
 }
 
-template <typename T>
-cudaError_t launch_logprobs(const LogprobParams& p, int N, cudaStream_t stream) {
+template <typename S>
+cudaError_t launch_shape(LogprobParams& p, int N, int sms, cudaStream_t stream) {
+  // parts of a row while they all run at once, none under two vectors a thread
+  p.cluster = 1;
+  while (p.cluster < kMaxCluster && (int64_t)N * p.cluster * 2 <= S::CTAS * sms &&
+         p.V / (2 * p.cluster) >= S::THREADS * S::VEC * 2)
+    p.cluster *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(N * p.cluster));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(S::THREADS);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -459,7 +480,21 @@ cudaError_t launch_logprobs(const LogprobParams& p, int N, cudaStream_t stream) 
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, logprob_kernel<T>, p);
+  return cudaLaunchKernelEx(&cfg, logprob_kernel<S>, p);
+}
+
+// Many short rows: smaller CTAs, whose start, alternatives and end overlap better with others' passes (2048 rows of
+// bf16, top 5: V 1000 21.4 us with 256 threads, 12.5 with 128; 8192 23.1 and 16.2; 32768 38.1 and 33.9; 50257 53.4 and
+// 49.8; 80000 69.7 and 69.8; f32 at 50257 83.3 and 82.8, at 80000 117 and 125; 64 threads lose from 8192 on).  At f32
+// 128 bytes a thread and step in three CTAs per SM stream best (2048 rows of 128256: 158 us, 6.6 TB/s, a copy's rate;
+// 64 bytes in four 168), at bf16, where a step is more arithmetic, 64 in four (512 rows 31 us, 35 the other way; 2048
+// rows 101 and 98).
+constexpr int kShortRow = 65536;
+template <typename T>
+cudaError_t launch_logprobs(LogprobParams& p, int N, int sms, cudaStream_t stream) {
+  constexpr bool f32 = sizeof(T) == 4;
+  if (p.V <= kShortRow && N > sms) return launch_shape<Shape<T, 128, 64, 8>>(p, N, sms, stream);
+  return launch_shape<Shape<T, 256, f32 ? 128 : 64, f32 ? 3 : 4>>(p, N, sms, stream);
 }
 
 }  // namespace
@@ -485,11 +520,9 @@ extern "C" int mk_token_logprobs(void* stream, int N, int V, const void* logits,
   int sms = 0;
   if (int rc = device_sms("mk_token_logprobs", &sms)) return rc;
   LogprobParams p{logits, ld, tokens, logprobs, entropy, top_logprobs, top_ids, status, V, top, 1};
-  // parts of a row while there are SMs without one, none under a step of a CTA
-  while (p.cluster < kMaxCluster && (int64_t)N * p.cluster * 2 <= 4 * sms && V / (2 * p.cluster) >= kThreads * kBytes / 4)
-    p.cluster *= 2;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return launch_result(logits_dtype == MK_F32 ? launch_logprobs<float>(p, N, s) : launch_logprobs<__nv_bfloat16>(p, N, s),
+  return launch_result(logits_dtype == MK_F32 ? launch_logprobs<float>(p, N, sms, s)
+                                              : launch_logprobs<__nv_bfloat16>(p, N, sms, s),
                        "mk_token_logprobs");
 } catch (...) {
   return MK_ERR_NOMEM;
