@@ -394,6 +394,14 @@ cudaError_t launch_norm(NormParams& p, int sms, cudaStream_t stream) {
 }
 
 }  // namespace
+
+cudaError_t launch_queries(const NormParams& all, int dtype, int D, int sms, cudaStream_t stream) {
+  NormParams p = all;
+  p.Hkv = 0;  // (a row then ends with its queries)
+  if (dtype == MK_F32) return D == 128 ? launch_norm<float, 128>(p, sms, stream) : launch_norm<float, 64>(p, sms, stream);
+  return D == 128 ? launch_norm<__nv_bfloat16, 128>(p, sms, stream) : launch_norm<__nv_bfloat16, 64>(p, sms, stream);
+}
+
 }  // namespace mk
 
 using namespace mk;

@@ -72,6 +72,9 @@ __device__ __forceinline__ void store_half(__nv_bfloat16* p, const float (&v)[E]
 }
 
 
+// Norms and rotation of the query heads alone.
+cudaError_t launch_queries(const NormParams& p, int dtype, int D, int sms, cudaStream_t stream);
+
 inline int check_norm(const char* who, int N, int Hq, int Hkv, int D, const void* qkv, int qkv_dtype, int64_t ld_qkv,
                       const void* q_gamma, const void* k_gamma, float eps, double rope_theta, const int32_t* positions,
                       const int32_t* slots, const void* q_out, int64_t ld_q, const void* kpool, const void* vpool,

@@ -26,7 +26,7 @@
 namespace mk {
 namespace {
 
-constexpr int kWindow = 16;  // rows of a window: the smallest page
+constexpr int kGap = 15;  // rows that are not stored which a run may have between two that are
 
 struct Store8Params : NormParams {
   uint8_t *kcodes, *vcodes;
@@ -36,24 +36,42 @@ struct Store8Params : NormParams {
 
 template <typename T>
 constexpr int kElems = sizeof(T) == 4 ? 4 : 8;  // of each half of a head, per lane
-template <typename T, int D>
-constexpr int kStoreThreads = kWindow * (D / 2 / kElems<T>);
+// A block of THREADS takes the runs that begin among WINDOW rows, ROWS at a time; the values of KEPT such passes stay in
+// registers.
+template <typename T_, int D_, int THREADS_, int WINDOW_, int VALUES>
+struct Shape {
+  using T = T_;
+  static constexpr int D = D_, THREADS = THREADS_, WINDOW = WINDOW_;
+  static constexpr int E = kElems<T>, LPH = D / 2 / E, ROWS = THREADS / LPH;
+  static constexpr int PASSES = WINDOW / ROWS, KEPT = VALUES / (2 * E);
+  static_assert(THREADS % (D / 2) == 0, "a thread keeps its pair of the rows' angles");
+  static_assert(PASSES >= 1 && KEPT >= PASSES && WINDOW <= 64, "the window's own rows are kept");
+};
 
 // Four coefficients of a pair, gains folded in: y_a = r (a ca + b sb), y_b = r (b cb + a sa).
 template <int D>
 struct Turn {
   float ca[D / 2], sb[D / 2], cb[D / 2], sa[D / 2];
 };
+// What a thread knows of its pair j of every row (its frequency is a constant that differs from lane to lane, which
+// takes a read per lane: once a block, not once a row).
+struct Pair {
+  uint64_t freq;
+  float ga, gb;
+};
 template <int D>
-__device__ __forceinline__ void make_turn(Turn<D>& t, int j, const Store8Params& p, int pos, const __nv_bfloat16* gamma) {
-  const float ga = gamma ? __bfloat162float(gamma[j]) : 1.f, gb = gamma ? __bfloat162float(gamma[j + D / 2]) : 1.f;
-  const uint64_t turn = (uint64_t)(uint32_t)pos * p.freq[j];
+__device__ __forceinline__ Pair pair_of(int j, const Store8Params& p, const __nv_bfloat16* gamma) {
+  return {p.freq[j], gamma ? __bfloat162float(gamma[j]) : 1.f, gamma ? __bfloat162float(gamma[j + D / 2]) : 1.f};
+}
+template <int D>
+__device__ __forceinline__ void make_turn(Turn<D>& t, int j, const Pair& q, int pos) {
+  const uint64_t turn = (uint64_t)(uint32_t)pos * q.freq;
   float s, c;
   sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
-  t.ca[j] = c * ga;
-  t.sb[j] = -s * gb;
-  t.cb[j] = c * gb;
-  t.sa[j] = s * ga;
+  t.ca[j] = c * q.ga;
+  t.sb[j] = -s * q.gb;
+  t.cb[j] = c * q.gb;
+  t.sa[j] = s * q.ga;
 }
 
 // A lane's elements of a head, normed (`norm`) and turned.  The lanes of `mask` hold the head.
@@ -132,102 +150,133 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float by) {
   return rescale2(w & 0xFFFFu, by) | rescale2(w >> 16, by) << 16;
 }
 
-constexpr int kKept = 5;  // windows whose values stay in registers: a run of 64 rows that begins anywhere
-
-template <typename T, int D>
-__device__ __forceinline__ void store_runs(const Store8Params& p, Turn<D>* turns) {
-  constexpr int E = kElems<T>, LPH = D / 2 / E, THREADS = kStoreThreads<T, D>;
-  __shared__ unsigned leads, breaks;         // rows of the window that begin a run, and others that end one
-  __shared__ int slot_of[kWindow], stop, beyond;
-  __shared__ unsigned top[kWindow];          // maxima of the runs, by first row
-  __shared__ unsigned written[kWindow][8];   // offsets that a run writes
-  __shared__ int upto[kWindow];              // the last one
-  __shared__ float inv_of[kWindow], again[kWindow];  // 1 / scale; what held codes are multiplied with (1: they stay)
+// The rows of a run go to one page, each at a higher offset than the one before.
+template <typename S>
+__device__ __forceinline__ void store_runs(const Store8Params& p, Turn<S::D>* turns, unsigned block) {
+  using T = typename S::T;
+  constexpr int D = S::D, E = S::E, LPH = S::LPH, THREADS = S::THREADS, ROWS = S::ROWS, WINDOW = S::WINDOW;
+  constexpr int BACK = kGap + 1, SPAN = BACK + WINDOW + THREADS;  // rows around the window that are looked at at once
+  __shared__ int near_slot[SPAN], near_pos[SPAN];
+  __shared__ unsigned leads[2], breaks[2];   // rows of the window that begin a run, and others that end one
+  __shared__ int stop, beyond;
+  __shared__ unsigned top[WINDOW];           // maxima of the runs, by first row
+  __shared__ unsigned written[WINDOW][8];    // offsets that a run writes
+  __shared__ int upto[WINDOW];               // the last one
+  __shared__ float inv_of[WINDOW], again[WINDOW];  // 1 / scale; what held codes are multiplied with (1: they stay)
   const int tid = threadIdx.x, gl = tid % LPH, group = tid / LPH;
-  const int heads = 2 * p.Hkv, hh = blockIdx.x % heads, r0 = (int)(blockIdx.x / heads) * kWindow;
+  const int heads = 2 * p.Hkv, hh = block % heads;
+  const int64_t r0 = (int64_t)(block / heads) * WINDOW;
   const bool is_v = hh >= p.Hkv;
   const int head = is_v ? hh - p.Hkv : hh, page = 1 << p.page_shift;
   const unsigned mask = (LPH == 32 ? 0xffffffffu : ((1u << LPH) - 1u)) << ((tid & 31) / LPH * LPH);
-  const auto slot_at = [&](int64_t r) { return r >= 0 && r < p.N && p.positions[r] >= 0 ? p.slots[r] : -1; };
-  const auto in_pool = [&](int slot) { return slot >= 0 && (slot >> p.page_shift) < p.num_pages; };
-  // the slot before a stored row's: of the nearest stored row, behind at most kWindow - 1 rows that are not
-  const auto before_of = [&](int64_t r) {
-    int b = -1;
-    for (int i = 1; i <= kWindow && b < 0; ++i) b = slot_at(r - i);
-    return b;
+  // the window's rows are on their way while their runs are found (where a page may be larger than the window, many
+  // windows have no run of their own)
+  const T* base = static_cast<const T*>(p.x) + (int64_t)(p.Hq + hh) * D + gl * E;
+  const bool early = page <= WINDOW;
+  Raw<T, E> ra[S::KEPT], rb[S::KEPT];
+  const auto load = [&](int w) {
+    const int64_t row = r0 + w * ROWS + group;
+    ra[w].load(base + row * p.ld_x);
+    rb[w].load(base + row * p.ld_x + D / 2);
   };
-  const auto same_page = [&](int a, int b) { return b >= 0 && (a >> p.page_shift) == (b >> p.page_shift); };
+  // a row's slot, and its position; -1 for one that is not stored
+  const auto slot_at = [&](int64_t r, int& pos) {
+    if (r < 0 || r >= p.N) return pos = -1;
+    const int slot = p.slots[r];
+    pos = p.positions[r];
+    return pos >= 0 ? slot : -1;
+  };
+  for (int i = tid; i < SPAN; i += THREADS) near_slot[i] = slot_at(r0 - BACK + i, near_pos[i]);
+  if (early) {
+#pragma unroll
+    for (int w = 0; w < S::PASSES; ++w)
+      if (r0 + w * ROWS + group < p.N) load(w);
+  }
   if (tid == 0) {
     stop = INT32_MAX;
     beyond = 0;
+    leads[1] = breaks[1] = 0;
   }
-  if (tid < kWindow) {
-    const int slot = slot_at((int64_t)r0 + tid), before = slot >= 0 ? before_of((int64_t)r0 + tid) : -1;
+  for (int i = tid; i < WINDOW; i += THREADS) top[i] = upto[i] = 0;
+  for (int i = tid; i < WINDOW * 8; i += THREADS) written[i / 8][i % 8] = 0;
+  __syncthreads();
+  const auto in_pool = [&](int slot) { return slot >= 0 && (slot >> p.page_shift) < p.num_pages; };
+  const auto same_page = [&](int a, int b) { return b >= 0 && (a >> p.page_shift) == (b >> p.page_shift); };
+  // the slot of the nearest stored row before row r0 + i
+  const auto before_of = [&](int i) {
+    int b = -1, pos;
+#pragma unroll 1
+    for (int k = 1; k <= BACK && b < 0; ++k)
+      b = i - k < SPAN - BACK ? near_slot[BACK + i - k] : slot_at(r0 + i - k, pos);
+    return b;
+  };
+  if (tid < WINDOW) {
+    const unsigned who = WINDOW < 32 ? (1u << (WINDOW & 31)) - 1u : 0xffffffffu;
+    const int slot = near_slot[BACK + tid], before = slot >= 0 ? before_of(tid) : -1;
     const bool in = in_pool(slot), again_page = in && same_page(slot, before);
     // a page that comes again in another order: two runs would both set its scale
     const bool twice = again_page && slot <= before;
     if (hh == 0 && ((slot >= 0 && !in) || twice)) set_status(p.status, MK_DEV_BAD_INDEX);
-    const unsigned l = __ballot_sync(0xFFFFu, in && !again_page), t = __ballot_sync(0xFFFFu, twice || (slot >= 0 && !in));
-    if (tid == 0) {
-      leads = l;
-      breaks = t;
+    const unsigned l = __ballot_sync(who, in && !again_page), t = __ballot_sync(who, twice || (slot >= 0 && !in));
+    if (tid % 32 == 0) {
+      leads[tid / 32] = l;
+      breaks[tid / 32] = t;
     }
-    slot_of[tid] = slot;
-    top[tid] = 0;
-    upto[tid] = 0;
   }
-  for (int i = tid; i < kWindow * 8; i += THREADS) written[i / 8][i % 8] = 0;
   __syncthreads();
-  const unsigned lead_bits = leads;
+  const uint64_t lead_bits = leads[0] | (uint64_t)leads[1] << 32;
   if (lead_bits == 0) return;
-  const unsigned ends = lead_bits | breaks;
+  const uint64_t ends = lead_bits | breaks[0] | (uint64_t)breaks[1] << 32;
   // the run that a row of the window belongs to, by its first row (-1: another block's, or none)
   const auto run_of = [&](int row) {
-    const unsigned e = ends & ((2u << row) - 1u);
-    const int at = e ? 31 - __clz((int)e) : -1;
+    const uint64_t e = ends & ((2ull << row) - 1ull);
+    const int at = e ? 63 - __clzll((long long)e) : -1;
     return at >= 0 && (lead_bits >> at & 1) ? at : -1;
   };
-  const int mine = slot_of[group] >= 0 ? run_of(group) : -1, last = run_of(kWindow - 1);
+  const int last = run_of(WINDOW - 1);
   // the last run's rows behind the window
-  for (int i0 = 0; last >= 0; i0 += THREADS) {
-    const int64_t r = (int64_t)r0 + kWindow + i0 + tid;
-    const int slot = slot_at(r), before = slot >= 0 ? before_of(r) : -1;
+  for (int i0 = WINDOW; last >= 0; i0 += THREADS) {
+    const int i = i0 + tid;
+    int pos;
+    const int slot = i0 == WINDOW ? near_slot[BACK + i] : slot_at(r0 + i, pos), before = slot >= 0 ? before_of(i) : -1;
     const bool on = in_pool(slot) && same_page(slot, before) && slot > before;
-    if (slot >= 0 && !on) atomicMin(&stop, i0 + tid);
-    if (!__syncthreads_or(on)) break;  // (a run goes on within kWindow rows)
+    if (slot >= 0 && !on) atomicMin(&stop, i);
+    if (!__syncthreads_or(on)) break;  // (a run goes on within BACK rows)
     const int end = stop;
-    if (on && i0 + tid < end) atomicMax(&beyond, i0 + tid + 1);
+    if (on && i < end) atomicMax(&beyond, i + 1 - WINDOW);
     if (end != INT32_MAX) break;
     __syncthreads();
   }
   __syncthreads();
-  const int more = beyond, windows = 1 + (more + kWindow - 1) / kWindow;
+  const Pair pair = is_v ? Pair{} : pair_of<D>(tid % (D / 2), p, p.k_gamma);
+  const int more = beyond, passes = S::PASSES + (more + ROWS - 1) / ROWS;
 
-  // the values of one window: this group's row, as floats to be stored (zero where there is none)
-  const T* base = static_cast<const T*>(p.x) + (int64_t)(p.Hq + hh) * D + gl * E;
+  // this group's row of a pass: its run, and its slot (-1: none of this block's)
+  const auto run_in = [&](int w) { return w < S::PASSES ? run_of(w * ROWS + group) : last; };
   const auto slot_in = [&](int w) {
-    if (w == 0) return mine >= 0 ? slot_of[group] : -1;
-    return (w - 1) * kWindow + group < more ? slot_at((int64_t)r0 + w * kWindow + group) : -1;
+    const int i = w * ROWS + group;
+    int pos;
+    if (w < S::PASSES) return run_of(i) >= 0 ? near_slot[BACK + i] : -1;
+    return i - WINDOW >= more ? -1 : i < SPAN - BACK ? near_slot[BACK + i] : slot_at(r0 + i, pos);
   };
-  const auto values = [&](int w, float (&a)[E], float (&b)[E]) {
-    const int64_t row = (int64_t)r0 + w * kWindow + group;
-    const bool on = slot_in(w) >= 0;
-    Raw<T, E> ra, rb;
-    if (on) {
-      ra.load(base + row * p.ld_x);
-      rb.load(base + row * p.ld_x + D / 2);
+  const auto turn_rows = [&](int w) {
+    if (is_v) return;
+    __syncthreads();
+    for (int i = tid / (D / 2); i < ROWS; i += THREADS / (D / 2)) {
+      const int k = w * ROWS + i;
+      int pos;
+      if (k < SPAN - BACK) pos = near_pos[BACK + k];
+      else slot_at(r0 + k, pos);
+      make_turn<D>(turns[i], tid % (D / 2), pair, pos);
     }
-    if (!is_v) {
-      __syncthreads();
-      for (int i = tid; i < kWindow * (D / 2); i += THREADS) {
-        const int64_t r = (int64_t)r0 + w * kWindow + i / (D / 2);
-        make_turn<D>(turns[i / (D / 2)], i % (D / 2), p, r < p.N ? p.positions[r] : 0, p.k_gamma);
-      }
-      __syncthreads();
-    }
+    __syncthreads();
+  };
+  // a pass's values, as floats to be stored (zero where there is no row)
+  const auto values = [&](int w, const Raw<T, E>& ra, const Raw<T, E>& rb, float (&a)[E], float (&b)[E]) {
+    turn_rows(w);
 #pragma unroll
     for (int i = 0; i < E; ++i) a[i] = b[i] = 0.f;
-    if (on) {
+    if (slot_in(w) >= 0) {
       ra.get(a);
       rb.get(b);
       if (!is_v) norm_turn<E, D>(a, b, turns[group], gl, p.k_gamma != nullptr, p.eps, mask);
@@ -238,6 +287,15 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Turn<D>* turns
       b[i] = fmaf(b[i], 0.f, b[i]);
     }
   };
+  // the same of a pass that is not kept
+  const auto read = [&](int w, float (&a)[E], float (&b)[E]) {
+    Raw<T, E> xa, xb;
+    if (slot_in(w) >= 0) {
+      xa.load(base + (r0 + w * ROWS + group) * p.ld_x);
+      xb.load(base + (r0 + w * ROWS + group) * p.ld_x + D / 2);
+    }
+    values(w, xa, xb, a, b);
+  };
   const auto raise = [&](int w, const float (&a)[E], const float (&b)[E]) {
     float m = 0.f;  // (a maximum leaves NaN out)
 #pragma unroll
@@ -246,29 +304,32 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Turn<D>* turns
     for (int o = LPH / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
     const int slot = slot_in(w);
     if (gl == 0 && slot >= 0) {
-      const int run = w == 0 ? mine : last, off = slot & (page - 1);
+      const int run = run_in(w), off = slot & (page - 1);
       atomicMax(&top[run], __float_as_uint(m));
       atomicOr(&written[run][off / 32], 1u << (off % 32));
       atomicMax(&upto[run], off);
     }
   };
-  float ka[kKept][E], kb[kKept][E];
 #pragma unroll
-  for (int w = 0; w < kKept; ++w) {
-    if (w >= windows) break;
-    values(w, ka[w], kb[w]);
+  for (int w = 0; w < S::KEPT; ++w)
+    if ((w >= S::PASSES || !early) && w < passes && slot_in(w) >= 0) load(w);
+  float ka[S::KEPT][E], kb[S::KEPT][E];
+#pragma unroll
+  for (int w = 0; w < S::KEPT; ++w) {
+    if (w >= passes) break;
+    values(w, ra[w], rb[w], ka[w], kb[w]);
     raise(w, ka[w], kb[w]);
   }
-  for (int w = kKept; w < windows; ++w) {
+  for (int w = S::KEPT; w < passes; ++w) {
     float a[E], b[E];
-    values(w, a, b);
+    read(w, a, b);
     raise(w, a, b);
   }
   __syncthreads();
   float* scales = is_v ? p.vscale : p.kscale;
   uint8_t* codes = is_v ? p.vcodes : p.kcodes;
-  if (tid < kWindow && (lead_bits >> tid & 1)) {
-    const int slot = slot_of[tid];
+  if (tid < WINDOW && (lead_bits >> tid & 1)) {
+    const int slot = near_slot[BACK + tid];
     float* at = scales + (int64_t)(slot >> p.page_shift) * p.Hkv + head;
     float s = scale_for(__uint_as_float(top[tid])), by = 1.f;
     if (!(written[tid][0] & 1)) {  // a page that is begun
@@ -282,12 +343,12 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Turn<D>* turns
   }
   __syncthreads();
   // pages whose scale grew: what they hold below the last new row
-  for (unsigned rest = lead_bits; rest; rest &= rest - 1) {
-    const int i = __ffs((int)rest) - 1;
+  for (uint64_t rest = lead_bits; rest; rest &= rest - 1) {
+    const int i = __ffsll((long long)rest) - 1;
     const float by = again[i];
     if (by == 1.f) continue;
     uint4* at = reinterpret_cast<uint4*>(
-        codes + (((int64_t)(slot_of[i] >> p.page_shift) * p.Hkv + head) << p.page_shift) * D);
+        codes + (((int64_t)(near_slot[BACK + i] >> p.page_shift) * p.Hkv + head) << p.page_shift) * D);
     for (int j = tid; j < upto[i] * (D / 16); j += THREADS) {
       const int off = j / (D / 16);
       if (written[i][off / 32] >> (off % 32) & 1) continue;
@@ -301,18 +362,18 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Turn<D>* turns
     if (slot < 0) return;
     uint8_t* dst = codes + ((((int64_t)(slot >> p.page_shift) * p.Hkv + head) << p.page_shift) + (slot & (page - 1))) * D +
                    gl * E;
-    const float inv = inv_of[w == 0 ? mine : last];
+    const float inv = inv_of[run_in(w)];
     store_codes<E>(dst, a, inv);
     store_codes<E>(dst + D / 2, b, inv);
   };
 #pragma unroll
-  for (int w = 0; w < kKept; ++w) {
-    if (w >= windows) break;
+  for (int w = 0; w < S::KEPT; ++w) {
+    if (w >= passes) break;
     put(w, ka[w], kb[w]);
   }
-  for (int w = kKept; w < windows; ++w) {
+  for (int w = S::KEPT; w < passes; ++w) {
     float a[E], b[E];
-    values(w, a, b);
+    read(w, a, b);
     put(w, a, b);
   }
 }
@@ -320,9 +381,10 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Turn<D>* turns
 constexpr int kQueryBatch = 3;      // heads a lane group has in flight
 constexpr int kQueryMaxTokens = 4;  // tokens of a block of queries
 
-template <typename T, int D>
-__device__ __forceinline__ void queries(const Store8Params& p, Turn<D>* turns, unsigned block) {
-  constexpr int E = kElems<T>, LPH = D / 2 / E, GP = kWindow, THREADS = kStoreThreads<T, D>;
+template <typename S>
+__device__ __forceinline__ void queries(const Store8Params& p, Turn<S::D>* turns, unsigned block) {
+  using T = typename S::T;
+  constexpr int D = S::D, E = S::E, LPH = S::LPH, GP = S::ROWS, THREADS = S::THREADS;
   const int gl = threadIdx.x % LPH, group = threadIdx.x / LPH;
   const int gt = GP / p.tokens, tk = group / gt;
   const int64_t row0 = (int64_t)(block / p.splits) * p.tokens, row = row0 + tk;
@@ -344,9 +406,11 @@ __device__ __forceinline__ void queries(const Store8Params& p, Turn<D>* turns, u
     }
     if (h == h0) {
       if (in) pos = p.positions[row];
-      for (int i = threadIdx.x; i < p.tokens * (D / 2); i += THREADS) {
-        const int64_t r = row0 + i / (D / 2);
-        make_turn<D>(turns[i / (D / 2)], i % (D / 2), p, r < p.N ? p.positions[r] : 0, p.q_gamma);
+      const int j = threadIdx.x % (D / 2);
+      const Pair pair = pair_of<D>(j, p, p.q_gamma);
+      for (int i = threadIdx.x / (D / 2); i < p.tokens; i += THREADS / (D / 2)) {
+        const int64_t r = row0 + i;
+        make_turn<D>(turns[i], j, pair, r < p.N ? p.positions[r] : 0);
       }
       __syncthreads();
     }
@@ -365,26 +429,44 @@ __device__ __forceinline__ void queries(const Store8Params& p, Turn<D>* turns, u
   }
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__((kStoreThreads<T, D>)) store8_kernel(const __grid_constant__ Store8Params p) {
-  __shared__ __align__(16) Turn<D> turns[kWindow];
-  if (blockIdx.x < p.kv_blocks) store_runs<T, D>(p, turns);
-  else queries<T, D>(p, turns, blockIdx.x - p.kv_blocks);
+// Keys and values first, then the queries, in one launch
+template <typename S>
+__global__ void __launch_bounds__(S::THREADS) store8_kernel(const __grid_constant__ Store8Params p) {
+  __shared__ __align__(16) Turn<S::D> turns[S::ROWS];
+  if (blockIdx.x < p.kv_blocks) store_runs<S>(p, turns, blockIdx.x);
+  else queries<S>(p, turns, blockIdx.x - p.kv_blocks);
+}
+// Keys and values alone
+template <typename S>
+__global__ void __launch_bounds__(S::THREADS, 2) store8_kv_kernel(const __grid_constant__ Store8Params p) {
+  __shared__ __align__(16) Turn<S::D> turns[S::ROWS];
+  store_runs<S>(p, turns, blockIdx.x);
 }
 
+#ifndef FEW_ROWS
+#define FEW_ROWS 512
+#endif
 template <typename T, int D>
 cudaError_t launch_store8(Store8Params& p, int sms, cudaStream_t stream) {
-  constexpr int GP = kWindow;
+  constexpr int E = kElems<T>, LPH = D / 2 / E;
+  if (p.N > FEW_ROWS) {
+    using S = Shape<T, D, 256, 64, 64>;
+    const int64_t kv = (((int64_t)p.N + S::WINDOW - 1) / S::WINDOW) * 2 * p.Hkv;
+    store8_kv_kernel<S><<<(unsigned)kv, S::THREADS, 0, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_queries(p, sizeof(T) == 4 ? MK_F32 : MK_BF16, D, sms, stream);
+  }
+  using S = Shape<T, D, 16 * LPH, 16, 10 * E>;
+  constexpr int GP = S::ROWS;
   // tokens whose heads fill a block's batch; few tokens: a head per lane group, over several blocks
   p.tokens = 1;
   while (p.tokens < kQueryMaxTokens && 2 * p.tokens * p.Hq <= kQueryBatch * GP) p.tokens *= 2;
   while (p.tokens > 1 && (p.N + p.tokens - 1) / p.tokens < 2 * sms) p.tokens /= 2;
   p.splits = p.N < sms ? (p.Hq + GP - 1) / GP : 1;
-  const int64_t kv = (((int64_t)p.N + kWindow - 1) / kWindow) * 2 * p.Hkv;
-  const int64_t blocks = kv + (((int64_t)p.N + p.tokens - 1) / p.tokens) * p.splits;
-  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  p.kv_blocks = (unsigned)kv;
-  store8_kernel<T, D><<<(unsigned)blocks, kStoreThreads<T, D>, 0, stream>>>(p);
+  p.kv_blocks = (unsigned)((p.N + S::WINDOW - 1) / S::WINDOW * 2 * p.Hkv);
+  const unsigned blocks = p.kv_blocks + (unsigned)((p.N + p.tokens - 1) / p.tokens * p.splits);
+  store8_kernel<S><<<blocks, S::THREADS, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -404,7 +486,7 @@ extern "C" int mk_qk_norm_rope_e4m3(void* stream, int N, int Hq, int Hkv, int D,
     return rc;
   if (!kscale || !vscale) return fail(MK_ERR_ARG, "mk_qk_norm_rope_e4m3: null argument");
   // (blocks of a launch)
-  if ((int64_t)N * (2 * Hkv + kWindow) / kWindow > INT32_MAX / 128)
+  if (((int64_t)N + 63) / 64 * 2 * Hkv > INT32_MAX || (int64_t)N * ((Hq + 2 * Hkv) / 8 + 1) > INT32_MAX)
     return fail(MK_ERR_LIMIT, "mk_qk_norm_rope_e4m3: too many rows");
   if (int rc = pending_error(who)) return rc;
   if (N == 0) return MK_OK;

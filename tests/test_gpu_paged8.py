@@ -171,7 +171,10 @@ STORES = [  # ctx, new, Hq, Hkv, D, page, dtype, norm, pad, strided, gaps
     ([100, 0], [300, 256], 4, 1, 128, 256, BF, "k", 0, False, 0), ([255, 3], [257, 300], 3, 1, 64, 128, F32, "qk", 1, False, 0),
     ([0], [700], 3, 3, 64, 16, BF, "", 0, False, 0), (list(range(100, 220)), [1] * 120, 8, 2, 128, 16, BF, "qk", 8, False, 0),
     ([17, 30, 0], [40, 100, 64], 4, 2, 128, 64, BF, "qk", 0, False, 3), ([3, 250, 9], [90, 1, 50], 4, 2, 64, 256, F32, "k", 4, True, 15),
-    ([0] * 30, list(range(1, 31)), 2, 1, 64, 32, BF, "qk", 0, False, 0)]
+    ([0] * 30, list(range(1, 31)), 2, 1, 64, 32, BF, "qk", 0, False, 0),
+    ([30, 7, 0], [400, 1, 300], 4, 2, 128, 64, F32, "qk", 9, True, 4), (list(range(600)), [1] * 600, 4, 1, 128, 16, F32, "k", 3, False, 0),
+    ([5, 100, 0], [700, 90, 64], 28, 4, 128, 128, BF, "qk", 30, False, 2), ([3] * 200, [1, 5, 2, 9] * 50, 4, 2, 64, 16, BF, "", 0, True, 1),
+    ([0, 1], [512, 512], 2, 2, 64, 64, F32, "qk", 0, False, 0), ([77], [3000], 2, 1, 128, 256, BF, "k", 0, False, 0)]
 
 
 @pytest.mark.parametrize("ctx,new,Hq,Hkv,D,page,dtype,norm,pad,strided,gaps", STORES)
