@@ -376,10 +376,12 @@ __global__ void __launch_bounds__((kNormThreads<T, D>), (768 / kNormThreads<T, D
       store_half<E>(dst + D / 2, b);
     }
   }
+  ptx::wait_dependency();  // (where it was launched beside another: this one ends behind it)
 }
 
+// `beside`: beside the launch before it, which makes nothing that this one reads (the kernel ends behind it)
 template <typename T, int D>
-cudaError_t launch_norm(NormParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_norm(NormParams& p, int sms, cudaStream_t stream, bool beside = false) {
   constexpr int E = sizeof(T) == 4 ? 4 : 8;
   constexpr int GP = kNormThreads<T, D> / (D / 2 / E);
   const int heads = p.Hq + 2 * p.Hkv;
@@ -389,6 +391,7 @@ cudaError_t launch_norm(NormParams& p, int sms, cudaStream_t stream) {
   while (p.tokens > 1 && (p.N + p.tokens - 1) / p.tokens < 2 * sms) p.tokens /= 2;
   p.splits = p.N < sms ? (heads + GP - 1) / GP : 1;
   const int64_t blocks = (int64_t)((p.N + p.tokens - 1) / p.tokens) * p.splits;
+  if (beside) return launch_early(norm_rope_kernel<T, D>, dim3((unsigned)blocks), dim3(kNormThreads<T, D>), 0, stream, p);
   norm_rope_kernel<T, D><<<(unsigned)blocks, kNormThreads<T, D>, 0, stream>>>(p);
   return cudaGetLastError();
 }
@@ -398,8 +401,10 @@ cudaError_t launch_norm(NormParams& p, int sms, cudaStream_t stream) {
 cudaError_t launch_queries(const NormParams& all, int dtype, int D, int sms, cudaStream_t stream) {
   NormParams p = all;
   p.Hkv = 0;  // (a row then ends with its queries)
-  if (dtype == MK_F32) return D == 128 ? launch_norm<float, 128>(p, sms, stream) : launch_norm<float, 64>(p, sms, stream);
-  return D == 128 ? launch_norm<__nv_bfloat16, 128>(p, sms, stream) : launch_norm<__nv_bfloat16, 64>(p, sms, stream);
+  if (dtype == MK_F32)
+    return D == 128 ? launch_norm<float, 128>(p, sms, stream, true) : launch_norm<float, 64>(p, sms, stream, true);
+  return D == 128 ? launch_norm<__nv_bfloat16, 128>(p, sms, stream, true)
+                  : launch_norm<__nv_bfloat16, 64>(p, sms, stream, true);
 }
 
 }  // namespace mk

@@ -72,7 +72,8 @@ __device__ __forceinline__ void store_half(__nv_bfloat16* p, const float (&v)[E]
 }
 
 
-// Norms and rotation of the query heads alone.
+// Norms and rotation of the query heads alone, beside the launch before it, which calls launch_dependents() and makes
+// nothing that this one reads.
 cudaError_t launch_queries(const NormParams& p, int dtype, int D, int sms, cudaStream_t stream);
 
 inline int check_norm(const char* who, int N, int Hq, int Hkv, int D, const void* qkv, int qkv_dtype, int64_t ld_qkv,

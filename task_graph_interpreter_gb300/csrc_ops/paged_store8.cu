@@ -63,11 +63,18 @@ template <int D>
 __device__ __forceinline__ Pair pair_of(int j, const Store8Params& p, const __nv_bfloat16* gamma) {
   return {p.freq[j], gamma ? __bfloat162float(gamma[j]) : 1.f, gamma ? __bfloat162float(gamma[j + D / 2]) : 1.f};
 }
-template <int D>
+// KEYS: with the hardware's sine and cosine, which are off by under 2^-20: keys are rounded to e4m3 (2^-4).
+template <int D, bool KEYS>
 __device__ __forceinline__ void make_turn(Turn<D>& t, int j, const Pair& q, int pos) {
   const uint64_t turn = (uint64_t)(uint32_t)pos * q.freq;
+  const float half_turns = (float)(int32_t)(turn >> 32) * 0x1p-31f;  // in [-1, 1)
   float s, c;
-  sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
+  if constexpr (KEYS) {
+    s = __sinf(half_turns * 3.14159265f);
+    c = __cosf(half_turns * 3.14159265f);
+  } else {
+    sincospif(half_turns, &s, &c);
+  }
   t.ca[j] = c * q.ga;
   t.sb[j] = -s * q.gb;
   t.cb[j] = c * q.gb;
@@ -158,9 +165,9 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Turn<S::D>* tu
   constexpr int BACK = kGap + 1, SPAN = BACK + WINDOW + THREADS;  // rows around the window that are looked at at once
   __shared__ int near_slot[SPAN], near_pos[SPAN];
   __shared__ unsigned leads[2], breaks[2];   // rows of the window that begin a run, and others that end one
-  __shared__ int stop, beyond;
+  __shared__ int stop, beyond, grown;
   __shared__ unsigned top[WINDOW];           // maxima of the runs, by first row
-  __shared__ unsigned written[WINDOW][8];    // offsets that a run writes
+  __shared__ unsigned written[WINDOW][8];    // offsets that a run writes, where what a page holds is looked at again
   __shared__ int upto[WINDOW];               // the last one
   __shared__ float inv_of[WINDOW], again[WINDOW];  // 1 / scale; what held codes are multiplied with (1: they stay)
   const int tid = threadIdx.x, gl = tid % LPH, group = tid / LPH;
@@ -194,11 +201,10 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Turn<S::D>* tu
   }
   if (tid == 0) {
     stop = INT32_MAX;
-    beyond = 0;
+    beyond = grown = 0;
     leads[1] = breaks[1] = 0;
   }
-  for (int i = tid; i < WINDOW; i += THREADS) top[i] = upto[i] = 0;
-  for (int i = tid; i < WINDOW * 8; i += THREADS) written[i / 8][i % 8] = 0;
+  for (int i = tid; i < WINDOW; i += THREADS) top[i] = 0;
   __syncthreads();
   const auto in_pool = [&](int slot) { return slot >= 0 && (slot >> p.page_shift) < p.num_pages; };
   const auto same_page = [&](int a, int b) { return b >= 0 && (a >> p.page_shift) == (b >> p.page_shift); };
@@ -267,63 +273,65 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Turn<S::D>* tu
       int pos;
       if (k < SPAN - BACK) pos = near_pos[BACK + k];
       else slot_at(r0 + k, pos);
-      make_turn<D>(turns[i], tid % (D / 2), pair, pos);
+      make_turn<D, true>(turns[i], tid % (D / 2), pair, pos);
     }
     __syncthreads();
   };
   // a pass's values, as floats to be stored (zero where there is no row)
-  const auto values = [&](int w, const Raw<T, E>& ra, const Raw<T, E>& rb, float (&a)[E], float (&b)[E]) {
+  const auto values = [&](int w, int slot, const Raw<T, E>& ra, const Raw<T, E>& rb, float (&a)[E], float (&b)[E]) {
     turn_rows(w);
 #pragma unroll
     for (int i = 0; i < E; ++i) a[i] = b[i] = 0.f;
-    if (slot_in(w) >= 0) {
+    if (slot >= 0) {
       ra.get(a);
       rb.get(b);
       if (!is_v) norm_turn<E, D>(a, b, turns[group], gl, p.k_gamma != nullptr, p.eps, mask);
-    }
 #pragma unroll
-    for (int i = 0; i < E; ++i) {  // an infinity becomes NaN
-      a[i] = fmaf(a[i], 0.f, a[i]);
-      b[i] = fmaf(b[i], 0.f, b[i]);
+      for (int i = 0; i < E; i += 2) {  // an infinity becomes NaN
+        const uint64_t u = ptx::pair_f32(a[i], a[i + 1]), v = ptx::pair_f32(b[i], b[i + 1]);
+        const float2 x = ptx::unpair_f32(ptx::fma2(u, 0, u)), y = ptx::unpair_f32(ptx::fma2(v, 0, v));
+        a[i] = x.x;
+        a[i + 1] = x.y;
+        b[i] = y.x;
+        b[i + 1] = y.y;
+      }
     }
   };
   // the same of a pass that is not kept
-  const auto read = [&](int w, float (&a)[E], float (&b)[E]) {
+  const auto read = [&](int w, int slot, float (&a)[E], float (&b)[E]) {
     Raw<T, E> xa, xb;
-    if (slot_in(w) >= 0) {
+    if (slot >= 0) {
       xa.load(base + (r0 + w * ROWS + group) * p.ld_x);
       xb.load(base + (r0 + w * ROWS + group) * p.ld_x + D / 2);
     }
-    values(w, xa, xb, a, b);
+    values(w, slot, xa, xb, a, b);
   };
-  const auto raise = [&](int w, const float (&a)[E], const float (&b)[E]) {
+  const auto raise = [&](int run, const float (&a)[E], const float (&b)[E]) {
     float m = 0.f;  // (a maximum leaves NaN out)
 #pragma unroll
     for (int i = 0; i < E; ++i) m = fmaxf(m, fmaxf(fabsf(a[i]), fabsf(b[i])));
 #pragma unroll
     for (int o = LPH / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
-    const int slot = slot_in(w);
-    if (gl == 0 && slot >= 0) {
-      const int run = run_in(w), off = slot & (page - 1);
-      atomicMax(&top[run], __float_as_uint(m));
-      atomicOr(&written[run][off / 32], 1u << (off % 32));
-      atomicMax(&upto[run], off);
-    }
+    if (gl == 0 && m > 0.f) atomicMax(&top[run], __float_as_uint(m));
   };
+  int slot_k[S::KEPT], run_k[S::KEPT];
 #pragma unroll
-  for (int w = 0; w < S::KEPT; ++w)
-    if ((w >= S::PASSES || !early) && w < passes && slot_in(w) >= 0) load(w);
+  for (int w = 0; w < S::KEPT; ++w) {
+    slot_k[w] = w < passes ? slot_in(w) : -1;
+    run_k[w] = max(run_in(w), 0);
+    if ((w >= S::PASSES || !early) && slot_k[w] >= 0) load(w);
+  }
   float ka[S::KEPT][E], kb[S::KEPT][E];
 #pragma unroll
   for (int w = 0; w < S::KEPT; ++w) {
     if (w >= passes) break;
-    values(w, ra[w], rb[w], ka[w], kb[w]);
-    raise(w, ka[w], kb[w]);
+    values(w, slot_k[w], ra[w], rb[w], ka[w], kb[w]);
+    raise(run_k[w], ka[w], kb[w]);
   }
   for (int w = S::KEPT; w < passes; ++w) {
     float a[E], b[E];
-    read(w, a, b);
-    raise(w, a, b);
+    read(w, slot_in(w), a, b);
+    raise(last, a, b);
   }
   __syncthreads();
   float* scales = is_v ? p.vscale : p.kscale;
@@ -332,49 +340,59 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Turn<S::D>* tu
     const int slot = near_slot[BACK + tid];
     float* at = scales + (int64_t)(slot >> p.page_shift) * p.Hkv + head;
     float s = scale_for(__uint_as_float(top[tid])), by = 1.f;
-    if (!(written[tid][0] & 1)) {  // a page that is begun
+    if ((slot & (page - 1)) != 0) {  // a page that is begun
       const float old = *at;
       if (old >= s) s = old;
       else by = old / s;
+      if (by != 1.f) grown = 1;
     }
     *at = s;
     inv_of[tid] = 1.f / s;
     again[tid] = by;
   }
   __syncthreads();
-  // pages whose scale grew: what they hold below the last new row
-  for (uint64_t rest = lead_bits; rest; rest &= rest - 1) {
-    const int i = __ffsll((long long)rest) - 1;
-    const float by = again[i];
-    if (by == 1.f) continue;
-    uint4* at = reinterpret_cast<uint4*>(
-        codes + (((int64_t)(near_slot[BACK + i] >> p.page_shift) * p.Hkv + head) << p.page_shift) * D);
-    for (int j = tid; j < upto[i] * (D / 16); j += THREADS) {
-      const int off = j / (D / 16);
-      if (written[i][off / 32] >> (off % 32) & 1) continue;
-      uint4 v = at[j];
-      v.x = rescale4(v.x, by); v.y = rescale4(v.y, by); v.z = rescale4(v.z, by); v.w = rescale4(v.w, by);
-      at[j] = v;
+  if (grown) {
+    // pages whose scale grew: what they hold below the last new row, but for what is new
+    for (int i = tid; i < WINDOW; i += THREADS) upto[i] = 0;
+    for (int i = tid; i < WINDOW * 8; i += THREADS) written[i / 8][i % 8] = 0;
+    __syncthreads();
+    for (int w = 0; w < passes; ++w) {
+      const int slot = slot_in(w), off = slot & (page - 1);
+      if (gl != 0 || slot < 0) continue;
+      atomicOr(&written[run_in(w)][off / 32], 1u << (off % 32));
+      atomicMax(&upto[run_in(w)], off);
+    }
+    __syncthreads();
+    for (uint64_t rest = lead_bits; rest; rest &= rest - 1) {
+      const int i = __ffsll((long long)rest) - 1;
+      const float by = again[i];
+      if (by == 1.f) continue;
+      uint4* at = reinterpret_cast<uint4*>(
+          codes + (((int64_t)(near_slot[BACK + i] >> p.page_shift) * p.Hkv + head) << p.page_shift) * D);
+      for (int j = tid; j < upto[i] * (D / 16); j += THREADS) {
+        const int off = j / (D / 16);
+        if (written[i][off / 32] >> (off % 32) & 1) continue;
+        uint4 v = at[j];
+        v.x = rescale4(v.x, by); v.y = rescale4(v.y, by); v.z = rescale4(v.z, by); v.w = rescale4(v.w, by);
+        at[j] = v;
+      }
     }
   }
-  const auto put = [&](int w, const float (&a)[E], const float (&b)[E]) {
-    const int slot = slot_in(w);
+  const auto put = [&](int slot, int run, const float (&a)[E], const float (&b)[E]) {
     if (slot < 0) return;
     uint8_t* dst = codes + ((((int64_t)(slot >> p.page_shift) * p.Hkv + head) << p.page_shift) + (slot & (page - 1))) * D +
                    gl * E;
-    const float inv = inv_of[run_in(w)];
+    const float inv = inv_of[run];
     store_codes<E>(dst, a, inv);
     store_codes<E>(dst + D / 2, b, inv);
   };
 #pragma unroll
-  for (int w = 0; w < S::KEPT; ++w) {
-    if (w >= passes) break;
-    put(w, ka[w], kb[w]);
-  }
+  for (int w = 0; w < S::KEPT; ++w) put(slot_k[w], run_k[w], ka[w], kb[w]);
   for (int w = S::KEPT; w < passes; ++w) {
     float a[E], b[E];
-    read(w, a, b);
-    put(w, a, b);
+    const int slot = slot_in(w);
+    read(w, slot, a, b);
+    put(slot, last, a, b);
   }
 }
 
@@ -410,7 +428,7 @@ __device__ __forceinline__ void queries(const Store8Params& p, Turn<S::D>* turns
       const Pair pair = pair_of<D>(j, p, p.q_gamma);
       for (int i = threadIdx.x / (D / 2); i < p.tokens; i += THREADS / (D / 2)) {
         const int64_t r = row0 + i;
-        make_turn<D>(turns[i], j, pair, r < p.N ? p.positions[r] : 0);
+        make_turn<D, false>(turns[i], j, pair, r < p.N ? p.positions[r] : 0);
       }
       __syncthreads();
     }
@@ -439,6 +457,7 @@ __global__ void __launch_bounds__(S::THREADS) store8_kernel(const __grid_constan
 // Keys and values alone
 template <typename S>
 __global__ void __launch_bounds__(S::THREADS, 2) store8_kv_kernel(const __grid_constant__ Store8Params p) {
+  ptx::launch_dependents();  // the queries' blocks follow as these end
   __shared__ __align__(16) Turn<S::D> turns[S::ROWS];
   store_runs<S>(p, turns, blockIdx.x);
 }
