@@ -14,11 +14,14 @@
 // queries written in 16 bits, keys and values in 8.  A page's maximum has to
 // be known before its first value is stored, so the unit of work is a run: the
 // neighbouring rows that go to one page, of one key or value head.  A block
-// takes the runs that begin in its window of 16 rows, a row per lane group,
-// follows the last of them over up to four more windows, whose values stay in
-// registers between the maximum and the store (rows of longer runs are read
-// again), and holds a row's angles in shared memory, one window at a time.
-// Blocks of queries follow those of keys and values in the same launch.
+// takes the runs that begin in its window of rows, a few rows per pass, and
+// follows the last of them behind the window.  Values stay in registers between
+// the maximum and the store (those of runs that reach far behind the window are
+// read again), each lane turns its pairs itself, and every warp finds the runs
+// for itself, so the block meets three times.  For a prompt's 8192 tokens of 8
+// heads keys and values took 38 us with the rows' angles in shared memory, whose
+// barriers and bookkeeping were most of it, and a warp alone per window and head,
+// without any barrier, 14 us for each of its runs of 64 rows.
 #include <cuda_fp16.h>
 
 #include "paged_norm.cuh"
@@ -38,14 +41,12 @@ template <typename T>
 constexpr int kElems = sizeof(T) == 4 ? 4 : 8;  // of each half of a head, per lane
 // A block of THREADS takes the runs that begin among WINDOW rows, ROWS at a time; the values of KEPT such passes stay in
 // registers.
-template <typename T_, int D_, int THREADS_, int WINDOW_, int VALUES>
+template <typename T_, int D_, int THREADS_, int WINDOW_, int KEPT_>
 struct Shape {
   using T = T_;
-  static constexpr int D = D_, THREADS = THREADS_, WINDOW = WINDOW_;
-  static constexpr int E = kElems<T>, LPH = D / 2 / E, ROWS = THREADS / LPH;
-  static constexpr int PASSES = WINDOW / ROWS, KEPT = VALUES / (2 * E);
-  static_assert(THREADS % (D / 2) == 0, "a thread keeps its pair of the rows' angles");
-  static_assert(PASSES >= 1 && KEPT >= PASSES && WINDOW <= 64, "the window's own rows are kept");
+  static constexpr int D = D_, THREADS = THREADS_, WINDOW = WINDOW_, KEPT = KEPT_;
+  static constexpr int E = kElems<T>, LPH = D / 2 / E, ROWS = THREADS / LPH, PASSES = WINDOW / ROWS;
+  static_assert(PASSES >= 1 && WINDOW % ROWS == 0 && KEPT >= PASSES && WINDOW <= 64, "the window's own rows are kept");
 };
 
 // Four coefficients of a pair, gains folded in: y_a = r (a ca + b sb), y_b = r (b cb + a sa).
@@ -53,32 +54,17 @@ template <int D>
 struct Turn {
   float ca[D / 2], sb[D / 2], cb[D / 2], sa[D / 2];
 };
-// What a thread knows of its pair j of every row (its frequency is a constant that differs from lane to lane, which
-// takes a read per lane: once a block, not once a row).
-struct Pair {
-  uint64_t freq;
-  float ga, gb;
-};
 template <int D>
-__device__ __forceinline__ Pair pair_of(int j, const Store8Params& p, const __nv_bfloat16* gamma) {
-  return {p.freq[j], gamma ? __bfloat162float(gamma[j]) : 1.f, gamma ? __bfloat162float(gamma[j + D / 2]) : 1.f};
-}
-// KEYS: with the hardware's sine and cosine, which are off by under 2^-20: keys are rounded to e4m3 (2^-4).
-template <int D, bool KEYS>
-__device__ __forceinline__ void make_turn(Turn<D>& t, int j, const Pair& q, int pos) {
-  const uint64_t turn = (uint64_t)(uint32_t)pos * q.freq;
-  const float half_turns = (float)(int32_t)(turn >> 32) * 0x1p-31f;  // in [-1, 1)
+__device__ __forceinline__ void make_turn(Turn<D>& t, int j, const Store8Params& p, int pos) {
+  const __nv_bfloat16* gamma = p.q_gamma;
+  const float ga = gamma ? __bfloat162float(gamma[j]) : 1.f, gb = gamma ? __bfloat162float(gamma[j + D / 2]) : 1.f;
+  const uint64_t turn = (uint64_t)(uint32_t)pos * p.freq[j];
   float s, c;
-  if constexpr (KEYS) {
-    s = __sinf(half_turns * 3.14159265f);
-    c = __cosf(half_turns * 3.14159265f);
-  } else {
-    sincospif(half_turns, &s, &c);
-  }
-  t.ca[j] = c * q.ga;
-  t.sb[j] = -s * q.gb;
-  t.cb[j] = c * q.gb;
-  t.sa[j] = s * q.ga;
+  sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
+  t.ca[j] = c * ga;
+  t.sb[j] = -s * gb;
+  t.cb[j] = c * gb;
+  t.sa[j] = s * ga;
 }
 
 // A lane's elements of a head, normed (`norm`) and turned.  The lanes of `mask` hold the head.
@@ -157,35 +143,32 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float by) {
   return rescale2(w & 0xFFFFu, by) | rescale2(w >> 16, by) << 16;
 }
 
-// The rows of a run go to one page, each at a higher offset than the one before.
+// What a block keeps in shared memory.
+template <int WINDOW>
+struct Runs {
+  static constexpr int BACK = kGap + 1, SPAN = BACK + WINDOW + 64;  // rows around the window that are looked at at once
+  int slot[SPAN], pos[SPAN];
+  unsigned top[WINDOW];             // maxima of the runs, by first row
+  float inv[WINDOW], again[WINDOW]; // 1 / scale; what held codes are multiplied with (1: they stay)
+  unsigned written[WINDOW][8];      // offsets that a run writes, where what a page holds is looked at again
+  int upto[WINDOW];                 // the last one
+  int grown;
+};
+
+// The runs of a key or value head that begin in a window; the rows of a run go to one page, each at a higher offset than
+// the one before.
 template <typename S>
-__device__ __forceinline__ void store_runs(const Store8Params& p, Turn<S::D>* turns, unsigned block) {
+__device__ __forceinline__ void store_runs(const Store8Params& p, Runs<S::WINDOW>& sm, unsigned block) {
   using T = typename S::T;
-  constexpr int D = S::D, E = S::E, LPH = S::LPH, THREADS = S::THREADS, ROWS = S::ROWS, WINDOW = S::WINDOW;
-  constexpr int BACK = kGap + 1, SPAN = BACK + WINDOW + THREADS;  // rows around the window that are looked at at once
-  __shared__ int near_slot[SPAN], near_pos[SPAN];
-  __shared__ unsigned leads[2], breaks[2];   // rows of the window that begin a run, and others that end one
-  __shared__ int stop, beyond, grown;
-  __shared__ unsigned top[WINDOW];           // maxima of the runs, by first row
-  __shared__ unsigned written[WINDOW][8];    // offsets that a run writes, where what a page holds is looked at again
-  __shared__ int upto[WINDOW];               // the last one
-  __shared__ float inv_of[WINDOW], again[WINDOW];  // 1 / scale; what held codes are multiplied with (1: they stay)
-  const int tid = threadIdx.x, gl = tid % LPH, group = tid / LPH;
-  const int heads = 2 * p.Hkv, hh = block % heads;
-  const int64_t r0 = (int64_t)(block / heads) * WINDOW;
+  constexpr int D = S::D, E = S::E, LPH = S::LPH, ROWS = S::ROWS, WINDOW = S::WINDOW, PASSES = S::PASSES, KEPT = S::KEPT;
+  constexpr int THREADS = S::THREADS, BACK = Runs<WINDOW>::BACK, SPAN = Runs<WINDOW>::SPAN;
+  const int tid = threadIdx.x, lane = tid % 32, gl = tid % LPH, group = tid / LPH;
+  const int hh = block % (2 * p.Hkv);
+  const int64_t r0 = (int64_t)(block / (2 * p.Hkv)) * WINDOW;
   const bool is_v = hh >= p.Hkv;
   const int head = is_v ? hh - p.Hkv : hh, page = 1 << p.page_shift;
-  const unsigned mask = (LPH == 32 ? 0xffffffffu : ((1u << LPH) - 1u)) << ((tid & 31) / LPH * LPH);
-  // the window's rows are on their way while their runs are found (where a page may be larger than the window, many
-  // windows have no run of their own)
+  const unsigned mask = (LPH == 32 ? 0xffffffffu : ((1u << LPH) - 1u)) << (lane / LPH * LPH);
   const T* base = static_cast<const T*>(p.x) + (int64_t)(p.Hq + hh) * D + gl * E;
-  const bool early = page <= WINDOW;
-  Raw<T, E> ra[S::KEPT], rb[S::KEPT];
-  const auto load = [&](int w) {
-    const int64_t row = r0 + w * ROWS + group;
-    ra[w].load(base + row * p.ld_x);
-    rb[w].load(base + row * p.ld_x + D / 2);
-  };
   // a row's slot, and its position; -1 for one that is not stored
   const auto slot_at = [&](int64_t r, int& pos) {
     if (r < 0 || r >= p.N) return pos = -1;
@@ -193,47 +176,65 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Turn<S::D>* tu
     pos = p.positions[r];
     return pos >= 0 ? slot : -1;
   };
-  for (int i = tid; i < SPAN; i += THREADS) near_slot[i] = slot_at(r0 - BACK + i, near_pos[i]);
+  for (int i = tid; i < SPAN; i += THREADS) sm.slot[i] = slot_at(r0 - BACK + i, sm.pos[i]);
+  // the window's rows are on their way while their runs are found (where a page may be larger than the window, many
+  // windows have no run of their own)
+  const bool early = page <= WINDOW;
+  Raw<T, E> ra[KEPT], rb[KEPT];
+  const auto load = [&](int w, Raw<T, E>& a, Raw<T, E>& b) {
+    const T* x = base + (r0 + w * ROWS + group) * p.ld_x;
+    a.load(x);
+    b.load(x + D / 2);
+  };
   if (early) {
 #pragma unroll
-    for (int w = 0; w < S::PASSES; ++w)
-      if (r0 + w * ROWS + group < p.N) load(w);
+    for (int w = 0; w < PASSES; ++w)
+      if (r0 + w * ROWS + group < p.N) load(w, ra[w], rb[w]);
   }
-  if (tid == 0) {
-    stop = INT32_MAX;
-    beyond = grown = 0;
-    leads[1] = breaks[1] = 0;
+  // this lane's pairs of a row: frequencies, and gains
+  uint64_t freq[E];
+  float ga[E], gb[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int j = gl * E + i;
+    freq[i] = is_v ? 0 : p.freq[j];
+    const bool gain = !is_v && p.k_gamma;
+    ga[i] = gain ? __bfloat162float(p.k_gamma[j]) : 1.f;
+    gb[i] = gain ? __bfloat162float(p.k_gamma[j + D / 2]) : 1.f;
   }
-  for (int i = tid; i < WINDOW; i += THREADS) top[i] = 0;
+  for (int i = tid; i < WINDOW; i += THREADS) sm.top[i] = 0;
+  if (tid == 0) sm.grown = 0;
   __syncthreads();
   const auto in_pool = [&](int slot) { return slot >= 0 && (slot >> p.page_shift) < p.num_pages; };
   const auto same_page = [&](int a, int b) { return b >= 0 && (a >> p.page_shift) == (b >> p.page_shift); };
-  // the slot of the nearest stored row before row r0 + i
+  // the slot, and the position, of row r0 + i
+  const auto slot_of = [&](int i) {
+    int pos;
+    return i < SPAN - BACK ? sm.slot[BACK + i] : slot_at(r0 + i, pos);
+  };
+  // the slot of the nearest stored row before it
   const auto before_of = [&](int i) {
-    int b = -1, pos;
+    int b = -1;
 #pragma unroll 1
-    for (int k = 1; k <= BACK && b < 0; ++k)
-      b = i - k < SPAN - BACK ? near_slot[BACK + i - k] : slot_at(r0 + i - k, pos);
+    for (int k = 1; k <= BACK && b < 0; ++k) b = slot_of(i - k);
     return b;
   };
-  if (tid < WINDOW) {
-    const unsigned who = WINDOW < 32 ? (1u << (WINDOW & 31)) - 1u : 0xffffffffu;
-    const int slot = near_slot[BACK + tid], before = slot >= 0 ? before_of(tid) : -1;
+  // rows of the window that begin a run, and all that end one
+  uint64_t lead_bits = 0, ends = 0;
+#pragma unroll
+  for (int i0 = 0; i0 < WINDOW; i0 += 32) {
+    const int i = i0 + lane, slot = i < WINDOW ? sm.slot[BACK + i] : -1, before = slot >= 0 ? before_of(i) : -1;
     const bool in = in_pool(slot), again_page = in && same_page(slot, before);
     // a page that comes again in another order: two runs would both set its scale
     const bool twice = again_page && slot <= before;
-    if (hh == 0 && ((slot >= 0 && !in) || twice)) set_status(p.status, MK_DEV_BAD_INDEX);
-    const unsigned l = __ballot_sync(who, in && !again_page), t = __ballot_sync(who, twice || (slot >= 0 && !in));
-    if (tid % 32 == 0) {
-      leads[tid / 32] = l;
-      breaks[tid / 32] = t;
-    }
+    if (hh == 0 && tid < 32 && ((slot >= 0 && !in) || twice)) set_status(p.status, MK_DEV_BAD_INDEX);
+    const unsigned l = __ballot_sync(0xffffffffu, in && !again_page);
+    const unsigned t = __ballot_sync(0xffffffffu, twice || (slot >= 0 && !in));
+    lead_bits |= (uint64_t)l << i0;
+    ends |= (uint64_t)(l | t) << i0;
   }
-  __syncthreads();
-  const uint64_t lead_bits = leads[0] | (uint64_t)leads[1] << 32;
   if (lead_bits == 0) return;
-  const uint64_t ends = lead_bits | breaks[0] | (uint64_t)breaks[1] << 32;
-  // the run that a row of the window belongs to, by its first row (-1: another block's, or none)
+  // the run that a row of the window belongs to, by its first row (-1: another window's, or none)
   const auto run_of = [&](int row) {
     const uint64_t e = ends & ((2ull << row) - 1ull);
     const int at = e ? 63 - __clzll((long long)e) : -1;
@@ -241,70 +242,79 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Turn<S::D>* tu
   };
   const int last = run_of(WINDOW - 1);
   // the last run's rows behind the window
-  for (int i0 = WINDOW; last >= 0; i0 += THREADS) {
-    const int i = i0 + tid;
-    int pos;
-    const int slot = i0 == WINDOW ? near_slot[BACK + i] : slot_at(r0 + i, pos), before = slot >= 0 ? before_of(i) : -1;
+  int more = 0;
+#pragma unroll 1
+  for (int i0 = WINDOW; last >= 0; i0 += 32) {
+    const int i = i0 + lane, slot = slot_of(i), before = slot >= 0 ? before_of(i) : -1;
     const bool on = in_pool(slot) && same_page(slot, before) && slot > before;
-    if (slot >= 0 && !on) atomicMin(&stop, i);
-    if (!__syncthreads_or(on)) break;  // (a run goes on within BACK rows)
-    const int end = stop;
-    if (on && i < end) atomicMax(&beyond, i + 1 - WINDOW);
-    if (end != INT32_MAX) break;
-    __syncthreads();
+    const unsigned stop = __ballot_sync(0xffffffffu, slot >= 0 && !on);
+    const unsigned all = __ballot_sync(0xffffffffu, on), mine = stop ? all & ((stop & -stop) - 1) : all;
+    if (mine) more = i0 - WINDOW + 32 - __clz((int)mine);
+    if (stop || !all) break;  // (a run goes on within BACK rows)
   }
-  __syncthreads();
-  const Pair pair = is_v ? Pair{} : pair_of<D>(tid % (D / 2), p, p.k_gamma);
-  const int more = beyond, passes = S::PASSES + (more + ROWS - 1) / ROWS;
+  const int passes = PASSES + (more + ROWS - 1) / ROWS;
 
-  // this group's row of a pass: its run, and its slot (-1: none of this block's)
-  const auto run_in = [&](int w) { return w < S::PASSES ? run_of(w * ROWS + group) : last; };
+  // this group's row of a pass: its run, and its slot (-1: none of this window's)
+  const auto run_in = [&](int w) { return w < PASSES ? run_of(w * ROWS + group) : last; };
   const auto slot_in = [&](int w) {
     const int i = w * ROWS + group;
-    int pos;
-    if (w < S::PASSES) return run_of(i) >= 0 ? near_slot[BACK + i] : -1;
-    return i - WINDOW >= more ? -1 : i < SPAN - BACK ? near_slot[BACK + i] : slot_at(r0 + i, pos);
+    if (w < PASSES) return run_of(i) >= 0 ? sm.slot[BACK + i] : -1;
+    return i - WINDOW < more ? slot_of(i) : -1;
   };
-  const auto turn_rows = [&](int w) {
-    if (is_v) return;
-    __syncthreads();
-    for (int i = tid / (D / 2); i < ROWS; i += THREADS / (D / 2)) {
-      const int k = w * ROWS + i;
+  // the values to be stored, with the hardware's sine and cosine: off by under 2^-20, and keys are rounded to 2^-4
+  const auto values = [&](int w, const Raw<T, E>& ra, const Raw<T, E>& rb, float (&a)[E], float (&b)[E]) {
+    ra.get(a);
+    rb.get(b);
+    if (!is_v) {
+      float r = 1.f;
+      if (p.k_gamma) {
+        uint64_t ss = 0;
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+          const uint64_t u = ptx::pair_f32(a[i], a[i + 1]), v = ptx::pair_f32(b[i], b[i + 1]);
+          ss = ptx::fma2(u, u, ptx::fma2(v, v, ss));
+        }
+        const float2 two = ptx::unpair_f32(ss);
+        float sum = two.x + two.y;
+#pragma unroll
+        for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
+        r = rsqrtf(sum * (1.0f / D) + p.eps);
+      }
+      const int k = w * ROWS + group;
       int pos;
-      if (k < SPAN - BACK) pos = near_pos[BACK + k];
+      if (k < SPAN - BACK) pos = sm.pos[BACK + k];
       else slot_at(r0 + k, pos);
-      make_turn<D, true>(turns[i], tid % (D / 2), pair, pos);
-    }
-    __syncthreads();
-  };
-  // a pass's values, as floats to be stored (zero where there is no row)
-  const auto values = [&](int w, int slot, const Raw<T, E>& ra, const Raw<T, E>& rb, float (&a)[E], float (&b)[E]) {
-    turn_rows(w);
+      const uint64_t r2 = ptx::pair_f32(r, r);
 #pragma unroll
-    for (int i = 0; i < E; ++i) a[i] = b[i] = 0.f;
-    if (slot >= 0) {
-      ra.get(a);
-      rb.get(b);
-      if (!is_v) norm_turn<E, D>(a, b, turns[group], gl, p.k_gamma != nullptr, p.eps, mask);
+      for (int i = 0; i < E; i += 2) {
+        float s[2], c[2];
 #pragma unroll
-      for (int i = 0; i < E; i += 2) {  // an infinity becomes NaN
-        const uint64_t u = ptx::pair_f32(a[i], a[i + 1]), v = ptx::pair_f32(b[i], b[i + 1]);
-        const float2 x = ptx::unpair_f32(ptx::fma2(u, 0, u)), y = ptx::unpair_f32(ptx::fma2(v, 0, v));
-        a[i] = x.x;
-        a[i + 1] = x.y;
-        b[i] = y.x;
-        b[i + 1] = y.y;
+        for (int e = 0; e < 2; ++e) {
+          const uint64_t turn = (uint64_t)(uint32_t)pos * freq[i + e];
+          const float angle = (float)(int32_t)(turn >> 32) * (0x1p-31f * 3.14159265f);
+          s[e] = __sinf(angle);
+          c[e] = __cosf(angle);
+        }
+        const uint64_t u = ptx::mul2(ptx::mul2(r2, ptx::pair_f32(ga[i], ga[i + 1])), ptx::pair_f32(a[i], a[i + 1]));
+        const uint64_t v = ptx::mul2(ptx::mul2(r2, ptx::pair_f32(gb[i], gb[i + 1])), ptx::pair_f32(b[i], b[i + 1]));
+        const uint64_t c2 = ptx::pair_f32(c[0], c[1]), s2 = ptx::pair_f32(s[0], s[1]), n2 = ptx::pair_f32(-s[0], -s[1]);
+        const float2 ya = ptx::unpair_f32(ptx::fma2(v, n2, ptx::mul2(u, c2)));
+        const float2 yb = ptx::unpair_f32(ptx::fma2(u, s2, ptx::mul2(v, c2)));
+        a[i] = ya.x;
+        a[i + 1] = ya.y;
+        b[i] = yb.x;
+        b[i + 1] = yb.y;
       }
     }
-  };
-  // the same of a pass that is not kept
-  const auto read = [&](int w, int slot, float (&a)[E], float (&b)[E]) {
-    Raw<T, E> xa, xb;
-    if (slot >= 0) {
-      xa.load(base + (r0 + w * ROWS + group) * p.ld_x);
-      xb.load(base + (r0 + w * ROWS + group) * p.ld_x + D / 2);
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {  // an infinity becomes NaN
+      const uint64_t u = ptx::pair_f32(a[i], a[i + 1]), v = ptx::pair_f32(b[i], b[i + 1]);
+      const float2 x = ptx::unpair_f32(ptx::fma2(u, 0, u)), y = ptx::unpair_f32(ptx::fma2(v, 0, v));
+      a[i] = x.x;
+      a[i + 1] = x.y;
+      b[i] = y.x;
+      b[i + 1] = y.y;
     }
-    values(w, slot, xa, xb, a, b);
   };
   const auto raise = [&](int run, const float (&a)[E], const float (&b)[E]) {
     float m = 0.f;  // (a maximum leaves NaN out)
@@ -312,66 +322,70 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Turn<S::D>* tu
     for (int i = 0; i < E; ++i) m = fmaxf(m, fmaxf(fabsf(a[i]), fabsf(b[i])));
 #pragma unroll
     for (int o = LPH / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
-    if (gl == 0 && m > 0.f) atomicMax(&top[run], __float_as_uint(m));
+    if (gl == 0) atomicMax(&sm.top[run], __float_as_uint(m));
   };
-  int slot_k[S::KEPT], run_k[S::KEPT];
+  int slot_k[KEPT], run_k[KEPT];
 #pragma unroll
-  for (int w = 0; w < S::KEPT; ++w) {
+  for (int w = 0; w < KEPT; ++w) {
     slot_k[w] = w < passes ? slot_in(w) : -1;
     run_k[w] = max(run_in(w), 0);
-    if ((w >= S::PASSES || !early) && slot_k[w] >= 0) load(w);
+    if ((w >= PASSES || !early) && slot_k[w] >= 0) load(w, ra[w], rb[w]);
   }
-  float ka[S::KEPT][E], kb[S::KEPT][E];
+  float ka[KEPT][E], kb[KEPT][E];
 #pragma unroll
-  for (int w = 0; w < S::KEPT; ++w) {
-    if (w >= passes) break;
-    values(w, slot_k[w], ra[w], rb[w], ka[w], kb[w]);
+  for (int w = 0; w < KEPT; ++w) {
+    if (slot_k[w] < 0) continue;  // (whole lane groups; the shuffles name their lanes only)
+    values(w, ra[w], rb[w], ka[w], kb[w]);
     raise(run_k[w], ka[w], kb[w]);
   }
-  for (int w = S::KEPT; w < passes; ++w) {
+#pragma unroll 1
+  for (int w = KEPT; w < passes; ++w) {
+    if (slot_in(w) < 0) continue;
+    Raw<T, E> xa, xb;
     float a[E], b[E];
-    read(w, slot_in(w), a, b);
+    load(w, xa, xb);
+    values(w, xa, xb, a, b);
     raise(last, a, b);
   }
   __syncthreads();
   float* scales = is_v ? p.vscale : p.kscale;
   uint8_t* codes = is_v ? p.vcodes : p.kcodes;
   if (tid < WINDOW && (lead_bits >> tid & 1)) {
-    const int slot = near_slot[BACK + tid];
+    const int slot = sm.slot[BACK + tid];
     float* at = scales + (int64_t)(slot >> p.page_shift) * p.Hkv + head;
-    float s = scale_for(__uint_as_float(top[tid])), by = 1.f;
+    float s = scale_for(__uint_as_float(sm.top[tid])), by = 1.f;
     if ((slot & (page - 1)) != 0) {  // a page that is begun
       const float old = *at;
       if (old >= s) s = old;
       else by = old / s;
-      if (by != 1.f) grown = 1;
+      if (by != 1.f) sm.grown = 1;
     }
     *at = s;
-    inv_of[tid] = 1.f / s;
-    again[tid] = by;
+    sm.inv[tid] = 1.f / s;
+    sm.again[tid] = by;
   }
   __syncthreads();
-  if (grown) {
+  if (sm.grown) {
     // pages whose scale grew: what they hold below the last new row, but for what is new
-    for (int i = tid; i < WINDOW; i += THREADS) upto[i] = 0;
-    for (int i = tid; i < WINDOW * 8; i += THREADS) written[i / 8][i % 8] = 0;
+    for (int i = tid; i < WINDOW; i += THREADS) sm.upto[i] = 0;
+    for (int i = tid; i < WINDOW * 8; i += THREADS) sm.written[i / 8][i % 8] = 0;
     __syncthreads();
     for (int w = 0; w < passes; ++w) {
       const int slot = slot_in(w), off = slot & (page - 1);
       if (gl != 0 || slot < 0) continue;
-      atomicOr(&written[run_in(w)][off / 32], 1u << (off % 32));
-      atomicMax(&upto[run_in(w)], off);
+      atomicOr(&sm.written[run_in(w)][off / 32], 1u << (off % 32));
+      atomicMax(&sm.upto[run_in(w)], off);
     }
     __syncthreads();
     for (uint64_t rest = lead_bits; rest; rest &= rest - 1) {
       const int i = __ffsll((long long)rest) - 1;
-      const float by = again[i];
+      const float by = sm.again[i];
       if (by == 1.f) continue;
       uint4* at = reinterpret_cast<uint4*>(
-          codes + (((int64_t)(near_slot[BACK + i] >> p.page_shift) * p.Hkv + head) << p.page_shift) * D);
-      for (int j = tid; j < upto[i] * (D / 16); j += THREADS) {
+          codes + (((int64_t)(sm.slot[BACK + i] >> p.page_shift) * p.Hkv + head) << p.page_shift) * D);
+      for (int j = tid; j < sm.upto[i] * (D / 16); j += THREADS) {
         const int off = j / (D / 16);
-        if (written[i][off / 32] >> (off % 32) & 1) continue;
+        if (sm.written[i][off / 32] >> (off % 32) & 1) continue;
         uint4 v = at[j];
         v.x = rescale4(v.x, by); v.y = rescale4(v.y, by); v.z = rescale4(v.z, by); v.w = rescale4(v.w, by);
         at[j] = v;
@@ -379,19 +393,23 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Turn<S::D>* tu
     }
   }
   const auto put = [&](int slot, int run, const float (&a)[E], const float (&b)[E]) {
-    if (slot < 0) return;
     uint8_t* dst = codes + ((((int64_t)(slot >> p.page_shift) * p.Hkv + head) << p.page_shift) + (slot & (page - 1))) * D +
                    gl * E;
-    const float inv = inv_of[run];
+    const float inv = sm.inv[run];
     store_codes<E>(dst, a, inv);
     store_codes<E>(dst + D / 2, b, inv);
   };
 #pragma unroll
-  for (int w = 0; w < S::KEPT; ++w) put(slot_k[w], run_k[w], ka[w], kb[w]);
-  for (int w = S::KEPT; w < passes; ++w) {
-    float a[E], b[E];
+  for (int w = 0; w < KEPT; ++w)
+    if (slot_k[w] >= 0) put(slot_k[w], run_k[w], ka[w], kb[w]);
+#pragma unroll 1
+  for (int w = KEPT; w < passes; ++w) {
     const int slot = slot_in(w);
-    read(w, slot, a, b);
+    if (slot < 0) continue;
+    Raw<T, E> xa, xb;
+    float a[E], b[E];
+    load(w, xa, xb);
+    values(w, xa, xb, a, b);
     put(slot, last, a, b);
   }
 }
@@ -424,11 +442,9 @@ __device__ __forceinline__ void queries(const Store8Params& p, Turn<S::D>* turns
     }
     if (h == h0) {
       if (in) pos = p.positions[row];
-      const int j = threadIdx.x % (D / 2);
-      const Pair pair = pair_of<D>(j, p, p.q_gamma);
-      for (int i = threadIdx.x / (D / 2); i < p.tokens; i += THREADS / (D / 2)) {
-        const int64_t r = row0 + i;
-        make_turn<D, false>(turns[i], j, pair, r < p.N ? p.positions[r] : 0);
+      for (int i = threadIdx.x; i < p.tokens * (D / 2); i += THREADS) {
+        const int64_t r = row0 + i / (D / 2);
+        make_turn<D>(turns[i / (D / 2)], i % (D / 2), p, r < p.N ? p.positions[r] : 0);
       }
       __syncthreads();
     }
@@ -450,40 +466,49 @@ __device__ __forceinline__ void queries(const Store8Params& p, Turn<S::D>* turns
 // Keys and values first, then the queries, in one launch
 template <typename S>
 __global__ void __launch_bounds__(S::THREADS) store8_kernel(const __grid_constant__ Store8Params p) {
-  __shared__ __align__(16) Turn<S::D> turns[S::ROWS];
-  if (blockIdx.x < p.kv_blocks) store_runs<S>(p, turns, blockIdx.x);
-  else queries<S>(p, turns, blockIdx.x - p.kv_blocks);
+  __shared__ union alignas(16) Both {
+    __device__ Both() {}
+    Runs<S::WINDOW> runs;
+    Turn<S::D> turns[kQueryMaxTokens];
+  } sm;
+  if (blockIdx.x < p.kv_blocks) store_runs<S>(p, sm.runs, blockIdx.x);
+  else queries<S>(p, sm.turns, blockIdx.x - p.kv_blocks);
 }
 // Keys and values alone
 template <typename S>
-__global__ void __launch_bounds__(S::THREADS, 2) store8_kv_kernel(const __grid_constant__ Store8Params p) {
+__global__ void __launch_bounds__(S::THREADS, 512 / S::THREADS) store8_kv_kernel(const __grid_constant__ Store8Params p) {
+  __shared__ Runs<S::WINDOW> runs;
   ptx::launch_dependents();  // the queries' blocks follow as these end
-  __shared__ __align__(16) Turn<S::D> turns[S::ROWS];
-  store_runs<S>(p, turns, blockIdx.x);
+  store_runs<S>(p, runs, blockIdx.x);
 }
 
 #ifndef FEW_ROWS
 #define FEW_ROWS 512
 #endif
+#ifndef KVT
+#define KVT 256
+#define KVW 64
+#define KVK 1
+#endif
 template <typename T, int D>
 cudaError_t launch_store8(Store8Params& p, int sms, cudaStream_t stream) {
   constexpr int E = kElems<T>, LPH = D / 2 / E;
+  const auto kv_blocks = [&](int window) { return (unsigned)(((int64_t)p.N + window - 1) / window * 2 * p.Hkv); };
   if (p.N > FEW_ROWS) {
-    using S = Shape<T, D, 256, 64, 64>;
-    const int64_t kv = (((int64_t)p.N + S::WINDOW - 1) / S::WINDOW) * 2 * p.Hkv;
-    store8_kv_kernel<S><<<(unsigned)kv, S::THREADS, 0, stream>>>(p);
+    using S = Shape<T, D, KVT, KVW, KVK * KVW / (KVT / LPH)>;
+    store8_kv_kernel<S><<<kv_blocks(S::WINDOW), S::THREADS, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_queries(p, sizeof(T) == 4 ? MK_F32 : MK_BF16, D, sms, stream);
   }
-  using S = Shape<T, D, 16 * LPH, 16, 10 * E>;
+  using S = Shape<T, D, 16 * LPH, 16, 5>;
   constexpr int GP = S::ROWS;
   // tokens whose heads fill a block's batch; few tokens: a head per lane group, over several blocks
   p.tokens = 1;
   while (p.tokens < kQueryMaxTokens && 2 * p.tokens * p.Hq <= kQueryBatch * GP) p.tokens *= 2;
   while (p.tokens > 1 && (p.N + p.tokens - 1) / p.tokens < 2 * sms) p.tokens /= 2;
   p.splits = p.N < sms ? (p.Hq + GP - 1) / GP : 1;
-  p.kv_blocks = (unsigned)((p.N + S::WINDOW - 1) / S::WINDOW * 2 * p.Hkv);
+  p.kv_blocks = kv_blocks(S::WINDOW);
   const unsigned blocks = p.kv_blocks + (unsigned)((p.N + p.tokens - 1) / p.tokens * p.splits);
   store8_kernel<S><<<blocks, S::THREADS, 0, stream>>>(p);
   return cudaGetLastError();
