@@ -144,10 +144,15 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float by) {
 }
 
 // What a block keeps in shared memory.
-template <int WINDOW>
+template <int WINDOW, int D>
 struct Runs {
   static constexpr int BACK = kGap + 1, SPAN = BACK + WINDOW + 64;  // rows around the window that are looked at at once
+  uint64_t freq[D / 2];
+  float2 gain[D / 2];               // of both elements of a pair
   int slot[SPAN], pos[SPAN];
+  int run[WINDOW];                  // the first row of a row's run; -1: of another window's, or none
+  uint64_t leads;                   // rows that begin a run
+  int more;                         // rows behind the window up to the end of the last run
   unsigned top[WINDOW];             // maxima of the runs, by first row
   float inv[WINDOW], again[WINDOW]; // 1 / scale; what held codes are multiplied with (1: they stay)
   unsigned written[WINDOW][8];      // offsets that a run writes, where what a page holds is looked at again
@@ -158,10 +163,10 @@ struct Runs {
 // The runs of a key or value head that begin in a window; the rows of a run go to one page, each at a higher offset than
 // the one before.
 template <typename S>
-__device__ __forceinline__ void store_runs(const Store8Params& p, Runs<S::WINDOW>& sm, unsigned block) {
+__device__ __forceinline__ void store_runs(const Store8Params& p, Runs<S::WINDOW, S::D>& sm, unsigned block) {
   using T = typename S::T;
   constexpr int D = S::D, E = S::E, LPH = S::LPH, ROWS = S::ROWS, WINDOW = S::WINDOW, PASSES = S::PASSES, KEPT = S::KEPT;
-  constexpr int THREADS = S::THREADS, BACK = Runs<WINDOW>::BACK, SPAN = Runs<WINDOW>::SPAN;
+  constexpr int THREADS = S::THREADS, BACK = Runs<WINDOW, D>::BACK, SPAN = Runs<WINDOW, D>::SPAN;
   const int tid = threadIdx.x, lane = tid % 32, gl = tid % LPH, group = tid / LPH;
   const int hh = block % (2 * p.Hkv);
   const int64_t r0 = (int64_t)(block / (2 * p.Hkv)) * WINDOW;
@@ -176,7 +181,11 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Runs<S::WINDOW
     pos = p.positions[r];
     return pos >= 0 ? slot : -1;
   };
-  for (int i = tid; i < SPAN; i += THREADS) sm.slot[i] = slot_at(r0 - BACK + i, sm.pos[i]);
+  // the slot of row r0 + i
+  const auto slot_of = [&](int i) {
+    int pos;
+    return i < SPAN - BACK ? sm.slot[BACK + i] : slot_at(r0 + i, pos);
+  };
   // the window's rows are on their way while their runs are found (where a page may be larger than the window, many
   // windows have no run of their own)
   const bool early = page <= WINDOW;
@@ -186,79 +195,79 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Runs<S::WINDOW
     a.load(x);
     b.load(x + D / 2);
   };
+  if (tid < 32) {
+    // the first warp finds the runs
+#pragma unroll
+    for (int i = lane; i < SPAN; i += 32) sm.slot[i] = slot_at(r0 - BACK + i, sm.pos[i]);
+    __syncwarp();
+    const auto in_pool = [&](int slot) { return slot >= 0 && (slot >> p.page_shift) < p.num_pages; };
+    const auto same_page = [&](int a, int b) { return b >= 0 && (a >> p.page_shift) == (b >> p.page_shift); };
+    // the slot of the nearest stored row before row r0 + i
+    const auto before_of = [&](int i) {
+      int b = slot_of(i - 1);
+#pragma unroll 1
+      for (int k = 2; k <= BACK && b < 0; ++k) b = slot_of(i - k);
+      return b;
+    };
+    uint64_t leads = 0, ends = 0;  // rows that begin a run, and all that end one
+#pragma unroll
+    for (int i0 = 0; i0 < WINDOW; i0 += 32) {
+      const int i = i0 + lane, slot = i < WINDOW ? sm.slot[BACK + i] : -1, before = slot >= 0 ? before_of(i) : -1;
+      const bool in = in_pool(slot), again_page = in && same_page(slot, before);
+      // a page that comes again in another order: two runs would both set its scale
+      const bool twice = again_page && slot <= before;
+      if (hh == 0 && ((slot >= 0 && !in) || twice)) set_status(p.status, MK_DEV_BAD_INDEX);
+      const unsigned l = __ballot_sync(0xffffffffu, in && !again_page);
+      const unsigned t = __ballot_sync(0xffffffffu, twice || (slot >= 0 && !in));
+      leads |= (uint64_t)l << i0;
+      ends |= (uint64_t)(l | t) << i0;
+    }
+    const auto run_of = [&](int row) {
+      const uint64_t e = ends & ((2ull << row) - 1ull);
+      const int at = e ? 63 - __clzll((long long)e) : -1;
+      return at >= 0 && (leads >> at & 1) ? at : -1;
+    };
+    for (int i = lane; i < WINDOW; i += 32) sm.run[i] = sm.slot[BACK + i] >= 0 ? run_of(i) : -1;
+    // the last run's rows behind the window
+    int more = 0;
+    const bool goes_on = run_of(WINDOW - 1) >= 0;
+#pragma unroll 1
+    for (int i0 = WINDOW; goes_on; i0 += 32) {
+      const int i = i0 + lane, slot = slot_of(i), before = slot >= 0 ? before_of(i) : -1;
+      const bool on = in_pool(slot) && same_page(slot, before) && slot > before;
+      const unsigned stop = __ballot_sync(0xffffffffu, slot >= 0 && !on);
+      const unsigned all = __ballot_sync(0xffffffffu, on), mine = stop ? all & ((stop & -stop) - 1) : all;
+      if (mine) more = i0 - WINDOW + 32 - __clz((int)mine);
+      if (stop || !all) break;  // (a run goes on within BACK rows)
+    }
+    if (lane == 0) {
+      sm.leads = leads;
+      sm.more = more;
+      sm.grown = 0;
+    }
+  } else if (!is_v) {
+    for (int j = tid - 32; j < D / 2; j += THREADS - 32) {
+      sm.freq[j] = p.freq[j];
+      sm.gain[j] = p.k_gamma ? make_float2(__bfloat162float(p.k_gamma[j]), __bfloat162float(p.k_gamma[j + D / 2]))
+                             : make_float2(1.f, 1.f);
+    }
+  }
   if (early) {
 #pragma unroll
     for (int w = 0; w < PASSES; ++w)
       if (r0 + w * ROWS + group < p.N) load(w, ra[w], rb[w]);
   }
-  // this lane's pairs of a row: frequencies, and gains
-  uint64_t freq[E];
-  float ga[E], gb[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int j = gl * E + i;
-    freq[i] = is_v ? 0 : p.freq[j];
-    const bool gain = !is_v && p.k_gamma;
-    ga[i] = gain ? __bfloat162float(p.k_gamma[j]) : 1.f;
-    gb[i] = gain ? __bfloat162float(p.k_gamma[j + D / 2]) : 1.f;
-  }
   for (int i = tid; i < WINDOW; i += THREADS) sm.top[i] = 0;
-  if (tid == 0) sm.grown = 0;
   __syncthreads();
-  const auto in_pool = [&](int slot) { return slot >= 0 && (slot >> p.page_shift) < p.num_pages; };
-  const auto same_page = [&](int a, int b) { return b >= 0 && (a >> p.page_shift) == (b >> p.page_shift); };
-  // the slot, and the position, of row r0 + i
-  const auto slot_of = [&](int i) {
-    int pos;
-    return i < SPAN - BACK ? sm.slot[BACK + i] : slot_at(r0 + i, pos);
-  };
-  // the slot of the nearest stored row before it
-  const auto before_of = [&](int i) {
-    int b = -1;
-#pragma unroll 1
-    for (int k = 1; k <= BACK && b < 0; ++k) b = slot_of(i - k);
-    return b;
-  };
-  // rows of the window that begin a run, and all that end one
-  uint64_t lead_bits = 0, ends = 0;
-#pragma unroll
-  for (int i0 = 0; i0 < WINDOW; i0 += 32) {
-    const int i = i0 + lane, slot = i < WINDOW ? sm.slot[BACK + i] : -1, before = slot >= 0 ? before_of(i) : -1;
-    const bool in = in_pool(slot), again_page = in && same_page(slot, before);
-    // a page that comes again in another order: two runs would both set its scale
-    const bool twice = again_page && slot <= before;
-    if (hh == 0 && tid < 32 && ((slot >= 0 && !in) || twice)) set_status(p.status, MK_DEV_BAD_INDEX);
-    const unsigned l = __ballot_sync(0xffffffffu, in && !again_page);
-    const unsigned t = __ballot_sync(0xffffffffu, twice || (slot >= 0 && !in));
-    lead_bits |= (uint64_t)l << i0;
-    ends |= (uint64_t)(l | t) << i0;
-  }
+  const uint64_t lead_bits = sm.leads;
   if (lead_bits == 0) return;
-  // the run that a row of the window belongs to, by its first row (-1: another window's, or none)
-  const auto run_of = [&](int row) {
-    const uint64_t e = ends & ((2ull << row) - 1ull);
-    const int at = e ? 63 - __clzll((long long)e) : -1;
-    return at >= 0 && (lead_bits >> at & 1) ? at : -1;
-  };
-  const int last = run_of(WINDOW - 1);
-  // the last run's rows behind the window
-  int more = 0;
-#pragma unroll 1
-  for (int i0 = WINDOW; last >= 0; i0 += 32) {
-    const int i = i0 + lane, slot = slot_of(i), before = slot >= 0 ? before_of(i) : -1;
-    const bool on = in_pool(slot) && same_page(slot, before) && slot > before;
-    const unsigned stop = __ballot_sync(0xffffffffu, slot >= 0 && !on);
-    const unsigned all = __ballot_sync(0xffffffffu, on), mine = stop ? all & ((stop & -stop) - 1) : all;
-    if (mine) more = i0 - WINDOW + 32 - __clz((int)mine);
-    if (stop || !all) break;  // (a run goes on within BACK rows)
-  }
-  const int passes = PASSES + (more + ROWS - 1) / ROWS;
-
+  const int more = sm.more, passes = PASSES + (more + ROWS - 1) / ROWS;
+  const int last = passes > PASSES ? sm.run[63 - __clzll((long long)lead_bits)] : 0;  // the run that goes on
   // this group's row of a pass: its run, and its slot (-1: none of this window's)
-  const auto run_in = [&](int w) { return w < PASSES ? run_of(w * ROWS + group) : last; };
+  const auto run_in = [&](int w) { return w < PASSES ? sm.run[w * ROWS + group] : last; };
   const auto slot_in = [&](int w) {
     const int i = w * ROWS + group;
-    if (w < PASSES) return run_of(i) >= 0 ? sm.slot[BACK + i] : -1;
+    if (w < PASSES) return sm.run[i] >= 0 ? sm.slot[BACK + i] : -1;
     return i - WINDOW < more ? slot_of(i) : -1;
   };
   // the values to be stored, with the hardware's sine and cosine: off by under 2^-20, and keys are rounded to 2^-4
@@ -290,13 +299,14 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Runs<S::WINDOW
         float s[2], c[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const uint64_t turn = (uint64_t)(uint32_t)pos * freq[i + e];
+          const uint64_t turn = (uint64_t)(uint32_t)pos * sm.freq[gl * E + i + e];
           const float angle = (float)(int32_t)(turn >> 32) * (0x1p-31f * 3.14159265f);
           s[e] = __sinf(angle);
           c[e] = __cosf(angle);
         }
-        const uint64_t u = ptx::mul2(ptx::mul2(r2, ptx::pair_f32(ga[i], ga[i + 1])), ptx::pair_f32(a[i], a[i + 1]));
-        const uint64_t v = ptx::mul2(ptx::mul2(r2, ptx::pair_f32(gb[i], gb[i + 1])), ptx::pair_f32(b[i], b[i + 1]));
+        const float2 g0 = sm.gain[gl * E + i], g1 = sm.gain[gl * E + i + 1];
+        const uint64_t u = ptx::mul2(ptx::mul2(r2, ptx::pair_f32(g0.x, g1.x)), ptx::pair_f32(a[i], a[i + 1]));
+        const uint64_t v = ptx::mul2(ptx::mul2(r2, ptx::pair_f32(g0.y, g1.y)), ptx::pair_f32(b[i], b[i + 1]));
         const uint64_t c2 = ptx::pair_f32(c[0], c[1]), s2 = ptx::pair_f32(s[0], s[1]), n2 = ptx::pair_f32(-s[0], -s[1]);
         const float2 ya = ptx::unpair_f32(ptx::fma2(v, n2, ptx::mul2(u, c2)));
         const float2 yb = ptx::unpair_f32(ptx::fma2(u, s2, ptx::mul2(v, c2)));
@@ -463,12 +473,15 @@ __device__ __forceinline__ void queries(const Store8Params& p, Turn<S::D>* turns
   }
 }
 
+#ifndef KVB
+#define KVB 3
+#endif
 // Keys and values first, then the queries, in one launch
 template <typename S>
 __global__ void __launch_bounds__(S::THREADS) store8_kernel(const __grid_constant__ Store8Params p) {
   __shared__ union alignas(16) Both {
     __device__ Both() {}
-    Runs<S::WINDOW> runs;
+    Runs<S::WINDOW, S::D> runs;
     Turn<S::D> turns[kQueryMaxTokens];
   } sm;
   if (blockIdx.x < p.kv_blocks) store_runs<S>(p, sm.runs, blockIdx.x);
@@ -476,8 +489,8 @@ __global__ void __launch_bounds__(S::THREADS) store8_kernel(const __grid_constan
 }
 // Keys and values alone
 template <typename S>
-__global__ void __launch_bounds__(S::THREADS, 512 / S::THREADS) store8_kv_kernel(const __grid_constant__ Store8Params p) {
-  __shared__ Runs<S::WINDOW> runs;
+__global__ void __launch_bounds__(S::THREADS, KVB) store8_kv_kernel(const __grid_constant__ Store8Params p) {
+  __shared__ Runs<S::WINDOW, S::D> runs;
   ptx::launch_dependents();  // the queries' blocks follow as these end
   store_runs<S>(p, runs, blockIdx.x);
 }
