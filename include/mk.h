@@ -575,8 +575,8 @@ int mk_qk_norm_rope_e4m3(void* stream, int N, int Hq, int Hkv, int D, const void
                          const int32_t* positions, const int32_t* slots, void* q_out, int64_t ld_q, void* kpool,
                          void* vpool, float* kscale, float* vscale, int num_pages, int page_size, int32_t* status);
 
-/* Attention: arguments, workspace, checks and status of mk_paged_attention.  Scales
- * are positive and finite.  Queries keep 2^-18 of a row's largest element and more.
+/* Attention: arguments, checks and status of mk_paged_attention, and a workspace of
+ * mk_paged_attention_e4m3_workspace bytes.  Scales are positive and finite.  Queries keep 2^-18 of a row's largest element and more.
  * Probabilities are rounded to f16 (2^-11) in both kernels, maxima, sums and results
  * are f32.  Keys' scales are f32 factors of the scores.  Values' scales are exact
  * where they are powers of two (what the stores write) within 2^15 of each other;
@@ -586,6 +586,9 @@ int mk_paged_attention_e4m3(void* stream, int B, int N, int max_new, int Hq, int
                             const float* vscale, int num_pages, int page_size, const int32_t* table, int max_pages,
                             const int32_t* cu, const int32_t* ctx_len, float scale, void* out, int64_t ld_out,
                             void* workspace, size_t workspace_size, int32_t* status);
+
+/* Bytes of workspace mk_paged_attention_e4m3 needs on the current device. */
+int mk_paged_attention_e4m3_workspace(int max_new, int Hq, int Hkv, int D, size_t* bytes);
 
 /* Verification of drafted tokens from given random numbers (speculative
  * sampling).  Per request, K drafts (draft_len[b] of them; NULL: all K):

@@ -112,6 +112,7 @@ def lib():
         "mk_paged_attention_e4m3": (c_int, [c_void_p] + [c_int] * 6 + [c_void_p, c_int64] + [c_void_p] * 4 +
                                     [c_int, c_int, c_void_p, c_int, c_void_p, c_void_p, c_float, c_void_p, c_int64,
                                      c_void_p, c_size_t, c_void_p]),
+        "mk_paged_attention_e4m3_workspace": (c_int, [c_int, c_int, c_int, c_int, POINTER(c_size_t)]),
         "mk_token_logprobs": (c_int, [c_void_p, c_int, c_int, c_void_p, c_int, c_int64, c_void_p, c_int] +
                               [c_void_p] * 5),
         "mk_verify_drafts": (c_int, [c_void_p, c_int, c_int, c_int, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
@@ -152,7 +153,7 @@ def calls():
     m.bind(MkError, *[ctypes.cast(getattr(L, f), c_void_p).value for f in
                       ("mk_paged_plan", "mk_qk_norm_rope", "mk_paged_attention", "mk_paged_attention_workspace",
                        "mk_verify_drafts", "mk_last_error", "mk_qk_norm_rope_e4m3", "mk_paged_attention_e4m3",
-                       "mk_token_logprobs")])
+                       "mk_token_logprobs", "mk_paged_attention_e4m3_workspace")])
     _calls = m
     return m
 
@@ -403,6 +404,13 @@ def mk_token_logprobs(stream: int, N: int, V: int, logits: int, logits_dtype: in
 def mk_paged_attention_workspace(max_new: int, Hq: int, Hkv: int, D: int) -> int:
     n = c_size_t()
     check(lib().mk_paged_attention_workspace(max_new, Hq, Hkv, D, ctypes.byref(n)), "mk_paged_attention_workspace")
+    return n.value
+
+
+def mk_paged_attention_e4m3_workspace(max_new: int, Hq: int, Hkv: int, D: int) -> int:
+    n = c_size_t()
+    check(lib().mk_paged_attention_e4m3_workspace(max_new, Hq, Hkv, D, ctypes.byref(n)),
+          "mk_paged_attention_e4m3_workspace")
     return n.value
 
 

@@ -36,6 +36,7 @@ decltype(&mk_verify_drafts) verify_drafts = nullptr;
 decltype(&mk_qk_norm_rope_e4m3) qk_norm_rope_e4m3 = nullptr;
 decltype(&mk_paged_attention_e4m3) paged_attention_e4m3 = nullptr;
 decltype(&mk_token_logprobs) token_logprobs = nullptr;
+decltype(&mk_paged_attention_e4m3_workspace) paged_attention_e4m3_workspace = nullptr;
 decltype(&mk_last_error) last_error = nullptr;
 PyObject* mk_error = nullptr;  // the binding's exception class
 
@@ -300,17 +301,18 @@ PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // Workspace bytes, asked of the library once per device and shape.  The lock is never held where Python code can
 // run (the exception of a refused shape is Python code): another thread may be waiting for it with the interpreter's
 // lock.
-size_t workspace_size(int dev, int max_new, int Hq, int Hkv, int D) {
+size_t workspace_size(bool e4m3, int dev, int max_new, int Hq, int Hkv, int D) {
   static std::mutex mu;
-  static std::map<std::tuple<int, int, int, int, int>, size_t> known;
-  const auto key = std::make_tuple(dev, max_new, Hq, Hkv, D);
+  static std::map<std::tuple<bool, int, int, int, int, int>, size_t> known;
+  const auto key = std::make_tuple(e4m3, dev, max_new, Hq, Hkv, D);
   {
     const std::lock_guard<std::mutex> lock(mu);
     const auto it = known.find(key);
     if (it != known.end()) return it->second;
   }
   size_t bytes = 0;
-  check(paged_attention_workspace(max_new, Hq, Hkv, D, &bytes), "mk_paged_attention_workspace");
+  if (e4m3) check(paged_attention_e4m3_workspace(max_new, Hq, Hkv, D, &bytes), "mk_paged_attention_e4m3_workspace");
+  else check(paged_attention_workspace(max_new, Hq, Hkv, D, &bytes), "mk_paged_attention_workspace");
   const std::lock_guard<std::mutex> lock(mu);
   known.emplace(key, bytes);
   return bytes;
@@ -355,7 +357,7 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         work = ws->data_ptr();
         size = ws->nbytes();
       } else {
-        size = workspace_size(dev, max_new, Hq, pl.Hkv, pl.D);
+        size = workspace_size(pl.kscale != nullptr, dev, max_new, Hq, pl.Hkv, pl.D);
         work = scratch.p = c10::cuda::CUDACachingAllocator::raw_alloc(size);
       }
       void* stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
@@ -468,11 +470,12 @@ PyObject* py_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // bind(MkError, addresses of mk_paged_plan, mk_qk_norm_rope, mk_paged_attention, mk_paged_attention_workspace,
-//      mk_verify_drafts, mk_last_error, mk_qk_norm_rope_e4m3, mk_paged_attention_e4m3, mk_token_logprobs)
+//      mk_verify_drafts, mk_last_error, mk_qk_norm_rope_e4m3, mk_paged_attention_e4m3, mk_token_logprobs,
+//      mk_paged_attention_e4m3_workspace)
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  constexpr int kFunctions = 9;
+  constexpr int kFunctions = 10;
   if (n != kFunctions + 1) {
-    PyErr_SetString(PyExc_TypeError, "bind takes 10 arguments");
+    PyErr_SetString(PyExc_TypeError, "bind takes 11 arguments");
     return nullptr;
   }
   void* f[kFunctions];
@@ -491,6 +494,7 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   qk_norm_rope_e4m3 = reinterpret_cast<decltype(qk_norm_rope_e4m3)>(f[6]);
   paged_attention_e4m3 = reinterpret_cast<decltype(paged_attention_e4m3)>(f[7]);
   token_logprobs = reinterpret_cast<decltype(token_logprobs)>(f[8]);
+  paged_attention_e4m3_workspace = reinterpret_cast<decltype(paged_attention_e4m3_workspace)>(f[9]);
   paged_plan = reinterpret_cast<decltype(paged_plan)>(f[0]);
   Py_RETURN_NONE;
 }

@@ -43,9 +43,9 @@ bool encode(EncodeTiledFn enc, CUtensorMap* m, const void* ptr, int rank, const 
 bool few_rows(int max_new, int G) { return (int64_t)max_new * G <= kMaxFewRows; }
 
 // Two partial records and a note per worker (paged_attention.cuh).
-size_t workspace_bytes(int max_new, int G, int D, int sms) {
+size_t workspace_bytes(int max_new, int G, int D, int sms, bool e4m3) {
   const bool few = few_rows(max_new, G);
-  const size_t workers = (size_t)sms * (few ? kRowWarps : 1), rows = few ? max_new * G : kTileRows;
+  const size_t workers = (size_t)sms * (!few ? 1 : e4m3 ? kRowWarps8 : kRowWarps), rows = few ? max_new * G : kTileRows;
   return 2 * workers * rows * (D + 2) * 4 + workers * 16;
 }
 
@@ -62,13 +62,23 @@ int check_shape(const char* who, int max_new, int Hq, int Hkv, int D) {
 
 using namespace mk;
 
-extern "C" int mk_paged_attention_workspace(int max_new, int Hq, int Hkv, int D, size_t* bytes) try {
-  if (!bytes) return fail(MK_ERR_ARG, "mk_paged_attention_workspace: null argument");
-  if (int rc = check_shape("mk_paged_attention_workspace", max_new, Hq, Hkv, D)) return rc;
+static int attention_workspace(const char* who, bool e4m3, int max_new, int Hq, int Hkv, int D, size_t* bytes) {
+  if (!bytes) return fail(MK_ERR_ARG, std::string(who) + ": null argument");
+  if (int rc = check_shape(who, max_new, Hq, Hkv, D)) return rc;
   int sms = 0;
-  if (int rc = device_sms("mk_paged_attention_workspace", &sms)) return rc;
-  *bytes = workspace_bytes(max_new, Hq / Hkv, D, sms);
+  if (int rc = device_sms(who, &sms)) return rc;
+  *bytes = workspace_bytes(max_new, Hq / Hkv, D, sms, e4m3);
   return MK_OK;
+}
+
+extern "C" int mk_paged_attention_workspace(int max_new, int Hq, int Hkv, int D, size_t* bytes) try {
+  return attention_workspace("mk_paged_attention_workspace", false, max_new, Hq, Hkv, D, bytes);
+} catch (...) {
+  return MK_ERR_NOMEM;
+}
+
+extern "C" int mk_paged_attention_e4m3_workspace(int max_new, int Hq, int Hkv, int D, size_t* bytes) try {
+  return attention_workspace("mk_paged_attention_e4m3_workspace", true, max_new, Hq, Hkv, D, bytes);
 } catch (...) {
   return MK_ERR_NOMEM;
 }
@@ -101,9 +111,9 @@ static int attention(const char* who, bool e4m3, void* stream_, int B, int N, in
   int sms = 0;
   if (int rc = device_sms(who, &sms)) return rc;
   const int G = Hq / Hkv;
-  if (workspace_size < workspace_bytes(max_new, G, D, sms))
+  if (workspace_size < workspace_bytes(max_new, G, D, sms, e4m3))
     return fail(MK_ERR_LIMIT, name + ": the workspace needs " +
-                                  std::to_string(workspace_bytes(max_new, G, D, sms)) + " bytes");
+                                  std::to_string(workspace_bytes(max_new, G, D, sms, e4m3)) + " bytes");
   if (B == 0 || N == 0) return MK_OK;
   EncodeTiledFn enc = encoder();
   if (!enc) return fail(MK_ERR_CUDA, name + ": cuTensorMapEncodeTiled is not available");
@@ -123,7 +133,7 @@ static int attention(const char* who, bool e4m3, void* stream_, int B, int N, in
   p.B = B; p.N = N; p.Hq = Hq; p.Hkv = Hkv; p.G = G; p.max_new = max_new;
   p.max_pages = max_pages; p.num_pages = num_pages;
   while ((1 << p.page_shift) < page_size) ++p.page_shift;
-  p.workers = few ? sms * kRowWarps : sms;
+  p.workers = sms * (!few ? 1 : e4m3 ? kRowWarps8 : kRowWarps);
   p.rows = few ? max_new * G : kTileRows;
   p.tq = few ? 0 : 128 / G;
   // The chunk kernel's softmax of a tile without tokens, and its warp for masked values, wait while a part's other
@@ -132,7 +142,7 @@ static int attention(const char* who, bool e4m3, void* stream_, int B, int N, in
 
   // pools as [rows, D], pages one after the other; a box is what one page gives a block of keys
   CUtensorMap kmap, vmap, qmap;
-  const int keys = !few ? 128 : e4m3 ? kRowKeys8 : kRowBlockBytes / D / 4, size = e4m3 ? 1 : 2;
+  const int keys = !few ? 128 : e4m3 ? kRowBlockBytes8 / D / 2 : kRowBlockBytes / D / 4, size = e4m3 ? 1 : 2;
   const cuuint64_t dim[2] = {(cuuint64_t)D, (cuuint64_t)num_pages * Hkv * page_size}, stride[1] = {(cuuint64_t)D * size};
   const cuuint32_t box[2] = {e4m3 ? (cuuint32_t)D : 64u, (cuuint32_t)(page_size < keys ? page_size : keys)};
   const CUtensorMapDataType type = e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;

@@ -50,17 +50,18 @@ struct Attn8Params : AttnParams {
   const uint8_t* v8;
   const float *kscale, *vscale;
 };
-constexpr int kRowKeys8 = 64;  // keys of a few-rows block of e4m3
+constexpr int kRowBlockBytes8 = 8192;  // keys and values of a few-rows block
+constexpr int kRowWarps8 = 8;          // warps (workers) per CTA of its kernel, a multiple of kRowWarps
 
 // Geometry of an item: few query rows (all of a request's), or a pair of
 // 128-row query tiles; E8: of e4m3 pages.
 template <int D, bool CHUNK, bool E8 = false>
 struct Geometry {
-  static constexpr int kKeys = CHUNK ? 128 : E8 ? kRowKeys8 : kRowBlockBytes / D / 4;  // keys per block
+  static constexpr int kKeys = CHUNK ? 128 : E8 ? kRowBlockBytes8 / D / 2 : kRowBlockBytes / D / 4;  // keys per block
   // an item's fixed cost, in keys: measured for few rows (paged_rows.cu); for chunks what surrounds a part's
   // blocks, some 2 us at 1.1 us for 128 keys of both tiles (256, 288 and 384 took the same time within noise, on
   // seven ragged chunks)
-  static constexpr int kFixed = CHUNK ? 320 : E8 ? 192 : 96;
+  static constexpr int kFixed = CHUNK ? 320 : E8 ? 128 : 96;
 };
 
 struct Seq {
@@ -130,6 +131,9 @@ struct Line {
 };
 
 // A whole warp; lanes agree but for `own`.
+#ifndef LEAST8
+#define LEAST8 2
+#endif
 template <int D, bool CHUNK, bool E8 = false>
 __device__ __forceinline__ Line measure_line(const AttnParams& p, int lane) {
   Line l;
@@ -150,7 +154,7 @@ __device__ __forceinline__ Line measure_line(const AttnParams& p, int lane) {
   l.u = u;
   // whole blocks, a few at least: fewer records to join where there is little to do, and a worker behind an
   // item's first block always has a part of it
-  constexpr int K = Geometry<D, CHUNK, E8>::kKeys, kLeast = (CHUNK ? 1 : 2) * K;
+  constexpr int K = Geometry<D, CHUNK, E8>::kKeys, kLeast = (CHUNK ? 1 : E8 ? LEAST8 : 2) * K;
   const int64_t even = (u + p.workers - 1) / p.workers;
   l.part = even <= kLeast ? kLeast : (even + K - 1) / K * K;
   return l;

@@ -28,18 +28,10 @@ namespace {
 using namespace ptx;
 
 static_assert(kMaxFewRows == 8, "the query rows are the eight columns of a product");
-constexpr int KU = kRowKeys8, NK = KU / 16;  // keys of a block, key tiles
-constexpr int kMostPages = KU / 16;          // pages that a block touches
 constexpr float kBias = 14.f;                // probabilities are kept times 2^kBias
-template <int D>
-constexpr int kStages8 = D == 128 ? 3 : 6;
-template <int D>
-constexpr int kStageBytes8 = 2 * KU * D;
-
-template <int D>
-constexpr int smem_bytes_rows8() {
-  return 1024 + kRowWarps * kStages8<D> * kStageBytes8<D>;
-}
+constexpr int kStages8 = 3;
+constexpr int kSmemBytes8 = 1024 + kRowWarps8 * kStages8 * kRowBlockBytes8;
+static_assert(kSmemBytes8 <= 229376, "shared memory of a CTA, beside the static part");
 
 // 16-byte chunk c of row r in a tile of D-byte rows: 128-byte or 64-byte swizzle
 template <int D>
@@ -54,14 +46,16 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return __vcmpeq4(w &
 __device__ __forceinline__ float exp2_down(int d) { return d < -126 ? 0.f : __uint_as_float((uint32_t)(127 + d) << 23); }
 
 template <int D>
-__global__ void __launch_bounds__(kRowWarps * 32, 1)
+__global__ void __launch_bounds__(kRowWarps8 * 32, 1)
     rows8_kernel(const __grid_constant__ Attn8Params p, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap) {
-  constexpr int STAGES = kStages8<D>, STAGE = kStageBytes8<D>, HALF = STAGE / 2;
+  constexpr int KU = Geometry<D, false, true>::kKeys, NK = KU / 16;  // keys of a block, key tiles
+  constexpr int kMostPages = KU / 16;                                // pages that a block touches
+  constexpr int STAGES = kStages8, STAGE = kRowBlockBytes8, HALF = STAGE / 2;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kRowWarps][STAGES];
-  __shared__ uint64_t live[kRowWarps][STAGES];                     // keys of a block that were loaded
-  __shared__ float scales[kRowWarps][STAGES][2][kMostPages];       // of its pages' keys and values
+  __shared__ __align__(8) uint64_t full[kRowWarps8][STAGES];
+  __shared__ uint64_t live[kRowWarps8][STAGES];                     // keys of a block that were loaded
+  __shared__ float scales[kRowWarps8][STAGES][2][kMostPages];       // of its pages' keys and values
   __shared__ Patience patience;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -69,7 +63,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   if (threadIdx.x == 0) {
     patience.gave_up = 0;
     patience.limit = 1;  // (a block's copies)
-    for (int i = 0; i < kRowWarps; ++i)
+    for (int i = 0; i < kRowWarps8; ++i)
       for (int j = 0; j < STAGES; ++j) mbar_init(&full[i][j], 1 + 32);
     fence_mbar_init();
     prefetch_tmap(&kmap);
@@ -235,7 +229,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
         const uint32_t ks = smem_addr(ring + st * STAGE), vs = ks + HALF;
         const uint64_t keys = live[warp][st];
         const int key0 = ck * KU;
-        const bool masked = keys != ~0ull || key0 + KU > ctx + 1;
+        constexpr uint64_t kAll = KU == 64 ? ~0ull : (1ull << (KU & 63)) - 1;
+        const bool masked = keys != kAll || key0 + KU > ctx + 1;
         float ksc[NK], vsc[NK];  // scales, by tiles of 16 keys
 #pragma unroll
         for (int t = 0; t < NK; ++t) {
@@ -453,11 +448,10 @@ float kf[NK][2];  // what a score is worth in the exponent of two (a masked one 
 template <int D>
 cudaError_t launch_rows8_d(const Attn8Params& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                            cudaStream_t stream) {
-  constexpr int smem = smem_bytes_rows8<D>();
   static std::atomic<uint64_t> allowed{0};
-  const cudaError_t e = allow_smem(rows8_kernel<D>, smem, &allowed);
+  const cudaError_t e = allow_smem(rows8_kernel<D>, kSmemBytes8, &allowed);
   if (e != cudaSuccess) return e;
-  return launch_early(rows8_kernel<D>, dim3((unsigned)(p.workers / kRowWarps)), dim3(kRowWarps * 32), smem, stream, p,
+  return launch_early(rows8_kernel<D>, dim3((unsigned)(p.workers / kRowWarps8)), dim3(kRowWarps8 * 32), kSmemBytes8, stream, p,
                       kmap, vmap);
 }
 

@@ -92,11 +92,12 @@ def qk_norm_rope(qkv, Hq: int, Hkv: int, D: int, positions, slots, kpool, vpool,
     return L.calls().qk_norm_rope(*args) if stream is None else on_stream(L.calls().qk_norm_rope, stream, args)
 
 
-def attention_workspace(max_new: int, Hq: int, Hkv: int, D: int, device="cuda") -> torch.Tensor:
-    """A workspace for ``attention`` with these sizes.  Calls that share one
-    must not overlap: run them on one stream."""
+def attention_workspace(max_new: int, Hq: int, Hkv: int, D: int, device="cuda", dtype=torch.bfloat16) -> torch.Tensor:
+    """A workspace for ``attention`` with these sizes over pools of ``dtype``.
+    Calls that share one must not overlap: run them on one stream."""
+    size = L.mk_paged_attention_workspace if dtype == torch.bfloat16 else L.mk_paged_attention_e4m3_workspace
     with torch.cuda.device(device):
-        return torch.empty(L.mk_paged_attention_workspace(max_new, Hq, Hkv, D), dtype=torch.uint8, device=device)
+        return torch.empty(size(max_new, Hq, Hkv, D), dtype=torch.uint8, device=device)
 
 
 def attention(q, kpool, vpool, table, cu, ctx_len, max_new: int, *, kscale=None, vscale=None, scale: float = None,

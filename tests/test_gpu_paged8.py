@@ -582,7 +582,7 @@ def test_captured_calls_replay_on_new_inputs_and_repeat_themselves():
     ctx, new, Hq, Hkv, D, page = [900, 33, 4000], [1, 2, 70], 8, 2, 128, 16
     for most, lens in ((2, [1, 2, 1]), (70, new)):
         q, k, v, ks, vs, table, cu = attention_case(ctx, lens, Hq, Hkv, D, page, 21)
-        ws = paged.attention_workspace(most, Hq, Hkv, D)
+        ws = paged.attention_workspace(most, Hq, Hkv, D, dtype=E4M3)
         cu_t, ctx_t, out = i32(cu), i32(ctx), torch.zeros_like(q)
         call = lambda: paged.attention(q, k, v, table, cu_t, ctx_t, most, kscale=ks, vscale=vs, out=out, workspace=ws)  # noqa: E731,B023
         call()
