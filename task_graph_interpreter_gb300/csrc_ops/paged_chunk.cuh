@@ -17,6 +17,7 @@ struct Segment {
   int end[2];     // end of each tile's key blocks, >= k0
   int slot;       // partial record, or -1: the part is the whole item
   int valid;      // 0: no more parts
+  int split;      // the item has one tile, and the two take its key blocks in turn (over e4m3 pages)
 };
 
 // The first key that the item's first row does not see, and the first that no row of it does.

@@ -64,12 +64,14 @@ struct Block {  // what is known of a block of keys
 struct Control {
   uint64_t k_full[4], k_empty[4], raw_full[4], raw_empty[4], v_full[4], v_empty[4], q_full[2], q_ready[2], q_empty[2],
       s_full[2], p_full[2][2], o_done[2], s_free[2], turn[2], seg_full[kSegRing], seg_empty[kSegRing], drained[2],
-      known[8], half_done[2];
+      known[8], half_done[2], second_done, second_read;
   Segment segs[kSegRing];
   int odd[kSegRing];      // a value set aside in this part
   Block blocks[8];        // ring
   uint32_t tmem;
   Patience patience;
+  float2 ml[128];            // maximum and sum of a row's second half of key blocks (a split part),
+  int second_ve;             // and the unit of its results
   uint8_t q_exp[2][2][128];  // exponents of the query rows' largest elements, by part's parity and tile
 };
 static_assert(sizeof(Control) <= Smem<128>::kControl, "control block");
@@ -288,6 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl.half_done[i], 1);
     }
     for (int i = 0; i < 8; ++i) mbar_init(&ctl.known[i], 1);
+    mbar_init(&ctl.second_done, 4);
+    mbar_init(&ctl.second_read, 4);
     for (int i = 0; i < kSegRing; ++i) {
       mbar_init(&ctl.seg_full[i], 1);
       mbar_init(&ctl.seg_empty[i], kThreads / 32 - 1);  // every warp but the one that makes them
@@ -322,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Segment& s = segs[sst];
       if (!s.valid) break;
       const int k0 = s.k0, k1 = s.k1, from = masked_from(s), to = masked_to(s, p);
-      const bool second = s.t0 + p.tq < s.n;
+      const bool second = s.split || s.t0 + p.tq < s.n;
 #pragma unroll 1
       for (int w = 0; w < 2; ++w) {
         if (!(ok = wait_phase(&ctl.q_full[w], i & 1, &patience))) break;
@@ -429,12 +433,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             s.row0 = c.s.row0 + t0;
             s.k0 = k0;
             s.k1 = k1;
+            s.split = c.s.n - t0 <= p.tq && k1 - k0 > 1;
             s.slot = k0 == 0 && k1 == nk ? -1 : 2 * (int)blockIdx.x + (k0 == 0 ? 1 : 0);
             if (k0 != 0 && k1 == nk)
               *note_of(p, D, blockIdx.x) = Note{c.first_worker(line), s.row0, c.g, min(2 * p.tq, c.s.n - t0)};
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-              const int first = t0 + w * p.tq, last = min(first + p.tq, c.s.n) - 1;
+              const int first = t0 + (s.split ? 0 : w * p.tq), last = min(first + p.tq, c.s.n) - 1;
               s.end[w] = first < c.s.n ? max(k0, min(k1, (c.s.ctx + last) / 128 + 1)) : k0;
             }
           }
@@ -453,11 +458,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int w = 0; w < 2; ++w) {
           if (!wait_phase(&ctl.q_empty[w], (nq & 1) ^ 1, &patience)) return false;
           if (lane == 0) {
-            // (a second tile without tokens is not read)
-            const bool some = w == 0 || s.t0 + p.tq < s.n;
+            // (a second tile without tokens is not read; one that shares the first's has them too)
+            const bool some = w == 0 || s.split || s.t0 + p.tq < s.n;
             mbar_arrive_expect_tx(&ctl.q_full[w], some ? NH * p.tq * p.G * 128 : 0);
             for (int h = 0; h < NH && some; ++h)
-              tma_load_3d(qt + w * S::kQuery + h * S::kHalf, &qmap, h * 64, s.g * p.G, s.row0 + w * p.tq,
+              tma_load_3d(qt + w * S::kQuery + h * S::kHalf, &qmap, h * 64, s.g * p.G, s.row0 + (s.split ? 0 : w * p.tq),
                           &ctl.q_full[w]);
           }
           __syncwarp();
@@ -569,7 +574,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait(&ctl.seg_full[sst], (i / kSegRing) & 1))) break;
         const int valid = __shfl_sync(0xffffffffu, segs[sst].valid, 0), k0 = segs[sst].k0;
         const int nt = __shfl_sync(0xffffffffu, segs[sst].k1 - k0, 0);
-        const int ntw = __shfl_sync(0xffffffffu, segs[sst].end[w] - k0, 0);
+        const int split = __shfl_sync(0xffffffffu, segs[sst].split, 0);
+        // this tile's blocks: the first ones, or every other one from the w-th on (a split part)
+        const int ntw = split ? (nt + 1 - w) / 2 : __shfl_sync(0xffffffffu, segs[sst].end[w] - k0, 0);
+        const int steps = split ? (nt + 1) / 2 : nt, stride = split ? 2 : 1, first = split ? w : 0;
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.seg_empty[sst]);
         if (!valid) break;
@@ -620,12 +628,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         };
-        for (int j = -1; j < nt; ++j) {
-          const uint32_t kb = blk + j + 1, vb = blk + j, kst = kb % KS, vst = vb % VS;
-          const bool pv = j >= 0 && j < ntw, qk = j + 1 < ntw;
+        // the other tile's block of a split part, handed back as it comes
+        const auto pass_on = [&](uint64_t* full, uint64_t* empty, uint32_t stages, int j) {
+          if (!split || j >= nt) return true;
+          const uint32_t n = blk + j, st = n % stages;
+          if (!wait(&full[st], (n / stages) & 1)) return false;
+          if (lane == 0) mbar_arrive(&empty[st]);
+          __syncwarp();
+          return true;
+        };
+        for (int j = -1; j < steps; ++j) {
+          // j-th block's values, next block's keys
+          const int jv = j * stride + first, jk = jv + stride;
+          const uint32_t kb = blk + jk, vb = blk + jv, kst = kb % KS, vst = vb % VS;
+          const bool there_v = j >= 0 && jv < nt, there_k = jk < nt, pv = there_v && j < ntw, qk = there_k && j + 1 < ntw;
           if constexpr (kApart) {
             // S (block j + 1) as soon as the softmax has S (block j) in registers, P V (block j) as P comes
-            if (j + 1 < nt) {
+            if (there_k) {
               if (!(ok = wait(&ctl.k_full[kst], (kb / KS) & 1))) break;
               if (qk) {
                 if (!(ok = wait(&ctl.s_free[w], (nturn & 1) ^ 1))) break;
@@ -636,7 +655,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&ctl.k_empty[kst]);
               }
             }
-            if (j >= 0) {
+            if (!(ok = pass_on(ctl.k_full, ctl.k_empty, KS, 2 * j + 2 + (w ^ 1)))) break;
+            if (there_v) {
               if (!(ok = wait(&ctl.v_full[vst], (vb / VS) & 1))) break;
               if (pv) {
                 if (!(ok = wait(&ctl.p_full[w][0], np & 1))) break;
@@ -649,8 +669,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           } else {
             // P V (block j) before S (block j + 1).  A block that this tile does not need is handed back as it comes
-            if (j >= 0 && !(ok = wait(&ctl.v_full[vst], (vb / VS) & 1))) break;
-            if (j + 1 < nt && !(ok = wait(&ctl.k_full[kst], (kb / KS) & 1))) break;
+            if (there_v && !(ok = wait(&ctl.v_full[vst], (vb / VS) & 1))) break;
+            if (there_k && !(ok = wait(&ctl.k_full[kst], (kb / KS) & 1))) break;
             // tile 0 starts; then each block's products of one tile, then of the other
             if (!(ok = wait(&ctl.turn[w], (nturn & 1) ^ (w ^ 1)))) break;
             ++nturn;
@@ -658,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             if (pv) {
               if (!(ok = values(j, vst))) break;
-            } else if (j >= 0 && lane == 0) {
+            } else if (there_v && lane == 0) {
               mbar_arrive(&ctl.v_empty[vst]);
             }
             if (qk) {
@@ -666,11 +686,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               if (lane == 0) {
                 mbar_arrive(&ctl.turn[w ^ 1]);
-                if (j + 1 < nt) mbar_arrive(&ctl.k_empty[kst]);
+                if (there_k) mbar_arrive(&ctl.k_empty[kst]);
               }
               __syncwarp();
             }
+            if (!(ok = pass_on(ctl.k_full, ctl.k_empty, KS, 2 * j + 2 + (w ^ 1)))) break;
           }
+          if (j >= 0 && !(ok = pass_on(ctl.v_full, ctl.v_empty, VS, 2 * j + (w ^ 1)))) break;
         }
         blk += nt;
       }
@@ -691,17 +713,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                    tp = tmem + lanes + kPCol + w * kPStep;
     const int tok_in = row / p.G, head = row % p.G;
     const int per16 = p.page_shift - 4;  // a page has 2^per16 sixteens of keys
-    uint32_t ns = 0, no = 0, np = 0, blk = 0;  // scores, results seen; P handed over; blocks
+    uint32_t ns = 0, no = 0, np = 0, blk = 0, nsplit = 0;  // scores, results seen; P handed over; blocks; split parts
     for (uint32_t i = 0;; ++i) {
       const int sst = i % kSegRing;
       if (!wait_phase(&ctl.seg_full[sst], (i / kSegRing) & 1, &patience)) break;
       const Segment& s = segs[sst];
       if (!s.valid) break;
-      const int k0 = s.k0, nt = s.end[w] - k0;
-      const int tok = s.t0 + w * p.tq + tok_in;  // in the request
+      const int k0 = s.k0, nb = s.end[w] - k0;
+      // this tile's blocks: the first nb, or every other one from the w-th on (a split part, whose tokens are the first
+      // tile's)
+      const bool split = s.split != 0;
+      const int nt = split ? (nb + 1 - w) / 2 : nb, stride = split ? 2 : 1, first = split ? w : 0;
+      const int t1 = s.t0 + (split ? 0 : w * p.tq), tok = t1 + tok_in;  // in the request
       const bool mine = tok_in < p.tq && tok < s.n;
-      const int lim = min(s.ctx + tok, s.ctx + s.n - 1);       // the last key this row sees
-      const int jm = ((s.ctx + s.t0 + w * p.tq + 1) >> 7) - k0;  // the first block that the tile does not wholly see
+      const int lim = min(s.ctx + tok, s.ctx + s.n - 1);  // the last key this row sees
+      const int jm = ((s.ctx + t1 + 1) >> 7) - k0;          // the first block that the tile does not wholly see
       float m = -INFINITY, l = 0.f, rowf = 0.f;
       int ve = 127;
       bool ok = true;
@@ -718,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 8; ++e) kf[e] = b.ks[e >> per16];
         return true;
       };
-      if (nt > 0) ok = look(blk);
+      if (nt > 0) ok = look(blk + first);
       const int fold_slot = s.slot >= 0 ? s.slot : 2 * (int)blockIdx.x + 1;
 #pragma unroll 1
       for (int j = 0, stop = kFold; ok; stop += kFold) {
@@ -726,10 +752,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = wait_phase(&ctl.s_full[w], ns & 1, &patience))) break;
           ++ns;
           tc_fence_after();
-          if (j >= jm || miss) {
+          const int jb = j * stride + first;  // the block
+          if (jb >= jm || miss) {
             // scores of keys that the row does not see become -inf where they lie, 32 columns at a time (a loop,
             // for the sake of the code's size)
-            const int last = lim - (k0 + j) * 128;
+            const int last = lim - (k0 + jb) * 128;
 #pragma unroll 1
             for (int c = 0; c < 128; c += 32) {
               const int n = last + 1 - c;
@@ -825,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++np;
           const float2 t = unpair_f32(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
           l += t.x + t.y;
-          if (j + 1 < nt && !(ok = look(blk + j + 1))) break;
+          if (j + 1 < nt && !(ok = look(blk + jb + stride))) break;
         }
         if (!ok || j >= nt) break;
         // O is whole once the next scores are there (at D = 64, once its last product is done)
@@ -844,25 +871,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         l = fold_results(p, D, fold_slot, w * 128 + row, to, m, l, unit_of(ve), mine, true, true);
         ve = 127;
       }
+      // the two tiles of a split part: the second's maxima and sums go by shared memory, its results are read where they
+      // are
+      float fa = unit_of(ve), fb = 0.f;
+      if (split && w == 1) {
+        ctl.ml[row] = make_float2(m, l);
+        if (row == 0) ctl.second_ve = ve;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.second_done);
+      } else if (split) {
+        if (!wait_phase(&ctl.second_done, nsplit & 1, &patience)) break;
+        tc_fence_after();
+        const float2 other = ctl.ml[row];
+        const float mn = fmaxf(m, other.x), mu = mn == -INFINITY ? 0.f : mn;
+        const float f0 = ex2(m - mu), f1 = ex2(other.x - mu);
+        m = mn;
+        l = l * f0 + other.y * f1;
+        fa *= f0;
+        fb = unit_of(ctl.second_ve) * f1;
+      }
+      const bool stores = mine && !(split && w == 1);
       const bool set_aside = nt > 0 && ctl.odd[sst];
-      const float f = unit_of(ve) * (s.slot >= 0 ? 1.f : nt == 0 || l == 0.f ? 0.f : 1.0f / l);
+      const float f = s.slot >= 0 ? 1.f : nt == 0 || l == 0.f ? 0.f : 1.0f / l;
       const bool none = nt == 0 || (s.slot < 0 && l == 0.f);  // a row without keys is zero
-      __nv_bfloat16* dst = p.out + ((int64_t)s.row0 + w * p.tq + tok_in) * p.ld_out + (int64_t)(s.g * p.G + head) * D;
+      __nv_bfloat16* dst = p.out + ((int64_t)s.row0 + (split ? 0 : w * p.tq) + tok_in) * p.ld_out + (int64_t)(s.g * p.G + head) * D;
       float4* rec = nullptr;
       if (s.slot >= 0) {
         rec = part_cols(p, D, s.slot, w * 128 + row, 0);
-        if (mine) *reinterpret_cast<float2*>(part_ml(p, D, s.slot, w * 128 + row)) = make_float2(m, nt > 0 ? l : 0.f);
+        if (stores) *reinterpret_cast<float2*>(part_ml(p, D, s.slot, w * 128 + row)) = make_float2(m, nt > 0 ? l : 0.f);
       }
       // (32-byte stores where a row allows it: lanes hold different rows, and each store takes a cycle per lane)
       const bool wide = (p.ld_out & 15) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = 0; c < (split && w == 1 ? 0 : D); c += 32) {
         float o[32];
         if (nt > 0) {
           tmem_ld32(to + c, o);
           tmem_wait_ld();
         }
-        if (set_aside && mine) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] *= fa;
+        if (split) {
+          float o1[32];
+          tmem_ld32(to + D + c, o1);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], fb, o[e]);
+        }
+        if (set_aside && stores) {
           float add[32] = {};
           add_odd_values(p, s, lim, D, c, add);
 #pragma unroll
@@ -870,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * f;
-        if (mine && !rec) {
+        if (stores && !rec) {
 #pragma unroll
           for (int e = 0; e < 32; e += 16) {
             uint32_t v[8];
@@ -883,11 +940,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint4*>(dst + c + e + 8) = make_uint4(v[4], v[5], v[6], v[7]);
             }
           }
-        } else if (mine && nt > 0) {
+        } else if (stores && nt > 0) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             rec[(c + e) / 4 * kTileRows] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
+      }
+      if (split) {  // the second tile's results are read before it goes on
+        if (w == 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.second_read);
+        } else if (!wait_phase(&ctl.second_read, nsplit & 1, &patience)) {
+          break;
+        }
+        ++nsplit;
       }
       tc_fence_before();  // O is read before the next part's first P is handed over
       __syncwarp();

@@ -718,3 +718,17 @@ def test_calls_on_another_stream_and_two_workspaces():
     torch.cuda.synchronize()
     for (c, ctx, m), g in zip(cases, got):
         close(g, *attention_ref(c[0], c[1], c[2], c[3], c[4], c[5], c[6], ctx, 16, 128 ** -0.5))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [9, 31, 32, 33])
+def test_items_of_one_tile_whose_key_blocks_two_take_in_turn(n, D):
+    """One to many blocks of keys, odd and even in number, whole items and cut ones, beside items of two tiles."""
+    for ctx in ([0], [100], [128 - n], [129 - n], [256 - n], [257 - n], [300, 0, 600, 1000, 127], [5000, 20], [12345]):
+        q, k, v, ks, vs, table, cu = attention_case(ctx, [n] * len(ctx), 8, 2, D, 16, n + ctx[0])
+        got = paged.attention(q, k, v, table, i32(cu), i32(ctx), n, kscale=ks, vscale=vs)
+        close(got, *attention_ref(q, k, v, ks, vs, table, cu, ctx, 16, D ** -0.5))
+    ctx, new = [700, 90, 3000, 0], [n, 80, 5, 200]
+    q, k, v, ks, vs, table, cu = attention_case(ctx, new, 8, 2, D, 32, n)
+    got = paged.attention(q, k, v, table, i32(cu), i32(ctx), 200, kscale=ks, vscale=vs)
+    close(got, *attention_ref(q, k, v, ks, vs, table, cu, ctx, 32, D ** -0.5))
