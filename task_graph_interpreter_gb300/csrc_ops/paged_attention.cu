@@ -40,11 +40,11 @@ bool encode(EncodeTiledFn enc, CUtensorMap* m, const void* ptr, int rank, const 
 // Few query rows or chunks: a request and head of at most eight rows fills one
 // warp product; beyond that the 128-row tensor-core tiles are faster although
 // mostly empty (paged_rows.cu has both sides).
-bool few_rows(int max_new, int G) { return (int64_t)max_new * G <= kMaxFewRows; }
+bool few_rows(int max_new, int G, bool e4m3) { return (int64_t)max_new * G <= (e4m3 ? kMaxFewRows8 : kMaxFewRows); }
 
 // Two partial records and a note per worker (paged_attention.cuh).
 size_t workspace_bytes(int max_new, int G, int D, int sms, bool e4m3) {
-  const bool few = few_rows(max_new, G);
+  const bool few = few_rows(max_new, G, e4m3);
   const size_t workers = (size_t)sms * (!few ? 1 : e4m3 ? kRowWarps8 : kRowWarps), rows = few ? max_new * G : kTileRows;
   return 2 * workers * rows * (D + 2) * 4 + workers * 16;
 }
@@ -118,7 +118,7 @@ static int attention(const char* who, bool e4m3, void* stream_, int B, int N, in
   EncodeTiledFn enc = encoder();
   if (!enc) return fail(MK_ERR_CUDA, name + ": cuTensorMapEncodeTiled is not available");
 
-  const bool few = few_rows(max_new, G);
+  const bool few = few_rows(max_new, G, e4m3);
   Attn8Params p{};
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.v = static_cast<const __nv_bfloat16*>(vpool);

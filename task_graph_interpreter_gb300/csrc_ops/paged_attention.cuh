@@ -300,5 +300,6 @@ cudaError_t launch_chunk8(const Attn8Params& p, const CUtensorMap& qmap, const C
                           const CUtensorMap& vmap, int D, cudaStream_t stream);
 constexpr int kRowWarps = 4;    // warps (workers) per CTA of the few-rows kernel
 constexpr int kMaxFewRows = 8;  // query rows of a request and head that it takes
+constexpr int kMaxFewRows8 = 16;  // and over e4m3 pages
 
 }  // namespace mk

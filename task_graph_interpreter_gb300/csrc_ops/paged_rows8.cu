@@ -27,7 +27,6 @@ namespace {
 
 using namespace ptx;
 
-static_assert(kMaxFewRows == 8, "the query rows are the eight columns of a product");
 constexpr float kBias = 14.f;                // probabilities are kept times 2^kBias
 constexpr int kStages8 = 3;
 constexpr int kSmemBytes8 = 1024 + kRowWarps8 * kStages8 * kRowBlockBytes8;
@@ -45,7 +44,8 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return __vcmpeq4(w &
 // 2^(d) for d <= 0 (zero where it is not a normal number)
 __device__ __forceinline__ float exp2_down(int d) { return d < -126 ? 0.f : __uint_as_float((uint32_t)(127 + d) << 23); }
 
-template <int D>
+// NR: eights of query rows
+template <int D, int NR>
 __global__ void __launch_bounds__(kRowWarps8 * 32, 1)
     rows8_kernel(const __grid_constant__ Attn8Params p, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap) {
@@ -161,59 +161,77 @@ __global__ void __launch_bounds__(kRowWarps8 * 32, 1)
 
   // this lane's place in the products: row g of their eight or sixteen, elements (columns) c0, c0 + 1
   const int g = lane >> 2, c0 = (lane & 3) * 2;
-  // row g of an item's query rows (row r = token * G + head; rows past the last are zero), four elements of every 16,
-  // read while the item before is worked on
+  // row 8 h + g of an item's query rows (row r = token * G + head; rows past the last are zero), four elements of every
+  // 16; with one eight of rows read while the item before is worked on
   uint2 qv[D / 16];
-  auto load_q = [&](const Place& c) {
-    const bool in = g < c.s.n * p.G;
-    const __nv_bfloat16* qr = p.q + (int64_t)(c.s.row0 + (in ? g / p.G : 0)) * p.ld_q +
-                              ((int64_t)c.g * p.G + (in ? g % p.G : 0)) * D + 2 * c0;
+  auto load_q = [&](const Place& c, int h) {
+    const int r = 8 * h + g;
+    const bool in = r < c.s.n * p.G;
+    const __nv_bfloat16* qr = p.q + (int64_t)(c.s.row0 + (in ? r / p.G : 0)) * p.ld_q +
+                              ((int64_t)c.g * p.G + (in ? r % p.G : 0)) * D + 2 * c0;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
       qv[j] = in ? __ldg(reinterpret_cast<const uint2*>(qr + j * 16)) : make_uint2(0, 0);
   };
-  load_q(cons);
+  if (NR == 1) load_q(cons, 0);
   for (bool more = true; more;) {
     const int n = cons.s.n, ctx = cons.s.ctx, L = ctx + n, nrows = n * p.G;
     const int nk = cons.blocks(p), kb = ck;
-    // the row's largest element, as bf16 bits, to [2^14, 2^15)
-    uint32_t big = 0;
+    float rs[NR][2];
+    uint32_t qf[NR][D / 16][2];
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j) big = __vmaxu2(big, __vmaxu2(qv[j].x & 0x7FFF7FFFu, qv[j].y & 0x7FFF7FFFu));
-    big = max(big & 0xFFFFu, big >> 16);
-    big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-    big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-    const int qe = min(max((int)(big >> 7), 15), 254);
-    const float up = __uint_as_float((uint32_t)(141 + 127 - qe) << 23);           // 2^(14 - e)
-    const float down = p.scale * __uint_as_float((uint32_t)(qe - 14) << 23);      // softmax scale 2^(e - 14)
-    float rs[2];
+    for (int h = 0; h < NR; ++h) {
+      if (NR > 1) load_q(cons, h);
+      // the row's largest element, as bf16 bits, to [2^14, 2^15)
+      uint32_t big = 0;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) rs[e] = __shfl_sync(0xffffffffu, down, (c0 + e) * 4);
-    uint32_t qf[D / 16][2];
+      for (int j = 0; j < D / 16; ++j) big = __vmaxu2(big, __vmaxu2(qv[j].x & 0x7FFF7FFFu, qv[j].y & 0x7FFF7FFFu));
+      big = max(big & 0xFFFFu, big >> 16);
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      const int qe = min(max((int)(big >> 7), 15), 254);
+      const float up = __uint_as_float((uint32_t)(141 + 127 - qe) << 23);       // 2^(14 - e)
+      const float down = p.scale * __uint_as_float((uint32_t)(qe - 14) << 23);  // softmax scale 2^(e - 14)
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-      qf[j][0] = pack_f16(bf_lo(qv[j].x) * up, bf_hi(qv[j].x) * up);
-      qf[j][1] = pack_f16(bf_lo(qv[j].y) * up, bf_hi(qv[j].y) * up);
+      for (int e = 0; e < 2; ++e) rs[h][e] = __shfl_sync(0xffffffffu, down, (c0 + e) * 4);
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        qf[h][j][0] = pack_f16(bf_lo(qv[j].x) * up, bf_hi(qv[j].x) * up);
+        qf[h][j][1] = pack_f16(bf_lo(qv[j].y) * up, bf_hi(qv[j].y) * up);
+      }
     }
     Place coming = cons;
     int nk0 = 0, nk1 = 0;
     more = next_part(coming, nk0, nk1);
-    if (more) load_q(coming);
-    // the last key each of this lane's two rows sees
-    int lim[2];
+    if (NR == 1 && more) load_q(coming, 0);
+    // the last key each of this lane's two rows of an eight sees
+    const auto last_key = [&](int h, int e) {
+      const int r = 8 * h + c0 + e;
+      return r < nrows ? ctx + r / p.G : L - 1;
+    };
+    int lim[NR][2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) lim[e] = c0 + e < nrows ? ctx + (c0 + e) / p.G : L - 1;
+    for (int h = 0; h < NR; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) lim[h][e] = last_key(h, e);
     const int slot = 2 * w + (kb == 0 ? 1 : 0);  // of the part's record (free while a whole item is worked on)
     // results, in units of 2^(ve - 127): the power of two of the largest scale of values so far
-    float o[D / 16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[NR][D / 16][4], m[NR][2], l[NR][2];
     int ve = 1;
-#pragma unroll
-    for (int t = 0; t < D / 16; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
-
     constexpr int kFold = kFoldKeys / KU;
-    float mfold[2] = {-INFINITY, -INFINITY}, lfold[2] = {0.f, 0.f};  // the maxima of folded results, and their sums
+    float mfold[NR][2], lfold[NR][2];  // the maxima of folded results, and their sums
+#pragma unroll
+    for (int h = 0; h < NR; ++h) {
+#pragma unroll
+      for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[h][t][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[h][e] = mfold[h][e] = -INFINITY;
+        l[h][e] = lfold[h][e] = 0.f;
+      }
+    }
 #pragma unroll 1
     for (int stop = kb + kFold;; stop += kFold) {
       for (; ck < min(cke, stop); ++ck) {
@@ -239,11 +257,13 @@ __global__ void __launch_bounds__(kRowWarps8 * 32, 1)
           vsc[t] = scales[warp][st][1][pg];
         }
 
-        float s[NK][4];
+        float s[NR][NK][4];
 #pragma unroll
-        for (int t = 0; t < NK; ++t)
+        for (int h = 0; h < NR; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+          for (int t = 0; t < NK; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[h][t][e] = 0.f;
 #pragma unroll
         for (int j = 0; j < D / 16; j += 2) {
 #pragma unroll
@@ -252,78 +272,93 @@ __global__ void __launch_bounds__(kRowWarps8 * 32, 1)
             uint32_t k[4];
             ldsm4(swz8<D>(ks, t * 16 + (lane & 15), j + (lane >> 4)), k);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int i = 0; i < 2; ++i) {
               uint32_t a[4];
-              widen_e4m3(k[2 * h], a[0], a[2]);
-              widen_e4m3(k[2 * h + 1], a[1], a[3]);
-              mma_f16(s[t], a, qf[j + h][0], qf[j + h][1]);
+              widen_e4m3(k[2 * i], a[0], a[2]);
+              widen_e4m3(k[2 * i + 1], a[1], a[3]);
+#pragma unroll
+              for (int h = 0; h < NR; ++h) mma_f16(s[h][t], a, qf[h][j + i][0], qf[h][j + i][1]);
             }
           }
         }
-float kf[NK][2];  // what a score is worth in the exponent of two (a masked one times zero would be NaN)
-#pragma unroll
-        for (int t = 0; t < NK; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) kf[t][e] = fmaxf(ksc[t] * rs[e], 0x1p-126f);
         if (masked) {
 #pragma unroll
-          for (int t = 0; t < NK; ++t)
+          for (int h = 0; h < NR; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int k = t * 16 + g + (e >> 1) * 8;
-              if (!((keys >> k) & 1) || key0 + k > lim[e & 1]) s[t][e] = -INFINITY;
-            }
+            for (int t = 0; t < NK; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int k = t * 16 + g + (e >> 1) * 8;
+                if (!((keys >> k) & 1) || key0 + k > lim[h][e & 1]) s[h][t][e] = -INFINITY;
+              }
         }
         int vmax = ve;
 #pragma unroll
         for (int t = 0; t < NK; ++t) vmax = max(vmax, (int)(__float_as_uint(vsc[t]) >> 23 & 0xFF));
         vmax = min(vmax, 253);
         bool moved = vmax != ve;
-        float mnew[2], muse[2];
+        float mnew[NR][2];
+        // what a score is worth in the exponent of two (a masked one times zero would be NaN)
+        const auto worth = [&](int h, int t, int e) { return fmaxf(ksc[t] * rs[h][e], 0x1p-126f); };
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = fmaxf(s[0][e], s[0][e + 2]) * kf[0][e];
+        for (int h = 0; h < NR; ++h)
 #pragma unroll
-          for (int t = 1; t < NK; ++t) x = fmaxf(x, fmaxf(s[t][e], s[t][e + 2]) * kf[t][e]);
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          mnew[e] = fmaxf(m[e], x);
-          muse[e] = mnew[e] == -INFINITY ? 0.f : mnew[e];  // a row without any key so far
-          moved |= mnew[e] != m[e];
-        }
+          for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(s[h][0][e], s[h][0][e + 2]) * worth(h, 0, e);
+#pragma unroll
+            for (int t = 1; t < NK; ++t) x = fmaxf(x, fmaxf(s[h][t][e], s[h][t][e + 2]) * worth(h, t, e));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            mnew[h][e] = fmaxf(m[h][e], x);
+            moved |= mnew[h][e] != m[h][e];
+          }
+        const auto from = [&](float mx) { return mx == -INFINITY ? 0.f : mx; };  // a row without any key so far
         if (__any_sync(0xffffffffu, moved)) {
           const float fv = exp2_down(ve - vmax);
           ve = vmax;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float f = ex2(m[e] - muse[e]);
-            m[e] = mnew[e];
-            l[e] *= f;
+          for (int h = 0; h < NR; ++h)
 #pragma unroll
-            for (int t = 0; t < D / 16; ++t) {
-              o[t][e] *= f * fv;
-              o[t][e + 2] *= f * fv;
+            for (int e = 0; e < 2; ++e) {
+              const float f = ex2(m[h][e] - from(mnew[h][e]));
+              m[h][e] = mnew[h][e];
+              l[h][e] *= f;
+#pragma unroll
+              for (int t = 0; t < D / 16; ++t) {
+                o[h][t][e] *= f * fv;
+                o[h][t][e + 2] *= f * fv;
+              }
             }
-          }
         }
         const float vref = __uint_as_float((uint32_t)(254 - ve) << 23);  // 2^(127 - ve)
 #pragma unroll
-        for (int t = 0; t < NK; ++t)
+        for (int h = 0; h < NR; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = ex2(fmaf(s[t][e], kf[t][e & 1], kBias - muse[e & 1]));
-            s[t][e] = x;
-            l[e & 1] += x;
+          for (int e = 0; e < 2; ++e) {
+            const float mu = kBias - from(m[h][e]);
+#pragma unroll
+            for (int t = 0; t < NK; ++t) {
+              const float f = worth(h, t, e);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float x = ex2(fmaf(s[h][t][e + 2 * i], f, mu));
+                s[h][t][e + 2 * i] = x;
+                l[h][e] += x;
+              }
+            }
           }
         bool bad_v = false;  // a value that is not finite behind a mask
 #pragma unroll
         for (int t = 0; t < NK; ++t) {
           // probabilities as operands: 16 keys by 8 rows, transposed
           const float vf = vsc[t] * vref;
-          uint32_t pr[2];
+          uint32_t pr[NR][2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) pr[e] = movm_trans(pack_f16(s[t][2 * e] * vf, s[t][2 * e + 1] * vf));
+          for (int h = 0; h < NR; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              pr[h][e] = movm_trans(pack_f16(s[h][t][2 * e] * vf, s[h][t][2 * e + 1] * vf));
           // this lane's four keys of the 16: c0, c0 + 1, c0 + 8, c0 + 9
           uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
           if (masked) {
@@ -350,11 +385,12 @@ float kf[NK][2];  // what a score is worth in the exponent of two (a masked one 
               }
             }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int i = 0; i < 2; ++i) {
               uint32_t a[4];
-              widen_e4m3(__byte_perm(v[2 * h], 0, 0x3120), a[0], a[1]);
-              widen_e4m3(__byte_perm(v[2 * h + 1], 0, 0x3120), a[2], a[3]);
-              mma_f16(o[d + h], a, pr[0], pr[1]);
+              widen_e4m3(__byte_perm(v[2 * i], 0, 0x3120), a[0], a[1]);
+              widen_e4m3(__byte_perm(v[2 * i + 1], 0, 0x3120), a[2], a[3]);
+#pragma unroll
+              for (int h = 0; h < NR; ++h) mma_f16(o[h][d + i], a, pr[h][0], pr[h][1]);
             }
           }
         }
@@ -371,8 +407,10 @@ float kf[NK][2];  // what a score is worth in the exponent of two (a masked one 
               for (int q = 0; q < 2; ++q) {
                 if ((two >> (8 * q) & 0x7Fu) != 0x7Fu) continue;
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  if (key0 + k <= lim[e]) o[d][2 * q + e] = __uint_as_float(0x7FC00000u);
+                for (int h = 0; h < NR; ++h)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    if (key0 + k <= lim[h][e]) o[h][d][2 * q + e] = __uint_as_float(0x7FC00000u);
               }
             }
           }
@@ -386,23 +424,25 @@ float kf[NK][2];  // what a score is worth in the exponent of two (a masked one 
       const bool some = stop > kb + kFold, last = ck >= cke;
       const float unit = __uint_as_float((uint32_t)ve << 23);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = c0 + e;
-        if (r >= nrows) continue;
-        const float f = fold_weight(mfold[e], m[e]);
-        mfold[e] = m[e];
-        lfold[e] = lfold[e] * f + l[e];
-        l[e] = last ? lfold[e] : 0.f;
+      for (int h = 0; h < NR; ++h)
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d) {
-          float2* at = reinterpret_cast<float2*>(part_o(p, D, slot, r) + d * 16 + 2 * g);
-          const float2 was = some ? *at : make_float2(0.f, 0.f);
-          const float2 x = make_float2(o[d][e] * unit + was.x * f, o[d][2 + e] * unit + was.y * f);
-          if (!last) *at = x;
-          o[d][e] = last ? x.x : 0.f;
-          o[d][2 + e] = last ? x.y : 0.f;
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * h + c0 + e;
+          if (r >= nrows) continue;
+          const float f = fold_weight(mfold[h][e], m[h][e]);
+          mfold[h][e] = m[h][e];
+          lfold[h][e] = lfold[h][e] * f + l[h][e];
+          l[h][e] = last ? lfold[h][e] : 0.f;
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) {
+            float2* at = reinterpret_cast<float2*>(part_o(p, D, slot, r) + d * 16 + 2 * g);
+            const float2 was = some ? *at : make_float2(0.f, 0.f);
+            const float2 x = make_float2(o[h][d][e] * unit + was.x * f, o[h][d][2 + e] * unit + was.y * f);
+            if (!last) *at = x;
+            o[h][d][e] = last ? x.x : 0.f;
+            o[h][d][2 + e] = last ? x.y : 0.f;
+          }
         }
-      }
       if (last) {
         ve = 127;
         break;
@@ -411,33 +451,37 @@ float kf[NK][2];  // what a score is worth in the exponent of two (a masked one 
     }
 
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
-    }
+    for (int h = 0; h < NR; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[h][e] += __shfl_xor_sync(0xffffffffu, l[h][e], 4);
+        l[h][e] += __shfl_xor_sync(0xffffffffu, l[h][e], 8);
+        l[h][e] += __shfl_xor_sync(0xffffffffu, l[h][e], 16);
+      }
     const bool whole = kb == 0 && cke == nk;
     if (kb != 0 && cke == nk) note = {cons.first_worker(line), cons.s.row0, cons.g, n};
     __nv_bfloat16* ob = p.out + (int64_t)cons.s.row0 * p.ld_out + (int64_t)cons.g * p.G * D;
     const float unit = __uint_as_float((uint32_t)ve << 23);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = c0 + e;
-      if (r >= nrows) continue;
-      if (whole) {
-        const float f = l[e] == 0.f ? 0.f : 1.0f / l[e];  // (a row without keys is zero)
-        __nv_bfloat16* dst = ob + (int64_t)(r / p.G) * p.ld_out + (r % p.G) * D + 2 * g;
+    for (int h = 0; h < NR; ++h)
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d)
-          *reinterpret_cast<uint32_t*>(dst + d * 16) = pack_bf16(o[d][e] * unit * f, o[d][2 + e] * unit * f);
-      } else {
-        float* dst = part_o(p, D, slot, r) + 2 * g;
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * h + c0 + e;
+        if (r >= nrows) continue;
+        if (whole) {
+          const float f = l[h][e] == 0.f ? 0.f : 1.0f / l[h][e];  // (a row without keys is zero)
+          __nv_bfloat16* dst = ob + (int64_t)(r / p.G) * p.ld_out + (r % p.G) * D + 2 * g;
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d)
-          *reinterpret_cast<float2*>(dst + d * 16) = make_float2(o[d][e] * unit, o[d][2 + e] * unit);
-        if (g == 0) *reinterpret_cast<float2*>(part_ml(p, D, slot, r)) = make_float2(m[e], l[e]);
+          for (int d = 0; d < D / 16; ++d)
+            *reinterpret_cast<uint32_t*>(dst + d * 16) = pack_bf16(o[h][d][e] * unit * f, o[h][d][2 + e] * unit * f);
+        } else {
+          float* dst = part_o(p, D, slot, r) + 2 * g;
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d)
+            *reinterpret_cast<float2*>(dst + d * 16) = make_float2(o[h][d][e] * unit, o[h][d][2 + e] * unit);
+          if (g == 0) *reinterpret_cast<float2*>(part_ml(p, D, slot, r)) = make_float2(m[h][e], l[h][e]);
+        }
       }
-    }
     cons = coming;
     ck = nk0;
     cke = nk1;
@@ -445,14 +489,21 @@ float kf[NK][2];  // what a score is worth in the exponent of two (a masked one 
   if (lane == 0 && note.tokens) *note_of(p, D, w) = note;
 }
 
+template <int D, int NR>
+cudaError_t launch_rows8_t(const Attn8Params& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                           cudaStream_t stream) {
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(rows8_kernel<D, NR>, kSmemBytes8, &allowed);
+  if (e != cudaSuccess) return e;
+  return launch_early(rows8_kernel<D, NR>, dim3((unsigned)(p.workers / kRowWarps8)), dim3(kRowWarps8 * 32), kSmemBytes8,
+                      stream, p, kmap, vmap);
+}
 template <int D>
 cudaError_t launch_rows8_d(const Attn8Params& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                            cudaStream_t stream) {
-  static std::atomic<uint64_t> allowed{0};
-  const cudaError_t e = allow_smem(rows8_kernel<D>, kSmemBytes8, &allowed);
-  if (e != cudaSuccess) return e;
-  return launch_early(rows8_kernel<D>, dim3((unsigned)(p.workers / kRowWarps8)), dim3(kRowWarps8 * 32), kSmemBytes8, stream, p,
-                      kmap, vmap);
+  static_assert(kMaxFewRows8 == 16, "two eights of rows at most");
+  if (p.rows <= 8) return launch_rows8_t<D, 1>(p, kmap, vmap, stream);
+  return launch_rows8_t<D, 2>(p, kmap, vmap, stream);
 }
 
 }  // namespace
