@@ -39,7 +39,7 @@ using namespace ptx;
 
 constexpr int kThreads = 512;
 // registers: the launch's 4 x 128 threads x 128, moved to the softmax warpgroups
-constexpr int kLaunchRegs = 128, kConsumerRegs = 160, kOtherRegs = 96, kWidenRegs = 96;
+constexpr int kLaunchRegs = 128, kConsumerRegs = 176, kOtherRegs = 80, kWidenRegs = 80;
 static_assert(2 * kConsumerRegs + kOtherRegs + kWidenRegs <= 4 * kLaunchRegs, "register shares within the launch's");
 constexpr float kBias = 6.f;  // probabilities are kept times 2^kBias; a row's maximum may lag by 2^8
 
@@ -154,9 +154,12 @@ __device__ __forceinline__ int split_query(uint32_t tile, int row) {
     split4(b.x, b.y, up, hi.z, low[c].z);
     split4(b.z, b.w, up, hi.w, low[c].w);
     sts128(piece(c), hi);
+    // (the second parts follow where pieces have been read)
+    if (c >= NC / 2) {
+      sts128(piece(2 * c), low[2 * c - NC]);
+      sts128(piece(2 * c + 1), low[2 * c - NC + 1]);
+    }
   }
-#pragma unroll
-  for (int c = 0; c < NC; ++c) sts128(piece(NC + c), low[c]);
   return e;
 }
 
@@ -365,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         bool odd = false;
         if (k * 128 + 128 <= from && b.missing == 0) {
-#pragma unroll
+#pragma unroll 4
           for (int c = 0; c < D / 16; ++c) put(c, codes(c));
         } else {
           // keys that were not loaded are zero; a NaN of a key that some row of the item does not see is set aside
@@ -602,6 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (c == 0) tc_commit(&ctl.half_done[w]);
               if (c == 1) {
                 tc_commit(&ctl.v_empty[vst]);
+                if (split) tc_commit(&ctl.v_empty[vst]);  // (for the other tile, which does not see the block)
                 if (kApart || j + 1 == ntw) tc_commit(&ctl.o_done[w]);
               }
             }
@@ -624,18 +628,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_commit(&ctl.s_full[w]);
             tc_commit(&ctl.k_empty[kst]);
+            if (split) tc_commit(&ctl.k_empty[kst]);
             if (j + 1 == ntw) tc_commit(&ctl.q_empty[w]);
           }
           __syncwarp();
-        };
-        // the other tile's block of a split part, handed back as it comes
-        const auto pass_on = [&](uint64_t* full, uint64_t* empty, uint32_t stages, int j) {
-          if (!split || j >= nt) return true;
-          const uint32_t n = blk + j, st = n % stages;
-          if (!wait(&full[st], (n / stages) & 1)) return false;
-          if (lane == 0) mbar_arrive(&empty[st]);
-          __syncwarp();
-          return true;
         };
         for (int j = -1; j < steps; ++j) {
           // j-th block's values, next block's keys
@@ -655,7 +651,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&ctl.k_empty[kst]);
               }
             }
-            if (!(ok = pass_on(ctl.k_full, ctl.k_empty, KS, 2 * j + 2 + (w ^ 1)))) break;
             if (there_v) {
               if (!(ok = wait(&ctl.v_full[vst], (vb / VS) & 1))) break;
               if (pv) {
@@ -690,9 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               __syncwarp();
             }
-            if (!(ok = pass_on(ctl.k_full, ctl.k_empty, KS, 2 * j + 2 + (w ^ 1)))) break;
           }
-          if (j >= 0 && !(ok = pass_on(ctl.v_full, ctl.v_empty, VS, 2 * j + (w ^ 1)))) break;
         }
         blk += nt;
       }
