@@ -131,9 +131,6 @@ struct Line {
 };
 
 // A whole warp; lanes agree but for `own`.
-#ifndef LEAST8
-#define LEAST8 2
-#endif
 template <int D, bool CHUNK, bool E8 = false>
 __device__ __forceinline__ Line measure_line(const AttnParams& p, int lane) {
   Line l;
@@ -154,7 +151,7 @@ __device__ __forceinline__ Line measure_line(const AttnParams& p, int lane) {
   l.u = u;
   // whole blocks, a few at least: fewer records to join where there is little to do, and a worker behind an
   // item's first block always has a part of it
-  constexpr int K = Geometry<D, CHUNK, E8>::kKeys, kLeast = (CHUNK ? 1 : E8 ? LEAST8 : 2) * K;
+  constexpr int K = Geometry<D, CHUNK, E8>::kKeys, kLeast = (CHUNK ? 1 : 2) * K;
   const int64_t even = (u + p.workers - 1) / p.workers;
   l.part = even <= kLeast ? kLeast : (even + K - 1) / K * K;
   return l;

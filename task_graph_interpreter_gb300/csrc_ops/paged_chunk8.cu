@@ -50,7 +50,7 @@ struct Smem {
   static constexpr int kHalf = 128 * 128;        // 128 rows of 128 bytes
   static constexpr int kValues = kHalf * (D / 64);
   static constexpr int kKeyStages = D == 128 ? 3 : 4, kRawStages = D == 128 ? 3 : 4, kValueStages = D == 128 ? 2 : 3;
-  static constexpr int kControl = 3072;          // barriers, descriptors (struct Control)
+  static constexpr int kControl = 3 * 1024;      // barriers, descriptors (struct Control)
   static constexpr int kBytes =
       kControl + 2 * kQuery + kKeyStages * kCodes + kRawStages * kCodes + kValueStages * kValues;
 };

@@ -436,8 +436,13 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
 // workers and deals their items' rows out to its warps; with few rows several
 // warps share the records of one and meet in shared memory.  (A block per
 // worker spent more on its 608 blocks than on the records: one request of 4096
-// keys 14.2 us, 64 of 512 to 8192 keys 175.4; this way 13.2 and 173.8.)
+// keys 14.2 us, 64 of 512 to 8192 keys 175.4; this way 13.2 and 173.8.)  More
+// rows than eight (e4m3 pages have up to sixteen) are dealt to two blocks: one
+// request of 8192 keys and 12 rows, whose 128 records a head are all the work
+// that is left, 32 us with one, 24 with two, 22 with four; 64 requests of 512 to
+// 2048 keys 56, 58 and 63.
 constexpr int kJoinWarps = 16;
+constexpr int kManyRowsDeal = 2;
 
 __device__ __forceinline__ Note read_note(const AttnParams& p, int D, int w) {
   const int4 n = __ldcg(reinterpret_cast<const int4*>(note_of(p, D, w)));
@@ -456,11 +461,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_rows_kernel(const __grid
   Note notes[kRowWarps];
 #pragma unroll
   for (int k = 0; k < kRowWarps; ++k) notes[k] = read_note(p, D, blockIdx.x + k * gridDim.x);
+  const int deal = gridDim.y, mine = blockIdx.y;  // this block's rows: mine, mine + deal, ... of each item
+  const auto rows_of = [&](const Note& n) { return (n.tokens * p.G - mine + deal - 1) / deal; };
   int total = 0, most = 0;  // rows of the noted items; records of the longest
 #pragma unroll
   for (int k = 0; k < kRowWarps; ++k) {
     if (notes[k].tokens == 0) continue;
-    total += notes[k].tokens * p.G;
+    total += rows_of(notes[k]);
     most = max(most, (int)(blockIdx.x + k * gridDim.x) - notes[k].first + 1);
   }
   int shares = 1;
@@ -474,7 +481,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_rows_kernel(const __grid
     bool found = false;
 #pragma unroll
     for (int k = 0; k < kRowWarps; ++k) {
-      const int rows = notes[k].tokens * p.G;
+      const int rows = notes[k].tokens == 0 ? 0 : rows_of(notes[k]);
       if (on && !found) {
         if (row < rows) {
           found = true;
@@ -485,6 +492,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_rows_kernel(const __grid
         }
       }
     }
+    row = row * deal + mine;
     const int count = on ? w - note.first + 1 : 0, tok = row / p.G, head = row % p.G;
     float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
@@ -614,7 +622,8 @@ cudaError_t launch_join(const AttnParams& p, int D, bool chunk, cudaStream_t str
   if (chunk)  // a block per worker and eight columns
     return launch_early(D == 128 ? join_chunk_kernel<128> : join_chunk_kernel<64>,
                         dim3((unsigned)p.workers, (unsigned)(D / kJoinCols)), dim3(kTileRows), 0, stream, p);
-  return launch_early(D == 128 ? join_rows_kernel<128> : join_rows_kernel<64>, dim3((unsigned)(p.workers / kRowWarps)),
+  return launch_early(D == 128 ? join_rows_kernel<128> : join_rows_kernel<64>,
+                      dim3((unsigned)(p.workers / kRowWarps), p.rows > kMaxFewRows ? kManyRowsDeal : 1),
                       dim3(kJoinWarps * 32), 0, stream, p);
 }
 

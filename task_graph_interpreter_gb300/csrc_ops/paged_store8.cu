@@ -424,6 +424,14 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Runs<S::WINDOW
   }
 }
 
+// Windows of 16 rows in one launch with the queries while the lanes that keys and values have work for are about half
+// of what the GPU holds at once; else windows of 64 in a launch of their own, the queries' beside it.  One launch and two,
+// 8/32 heads of bf16: 256 tokens 6.4 and 5.7 us, 512 6.5 and 9.3, 1024 8.7 and 10.8, 2048 17.0 and 16.8, 8192 60 and
+// 50; 16/64 heads: 600 tokens 10.7 and 14.9, 1024 19.6 and 17.7; 512 requests of one token 6.1 and 9.5.
+constexpr int kFewLanes = 160 * 1024;
+// Three blocks of 256 threads and 64 rows per SM: a prompt of 8192 tokens 50 us.  Two of them 56, four of 128 threads
+// and 32 rows 60.
+constexpr int kKvThreads = 256, kKvWindow = 64, kKvBlocks = 3;
 constexpr int kQueryBatch = 3;      // heads a lane group has in flight
 constexpr int kQueryMaxTokens = 4;  // tokens of a block of queries
 
@@ -473,9 +481,6 @@ __device__ __forceinline__ void queries(const Store8Params& p, Turn<S::D>* turns
   }
 }
 
-#ifndef KVB
-#define KVB 3
-#endif
 // Keys and values first, then the queries, in one launch
 template <typename S>
 __global__ void __launch_bounds__(S::THREADS) store8_kernel(const __grid_constant__ Store8Params p) {
@@ -489,26 +494,18 @@ __global__ void __launch_bounds__(S::THREADS) store8_kernel(const __grid_constan
 }
 // Keys and values alone
 template <typename S>
-__global__ void __launch_bounds__(S::THREADS, KVB) store8_kv_kernel(const __grid_constant__ Store8Params p) {
+__global__ void __launch_bounds__(S::THREADS, kKvBlocks) store8_kv_kernel(const __grid_constant__ Store8Params p) {
   __shared__ Runs<S::WINDOW, S::D> runs;
   ptx::launch_dependents();  // the queries' blocks follow as these end
   store_runs<S>(p, runs, blockIdx.x);
 }
 
-#ifndef FEW_ROWS
-#define FEW_ROWS 512
-#endif
-#ifndef KVT
-#define KVT 256
-#define KVW 64
-#define KVK 1
-#endif
 template <typename T, int D>
 cudaError_t launch_store8(Store8Params& p, int sms, cudaStream_t stream) {
   constexpr int E = kElems<T>, LPH = D / 2 / E;
   const auto kv_blocks = [&](int window) { return (unsigned)(((int64_t)p.N + window - 1) / window * 2 * p.Hkv); };
-  if (p.N > FEW_ROWS) {
-    using S = Shape<T, D, KVT, KVW, KVK * KVW / (KVT / LPH)>;
+  if ((int64_t)p.N * 2 * p.Hkv * LPH > kFewLanes) {
+    using S = Shape<T, D, kKvThreads, kKvWindow, kKvWindow / (kKvThreads / LPH)>;
     store8_kv_kernel<S><<<kv_blocks(S::WINDOW), S::THREADS, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;

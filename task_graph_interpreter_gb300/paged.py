@@ -95,6 +95,8 @@ def qk_norm_rope(qkv, Hq: int, Hkv: int, D: int, positions, slots, kpool, vpool,
 def attention_workspace(max_new: int, Hq: int, Hkv: int, D: int, device="cuda", dtype=torch.bfloat16) -> torch.Tensor:
     """A workspace for ``attention`` with these sizes over pools of ``dtype``.
     Calls that share one must not overlap: run them on one stream."""
+    if dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise ValueError(f"pools are torch.bfloat16 or torch.float8_e4m3fn, not {dtype}")
     size = L.mk_paged_attention_workspace if dtype == torch.bfloat16 else L.mk_paged_attention_e4m3_workspace
     with torch.cuda.device(device):
         return torch.empty(size(max_new, Hq, Hkv, D), dtype=torch.uint8, device=device)

@@ -198,3 +198,53 @@ def test_tensor_functions_refuse_what_does_not_fit():
             f(*args, **kw)
     with pytest.raises(L.MkError):  # rows that overlap
         f(x[:1].expand(4, 100), t)
+
+
+def test_a_tensor_that_carries_a_tangent_is_refused():
+    import torch.autograd.forward_ad as forward_ad
+    x, t = torch.randn(4, 100, device=DEV), i32([0] * 4)
+    with forward_ad.dual_level(), torch.no_grad():
+        with pytest.raises(ValueError, match="tangent"):
+            logprobs.token_logprobs(forward_ad.make_dual(x, torch.ones_like(x)), t)
+    with torch.no_grad():
+        logprobs.token_logprobs(x.requires_grad_(), t)
+
+
+def test_logits_dropped_behind_a_call_on_another_stream_are_not_made_over():
+    x = torch.randn(20, 30011, device=DEV)
+    t = torch.randint(0, 30011, (20,), device=DEV).int()
+    want = logprobs.token_logprobs(x, t, top=7)
+    s, dropped = torch.cuda.Stream(), x.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(400_000_000)  # about 0.2 s
+    got = logprobs.token_logprobs(dropped, t, top=7, stream=s)
+    at = dropped.data_ptr()
+    del dropped
+    over = [torch.zeros_like(x) for _ in range(4)]
+    assert at not in [o.data_ptr() for o in over]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_calls_that_overlap_on_two_streams():
+    xs = [torch.randn(n, 128256, device=DEV) for n in (1, 30)]
+    ts = [torch.zeros(n, dtype=torch.int32, device=DEV) for n in (1, 30)]
+    want = [logprobs.token_logprobs(x, t, top=20) for x, t in zip(xs, ts)]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [[logprobs.token_logprobs(x, t, top=20, stream=s) for x, t, s in zip(xs, ts, streams)] for _ in range(10)]
+    torch.cuda.synchronize()
+    for both in got:
+        for a, b in zip(both, want):
+            assert all(torch.equal(c, d) for c, d in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_offsets_past_32_bits(dtype):
+    """Rows 2^29 and more elements apart: the last begins behind 2^32 bytes."""
+    ld, N, V = (1 << 29) + 7, 4 if dtype == torch.float32 else 8, 1003
+    x = torch.zeros((N - 1) * ld + V, dtype=dtype, device=DEV).as_strided((N, V), (ld, 1))
+    x.copy_(torch.randn(N, V, device=DEV))
+    assert (N - 1) * ld * x.element_size() > 1 << 32
+    check(x, i32([3] * N), 5)

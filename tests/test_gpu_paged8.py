@@ -183,6 +183,36 @@ def test_stores_match_float64(ctx, new, Hq, Hkv, D, page, dtype, norm, pad, stri
     run_store(c, Hq, Hkv, D, page)
 
 
+LARGE = [  # as above: keys and values in a launch of their own
+    ([0], [700], 16, 8, 128, 64, F32, "qk", 0, False, 0), ([5, 100, 0, 77], [300, 90, 264, 1], 16, 16, 128, 16, BF, "k", 30, True, 0),
+    ([30, 7, 0], [400, 1, 300], 32, 32, 64, 32, BF, "", 9, True, 4), (list(range(700)), [1] * 700, 8, 8, 128, 16, F32, "q", 3, False, 0),
+    ([255, 3, 64], [257, 300, 130], 16, 16, 64, 128, F32, "qk", 1, False, 2), ([77], [900], 8, 8, 128, 256, F32, "k", 0, False, 15),
+    ([3] * 200, [1, 5, 2, 9] * 50, 16, 16, 128, 64, BF, "qk", 0, True, 1)]
+
+
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D,page,dtype,norm,pad,strided,gaps", LARGE)
+def test_large_stores_match_float64(ctx, new, Hq, Hkv, D, page, dtype, norm, pad, strided, gaps):
+    c = store_case(ctx, new, Hq, Hkv, D, page, dtype, norm, len(ctx) * 31 + page, pad, strided, gaps)
+    run_store(c, Hq, Hkv, D, page)
+
+
+def test_a_large_store_holds_what_its_parts_store():
+    """The two forms of the launch round alike."""
+    c = store_case([0], [1472], 8, 8, 128, 64, BF, "qk", 12, junk=True)
+    whole = run_store(c, 8, 8, 128, 64, check=False)
+    step = dict(c)
+    for a, b in ((0, 640), (640, 1280), (1280, 1472)):
+        part = dict(step, qkv=c["qkv"][a:b], pos=c["pos"][a:b], slots=c["slots"][a:b])
+        out, *now = run_store(part, 8, 8, 128, 64, check=False)
+        # the large form's queries are those of bf16 pages: half a bf16 step of their own
+        assert bool(((out.float() - whole[0][a:b].float()).abs() <= 2.0 ** -7 * whole[0][a:b].float().abs() + 2.0 ** -16).all())
+        step.update(zip(("kpool", "vpool", "kscale", "vscale"), now))
+    for k, w in zip(("kscale", "vscale"), whole[3:]):
+        assert torch.equal(step[k].view(torch.int32), w.view(torch.int32))
+    for k, w in zip(("kpool", "vpool"), whole[1:3]):
+        assert torch.equal(step[k].view(torch.uint8), w.view(torch.uint8))
+
+
 @pytest.mark.parametrize("spread", [0.0, 12.0])
 def test_scales_far_below_and_above_the_new_values(spread):
     """Pages begun with scales of 2^-40 to 2^40 times the new values', held codes become subnormal or zero."""
@@ -510,6 +540,19 @@ def test_attention_with_items_cut_at_every_place(G):
     close(got, *attention_ref(q, k, v, ks, vs, table, cu, ctx, 16, 64 ** -0.5))
 
 
+@pytest.mark.parametrize("G,n", [(1, 9), (1, 16), (2, 7), (2, 8), (3, 3), (3, 5), (4, 3), (4, 4), (5, 2), (5, 3), (7, 2), (8, 2),
+                                 (9, 1), (13, 1), (16, 1)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_of_nine_to_sixteen_rows(G, n, D):
+    """Two eights of rows, items cut at every place and whole ones, and one long item whose records two blocks join."""
+    for ctx in ([700 + 37 * i for i in range(17)], [20011], [0, 5, 31, 32, 33, 64, 127, 9000]):
+        new = [1 + i % n for i in range(len(ctx))][::-1]
+        new[0] = n
+        q, k, v, ks, vs, table, cu = attention_case(ctx, new, 2 * G, 2, D, 16, G + n)
+        got = paged.attention(q, k, v, table, i32(cu), i32(ctx), n, kscale=ks, vscale=vs)
+        close(got, *attention_ref(q, k, v, ks, vs, table, cu, ctx, 16, D ** -0.5))
+
+
 @pytest.mark.parametrize("Hq,n,D,ctx", [(4, 1, 128, (1 << 22) + 5), (4, 2, 64, 3 << 20), (1, 9, 128, (1 << 22) - 9), (1, 40, 64, 3 << 20)])
 def test_attention_over_millions_of_keys_keeps_its_sums(Hq, n, D, ctx):
     """Equal scores and values of one: every result is one, whatever the sums have to hold; pages of two scales."""
@@ -732,3 +775,115 @@ def test_items_of_one_tile_whose_key_blocks_two_take_in_turn(n, D):
     q, k, v, ks, vs, table, cu = attention_case(ctx, new, 8, 2, D, 32, n)
     got = paged.attention(q, k, v, table, i32(cu), i32(ctx), 200, kscale=ks, vscale=vs)
     close(got, *attention_ref(q, k, v, ks, vs, table, cu, ctx, 32, D ** -0.5))
+
+
+# ------------------------------------------------------------------ workspaces, lifetimes, layouts
+MIXED = [  # ctx, new, Hq, Hkv, D: both kernels, cut and whole items, many records and few
+    ([4096], [1], 32, 8, 128), ([0, 1000, 0, 64], [700, 33, 0, 256], 32, 4, 64), ([31, 900], [1, 1], 12, 12, 64),
+    ([8000], [4], 32, 8, 128), ([2000], [64], 8, 1, 128), ([513, 100], [4, 2], 4, 2, 128), ([0], [1500], 5, 5, 128),
+    ([5], [2], 32, 1, 64)]
+
+
+def test_attention_on_a_workspace_of_the_caller():
+    """One buffer of the largest size for calls of both kernels in turn, and one of each call's own size, both full of
+    NaN and of the call before: the same bits as without."""
+    sizes = [paged.attention_workspace(max(new), Hq, Hkv, D, dtype=E4M3).numel() for _, new, Hq, Hkv, D in MIXED]
+    shared = torch.full((max(sizes),), 255, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        for i, (ctx, new, Hq, Hkv, D) in enumerate(MIXED):
+            q, k, v, ks, vs, table, cu = attention_case(ctx, new, Hq, Hkv, D, 32, 61 + i)
+            status = i32([0])
+            args, kw = (q, k, v, table, i32(cu), i32(ctx), max(new)), dict(kscale=ks, vscale=vs, status=status)
+            want = paged.attention(*args, **kw)
+            own = torch.full((sizes[i] + 64,), 255, dtype=torch.uint8, device=DEV)
+            for ws in (shared, own[:sizes[i]]):
+                assert torch.equal(paged.attention(*args, workspace=ws, **kw), want)
+            assert torch.all(own[sizes[i]:] == 255) and int(status) == 0
+            with pytest.raises(L.MkError) as e:
+                paged.attention(*args, workspace=own[:sizes[i] - 1], **kw)
+            assert e.value.code == L.MK_ERR_LIMIT
+
+
+def test_graphs_that_share_a_workspace_replay_one_after_the_other():
+    sizes = [paged.attention_workspace(max(new), Hq, Hkv, D, dtype=E4M3).numel() for _, new, Hq, Hkv, D in MIXED]
+    ws = torch.full((max(sizes),), 255, dtype=torch.uint8, device=DEV)
+    held = []
+    for i, (ctx, new, Hq, Hkv, D) in enumerate(MIXED):
+        q, k, v, ks, vs, table, cu = attention_case(ctx, new, Hq, Hkv, D, 64, 91 + i)
+        out, lens = torch.zeros_like(q), (i32(cu), i32(ctx))
+        call = lambda: paged.attention(q, k, v, table, *lens, max(new), kscale=ks, vscale=vs, out=out, workspace=ws)  # noqa: E731,B023
+        want = call().clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        out.zero_()
+        held.append((graph, out, want, (q, k, v, ks, vs, table, lens)))
+    for order in (range(len(held)), reversed(range(len(held)))):
+        for i in order:
+            held[i][0].replay()
+        for _, out, want, _ in held:
+            assert torch.equal(out, want)
+            out.zero_()
+
+
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D", [([0, 1000, 0, 64], [700, 33, 0, 256], 32, 4, 64), ([2000], [64], 8, 1, 128),
+                                              ([40] * 300, [9] * 300, 4, 1, 128), ([0, 7], [130, 3], 4, 2, 64),
+                                              ([4096, 3], [1, 1], 8, 2, 128), ([4096, 3], [3, 2], 8, 2, 128)])
+def test_attention_into_rows_that_are_aligned_to_16_bytes_only(ctx, new, Hq, Hkv, D):
+    q, k, v, ks, vs, table, cu = attention_case(ctx, new, Hq, Hkv, D, 16, 81)
+    args, kw = (q, k, v, table, i32(cu), i32(ctx), max(new)), dict(kscale=ks, vscale=vs)
+    want = paged.attention(*args, **kw)
+    n, row = cu[-1], Hq * D
+    for ld, first in ((row + 8, 0), (row + 16, 8), (row, 8), (row + 24, 8)):
+        buf = torch.full((n * ld + 64,), 5.0, dtype=torch.bfloat16, device=DEV)
+        out = buf.as_strided((n, Hq, D), (ld, D, 1), first)
+        paged.attention(*args, out=out, **kw)
+        assert torch.equal(out, want)
+        out.fill_(5.0)
+        assert torch.all(buf == 5.0)
+
+
+@pytest.mark.parametrize("op", ["stores", "attention"])
+def test_an_input_dropped_behind_a_call_on_another_stream_is_not_made_over(op):
+    if op == "stores":
+        g = torch.Generator(device=DEV).manual_seed(51)
+        source, at = torch.randn(40, 12 * 64, device=DEV, generator=g), torch.arange(40, dtype=torch.int32, device=DEV)
+        pools = [torch.zeros(4, 2, 16, 64, device=DEV).to(E4M3) for _ in range(2)]
+        scales = dict(kscale=torch.ones(4, 2, device=DEV), vscale=torch.ones(4, 2, device=DEV))
+        run = lambda x, **kw: paged.qk_norm_rope(x, 8, 2, 64, at, at, *pools, **scales, **kw)  # noqa: E731
+    else:
+        source, k, v, ks, vs, table, cu = attention_case([300], [3], 8, 2, 64, 16, 51)
+        lens = i32(cu), i32([300])
+        run = lambda x, **kw: paged.attention(x, k, v, table, *lens, 3, kscale=ks, vscale=vs, **kw)  # noqa: E731
+    want = run(source.clone()).clone()
+    s, dropped = torch.cuda.Stream(), source.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(400_000_000)  # about 0.2 s
+    got = run(dropped, stream=s)
+    at_address = dropped.data_ptr()
+    del dropped
+    over = [torch.zeros_like(source) for _ in range(4)]
+    assert at_address not in [t.data_ptr() for t in over]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_a_gradient_or_a_tangent_is_refused():
+    import torch.autograd.forward_ad as forward_ad
+    q, k, v, ks, vs, table, cu = attention_case([30], [2], 8, 2, 64, 16, 31)
+    lens, x, pos = (i32(cu), i32([30])), torch.zeros(2, 12 * 64, device=DEV), i32([0, 1])
+    attend = lambda a, b, c: paged.attention(a, k, v, table, *lens, 2, kscale=b, vscale=c)  # noqa: E731
+    store = lambda a, b, c: paged.qk_norm_rope(a, 8, 2, 64, pos, pos, k, v, kscale=b, vscale=c)  # noqa: E731
+    grad = lambda t: t.clone().requires_grad_()  # noqa: E731
+    for f, a in ((attend, q), (store, x)):
+        for args in ((grad(a), ks, vs), (a, grad(ks), vs), (a, ks, grad(vs))):
+            with pytest.raises(ValueError, match="gradient"):
+                f(*args)
+        with forward_ad.dual_level(), torch.no_grad():
+            dual = lambda t: forward_ad.make_dual(t, torch.ones_like(t))  # noqa: E731
+            for args in ((dual(a), ks, vs), (a, dual(ks), vs), (a, ks, dual(vs))):
+                with pytest.raises(ValueError, match="tangent"):
+                    f(*args)
+        with torch.no_grad():
+            f(grad(a), ks, vs)

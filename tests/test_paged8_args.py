@@ -39,6 +39,26 @@ def test_attention_refuses(L, change):  # noqa: F811
     refused(L, "mk_paged_attention_e4m3", ATTN8, L.MK_ERR_ARG, **change)
 
 
+def test_attention_workspace_refuses(L):  # noqa: F811
+    for args in ((0, 8, 2, 64), (1, 7, 2, 64), (1, 8, 2, 65), (1, 8, 0, 64), (1, 258, 2, 64)):
+        with pytest.raises(L.MkError) as e:
+            L.mk_paged_attention_e4m3_workspace(*args)
+        assert e.value.code == L.MK_ERR_ARG
+
+
+@pytest.mark.parametrize("page_size,max_pages", [(16, (1 << 27) - 1), (16, (1 << 27) - 15), (128, (1 << 24) - 1)])
+def test_attention_refuses_tables_up_to_the_end_of_int32(L, page_size, max_pages):  # noqa: F811
+    assert max_pages * page_size < 2 ** 31
+    refused(L, "mk_paged_attention_e4m3", ATTN8, L.MK_ERR_ARG, page_size=page_size, max_pages=max_pages)
+
+
+def test_pools_of_another_type_and_their_workspace_are_refused():
+    from task_graph_interpreter_gb300 import paged
+    for dtype in (torch.float8_e5m2, torch.uint8, torch.float16, torch.float32):
+        with pytest.raises(ValueError, match="pools"):
+            paged.attention_workspace(1, 8, 2, 64, dtype=dtype)
+
+
 @pytest.mark.parametrize("change", [dict(N=-1), dict(V=0), dict(V=1 << 30), dict(top=-1), dict(top=33), dict(V=4, top=5),
                                     dict(logits_dtype=0), dict(logits_dtype=3), dict(ld=999), dict(ld=-1000),
                                     dict(logits=P + 2), dict(logits=P + 1, logits_dtype=1), dict(logits=0),
