@@ -17,11 +17,16 @@
 // takes the runs that begin in its window of rows, a few rows per pass, and
 // follows the last of them behind the window.  Values stay in registers between
 // the maximum and the store (those of runs that reach far behind the window are
-// read again), each lane turns its pairs itself, and every warp finds the runs
-// for itself, so the block meets three times.  For a prompt's 8192 tokens of 8
-// heads keys and values took 38 us with the rows' angles in shared memory, whose
-// barriers and bookkeeping were most of it, and a warp alone per window and head,
-// without any barrier, 14 us for each of its runs of 64 rows.
+// read again), each lane turns its pairs itself, and one warp finds the runs
+// while the rows are on their way, so the block meets three times.
+//
+// A prompt of 8192 tokens, 8/32 heads of 128, bf16: 51 us, of which queries
+// are 24.5 (5.5 TB/s) and keys and values 26, where bytes alone would take 8:
+// a third of the warps' time is the three meetings, a third the rows' first
+// arrival.  Measured on the way: angles shared by a row's heads in shared memory
+// 38 us for keys and values (more meetings), a warp alone per window and head,
+// without any, 14 us for each of its runs of 64 rows.  One token 3.8 us, 64
+// tokens of as many requests 4.2 us: the chain positions, runs, rows, store.
 #include <cuda_fp16.h>
 
 #include "paged_norm.cuh"
@@ -65,6 +70,38 @@ __device__ __forceinline__ void make_turn(Turn<D>& t, int j, const Store8Params&
   t.sb[j] = -s * gb;
   t.cb[j] = c * gb;
   t.sa[j] = s * ga;
+}
+
+// Sines and cosines of two angles, in 2^-32 turns: the nearest quarter turn is taken off, the series of what is left (at
+// most an eighth of a turn) are summed up to the terms under 2^-25, and the quarter turns swap and sign the two.
+__device__ __forceinline__ void sincos2(const uint32_t (&turn)[2], uint64_t& sine, uint64_t& cosine) {
+  float x[2];
+  uint32_t quarter[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    quarter[e] = (turn[e] + 0x20000000u) >> 30;
+    x[e] = (float)(int32_t)(turn[e] - (quarter[e] << 30)) * (0x1p-31f * 3.14159265f);
+  }
+  const auto both = [](float c) { return ptx::pair_f32(c, c); };
+  const uint64_t a = ptx::pair_f32(x[0], x[1]), a2 = ptx::mul2(a, a);
+  uint64_t s = ptx::fma2(a2, both(1.f / 362880.f), both(-1.f / 5040.f));
+  uint64_t c = ptx::fma2(a2, both(1.f / 40320.f), both(-1.f / 720.f));
+  s = ptx::fma2(a2, s, both(1.f / 120.f));
+  c = ptx::fma2(a2, c, both(1.f / 24.f));
+  s = ptx::fma2(a2, s, both(-1.f / 6.f));
+  c = ptx::fma2(a2, c, both(-0.5f));
+  s = ptx::fma2(ptx::mul2(a2, a), s, a);
+  c = ptx::fma2(a2, c, both(1.f));
+  const float2 s1 = ptx::unpair_f32(s), c1 = ptx::unpair_f32(c);
+  float sv[2] = {s1.x, s1.y}, cv[2] = {c1.x, c1.y};
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float u = quarter[e] & 1 ? cv[e] : sv[e], v = quarter[e] & 1 ? sv[e] : cv[e];
+    sv[e] = __uint_as_float(__float_as_uint(u) ^ (quarter[e] & 2) << 30);
+    cv[e] = __uint_as_float(__float_as_uint(v) ^ ((quarter[e] + 1) & 2) << 30);
+  }
+  sine = ptx::pair_f32(sv[0], sv[1]);
+  cosine = ptx::pair_f32(cv[0], cv[1]);
 }
 
 // A lane's elements of a head, normed (`norm`) and turned.  The lanes of `mask` hold the head.
@@ -270,7 +307,7 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Runs<S::WINDOW
     if (w < PASSES) return sm.run[i] >= 0 ? sm.slot[BACK + i] : -1;
     return i - WINDOW < more ? slot_of(i) : -1;
   };
-  // the values to be stored, with the hardware's sine and cosine: off by under 2^-20, and keys are rounded to 2^-4
+  // the values to be stored
   const auto values = [&](int w, const Raw<T, E>& ra, const Raw<T, E>& rb, float (&a)[E], float (&b)[E]) {
     ra.get(a);
     rb.get(b);
@@ -296,18 +333,15 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Runs<S::WINDOW
       const uint64_t r2 = ptx::pair_f32(r, r);
 #pragma unroll
       for (int i = 0; i < E; i += 2) {
-        float s[2], c[2];
+        uint32_t turn[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint64_t turn = (uint64_t)(uint32_t)pos * sm.freq[gl * E + i + e];
-          const float angle = (float)(int32_t)(turn >> 32) * (0x1p-31f * 3.14159265f);
-          s[e] = __sinf(angle);
-          c[e] = __cosf(angle);
-        }
+        for (int e = 0; e < 2; ++e) turn[e] = (uint32_t)((uint64_t)(uint32_t)pos * sm.freq[gl * E + i + e] >> 32);
+        uint64_t s2, c2;
+        sincos2(turn, s2, c2);
         const float2 g0 = sm.gain[gl * E + i], g1 = sm.gain[gl * E + i + 1];
         const uint64_t u = ptx::mul2(ptx::mul2(r2, ptx::pair_f32(g0.x, g1.x)), ptx::pair_f32(a[i], a[i + 1]));
         const uint64_t v = ptx::mul2(ptx::mul2(r2, ptx::pair_f32(g0.y, g1.y)), ptx::pair_f32(b[i], b[i + 1]));
-        const uint64_t c2 = ptx::pair_f32(c[0], c[1]), s2 = ptx::pair_f32(s[0], s[1]), n2 = ptx::pair_f32(-s[0], -s[1]);
+        const uint64_t n2 = s2 ^ 0x8000000080000000ull;
         const float2 ya = ptx::unpair_f32(ptx::fma2(v, n2, ptx::mul2(u, c2)));
         const float2 yb = ptx::unpair_f32(ptx::fma2(u, s2, ptx::mul2(v, c2)));
         a[i] = ya.x;
@@ -427,10 +461,11 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Runs<S::WINDOW
 // Windows of 16 rows in one launch with the queries while the lanes that keys and values have work for are about half
 // of what the GPU holds at once; else windows of 64 in a launch of their own, the queries' beside it.  One launch and two,
 // 8/32 heads of bf16: 256 tokens 6.4 and 5.7 us, 512 6.5 and 9.3, 1024 8.7 and 10.8, 2048 17.0 and 16.8, 8192 60 and
-// 50; 16/64 heads: 600 tokens 10.7 and 14.9, 1024 19.6 and 17.7; 512 requests of one token 6.1 and 9.5.
+// 51; 16/64 heads: 600 tokens 10.7 and 14.9, 1024 19.6 and 17.7; 512 requests of one token 6.1 and 9.5.
 constexpr int kFewLanes = 160 * 1024;
-// Three blocks of 256 threads and 64 rows per SM: a prompt of 8192 tokens 50 us.  Two of them 56, four of 128 threads
-// and 32 rows 60.
+// Three blocks of 256 threads and 64 rows per SM: a prompt of 8192 tokens 51 us.  Two of them 56, four 50 (but 41 for
+// 39 where eleven ragged chunks meet), four of 128 threads and 32 rows 60.  Blocks that stay and take the heads of a
+// window one after the other, its runs found once and the next head's rows on their way, took 52.
 constexpr int kKvThreads = 256, kKvWindow = 64, kKvBlocks = 3;
 constexpr int kQueryBatch = 3;      // heads a lane group has in flight
 constexpr int kQueryMaxTokens = 4;  // tokens of a block of queries
@@ -481,9 +516,12 @@ __device__ __forceinline__ void queries(const Store8Params& p, Turn<S::D>* turns
   }
 }
 
-// Keys and values first, then the queries, in one launch
+// Keys and values first, then the queries, in one launch.  Threads that an SM holds are worth a few spilled registers: 777
+// rows of f32 with 768 of them 7.2 us, with 512 8.6; 1024 tokens of bf16 with 512 8.6, with 384 9.8.
+template <typename T>
+constexpr int kMixedThreads = sizeof(T) == 4 ? 768 : 512;
 template <typename S>
-__global__ void __launch_bounds__(S::THREADS) store8_kernel(const __grid_constant__ Store8Params p) {
+__global__ void __launch_bounds__(S::THREADS, kMixedThreads<typename S::T> / S::THREADS) store8_kernel(const __grid_constant__ Store8Params p) {
   __shared__ union alignas(16) Both {
     __device__ Both() {}
     Runs<S::WINDOW, S::D> runs;
