@@ -576,9 +576,12 @@ int mk_qk_norm_rope_e4m3(void* stream, int N, int Hq, int Hkv, int D, const void
                          void* vpool, float* kscale, float* vscale, int num_pages, int page_size, int32_t* status);
 
 /* Attention: arguments, checks and status of mk_paged_attention, and a workspace of
- * mk_paged_attention_e4m3_workspace bytes.  Scales are positive and finite.  Queries keep 2^-18 of a row's largest element and more.
- * Probabilities are rounded to f16 (2^-11) in both kernels, maxima, sums and results
- * are f32.  Keys' scales are f32 factors of the scores.  Values' scales are exact
+ * mk_paged_attention_e4m3_workspace bytes.  With max_new * Hq / Hkv at most 16 the
+ * kernel for few rows runs, else the one for chunks.  The scales of pages that are
+ * read are positive and finite (others give any result).  Queries keep 2^-18 of a
+ * row's largest element and more.  Probabilities are rounded to f16 (2^-11) in both
+ * kernels, maxima, sums and results are f32.  Keys' scales are f32 factors of the
+ * scores.  Values' scales are exact
  * where they are powers of two (what the stores write) within 2^15 of each other;
  * others are rounded to f16 in the kernel for chunks. */
 int mk_paged_attention_e4m3(void* stream, int B, int N, int max_new, int Hq, int Hkv, int D, const void* q,

@@ -19,7 +19,16 @@
 //             so far, which the results carry
 //
 // Probabilities are kept times 2^14, and rounded to f16 (2^-11) once the
-// scale of the values is on them; what they are summed to is not rounded.
+// scale of the values is on them; what they are summed to is not rounded.  (Two
+// parts, as over bf16 pages, would keep what codes of four bits do not have.)
+//
+// Eight warps of 8 KB blocks, three in flight: 64 requests of 512 to 8192 keys
+// and four rows 100 us (5.8 TB/s; bf16 pages 178), four warps of 16 KB 126, for
+// a block's chain of products, softmax and products has half the time that it
+// has over bf16 pages; heads of 64 56 and 80.  What is left there is that chain
+// and the join.  One request of 4096 keys 13.5 us: two launches and eight
+// dependent round trips.  Up to two eights of rows run here (four requests of
+// 32768 keys and 12 rows 65 us); with three eights registers leave no room.
 #include "paged_attention.cuh"
 
 namespace mk {

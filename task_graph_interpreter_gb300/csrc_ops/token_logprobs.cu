@@ -18,6 +18,12 @@
 // Should more reach the bound than there is room for (equal logits), each warp
 // goes through its part with a buffer that is cut down to its `top` largest when
 // it is full.  A key's rank is the number of larger keys, counted by four threads.
+//
+// 2048 rows of 128256: f32 158 us (6.6 TB/s, a copy's rate), bf16 94 (5.6 TB/s:
+// twice the arithmetic per byte) and 101 with one
+// alternative, 120 with 20.  61 rows of f32 with 20 alternatives 12.5 us, of
+// which 4.2 are those; one row 4.4 us, 8.1 with 20: start, one trip to memory
+// and the cluster's meeting, then the chain bound, hits, logits, ranks.
 #include <cuda_bf16.h>
 
 #include "paged.h"

@@ -777,6 +777,47 @@ def test_items_of_one_tile_whose_key_blocks_two_take_in_turn(n, D):
     close(got, *attention_ref(q, k, v, ks, vs, table, cu, ctx, 32, D ** -0.5))
 
 
+@pytest.mark.parametrize("n,page", [(1, 16), (3, 32), (700, 64)])
+def test_a_captured_step_replays_on_new_inputs(n, page):
+    """Plan, stores, attention and log probabilities of a step in one graph: the bits of the same step called eagerly,
+    with small stores (one launch) and large ones (two, beside each other)."""
+    from task_graph_interpreter_gb300 import logprobs
+    Hq, Hkv, D, B = 16, 8, 128, 2
+    made = [paged.PagedCache(1, 140, page, Hkv, D, B, 64, B * n, dtype=E4M3) for _ in range(2)]
+    x = torch.zeros(B * n, (Hq + 2 * Hkv) * D, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(n)
+    head = torch.randn(Hq * D, 3000, device=DEV, generator=g) * 0.02
+    ctx, new, tokens = i32([0] * B), i32([n] * B), torch.randint(0, 3000, (B * n,), device=DEV, generator=g).int()
+
+    def step(cache):
+        cache.plan(ctx, new)
+        q = cache.append(0, x, Hq)
+        out = cache.attention(0, q, n)
+        return q, out, *logprobs.token_logprobs(out.view(B * n, -1).float() @ head, tokens, top=4)
+
+    def start(cache):
+        for t in (cache.kpool, cache.vpool):
+            t[0].view(torch.uint8).zero_()
+        cache.plan(i32([0] * B), i32([0] * B))
+
+    step(made[0])  # (allocations and kernels' first use)
+    start(made[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(made[0])
+    start(made[1])
+    for t in range(3):
+        x.normal_(generator=g).mul_(1 + t)
+        ctx.fill_(t * n)
+        graph.replay()
+        want = step(made[1])
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), t
+    for c in made:
+        c.check()
+
+
 # ------------------------------------------------------------------ workspaces, lifetimes, layouts
 MIXED = [  # ctx, new, Hq, Hkv, D: both kernels, cut and whole items, many records and few
     ([4096], [1], 32, 8, 128), ([0, 1000, 0, 64], [700, 33, 0, 256], 32, 4, 64), ([31, 900], [1, 1], 12, 12, 64),
