@@ -35,7 +35,9 @@ EXPORTS = [
     "mk_get_trace", "mk_kernel_info", "mk_destroy", "mk_last_error", "mk_debug_patch_task",
     "mk_attention_decode_noalloc", "mk_gemv_tensor_core_tiles", "mk_debug_set_epoch", "mk_set_chunk",
     "mk_paged_plan", "mk_qk_norm_rope", "mk_paged_attention", "mk_paged_attention_workspace", "mk_verify_drafts",
+    "mk_token_logprobs",
 ]
+EXPORTS_E4M3 = ["mk_qk_norm_rope_e4m3", "mk_paged_attention_e4m3", "mk_paged_attention_e4m3_workspace"]
 
 
 class MkConfig(ctypes.Structure):

@@ -1,5 +1,8 @@
 """Refusals of the operators on 8-bit pages and of token log probabilities (no GPU: what the host checks is refused
 before any device work, so fake aligned addresses stand in for device memory)."""
+import pathlib
+import re
+
 import pytest
 import torch
 
@@ -69,6 +72,13 @@ def test_log_probabilities_refuse(L, change):  # noqa: F811
 
 def test_log_probabilities_refuse_too_many_rows(L):  # noqa: F811
     refused(L, "mk_token_logprobs", SCORE, L.MK_ERR_LIMIT, N=2 ** 31 - 1)
+
+
+def test_the_library_exports_the_operators_on_8_bit_pages(L):  # noqa: F811
+    header = re.sub(r"/\*.*?\*/", "", (pathlib.Path(__file__).parents[1] / "include" / "mk.h").read_text(), flags=re.S)
+    declared = set(re.findall(r"\b(mk_\w+)\s*\(", header))
+    assert declared == set(L.EXPORTS) | set(L.EXPORTS_E4M3)
+    assert all(hasattr(L.lib(), name) for name in L.EXPORTS_E4M3)
 
 
 def test_tensors_on_the_cpu_are_refused(L):  # noqa: F811
