@@ -66,8 +66,10 @@ __device__ __forceinline__ Sums merge(Sums a, Sums b) {
   const float m = fmaxf(a.m, b.m), at = m == -INFINITY ? 0.f : m;
   constexpr float kLog2e = 1.4426950408889634f;
   const float da = a.m - at, db = b.m - at, fa = ex2(da * kLog2e), fb = ex2(db * kLog2e);
-  // (a part without weight may have a maximum of -inf)
-  const float ua = a.s == 0.f ? 0.f : fa * fmaf(a.s, da, a.u), ub = b.s == 0.f ? 0.f : fb * fmaf(b.s, db, b.u);
+  // (a part without weight adds nothing, although its maximum may be -inf, and s (x - m) past the largest f32 where it
+  // is finite, as masks of the type's lowest value make it: zero times infinity would be NaN)
+  const float ua = a.s == 0.f || fa == 0.f ? 0.f : fa * fmaf(a.s, da, a.u);
+  const float ub = b.s == 0.f || fb == 0.f ? 0.f : fb * fmaf(b.s, db, b.u);
   return {m, a.s * fa + b.s * fb, ua + ub};
 }
 

@@ -248,3 +248,39 @@ def test_offsets_past_32_bits(dtype):
     x.copy_(torch.randn(N, V, device=DEV))
     assert (N - 1) * ld * x.element_size() > 1 << 32
     check(x, i32([3] * N), 5)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("low", [0.0, -1e38, -1e34, -3e30])  # 0: the type's lowest value
+@pytest.mark.parametrize("N,V", [(3, 300), (3, 20011), (3, 128256), (200, 9001)])
+def test_vocabularies_masked_with_finite_values(N, V, low, dtype):
+    """Masks of the type's lowest value, and of others so low that their number times their distance to an ordinary
+    logit is past the largest f32: without weight, whether threads, warps or parts hold nothing else."""
+    g = torch.Generator(device=DEV).manual_seed(V)
+    low = low or torch.finfo(dtype).min
+    x = torch.full((N, V), low, device=DEV).to(dtype)
+    x[0, -5:] = torch.tensor([3, 1, -2, 5, 0.5], device=DEV).to(dtype)  # ordinary ones last
+    some = torch.randperm(V, device=DEV, generator=g)[:V // 50 + 1]     # scattered
+    x[1:, some] = (4 * torch.randn(N - 1, some.numel(), device=DEV, generator=g)).to(dtype)
+    tokens = torch.full((N,), V - 4, dtype=torch.int32, device=DEV)
+    tokens[1:] = some[0].int()
+    check(x, tokens, 5)
+    x[0, 7] = 1e38  # an ordinary one is as far from the largest
+    x[-1] = x[-1].flip(0)
+    r = logprobs.token_logprobs(x, None, top=1)
+    assert int(r.top_ids[0, 0]) == 7 and float(r.entropy[0]) == 0.0 and float(r.top_logprobs[0, 0]) == 0.0
+    assert bool(torch.isfinite(r.entropy).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [300, 128256])
+def test_rows_of_lowest_values_alone_are_uniform(V, dtype):
+    low = torch.finfo(dtype).min
+    x = torch.full((2, V), low, device=DEV).to(dtype)
+    x[1, V // 3:] = -math.inf
+    r = logprobs.token_logprobs(x, i32([V // 4, V // 4]), top=3)
+    want = torch.tensor([math.log(V), math.log(V // 3)], dtype=torch.float64, device=DEV)
+    near(r.logprobs, -want)
+    assert bool(((r.entropy.double() - want).abs() <= TOL * (1 + want)).all())
+    near(r.top_logprobs, -want[:, None].expand(2, 3))
+    assert r.top_ids.tolist() == [[0, 1, 2]] * 2
