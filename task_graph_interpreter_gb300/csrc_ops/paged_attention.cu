@@ -93,34 +93,34 @@ static int attention(const char* who, bool e4m3, void* stream_, int B, int N, in
                      const float* vscale, int num_pages, int page_size, const int32_t* table, int max_pages,
                      const int32_t* cu, const int32_t* ctx_len, float scale, void* out, int64_t ld_out, void* workspace,
                      size_t workspace_size, int32_t* status) {
-  const std::string name(who);
+  const auto refuse = [who](int code, const std::string& why) { return fail(code, std::string(who) + ": " + why); };
   if (!q || !kpool || !vpool || !table || !cu || !ctx_len || !out || !workspace ||
       (e4m3 && (!kscale || !vscale)))
-    return fail(MK_ERR_ARG, name + ": null argument");
+    return refuse(MK_ERR_ARG, "null argument");
   if (int rc = check_shape(who, max_new, Hq, Hkv, D)) return rc;
-  if (B < 0 || N < 0 || max_pages < 1) return fail(MK_ERR_ARG, name + ": need B, N >= 0 and max_pages >= 1");
+  if (B < 0 || N < 0 || max_pages < 1) return refuse(MK_ERR_ARG, "need B, N >= 0 and max_pages >= 1");
   if (!page_size_ok(page_size))
-    return fail(MK_ERR_ARG, name + ": page_size must be 16, 32, 64, 128 or 256");
+    return refuse(MK_ERR_ARG, "page_size must be 16, 32, 64, 128 or 256");
   // (positions are counted on to the end of a block of 128 keys, and past a request's last token to the end of two
   // tiles' rows: at most 254)
   if (num_pages < 1 || (int64_t)num_pages * Hkv * page_size > INT32_MAX ||
       (int64_t)max_pages * page_size > INT32_MAX - 255)
-    return fail(MK_ERR_ARG, name + ": rows of the pools must fit int32, max_pages * page_size 2^31 - 256");
+    return refuse(MK_ERR_ARG, "rows of the pools must fit int32, max_pages * page_size 2^31 - 256");
   if (ld_q < (int64_t)Hq * D || ld_q % 8 || ld_out < (int64_t)Hq * D || ld_out % 8)
-    return fail(MK_ERR_ARG, name + ": row strides must cover a row and be multiples of 16 bytes");
+    return refuse(MK_ERR_ARG, "row strides must cover a row and be multiples of 16 bytes");
   if (!aligned16(q) || !aligned16(kpool) || !aligned16(vpool) || !aligned16(out) || !aligned16(workspace))
-    return fail(MK_ERR_ARG, name + ": pointers must be 16-byte aligned");
-  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(MK_ERR_ARG, name + ": scale must be positive");
+    return refuse(MK_ERR_ARG, "pointers must be 16-byte aligned");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return refuse(MK_ERR_ARG, "scale must be positive");
   if (int rc = pending_error(who)) return rc;
   int sms = 0;
   if (int rc = device_sms(who, &sms)) return rc;
   const int G = Hq / Hkv;
   if (workspace_size < workspace_bytes(max_new, G, D, sms, e4m3))
-    return fail(MK_ERR_LIMIT, name + ": the workspace needs " +
+    return refuse(MK_ERR_LIMIT, "the workspace needs " +
                                   std::to_string(workspace_bytes(max_new, G, D, sms, e4m3)) + " bytes");
   if (B == 0 || N == 0) return MK_OK;
   EncodeTiledFn enc = encoder();
-  if (!enc) return fail(MK_ERR_CUDA, name + ": cuTensorMapEncodeTiled is not available");
+  if (!enc) return refuse(MK_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
 
   const bool few = few_rows(max_new, G, e4m3);
   Attn8Params p{};
@@ -159,7 +159,7 @@ static int attention(const char* who, bool e4m3, void* stream_, int B, int N, in
     const cuuint32_t qbox[3] = {64u, (cuuint32_t)G, (cuuint32_t)p.tq};
     ok = encode(enc, &qmap, q, 3, qdim, qstride, qbox);
   }
-  if (!ok) return fail(MK_ERR_CUDA, name + ": a tensor map could not be encoded");
+  if (!ok) return refuse(MK_ERR_CUDA, "a tensor map could not be encoded");
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   const cudaError_t e = e4m3 ? few ? launch_rows8(p, kmap, vmap, D, stream) : launch_chunk8(p, qmap, kmap, vmap, D, stream)
                         : few ? launch_rows(p, kmap, vmap, D, stream)
