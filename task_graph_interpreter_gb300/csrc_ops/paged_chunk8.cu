@@ -18,7 +18,11 @@
 // widened, relative to the power of two of the largest scale of the part so far;
 // O carries that unit and is rescaled where it rises, as where the running
 // maximum does.  (Widened values are exact where scales are powers of two within
-// 2^15 of each other; others are rounded to f16.)
+// 2^15 of each other; others are rounded to f16.)  That is the largest scale that
+// all rows of the item see.  In a block of which some rows see a part only, one
+// page may hold values so large that others, which more rows see, would be lost
+// in the common unit: such a block's values stay codes, and its scales go onto
+// each row's P, relative to the largest scale that the row sees.
 //
 // An item with one tile of tokens (drafts, the end of a prompt) would leave the
 // other tile's products and softmax idle: its key blocks are dealt to both in
@@ -58,6 +62,7 @@ constexpr int kThreads = 512;
 constexpr int kLaunchRegs = 128, kConsumerRegs = 176, kOtherRegs = 80, kWidenRegs = 80;
 static_assert(2 * kConsumerRegs + kOtherRegs + kWidenRegs <= 4 * kLaunchRegs, "register shares within the launch's");
 constexpr float kBias = 6.f;  // probabilities are kept times 2^kBias; a row's maximum may lag by 2^8
+constexpr int kFar = 15;      // widened values are exact down to scales 2^kFar below the unit
 
 template <int D>
 struct Smem {
@@ -76,6 +81,7 @@ struct Block {  // what is known of a block of keys
   float ks[8], vs[8];  // scales of its pages
   uint32_t missing;    // pages that are not in the pool, one bit each
   int ve;              // exponent of the largest scale of values of the part so far
+  int apart;           // its values are codes, and P carries their scales
 };
 struct Control {
   uint64_t k_full[4], k_empty[4], raw_full[4], raw_empty[4], v_full[4], v_empty[4], q_full[2], q_ready[2], q_empty[2],
@@ -87,7 +93,7 @@ struct Control {
   uint32_t tmem;
   Patience patience;
   float2 ml[128];            // maximum and sum of a row's second half of key blocks (a split part),
-  int second_ve;             // and the unit of its results
+  uint8_t second_ve[128];    // and the unit of its results
   uint8_t q_exp[2][2][128];  // exponents of the query rows' largest elements, by part's parity and tile
 };
 static_assert(sizeof(Control) <= Smem<128>::kControl, "control block");
@@ -260,6 +266,74 @@ __device__ __forceinline__ void rescale(uint32_t to, float f) {
   }
 }
 
+// The softmax of a block whose values are codes: what chunk8_kernel does with others, but for the row's unit, which is
+// that of the largest scale of the pages that it sees (to its `last` key of the block), and the scales on P.  Out of
+// line and of the loop over blocks: few are such, and a branch to it inside took a prompt of 8192 tokens from 419 to 488 us.
+struct RowState {
+  float m, l;  // maximum, sum of probabilities
+  int ve;      // unit of the results
+};
+template <int D>
+__device__ __noinline__ RowState scores_apart(const Attn8Params& p, Control& ctl, int w, int block, uint32_t ts, uint32_t to,
+                                              uint32_t tp, int last, float rowf, RowState row, bool first) {
+  const Block& b = ctl.blocks[block];
+  float x[32], top = -INFINITY;
+  int ve = row.ve;
+  // 32 scores; those of keys that the row does not see are -inf
+  const auto load = [&](int c) {
+    const int n = last + 1 - c;
+    uint32_t see = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
+    if (b.missing) see &= ~missing_keys(b.missing, c, p.page_shift);
+    tmem_ld32(ts + c, x);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] = see >> e & 1 ? x[e] : -INFINITY;
+  };
+  const auto factor = [&](int c, int e) { return fmaxf(b.ks[(c + e) >> p.page_shift] * rowf, 0x1p-126f); };
+#pragma unroll 1
+  for (int c = 0; c < 128; c += 32) {
+    load(c);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) top = fmaxf(top, x[e] * factor(c, e / 16 * 16));
+    if (c <= last) ve = max(ve, min((int)(__float_as_uint(b.vs[c >> p.page_shift]) >> 23 & 0xFF), 253));
+    if (c + 16 <= last) ve = max(ve, min((int)(__float_as_uint(b.vs[(c + 16) >> p.page_shift]) >> 23 & 0xFF), 253));
+  }
+  const bool far = first || top > row.m + 8.f;
+  if (!first && __any_sync(0xffffffffu, far || ve != row.ve)) {
+    const float f = far ? ex2(row.m - top) : 1.f;
+    row.l *= f;
+    rescale<D>(to, ve - row.ve > 126 ? 0.f : f * unit_of(127 + row.ve - ve));
+  }
+  if (far) row.m = top;
+  row.ve = ve;
+  const float mu = row.m == -INFINITY ? 0.f : kBias - row.m;
+#pragma unroll 1
+  for (int c = 0; c < 128; c += 32) {
+    uint32_t r[16];
+    load(c);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float f = factor(c, e / 8 * 16);
+      // (a page that the row does not see may have any scale: its P is zero)
+      const float v = fminf(b.vs[(c + e / 8 * 16) >> p.page_shift] * unit_of(254 - ve), 2.f);
+      const float a = ex2(fmaf(x[2 * e], f, mu)), d = ex2(fmaf(x[2 * e + 1], f, mu));
+      row.l += a + d;
+      r[e] = pack_f16(a * v, d * v);
+    }
+    tmem_st16(tp + c / 2, r);  // (over scores that have been read, where P lies there)
+    if (c & 32) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (threadIdx.x % 32 == 0) {
+        mbar_arrive(&ctl.p_full[w][c >> 6]);
+        if (D == 64 && c == 96) mbar_arrive(&ctl.s_free[w]);
+      }
+    }
+  }
+  return row;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk8_kernel(const __grid_constant__ Attn8Params p, const __grid_constant__ CUtensorMap qmap,
@@ -362,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait_phase(&ctl.v_empty[vst], ((blk / VS) & 1) ^ 1, &patience))) break;
         const Block& b = ctl.blocks[blk & 7];
         const int key = k * 128 + row;
-        const float rel = b.vs[min(row >> p.page_shift, 7)] * unit_of(254 - b.ve);
+        const float rel = b.apart ? 1.f : b.vs[min(row >> p.page_shift, 7)] * unit_of(254 - b.ve);
         const __half2 rel2 = __float2half2_rn(rel);
         // 16 codes of the row, from and to where the swizzles put them
         const uint32_t src = raw0 + rst * S::kCodes + row * D, dst = v0 + vst * S::kValues + row * 128;
@@ -531,11 +605,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             b.ks[lane] = ks;
             b.vs[lane] = vs;
           }
-          ve = max(ve, __reduce_max_sync(0xffffffffu, (int)(__float_as_uint(vs) >> 23 & 0xFF)));
+          const int e = (int)(__float_as_uint(vs) >> 23 & 0xFF);
+          ve = max(ve, __reduce_max_sync(0xffffffffu, e));
           ve = min(ve, 253);
+          const bool far = __any_sync(0xffffffffu, good && e != 0 && e + kFar < ve);
           if (lane == 0) {
             b.missing = miss;
             b.ve = ve;
+            b.apart = far && k * 128 + 128 > masked_from(s);
           }
           __syncwarp();
           if (lane == 0) {
@@ -738,17 +815,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim = min(s.ctx + tok, s.ctx + s.n - 1);  // the last key this row sees
       const int jm = ((s.ctx + t1 + 1) >> 7) - k0;          // the first block that the tile does not wholly see
       float m = -INFINITY, l = 0.f, rowf = 0.f;
-      int ve = 127;
+      int ve = 1;
       bool ok = true;
       // what is known of the next block, read while its scores are on their way
       float kf[8];
       uint32_t miss = 0;
-      int now = 127;
+      int now = 1, apart = 0;
       const auto look = [&](uint32_t n) {
         if (!wait_phase(&ctl.known[n & 7], (n >> 3) & 1, &patience)) return false;
         const Block& b = ctl.blocks[n & 7];
         miss = b.missing;
         now = b.ve;
+        apart = b.apart;
 #pragma unroll
         for (int e = 0; e < 8; ++e) kf[e] = b.ks[e >> per16];
         return true;
@@ -756,8 +834,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (nt > 0) ok = look(blk + first);
       const int fold_slot = s.slot >= 0 ? s.slot : 2 * (int)blockIdx.x + 1;
 #pragma unroll 1
-      for (int j = 0, stop = kFold; ok; stop += kFold) {
-        for (; j < min(nt, stop); ++j) {
+      for (int j = 0, stop = kFold; ok;) {
+        for (; j < min(nt, stop) && !apart; ++j) {
           if (!(ok = wait_phase(&ctl.s_full[w], ns & 1, &patience))) break;
           ++ns;
           tc_fence_after();
@@ -864,10 +942,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j + 1 < nt && !(ok = look(blk + jb + stride))) break;
         }
         if (!ok || j >= nt) break;
+        if (j < stop) {  // a block of codes
+          if (!(ok = wait_phase(&ctl.s_full[w], ns & 1, &patience))) break;
+          ++ns;
+          if (kApart && j > 0) {
+            if (!(ok = wait_phase(&ctl.o_done[w], no & 1, &patience))) break;
+            ++no;
+          }
+          tc_fence_after();
+          if (j == 0) rowf = p.scale * unit_of(max((int)ctl.q_exp[i & 1][w][row] - 7, 1));
+          const int jb = j * stride + first;
+          const RowState r = scores_apart<D>(p, ctl, w, (blk + jb) & 7, ts, to, tp, lim - (k0 + jb) * 128, rowf, {m, l, ve},
+                                             j == 0);
+          m = r.m;
+          l = r.l;
+          ve = r.ve;
+          ++np;
+          apart = 0;
+          if (++j < nt) ok = look(blk + jb + stride);
+          continue;
+        }
         // O is whole once the next scores are there (at D = 64, once its last product is done)
         if (!(ok = wait_phase(kApart ? &ctl.o_done[w] : &ctl.s_full[w], (kApart ? no : ns) & 1, &patience))) break;
         tc_fence_after();
         l = fold_results(p, D, fold_slot, w * 128 + row, to, m, l, unit_of(ve), mine, stop > kFold, false);
+        stop += kFold;
       }
       if (!ok) break;
       blk += s.k1 - k0;
@@ -885,7 +984,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float fa = unit_of(ve), fb = 0.f;
       if (split && w == 1) {
         ctl.ml[row] = make_float2(m, l);
-        if (row == 0) ctl.second_ve = ve;
+        ctl.second_ve[row] = (uint8_t)ve;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.second_done);
@@ -898,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = mn;
         l = l * f0 + other.y * f1;
         fa *= f0;
-        fb = unit_of(ctl.second_ve) * f1;
+        fb = unit_of(ctl.second_ve[row]) * f1;
       }
       const bool stores = mine && !(split && w == 1);
       const bool set_aside = nt > 0 && ctl.odd[sst];

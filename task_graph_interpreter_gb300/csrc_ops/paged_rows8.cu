@@ -16,7 +16,10 @@
 //   scales    of keys: one factor per 16 keys (a page has at least 16), with
 //             the row's and the softmax scale; of values: onto the
 //             probabilities, relative to the power of two of the largest scale
-//             so far, which the results carry
+//             so far, which the results carry (a tile 2^kFar and more below it is
+//             added to results in a smaller unit, or its probabilities would
+//             leave f16: a page that some rows do not see, or that has no
+//             weight, takes nothing from the others)
 //
 // Probabilities are kept times 2^14, and rounded to f16 (2^-11) once the
 // scale of the values is on them; what they are summed to is not rounded.  (Two
@@ -29,6 +32,8 @@
 // and the join.  One request of 4096 keys 13.5 us: two launches and eight
 // dependent round trips.  Up to two eights of rows run here (four requests of
 // 32768 keys and 12 rows 65 us); with three eights registers leave no room.
+#include <type_traits>
+
 #include "paged_attention.cuh"
 
 namespace mk {
@@ -37,6 +42,11 @@ namespace {
 using namespace ptx;
 
 constexpr float kBias = 14.f;                // probabilities are kept times 2^kBias
+// A tile whose scale is 2^kFar and more below the unit: nearer ones keep 2^-11 of probabilities down to 2^-13.
+constexpr int kFar = 15;
+// The results' unit goes down by 2^kMostDown at most: they are under 2^41 in it (kFoldKeys keys of at most 2 * 448 times
+// 2^kBias).
+constexpr int kMostDown = 60;
 constexpr int kStages8 = 3;
 constexpr int kSmemBytes8 = 1024 + kRowWarps8 * kStages8 * kRowBlockBytes8;
 static_assert(kSmemBytes8 <= 229376, "shared memory of a CTA, beside the static part");
@@ -52,6 +62,18 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return __vcmpeq4(w &
 
 // 2^(d) for d <= 0 (zero where it is not a normal number)
 __device__ __forceinline__ float exp2_down(int d) { return d < -126 ? 0.f : __uint_as_float((uint32_t)(127 + d) << 23); }
+
+__device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23 & 0xFF); }
+
+template <int NR, int N>
+__device__ __forceinline__ void times(float (&o)[NR][N][4], float f) {
+#pragma unroll
+  for (int h = 0; h < NR; ++h)
+#pragma unroll
+    for (int t = 0; t < N; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[h][t][e] *= f;
+}
 
 // NR: eights of query rows
 template <int D, int NR>
@@ -301,9 +323,13 @@ __global__ void __launch_bounds__(kRowWarps8 * 32, 1)
                 if (!((keys >> k) & 1) || key0 + k > lim[h][e & 1]) s[h][t][e] = -INFINITY;
               }
         }
-        int vmax = ve;
+        int vmax = ve, vmin = 254;
 #pragma unroll
-        for (int t = 0; t < NK; ++t) vmax = max(vmax, (int)(__float_as_uint(vsc[t]) >> 23 & 0xFF));
+        for (int t = 0; t < NK; ++t) {
+          const int e = exponent(vsc[t]);
+          vmax = max(vmax, e);
+          vmin = min(vmin, e == 0 ? 254 : e);  // (pages without keys have none)
+        }
         vmax = min(vmax, 253);
         bool moved = vmax != ve;
         float mnew[NR][2];
@@ -358,51 +384,63 @@ __global__ void __launch_bounds__(kRowWarps8 * 32, 1)
             }
           }
         bool bad_v = false;  // a value that is not finite behind a mask
+        // (APART: a tile's scale lies far below the unit; code of its own, as a branch per tile cost heads of 64 5 %)
+        const auto add_values = [&](auto APART) {
 #pragma unroll
-        for (int t = 0; t < NK; ++t) {
-          // probabilities as operands: 16 keys by 8 rows, transposed
-          const float vf = vsc[t] * vref;
-          uint32_t pr[NR][2];
+          for (int t = 0; t < NK; ++t) {
+            // probabilities as operands: 16 keys by 8 rows, transposed
+            float vf = vsc[t] * vref;
+            const int down = min(ve - exponent(vsc[t]), kMostDown);
+            if (APART.value) {
+              const float up = __uint_as_float((uint32_t)(127 + down) << 23);
+              vf *= up;
+              times(o, up);
+            }
+            uint32_t pr[NR][2];
 #pragma unroll
-          for (int h = 0; h < NR; ++h)
+            for (int h = 0; h < NR; ++h)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              pr[h][e] = movm_trans(pack_f16(s[h][t][2 * e] * vf, s[h][t][2 * e + 1] * vf));
-          // this lane's four keys of the 16: c0, c0 + 1, c0 + 8, c0 + 9
-          uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-          if (masked) {
-            const uint32_t k16 = (uint32_t)(keys >> (t * 16)) >> c0;
-            keep0 = ((k16 & 1) ? 0xFFFFu : 0u) | ((k16 & 2) ? 0xFFFF0000u : 0u);
-            keep1 = ((k16 & 0x100) ? 0xFFFFu : 0u) | ((k16 & 0x200) ? 0xFFFF0000u : 0u);
-          }
-#pragma unroll
-          for (int d = 0; d < D / 16; d += 2) {
-            // columns d * 16 .. + 31 of the 16 keys: columns 2 g and 2 g + 1 of each 16, of keys c0 and c0 + 1, then
-            // c0 + 8 and c0 + 9
-            uint32_t v[4];
-            ldsm4t(swz8<D>(vs, t * 16 + (lane & 15), d + (lane >> 4)), v);
+              for (int e = 0; e < 2; ++e)
+                pr[h][e] = movm_trans(pack_f16(s[h][t][2 * e] * vf, s[h][t][2 * e + 1] * vf));
+            // this lane's four keys of the 16: c0, c0 + 1, c0 + 8, c0 + 9
+            uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
             if (masked) {
-              // values that were not loaded are zero, whatever the memory held
-              v[0] &= keep0; v[1] &= keep1; v[2] &= keep0; v[3] &= keep1;
-              if (n > 1) {
+              const uint32_t k16 = (uint32_t)(keys >> (t * 16)) >> c0;
+              keep0 = ((k16 & 1) ? 0xFFFFu : 0u) | ((k16 & 2) ? 0xFFFF0000u : 0u);
+              keep1 = ((k16 & 0x100) ? 0xFFFFu : 0u) | ((k16 & 0x200) ? 0xFFFF0000u : 0u);
+            }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const uint32_t odd = nan_codes(v[e]);
-                  bad_v |= odd != 0;
-                  v[e] &= ~odd;
+            for (int d = 0; d < D / 16; d += 2) {
+              // columns d * 16 .. + 31 of the 16 keys: columns 2 g and 2 g + 1 of each 16, of keys c0 and c0 + 1, then
+              // c0 + 8 and c0 + 9
+              uint32_t v[4];
+              ldsm4t(swz8<D>(vs, t * 16 + (lane & 15), d + (lane >> 4)), v);
+              if (masked) {
+                // values that were not loaded are zero, whatever the memory held
+                v[0] &= keep0; v[1] &= keep1; v[2] &= keep0; v[3] &= keep1;
+                if (n > 1) {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const uint32_t odd = nan_codes(v[e]);
+                    bad_v |= odd != 0;
+                    v[e] &= ~odd;
+                  }
                 }
               }
-            }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint32_t a[4];
-              widen_e4m3(__byte_perm(v[2 * i], 0, 0x3120), a[0], a[1]);
-              widen_e4m3(__byte_perm(v[2 * i + 1], 0, 0x3120), a[2], a[3]);
+              for (int i = 0; i < 2; ++i) {
+                uint32_t a[4];
+                widen_e4m3(__byte_perm(v[2 * i], 0, 0x3120), a[0], a[1]);
+                widen_e4m3(__byte_perm(v[2 * i + 1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
-              for (int h = 0; h < NR; ++h) mma_f16(o[h][d + i], a, pr[h][0], pr[h][1]);
+                for (int h = 0; h < NR; ++h) mma_f16(o[h][d + i], a, pr[h][0], pr[h][1]);
+              }
             }
+            if (APART.value) times(o, exp2_down(-down));
           }
-        }
+        };
+        if (vmin + kFar < ve) add_values(std::true_type());
+        else add_values(std::false_type());
         if (masked && n > 1 && __any_sync(0xffffffffu, bad_v)) {
           // 0 * NaN would reach the rows that do not see the key: such values were left
           // out above and go to the rows that see it only

@@ -928,3 +928,52 @@ def test_a_gradient_or_a_tangent_is_refused():
                     f(*args)
         with torch.no_grad():
             f(grad(a), ks, vs)
+
+
+UNSEEN = [  # ctx, new, Hq, Hkv, D, page: pages begin among the new tokens
+    (30, 4, 4, 1, 128, 16), (30, 4, 4, 2, 64, 16), (63, 2, 8, 1, 128, 64), (310, 16, 3, 3, 64, 32), (30014, 4, 8, 2, 128, 16),
+    (200, 70, 4, 1, 128, 16), (200, 70, 4, 2, 64, 32), (100, 300, 8, 2, 128, 64), (30014, 6, 4, 1, 128, 16),
+    (30014, 6, 4, 1, 64, 32), (0, 500, 12, 12, 64, 16), (127, 128, 6, 2, 128, 128), (250, 20, 16, 1, 128, 256)]
+
+
+@pytest.mark.parametrize("far", [20, 60])
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D,page", UNSEEN)
+def test_large_values_of_pages_that_a_row_does_not_see_cost_it_nothing(ctx, new, Hq, Hkv, D, page, far):
+    """Values 2^20 and 2^60 times larger from some new token's page on: the rows before it are as exact as without them.
+    A key's probability loses 2^-39 (few rows) or 2^-31 (chunks) of the largest, times its value."""
+    q, k, v, ks, vs, table, cu = attention_case([ctx], [new], Hq, Hkv, D, page, 21)
+    first = min(-(-(ctx + max(1, new // 3)) // page), (ctx + new - 1) // page)  # the first large page
+    assert ctx // page < first
+    vs[table[0, first:-(-(ctx + new) // page)].long()] *= 2.0 ** far
+    got = paged.attention(q, k, v, table, i32(cu), i32([ctx]), new, kscale=ks, vscale=vs)
+    want, size, e, _ = attention_ref(q, k, v, ks, vs, table, cu, [ctx], page, D ** -0.5)
+    few = new * Hq // Hkv <= 16
+    top = 448 * torch.stack([vs[table[0, :(ctx + t) // page + 1].long()].amax(0) for t in range(new)])  # [new, Hkv]
+    top = top.double().repeat_interleave(Hq // Hkv, 1)[:, :, None]
+    tol = 2.0 ** -8 * want.abs() + 2 * e * size + (2.0 ** -39 if few else 2.0 ** -31) * (ctx + new) * top
+    err = (got.double() - want).abs()
+    assert bool((err <= tol).all()), f"max excess {float(((err - tol) / top).max())} of the largest value a row sees"
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_few_rows_keep_values_far_below_the_largest(D):
+    """A row sees keys without weight (scores 400 lower) whose values are 2^60 times those that count."""
+    ctx, new, Hq, Hkv, page = 500, 2, 4, 1, 16
+    q, k, v, ks, vs, table, cu = attention_case([ctx], [new], Hq, Hkv, D, page, 22)
+    ids = table[0, :32].long()
+    q.zero_()
+    q[:, :, 0] = 1.0
+    low = torch.zeros(32, dtype=torch.bool, device=DEV)
+    low[[0, 7, 8, 20]] = True
+    ks[ids] = 1.0
+    k.view(torch.uint8)[ids, 0, :, 0] = torch.where(low, -400.0, 0.0).to(E4M3).view(torch.uint8)[:, None]
+    vs[ids[low]] *= 2.0 ** 60
+    got = paged.attention(q, k, v, table, i32(cu), i32([ctx]), new, kscale=ks, vscale=vs, scale=1.0)
+    assert float(k[ids[low]][..., 0].float().max()) <= -384  # (2^-553 of the others)
+    seen = torch.stack([torch.arange(512, device=DEV) <= ctx + t for t in range(new)]).double()
+    w = seen * (~low).double().repeat_interleave(page)
+    w /= w.sum(-1, keepdim=True)
+    val = torch.nan_to_num((v.double() * vs.double()[:, :, None, None])[ids, 0].reshape(512, D)) * (w.sum(0) > 0)[:, None]
+    want, size = (w @ val)[:, None], (w @ val.abs())[:, None]
+    tol = 2.0 ** -8 * want.abs() + (2.0 ** -10 + D * 2.0 ** -22) * size
+    assert bool(((got.double() - want).abs() <= tol).all())
