@@ -977,3 +977,28 @@ def test_few_rows_keep_values_far_below_the_largest(D):
     want, size = (w @ val)[:, None], (w @ val.abs())[:, None]
     tol = 2.0 ** -8 * want.abs() + (2.0 ** -10 + D * 2.0 ** -22) * size
     assert bool(((got.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("bits", [22, 26, 30, 36])
+@pytest.mark.parametrize("new,D", [(1, 64), (2, 128), (5, 128), (5, 64)])
+def test_one_key_above_a_million_others(new, D, bits):
+    """A key whose weight is 2^22 to 2^36 times each other's, of which there are 2^20: f16 has few bits left of theirs, or
+    none.  Each loses 2^-39 of the largest (few rows) or 2^-31 (chunks) at most."""
+    ctx, Hq, Hkv, page = (1 << 20) - new, 4, 1, 64
+    pages = (ctx + new) // page
+    k = torch.zeros(pages, Hkv, page, D, device=DEV).to(E4M3)
+    v = torch.ones(pages, Hkv, page, D, device=DEV).to(E4M3)
+    k.view(torch.uint8)[777, 0, 5, 0] = torch.tensor(float(bits), device=DEV).to(E4M3).view(torch.uint8)
+    v.view(torch.uint8)[777, 0, 5] = 0
+    assert float(k[777, 0, 5, 0].float()) == bits
+    ones = torch.ones(pages, Hkv, device=DEV)
+    table = torch.randperm(pages, device=DEV).int()[None]
+    q = torch.zeros(new, Hq, D, dtype=torch.bfloat16, device=DEV)
+    q[:, :, 0] = 1
+    scale = 0.98 * math.log(2.0)  # (weights that are no powers of two)
+    got = paged.attention(q, k, v, table, i32([0, new]), i32([ctx]), new, kscale=ones, vscale=ones, scale=scale)
+    tail = torch.tensor([(ctx + t) * 2.0 ** (-0.98 * bits) for t in range(new)], dtype=torch.float64, device=DEV)
+    want = (tail / (1 + tail))[:, None, None]
+    e = 2.0 ** -11 + (bits + D + 4) * 2.0 ** -23
+    tol = 2.0 ** -8 * want + 2 * e * want + (1 << 20) * 2.0 ** (-39 if new * Hq <= 16 else -31)
+    assert bool(((got.double() - want).abs() <= tol).all())
