@@ -1002,3 +1002,28 @@ def test_one_key_above_a_million_others(new, D, bits):
     e = 2.0 ** -11 + (bits + D + 4) * 2.0 ** -23
     tol = 2.0 ** -8 * want + 2 * e * want + (1 << 20) * 2.0 ** (-39 if new * Hq <= 16 else -31)
     assert bool(((got.double() - want).abs() <= tol).all())
+
+
+def reordered(c, order):
+    index = torch.tensor(order, device=DEV)
+    return dict(c, qkv=c["qkv"][index], pos=[c["pos"][r] for r in order], slots=[c["slots"][r] for r in order])
+
+
+def test_a_slot_outside_the_pool_is_left_out_of_its_page_s_rows():
+    """The rows around it are stored as without it: together, at one scale."""
+    for ctx, n, Hkv in ((0, 8, 1), (5, 40, 2), (0, 800, 16)):
+        c = store_case([ctx], [n], 2 * Hkv, Hkv, 128, 32, F32, "qk", 31)
+        for bad in (10 ** 6, 2 ** 31 - 1, c["kpool"].shape[0] * 32):
+            order, left = [], set()
+            for r in range(n):
+                order.append(r)
+                if r % 5 == 2:  # a row that goes nowhere behind it
+                    left.add(len(order))
+                    order.append(r)
+            c2 = reordered(c, order)
+            c2["slots"] = [bad if i in left else s for i, s in enumerate(c2["slots"])]
+            status = i32([0])
+            out, *got = run_store(c2, 2 * Hkv, Hkv, 128, 32, check=False, status=status)
+            assert int(status) == L.MK_DEV_BAD_INDEX
+            _, *want = run_store(c, 2 * Hkv, Hkv, 128, 32)
+            assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
