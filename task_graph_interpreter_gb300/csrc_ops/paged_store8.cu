@@ -39,7 +39,7 @@ constexpr int kGap = 15;  // rows that are not stored which a run may have betwe
 struct Store8Params : NormParams {
   uint8_t *kcodes, *vcodes;
   float *kscale, *vscale;
-  unsigned kv_blocks;
+  unsigned checks, kv_blocks;  // blocks that look for pages of two runs; of keys and values
 };
 
 template <typename T>
@@ -208,6 +208,75 @@ __device__ __forceinline__ int stored_row(const Store8Params& p, int64_t r, int&
   const int slot = p.slots[r];
   pos = p.positions[r];
   return stored_slot(p, slot, pos);
+}
+
+// Two runs of a page would set its scale both, each for its own rows.  None of the blocks that store them sees the other,
+// so blocks of their own, beside those, enter the page of every row that begins a run in a table; a page that is there
+// already is reported.  Pages are dealt to the blocks, a block per kPartRows rows, and, should a table be full (many runs
+// of few rows), to several passes over the rows; a class of pages that 21 bits of the mixed number name fits for certain.
+// They end before the others do: calls take as long as without them.
+constexpr int kTable = 2048, kPartRows = 16384;
+struct Table {
+  int page[kTable];
+  int full;
+};
+template <int THREADS>
+__device__ __forceinline__ void check_runs(const Store8Params& p, Table& sm, unsigned part) {
+  constexpr int ROWS = 8;  // of a thread at a time, fewer where there are few
+  const int rows = min(ROWS, (p.N + THREADS - 1) / THREADS);
+  const auto enter = [&](int page, unsigned pass, unsigned passes) {
+    // mixed by odd factors (the fractions of the golden section and of the root of two) and a fold: different pages stay
+    // different
+    unsigned h = (unsigned)page * 0x9E3779B1u;
+    h ^= h >> 16;
+    h *= 0x6A09E667u;
+    h ^= h >> 15;
+    if (__umulhi(h, p.checks) != part || (h & (passes - 1)) != pass) return;
+    for (int i = 0; i < kTable; ++i) {
+      int& at = sm.page[((h >> 12) + i) % kTable];
+      const int was = at == page ? page : atomicCAS(&at, -1, page);
+      if (was == -1) return;
+      if (was == page) return set_status(p.status, MK_DEV_BAD_INDEX);
+    }
+    sm.full = 1;
+  };
+#pragma unroll 1
+  for (unsigned pass = 0, passes = 1; pass < passes;) {
+    for (int i = threadIdx.x; i < kTable; i += THREADS) sm.page[i] = -1;
+    if (threadIdx.x == 0) sm.full = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int64_t r0 = threadIdx.x * rows; r0 < p.N; r0 += THREADS * rows) {
+      int slot[ROWS + 1], pos[ROWS + 1], one;  // of the row before first
+#pragma unroll
+      for (int i = 0; i <= ROWS; ++i) {
+        const int64_t r = r0 - 1 + i;
+        const bool there = i <= rows && r >= 0 && r < p.N;
+        slot[i] = there ? p.slots[r] : -1;
+        pos[i] = there ? p.positions[r] : -1;
+      }
+#pragma unroll
+      for (int i = 0; i <= ROWS; ++i) slot[i] = stored_slot(p, slot[i], pos[i]);
+      int before = slot[0], gap = 0;  // of the nearest stored row before; rows between that are not
+#pragma unroll 1
+      while (before < 0 && ++gap <= kGap) before = stored_row(p, r0 - 1 - gap, one);
+#pragma unroll
+      for (int i = 1; i <= ROWS; ++i) {
+        if (slot[i] < 0) {
+          ++gap;
+          continue;
+        }
+        if (before < 0 || gap > kGap || (before ^ slot[i]) >> p.page_shift != 0) enter(slot[i] >> p.page_shift, pass, passes);
+        before = slot[i];
+        gap = 0;
+      }
+    }
+    __syncthreads();
+    const bool full = sm.full != 0;
+    __syncthreads();
+    pass = full ? 0 : pass + 1;
+    if (full) passes *= 2;
+  }
 }
 
 // The runs of a key or value head that begin in a window; the rows of a run go to one page, each at a higher offset than
@@ -543,29 +612,39 @@ template <typename T>
 constexpr int kMixedThreads = sizeof(T) == 4 ? 768 : 512;
 template <typename S>
 __global__ void __launch_bounds__(S::THREADS, kMixedThreads<typename S::T> / S::THREADS) store8_kernel(const __grid_constant__ Store8Params p) {
-  __shared__ union alignas(16) Both {
-    __device__ Both() {}
+  __shared__ union alignas(16) Any {
+    __device__ Any() {}
     Runs<S::WINDOW, S::D> runs;
     Turn<S::D> turns[kQueryMaxTokens];
+    Table table;
   } sm;
-  if (blockIdx.x < p.kv_blocks) store_runs<S>(p, sm.runs, blockIdx.x);
-  else queries<S>(p, sm.turns, blockIdx.x - p.kv_blocks);
+  const unsigned block = blockIdx.x;
+  if (block < p.checks) check_runs<S::THREADS>(p, sm.table, block);
+  else if (block < p.checks + p.kv_blocks) store_runs<S>(p, sm.runs, block - p.checks);
+  else queries<S>(p, sm.turns, block - p.checks - p.kv_blocks);
 }
 // Keys and values alone
 template <typename S>
 __global__ void __launch_bounds__(S::THREADS, kKvBlocks) store8_kv_kernel(const __grid_constant__ Store8Params p) {
-  __shared__ Runs<S::WINDOW, S::D> runs;
+  __shared__ union alignas(16) Either {
+    __device__ Either() {}
+    Runs<S::WINDOW, S::D> runs;
+    Table table;
+  } sm;
   ptx::launch_dependents();  // the queries' blocks follow as these end
-  store_runs<S>(p, runs, blockIdx.x);
+  if (blockIdx.x < p.checks) check_runs<S::THREADS>(p, sm.table, blockIdx.x);
+  else store_runs<S>(p, sm.runs, blockIdx.x - p.checks);
 }
 
 template <typename T, int D>
 cudaError_t launch_store8(Store8Params& p, int sms, cudaStream_t stream) {
   constexpr int E = kElems<T>, LPH = D / 2 / E;
+  // (two runs of a page have a row of another between them)
+  p.checks = p.status && p.N > 2 ? (unsigned)((p.N - 1) / kPartRows + 1) : 0;
   const auto kv_blocks = [&](int window) { return (unsigned)(((int64_t)p.N + window - 1) / window * 2 * p.Hkv); };
   if ((int64_t)p.N * 2 * p.Hkv * LPH > kFewLanes) {
     using S = Shape<T, D, kKvThreads, kKvWindow, kKvWindow / (kKvThreads / LPH)>;
-    store8_kv_kernel<S><<<kv_blocks(S::WINDOW), S::THREADS, 0, stream>>>(p);
+    store8_kv_kernel<S><<<p.checks + kv_blocks(S::WINDOW), S::THREADS, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_queries(p, sizeof(T) == 4 ? MK_F32 : MK_BF16, D, sms, stream);
@@ -578,7 +657,7 @@ cudaError_t launch_store8(Store8Params& p, int sms, cudaStream_t stream) {
   while (p.tokens > 1 && (p.N + p.tokens - 1) / p.tokens < 2 * sms) p.tokens /= 2;
   p.splits = p.N < sms ? (p.Hq + GP - 1) / GP : 1;
   p.kv_blocks = kv_blocks(S::WINDOW);
-  const unsigned blocks = p.kv_blocks + (unsigned)((p.N + p.tokens - 1) / p.tokens * p.splits);
+  const unsigned blocks = p.checks + p.kv_blocks + (unsigned)((p.N + p.tokens - 1) / p.tokens * p.splits);
   store8_kernel<S><<<blocks, S::THREADS, 0, stream>>>(p);
   return cudaGetLastError();
 }
@@ -599,7 +678,7 @@ extern "C" int mk_qk_norm_rope_e4m3(void* stream, int N, int Hq, int Hkv, int D,
     return rc;
   if (!kscale || !vscale) return fail(MK_ERR_ARG, "mk_qk_norm_rope_e4m3: null argument");
   // (blocks of a launch)
-  if (((int64_t)N + 63) / 64 * 2 * Hkv > INT32_MAX || (int64_t)N * ((Hq + 2 * Hkv) / 8 + 1) > INT32_MAX)
+  if (((int64_t)N + 63) / 64 * 2 * Hkv + N / kPartRows + 1 > INT32_MAX || (int64_t)N * ((Hq + 2 * Hkv) / 8 + 1) > INT32_MAX)
     return fail(MK_ERR_LIMIT, "mk_qk_norm_rope_e4m3: too many rows");
   if (int rc = pending_error(who)) return rc;
   if (N == 0) return MK_OK;

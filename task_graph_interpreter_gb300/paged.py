@@ -85,8 +85,9 @@ def qk_norm_rope(qkv, Hq: int, Hkv: int, D: int, positions, slots, kpool, vpool,
     power of two s with max |x| <= 448 s, set by the call that stores its first
     token and raised by later ones, when what the page holds is rounded to the
     larger scale.  A page's new tokens are neighbouring rows in ascending order,
-    as ``plan`` makes them; rows that go back in a page are not stored
-    (MK_DEV_BAD_INDEX).  Values that are not finite are stored as NaN."""
+    as ``plan`` makes them; rows that go back in a page are not stored, and a
+    page whose rows lie apart, with another's between them, holds anything
+    (MK_DEV_BAD_INDEX both).  Values that are not finite are stored as NaN."""
     args = (qkv, Hq, Hkv, D, positions, slots, kpool, vpool, q_gamma, k_gamma, eps, rope_theta, out, status, kscale,
             vscale)
     return L.calls().qk_norm_rope(*args) if stream is None else on_stream(L.calls().qk_norm_rope, stream, args)

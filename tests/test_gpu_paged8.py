@@ -1027,3 +1027,71 @@ def test_a_slot_outside_the_pool_is_left_out_of_its_page_s_rows():
             assert int(status) == L.MK_DEV_BAD_INDEX
             _, *want = run_store(c, 2 * Hkv, Hkv, 128, 32)
             assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
+
+
+TWO_RUNS = [  # requests' tokens, where the last rows of the first one's page go, heads, page
+    ([4, 4], 8, 1, 16), ([9, 30, 30], 69, 2, 16), ([20, 300], 320, 1, 32), ([3, 30, 1100], 500, 16, 64), ([3, 30, 1100], 1133, 16, 16),
+    ([100, 100] * 12, 2400, 8, 128)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("new,to,Hkv,page", TWO_RUNS)
+def test_a_page_whose_rows_lie_apart_is_reported_and_others_are_stored(new, to, Hkv, page, dtype):
+    Hq, D = 2 * Hkv, 64
+    c = store_case([0] * len(new), new, Hq, Hkv, D, page, dtype, "qk", 33)
+    n = len(c["slots"])
+    cut = min(new[0], page) - 2  # the first page's last two rows
+    rest = [r for r in range(n) if r not in (cut, cut + 1)]
+    at = to - 2
+    assert at > cut and c["slots"][rest[at - 1]] // page != c["slots"][0] // page
+    apart = reordered(c, rest[:at] + [cut, cut + 1] + rest[at:])
+    status = i32([0])
+    out, *got = run_store(apart, Hq, Hkv, D, page, check=False, status=status)
+    assert int(status) == L.MK_DEV_BAD_INDEX
+    # every other page as in the right order; one that the moved rows cut in two may be reported too
+    want_out, *want = run_store(c, Hq, Hkv, D, page)
+    cut_page = {c["slots"][rest[at - 1]] // page} & {c["slots"][r] // page for r in rest[at:at + 1]}
+    others = [pg for pg in range(c["kpool"].shape[0]) if pg != c["slots"][0] // page and pg not in cut_page]
+    assert all(torch.equal(a.view(torch.uint8)[others], b.view(torch.uint8)[others]) for a, b in zip(got, want))
+    inverse = torch.tensor(rest[:at] + [cut, cut + 1] + rest[at:], device=DEV).argsort()
+    assert torch.equal(out[inverse], want_out)
+
+
+@pytest.mark.parametrize("n,Hkv", [(40, 1), (300, 1), (1500, 8), (5000, 1), (5000, 16), (20000, 1), (40000, 4)])
+def test_runs_of_one_row_in_many_pages(n, Hkv):
+    """Each row in a page of its own: nothing is reported; then one page comes twice, far apart or behind 16 rows that
+    are not stored."""
+    D, page = 64, 16
+    g = torch.Generator(device=DEV).manual_seed(n)
+    slots = torch.randperm(n + 5, device=DEV, generator=g)[:n].int() * page + 3
+    qkv = torch.randn(n, 3 * Hkv * D, device=DEV, generator=g).bfloat16()
+    pos = torch.full((n,), 3, dtype=torch.int32, device=DEV)
+    pools = [torch.zeros(n + 5, Hkv, page, D, device=DEV).to(E4M3) for _ in range(2)]
+    scales = [torch.full((n + 5, Hkv), 2.0 ** -20, device=DEV) for _ in range(2)]
+
+    def run(slots, pos):
+        status = i32([0])
+        paged.qk_norm_rope(qkv, Hkv, Hkv, D, pos, slots, *pools, kscale=scales[0], vscale=scales[1], status=status)
+        return int(status)
+    assert run(slots, pos) == 0
+    v = qkv.view(n, 3, Hkv, D)[:, 2].double()
+    want = pow2_scale(v.abs().amax(-1))
+    at = slots.long() // page
+    assert torch.equal(scales[1][at].double(), want)
+    assert torch.equal(pools[1][at][:, :, 3].double(), e4m3(v / want[..., None]))
+    for a, b in ((0, n - 1), (n // 2, n // 2 + 2), (n - 3, n - 1)):
+        again = slots.clone()
+        again[b] = slots[a] + 1
+        assert run(again, pos) == L.MK_DEV_BAD_INDEX
+    gap = slots.clone()
+    gap[-17:] = -1
+    gap[-1] = gap[-18] + 1      # behind 16 rows that are not stored
+    assert run(gap, pos) == L.MK_DEV_BAD_INDEX
+    gap[-2] = gap[-18] + 1      # behind 15: one run
+    gap[-1] = -1
+    assert run(gap, pos) == 0
+    none = pos.clone()
+    none[n // 3:n // 3 + 20] = -1  # rows that are left out have no page
+    again = slots.clone()
+    again[n // 3:n // 3 + 20] = slots[0]
+    assert run(again, none) == 0
