@@ -40,6 +40,7 @@ struct Store8Params : NormParams {
   uint8_t *kcodes, *vcodes;
   float *kscale, *vscale;
   unsigned checks, kv_blocks;  // blocks that look for pages of two runs; of keys and values
+  bool behind;                 // beside a launch that does so: the last block ends behind it
 };
 
 template <typename T>
@@ -211,71 +212,49 @@ __device__ __forceinline__ int stored_row(const Store8Params& p, int64_t r, int&
 }
 
 // Two runs of a page would set its scale both, each for its own rows.  None of the blocks that store them sees the other,
-// so blocks of their own, beside those, enter the page of every row that begins a run in a table; a page that is there
-// already is reported.  Pages are dealt to the blocks, a block per kPartRows rows, and, should a table be full (many runs
-// of few rows), to several passes over the rows; a class of pages that 21 bits of the mixed number name fits for certain.
-// They end before the others do: calls take as long as without them.
-constexpr int kTable = 2048, kPartRows = 16384;
-struct Table {
-  int page[kTable];
-  int full;
+// so blocks of their own, before those, look at all rows and mark the page of each that begins a run in a bitmap; a page
+// that is marked already is reported.  A block per kSeen pages of the pool.  These blocks are short while a thread has few
+// rows; a call of more has them in a launch of their own with more threads, and the stores beside it.
+constexpr int kSeen = 65536;
+struct Seen {
+  unsigned bits[kSeen / 32];
 };
+// Row r goes to `slot`; `before`: the slot of the row before, where that is stored.
+__device__ __forceinline__ void mark_run(const Store8Params& p, Seen& sm, int first, int64_t r, int slot, int before) {
+  if (slot < 0) return;
+  if (before < 0) {
+    int pos;
+#pragma unroll 1
+    for (int i = 2; i <= kGap + 1 && before < 0; ++i) before = stored_row(p, r - i, pos);
+  }
+  if (before >= 0 && (before ^ slot) >> p.page_shift == 0) return;  // goes on
+  const unsigned at = (unsigned)((slot >> p.page_shift) - first);
+  if (at < kSeen && (atomicOr(&sm.bits[at / 32], 1u << (at % 32)) >> (at % 32) & 1)) set_status(p.status, MK_DEV_BAD_INDEX);
+}
 template <int THREADS>
-__device__ __forceinline__ void check_runs(const Store8Params& p, Table& sm, unsigned part) {
-  constexpr int ROWS = 8;  // of a thread at a time, fewer where there are few
-  const int rows = min(ROWS, (p.N + THREADS - 1) / THREADS);
-  const auto enter = [&](int page, unsigned pass, unsigned passes) {
-    // mixed by odd factors (the fractions of the golden section and of the root of two) and a fold: different pages stay
-    // different
-    unsigned h = (unsigned)page * 0x9E3779B1u;
-    h ^= h >> 16;
-    h *= 0x6A09E667u;
-    h ^= h >> 15;
-    if (__umulhi(h, p.checks) != part || (h & (passes - 1)) != pass) return;
-    for (int i = 0; i < kTable; ++i) {
-      int& at = sm.page[((h >> 12) + i) % kTable];
-      const int was = at == page ? page : atomicCAS(&at, -1, page);
-      if (was == -1) return;
-      if (was == page) return set_status(p.status, MK_DEV_BAD_INDEX);
+__device__ __forceinline__ void check_runs(const Store8Params& p, Seen& sm, unsigned part) {
+  constexpr unsigned AHEAD = 4;  // rows of a thread on their way
+  const int first = (int)part * kSeen;
+  const unsigned lane = threadIdx.x % 32, n = p.N;
+  for (int i = threadIdx.x; i < kSeen / 32; i += THREADS) sm.bits[i] = 0;
+  __syncthreads();
+#pragma unroll 1
+  for (unsigned base = threadIdx.x - lane; base < n; base += AHEAD * THREADS) {
+    int slot[AHEAD][2], pos[AHEAD][2];  // of a row, and of the one before
+#pragma unroll
+    for (unsigned k = 0; k < AHEAD; ++k) {
+      const unsigned r = min(base + k * THREADS + lane, n - 1), before = r > 0 ? r - 1 : 0;
+      slot[k][0] = p.slots[r];
+      pos[k][0] = p.positions[r];
+      slot[k][1] = p.slots[before];
+      pos[k][1] = p.positions[before];
     }
-    sm.full = 1;
-  };
-#pragma unroll 1
-  for (unsigned pass = 0, passes = 1; pass < passes;) {
-    for (int i = threadIdx.x; i < kTable; i += THREADS) sm.page[i] = -1;
-    if (threadIdx.x == 0) sm.full = 0;
-    __syncthreads();
-#pragma unroll 1
-    for (int64_t r0 = threadIdx.x * rows; r0 < p.N; r0 += THREADS * rows) {
-      int slot[ROWS + 1], pos[ROWS + 1], one;  // of the row before first
 #pragma unroll
-      for (int i = 0; i <= ROWS; ++i) {
-        const int64_t r = r0 - 1 + i;
-        const bool there = i <= rows && r >= 0 && r < p.N;
-        slot[i] = there ? p.slots[r] : -1;
-        pos[i] = there ? p.positions[r] : -1;
-      }
-#pragma unroll
-      for (int i = 0; i <= ROWS; ++i) slot[i] = stored_slot(p, slot[i], pos[i]);
-      int before = slot[0], gap = 0;  // of the nearest stored row before; rows between that are not
-#pragma unroll 1
-      while (before < 0 && ++gap <= kGap) before = stored_row(p, r0 - 1 - gap, one);
-#pragma unroll
-      for (int i = 1; i <= ROWS; ++i) {
-        if (slot[i] < 0) {
-          ++gap;
-          continue;
-        }
-        if (before < 0 || gap > kGap || (before ^ slot[i]) >> p.page_shift != 0) enter(slot[i] >> p.page_shift, pass, passes);
-        before = slot[i];
-        gap = 0;
-      }
+    for (unsigned k = 0; k < AHEAD; ++k) {
+      const unsigned r = base + k * THREADS + lane;
+      if (r < n)
+        mark_run(p, sm, first, r, stored_slot(p, slot[k][0], pos[k][0]), r > 0 ? stored_slot(p, slot[k][1], pos[k][1]) : -1);
     }
-    __syncthreads();
-    const bool full = sm.full != 0;
-    __syncthreads();
-    pass = full ? 0 : pass + 1;
-    if (full) passes *= 2;
   }
 }
 
@@ -616,12 +595,13 @@ __global__ void __launch_bounds__(S::THREADS, kMixedThreads<typename S::T> / S::
     __device__ Any() {}
     Runs<S::WINDOW, S::D> runs;
     Turn<S::D> turns[kQueryMaxTokens];
-    Table table;
+    Seen seen;
   } sm;
   const unsigned block = blockIdx.x;
-  if (block < p.checks) check_runs<S::THREADS>(p, sm.table, block);
+  if (block < p.checks) check_runs<S::THREADS>(p, sm.seen, block);
   else if (block < p.checks + p.kv_blocks) store_runs<S>(p, sm.runs, block - p.checks);
   else queries<S>(p, sm.turns, block - p.checks - p.kv_blocks);
+  if (p.behind && block == gridDim.x - 1) ptx::wait_dependency();
 }
 // Keys and values alone
 template <typename S>
@@ -629,23 +609,49 @@ __global__ void __launch_bounds__(S::THREADS, kKvBlocks) store8_kv_kernel(const 
   __shared__ union alignas(16) Either {
     __device__ Either() {}
     Runs<S::WINDOW, S::D> runs;
-    Table table;
+    Seen seen;
   } sm;
   ptx::launch_dependents();  // the queries' blocks follow as these end
-  if (blockIdx.x < p.checks) check_runs<S::THREADS>(p, sm.table, blockIdx.x);
+  if (blockIdx.x < p.checks) check_runs<S::THREADS>(p, sm.seen, blockIdx.x);
   else store_runs<S>(p, sm.runs, blockIdx.x - p.checks);
+  if (p.behind && blockIdx.x == gridDim.x - 1) ptx::wait_dependency();
 }
+constexpr int kCheckThreads = 1024;
+__global__ void __launch_bounds__(kCheckThreads, 1) check8_kernel(const __grid_constant__ Store8Params p) {
+  __shared__ Seen seen;
+  ptx::launch_dependents();  // the stores' blocks follow
+  check_runs<kCheckThreads>(p, seen, blockIdx.x);
+}
+
+// Rows of a thread (windows of 16) and of a call (windows of 64) up to which the stores' launch looks for pages of two
+// runs, in the time that the stores take anyway.  In it and in a launch of its own: 1024 tokens of 32/4 heads of 64 6.5 and
+// 7.0 us, 1536 8.3 and 7.4 (6.5 without looking); 2000 requests of one head 8.6 and 5.1; 16000 tokens of one head 37 and
+// 11.8 (10.5 without).  60000 tokens of 8/2 heads 93 us in a launch of its own.
+constexpr int kCheckRows = 16, kKvCheckRows = 16384;
 
 template <typename T, int D>
 cudaError_t launch_store8(Store8Params& p, int sms, cudaStream_t stream) {
   constexpr int E = kElems<T>, LPH = D / 2 / E;
-  // (two runs of a page have a row of another between them)
-  p.checks = p.status && p.N > 2 ? (unsigned)((p.N - 1) / kPartRows + 1) : 0;
   const auto kv_blocks = [&](int window) { return (unsigned)(((int64_t)p.N + window - 1) / window * 2 * p.Hkv); };
+  // the blocks that look for pages of two runs: with the stores up to `rows` of a thread (two runs of a page have a row of
+  // another between them)
+  const auto checks = [&](int rows) {
+    p.checks = p.status && p.N > 2 ? (unsigned)((p.num_pages - 1) / kSeen + 1) : 0;
+    p.behind = p.checks > 0 && p.N > rows;
+    if (!p.behind) return cudaSuccess;
+    check8_kernel<<<p.checks, kCheckThreads, 0, stream>>>(p);
+    p.checks = 0;
+    return cudaGetLastError();
+  };
+  const auto launch = [&](auto* kernel, unsigned blocks, int threads) {
+    if (p.behind) return launch_early(kernel, dim3(blocks), dim3(threads), 0, stream, p);
+    kernel<<<blocks, threads, 0, stream>>>(p);
+    return cudaGetLastError();
+  };
   if ((int64_t)p.N * 2 * p.Hkv * LPH > kFewLanes) {
     using S = Shape<T, D, kKvThreads, kKvWindow, kKvWindow / (kKvThreads / LPH)>;
-    store8_kv_kernel<S><<<p.checks + kv_blocks(S::WINDOW), S::THREADS, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    cudaError_t e = checks(kKvCheckRows);
+    if (e == cudaSuccess) e = launch(store8_kv_kernel<S>, p.checks + kv_blocks(S::WINDOW), S::THREADS);
     if (e != cudaSuccess) return e;
     return launch_queries(p, sizeof(T) == 4 ? MK_F32 : MK_BF16, D, sms, stream);
   }
@@ -656,10 +662,10 @@ cudaError_t launch_store8(Store8Params& p, int sms, cudaStream_t stream) {
   while (p.tokens < kQueryMaxTokens && 2 * p.tokens * p.Hq <= kQueryBatch * GP) p.tokens *= 2;
   while (p.tokens > 1 && (p.N + p.tokens - 1) / p.tokens < 2 * sms) p.tokens /= 2;
   p.splits = p.N < sms ? (p.Hq + GP - 1) / GP : 1;
+  if (const cudaError_t e = checks(kCheckRows * S::THREADS); e != cudaSuccess) return e;
   p.kv_blocks = kv_blocks(S::WINDOW);
   const unsigned blocks = p.checks + p.kv_blocks + (unsigned)((p.N + p.tokens - 1) / p.tokens * p.splits);
-  store8_kernel<S><<<blocks, S::THREADS, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch(store8_kernel<S>, blocks, S::THREADS);
 }
 
 }  // namespace
@@ -678,7 +684,7 @@ extern "C" int mk_qk_norm_rope_e4m3(void* stream, int N, int Hq, int Hkv, int D,
     return rc;
   if (!kscale || !vscale) return fail(MK_ERR_ARG, "mk_qk_norm_rope_e4m3: null argument");
   // (blocks of a launch)
-  if (((int64_t)N + 63) / 64 * 2 * Hkv + N / kPartRows + 1 > INT32_MAX || (int64_t)N * ((Hq + 2 * Hkv) / 8 + 1) > INT32_MAX)
+  if (((int64_t)N + 63) / 64 * 2 * Hkv + num_pages / kSeen + 1 > INT32_MAX || (int64_t)N * ((Hq + 2 * Hkv) / 8 + 1) > INT32_MAX)
     return fail(MK_ERR_LIMIT, "mk_qk_norm_rope_e4m3: too many rows");
   if (int rc = pending_error(who)) return rc;
   if (N == 0) return MK_OK;

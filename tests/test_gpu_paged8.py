@@ -1095,3 +1095,62 @@ def test_runs_of_one_row_in_many_pages(n, Hkv):
     again = slots.clone()
     again[n // 3:n // 3 + 20] = slots[0]
     assert run(again, none) == 0
+
+
+@pytest.mark.parametrize("pages", [65536, 65537, 200000])
+def test_runs_in_pools_of_many_pages(pages):
+    n, D, page = 700, 64, 16
+    at = torch.linspace(0, pages - 1, n, device=DEV).int()  # the first and the last page among them
+    assert torch.unique(at).numel() == n
+    pools = [torch.zeros(pages, 1, page, D, device=DEV, dtype=torch.uint8).view(E4M3) for _ in range(2)]
+    scales = [torch.full((pages, 1), 2.0 ** -20, device=DEV) for _ in range(2)]
+    qkv = torch.randn(n, 3 * D, device=DEV).bfloat16()
+    pos = torch.zeros(n, dtype=torch.int32, device=DEV)
+    for row, to in ((None, None), (n - 1, 0), (5, n - 1), (300, 400)):
+        slots = at * page
+        if row is not None:
+            slots[row] = slots[to] + 1
+        status = i32([0])
+        paged.qk_norm_rope(qkv, 1, 1, D, pos, slots, *pools, kscale=scales[0], vscale=scales[1], status=status)
+        assert int(status) == (0 if row is None else L.MK_DEV_BAD_INDEX)
+
+
+@pytest.mark.parametrize("n,Hkv", [(500, 1), (3000, 1), (2000, 16), (20000, 6)])
+def test_captured_stores_report_a_page_of_two_runs_on_replay(n, Hkv):
+    """Each way of looking for such pages, captured behind what makes its inputs and ahead of what reads its results."""
+    D, page = 64, 16
+    pages = n // 4 + 2
+    c = [torch.zeros(pages, Hkv, page, D, device=DEV, dtype=torch.uint8).view(E4M3) for _ in range(2)]
+    scales = [torch.ones(pages, Hkv, device=DEV) for _ in range(2)]
+    source, qkv = (torch.randn(n, 3 * Hkv * D, device=DEV).bfloat16() for _ in range(2))
+    pos = torch.arange(n, device=DEV).int()
+    good = (torch.arange(n, device=DEV) // 4 * page + torch.arange(n, device=DEV) % 4).int()  # four rows a page
+    slots, status, out = good.clone(), i32([0]), torch.empty(n, Hkv, D, dtype=torch.bfloat16, device=DEV)
+    code, sum_ = i32([0]), torch.zeros(1, device=DEV)
+
+    def step():
+        qkv.copy_(source)
+        for pool in c:  # (a step with a wrong slot leaves what later ones do not write)
+            pool.view(torch.uint8).zero_()
+        status.zero_()
+        paged.qk_norm_rope(qkv, Hkv, Hkv, D, pos, slots, *c, kscale=scales[0], vscale=scales[1], out=out, status=status)
+        code.copy_(status)
+        sum_.copy_(c[1].view(torch.uint8).float().sum() + out.float().sum())
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for again in range(3):
+        source.normal_()
+        slots.copy_(good)
+        graph.replay()
+        assert int(code) == 0
+        want, got = [t.clone() for t in c + scales] + [out.clone()], sum_.clone()
+        slots.copy_(good)
+        slots[n - 1] = good[4 * again] + 5
+        graph.replay()
+        assert int(code) == L.MK_DEV_BAD_INDEX
+        slots.copy_(good)
+        step()
+        assert int(code) == 0 and torch.equal(sum_, got)
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(want, c + scales + [out]))
