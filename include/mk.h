@@ -563,17 +563,19 @@ int mk_paged_attention_workspace(int max_new, int Hq, int Hkv, int D, size_t* by
  * power of two (2^-126 at least) with max |x| <= 448 s.  A page whose first token
  * (offset 0) is among the new ones gets the scale s; a page that is begun keeps its
  * scale if that is at least s, else what it holds at offsets below its last new one
- * is rounded to s.  x / scale is rounded to e4m3, to nearest; a value that is not
- * finite is stored as NaN.  The new tokens of a page are to be in ascending order in
- * rows that follow one another (as mk_paged_plan makes them), with at most 15 rows
- * between them that are not stored; a row that comes back to its predecessor's page
- * at no higher offset is not stored, nor what follows it there (MK_DEV_BAD_INDEX).
- * The rows of a call that go to a page are to be of one such run (mk_qk_norm_rope
- * takes them in any order): a page whose rows form more than one, with rows of other
- * pages or more than 15 that are not stored between them, is reported
- * (MK_DEV_BAD_INDEX), and what it and its scales hold then is not defined; other pages
- * are stored as they should be.  A slot outside the pool is left out and reported, as
- * there.  Queries, norms and rotation as in mk_qk_norm_rope. */
+ * is rounded to s (exactly but for codes that become subnormal); a scale that a
+ * token raised stays when the token is rejected later.  x / scale is rounded to
+ * e4m3, to nearest; a value that is not finite is stored as NaN.  The new tokens of
+ * a page are to be in ascending order in rows that follow one another (as
+ * mk_paged_plan makes them), with at most 15 rows between them that are not stored;
+ * a row that comes back to its predecessor's page at no higher offset is not
+ * stored, nor what follows it there (MK_DEV_BAD_INDEX). The rows of a call that go
+ * to a page are to be of one such run (mk_qk_norm_rope takes them in any order): a
+ * page whose rows form more than one, with rows of other pages or more than 15 that
+ * are not stored between them, is reported (MK_DEV_BAD_INDEX), and what it and its
+ * scales hold then is not defined; other pages are stored as they should be.  A
+ * slot outside the pool is left out and reported, as there.  Queries, norms and
+ * rotation as in mk_qk_norm_rope. */
 int mk_qk_norm_rope_e4m3(void* stream, int N, int Hq, int Hkv, int D, const void* qkv, int qkv_dtype, int64_t ld_qkv,
                          const void* q_gamma, const void* k_gamma, float eps, double rope_theta,
                          const int32_t* positions, const int32_t* slots, void* q_out, int64_t ld_q, void* kpool,

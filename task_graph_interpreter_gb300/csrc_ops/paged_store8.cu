@@ -6,9 +6,11 @@
 //
 // over the page's new tokens and, where the page is begun (its first token is not
 // among them), s at least its old scale; if that grows, what the page holds is
-// rounded to the new one, e4m3(code s_old / s).  A power of two makes that exact but for codes that
-// become subnormal, and a stored value does not depend on the steps in which
-// the page was filled.
+// rounded to the new one, e4m3(code s_old / s).  A power of two makes that exact but
+// for codes that become subnormal, which are rounded twice then: others do not depend
+// on the steps in which the page was filled.  A scale does not go down again before
+// the page's first token is stored anew: one that a rejected draft raised stays, and
+// what it rounded.
 //
 // Bound by bytes, as the bf16 form is (paged.cu): activations are read once,
 // queries written in 16 bits, keys and values in 8.  A page's maximum has to

@@ -138,7 +138,8 @@ class PagedCache:
     another: the caller orders a step on another stream behind both.
 
     ``dtype`` torch.float8_e4m3fn holds it in 8 bits, with ``kscale`` and
-    ``vscale`` [num_pages, Hkv] per layer (None in 16 bits)."""
+    ``vscale`` [num_pages, Hkv] per layer (None in 16 bits).  A page's scale
+    that a rejected draft raised stays until the page is begun anew."""
 
     def __init__(self, layers: int, num_pages: int, page_size: int, Hkv: int, D: int, max_requests: int,
                  max_pages: int, max_tokens: int, device="cuda", dtype=torch.bfloat16):

@@ -1154,3 +1154,17 @@ def test_captured_stores_report_a_page_of_two_runs_on_replay(n, Hkv):
         step()
         assert int(code) == 0 and torch.equal(sum_, got)
         assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(want, c + scales + [out]))
+
+
+def test_a_scale_that_a_rejected_draft_raised_stays_until_the_page_is_begun_anew():
+    c = store_case([3], [3], 2, 1, 64, 16, F32, "", 41)
+    c["qkv"][2] *= 2.0 ** 12  # the draft
+    after = run_store(c, 2, 1, 64, 16)
+    base = c["slots"][0] - 3
+    pg = base // 16
+    step = dict(c, qkv=c["qkv"][:1] * 0.5, pos=[5], slots=[base + 5], **dict(zip(("kpool", "vpool", "kscale", "vscale"), after[1:])))
+    out, kp, vp, ks, vs = run_store(step, 2, 1, 64, 16)  # another token in its place
+    assert torch.equal(ks[pg], after[3][pg]) and torch.equal(vs[pg], after[4][pg])
+    first = dict(step, pos=[0], slots=[base])            # the page's first token
+    out, kp, vp, ks, vs = run_store(first, 2, 1, 64, 16)
+    assert bool((ks[pg] * 2 ** 9 <= after[3][pg]).all()) and bool((vs[pg] * 2 ** 9 <= after[4][pg]).all())
