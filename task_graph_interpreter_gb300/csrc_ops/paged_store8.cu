@@ -22,13 +22,14 @@
 // read again), each lane turns its pairs itself, and one warp finds the runs
 // while the rows are on their way, so the block meets three times.
 //
-// A prompt of 8192 tokens, 8/32 heads of 128, bf16: 51 us, of which queries
-// are 24.5 (5.5 TB/s) and keys and values 26, where bytes alone would take 8:
+// A prompt of 8192 tokens, 8/32 heads of 128, bf16: 49 us, of which queries
+// are 24.5 (5.5 TB/s) and keys and values the rest, where bytes alone would take 8
+// (f32: 60.5 of 43):
 // a third of the warps' time is the three meetings, a third the rows' first
 // arrival.  Measured on the way: angles shared by a row's heads in shared memory
 // 38 us for keys and values (more meetings), a warp alone per window and head,
-// without any, 14 us for each of its runs of 64 rows.  One token 3.8 us, 64
-// tokens of as many requests 4.2 us: the chain positions, runs, rows, store.
+// without any, 14 us for each of its runs of 64 rows.  One token 4.0 us, 64
+// tokens of as many requests 4.3 us: the chain positions, runs, rows, store.
 #include <cuda_fp16.h>
 
 #include "paged_norm.cuh"
@@ -42,7 +43,6 @@ struct Store8Params : NormParams {
   uint8_t *kcodes, *vcodes;
   float *kscale, *vscale;
   unsigned checks, kv_blocks;  // blocks that look for pages of two runs; of keys and values
-  bool behind;                 // beside a launch that does so: the last block ends behind it
 };
 
 template <typename T>
@@ -233,8 +233,9 @@ __device__ __forceinline__ void mark_run(const Store8Params& p, Seen& sm, int fi
   const unsigned at = (unsigned)((slot >> p.page_shift) - first);
   if (at < kSeen && (atomicOr(&sm.bits[at / 32], 1u << (at % 32)) >> (at % 32) & 1)) set_status(p.status, MK_DEV_BAD_INDEX);
 }
+// (Out of line: inlined, 777 mixed rows took 7.4 us for 7.2.)
 template <int THREADS>
-__device__ __forceinline__ void check_runs(const Store8Params& p, Seen& sm, unsigned part) {
+__device__ __noinline__ void check_runs(const Store8Params& p, Seen& sm, unsigned part) {
   constexpr unsigned AHEAD = 4;  // rows of a thread on their way
   const int first = (int)part * kSeen;
   const unsigned lane = threadIdx.x % 32, n = p.N;
@@ -531,11 +532,13 @@ __device__ __forceinline__ void store_runs(const Store8Params& p, Runs<S::WINDOW
 
 // Windows of 16 rows in one launch with the queries while the lanes that keys and values have work for are about half
 // of what the GPU holds at once; else windows of 64 in a launch of their own, the queries' beside it.  One launch and two,
-// 8/32 heads of bf16: 256 tokens 6.4 and 5.7 us, 512 6.5 and 9.3, 1024 8.7 and 10.8, 2048 17.0 and 16.8, 8192 60 and
-// 51; 16/64 heads: 600 tokens 10.7 and 14.9, 1024 19.6 and 17.7; 512 requests of one token 6.1 and 9.5.
+// 8/32 heads of bf16: 256 tokens 6.7 and 5.7 us, 512 7.0 and 9.2, 1024 8.9 and 10.8, 2048 17.3 and 16.8, 8192 61 and
+// 49; 16/64 heads: 600 tokens 10.9 and 14.8, 1024 20.2 and 17.3; 512 requests of one token 6.2 and 9.3.  (Tokens that
+// follow one another in pages of 64 and more of few heads would rather have two: 600 of 1/8 heads 13.2 and 10.6 us, of 4/32
+// heads of 64 6.5 and 4.8; the rule does not know how long runs are.)
 constexpr int kFewLanes = 160 * 1024;
-// Three blocks of 256 threads and 64 rows per SM: a prompt of 8192 tokens 51 us.  Two of them 56, four 50 (but 41 for
-// 39 where eleven ragged chunks meet), four of 128 threads and 32 rows 60.  Blocks that stay and take the heads of a
+// Three blocks of 256 threads and 64 rows per SM: a prompt of 8192 tokens 49 us.  Two of them 54, four 48 (but 41 for
+// 39 where eleven ragged chunks meet); earlier, at 51, four of 128 threads and 32 rows took 60.  Blocks that stay and take the heads of a
 // window one after the other, its runs found once and the next head's rows on their way, took 52.
 constexpr int kKvThreads = 256, kKvWindow = 64, kKvBlocks = 3;
 constexpr int kQueryBatch = 3;      // heads a lane group has in flight
@@ -591,7 +594,8 @@ __device__ __forceinline__ void queries(const Store8Params& p, Turn<S::D>* turns
 // rows of f32 with 768 of them 7.2 us, with 512 8.6; 1024 tokens of bf16 with 512 8.6, with 384 9.8.
 template <typename T>
 constexpr int kMixedThreads = sizeof(T) == 4 ? 768 : 512;
-template <typename S>
+// BEHIND: beside a launch that looks for pages of two runs (check8_kernel); the last block ends behind it.
+template <typename S, bool BEHIND>
 __global__ void __launch_bounds__(S::THREADS, kMixedThreads<typename S::T> / S::THREADS) store8_kernel(const __grid_constant__ Store8Params p) {
   __shared__ union alignas(16) Any {
     __device__ Any() {}
@@ -603,10 +607,10 @@ __global__ void __launch_bounds__(S::THREADS, kMixedThreads<typename S::T> / S::
   if (block < p.checks) check_runs<S::THREADS>(p, sm.seen, block);
   else if (block < p.checks + p.kv_blocks) store_runs<S>(p, sm.runs, block - p.checks);
   else queries<S>(p, sm.turns, block - p.checks - p.kv_blocks);
-  if (p.behind && block == gridDim.x - 1) ptx::wait_dependency();
+  if (BEHIND && block == gridDim.x - 1) ptx::wait_dependency();
 }
 // Keys and values alone
-template <typename S>
+template <typename S, bool BEHIND>
 __global__ void __launch_bounds__(S::THREADS, kKvBlocks) store8_kv_kernel(const __grid_constant__ Store8Params p) {
   __shared__ union alignas(16) Either {
     __device__ Either() {}
@@ -616,7 +620,7 @@ __global__ void __launch_bounds__(S::THREADS, kKvBlocks) store8_kv_kernel(const 
   ptx::launch_dependents();  // the queries' blocks follow as these end
   if (blockIdx.x < p.checks) check_runs<S::THREADS>(p, sm.seen, blockIdx.x);
   else store_runs<S>(p, sm.runs, blockIdx.x - p.checks);
-  if (p.behind && blockIdx.x == gridDim.x - 1) ptx::wait_dependency();
+  if (BEHIND && blockIdx.x == gridDim.x - 1) ptx::wait_dependency();
 }
 constexpr int kCheckThreads = 1024;
 __global__ void __launch_bounds__(kCheckThreads, 1) check8_kernel(const __grid_constant__ Store8Params p) {
@@ -635,25 +639,24 @@ template <typename T, int D>
 cudaError_t launch_store8(Store8Params& p, int sms, cudaStream_t stream) {
   constexpr int E = kElems<T>, LPH = D / 2 / E;
   const auto kv_blocks = [&](int window) { return (unsigned)(((int64_t)p.N + window - 1) / window * 2 * p.Hkv); };
-  // the blocks that look for pages of two runs: with the stores up to `rows` of a thread (two runs of a page have a row of
-  // another between them)
-  const auto checks = [&](int rows) {
-    p.checks = p.status && p.N > 2 ? (unsigned)((p.num_pages - 1) / kSeen + 1) : 0;
-    p.behind = p.checks > 0 && p.N > rows;
-    if (!p.behind) return cudaSuccess;
+  // the blocks that look for pages of two runs (which have a row of another between them): in the stores' launch up to
+  // `rows` rows, else in one that the stores follow beside
+  p.checks = p.status && p.N > 2 ? (unsigned)((p.num_pages - 1) / kSeen + 1) : 0;
+  const auto launch = [&](auto* kernel, auto* kernel_behind, int rows, unsigned blocks, int threads) {
+    if (p.checks == 0 || p.N <= rows) {
+      kernel<<<p.checks + blocks, threads, 0, stream>>>(p);
+      return cudaGetLastError();
+    }
     check8_kernel<<<p.checks, kCheckThreads, 0, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     p.checks = 0;
-    return cudaGetLastError();
-  };
-  const auto launch = [&](auto* kernel, unsigned blocks, int threads) {
-    if (p.behind) return launch_early(kernel, dim3(blocks), dim3(threads), 0, stream, p);
-    kernel<<<blocks, threads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_early(kernel_behind, dim3(blocks), dim3(threads), 0, stream, p);
   };
   if ((int64_t)p.N * 2 * p.Hkv * LPH > kFewLanes) {
     using S = Shape<T, D, kKvThreads, kKvWindow, kKvWindow / (kKvThreads / LPH)>;
-    cudaError_t e = checks(kKvCheckRows);
-    if (e == cudaSuccess) e = launch(store8_kv_kernel<S>, p.checks + kv_blocks(S::WINDOW), S::THREADS);
+    const cudaError_t e = launch(store8_kv_kernel<S, false>, store8_kv_kernel<S, true>, kKvCheckRows, kv_blocks(S::WINDOW),
+                                 S::THREADS);
     if (e != cudaSuccess) return e;
     return launch_queries(p, sizeof(T) == 4 ? MK_F32 : MK_BF16, D, sms, stream);
   }
@@ -664,10 +667,9 @@ cudaError_t launch_store8(Store8Params& p, int sms, cudaStream_t stream) {
   while (p.tokens < kQueryMaxTokens && 2 * p.tokens * p.Hq <= kQueryBatch * GP) p.tokens *= 2;
   while (p.tokens > 1 && (p.N + p.tokens - 1) / p.tokens < 2 * sms) p.tokens /= 2;
   p.splits = p.N < sms ? (p.Hq + GP - 1) / GP : 1;
-  if (const cudaError_t e = checks(kCheckRows * S::THREADS); e != cudaSuccess) return e;
   p.kv_blocks = kv_blocks(S::WINDOW);
-  const unsigned blocks = p.checks + p.kv_blocks + (unsigned)((p.N + p.tokens - 1) / p.tokens * p.splits);
-  return launch(store8_kernel<S>, blocks, S::THREADS);
+  const unsigned blocks = p.kv_blocks + (unsigned)((p.N + p.tokens - 1) / p.tokens * p.splits);
+  return launch(store8_kernel<S, false>, store8_kernel<S, true>, kCheckRows * S::THREADS, blocks, S::THREADS);
 }
 
 }  // namespace
