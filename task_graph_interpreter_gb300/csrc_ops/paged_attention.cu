@@ -41,8 +41,8 @@ bool encode(EncodeTiledFn enc, CUtensorMap* m, const void* ptr, int rank, const 
 // warp product; beyond that the 128-row tensor-core tiles are faster although
 // mostly empty (paged_rows.cu has both sides).  Over e4m3 pages two eights have
 // as many bytes to wait for per key as one over bf16 pages: 12 and 16 rows take
-// there and as chunks 54 and 93 us (64 requests of 512 to 2048 keys), 45 and 56
-// (16 of 512 to 8192), 65 and 64 (4 of 32768), 24 and 20 (one of 8192); with 20
+// there and as chunks 56 and 93 us (64 requests of 512 to 2048 keys), 46 and 56
+// (16 of 512 to 8192), 66 and 64 (4 of 32768), 24 and 20 (one of 8192); with 20
 // rows and three eights 4 requests of 32768 keys took 95 us, 64 as chunks.
 bool few_rows(int max_new, int G, bool e4m3) { return (int64_t)max_new * G <= (e4m3 ? kMaxFewRows8 : kMaxFewRows); }
 

@@ -32,10 +32,10 @@
 // Bound by the chain of one tile (products of S, softmax, products of O: the
 // other tile's overlap it) and by shared memory: a pair of blocks takes 3050 to
 // 3450 cycles where bf16 pages take 2300.  Of a prompt of 8192 tokens, 8/32 heads
-// of 128, 420 us (1.31 PFLOP/s; bf16 pages 315): without the widening, which
+// of 128, 422 us (1.30 PFLOP/s; bf16 pages 315): without the widening, which
 // moves 48 KB of shared memory per block, 383; the second parts of the queries
 // are 82 of a form at 433; without powers, scales, or the packing of P no less.
-// Four requests of 32768 keys and 20 rows 64 us (4.2 TB/s; bf16 pages 90), and 76
+// Four requests of 32768 keys and 20 rows 65 us (4.1 TB/s; bf16 pages 90), and 76
 // before items of one tile were dealt to both; seven ragged chunks, 4/32 heads of
 // 64, 51 us.  Scores are read in halves of 64: a whole row's 128 left 140 to 312
 // bytes of spilled registers at every split of them.

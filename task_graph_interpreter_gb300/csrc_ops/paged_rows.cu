@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
 // rows than eight (e4m3 pages have up to sixteen) are dealt to two blocks: one
 // request of 8192 keys and 12 rows, whose 128 records a head are all the work
 // that is left, 32 us with one, 24 with two, 22 with four; 64 requests of 512 to
-// 2048 keys 56, 58 and 63.  (How many blocks share the rows is known when this is
+// 2048 keys 54, 56 and 61.  (How many blocks share the rows is known when this is
 // compiled: divided by at run time, one token over 4096 keys of bf16 took 13.8 us
 // where it takes 13.2.)
 constexpr int kJoinWarps = 16;

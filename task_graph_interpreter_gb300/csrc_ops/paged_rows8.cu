@@ -26,12 +26,12 @@
 // parts, as over bf16 pages, would keep what codes of four bits do not have.)
 //
 // Eight warps of 8 KB blocks, three in flight: 64 requests of 512 to 8192 keys
-// and four rows 100 us (5.8 TB/s; bf16 pages 178), four warps of 16 KB 126, for
+// and four rows 101.5 us (5.7 TB/s; bf16 pages 178), four warps of 16 KB 126, for
 // a block's chain of products, softmax and products has half the time that it
-// has over bf16 pages; heads of 64 56 and 80.  What is left there is that chain
-// and the join.  One request of 4096 keys 13.5 us: two launches and eight
+// has over bf16 pages; heads of 64 58 and 80.  What is left there is that chain
+// and the join.  One request of 4096 keys 13.4 us: two launches and eight
 // dependent round trips.  Up to two eights of rows run here (four requests of
-// 32768 keys and 12 rows 65 us); with three eights registers leave no room.
+// 32768 keys and 12 rows 66 us); with three eights registers leave no room.
 #include <type_traits>
 
 #include "paged_attention.cuh"
