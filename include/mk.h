@@ -587,12 +587,12 @@ int mk_qk_norm_rope_e4m3(void* stream, int N, int Hq, int Hkv, int D, const void
  * read are positive and finite (others give any result).  Queries keep 2^-18 of a
  * row's largest element and more.  Maxima, sums and results are f32; keys' scales are
  * f32 factors of the scores.  Probabilities are rounded to f16: to 2^-11 of
- * themselves, and where they lie far below the row's largest (2^-28 of it with few
- * rows, 2^-20 for chunks), to 2^-39 and 2^-31 of that.  Values' scales are exact where
+ * themselves, and where they lie far below the row's largest (2^-22 of it with few
+ * rows, 2^-20 for chunks), to 2^-33 and 2^-31 of that.  Values' scales are exact where
  * they are powers of two (what the stores write), others are rounded to f16 with the
  * probability or the value.  Scales far below the largest that the row sees cost
- * nothing with few rows (down to 2^-80 of it); for chunks, under 2^-15 of it, each
- * key's part of the result is off by at most 2^-31 of the row's largest probability
+ * nothing with few rows (down to 2^-80 of it); for chunks, with any under 2^-15 of it,
+ * each key's part of the result is off by at most 2^-31 of the row's largest probability
  * times 448 times that scale.  Pages that a row does not see cost it nothing while
  * their scales are at most 2^80 times the largest that it sees. */
 int mk_paged_attention_e4m3(void* stream, int B, int N, int max_new, int Hq, int Hkv, int D, const void* q,

@@ -16,7 +16,7 @@
 //   scales    of keys: one factor per 16 keys (a page has at least 16), with
 //             the row's and the softmax scale; of values: onto the
 //             probabilities, relative to the power of two of the largest scale
-//             so far, which the results carry (a tile 2^kFar and more below it is
+//             so far, which the results carry (a tile more than 2^kFar below it is
 //             added to results in a smaller unit, or its probabilities would
 //             leave f16: a page that some rows do not see, or that has no
 //             weight, takes nothing from the others)
@@ -42,8 +42,9 @@ namespace {
 using namespace ptx;
 
 constexpr float kBias = 14.f;                // probabilities are kept times 2^kBias
-// A tile whose scale is 2^kFar and more below the unit: nearer ones keep 2^-11 of probabilities down to 2^-13.
-constexpr int kFar = 15;
+// A tile whose scale is more than 2^kFar below the unit is added apart: nearer ones keep 2^-11 of probabilities down to
+// 2^-22, and 2^-33.  (4, 6 and 15 take the same time where pages' scales are some powers of two apart.)
+constexpr int kFar = 6;
 // The results' unit goes down by 2^kMostDown at most: they are under 2^41 in it (kFoldKeys keys of at most 2 * 448 times
 // 2^kBias).
 constexpr int kMostDown = 60;

@@ -121,7 +121,7 @@ def attention(q, kpool, vpool, table, cu, ctx_len, max_new: int, *, kscale=None,
 
     With e4m3 pools, ``kscale`` and ``vscale`` f32 [num_pages, Hkv] are the
     positive scales of their pages and heads; probabilities are rounded to f16
-    (2^-11) whatever max_new is, and far below a row's largest to 2^-39 of it
+    (2^-11) whatever max_new is, and far below a row's largest to 2^-33 of it
     (max_new Hq / Hkv <= 16) or 2^-31 (beyond)."""
     args = (q, kpool, vpool, table, cu, ctx_len, max_new, scale, out, workspace, status, kscale, vscale)
     return L.calls().attention(*args) if stream is None else on_stream(L.calls().attention, stream, args)

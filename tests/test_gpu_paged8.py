@@ -1168,3 +1168,31 @@ def test_a_scale_that_a_rejected_draft_raised_stays_until_the_page_is_begun_anew
     first = dict(step, pos=[0], slots=[base])            # the page's first token
     out, kp, vp, ks, vs = run_store(first, 2, 1, 64, 16)
     assert bool((ks[pg] * 2 ** 9 <= after[3][pg]).all()) and bool((vs[pg] * 2 ** 9 <= after[4][pg]).all())
+
+
+@pytest.mark.parametrize("higher", [4, 7, 14])
+@pytest.mark.parametrize("new,D", [(1, 64), (2, 128), (3, 64)])
+def test_few_rows_keep_small_weights_behind_large_values(new, D, higher):
+    """The keys of the first page have no weight, but values 2^4 to 2^14 times the others'; one key has 2^22 times the
+    weight of each of the others.  Each weight loses 2^-33 of the largest at most.  So many requests (of the same pages)
+    that a worker has a whole one."""
+    B, Hq, Hkv, page, pages, bits = 1300, 4, 1, 64, 32, 22
+    ctx = pages * page - new
+    k = torch.zeros(pages, Hkv, page, D, device=DEV).to(E4M3)
+    v = torch.ones(pages, Hkv, page, D, device=DEV).to(E4M3)
+    k.view(torch.uint8)[17, 0, 5, 0] = torch.tensor(float(bits), device=DEV).to(E4M3).view(torch.uint8)
+    v.view(torch.uint8)[17, 0, 5] = 0
+    k.view(torch.uint8)[0, 0, :, 0] = torch.tensor(-448.0, device=DEV).to(E4M3).view(torch.uint8)
+    ks, vs = torch.ones(pages, Hkv, device=DEV), torch.ones(pages, Hkv, device=DEV)
+    vs[0] = 2.0 ** higher
+    table = torch.arange(pages, device=DEV).int().expand(B, pages).contiguous()
+    q = torch.zeros(B * new, Hq, D, dtype=torch.bfloat16, device=DEV)
+    q[:, :, 0] = 1
+    cu = (torch.arange(B + 1, device=DEV) * new).int()
+    scale = 0.98 * math.log(2.0)
+    got = paged.attention(q, k, v, table, cu, i32([ctx] * B), new, kscale=ks, vscale=vs, scale=scale)
+    tail = torch.tensor([(ctx + t - page) * 2.0 ** (-0.98 * bits) for t in range(new)], dtype=torch.float64, device=DEV)
+    want = (tail / (1 + tail)).repeat(B)[:, None, None]
+    e = 2.0 ** -11 + (bits + D + 4) * 2.0 ** -23
+    tol = 2.0 ** -8 * want + 2 * e * want + ctx * 2.0 ** -33
+    assert bool(((got.double() - want).abs() <= tol).all()), f"{float((got.double() - want).abs().max())}, {float(tol.min())}"
